@@ -20,7 +20,8 @@ LIB_PATH = os.path.join(_PKG, "libsinkattn.so")
 _lock = threading.Lock()
 _lib = None
 
-OK, INVALID_ARG, UNSUPPORTED, CUDA_ERROR, TIMEOUT, BAD_LENGTHS = range(6)
+(OK, INVALID_ARG, UNSUPPORTED, CUDA_ERROR, TIMEOUT, BAD_LENGTHS, OUT_OF_PAGES,
+ BAD_PAGES) = range(8)
 
 
 class SinkAttnError(RuntimeError):
@@ -40,6 +41,7 @@ def lib() -> ctypes.CDLL:
                     "`python -c 'import __graft_entry__ as g; g.build()'`" % LIB_PATH)
             L = ctypes.CDLL(LIB_PATH)
             P, I32, F, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
+            I64 = ctypes.c_int64
             L.sinkattn_prefill.argtypes = [P, P, P, P, P, P, I32, I32, I32, I32, I32, I32, I32, F,
                                            I32, I32, P, P, P]
             L.sinkattn_decode_split.argtypes = [P, P, P, P, I32, I32, I32, I32, I32, I32, F, I32, I32,
@@ -73,6 +75,24 @@ def lib() -> ctypes.CDLL:
                                                     F, I32, I32, I32, P, P, P]
             L.sinkattn_decode_fp8.argtypes = [P, P, P, P, P, P, I32, I32, I32, I32, I32, I32, F,
                                               I32, I32, I32, P, P, SZ, P, P, P]
+            L.sinkattn_decode_shared_paged.argtypes = (
+                [P] * 8 + [I32] * 10 + [F] + [I32] * 4 + [P, P, SZ, P, P, P])
+            L.sinkattn_decode_shared_paged_fp8.argtypes = (
+                [P] * 10 + [I32] * 10 + [F] + [I32] * 4 + [P, P, SZ, P, P, P])
+            L.sinkattn_decode_shared_workspace_bytes.argtypes = [I32] * 7 + [ctypes.POINTER(SZ)]
+            L.sinkattn_decode_shared_default_splits.argtypes = (
+                [I32] * 8 + [ctypes.POINTER(I32)] * 2)
+            L.sinkattn_append_paged.argtypes = [P, P, I64, I64, P, I32, P, P, I32, I32, I32, I32, P]
+            L.sinkattn_append_paged_fp8.argtypes = [P, P, I64, I64, P, I32, P, P, P, P, I32, I32,
+                                                    I32, I32, P]
+            T = [P, I32, I32, I32, I32]
+            L.sinkattn_pages_table_ints.argtypes = [I32, I32, I32, ctypes.POINTER(I64)]
+            L.sinkattn_pages_init.argtypes = T + [P]
+            L.sinkattn_pages_reserve.argtypes = T + [P, P, I32, I32, P, P, I32, I64, I32, I32, P, P]
+            L.sinkattn_pages_fork.argtypes = T + [P, P, I32, P]
+            L.sinkattn_pages_truncate.argtypes = T + [P, P, I32, P]
+            L.sinkattn_pages_compact.argtypes = T + [P, P, I32, I64, I32, I32, P, P]
+            L.sinkattn_pages_lists.argtypes = T + [P, I32, P, P, P, I32, P]
             for name in ("sinkattn_prefill", "sinkattn_decode_split", "sinkattn_merge",
                          "sinkattn_decode", "sinkattn_decode_fused", "sinkattn_decode_noalloc",
                          "sinkattn_decode_workspace_bytes", "sinkattn_decode_default_splits",
@@ -81,7 +101,14 @@ def lib() -> ctypes.CDLL:
                          "sinkattn_set_prefill_kernel", "sinkattn_decode_split_fp8",
                          "sinkattn_decode_fp8",
                          "sinkattn_prefill_paged", "sinkattn_decode_split_paged",
-                         "sinkattn_decode_paged"):
+                         "sinkattn_decode_paged", "sinkattn_decode_shared_paged",
+                         "sinkattn_decode_shared_paged_fp8",
+                         "sinkattn_decode_shared_workspace_bytes",
+                         "sinkattn_decode_shared_default_splits", "sinkattn_append_paged",
+                         "sinkattn_append_paged_fp8", "sinkattn_pages_table_ints",
+                         "sinkattn_pages_init", "sinkattn_pages_reserve", "sinkattn_pages_fork",
+                         "sinkattn_pages_truncate", "sinkattn_pages_compact",
+                         "sinkattn_pages_lists"):
                 getattr(L, name).restype = ctypes.c_int
             _lib = L
     return _lib
@@ -380,6 +407,363 @@ def sinkattn_decode_fp8(q, k, v, k_scale, v_scale, kv_indptr, sinks, q_len, max_
         workspace.numel() * workspace.element_size(), _ptr(out), _ptr(lse), _stream(q, stream))
     _check(rc)
     return out, lse
+
+
+def _need(t, what, dtype, dev, shape=None):
+    """Refuses a tensor that the kernels would read as something else: wrong
+    type, device, layout or shape (None in `shape`: any size)."""
+    if not torch.is_tensor(t):
+        raise SinkAttnError(INVALID_ARG, "%s must be a tensor" % what)
+    if t.dtype is not dtype:
+        raise SinkAttnError(INVALID_ARG, "%s must be %s, not %s" % (what, dtype, t.dtype))
+    if t.device != dev:
+        raise SinkAttnError(INVALID_ARG, "%s must be on %s, not %s" % (what, dev, t.device))
+    if not t.is_contiguous():
+        raise SinkAttnError(INVALID_ARG, "%s must be contiguous" % what)
+    if shape is not None and (t.dim() != len(shape) or any(
+            b is not None and a != b for a, b in zip(t.shape, shape))):
+        raise SinkAttnError(INVALID_ARG, "%s must have shape %s, not %s" % (
+            what, tuple("any" if x is None else x for x in shape), tuple(t.shape)))
+    return t
+
+
+def _need_cuda(t, what):
+    if not torch.is_tensor(t) or not t.is_cuda:
+        raise SinkAttnError(INVALID_ARG, "%s must be a CUDA tensor" % what)
+    return t.device
+
+
+class _On:
+    """Makes `device` current for a launch (nothing to do if it already is)."""
+    __slots__ = ("guard",)
+
+    def __init__(self, device):
+        self.guard = (torch.cuda.device(device)
+                      if device.index != torch.cuda.current_device() else None)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def sinkattn_decode_shared_default_splits(batch, q_len, num_qo_heads, num_kv_heads, head_dim,
+                                          num_groups, max_prefix_len, max_suffix_len):
+    """(prefix_splits, num_splits) the shared-prefix decode uses by default."""
+    a, b = ctypes.c_int32(0), ctypes.c_int32(0)
+    _check(lib().sinkattn_decode_shared_default_splits(
+        int(batch), int(q_len), int(num_qo_heads), int(num_kv_heads), int(head_dim),
+        int(num_groups), int(max_prefix_len), int(max_suffix_len), ctypes.byref(a),
+        ctypes.byref(b)))
+    return int(a.value), int(b.value)
+
+
+def sinkattn_decode_shared_workspace_bytes(batch, q_len, num_qo_heads, head_dim, num_groups,
+                                           prefix_splits, num_splits) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().sinkattn_decode_shared_workspace_bytes(
+        int(batch), int(q_len), int(num_qo_heads), int(head_dim), int(num_groups),
+        int(prefix_splits), int(num_splits), ctypes.byref(n)))
+    return int(n.value)
+
+
+def _decode_shared(entry, pool_dtype, scales, q, k_pages, v_pages, kv_indptr, page_indptr,
+                   page_indices, group_indptr, prefix_lens, sinks, q_len, max_prefix_len,
+                   max_suffix_len, num_splits, prefix_splits, sm_scale, causal, window, workspace,
+                   out, lse, return_lse, stream):
+    dev = _need_cuda(q, "q")
+    _need(q, "q", torch.bfloat16, dev, (None, None, None))
+    rows, Hq, d = q.shape
+    _need(k_pages, "k_pages", pool_dtype, dev, (None, None, None, d))
+    num_pages, Hkv, page_size, _ = k_pages.shape
+    _need(v_pages, "v_pages", pool_dtype, dev, k_pages.shape)
+    for t, what in zip(scales, ("k_scale", "v_scale")):
+        _need(t, what, torch.float32, dev, (Hkv,))
+    _need(kv_indptr, "kv_indptr", torch.int32, dev, (None,))
+    batch = kv_indptr.numel() - 1
+    q_len = int(q_len)
+    if batch < 0 or rows != batch * q_len:
+        raise SinkAttnError(INVALID_ARG, "q has %d rows, batch * q_len is %d" % (rows, batch * q_len))
+    _need(page_indptr, "page_indptr", torch.int32, dev, (batch + 1,))
+    _need(page_indices, "page_indices", torch.int32, dev, (None,))
+    _need(prefix_lens, "prefix_lens", torch.int32, dev, (None,))
+    groups = prefix_lens.numel()
+    _need(group_indptr, "group_indptr", torch.int32, dev, (groups + 1,))
+    if sinks is not None:
+        _need(sinks, "sinks", torch.float32, dev, (Hq,))
+    if num_splits <= 0 or prefix_splits <= 0:
+        ps, ss = sinkattn_decode_shared_default_splits(batch, q_len, Hq, Hkv, d, groups,
+                                                       max_prefix_len, max_suffix_len)
+        prefix_splits = prefix_splits if prefix_splits > 0 else ps
+        num_splits = num_splits if num_splits > 0 else ss
+    if workspace is None:
+        need = sinkattn_decode_shared_workspace_bytes(batch, q_len, Hq, d, groups, prefix_splits,
+                                                      num_splits)
+        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+    elif not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
+        raise SinkAttnError(INVALID_ARG, "workspace must be contiguous and on %s" % dev)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _need(out, "out", torch.bfloat16, dev, q.shape)
+    if lse is not None:
+        _need(lse, "lse", torch.float32, dev, (rows, Hq))
+    elif return_lse:
+        lse = torch.empty((rows, Hq), dtype=torch.float32, device=dev)
+    if batch == 0:   # (an empty tensor has no address to check)
+        return out, lse
+    with _On(dev):
+        rc = entry(_ptr(q), _ptr(k_pages), _ptr(v_pages), *[_ptr(t) for t in scales],
+                   _ptr(kv_indptr), _ptr(page_indptr), _ptr(page_indices), _ptr(group_indptr),
+                   _ptr(prefix_lens), groups, num_pages, page_size, batch, q_len,
+                   int(max_prefix_len), int(max_suffix_len), Hq, Hkv, d, _scale(sm_scale, d),
+                   int(bool(causal)), int(window), int(prefix_splits), int(num_splits),
+                   _ptr(sinks), _ptr(workspace), workspace.numel() * workspace.element_size(),
+                   _ptr(out), _ptr(lse), _stream(q, stream))
+    _check(rc)
+    return out, lse
+
+
+def sinkattn_decode_shared_paged(q, k_pages, v_pages, kv_indptr, page_indptr, page_indices,
+                                 group_indptr, prefix_lens, sinks, q_len, max_prefix_len,
+                                 max_suffix_len, num_splits=0, prefix_splits=0, sm_scale=None,
+                                 causal=True, window=0, workspace=None, out=None, lse=None,
+                                 return_lse=True, stream=None):
+    """sinkattn_decode_paged for a batch whose sequences share prefixes: group
+    g holds sequences group_indptr[g] .. group_indptr[g+1] - 1 (int32, device),
+    whose first prefix_lens[g] keys (int32, device; a multiple of the page
+    size) are the same; they are read once, from the first sequence's page
+    list. max_prefix_len bounds prefix_lens, max_suffix_len the keys of a
+    sequence past its prefix (at least q_len each). Returns (out, lse)."""
+    return _decode_shared(lib().sinkattn_decode_shared_paged, torch.bfloat16, (), q, k_pages,
+                          v_pages, kv_indptr, page_indptr, page_indices, group_indptr, prefix_lens,
+                          sinks, q_len, max_prefix_len, max_suffix_len, num_splits, prefix_splits,
+                          sm_scale, causal, window, workspace, out, lse, return_lse, stream)
+
+
+def sinkattn_decode_shared_paged_fp8(q, k_pages, v_pages, k_scale, v_scale, kv_indptr, page_indptr,
+                                     page_indices, group_indptr, prefix_lens, sinks, q_len,
+                                     max_prefix_len, max_suffix_len, num_splits=0, prefix_splits=0,
+                                     sm_scale=None, causal=True, window=0, workspace=None,
+                                     out=None, lse=None, return_lse=True, stream=None):
+    """sinkattn_decode_shared_paged over pools of e4m3 codes (uint8) with
+    per-KV-head fp32 scales [Hkv]. Returns (out, lse)."""
+    return _decode_shared(lib().sinkattn_decode_shared_paged_fp8, torch.uint8, (k_scale, v_scale),
+                          q, k_pages, v_pages, kv_indptr, page_indptr, page_indices, group_indptr,
+                          prefix_lens, sinks, q_len, max_prefix_len, max_suffix_len, num_splits,
+                          prefix_splits, sm_scale, causal, window, workspace, out, lse, return_lse,
+                          stream)
+
+
+def _append(entry, pool_dtype, scales, k, v, slots, k_pages, v_pages, stream):
+    dev = _need_cuda(k_pages, "k_pages")
+    _need(k_pages, "k_pages", pool_dtype, dev, (None, None, None, None))
+    num_pages, Hkv, page_size, d = k_pages.shape
+    _need(v_pages, "v_pages", pool_dtype, dev, k_pages.shape)
+    _need(slots, "slots", torch.int32, dev, (None,))
+    tokens = slots.numel()
+    strides = []
+    for t, what in ((k, "k"), (v, "v")):
+        if not torch.is_tensor(t) or t.dtype is not torch.bfloat16 or t.device != dev:
+            raise SinkAttnError(INVALID_ARG, "%s must be bfloat16 on %s" % (what, dev))
+        if tuple(t.shape) != (tokens, Hkv, d) or (
+                tokens > 0 and (t.stride(2) != 1 or (Hkv > 1 and t.stride(1) != d))):
+            raise SinkAttnError(INVALID_ARG, "%s must have shape %s with contiguous rows" % (
+                what, (tokens, Hkv, d)))
+        strides.append(t.stride(0) if tokens > 1 else Hkv * d)
+    for t, what in zip(scales, ("k_scale", "v_scale")):
+        _need(t, what, torch.float32, dev, (Hkv,))
+    with _On(dev):
+        _check(entry(_ptr(k), _ptr(v), strides[0], strides[1], _ptr(slots), tokens,
+                     *[_ptr(t) for t in scales], _ptr(k_pages), _ptr(v_pages), num_pages,
+                     page_size, Hkv, d, _stream(k_pages, stream)))
+
+
+def sinkattn_append_paged(k, v, slots, k_pages, v_pages, stream=None):
+    """Writes new keys and values, bf16 [tokens, Hkv, d] (rows of a token
+    contiguous, any token stride that is a multiple of 8), to the slots (int32
+    [tokens], page * page_size + position; outside the pool: left out) of the
+    pools [num_pages, Hkv, page_size, d]."""
+    _append(lib().sinkattn_append_paged, torch.bfloat16, (), k, v, slots, k_pages, v_pages, stream)
+
+
+def sinkattn_append_paged_fp8(k, v, slots, k_scale, v_scale, k_pages, v_pages, stream=None):
+    """sinkattn_append_paged into pools of e4m3 codes (uint8): the code
+    nearest to x / scale[head] (ties to even, saturating at 448)."""
+    _append(lib().sinkattn_append_paged_fp8, torch.uint8, (k_scale, v_scale), k, v, slots, k_pages,
+            v_pages, stream)
+
+
+def sinkattn_pages_table_ints(num_pages, max_seqs, max_pages) -> int:
+    n = ctypes.c_int64(0)
+    _check(lib().sinkattn_pages_table_ints(int(num_pages), int(max_seqs), int(max_pages),
+                                           ctypes.byref(n)))
+    return int(n.value)
+
+
+class PageTable:
+    """A page table's buffer and sizes. ``state``: an int32 device tensor of at
+    least sinkattn_pages_table_ints() words that holds a table already; without
+    one, a new buffer on ``device`` is allocated and initialised (every page
+    free, every sequence empty)."""
+    __slots__ = ("state", "num_pages", "page_size", "max_seqs", "max_pages")
+
+    def __init__(self, state, num_pages, page_size, max_seqs, max_pages, device="cuda",
+                 stream=None):
+        self.num_pages, self.page_size = int(num_pages), int(page_size)
+        self.max_seqs, self.max_pages = int(max_seqs), int(max_pages)
+        need = sinkattn_pages_table_ints(num_pages, max_seqs, max_pages)
+        if state is None:
+            self.state = torch.empty((need,), dtype=torch.int32, device=device)
+            sinkattn_pages_init(self, stream=stream)
+            return
+        dev = _need_cuda(state, "state")
+        _need(state, "state", torch.int32, dev, (None,))
+        if state.numel() < need:
+            raise SinkAttnError(INVALID_ARG, "state has %d words, a table of these sizes %d" % (
+                state.numel(), need))
+        self.state = state
+
+    def _part(self, at, n):
+        return self.state[at:at + n]
+
+    @property
+    def free_count(self):
+        return self._part(0, 1)
+
+    @property
+    def seq_lens(self):
+        return self._part(16, self.max_seqs)
+
+    @property
+    def page_list(self):
+        return self._part(16 + self.max_seqs, self.max_seqs * self.max_pages).view(
+            self.max_seqs, self.max_pages)
+
+    @property
+    def refcount(self):
+        return self._part(16 + self.max_seqs * (1 + self.max_pages), self.num_pages)
+
+    @property
+    def free_list(self):
+        return self._part(16 + self.max_seqs * (1 + self.max_pages) + self.num_pages,
+                          self.num_pages)
+
+
+def _table(t):
+    return _ptr(t.state), t.num_pages, t.page_size, t.max_seqs, t.max_pages
+
+
+def _pools(table, k_pages, v_pages):
+    """(k, v, layers, layer stride, Hkv, row bytes) of the pools of one layer,
+    [num_pages, Hkv, page_size, d], or of several, [layers, ...]."""
+    dev = table.state.device
+    for t, what in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+        if not torch.is_tensor(t) or t.device != dev or t.dim() not in (4, 5):
+            raise SinkAttnError(INVALID_ARG, "%s must be a tensor of 4 or 5 dimensions on %s" % (
+                what, dev))
+        if not (t if t.dim() == 4 else t[0]).is_contiguous():
+            raise SinkAttnError(INVALID_ARG, "each layer of %s must be contiguous" % what)
+    if (k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype
+            or k_pages.stride() != v_pages.stride()):
+        raise SinkAttnError(INVALID_ARG, "k_pages and v_pages must have one shape, type and stride")
+    num_pages, Hkv, page_size, d = k_pages.shape[-4:]
+    if num_pages != table.num_pages or page_size != table.page_size:
+        raise SinkAttnError(INVALID_ARG, "the pools have %d pages of %d, the table %d of %d" % (
+            num_pages, page_size, table.num_pages, table.page_size))
+    el = k_pages.element_size()
+    layers = k_pages.shape[0] if k_pages.dim() == 5 else 1
+    stride = k_pages.stride(0) * el if layers > 1 else 0
+    return _ptr(k_pages), _ptr(v_pages), layers, stride, Hkv, d * el
+
+
+def sinkattn_pages_init(table, stream=None) -> None:
+    """Every page free (page 0 is the first to be taken), every sequence empty."""
+    with _On(table.state.device):
+        _check(lib().sinkattn_pages_init(*_table(table), _stream(table.state, stream)))
+
+
+def sinkattn_pages_reserve(table, seq_ids, cu_new, total_new, k_pages, v_pages, slots=None,
+                           stream=None):
+    """Room for cu_new[i+1] - cu_new[i] more tokens in sequence seq_ids[i]
+    (int32, device). Returns the new tokens' slots, int32 [total_new]. A
+    partly filled page that other sequences hold too is copied first, in the
+    pools of all layers."""
+    dev = table.state.device
+    n = _need(seq_ids, "seq_ids", torch.int32, dev, (None,)).numel()
+    _need(cu_new, "cu_new", torch.int32, dev, (n + 1,))
+    total_new = int(total_new)
+    if slots is None:
+        slots = torch.empty((max(total_new, 0),), dtype=torch.int32, device=dev)
+    else:
+        _need(slots, "slots", torch.int32, dev, (total_new,))
+    with _On(dev):
+        _check(lib().sinkattn_pages_reserve(*_table(table), _ptr(seq_ids), _ptr(cu_new), n,
+                                            total_new, *_pools(table, k_pages, v_pages),
+                                            _ptr(slots), _stream(table.state, stream)))
+    return slots
+
+
+def sinkattn_pages_fork(table, src_ids, dst_ids, stream=None) -> None:
+    """dst_ids[i] (empty sequences) become copies of src_ids[i] that share all
+    their pages (int32, device)."""
+    dev = table.state.device
+    n = _need(src_ids, "src_ids", torch.int32, dev, (None,)).numel()
+    _need(dst_ids, "dst_ids", torch.int32, dev, (n,))
+    with _On(dev):
+        _check(lib().sinkattn_pages_fork(*_table(table), _ptr(src_ids), _ptr(dst_ids), n,
+                                         _stream(table.state, stream)))
+
+
+def sinkattn_pages_truncate(table, seq_ids, new_lens=None, stream=None) -> None:
+    """Shortens seq_ids[i] to new_lens[i] tokens (int32, device; None: 0, which
+    frees the sequences); pages that no sequence holds any more become free."""
+    dev = table.state.device
+    n = _need(seq_ids, "seq_ids", torch.int32, dev, (None,)).numel()
+    if new_lens is not None:
+        _need(new_lens, "new_lens", torch.int32, dev, (n,))
+    with _On(dev):
+        _check(lib().sinkattn_pages_truncate(*_table(table), _ptr(seq_ids), _ptr(new_lens), n,
+                                             _stream(table.state, stream)))
+
+
+def sinkattn_pages_compact(table, k_pages, v_pages, page_map=None, stream=None):
+    """Moves the pages in use to the front of the pools (all layers). Returns
+    page_map, int32 [num_pages]: each old page's new index, -1 where it was free."""
+    dev = table.state.device
+    if page_map is None:
+        page_map = torch.empty((table.num_pages,), dtype=torch.int32, device=dev)
+    else:
+        _need(page_map, "page_map", torch.int32, dev, (table.num_pages,))
+    with _On(dev):
+        _check(lib().sinkattn_pages_compact(*_table(table), *_pools(table, k_pages, v_pages),
+                                            _ptr(page_map), _stream(table.state, stream)))
+    return page_map
+
+
+def sinkattn_pages_lists(table, seq_ids, kv_indptr=None, page_indptr=None, page_indices=None,
+                         stream=None):
+    """What the paged attention reads of the sequences seq_ids: returns
+    (kv_indptr [n+1], page_indptr [n+1], page_indices), int32."""
+    dev = table.state.device
+    n = _need(seq_ids, "seq_ids", torch.int32, dev, (None,)).numel()
+
+    def buf(t, what, size):
+        if t is None:   # (an empty batch writes nothing: its running sums are zero)
+            return (torch.empty if n > 0 else torch.zeros)((size,), dtype=torch.int32, device=dev)
+        return _need(t, what, torch.int32, dev, (None if what == "page_indices" else size,))
+
+    kv_indptr = buf(kv_indptr, "kv_indptr", n + 1)
+    page_indptr = buf(page_indptr, "page_indptr", n + 1)
+    page_indices = buf(page_indices, "page_indices", n * table.max_pages)
+    with _On(dev):
+        _check(lib().sinkattn_pages_lists(*_table(table), _ptr(seq_ids), n, _ptr(kv_indptr),
+                                          _ptr(page_indptr), _ptr(page_indices),
+                                          page_indices.numel(), _stream(table.state, stream)))
+    return kv_indptr, page_indptr, page_indices
 
 
 PREFILL_KERNELS = {"auto": 0, "one_block": 1, "persistent": 2}

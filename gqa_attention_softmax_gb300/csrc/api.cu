@@ -4,6 +4,7 @@
 // synchronises (except the diagnostic sinkattn_debug_status).
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdarg>
@@ -205,6 +206,8 @@ const char* sinkattn_status_string(int status) {
     case SINKATTN_CUDA_ERROR: return "SINKATTN_CUDA_ERROR";
     case SINKATTN_TIMEOUT: return "SINKATTN_TIMEOUT";
     case SINKATTN_BAD_LENGTHS: return "SINKATTN_BAD_LENGTHS";
+    case SINKATTN_OUT_OF_PAGES: return "SINKATTN_OUT_OF_PAGES";
+    case SINKATTN_BAD_PAGES: return "SINKATTN_BAD_PAGES";
     default: return "SINKATTN_UNKNOWN_STATUS";
   }
 }
@@ -433,6 +436,116 @@ int decode_impl(const void* q, const void* k, const void* v, const int32_t* kv_i
                       num_splits, out, lse, static_cast<cudaStream_t>(stream), true);
 }
 
+// Shared-prefix decode: the sequences' own keys and the groups' prefixes as
+// two sets of partials of the same rows, folded by one merge.
+size_t shared_plan_bytes(int64_t batch, int64_t q_len, int64_t groups) {
+  return (shared_plan_ints(batch, q_len, groups) * 4 + 255) & ~static_cast<size_t>(255);
+}
+
+int decode_shared_impl(const void* q, const void* k_pages, const void* v_pages, const Fp8Kv* f8,
+                       const int32_t* kv_indptr, const PagedKv& pg, const int32_t* group_indptr,
+                       const int32_t* prefix_lens, int32_t num_groups, int32_t batch,
+                       int32_t q_len, int32_t max_prefix_len, int32_t max_suffix_len,
+                       int32_t num_qo_heads, int32_t num_kv_heads, int32_t head_dim,
+                       float sm_scale, int32_t causal, int32_t window, int32_t prefix_splits,
+                       int32_t num_splits, const float* sinks, void* workspace,
+                       size_t workspace_bytes, void* out, float* lse, void* stream) {
+  g_last_error[0] = '\0';
+  if (!group_indptr || !prefix_lens)
+    return fail(SINKATTN_INVALID_ARG, "group_indptr and prefix_lens must be non-null");
+  if (num_groups < 1 || max_prefix_len < 0)
+    return fail(SINKATTN_INVALID_ARG, "num_groups must be positive, max_prefix_len non-negative");
+  if (num_groups > 65535) return fail(SINKATTN_UNSUPPORTED, "num_groups %d exceeds 65535", num_groups);
+  int32_t ps = 0, ss = 0;
+  int rc = sinkattn_decode_shared_default_splits(batch, q_len, num_qo_heads, num_kv_heads, head_dim,
+                                                 num_groups, max_prefix_len, max_suffix_len, &ps,
+                                                 &ss);
+  if (rc) return rc;
+  if (prefix_splits <= 0) prefix_splits = ps;
+  if (num_splits <= 0) num_splits = ss;
+  if (max_prefix_len == 0) prefix_splits = 0;   // nothing is shared
+  AttnArgs a;
+  rc = decode_args(q, k_pages, v_pages, kv_indptr, batch, q_len, max_suffix_len, num_qo_heads,
+                   num_kv_heads, head_dim, sm_scale, causal, window, num_splits, &a);
+  if (rc) return rc;
+  if ((rc = check_paged(pg, num_kv_heads))) return rc;
+  if (f8) {
+    if (!f8->k_scale || !f8->v_scale ||
+        (reinterpret_cast<uintptr_t>(f8->k_scale) | reinterpret_cast<uintptr_t>(f8->v_scale)) & 3u)
+      return fail(SINKATTN_INVALID_ARG, "k_scale and v_scale must be non-null and 4-byte aligned");
+    a.kv_fp8 = 1;
+    a.k_scale = f8->k_scale;
+    a.v_scale = f8->v_scale;
+  }
+  if (static_cast<int64_t>(batch) * q_len * num_qo_heads >= (int64_t{1} << 31))
+    return fail(SINKATTN_UNSUPPORTED, "problem exceeds 2^31 rows");
+  if (static_cast<int64_t>(max_prefix_len) + max_suffix_len >= (int64_t{1} << 31) ||
+      static_cast<int64_t>(num_groups) * max_prefix_len >= (int64_t{1} << 31))
+    return fail(SINKATTN_UNSUPPORTED, "prefixes reach 2^31 keys");
+  const int slots = prefix_splits + num_splits;
+  if (slots > 4096) return fail(SINKATTN_UNSUPPORTED, "%d splits in all exceed 4096", slots);
+  size_t need = 0;
+  rc = sinkattn_decode_shared_workspace_bytes(batch, q_len, num_qo_heads, head_dim, num_groups,
+                                              prefix_splits, num_splits, &need);
+  if (rc) return rc;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return fail(SINKATTN_INVALID_ARG, "workspace must be non-null and 256-byte aligned");
+  if (workspace_bytes < need)
+    return fail(SINKATTN_INVALID_ARG, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
+  if (!out || !aligned16(out)) return fail(SINKATTN_INVALID_ARG, "out must be non-null and 16-byte aligned");
+  if (lse && (reinterpret_cast<uintptr_t>(lse) & 3u))
+    return fail(SINKATTN_INVALID_ARG, "lse must be 4-byte aligned");
+  if (batch == 0) return SINKATTN_OK;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+
+  SharedPlan plan;
+  plan.kv = static_cast<int32_t*>(workspace);
+  plan.pages = plan.kv + batch + 1;
+  plan.grp_q = plan.pages + batch + 1;
+  plan.grp_k = plan.grp_q + num_groups + 1;
+  plan.grp_pages = plan.grp_k + num_groups + 1;
+  plan.row_pos = plan.grp_pages + num_groups + 1;
+  const size_t rows = static_cast<size_t>(batch) * q_len;
+  const size_t plan_bytes = shared_plan_bytes(batch, q_len, num_groups);
+  float* part_acc = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan_bytes);
+  float* part_md = reinterpret_cast<float*>(
+      reinterpret_cast<char*>(part_acc) +
+      ((rows * num_qo_heads * slots * head_dim * 4 + 255) & ~static_cast<size_t>(255)));
+  rc = launch_shared_plan(kv_indptr, pg.page_indptr, group_indptr, prefix_lens, num_groups,
+                          pg.page_size, batch, q_len, max_prefix_len, max_suffix_len, plan, s);
+  if (rc) return rc;
+
+  a.part_acc = part_acc;
+  a.part_md = part_md;
+  a.part_slots = slots;
+  if (prefix_splits > 0) {
+    AttnArgs pa = a;
+    PagedKv shared = pg;
+    shared.page_indptr = plan.grp_pages;
+    set_paged(&pa, &shared);
+    pa.cu_q = plan.grp_q;
+    pa.cu_k = plan.grp_k;
+    pa.batch = num_groups;
+    pa.q_len = 0;
+    pa.max_q = static_cast<int32_t>(rows);
+    pa.max_kv = max_prefix_len;
+    pa.total_q = static_cast<int32_t>(rows);
+    pa.causal = 0;
+    pa.num_splits = prefix_splits;
+    pa.free_rows = 1;
+    pa.row_pos = window > 0 ? plan.row_pos : nullptr;
+    if ((rc = launch_attn_mma(pa, s))) return rc;
+  }
+  PagedKv own = pg;
+  own.page_indptr = plan.pages;
+  set_paged(&a, &own);
+  a.cu_k = plan.kv;
+  a.part_first = prefix_splits;
+  if ((rc = launch_partials(a, s))) return rc;
+  return launch_merge(part_acc, part_md, sinks, static_cast<int32_t>(rows), num_qo_heads, head_dim,
+                      slots, out, lse, s, true);
+}
+
 }  // namespace
 
 extern "C" {
@@ -482,6 +595,73 @@ int sinkattn_decode_fp8(const void* q, const void* k, const void* v, const float
   return decode_impl(q, k, v, kv_indptr, nullptr, batch, q_len, max_kv_len, num_qo_heads,
                      num_kv_heads, head_dim, sm_scale, causal, window, num_splits, sinks,
                      workspace, workspace_bytes, out, lse, stream, &f8);
+}
+
+int sinkattn_decode_shared_paged(
+    const void* q, const void* k_pages, const void* v_pages, const int32_t* kv_indptr,
+    const int32_t* page_indptr, const int32_t* page_indices, const int32_t* group_indptr,
+    const int32_t* prefix_lens, int32_t num_groups, int32_t num_pages, int32_t page_size,
+    int32_t batch, int32_t q_len, int32_t max_prefix_len, int32_t max_suffix_len,
+    int32_t num_qo_heads, int32_t num_kv_heads, int32_t head_dim, float sm_scale, int32_t causal,
+    int32_t window, int32_t prefix_splits, int32_t num_splits, const float* sinks,
+    void* workspace, size_t workspace_bytes, void* out, float* lse, void* stream) {
+  const PagedKv pg{page_indptr, page_indices, num_pages, page_size};
+  return decode_shared_impl(q, k_pages, v_pages, nullptr, kv_indptr, pg, group_indptr, prefix_lens,
+                            num_groups, batch, q_len, max_prefix_len, max_suffix_len, num_qo_heads,
+                            num_kv_heads, head_dim, sm_scale, causal, window, prefix_splits,
+                            num_splits, sinks, workspace, workspace_bytes, out, lse, stream);
+}
+
+int sinkattn_decode_shared_paged_fp8(
+    const void* q, const void* k_pages, const void* v_pages, const float* k_scale,
+    const float* v_scale, const int32_t* kv_indptr, const int32_t* page_indptr,
+    const int32_t* page_indices, const int32_t* group_indptr, const int32_t* prefix_lens,
+    int32_t num_groups, int32_t num_pages, int32_t page_size, int32_t batch, int32_t q_len,
+    int32_t max_prefix_len, int32_t max_suffix_len, int32_t num_qo_heads, int32_t num_kv_heads,
+    int32_t head_dim, float sm_scale, int32_t causal, int32_t window, int32_t prefix_splits,
+    int32_t num_splits, const float* sinks, void* workspace, size_t workspace_bytes, void* out,
+    float* lse, void* stream) {
+  const PagedKv pg{page_indptr, page_indices, num_pages, page_size};
+  const Fp8Kv f8{k_scale, v_scale};
+  return decode_shared_impl(q, k_pages, v_pages, &f8, kv_indptr, pg, group_indptr, prefix_lens,
+                            num_groups, batch, q_len, max_prefix_len, max_suffix_len, num_qo_heads,
+                            num_kv_heads, head_dim, sm_scale, causal, window, prefix_splits,
+                            num_splits, sinks, workspace, workspace_bytes, out, lse, stream);
+}
+
+int sinkattn_decode_shared_workspace_bytes(int32_t batch, int32_t q_len, int32_t num_qo_heads,
+                                           int32_t head_dim, int32_t num_groups,
+                                           int32_t prefix_splits, int32_t num_splits,
+                                           size_t* bytes) {
+  g_last_error[0] = '\0';
+  if (num_groups < 1 || prefix_splits < 0) return fail(SINKATTN_INVALID_ARG, "bad sizes");
+  if (static_cast<int64_t>(prefix_splits) + num_splits > 4096)
+    return fail(SINKATTN_UNSUPPORTED, "the splits exceed 4096 in all");
+  const int rc = sinkattn_decode_workspace_bytes(batch, q_len, num_qo_heads, head_dim,
+                                                 prefix_splits + num_splits, bytes);
+  if (rc) return rc;
+  if (num_splits < 1) return fail(SINKATTN_INVALID_ARG, "bad sizes");
+  *bytes += shared_plan_bytes(batch, q_len, num_groups);
+  return SINKATTN_OK;
+}
+
+int sinkattn_decode_shared_default_splits(int32_t batch, int32_t q_len, int32_t num_qo_heads,
+                                          int32_t num_kv_heads, int32_t head_dim,
+                                          int32_t num_groups, int32_t max_prefix_len,
+                                          int32_t max_suffix_len, int32_t* prefix_splits,
+                                          int32_t* num_splits) {
+  g_last_error[0] = '\0';
+  if (!prefix_splits || !num_splits)
+    return fail(SINKATTN_INVALID_ARG, "prefix_splits and num_splits must be non-null");
+  if (num_groups < 1 || max_prefix_len < 0) return fail(SINKATTN_INVALID_ARG, "bad sizes");
+  int rc = sinkattn_decode_default_splits(batch, q_len, num_qo_heads, num_kv_heads, head_dim,
+                                          max_suffix_len, num_splits);
+  if (rc) return rc;
+  // the prefix as a batch of blocks of 64 query rows
+  const int64_t rows = static_cast<int64_t>(batch) * q_len * num_qo_heads / num_kv_heads;
+  const int64_t blocks = std::min<int64_t>(num_groups + rows / 64, int64_t{1} << 20);
+  return sinkattn_decode_default_splits(static_cast<int32_t>(blocks), 1, num_qo_heads, num_kv_heads,
+                                        head_dim, max_prefix_len, prefix_splits);
 }
 
 int sinkattn_set_prefill_kernel(int kind) {
@@ -623,12 +803,12 @@ int sinkattn_debug_status(void* stream, int* status) {
   g_last_error[0] = '\0';
   if (!status) return fail(SINKATTN_INVALID_ARG, "status must be non-null");
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  int a = 0, m = 0, t = 0, dt = 0;
+  int a = 0, m = 0, t = 0, dt = 0, sh = 0, pg = 0;
   if (read_status_attn_mma(s, &a) || read_status_merge(s, &m) || read_status_prefill_tc(s, &t) ||
-      read_status_decode_tc(s, &dt))
+      read_status_decode_tc(s, &dt) || read_status_shared(s, &sh) || read_status_pages(s, &pg))
     return fail(SINKATTN_CUDA_ERROR, "reading the device status failed: %s",
                 cudaGetErrorString(cudaGetLastError()));
-  *status = a ? a : (dt ? dt : (t ? t : m));
+  *status = a ? a : (dt ? dt : (t ? t : (m ? m : (sh ? sh : pg))));
   return SINKATTN_OK;
 }
 

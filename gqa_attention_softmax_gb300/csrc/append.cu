@@ -1,0 +1,158 @@
+// Writes new keys and values into the pages of a paged cache, as bf16 or as
+// e4m3 codes under one scale per KV head (rules: sinkattn.h).
+//
+// One pass, bound by HBM: each thread takes one 16-byte run of a pool row in
+// K and the same run in V, so a row (head_dim elements of one head of one
+// token) is written in full 16-byte lanes, and consecutive lanes read
+// consecutive heads of the token. With codes a thread reads two 16-byte runs
+// per pool instead of one. Quotients are IEEE divisions (the code is then the
+// one nearest to the fp32 quotient, whatever the scale), which the loads hide.
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace sinkattn {
+
+namespace {
+
+struct AppendParams {
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
+  long long k_stride, v_stride;   // elements between tokens
+  const int32_t* slots;
+  const float* k_scale;
+  const float* v_scale;
+  uint8_t* k_pages;
+  uint8_t* v_pages;
+  int tokens, Hkv, shift;         // page size = 1 << shift
+  long long n_slots;
+};
+
+// Sixteen bf16 (two 16-byte vectors) -> sixteen e4m3 codes of x / scale.
+__device__ __forceinline__ uint32_t codes4(uint32_t lo, uint32_t hi, float scale) {
+  const float a = __fdiv_rn(__uint_as_float(lo << 16), scale);
+  const float b = __fdiv_rn(__uint_as_float(lo & 0xffff0000u), scale);
+  const float c = __fdiv_rn(__uint_as_float(hi << 16), scale);
+  const float d = __fdiv_rn(__uint_as_float(hi & 0xffff0000u), scale);
+  uint16_t x, y;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(x) : "f"(b), "f"(a));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(y) : "f"(d), "f"(c));
+  return static_cast<uint32_t>(x) | (static_cast<uint32_t>(y) << 16);
+}
+
+__device__ __forceinline__ uint4 codes16(uint4 a, uint4 b, float scale) {
+  return make_uint4(codes4(a.x, a.y, scale), codes4(a.z, a.w, scale), codes4(b.x, b.y, scale),
+                    codes4(b.z, b.w, scale));
+}
+
+template <int D, bool FP8>
+__global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
+  constexpr int EL = FP8 ? 16 : 8;         // elements of a thread's 16-byte run in a pool
+  constexpr int RUNS = D / EL;
+  constexpr int ROW = D * (FP8 ? 1 : 2);   // bytes of a pool row
+  const int per = p.Hkv * RUNS;
+  const long long n = static_cast<long long>(p.tokens) * per;
+  const long long step = static_cast<long long>(gridDim.x) * blockDim.x;
+  for (long long u = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; u < n;
+       u += step) {
+    const int tok = static_cast<int>(u / per), r = static_cast<int>(u - static_cast<long long>(tok) * per);
+    const int h = r / RUNS, c = r % RUNS;
+    const int slot = p.slots[tok];
+    const uint4* ks = reinterpret_cast<const uint4*>(p.k + tok * p.k_stride + r * EL);
+    const uint4* vs = reinterpret_cast<const uint4*>(p.v + tok * p.v_stride + r * EL);
+    uint4 k = __ldcs(ks), v = __ldcs(vs);
+    if constexpr (FP8) {
+      const uint4 k2 = __ldcs(ks + 1), v2 = __ldcs(vs + 1);
+      k = codes16(k, k2, p.k_scale[h]);
+      v = codes16(v, v2, p.v_scale[h]);
+    }
+    if (slot < 0 || slot >= p.n_slots) continue;   // a padding token
+    const long long row =
+        ((static_cast<long long>(slot >> p.shift) * p.Hkv + h) << p.shift) + (slot & ((1 << p.shift) - 1));
+    *reinterpret_cast<uint4*>(p.k_pages + row * ROW + c * 16) = k;
+    *reinterpret_cast<uint4*>(p.v_pages + row * ROW + c * 16) = v;
+  }
+}
+
+int refuse(int status, const char* text) {
+  set_error("%s", text);
+  return status;
+}
+
+bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+
+int append(const void* k, const void* v, int64_t k_stride, int64_t v_stride, const int32_t* slots,
+           int32_t tokens, const float* k_scale, const float* v_scale, bool fp8, void* k_pages,
+           void* v_pages, int32_t num_pages, int32_t page_size, int32_t Hkv, int32_t d,
+           void* stream) {
+  set_error("%s", "");
+  if (tokens < 0) return refuse(SINKATTN_INVALID_ARG, "tokens must be non-negative");
+  if (!k_pages || !v_pages || !aligned(k_pages, 16) || !aligned(v_pages, 16))
+    return refuse(SINKATTN_INVALID_ARG, "k_pages and v_pages must be non-null and 16-byte aligned");
+  if (Hkv < 1 || num_pages < 1)
+    return refuse(SINKATTN_INVALID_ARG, "num_kv_heads and num_pages must be positive");
+  if (d != 64 && d != 128) return refuse(SINKATTN_UNSUPPORTED, "head_dim is not 64 or 128");
+  if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1)))
+    return refuse(SINKATTN_UNSUPPORTED, "page_size is not a power of two in [16, 256]");
+  if (static_cast<int64_t>(num_pages) * Hkv * page_size >= (int64_t{1} << 31))
+    return refuse(SINKATTN_UNSUPPORTED, "page pools exceed 2^31 rows");
+  if (fp8 && (!k_scale || !v_scale || !aligned(k_scale, 4) || !aligned(v_scale, 4)))
+    return refuse(SINKATTN_INVALID_ARG, "k_scale and v_scale must be non-null and 4-byte aligned");
+  if (tokens == 0) return SINKATTN_OK;
+  if (!k || !v || !aligned(k, 16) || !aligned(v, 16) || !slots || !aligned(slots, 4))
+    return refuse(SINKATTN_INVALID_ARG,
+                  "k and v must be non-null and 16-byte aligned, slots 4-byte aligned");
+  const int64_t width = static_cast<int64_t>(Hkv) * d;
+  if (k_stride < width || v_stride < width || k_stride % 8 || v_stride % 8)
+    return refuse(SINKATTN_INVALID_ARG,
+                  "k_stride and v_stride must be multiples of 8 and at least num_kv_heads * head_dim");
+  AppendParams p{};
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.slots = slots;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.k_pages = static_cast<uint8_t*>(k_pages);
+  p.v_pages = static_cast<uint8_t*>(v_pages);
+  p.tokens = tokens;
+  p.Hkv = Hkv;
+  while ((1 << p.shift) < page_size) ++p.shift;
+  p.n_slots = static_cast<long long>(num_pages) * page_size;
+  const int64_t units = tokens * (width / (fp8 ? 16 : 8));
+  const unsigned blocks =
+      static_cast<unsigned>(std::min<int64_t>((units + 255) / 256, int64_t{1} << 30));
+  auto kern = d == 64 ? (fp8 ? append_kernel<64, true> : append_kernel<64, false>)
+                      : (fp8 ? append_kernel<128, true> : append_kernel<128, false>);
+  kern<<<blocks, 256, 0, static_cast<cudaStream_t>(stream)>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) return SINKATTN_OK;
+  set_error("append launch: %s", cudaGetErrorString(e));
+  return SINKATTN_CUDA_ERROR;
+}
+
+}  // namespace
+}  // namespace sinkattn
+
+extern "C" {
+
+int sinkattn_append_paged(const void* k, const void* v, int64_t k_stride, int64_t v_stride,
+                          const int32_t* slots, int32_t tokens, void* k_pages, void* v_pages,
+                          int32_t num_pages, int32_t page_size, int32_t num_kv_heads,
+                          int32_t head_dim, void* stream) {
+  return sinkattn::append(k, v, k_stride, v_stride, slots, tokens, nullptr, nullptr, false, k_pages,
+                          v_pages, num_pages, page_size, num_kv_heads, head_dim, stream);
+}
+
+int sinkattn_append_paged_fp8(const void* k, const void* v, int64_t k_stride, int64_t v_stride,
+                              const int32_t* slots, int32_t tokens, const float* k_scale,
+                              const float* v_scale, void* k_pages, void* v_pages,
+                              int32_t num_pages, int32_t page_size, int32_t num_kv_heads,
+                              int32_t head_dim, void* stream) {
+  return sinkattn::append(k, v, k_stride, v_stride, slots, tokens, k_scale, v_scale, true, k_pages,
+                          v_pages, num_pages, page_size, num_kv_heads, head_dim, stream);
+}
+
+}  // extern "C"

@@ -41,7 +41,7 @@
 // partials read through distributed shared memory, seeded with the sink, and
 // writes out and lse; a second cluster barrier keeps every CTA's shared
 // memory alive until its peers have read it. No partials go to HBM.
-#include <cstdio>
+#include <algorithm>
 
 #include "common.cuh"
 #include "internal.h"
@@ -64,6 +64,9 @@ struct MmaParams {
   int causal, window;
   float* part_acc;
   float* part_md;
+  int part_slots, part_first;
+  int free_rows;
+  const int32_t* row_pos;
   const float* sinks;     // fused mode
   __nv_bfloat16* out;     // fused mode
   float* lse;             // fused mode
@@ -143,7 +146,7 @@ __global__ void __launch_bounds__(MmaCfg<D, RT, TG, KT, NST, FP8>::THREADS,
   const int q0 = qb * p.QB;
   if (q0 >= Lq) return;   // uniform over the CTA (and the cluster), before any barrier
   const int nq = min(p.QB, Lq - q0);
-  if (threadIdx.x == 0 && (Lk < Lq || Lk > p.max_kv || Lq < 0))
+  if (threadIdx.x == 0 && ((Lk < Lq && !p.free_rows) || Lk > p.max_kv || Lq < 0))
     atomicExch(&g_status_attn_mma, SINKATTN_BAD_LENGTHS);
 
   // Positions of the CTA's first and last query (queries are the last Lq keys).
@@ -155,7 +158,7 @@ __global__ void __launch_bounds__(MmaCfg<D, RT, TG, KT, NST, FP8>::THREADS,
   int k_lo = min(split * chunk, Lk);
   int k_hi = min(k_lo + chunk, Lk);
   if (p.causal) k_hi = min(k_hi, posN + 1);
-  if (p.window > 0) k_lo = max(k_lo, pos0 - p.window + 1);
+  if (p.window > 0 && !p.row_pos) k_lo = max(k_lo, pos0 - p.window + 1);
   // Tiles end at k_hi (contiguous: no copy reads past the last key needed),
   // or start on a multiple of KT (paged: no box straddles a page).
   const bool paged = p.page_size > 0;
@@ -284,8 +287,8 @@ __global__ void __launch_bounds__(MmaCfg<D, RT, TG, KT, NST, FP8>::THREADS,
     const int r = rt * 16 + (lane >> 2) + 8 * i;
     const int tl = r / G;
     valid[i] = tl < nq;
-    pos[i] = pos0 + tl;
     tok[i] = q_start + q0 + tl;
+    pos[i] = p.row_pos && valid[i] ? p.row_pos[tok[i]] : pos0 + tl;
     head[i] = kvh * G + (r - tl * G);
   }
 
@@ -397,7 +400,7 @@ __global__ void __launch_bounds__(MmaCfg<D, RT, TG, KT, NST, FP8>::THREADS,
 
     // Mask (skipped for tiles that every row sees whole).
     const bool whole = (j0 >= k_lo) && (j0 + KT <= k_hi) && (!p.causal || j0 + KT - 1 <= pos0) &&
-                       (p.window <= 0 || j0 > posN - p.window);
+                       (p.window <= 0 || (j0 > posN - p.window && !p.row_pos));
     if (!whole) {
 #pragma unroll
       for (int j = 0; j < KT / 8; ++j) {
@@ -557,7 +560,8 @@ __global__ void __launch_bounds__(MmaCfg<D, RT, TG, KT, NST, FP8>::THREADS,
     for (int i = 0; i < 2; ++i) {
       if (!valid[i]) continue;
       const size_t rowid = static_cast<size_t>(tok[i]) * p.Hq + head[i];
-      float* arow = p.part_acc + (rowid * S + split) * D;
+      const size_t slot = rowid * p.part_slots + p.part_first + split;
+      float* arow = p.part_acc + slot * D;
 #pragma unroll
       for (int jd = 0; jd < D / 8; ++jd) {
         const int col = jd * 8 + (lane & 3) * 2;
@@ -568,7 +572,7 @@ __global__ void __launch_bounds__(MmaCfg<D, RT, TG, KT, NST, FP8>::THREADS,
         float2 md;
         md.x = (m[i] == NEG_INF) ? NEG_INF : m[i] * (p.sm_scale * kscale);
         md.y = l[i];
-        *reinterpret_cast<float2*>(p.part_md + (rowid * S + split) * 2) = md;
+        *reinterpret_cast<float2*>(p.part_md + slot * 2) = md;
       }
     }
   }
@@ -682,8 +686,8 @@ static int launch_cfg(const AttnArgs& a, cudaStream_t stream) {
   p.Hq = a.Hq;
   p.Hkv = a.Hkv;
   p.G = a.Hq / a.Hkv;
-  p.QB = (a.q_len * p.G <= 16 * RT) ? a.q_len : (16 * RT) / p.G;
   const int maxq = a.cu_q ? a.max_q : a.q_len;
+  p.QB = std::min(maxq, (16 * RT) / p.G);
   p.nqb = (maxq + p.QB - 1) / p.QB;
   p.num_splits = a.num_splits;
   p.max_kv = a.max_kv;
@@ -693,6 +697,10 @@ static int launch_cfg(const AttnArgs& a, cudaStream_t stream) {
   p.window = a.window;
   p.part_acc = a.part_acc;
   p.part_md = a.part_md;
+  p.part_slots = part_slots(a);
+  p.part_first = a.part_first;
+  p.free_rows = a.free_rows;
+  p.row_pos = a.row_pos;
   p.page_size = a.page_size;
   p.box_rows = box;
   p.page_indptr = a.page_indptr;
@@ -748,8 +756,8 @@ static int launch_cfg(const AttnArgs& a, cudaStream_t stream) {
 template <bool FUSED, bool FP8>
 static int launch_attn_mma_t(const AttnArgs& a, cudaStream_t stream) {
   const int G = a.Hq / a.Hkv;
-  const int rows = G * a.q_len;
-  const int rt_needed = (rows + 15) / 16;
+  const int64_t rows = static_cast<int64_t>(G) * (a.cu_q ? a.max_q : a.q_len);
+  const int64_t rt_needed = (rows + 15) / 16;
   if (G > 64) {
     set_error("GQA group of %d query heads exceeds 64 rows per CTA", G);
     return SINKATTN_UNSUPPORTED;

@@ -37,6 +37,7 @@ struct DtcParams {
   int causal, window;
   float* part_acc;
   float* part_md;
+  int part_slots, part_first;
   // paged KV (page_size > 0): page-pool rows, boxes of box_rows keys
   int page_size, box_rows;
   const int32_t* page_indptr;
@@ -640,7 +641,6 @@ __global__ void __launch_bounds__(DtcCfg<RR, FP8>::THREADS, 1)
     const int tl = row / G;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     float* stage = reinterpret_cast<float*>(smem + C::OFF_STG);
-    const int S = p.num_splits;
     const uint64_t keep_policy = policy_evict_last();
     for (int k = 0; k < n_mine; ++k) {
       const DtcItem t = item_of(k);
@@ -680,7 +680,7 @@ __global__ void __launch_bounds__(DtcCfg<RR, FP8>::THREADS, 1)
           md.x = mlr.x * lscale + (lg2(mlr.y) - lg2(mlr.z)) * kLn2;
           md.y = mlr.z;
         }
-        *reinterpret_cast<float2*>(p.part_md + (rowid * S + t.split) * 2) = md;
+        *reinterpret_cast<float2*>(p.part_md + (rowid * p.part_slots + p.part_first + t.split) * 2) = md;
       }
       named_barrier_sync(1, 128);   // staging written
       const int nrows = t.nq * G;
@@ -691,7 +691,7 @@ __global__ void __launch_bounds__(DtcCfg<RR, FP8>::THREADS, 1)
         const float4 val = *reinterpret_cast<const float4*>(stage + r * C::XS + lane * 4);
         // kept in L2 as long as possible: the merge reads the newest partials first
         asm volatile("st.global.L2::cache_hint.v4.f32 [%0], {%1, %2, %3, %4}, %5;" ::"l"(
-                         p.part_acc + (rowid * S + t.split) * D + lane * 4),
+                         p.part_acc + (rowid * p.part_slots + p.part_first + t.split) * D + lane * 4),
                      "f"(val.x), "f"(val.y), "f"(val.z), "f"(val.w), "l"(keep_policy)
                      : "memory");
       }
@@ -769,6 +769,8 @@ static int launch_dtc(const AttnArgs& a, int QB, cudaStream_t stream) {
   p.window = a.window;
   p.part_acc = a.part_acc;
   p.part_md = a.part_md;
+  p.part_slots = part_slots(a);
+  p.part_first = a.part_first;
   auto kern = decode_tc_kernel<RR, PAGED, FP8>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) {

@@ -25,9 +25,16 @@ struct AttnArgs {
   const float* sinks;
   void* out;
   float* lse;
-  // split mode
+  // split mode: chunk s of a row is slot part_first + s of the row's
+  // part_slots partials (0: num_splits, this call writes all of them)
   float* part_acc;
   float* part_md;
+  int32_t part_slots, part_first;
+  // rows that are not the last queries of the keys they see (a shared prefix):
+  // any number of rows per key, and with a window the position of each query
+  // token counted from the first key (nullptr: no window)
+  int32_t free_rows;
+  const int32_t* row_pos;
   // paged KV (page_size > 0): k and v are page pools [num_pages, Hkv, page_size, d];
   // sequence b's keys [e * page_size, (e + 1) * page_size) live in page
   // page_indices[page_indptr[b] + e]; cu_k still gives the key counts
@@ -56,6 +63,9 @@ inline int kv_box_rows(const AttnArgs& a, int tile_keys) {
   const int pow2 = tile_keys & -tile_keys;
   return a.page_size < pow2 ? a.page_size : pow2;
 }
+
+// Partials of a row, this call's or shared with another call's.
+inline int part_slots(const AttnArgs& a) { return a.part_slots > 0 ? a.part_slots : a.num_splits; }
 
 // Encodes a 2-D tensor map over a [rows, d] bf16 buffer with [box_rows, 64]
 // boxes and 128-byte swizzling. Returns 0 or a SINKATTN_* status.
@@ -97,7 +107,27 @@ int launch_merge(const float* part_acc, const float* part_md, const float* sinks
                  int32_t Hq, int32_t d, int32_t num_splits, void* out, float* lse,
                  cudaStream_t stream, bool drop_partials);
 
+// Shared-prefix decode: what the prefix and the per-sequence passes read,
+// derived on the device from the page lists and the groups. All int32.
+struct SharedPlan {
+  int32_t* kv;        // [batch + 1] running sum of the sequences' own keys
+  int32_t* pages;     // [batch + 1] first entry of their own pages in page_indices
+  int32_t* grp_q;     // [groups + 1] first query token of each group
+  int32_t* grp_k;     // [groups + 1] running sum of the prefixes' keys
+  int32_t* grp_pages; // [groups + 1] first entry of the prefixes' pages
+  int32_t* row_pos;   // [batch * q_len] position of each query token
+};
+inline size_t shared_plan_ints(int64_t batch, int64_t q_len, int64_t groups) {
+  return static_cast<size_t>(2 * (batch + 1) + 3 * (groups + 1) + batch * q_len);
+}
+int launch_shared_plan(const int32_t* kv_indptr, const int32_t* page_indptr,
+                       const int32_t* group_indptr, const int32_t* prefix_lens, int32_t groups,
+                       int32_t page_size, int32_t batch, int32_t q_len, int32_t max_prefix,
+                       int32_t max_suffix, const SharedPlan& plan, cudaStream_t stream);
+
 // Reads and clears the device status word of one translation unit.
+int read_status_pages(cudaStream_t s, int* status);
+int read_status_shared(cudaStream_t s, int* status);
 int read_status_attn_mma(cudaStream_t s, int* status);
 int read_status_merge(cudaStream_t s, int* status);
 int read_status_prefill_tc(cudaStream_t s, int* status);

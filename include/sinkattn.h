@@ -74,7 +74,9 @@ enum sinkattn_status {
   SINKATTN_UNSUPPORTED = 2,  /* head_dim not 64/128, Hq % Hkv != 0, window without causal */
   SINKATTN_CUDA_ERROR = 3,   /* a CUDA runtime/driver call or launch failed */
   SINKATTN_TIMEOUT = 4,      /* device status: a bounded wait inside a kernel gave up */
-  SINKATTN_BAD_LENGTHS = 5   /* device status: cu_seqlens/kv_indptr contradict the host sizes */
+  SINKATTN_BAD_LENGTHS = 5,  /* device status: cu_seqlens/kv_indptr contradict the host sizes */
+  SINKATTN_OUT_OF_PAGES = 6, /* device status: a page table had fewer free pages than a call needs */
+  SINKATTN_BAD_PAGES = 7     /* device status: sequence ids or lengths a page table cannot serve */
 };
 
 /*
@@ -351,6 +353,189 @@ SINKATTN_API int sinkattn_decode_fp8(const void* q, const void* k, const void* v
                                      size_t workspace_bytes, void* out, float* lse,
                                      void* stream);
 
+/*
+ * Decode over a paged cache whose sequences share prefixes: the same result as
+ * sinkattn_decode_paged over the same page lists, with the shared pages read
+ * and multiplied once for all sequences that share them. The partials and
+ * the merge are those of split-KV decode, so the sink counts once.
+ *   The batch is cut into num_groups runs of consecutive sequences:
+ *   group_indptr int32 [num_groups + 1] (device; group g holds sequences
+ *   group_indptr[g] .. group_indptr[g+1] - 1, group_indptr[0] = 0,
+ *   group_indptr[num_groups] = batch, non-decreasing), and
+ *   prefix_lens int32 [num_groups] (device): the first prefix_lens[g] keys of
+ *   every sequence of group g are the same, a multiple of page_size (0: the
+ *   group shares nothing). They are read from the first sequence's page list;
+ *   every list still holds all of its own sequence's pages.
+ *   Each sequence needs Lk_b >= prefix_lens[g] + q_len (the drafts' own keys
+ *   are not shared), so every query sees the whole prefix but for the window.
+ *   max_prefix_len / max_suffix_len (host) bound prefix_lens[g] and
+ *   Lk_b - prefix_lens[g]; lengths that break one of these rules make the
+ *   call record SINKATTN_BAD_LENGTHS and treat the sequence's or group's own
+ *   part as empty (sinkattn_debug_status).
+ *   prefix_splits / num_splits: KV chunks of a prefix and of a sequence's own
+ *   keys; <= 0 selects sinkattn_decode_shared_default_splits().
+ *   workspace: at least sinkattn_decode_shared_workspace_bytes() bytes for
+ *   the split counts in use, 256-byte aligned, device memory; contents on
+ *   entry do not matter. Two calls that may overlap need two workspaces.
+ * Every other argument and rule is that of sinkattn_decode_paged
+ * (num_kv_heads groups of at most 64 query heads). The _fp8 form reads pools
+ * of e4m3 codes, uint8 [num_pages, Hkv, page_size, d], with the scales and
+ * rules of sinkattn_decode_fp8.
+ */
+SINKATTN_API int sinkattn_decode_shared_paged(
+    const void* q, const void* k_pages, const void* v_pages, const int32_t* kv_indptr,
+    const int32_t* page_indptr, const int32_t* page_indices, const int32_t* group_indptr,
+    const int32_t* prefix_lens, int32_t num_groups, int32_t num_pages, int32_t page_size,
+    int32_t batch, int32_t q_len, int32_t max_prefix_len, int32_t max_suffix_len,
+    int32_t num_qo_heads, int32_t num_kv_heads, int32_t head_dim, float sm_scale, int32_t causal,
+    int32_t window, int32_t prefix_splits, int32_t num_splits, const float* sinks,
+    void* workspace, size_t workspace_bytes, void* out, float* lse, void* stream);
+SINKATTN_API int sinkattn_decode_shared_paged_fp8(
+    const void* q, const void* k_pages, const void* v_pages, const float* k_scale,
+    const float* v_scale, const int32_t* kv_indptr, const int32_t* page_indptr,
+    const int32_t* page_indices, const int32_t* group_indptr, const int32_t* prefix_lens,
+    int32_t num_groups, int32_t num_pages, int32_t page_size, int32_t batch, int32_t q_len,
+    int32_t max_prefix_len, int32_t max_suffix_len, int32_t num_qo_heads, int32_t num_kv_heads,
+    int32_t head_dim, float sm_scale, int32_t causal, int32_t window, int32_t prefix_splits,
+    int32_t num_splits, const float* sinks, void* workspace, size_t workspace_bytes, void* out,
+    float* lse, void* stream);
+
+/* Workspace bytes of the shared-prefix decode for these sizes (host only, no CUDA call). */
+SINKATTN_API int sinkattn_decode_shared_workspace_bytes(int32_t batch, int32_t q_len,
+                                                        int32_t num_qo_heads, int32_t head_dim,
+                                                        int32_t num_groups, int32_t prefix_splits,
+                                                        int32_t num_splits, size_t* bytes);
+
+/* The split counts the shared-prefix decode uses when given <= 0 (host only). */
+SINKATTN_API int sinkattn_decode_shared_default_splits(
+    int32_t batch, int32_t q_len, int32_t num_qo_heads, int32_t num_kv_heads, int32_t head_dim,
+    int32_t num_groups, int32_t max_prefix_len, int32_t max_suffix_len, int32_t* prefix_splits,
+    int32_t* num_splits);
+
+/*
+ * Writes new keys and values into page pools.
+ *   k, v: bf16 [tokens, Hkv, d] (device), rows of one token contiguous, token
+ *     i at element i * k_stride (v_stride): multiples of 8 and at least
+ *     Hkv * d, so slices of a fused projection's output need no copy;
+ *   slots: int32 [tokens] (device), slot = page * page_size + position in the
+ *     page, as sinkattn_pages_reserve gives them; a token whose slot lies
+ *     outside [0, num_pages * page_size) is left out (padding: -1);
+ *   k_pages, v_pages: the pools, bf16 [num_pages, Hkv, page_size, d], or for
+ *     the _fp8 form uint8 e4m3 codes of the same shape: the code is the e4m3
+ *     value nearest to x / scale[head] (the fp32 quotient; ties to even; beyond
+ *     +-448 the largest code of that sign; NaN the NaN code).
+ * Two tokens with the same slot leave one of the two rows' elements.
+ */
+SINKATTN_API int sinkattn_append_paged(const void* k, const void* v, int64_t k_stride,
+                                       int64_t v_stride, const int32_t* slots, int32_t tokens,
+                                       void* k_pages, void* v_pages, int32_t num_pages,
+                                       int32_t page_size, int32_t num_kv_heads, int32_t head_dim,
+                                       void* stream);
+SINKATTN_API int sinkattn_append_paged_fp8(const void* k, const void* v, int64_t k_stride,
+                                           int64_t v_stride, const int32_t* slots, int32_t tokens,
+                                           const float* k_scale, const float* v_scale,
+                                           void* k_pages, void* v_pages, int32_t num_pages,
+                                           int32_t page_size, int32_t num_kv_heads,
+                                           int32_t head_dim, void* stream);
+
+/*
+ * Page tables: which pages each sequence holds, how many sequences hold each
+ * page, and which pages are free. One table serves all layers of a cache
+ * (page p is page p of every layer's pools).
+ * A table is one int32 device buffer of sinkattn_pages_table_ints() words,
+ * 16-byte aligned, owned by the caller:
+ *   word 0                 number of free pages (words 1 .. 15: scratch)
+ *   seq_lens  [max_seqs]             tokens of each sequence
+ *   page_list [max_seqs][max_pages]  its pages in order; -1 past the last
+ *   refcount  [num_pages]            lists that hold the page
+ *   free_list [num_pages]            the free pages are its first word-0 entries
+ *   scratch   [7 * max_seqs + 2 * num_pages]
+ * The j-th page that a call takes is free_list[count - 1 - j]; the j-th of K
+ * pages that it gives back goes to free_list[count + K - 1 - j]: results do
+ * not depend on timing. sinkattn_pages_init makes every page free (the first
+ * page taken is page 0) and every sequence empty.
+ * A call that cannot be served as a whole changes nothing and records
+ * SINKATTN_OUT_OF_PAGES, SINKATTN_BAD_PAGES (an id outside [0, max_seqs), an
+ * id twice, a length the table cannot hold) or SINKATTN_BAD_LENGTHS (cu_new
+ * contradicts total_new); see sinkattn_debug_status. Calls on one table must
+ * be ordered (one stream, or events); max_seqs * max_pages < 2^31, page_size
+ * as for the paged attention.
+ * Where a call copies pages it takes the pools of all layers:
+ *   k_pages, v_pages [num_layers][num_pages][Hkv][page_size] rows of
+ *   row_bytes bytes (d * 2, or d for codes; a multiple of 16), one layer
+ *   layer_stride bytes after the other (a multiple of 16, at least one
+ *   layer's bytes unless num_layers is 1).
+ */
+SINKATTN_API int sinkattn_pages_table_ints(int32_t num_pages, int32_t max_seqs, int32_t max_pages,
+                                           int64_t* ints);
+SINKATTN_API int sinkattn_pages_init(int32_t* table, int32_t num_pages, int32_t page_size,
+                                     int32_t max_seqs, int32_t max_pages, void* stream);
+
+/*
+ * Room for new tokens at the ends of n sequences: sequence seq_ids[i] grows by
+ * cu_new[i+1] - cu_new[i] tokens (seq_ids int32 [n], cu_new int32 [n + 1],
+ * device; total_new = cu_new[n], host), taking pages in the order of i, and
+ * slots [total_new] (device) gets each new token's slot. A sequence that
+ * starts inside a page that other sequences also hold first gets a page of
+ * its own, with the rows in use copied in every layer (copy on write): all
+ * writers do, except that when every holder writes in this call the first of
+ * them keeps the page. A call that cannot be served fills slots with -1.
+ */
+SINKATTN_API int sinkattn_pages_reserve(int32_t* table, int32_t num_pages, int32_t page_size,
+                                        int32_t max_seqs, int32_t max_pages,
+                                        const int32_t* seq_ids, const int32_t* cu_new, int32_t n,
+                                        int32_t total_new, void* k_pages, void* v_pages,
+                                        int32_t num_layers, int64_t layer_stride,
+                                        int32_t num_kv_heads, int32_t row_bytes, int32_t* slots,
+                                        void* stream);
+
+/*
+ * dst_ids[i] becomes a copy of src_ids[i] that shares all of its pages (the
+ * partly filled last one too: the first append to it copies it). The dst
+ * sequences must be empty, distinct and no src of the same call.
+ */
+SINKATTN_API int sinkattn_pages_fork(int32_t* table, int32_t num_pages, int32_t page_size,
+                                     int32_t max_seqs, int32_t max_pages, const int32_t* src_ids,
+                                     const int32_t* dst_ids, int32_t n, void* stream);
+
+/*
+ * Shortens seq_ids[i] to new_lens[i] tokens (0 <= new_lens[i] <= its length;
+ * new_lens NULL: 0, which frees the sequence). Pages past the new end leave
+ * its list; those that no list holds any more are free again, given back in
+ * the order (i, position in the list) of their first appearance.
+ */
+SINKATTN_API int sinkattn_pages_truncate(int32_t* table, int32_t num_pages, int32_t page_size,
+                                         int32_t max_seqs, int32_t max_pages,
+                                         const int32_t* seq_ids, const int32_t* new_lens,
+                                         int32_t n, void* stream);
+
+/*
+ * Packs the L pages in use into pages 0 .. L - 1: the live pages at or above L
+ * move, in order, into the free ones below L, in every layer; lists and
+ * reference counts follow, and the free list becomes num_pages - 1 .. L.
+ * page_map int32 [num_pages] (device): the new index of each old page, -1
+ * where it was free.
+ */
+SINKATTN_API int sinkattn_pages_compact(int32_t* table, int32_t num_pages, int32_t page_size,
+                                        int32_t max_seqs, int32_t max_pages, void* k_pages,
+                                        void* v_pages, int32_t num_layers, int64_t layer_stride,
+                                        int32_t num_kv_heads, int32_t row_bytes,
+                                        int32_t* page_map, void* stream);
+
+/*
+ * The paged attention's view of n sequences of a table: kv_indptr [n + 1] and
+ * page_indptr [n + 1] (running sums of lengths and of page counts), and their
+ * page lists one after the other in page_indices (capacity entries; what lies
+ * past the last list stays as it was). Lists that do not fit record
+ * SINKATTN_BAD_LENGTHS and are left out; an id outside the table counts as an
+ * empty sequence and records SINKATTN_BAD_PAGES.
+ */
+SINKATTN_API int sinkattn_pages_lists(const int32_t* table, int32_t num_pages, int32_t page_size,
+                                      int32_t max_seqs, int32_t max_pages,
+                                      const int32_t* seq_ids, int32_t n, int32_t* kv_indptr,
+                                      int32_t* page_indptr, int32_t* page_indices,
+                                      int32_t capacity, void* stream);
+
 /* Human-readable name of a status code (static string). */
 SINKATTN_API const char* sinkattn_status_string(int status);
 
@@ -360,7 +545,8 @@ SINKATTN_API const char* sinkattn_last_error(void);
 /*
  * Diagnostic, not for the hot path: synchronises `stream`, then reads and
  * clears the device status word of every kernel in the library. *status gets
- * SINKATTN_OK, SINKATTN_TIMEOUT or SINKATTN_BAD_LENGTHS. Returns
+ * SINKATTN_OK, SINKATTN_TIMEOUT, SINKATTN_BAD_LENGTHS, SINKATTN_OUT_OF_PAGES
+ * or SINKATTN_BAD_PAGES. Returns
  * SINKATTN_CUDA_ERROR if the synchronisation or the read failed.
  */
 SINKATTN_API int sinkattn_debug_status(void* stream, int* status);

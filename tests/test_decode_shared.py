@@ -1,0 +1,392 @@
+"""Shared-prefix decode over a paged cache, against the float64 oracle.
+
+The oracle attends each sequence's whole key range, contiguous; the CUDA path
+reads pages in random order in which the sequences of a group share their
+first pages, with unused slots and spare pages full of large finite values.
+
+Tolerances, per element. Every bf16 weight p_j is off by at most half a step
+(2^-8 of it), so sum p_j v_j / D by at most 2^-8 A with A = sum p_j |v_j| / D
+(the oracle's output for |v|), and the output's own rounding adds 2^-8 |out|.
+e4m3 caches use f16 weights (2^-11, and 2^-25 below f16's normal range). fp32
+sums of up to d products add, to each logit, at most d 2^-24 sum |q k| scale:
+below 6e-5 for unit normals at d 128; weights move by that much relatively.
+That bounds the log-sum-exp too (1e-4, with the exponential's 2^-21), times
+the scale that a case multiplies q with.
+"""
+import math
+import random
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import gqa_attention_softmax_gb300 as sa
+from gqa_attention_softmax_gb300._binding import BAD_LENGTHS, INVALID_ARG, UNSUPPORTED
+
+gpu = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from gqa_attention_softmax_gb300 import _build
+    _build.build()
+    oracle.build()
+    yield
+    if torch.cuda.is_available():
+        assert sa.sinkattn_debug_status() == 0
+
+
+def make(groups, q_len, Hq, Hkv, d, page, seed=0, q_scale=1.0, fp8=False):
+    """groups: [(prefix pages, [own keys of each sequence])]. CPU tensors: the
+    paged inputs, and the contiguous k, v the oracle reads."""
+    rng = random.Random(seed)
+    gen = torch.Generator().manual_seed(seed)
+    own = [n for _, lens in groups for n in lens]
+    lens = [pre * page + n for pre, ls in groups for n in ls]
+    B = len(own)
+    need = sum(pre for pre, _ in groups) + sum(-(-n // page) for n in own)
+    total = need + 3
+    ids = list(range(total))
+    rng.shuffle(ids)
+    shape = (total, Hkv, page, d)
+    if fp8:
+        # finite codes in every slot; the unused ones hold the largest values
+        pools = [torch.full(shape, 0x7e, dtype=torch.uint8) for _ in range(2)]
+    else:
+        pools = [(torch.randn(shape, generator=gen) * 100).to(torch.bfloat16) for _ in range(2)]
+
+    def draw(n):
+        x = torch.randn((Hkv, n, d), generator=gen)
+        if not fp8:
+            return x.to(torch.bfloat16)
+        return (x * 90.0).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+
+    def place(pool, x, pages):
+        for e, p in enumerate(pages):
+            part = x[:, e * page:(e + 1) * page]
+            pool[p, :, :part.shape[1]] = part
+
+    lists, flat, at = [], [[], []], 0
+    for pre, ls in groups:
+        shared = ids[at:at + pre]
+        at += pre
+        common = [draw(pre * page) for _ in range(2)]
+        for x, pool in zip(common, pools):
+            place(pool, x, shared)
+        for n in ls:
+            mine = ids[at:at + -(-n // page)]
+            at += len(mine)
+            for i in range(2):
+                x = draw(n)
+                place(pools[i], x, mine)
+                flat[i].append(torch.cat([common[i], x], dim=1).reshape(-1, d))
+            lists.append(shared + mine)
+    i32 = lambda x: torch.tensor(np.asarray(x), dtype=torch.int32)   # noqa: E731
+    q = (torch.randn((B * q_len, Hq, d), generator=gen) * q_scale).to(torch.bfloat16)
+    out = dict(q=q, k_pages=pools[0], v_pages=pools[1],
+               kv_indptr=i32(np.cumsum([0] + lens)),
+               page_indptr=i32(np.cumsum([0] + [len(x) for x in lists])),
+               page_indices=i32([p for x in lists for p in x]),
+               group_indptr=i32(np.cumsum([0] + [len(ls) for _, ls in groups])),
+               prefix_lens=i32([pre * page for pre, _ in groups]),
+               sinks=torch.rand(Hq, generator=gen) * 4 - 2,
+               cu_q=i32([b * q_len for b in range(B + 1)]),
+               k=torch.cat(flat[0]) if B else torch.zeros((0, d), dtype=pools[0].dtype),
+               v=torch.cat(flat[1]) if B else torch.zeros((0, d), dtype=pools[0].dtype))
+    if fp8:
+        out["k_scale"] = (0.8 + 0.4 * torch.rand(Hkv, generator=gen)) / 90.0
+        out["v_scale"] = (0.8 + 0.4 * torch.rand(Hkv, generator=gen)) / 90.0
+    host = dict(q_len=q_len, max_prefix=max((p for p, _ in groups), default=0) * page,
+                max_suffix=max(own, default=q_len), Hq=Hq, Hkv=Hkv, d=d, q_scale=q_scale, fp8=fp8,
+                keys=max(lens, default=1))
+    return out, host
+
+
+def call(x, h, sinks=True, **kw):
+    s = x["sinks"] if sinks else None
+    if h["fp8"]:
+        return sa.sinkattn_decode_shared_paged_fp8(
+            x["q"], x["k_pages"], x["v_pages"], x["k_scale"], x["v_scale"], x["kv_indptr"],
+            x["page_indptr"], x["page_indices"], x["group_indptr"], x["prefix_lens"], s,
+            h["q_len"], h["max_prefix"], h["max_suffix"], **kw)
+    return sa.sinkattn_decode_shared_paged(
+        x["q"], x["k_pages"], x["v_pages"], x["kv_indptr"], x["page_indptr"], x["page_indices"],
+        x["group_indptr"], x["prefix_lens"], s, h["q_len"], h["max_prefix"], h["max_suffix"], **kw)
+
+
+def want(x, h, window=0, causal=True, sinks=True):
+    """(out, lse, A) of the oracle; A: its output with |v| in the place of v."""
+    s = x["sinks"] if sinks else None
+    scales = {n: x[n] for n in ("k_scale", "v_scale") if n in x}
+    got = []
+    for absolute in (False, True):
+        v = x["v"]
+        if absolute:
+            v = v & 0x7f if h["fp8"] else v.abs()
+        got.append(oracle.attend(x["q"], x["k"], v, s, x["cu_q"], x["kv_indptr"], h["Hq"],
+                                 h["Hkv"], h["d"], 1.0 / math.sqrt(h["d"]), causal, window,
+                                 **scales))
+    return got[0][0], got[0][1], got[1][0]
+
+
+def check(out, lse, x, h, **kw):
+    o, l, A = want(x, h, **kw)
+    got = out.float().cpu().numpy().reshape(o.shape)
+    assert np.isfinite(got).all()
+    weight = 2.0 ** -11 if h["fp8"] else 2.0 ** -8
+    low = 2.0 ** -25 * h["keys"] * 6.0 if h["fp8"] else 0.0
+    logit = 1e-4 * h["q_scale"]
+    err = np.abs(got - o)
+    room = 2.0 ** -8 * np.abs(o) + (weight + 2 * logit) * A + low + 1e-6
+    assert (err <= room).all(), "off by %.3g of the room" % (err / room).max()
+    if lse is not None:
+        g = lse.cpu().numpy().reshape(l.shape)
+        both = np.isneginf(g) & np.isneginf(l)
+        assert np.where(both, 0.0, np.abs(g - l)).max() <= logit
+
+
+CASES = [
+    # groups, q_len, Hq, Hkv, d, page, window, prefix_splits, num_splits, q_scale
+    ([(4, [1, 40, 7])], 1, 64, 8, 64, 16, 0, 0, 0, 1.0),
+    ([(1, [1])], 1, 8, 8, 64, 16, 0, 1, 1, 1.0),                       # smallest: one sequence, MHA
+    ([(3, [3, 130, 64, 5])], 3, 64, 4, 128, 64, 0, 2, 3, 1.0),
+    ([(2, [5, 9]), (0, [33, 1, 70]), (7, [1, 2, 3, 4])], 1, 64, 8, 64, 32, 0, 3, 2, 1.0),
+    ([(0, [20, 30]), (0, [7])], 2, 32, 8, 128, 16, 0, 0, 0, 1.0),      # nothing is shared
+    ([(2, [4, 4]), (5, []), (1, [9])], 4, 16, 1, 128, 128, 0, 2, 2, 1.0),   # a group without sequences
+    ([(20, [1 + 5 * i for i in range(40)])], 1, 64, 8, 64, 16, 0, 4, 1, 1.0),   # 320 rows per head
+    ([(5, [3 + i for i in range(30)])], 3, 64, 4, 128, 64, 0, 3, 1, 3.0),   # 1440 rows, peaky
+    ([(9, [10, 300, 40])], 2, 24, 4, 64, 32, 100, 2, 2, 1.0),          # window: some see no prefix
+    ([(9, [10, 500, 40]), (4, [4, 4])], 4, 64, 4, 128, 16, 150, 3, 2, 1.0),
+    ([(2, [1, 1, 1, 1])], 1, 64, 1, 64, 256, 0, 9, 1, 1.0),            # 64 heads per KV head, empty chunks
+    ([(1, [7] * 5), (3, [2] * 150)], 2, 8, 2, 64, 16, 0, 1, 1, 1.0),   # 1200 rows of one short prefix
+    ([(33, [90, 91])], 1, 14, 2, 128, 16, 0, 5, 1, 1.0),               # 7 heads per KV head, odd tiles
+    ([(11, [6, 20, 300, 31, 8])], 6, 40, 2, 128, 64, 0, 2, 4, 1.0),    # 20 heads x 6 drafts
+]
+IDS = ["b%d_g%d_q%d_h%d-%d_d%d_p%d_w%d_s%d-%d" % (sum(len(g[1]) for g in c[0]), len(c[0]), *c[1:6],
+                                                 *c[6:9]) for c in CASES]
+
+
+@gpu
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("case", CASES, ids=IDS)
+def test_shared_decode_matches_oracle(case, fp8):
+    groups, q_len, Hq, Hkv, d, page, window, ps, ss, qs = case
+    x, h = make(groups, q_len, Hq, Hkv, d, page, seed=page + q_len, q_scale=qs, fp8=fp8)
+    g = {k: v.cuda() for k, v in x.items()}
+    out, lse = call(g, h, window=window, prefix_splits=ps, num_splits=ss)
+    check(out, lse, x, h, window=window)
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_without_sinks_and_without_causal_masking(d):
+    x, h = make([(3, [5, 70]), (1, [4])], 3, 16, 2, d, 32, seed=3)
+    g = {k: v.cuda() for k, v in x.items()}
+    out, lse = call(g, h, sinks=False)
+    check(out, lse, x, h, sinks=False)
+    out, lse = call(g, h, causal=False)
+    check(out, lse, x, h, causal=False)
+    out, lse = call(g, h, return_lse=False)
+    assert lse is None
+    check(out, None, x, h)
+
+
+@gpu
+def test_prefix_of_a_row_that_sees_only_its_own_keys():
+    """A window shorter than every sequence's own keys: the prefix is read by nobody."""
+    x, h = make([(4, [100, 90, 200])], 1, 64, 8, 64, 16, seed=8)
+    g = {k: v.cuda() for k, v in x.items()}
+    out, lse = call(g, h, window=64)
+    check(out, lse, x, h, window=64)
+
+
+@gpu
+def test_agrees_with_the_paged_decode():
+    x, h = make([(6, [3, 50, 12]), (2, [300, 3])], 3, 64, 4, 128, 64, seed=5)
+    g = {k: v.cuda() for k, v in x.items()}
+    o1, l1 = call(g, h)
+    o2, l2 = sa.sinkattn_decode_paged(g["q"], g["k_pages"], g["v_pages"], g["kv_indptr"],
+                                      g["page_indptr"], g["page_indices"], g["sinks"], 3,
+                                      h["keys"])
+    assert (o1.float() - o2.float()).abs().max().item() <= 1e-2
+    assert (l1 - l2).abs().max().item() <= 2e-4
+
+
+@gpu
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+def test_captured_call_replays_on_new_inputs(fp8):
+    """One graph, two inputs with other lengths and groups of the same sizes."""
+    first, h = make([(3, [5, 70, 9]), (1, [4, 30])], 2, 64, 8, 64, 16, seed=1, fp8=fp8)
+    other, h2 = make([(2, [33, 6]), (2, [8, 2, 60])], 2, 64, 8, 64, 16, seed=2, fp8=fp8)
+    rows = max(first["k_pages"].shape[0], other["k_pages"].shape[0])
+    n = max(first["page_indices"].numel(), other["page_indices"].numel())
+
+    def padded(x):
+        x = dict(x)
+        for name in ("k_pages", "v_pages"):
+            p = x[name]
+            x[name] = torch.cat([p, torch.zeros((rows - p.shape[0], *p.shape[1:]), dtype=p.dtype)])
+        i = x["page_indices"]
+        x["page_indices"] = torch.cat([i, torch.zeros(n - i.numel(), dtype=torch.int32)])
+        return x
+
+    h["max_prefix"], h["max_suffix"], h["keys"] = 48, 70, 118
+    a, b = padded(first), padded(other)
+    g = {k: v.cuda() for k, v in a.items() if k not in ("k", "v", "cu_q")}
+    bufs = dict(out=torch.empty_like(g["q"]),
+                lse=torch.empty(g["q"].shape[:2], dtype=torch.float32, device="cuda"),
+                workspace=torch.empty(sa.sinkattn_decode_shared_workspace_bytes(
+                    5, 2, 64, 64, 2, 2, 2), dtype=torch.uint8, device="cuda"))
+    call(g, h, num_splits=2, prefix_splits=2, **bufs)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(g, h, num_splits=2, prefix_splits=2, **bufs)
+    for x in (b, a, b):
+        for k in g:
+            g[k].copy_(x[k])
+        bufs["out"].fill_(float("nan"))
+        bufs["workspace"].fill_(0xff)   # NaN in every partial of the last replay
+        graph.replay()
+        torch.cuda.synchronize()
+        check(bufs["out"], bufs["lse"], x, h)
+
+
+@gpu
+def test_two_streams_with_their_own_workspaces():
+    x, h = make([(12, [1 + i for i in range(24)])], 1, 64, 8, 64, 16, seed=4)
+    y, hy = make([(5, [9 + i for i in range(7)])], 2, 64, 4, 128, 64, seed=6)
+    gx, gy = ({k: v.cuda() for k, v in z.items()} for z in (x, y))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for _ in range(3):
+        for st, g, hh in ((streams[0], gx, h), (streams[1], gy, hy)):
+            with torch.cuda.stream(st):
+                got.append(call(g, hh))
+    torch.cuda.synchronize()
+    for i, (o, l) in enumerate(got):
+        check(o, l, *((y, hy) if i % 2 else (x, h)))
+
+
+@gpu
+def test_outputs_of_an_empty_batch_are_left():
+    x, h = make([(1, [])], 1, 8, 1, 64, 16, seed=1)
+    g = {k: v.cuda() for k, v in x.items()}
+    out, lse = call(g, h)
+    assert out.shape[0] == 0 and lse.shape[0] == 0
+
+
+@gpu
+@pytest.mark.parametrize("bad", ["prefix_unaligned", "prefix_too_long", "suffix_short",
+                                 "suffix_long", "groups_end", "groups_back", "pages_few"])
+def test_wrong_lengths_are_recorded(bad):
+    """Device arrays that break a rule: recorded, and nothing is read outside
+    the pools or the lists (the plan turns the part into an empty one)."""
+    x, h = make([(3, [5, 70, 9]), (1, [4, 30])], 2, 16, 2, 64, 16, seed=1)
+    if bad == "prefix_unaligned":
+        x["prefix_lens"][0] = 40
+    elif bad == "prefix_too_long":
+        x["prefix_lens"][1] = 64     # past max_prefix_len
+    elif bad == "suffix_short":
+        x["prefix_lens"][1] = 32     # sequence 3 keeps no room for its two drafts
+    elif bad == "suffix_long":
+        h["max_suffix"] = 60
+    elif bad == "groups_end":
+        x["group_indptr"][2] = 4
+    elif bad == "groups_back":
+        x["group_indptr"][1] = 9
+    elif bad == "pages_few":
+        x["page_indptr"][1:] -= 1    # the first list is one page short
+        x["page_indices"] = x["page_indices"][1:].clone()
+    g = {k: v.cuda() for k, v in x.items()}
+    assert sa.sinkattn_debug_status() == 0
+    call(g, h)
+    assert sa.sinkattn_debug_status() == BAD_LENGTHS
+    assert sa.sinkattn_debug_status() == 0
+
+
+# ---------------------------------------------------------------------- host
+A16, WS = 0x1000, 0x10000
+
+
+def raw(**kw):
+    a = dict(q=A16, k=A16, v=A16, kv=A16, pp=A16, pi=A16, gp=A16, pl=A16, ng=2, npg=8, ps=16, B=4,
+             ql=1, mp=64, ms=40, Hq=8, Hkv=2, d=64, scale=0.125, causal=1, window=0, psp=2, ss=2,
+             sinks=None, ws=WS, wsb=1 << 30, out=A16, lse=None)
+    a.update(kw)
+    L = sa.lib()
+    return L.sinkattn_decode_shared_paged(
+        a["q"], a["k"], a["v"], a["kv"], a["pp"], a["pi"], a["gp"], a["pl"], a["ng"], a["npg"],
+        a["ps"], a["B"], a["ql"], a["mp"], a["ms"], a["Hq"], a["Hkv"], a["d"], a["scale"],
+        a["causal"], a["window"], a["psp"], a["ss"], a["sinks"], a["ws"], a["wsb"], a["out"],
+        a["lse"], None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(q=None), 1), (dict(gp=None), 1), (dict(pl=None), 1), (dict(pp=None), 1),
+    (dict(kv=None), 1), (dict(out=None), 1), (dict(out=A16 + 2), 1), (dict(lse=A16 + 2), 1),
+    (dict(ws=None), 1), (dict(ws=WS + 16), 1), (dict(wsb=1000), 1),
+    (dict(ng=0), 1), (dict(ng=70000), 2), (dict(mp=-1), 1), (dict(ms=0), 1), (dict(ql=41), 1),
+    (dict(ps=24), 2), (dict(ps=8), 2), (dict(d=96), 2), (dict(Hq=9), 2), (dict(Hq=130), 2),
+    (dict(window=8, causal=0), 2), (dict(psp=4000, ss=200), 2), (dict(B=-1), 1),
+    (dict(mp=2 ** 31 - 1), 2), (dict(scale=0.0), 1), (dict(npg=1 << 27), 2),
+])
+def test_rejects_bad_arguments(kw, status):
+    assert raw(**kw) == status
+    assert sa.sinkattn_last_error() != ""
+
+
+def test_empty_batch_is_a_no_op():
+    assert raw(B=0) == 0
+
+
+def test_fp8_rejects_missing_scales():
+    L = sa.lib()
+    for ks, vs in ((None, A16), (A16, None), (A16 + 2, A16)):
+        rc = L.sinkattn_decode_shared_paged_fp8(
+            A16, A16, A16, ks, vs, A16, A16, A16, A16, A16, 2, 8, 16, 4, 1, 64, 40, 8, 2, 64,
+            0.125, 1, 0, 2, 2, None, WS, 1 << 30, A16, None, None)
+        assert rc == INVALID_ARG and "scale" in sa.sinkattn_last_error()
+
+
+def test_workspace_holds_plan_and_partials():
+    n = sa.sinkattn_decode_shared_workspace_bytes(64, 2, 64, 64, 3, 4, 2)
+    parts = sa.sinkattn_decode_workspace_bytes(64, 2, 64, 64, 6)
+    assert n - parts >= 4 * (2 * 65 + 3 * 4 + 128)
+    with pytest.raises(sa.SinkAttnError):
+        sa.sinkattn_decode_shared_workspace_bytes(64, 2, 64, 64, 3, 4, 0)
+    with pytest.raises(sa.SinkAttnError):
+        sa.sinkattn_decode_shared_workspace_bytes(64, 2, 64, 96, 3, 4, 2)
+
+
+def test_default_splits_are_positive():
+    for B, ql, ng, mp, ms in ((1, 1, 1, 0, 1), (64, 1, 1, 8192, 512), (256, 3, 5, 4096, 9000)):
+        ps, ss = sa.sinkattn_decode_shared_default_splits(B, ql, 64, 8, 64, ng, mp, ms)
+        assert ps >= 1 and ss >= 1 and ps + ss <= 4096
+
+
+def test_refuses_tensors_of_another_kind():
+    x, h = make([(1, [3])], 1, 8, 1, 64, 16)
+    with pytest.raises(sa.SinkAttnError) as e:
+        call(x, h)   # CPU tensors
+    assert e.value.status == INVALID_ARG
+    assert UNSUPPORTED == 2
+
+
+@gpu
+@pytest.mark.parametrize("name,change", [
+    ("q", lambda t: t.float()), ("kv_indptr", lambda t: t.long()),
+    ("page_indptr", lambda t: t[:-1]), ("group_indptr", lambda t: torch.cat([t, t])),
+    ("prefix_lens", lambda t: t.long()), ("v_pages", lambda t: t[:-1]),
+    ("k_pages", lambda t: t.transpose(1, 2)), ("sinks", lambda t: t[:-1]),
+    ("page_indices", lambda t: t.cpu()), ("q", lambda t: torch.cat([t, t])),
+])
+def test_refuses_tensors_that_would_be_misread(name, change):
+    x, h = make([(2, [3, 9])], 1, 8, 2, 64, 16)
+    g = {k: v.cuda() for k, v in x.items()}
+    g[name] = change(g[name])
+    with pytest.raises(sa.SinkAttnError) as e:
+        call(g, h)
+    assert e.value.status == INVALID_ARG
