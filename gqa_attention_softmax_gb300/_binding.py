@@ -9,6 +9,7 @@ fallback: if the library is missing, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -33,6 +34,8 @@ class SinkAttnError(RuntimeError):
 def lib() -> ctypes.CDLL:
     """Load libsinkattn.so (built in-tree by ``_build.build()``); raise if absent."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -409,22 +412,32 @@ def sinkattn_decode_fp8(q, k, v, k_scale, v_scale, kv_indptr, sinks, q_len, max_
     return out, lse
 
 
-def _need(t, what, dtype, dev, shape=None):
-    """Refuses a tensor that the kernels would read as something else: wrong
-    type, device, layout or shape (None in `shape`: any size)."""
+def _bad(t, what, dtype, dev, shape):
+    """Raises what is wrong with a tensor that _need did not take."""
     if not torch.is_tensor(t):
-        raise SinkAttnError(INVALID_ARG, "%s must be a tensor" % what)
-    if t.dtype is not dtype:
-        raise SinkAttnError(INVALID_ARG, "%s must be %s, not %s" % (what, dtype, t.dtype))
-    if t.device != dev:
-        raise SinkAttnError(INVALID_ARG, "%s must be on %s, not %s" % (what, dev, t.device))
-    if not t.is_contiguous():
-        raise SinkAttnError(INVALID_ARG, "%s must be contiguous" % what)
-    if shape is not None and (t.dim() != len(shape) or any(
-            b is not None and a != b for a, b in zip(t.shape, shape))):
-        raise SinkAttnError(INVALID_ARG, "%s must have shape %s, not %s" % (
-            what, tuple("any" if x is None else x for x in shape), tuple(t.shape)))
-    return t
+        text = "%s must be a tensor" % what
+    elif t.dtype is not dtype:
+        text = "%s must be %s, not %s" % (what, dtype, t.dtype)
+    elif t.device != dev:
+        text = "%s must be on %s, not %s" % (what, dev, t.device)
+    elif not t.is_contiguous():
+        text = "%s must be contiguous" % what
+    elif isinstance(shape, int):
+        text = "%s must have %d dimension(s), not shape %s" % (what, shape, tuple(t.shape))
+    else:
+        text = "%s must have shape %s, not %s" % (what, tuple(shape), tuple(t.shape))
+    raise SinkAttnError(INVALID_ARG, text)
+
+
+def _need(t, what, dtype, dev, shape):
+    """The address of a tensor that the kernels read or write, once it is known
+    to have the type, device, layout and shape (a tuple, or the number of
+    dimensions) that they take it for. A call of the paged-cache functions
+    costs a few microseconds on the GPU, so this is one expression when all is well."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == dev and t.is_contiguous()
+            and (t.dim() == shape if shape.__class__ is int else t.shape == shape)):
+        return t.data_ptr()
+    _bad(t, what, dtype, dev, shape)
 
 
 def _need_cuda(t, what):
@@ -433,21 +446,25 @@ def _need_cuda(t, what):
     return t.device
 
 
-class _On:
-    """Makes `device` current for a launch (nothing to do if it already is)."""
-    __slots__ = ("guard",)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
-    def __init__(self, device):
-        self.guard = (torch.cuda.device(device)
-                      if device.index != torch.cuda.current_device() else None)
 
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
+def _stream_of(dev, stream):
+    if stream is None:
+        return (_raw_stream(dev.index) if _raw_stream is not None
+                else torch.cuda.current_stream(dev).cuda_stream)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+
+def _launch(dev, entry, *args):
+    """Calls a C entry point with `dev` current; raises on a non-zero status."""
+    if dev.index == torch.cuda.current_device():
+        rc = entry(*args)
+    else:
+        with torch.cuda.device(dev):
+            rc = entry(*args)
+    if rc != OK:
+        _check(rc)
 
 
 def sinkattn_decode_shared_default_splits(batch, q_len, num_qo_heads, num_kv_heads, head_dim,
@@ -470,60 +487,69 @@ def sinkattn_decode_shared_workspace_bytes(batch, q_len, num_qo_heads, head_dim,
     return int(n.value)
 
 
-def _decode_shared(entry, pool_dtype, scales, q, k_pages, v_pages, kv_indptr, page_indptr,
-                   page_indices, group_indptr, prefix_lens, sinks, q_len, max_prefix_len,
-                   max_suffix_len, num_splits, prefix_splits, sm_scale, causal, window, workspace,
-                   out, lse, return_lse, stream):
-    dev = _need_cuda(q, "q")
-    _need(q, "q", torch.bfloat16, dev, (None, None, None))
-    rows, Hq, d = q.shape
-    _need(k_pages, "k_pages", pool_dtype, dev, (None, None, None, d))
-    num_pages, Hkv, page_size, _ = k_pages.shape
-    _need(v_pages, "v_pages", pool_dtype, dev, k_pages.shape)
-    for t, what in zip(scales, ("k_scale", "v_scale")):
-        _need(t, what, torch.float32, dev, (Hkv,))
-    _need(kv_indptr, "kv_indptr", torch.int32, dev, (None,))
-    batch = kv_indptr.numel() - 1
-    q_len = int(q_len)
-    if batch < 0 or rows != batch * q_len:
-        raise SinkAttnError(INVALID_ARG, "q has %d rows, batch * q_len is %d" % (rows, batch * q_len))
-    _need(page_indptr, "page_indptr", torch.int32, dev, (batch + 1,))
-    _need(page_indices, "page_indices", torch.int32, dev, (None,))
-    _need(prefix_lens, "prefix_lens", torch.int32, dev, (None,))
-    groups = prefix_lens.numel()
-    _need(group_indptr, "group_indptr", torch.int32, dev, (groups + 1,))
-    if sinks is not None:
-        _need(sinks, "sinks", torch.float32, dev, (Hq,))
+@functools.lru_cache(maxsize=256)
+def _shared_sizes(device_index, prefix_splits, num_splits, batch, q_len, Hq, Hkv, d, groups,
+                  max_prefix_len, max_suffix_len):
+    """(prefix_splits, num_splits, workspace bytes) of these sizes (host arithmetic only)."""
     if num_splits <= 0 or prefix_splits <= 0:
         ps, ss = sinkattn_decode_shared_default_splits(batch, q_len, Hq, Hkv, d, groups,
                                                        max_prefix_len, max_suffix_len)
         prefix_splits = prefix_splits if prefix_splits > 0 else ps
         num_splits = num_splits if num_splits > 0 else ss
+    return prefix_splits, num_splits, sinkattn_decode_shared_workspace_bytes(
+        batch, q_len, Hq, d, groups, prefix_splits, num_splits)
+
+
+def _decode_shared(entry, pool_dtype, scales, q, k_pages, v_pages, kv_indptr, page_indptr,
+                   page_indices, group_indptr, prefix_lens, sinks, q_len, max_prefix_len,
+                   max_suffix_len, num_splits, prefix_splits, sm_scale, causal, window, workspace,
+                   out, lse, return_lse, stream):
+    dev = _need_cuda(q, "q")
+    i32, f32 = torch.int32, torch.float32
+    q_p = _need(q, "q", torch.bfloat16, dev, 3)
+    rows, Hq, d = q.shape
+    k_p = _need(k_pages, "k_pages", pool_dtype, dev, 4)
+    num_pages, Hkv, page_size, kd = k_pages.shape
+    if kd != d:
+        raise SinkAttnError(INVALID_ARG, "q has head_dim %d, the pools %d" % (d, kd))
+    v_p = _need(v_pages, "v_pages", pool_dtype, dev, k_pages.shape)
+    scale_p = [_need(t, what, f32, dev, (Hkv,)) for t, what in zip(scales, ("k_scale", "v_scale"))]
+    kv_p = _need(kv_indptr, "kv_indptr", i32, dev, 1)
+    batch, q_len = kv_indptr.shape[0] - 1, int(q_len)
+    if batch < 0 or rows != batch * q_len:
+        raise SinkAttnError(INVALID_ARG, "q has %d rows, batch * q_len is %d" % (rows, batch * q_len))
+    pp_p = _need(page_indptr, "page_indptr", i32, dev, (batch + 1,))
+    pi_p = _need(page_indices, "page_indices", i32, dev, 1)
+    pl_p = _need(prefix_lens, "prefix_lens", i32, dev, 1)
+    groups = prefix_lens.shape[0]
+    gp_p = _need(group_indptr, "group_indptr", i32, dev, (groups + 1,))
+    sinks_p = None if sinks is None else _need(sinks, "sinks", f32, dev, (Hq,))
+    max_prefix_len, max_suffix_len = int(max_prefix_len), int(max_suffix_len)
+    prefix_splits, num_splits, need = _shared_sizes(
+        dev.index, int(prefix_splits), int(num_splits), batch, q_len, Hq, Hkv, d, groups,
+        max_prefix_len, max_suffix_len)
     if workspace is None:
-        need = sinkattn_decode_shared_workspace_bytes(batch, q_len, Hq, d, groups, prefix_splits,
-                                                      num_splits)
         workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
     elif not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
         raise SinkAttnError(INVALID_ARG, "workspace must be contiguous and on %s" % dev)
     if out is None:
         out = torch.empty_like(q)
+        out_p = out.data_ptr()
     else:
-        _need(out, "out", torch.bfloat16, dev, q.shape)
+        out_p = _need(out, "out", torch.bfloat16, dev, q.shape)
+    lse_p = None
     if lse is not None:
-        _need(lse, "lse", torch.float32, dev, (rows, Hq))
+        lse_p = _need(lse, "lse", f32, dev, (rows, Hq))
     elif return_lse:
-        lse = torch.empty((rows, Hq), dtype=torch.float32, device=dev)
+        lse = torch.empty((rows, Hq), dtype=f32, device=dev)
+        lse_p = lse.data_ptr()
     if batch == 0:   # (an empty tensor has no address to check)
         return out, lse
-    with _On(dev):
-        rc = entry(_ptr(q), _ptr(k_pages), _ptr(v_pages), *[_ptr(t) for t in scales],
-                   _ptr(kv_indptr), _ptr(page_indptr), _ptr(page_indices), _ptr(group_indptr),
-                   _ptr(prefix_lens), groups, num_pages, page_size, batch, q_len,
-                   int(max_prefix_len), int(max_suffix_len), Hq, Hkv, d, _scale(sm_scale, d),
-                   int(bool(causal)), int(window), int(prefix_splits), int(num_splits),
-                   _ptr(sinks), _ptr(workspace), workspace.numel() * workspace.element_size(),
-                   _ptr(out), _ptr(lse), _stream(q, stream))
-    _check(rc)
+    _launch(dev, entry, q_p, k_p, v_p, *scale_p, kv_p, pp_p, pi_p, gp_p, pl_p, groups, num_pages,
+            page_size, batch, q_len, max_prefix_len, max_suffix_len, Hq, Hkv, d,
+            _scale(sm_scale, d), 1 if causal else 0, int(window), prefix_splits, num_splits,
+            sinks_p, workspace.data_ptr(), workspace.numel() * workspace.element_size(), out_p,
+            lse_p, _stream_of(dev, stream))
     return out, lse
 
 
@@ -560,26 +586,25 @@ def sinkattn_decode_shared_paged_fp8(q, k_pages, v_pages, k_scale, v_scale, kv_i
 
 def _append(entry, pool_dtype, scales, k, v, slots, k_pages, v_pages, stream):
     dev = _need_cuda(k_pages, "k_pages")
-    _need(k_pages, "k_pages", pool_dtype, dev, (None, None, None, None))
+    kp_p = _need(k_pages, "k_pages", pool_dtype, dev, 4)
     num_pages, Hkv, page_size, d = k_pages.shape
-    _need(v_pages, "v_pages", pool_dtype, dev, k_pages.shape)
-    _need(slots, "slots", torch.int32, dev, (None,))
-    tokens = slots.numel()
+    vp_p = _need(v_pages, "v_pages", pool_dtype, dev, k_pages.shape)
+    s_p = _need(slots, "slots", torch.int32, dev, 1)
+    tokens = slots.shape[0]
     strides = []
     for t, what in ((k, "k"), (v, "v")):
-        if not torch.is_tensor(t) or t.dtype is not torch.bfloat16 or t.device != dev:
-            raise SinkAttnError(INVALID_ARG, "%s must be bfloat16 on %s" % (what, dev))
-        if tuple(t.shape) != (tokens, Hkv, d) or (
-                tokens > 0 and (t.stride(2) != 1 or (Hkv > 1 and t.stride(1) != d))):
-            raise SinkAttnError(INVALID_ARG, "%s must have shape %s with contiguous rows" % (
-                what, (tokens, Hkv, d)))
-        strides.append(t.stride(0) if tokens > 1 else Hkv * d)
-    for t, what in zip(scales, ("k_scale", "v_scale")):
-        _need(t, what, torch.float32, dev, (Hkv,))
-    with _On(dev):
-        _check(entry(_ptr(k), _ptr(v), strides[0], strides[1], _ptr(slots), tokens,
-                     *[_ptr(t) for t in scales], _ptr(k_pages), _ptr(v_pages), num_pages,
-                     page_size, Hkv, d, _stream(k_pages, stream)))
+        if (not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or t.device != dev
+                or t.shape != (tokens, Hkv, d)):
+            raise SinkAttnError(INVALID_ARG, "%s must be bfloat16 %s on %s" % (
+                what, (tokens, Hkv, d), dev))
+        at, head, el = t.stride()
+        if tokens > 0 and (el != 1 or (head != d and Hkv > 1)):
+            raise SinkAttnError(INVALID_ARG, "the rows of a token of %s must be contiguous" % what)
+        strides.append(at if tokens > 1 else Hkv * d)
+    scale_p = [_need(t, what, torch.float32, dev, (Hkv,))
+               for t, what in zip(scales, ("k_scale", "v_scale"))]
+    _launch(dev, entry, k.data_ptr(), v.data_ptr(), strides[0], strides[1], s_p, tokens, *scale_p,
+            kp_p, vp_p, num_pages, page_size, Hkv, d, _stream_of(dev, stream))
 
 
 def sinkattn_append_paged(k, v, slots, k_pages, v_pages, stream=None):
@@ -608,24 +633,28 @@ class PageTable:
     """A page table's buffer and sizes. ``state``: an int32 device tensor of at
     least sinkattn_pages_table_ints() words that holds a table already; without
     one, a new buffer on ``device`` is allocated and initialised (every page
-    free, every sequence empty)."""
-    __slots__ = ("state", "num_pages", "page_size", "max_seqs", "max_pages")
+    free, every sequence empty). The parts are views of ``state``."""
+    __slots__ = ("state", "num_pages", "page_size", "max_seqs", "max_pages", "args", "device")
 
     def __init__(self, state, num_pages, page_size, max_seqs, max_pages, device="cuda",
                  stream=None):
-        self.num_pages, self.page_size = int(num_pages), int(page_size)
-        self.max_seqs, self.max_pages = int(max_seqs), int(max_pages)
-        need = sinkattn_pages_table_ints(num_pages, max_seqs, max_pages)
-        if state is None:
-            self.state = torch.empty((need,), dtype=torch.int32, device=device)
-            sinkattn_pages_init(self, stream=stream)
-            return
-        dev = _need_cuda(state, "state")
-        _need(state, "state", torch.int32, dev, (None,))
-        if state.numel() < need:
+        self.num_pages, self.page_size = num_pages, page_size
+        self.max_seqs, self.max_pages = max_seqs, max_pages
+        need = 16 + max_seqs * (8 + max_pages) + 4 * num_pages
+        new = state is None
+        if new:
+            state = torch.empty((sinkattn_pages_table_ints(num_pages, max_seqs, max_pages),),
+                                dtype=torch.int32, device=device)
+        self.device = _need_cuda(state, "state")
+        ptr = _need(state, "state", torch.int32, self.device, 1)
+        if state.shape[0] < need:
             raise SinkAttnError(INVALID_ARG, "state has %d words, a table of these sizes %d" % (
-                state.numel(), need))
+                state.shape[0], need))
         self.state = state
+        # what every entry point takes first (the buffer stays where it is while `state` lives)
+        self.args = (ptr, num_pages, page_size, max_seqs, max_pages)
+        if new:
+            sinkattn_pages_init(self, stream=stream)
 
     def _part(self, at, n):
         return self.state[at:at + n]
@@ -653,37 +682,33 @@ class PageTable:
                           self.num_pages)
 
 
-def _table(t):
-    return _ptr(t.state), t.num_pages, t.page_size, t.max_seqs, t.max_pages
-
-
 def _pools(table, k_pages, v_pages):
     """(k, v, layers, layer stride, Hkv, row bytes) of the pools of one layer,
     [num_pages, Hkv, page_size, d], or of several, [layers, ...]."""
-    dev = table.state.device
     for t, what in ((k_pages, "k_pages"), (v_pages, "v_pages")):
-        if not torch.is_tensor(t) or t.device != dev or t.dim() not in (4, 5):
+        if not isinstance(t, torch.Tensor) or t.device != table.device or t.dim() not in (4, 5):
             raise SinkAttnError(INVALID_ARG, "%s must be a tensor of 4 or 5 dimensions on %s" % (
-                what, dev))
-        if not (t if t.dim() == 4 else t[0]).is_contiguous():
-            raise SinkAttnError(INVALID_ARG, "each layer of %s must be contiguous" % what)
-    if (k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype
-            or k_pages.stride() != v_pages.stride()):
+                what, table.device))
+    shape, strides = k_pages.shape, k_pages.stride()
+    if shape != v_pages.shape or strides != v_pages.stride() or k_pages.dtype is not v_pages.dtype:
         raise SinkAttnError(INVALID_ARG, "k_pages and v_pages must have one shape, type and stride")
-    num_pages, Hkv, page_size, d = k_pages.shape[-4:]
+    if not k_pages.is_contiguous() and not (len(shape) == 5 and shape[0] > 0
+                                            and k_pages[0].is_contiguous()):
+        raise SinkAttnError(INVALID_ARG, "each layer of k_pages and v_pages must be contiguous")
+    num_pages, Hkv, page_size, d = shape[-4:]
     if num_pages != table.num_pages or page_size != table.page_size:
         raise SinkAttnError(INVALID_ARG, "the pools have %d pages of %d, the table %d of %d" % (
             num_pages, page_size, table.num_pages, table.page_size))
     el = k_pages.element_size()
-    layers = k_pages.shape[0] if k_pages.dim() == 5 else 1
-    stride = k_pages.stride(0) * el if layers > 1 else 0
-    return _ptr(k_pages), _ptr(v_pages), layers, stride, Hkv, d * el
+    layers = shape[0] if len(shape) == 5 else 1
+    return (k_pages.data_ptr(), v_pages.data_ptr(), layers, strides[0] * el if layers > 1 else 0,
+            Hkv, d * el)
 
 
 def sinkattn_pages_init(table, stream=None) -> None:
     """Every page free (page 0 is the first to be taken), every sequence empty."""
-    with _On(table.state.device):
-        _check(lib().sinkattn_pages_init(*_table(table), _stream(table.state, stream)))
+    dev = table.device
+    _launch(dev, lib().sinkattn_pages_init, *table.args, _stream_of(dev, stream))
 
 
 def sinkattn_pages_reserve(table, seq_ids, cu_new, total_new, k_pages, v_pages, slots=None,
@@ -692,55 +717,53 @@ def sinkattn_pages_reserve(table, seq_ids, cu_new, total_new, k_pages, v_pages, 
     (int32, device). Returns the new tokens' slots, int32 [total_new]. A
     partly filled page that other sequences hold too is copied first, in the
     pools of all layers."""
-    dev = table.state.device
-    n = _need(seq_ids, "seq_ids", torch.int32, dev, (None,)).numel()
-    _need(cu_new, "cu_new", torch.int32, dev, (n + 1,))
+    dev = table.device
+    ids_p = _need(seq_ids, "seq_ids", torch.int32, dev, 1)
+    n = seq_ids.shape[0]
+    cu_p = _need(cu_new, "cu_new", torch.int32, dev, (n + 1,))
     total_new = int(total_new)
     if slots is None:
         slots = torch.empty((max(total_new, 0),), dtype=torch.int32, device=dev)
+        slots_p = slots.data_ptr()
     else:
-        _need(slots, "slots", torch.int32, dev, (total_new,))
-    with _On(dev):
-        _check(lib().sinkattn_pages_reserve(*_table(table), _ptr(seq_ids), _ptr(cu_new), n,
-                                            total_new, *_pools(table, k_pages, v_pages),
-                                            _ptr(slots), _stream(table.state, stream)))
+        slots_p = _need(slots, "slots", torch.int32, dev, (total_new,))
+    _launch(dev, lib().sinkattn_pages_reserve, *table.args, ids_p, cu_p, n, total_new,
+            *_pools(table, k_pages, v_pages), slots_p, _stream_of(dev, stream))
     return slots
 
 
 def sinkattn_pages_fork(table, src_ids, dst_ids, stream=None) -> None:
     """dst_ids[i] (empty sequences) become copies of src_ids[i] that share all
     their pages (int32, device)."""
-    dev = table.state.device
-    n = _need(src_ids, "src_ids", torch.int32, dev, (None,)).numel()
-    _need(dst_ids, "dst_ids", torch.int32, dev, (n,))
-    with _On(dev):
-        _check(lib().sinkattn_pages_fork(*_table(table), _ptr(src_ids), _ptr(dst_ids), n,
-                                         _stream(table.state, stream)))
+    dev = table.device
+    src_p = _need(src_ids, "src_ids", torch.int32, dev, 1)
+    dst_p = _need(dst_ids, "dst_ids", torch.int32, dev, src_ids.shape)
+    _launch(dev, lib().sinkattn_pages_fork, *table.args, src_p, dst_p, src_ids.shape[0],
+            _stream_of(dev, stream))
 
 
 def sinkattn_pages_truncate(table, seq_ids, new_lens=None, stream=None) -> None:
     """Shortens seq_ids[i] to new_lens[i] tokens (int32, device; None: 0, which
     frees the sequences); pages that no sequence holds any more become free."""
-    dev = table.state.device
-    n = _need(seq_ids, "seq_ids", torch.int32, dev, (None,)).numel()
-    if new_lens is not None:
-        _need(new_lens, "new_lens", torch.int32, dev, (n,))
-    with _On(dev):
-        _check(lib().sinkattn_pages_truncate(*_table(table), _ptr(seq_ids), _ptr(new_lens), n,
-                                             _stream(table.state, stream)))
+    dev = table.device
+    ids_p = _need(seq_ids, "seq_ids", torch.int32, dev, 1)
+    new_p = None if new_lens is None else _need(new_lens, "new_lens", torch.int32, dev,
+                                                seq_ids.shape)
+    _launch(dev, lib().sinkattn_pages_truncate, *table.args, ids_p, new_p, seq_ids.shape[0],
+            _stream_of(dev, stream))
 
 
 def sinkattn_pages_compact(table, k_pages, v_pages, page_map=None, stream=None):
     """Moves the pages in use to the front of the pools (all layers). Returns
     page_map, int32 [num_pages]: each old page's new index, -1 where it was free."""
-    dev = table.state.device
+    dev = table.device
     if page_map is None:
         page_map = torch.empty((table.num_pages,), dtype=torch.int32, device=dev)
+        map_p = page_map.data_ptr()
     else:
-        _need(page_map, "page_map", torch.int32, dev, (table.num_pages,))
-    with _On(dev):
-        _check(lib().sinkattn_pages_compact(*_table(table), *_pools(table, k_pages, v_pages),
-                                            _ptr(page_map), _stream(table.state, stream)))
+        map_p = _need(page_map, "page_map", torch.int32, dev, (table.num_pages,))
+    _launch(dev, lib().sinkattn_pages_compact, *table.args, *_pools(table, k_pages, v_pages),
+            map_p, _stream_of(dev, stream))
     return page_map
 
 
@@ -748,21 +771,21 @@ def sinkattn_pages_lists(table, seq_ids, kv_indptr=None, page_indptr=None, page_
                          stream=None):
     """What the paged attention reads of the sequences seq_ids: returns
     (kv_indptr [n+1], page_indptr [n+1], page_indices), int32."""
-    dev = table.state.device
-    n = _need(seq_ids, "seq_ids", torch.int32, dev, (None,)).numel()
-
-    def buf(t, what, size):
-        if t is None:   # (an empty batch writes nothing: its running sums are zero)
-            return (torch.empty if n > 0 else torch.zeros)((size,), dtype=torch.int32, device=dev)
-        return _need(t, what, torch.int32, dev, (None if what == "page_indices" else size,))
-
-    kv_indptr = buf(kv_indptr, "kv_indptr", n + 1)
-    page_indptr = buf(page_indptr, "page_indptr", n + 1)
-    page_indices = buf(page_indices, "page_indices", n * table.max_pages)
-    with _On(dev):
-        _check(lib().sinkattn_pages_lists(*_table(table), _ptr(seq_ids), n, _ptr(kv_indptr),
-                                          _ptr(page_indptr), _ptr(page_indices),
-                                          page_indices.numel(), _stream(table.state, stream)))
+    dev = table.device
+    ids_p = _need(seq_ids, "seq_ids", torch.int32, dev, 1)
+    n = seq_ids.shape[0]
+    make = torch.empty if n > 0 else torch.zeros   # an empty batch writes nothing
+    if kv_indptr is None:
+        kv_indptr = make((n + 1,), dtype=torch.int32, device=dev)
+    if page_indptr is None:
+        page_indptr = make((n + 1,), dtype=torch.int32, device=dev)
+    if page_indices is None:
+        page_indices = make((n * table.max_pages,), dtype=torch.int32, device=dev)
+    kv_p = _need(kv_indptr, "kv_indptr", torch.int32, dev, (n + 1,))
+    pp_p = _need(page_indptr, "page_indptr", torch.int32, dev, (n + 1,))
+    pi_p = _need(page_indices, "page_indices", torch.int32, dev, 1)
+    _launch(dev, lib().sinkattn_pages_lists, *table.args, ids_p, n, kv_p, pp_p, pi_p,
+            page_indices.shape[0], _stream_of(dev, stream))
     return kv_indptr, page_indptr, page_indices
 
 

@@ -436,6 +436,15 @@ int decode_impl(const void* q, const void* k, const void* v, const int32_t* kv_i
                       num_splits, out, lse, static_cast<cudaStream_t>(stream), true);
 }
 
+// Whether the prefixes take the tcgen05 kernel, which works on row blocks of
+// 256 (128 at least), or the warp-level one, which takes up to 64 rows at a
+// time and re-reads the keys for each.
+bool prefix_on_tc(int64_t tokens, int G, int64_t groups) {
+  const int kind = g_decode_kernel.load(std::memory_order_relaxed);
+  if (kind != SINKATTN_DECODE_AUTO) return kind == SINKATTN_DECODE_TCGEN05;
+  return tokens * G > 64 * groups;
+}
+
 // Shared-prefix decode: the sequences' own keys and the groups' prefixes as
 // two sets of partials of the same rows, folded by one merge.
 size_t shared_plan_bytes(int64_t batch, int64_t q_len, int64_t groups) {
@@ -504,7 +513,8 @@ int decode_shared_impl(const void* q, const void* k_pages, const void* v_pages, 
   plan.grp_q = plan.pages + batch + 1;
   plan.grp_k = plan.grp_q + num_groups + 1;
   plan.grp_pages = plan.grp_k + num_groups + 1;
-  plan.row_pos = plan.grp_pages + num_groups + 1;
+  plan.grp_blk = plan.grp_pages + num_groups + 1;
+  plan.row_pos = plan.grp_blk + num_groups + 1;
   const size_t rows = static_cast<size_t>(batch) * q_len;
   const size_t plan_bytes = shared_plan_bytes(batch, q_len, num_groups);
   float* part_acc = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan_bytes);
@@ -512,7 +522,8 @@ int decode_shared_impl(const void* q, const void* k_pages, const void* v_pages, 
       reinterpret_cast<char*>(part_acc) +
       ((rows * num_qo_heads * slots * head_dim * 4 + 255) & ~static_cast<size_t>(255)));
   rc = launch_shared_plan(kv_indptr, pg.page_indptr, group_indptr, prefix_lens, num_groups,
-                          pg.page_size, batch, q_len, max_prefix_len, max_suffix_len, plan, s);
+                          pg.page_size, batch, q_len, max_prefix_len, max_suffix_len,
+                          prefix_block_tokens(num_qo_heads / num_kv_heads), plan, s);
   if (rc) return rc;
 
   a.part_acc = part_acc;
@@ -534,7 +545,8 @@ int decode_shared_impl(const void* q, const void* k_pages, const void* v_pages, 
     pa.num_splits = prefix_splits;
     pa.free_rows = 1;
     pa.row_pos = window > 0 ? plan.row_pos : nullptr;
-    if ((rc = launch_attn_mma(pa, s))) return rc;
+    const bool tc = prefix_on_tc(rows, num_qo_heads / num_kv_heads, num_groups);
+    if ((rc = tc ? launch_prefix_tc(pa, plan, s) : launch_attn_mma(pa, s))) return rc;
   }
   PagedKv own = pg;
   own.page_indptr = plan.pages;
@@ -657,9 +669,33 @@ int sinkattn_decode_shared_default_splits(int32_t batch, int32_t q_len, int32_t 
   int rc = sinkattn_decode_default_splits(batch, q_len, num_qo_heads, num_kv_heads, head_dim,
                                           max_suffix_len, num_splits);
   if (rc) return rc;
-  // the prefix as a batch of blocks of 64 query rows
-  const int64_t rows = static_cast<int64_t>(batch) * q_len * num_qo_heads / num_kv_heads;
-  const int64_t blocks = std::min<int64_t>(num_groups + rows / 64, int64_t{1} << 20);
+  const int G = num_qo_heads / num_kv_heads;
+  const int64_t tokens = static_cast<int64_t>(batch) * q_len;
+  if (G >= 1 && G <= 64 && prefix_on_tc(tokens, G, num_groups)) {
+    // rounds of work items over the SMs x (tiles of an item + its start and
+    // end), plus what the merge pays for one more partial of every row
+    const int kt = prefix_tile_keys(head_dim, false);
+    const int64_t bt = prefix_block_tokens(G);
+    const int64_t items = num_groups * ((tokens / num_groups + bt - 1) / bt) * num_kv_heads;
+    const int64_t tiles = (static_cast<int64_t>(max_prefix_len) + kt - 1) / kt;
+    const double step_us = head_dim == 64 ? 1.0 : 1.9;
+    const double part_us = static_cast<double>(tokens) * num_qo_heads * head_dim * 8 / 6e6;
+    const int sms = sm_count();
+    double best = 0;
+    *prefix_splits = 1;
+    for (int64_t s = 1; s <= 64 && s <= std::max<int64_t>(tiles, 1); ++s) {
+      const double us = static_cast<double>((items * s + sms - 1) / sms) *
+                            static_cast<double>((tiles + s - 1) / s + 3) * step_us +
+                        static_cast<double>(s) * part_us;
+      if (s == 1 || us < best) {
+        best = us;
+        *prefix_splits = static_cast<int32_t>(s);
+      }
+    }
+    return SINKATTN_OK;
+  }
+  // the warp-level kernel's blocks of up to 64 query rows
+  const int64_t blocks = std::min<int64_t>(num_groups + tokens * G / 64, int64_t{1} << 20);
   return sinkattn_decode_default_splits(static_cast<int32_t>(blocks), 1, num_qo_heads, num_kv_heads,
                                         head_dim, max_prefix_len, prefix_splits);
 }
@@ -803,12 +839,13 @@ int sinkattn_debug_status(void* stream, int* status) {
   g_last_error[0] = '\0';
   if (!status) return fail(SINKATTN_INVALID_ARG, "status must be non-null");
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  int a = 0, m = 0, t = 0, dt = 0, sh = 0, pg = 0;
+  int a = 0, m = 0, t = 0, dt = 0, sh = 0, pg = 0, px = 0;
   if (read_status_attn_mma(s, &a) || read_status_merge(s, &m) || read_status_prefill_tc(s, &t) ||
-      read_status_decode_tc(s, &dt) || read_status_shared(s, &sh) || read_status_pages(s, &pg))
+      read_status_decode_tc(s, &dt) || read_status_shared(s, &sh) || read_status_pages(s, &pg) ||
+      read_status_prefix_tc(s, &px))
     return fail(SINKATTN_CUDA_ERROR, "reading the device status failed: %s",
                 cudaGetErrorString(cudaGetLastError()));
-  *status = a ? a : (dt ? dt : (t ? t : (m ? m : (sh ? sh : pg))));
+  *status = a ? a : (dt ? dt : (t ? t : (m ? m : (px ? px : (sh ? sh : pg)))));
   return SINKATTN_OK;
 }
 
@@ -817,7 +854,8 @@ int sinkattn_debug_set_hooks(long long wait_limit_cycles, int skip_tile) {
   if (skip_tile < -1) return fail(SINKATTN_INVALID_ARG, "skip_tile must be -1 or a tile index");
   if (set_hooks_attn_mma(wait_limit_cycles, skip_tile) ||
       set_hooks_prefill_tc(wait_limit_cycles, skip_tile) ||
-      set_hooks_decode_tc(wait_limit_cycles, skip_tile))
+      set_hooks_decode_tc(wait_limit_cycles, skip_tile) ||
+      set_hooks_prefix_tc(wait_limit_cycles, skip_tile))
     return fail(SINKATTN_CUDA_ERROR, "setting the test hooks failed: %s",
                 cudaGetErrorString(cudaGetLastError()));
   return SINKATTN_OK;

@@ -23,7 +23,7 @@ struct PlanParams {
   const int32_t* page_indptr;
   const int32_t* group_indptr;
   const int32_t* prefix_lens;
-  int groups, page_size, batch, q_len, max_prefix, max_suffix;
+  int groups, page_size, batch, q_len, max_prefix, max_suffix, block_tokens;
   SharedPlan out;
 };
 
@@ -62,34 +62,46 @@ __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const PlanParams 
     if (!ok) *wrong = true;
     return ok ? len : 0;
   };
-  int run = 0, total;
+  // the groups have to cut the batch into runs, or none of them has rows
+  bool broken = false;
+  for (int g = tid; g < p.groups; g += kThreads) {
+    const int b0 = p.group_indptr[g], b1 = p.group_indptr[g + 1];
+    broken |= b0 < 0 || b1 < b0 || b1 > p.batch || (g == 0 && b0 != 0) ||
+              (g == p.groups - 1 && b1 != p.batch);
+  }
+  broken = __syncthreads_or(broken);
+  int run = 0, run_blk = 0, total;
   for (int base = 0; base < p.groups; base += kThreads) {
     const int g = base + tid;
-    int len = 0;
-    if (g < p.groups) {
-      int b0 = p.group_indptr[g], b1 = p.group_indptr[g + 1];
-      if (b0 < 0 || b1 < b0 || b1 > p.batch || (g == 0 && b0 != 0) ||
-          (g == p.groups - 1 && b1 != p.batch)) {
-        bad = true;
-        b0 = min(max(b0, 0), p.batch);
-        b1 = b0;
-      }
+    int len = 0, blocks = 0;
+    if (g < p.groups && !broken) {
+      const int b0 = p.group_indptr[g], b1 = p.group_indptr[g + 1];
       len = prefix_of(g, &bad);
       // the first sequence's list holds the prefix
       if (b1 > b0 && len > (p.page_indptr[b0 + 1] - p.page_indptr[b0]) * p.page_size) {
         bad = true;
         len = 0;
       }
+      blocks = ((b1 - b0) * p.q_len + p.block_tokens - 1) / p.block_tokens;
       p.out.grp_q[g] = b0 * p.q_len;
       p.out.grp_pages[g] = p.page_indptr[b0];
-      if (g == p.groups - 1) {
-        p.out.grp_q[p.groups] = p.batch * p.q_len;
-        p.out.grp_pages[p.groups] = p.page_indptr[p.batch];
-      }
+    } else if (g < p.groups) {
+      p.out.grp_q[g] = p.batch * p.q_len;
+      p.out.grp_pages[g] = p.page_indptr[p.batch];
     }
     const int upto = run + block_sum_scan(len, &total, sums);
-    if (g < p.groups) p.out.grp_k[g + 1] = upto;
     run += total;
+    const int upto_blk = run_blk + block_sum_scan(blocks, &total, sums);
+    run_blk += total;
+    if (g < p.groups) {
+      p.out.grp_k[g + 1] = upto;
+      p.out.grp_blk[g + 1] = upto_blk;
+    }
+  }
+  if (tid == 0) {
+    p.out.grp_q[p.groups] = p.batch * p.q_len;
+    p.out.grp_pages[p.groups] = p.page_indptr[p.batch];
+    p.out.grp_blk[0] = 0;
   }
   if (tid == 0) p.out.grp_k[0] = p.out.kv[0] = 0;
   run = 0;
@@ -97,7 +109,7 @@ __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const PlanParams 
     const int b = base + tid;
     int own = 0;
     if (b < p.batch) {
-      int lo = 0, hi = p.groups;   // the group with group_indptr[g] <= b < group_indptr[g + 1]
+      int lo = 0, hi = broken ? 1 : p.groups;   // the group with group_indptr[g] <= b < group_indptr[g + 1]
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (p.group_indptr[mid] <= b) lo = mid;
@@ -105,7 +117,7 @@ __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const PlanParams 
       }
       const int len = p.kv_indptr[b + 1] - p.kv_indptr[b];
       const int first = p.page_indptr[b], held = p.page_indptr[b + 1] - first;
-      int prefix = prefix_of(lo, &bad);
+      int prefix = broken ? 0 : prefix_of(lo, &bad);
       own = len - prefix;
       if (own < p.q_len || own > p.max_suffix || len > held * p.page_size) {
         bad = true;
@@ -119,7 +131,7 @@ __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const PlanParams 
     if (b < p.batch) p.out.kv[b + 1] = upto;
     run += total;
   }
-  if (__syncthreads_or(bad) && tid == 0) atomicExch(&g_status_shared, SINKATTN_BAD_LENGTHS);
+  if (__syncthreads_or(bad || broken) && tid == 0) atomicExch(&g_status_shared, SINKATTN_BAD_LENGTHS);
 }
 
 }  // namespace
@@ -127,9 +139,10 @@ __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const PlanParams 
 int launch_shared_plan(const int32_t* kv_indptr, const int32_t* page_indptr,
                        const int32_t* group_indptr, const int32_t* prefix_lens, int32_t groups,
                        int32_t page_size, int32_t batch, int32_t q_len, int32_t max_prefix,
-                       int32_t max_suffix, const SharedPlan& plan, cudaStream_t stream) {
-  const PlanParams p{kv_indptr, page_indptr, group_indptr, prefix_lens, groups,
-                     page_size, batch,       q_len,        max_prefix,  max_suffix, plan};
+                       int32_t max_suffix, int32_t block_tokens, const SharedPlan& plan,
+                       cudaStream_t stream) {
+  const PlanParams p{kv_indptr, page_indptr, group_indptr, prefix_lens, groups,       page_size,
+                     batch,     q_len,       max_prefix,   max_suffix,  block_tokens, plan};
   shared_plan_kernel<<<1, kThreads, 0, stream>>>(p);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) {

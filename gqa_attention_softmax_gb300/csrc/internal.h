@@ -115,19 +115,28 @@ struct SharedPlan {
   int32_t* grp_q;     // [groups + 1] first query token of each group
   int32_t* grp_k;     // [groups + 1] running sum of the prefixes' keys
   int32_t* grp_pages; // [groups + 1] first entry of the prefixes' pages
+  int32_t* grp_blk;   // [groups + 1] running sum of the tcgen05 kernel's row blocks
   int32_t* row_pos;   // [batch * q_len] position of each query token
 };
 inline size_t shared_plan_ints(int64_t batch, int64_t q_len, int64_t groups) {
-  return static_cast<size_t>(2 * (batch + 1) + 3 * (groups + 1) + batch * q_len);
+  return static_cast<size_t>(2 * (batch + 1) + 4 * (groups + 1) + batch * q_len);
 }
 int launch_shared_plan(const int32_t* kv_indptr, const int32_t* page_indptr,
                        const int32_t* group_indptr, const int32_t* prefix_lens, int32_t groups,
                        int32_t page_size, int32_t batch, int32_t q_len, int32_t max_prefix,
-                       int32_t max_suffix, const SharedPlan& plan, cudaStream_t stream);
+                       int32_t max_suffix, int32_t block_tokens, const SharedPlan& plan,
+                       cudaStream_t stream);
+
+// The groups' prefixes on the tcgen05/TMEM path: partials of every query row
+// over its group's prefix (a.batch: groups, a.total_q: query tokens).
+int launch_prefix_tc(const AttnArgs& a, const SharedPlan& plan, cudaStream_t stream);
+int prefix_block_tokens(int G);            // query tokens of one row block
+int prefix_tile_keys(int d, bool fp8);     // keys of one K/V tile
 
 // Reads and clears the device status word of one translation unit.
 int read_status_pages(cudaStream_t s, int* status);
 int read_status_shared(cudaStream_t s, int* status);
+int read_status_prefix_tc(cudaStream_t s, int* status);
 int read_status_attn_mma(cudaStream_t s, int* status);
 int read_status_merge(cudaStream_t s, int* status);
 int read_status_prefill_tc(cudaStream_t s, int* status);
@@ -139,6 +148,7 @@ int read_status_decode_tc(cudaStream_t s, int* status);
 int set_hooks_attn_mma(long long limit, int skip);
 int set_hooks_prefill_tc(long long limit, int skip);
 int set_hooks_decode_tc(long long limit, int skip);
+int set_hooks_prefix_tc(long long limit, int skip);
 
 // Thread-local error text used by the C ABI.
 void set_error(const char* fmt, ...);

@@ -1,0 +1,711 @@
+// The shared prefix of shared-prefix decode on the 5th-generation tensor
+// cores: all query rows of a group of sequences against the prefix's keys,
+// which every row sees (but for a window), read once per block of rows.
+//
+// Rows are (query token, head in group) pairs of one KV head, 128 to a tile;
+// a block has NT tiles that share each K/V tile in shared memory. A work item
+// is (row block, KV head, chunk of the keys); it leaves the rows' partials
+// (m, d, acc) WITHOUT the sink for the merge, like the split-KV kernels:
+//
+//   S_t = Q_t K^T     M 128 rows, N KT keys, K d   (operands in shared memory)
+//   O_t += P_t V      M 128 rows, N d, K KT keys   (P_t from TMEM)
+//
+// With hundreds of rows per KV head the prefix is compute-bound (4 d
+// operations per row and key against 4 d / rows bytes), so the kernel follows
+// the persistent prefill: one block per SM, a TMA producer warp, an MMA
+// issuer warp, and per tile four softmax warps, one thread per row. Two tiles
+// per block (three would not divide 512 rows, the gpt-oss-shaped batch of 64
+// sequences, and TMEM holds no more at d 128); the tiles' chains S -> softmax
+// -> P V interleave on the tensor core. A tile whose rows all lie behind the
+// group's last token is left out. Chunks fill the SMs when row blocks are few.
+//
+// e4m3 pools: the producer copies codes into a ring of their own, four
+// converter warps widen each tile to f16 in the layout the MMAs read (exact:
+// f16 holds every e4m3 value) and turn Q to f16 once per item; each code is
+// converted once per row block, not once per sequence. The key scale joins
+// the logit scale, the value scale the written accumulator.
+//
+// The running maximum is exact, so a row's largest weight is exactly 1 and
+// the others are rounded by at most half a step of bf16 (f16) for P V; the
+// row sum is kept in fp32 from the unrounded weights. Every wait is bounded.
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+#include "tc.cuh"
+
+namespace sinkattn {
+
+__device__ int g_status_prefix_tc;
+
+namespace {
+
+struct PxParams {
+  const int32_t* grp_q;      // [groups + 1] first query token
+  const int32_t* grp_k;      // [groups + 1] running sum of the prefixes' keys
+  const int32_t* grp_pages;  // [groups + 1] first entry in page_indices
+  const int32_t* grp_blk;    // [groups + 1] running sum of row blocks
+  const int32_t* row_pos;    // [tokens] position of each query token (windows)
+  const int32_t* page_indices;
+  int groups, Hq, Hkv, G, QB, num_splits;
+  int window;
+  float sm_scale, scale_log2;
+  int page_size, box_rows;
+  const float* k_scale;
+  const float* v_scale;
+  float* part_acc;
+  float* part_md;
+  int part_slots;
+};
+
+template <int D, bool FP8>
+struct PxCfg {
+  static constexpr int NT = 2;
+  static constexpr int NSUB = D / 64;
+  static constexpr int KT = D == 64 ? 96 : (FP8 ? 64 : 128);   // keys per tile
+  static constexpr int NST = D == 64 ? 4 : (FP8 ? 3 : 2);      // K/V stages
+  static constexpr int NSTF = FP8 ? (D == 64 ? 4 : 3) : 0;     // code stages
+  static constexpr int NSTF_MOD = FP8 ? NSTF : 1;
+  static constexpr int QSUB = 128 * 128;                       // [128 rows][64], 128-byte swizzle
+  static constexpr int KVSUB = KT * 128;
+  static constexpr int Q_TILE = NSUB * QSUB;
+  static constexpr int KV_TILE = NSUB * KVSUB;
+  static constexpr int STAGE = 2 * KV_TILE;
+  static constexpr int CODE_STAGE = 2 * KT * D;
+  static constexpr int OFF_KV = NT * Q_TILE;
+  static constexpr int OFF_CODE = OFF_KV + NST * STAGE;
+  static constexpr int GRP_CAP = 512;                          // groups staged in shared memory
+  static constexpr int OFF_GRP = OFF_CODE + NSTF * CODE_STAGE;
+  static constexpr int OFF_BAR = OFF_GRP + (4 * (GRP_CAP + 1) * 4 + 15) / 16 * 16;
+  static constexpr int N_BARS = 3 + 2 * NST + 3 * NT + 1 + 2 * NSTF;
+  static constexpr int SMEM = 1024 + OFF_BAR + N_BARS * 8 + 64;
+  static constexpr int N_CVT = 4;
+  static constexpr int W_CVT = 2 + 4 * NT;                     // first converter warp
+  static constexpr int THREADS = (2 + 4 * NT + (FP8 ? N_CVT : 0)) * 32;
+  // registers: 10 warps put 3 on two SM sub-partitions (168 a thread), 14
+  // warps put 4 there (128, bounded by a 512-thread launch)
+  static constexpr int LB_THREADS = FP8 ? 512 : 320;
+  static constexpr uint32_t TMEM_COLS = 512;
+  __host__ __device__ static constexpr uint32_t col_s(int t) { return static_cast<uint32_t>(KT * t); }
+  __host__ __device__ static constexpr uint32_t col_o(int t) {
+    return static_cast<uint32_t>(KT * NT + D * t);
+  }
+  static_assert(NT * (KT + D) <= 512, "TMEM budget");
+  static_assert(KVSUB % 1024 == 0 && KT % 32 == 0, "tile shape");
+  // one block per SM, so the 512-column TMEM allocation always succeeds
+  static_assert(SMEM <= 232448 && 2 * (SMEM + 1024) > 233472, "one block per SM");
+};
+
+struct PxItem {
+  int kvh, chunk, tok0, nq, tiles, keys, first, n, list0, pages;
+};
+
+// Item `it` of the list ordered by chunk, KV head, row block (blocks of the
+// same keys run side by side and find them in L2). Whole warp: with a window
+// the keys before the block's earliest visible one are left out, which takes
+// a minimum over its tokens.
+template <int KT, int NT>
+__device__ __forceinline__ PxItem px_item(const PxParams& p, const int32_t* gq, const int32_t* gk,
+                                          const int32_t* gp, const int32_t* gb, int it, int lane) {
+  PxItem t;
+  const int blocks = gb[p.groups];
+  const int r = it / blocks;
+  const int blk = it - r * blocks;
+  t.chunk = r / p.Hkv;
+  t.kvh = r - t.chunk * p.Hkv;
+  int lo = 0, hi = p.groups;
+  while (hi - lo > 1) {   // the group with gb[g] <= blk < gb[g + 1]
+    const int mid = (lo + hi) >> 1;
+    if (gb[mid] <= blk) lo = mid;
+    else hi = mid;
+  }
+  t.tok0 = gq[lo] + (blk - gb[lo]) * NT * p.QB;
+  t.nq = min(NT * p.QB, gq[lo + 1] - t.tok0);
+  t.tiles = (t.nq + p.QB - 1) / p.QB;
+  t.keys = gk[lo + 1] - gk[lo];
+  t.list0 = gp[lo];
+  t.pages = gp[lo + 1] - gp[lo];
+  const int all = (t.keys + KT - 1) / KT;
+  const int per = (all + p.num_splits - 1) / p.num_splits;
+  int t0 = min(t.chunk * per, all);
+  const int t1 = min(t0 + per, all);
+  if (p.window > 0) {
+    int pos = INT32_MAX;
+    for (int i = lane; i < t.nq; i += 32) pos = min(pos, p.row_pos[t.tok0 + i]);
+    pos = __reduce_min_sync(0xffffffffu, pos);
+    t0 = min(max(t0, max(0, pos - p.window + 1) / KT), t1);
+  }
+  t.first = t0 * KT;
+  t.n = t1 - t0;
+  return t;
+}
+
+// A tile row's accumulator from TMEM to its fp32 partial row, 32 columns at a
+// time: the eight 16-byte pieces of a lane's row are transposed within groups
+// of eight lanes, so that a store instruction writes four whole 128-byte rows.
+// Warp-collective; `zero` (warp-uniform) stores zeros without reading TMEM.
+template <int D>
+__device__ __forceinline__ void store_partial(uint32_t o_addr, bool zero, float scale, float* row,
+                                              bool valid, int lane) {
+  const int i = lane & 7;
+  const unsigned long long mine = valid ? reinterpret_cast<unsigned long long>(row) : 0ull;
+#pragma unroll
+  for (int blk = 0; blk < D / 32; ++blk) {
+    float o[32];
+    if (!zero) {
+      tc::tmem_ld32(o_addr + blk * 32, o);
+      tc::tmem_wait_ld();
+    } else {
+#pragma unroll
+      for (int e = 0; e < 32; ++e) o[e] = 0.f;
+    }
+    float4 ch[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      ch[e] = make_float4(o[4 * e] * scale, o[4 * e + 1] * scale, o[4 * e + 2] * scale,
+                          o[4 * e + 3] * scale);
+    transpose8_chunks(ch, lane);   // ch[e] of lane i: piece i of the group's row e
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const unsigned long long to = __shfl_sync(0xffffffffu, mine, (lane & ~7) + e);
+      if (to) *reinterpret_cast<float4*>(reinterpret_cast<float*>(to) + blk * 32 + i * 4) = ch[e];
+    }
+  }
+}
+
+template <int D, bool FP8>
+__global__ void __launch_bounds__(PxCfg<D, FP8>::LB_THREADS, 1)
+    prefix_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
+                     const __grid_constant__ CUtensorMap tmK,
+                     const __grid_constant__ CUtensorMap tmV, const PxParams p) {
+  using C = PxCfg<D, FP8>;
+  constexpr int KT = C::KT, NST = C::NST, NT = C::NT;
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);   // by item
+  uint64_t* q_empty = q_full + 1;       // the item's last S has completed
+  uint64_t* q_cvt = q_empty + 1;        // FP8: Q is f16
+  uint64_t* kv_full = q_cvt + 1;        // [NST] by K/V tile
+  uint64_t* kv_empty = kv_full + NST;
+  uint64_t* s_full = kv_empty + NST;    // [NT] by the tile's own steps
+  uint64_t* p_full = s_full + NT;       // [NT] P_t written and O_t rescaled (128 arrivals)
+  uint64_t* pv_done = p_full + NT;      // [NT]
+  uint64_t* drain = pv_done + NT;
+  uint64_t* c_full = drain + 1;         // FP8: [NSTF] codes landed
+  uint64_t* c_empty = c_full + C::NSTF;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(c_empty + C::NSTF);
+  int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
+  int* status = &g_status_prefix_tc;
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  // the groups' tables in shared memory: every role looks every item up
+  int32_t* gs = reinterpret_cast<int32_t*>(smem + C::OFF_GRP);
+  const bool staged = p.groups <= C::GRP_CAP;
+  const int32_t *gq = p.grp_q, *gk = p.grp_k, *gp = p.grp_pages, *gb = p.grp_blk;
+  if (staged) {
+    for (int i = threadIdx.x; i <= p.groups; i += blockDim.x) {
+      gs[i] = gq[i];
+      gs[C::GRP_CAP + 1 + i] = gk[i];
+      gs[2 * (C::GRP_CAP + 1) + i] = gp[i];
+      gs[3 * (C::GRP_CAP + 1) + i] = gb[i];
+    }
+    gq = gs;
+    gk = gs + C::GRP_CAP + 1;
+    gp = gs + 2 * (C::GRP_CAP + 1);
+    gb = gs + 3 * (C::GRP_CAP + 1);
+  }
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    mbar_init(q_cvt, C::N_CVT);
+    for (int i = 0; i < NST; ++i) {
+      mbar_init(&kv_full[i], FP8 ? C::N_CVT : 1);
+      mbar_init(&kv_empty[i], 1);
+    }
+    for (int t = 0; t < NT; ++t) {
+      mbar_init(&s_full[t], 1);
+      mbar_init(&p_full[t], 128);
+      mbar_init(&pv_done[t], 1);
+    }
+    mbar_init(drain, 1);
+    for (int i = 0; i < C::NSTF; ++i) {
+      mbar_init(&c_full[i], 1);
+      mbar_init(&c_empty[i], C::N_CVT);
+    }
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tc::tmem_alloc(tmem_slot, C::TMEM_COLS);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  const int n_items = gb[p.groups] * p.Hkv * p.num_splits;
+  const int step = static_cast<int>(gridDim.x);
+  auto item = [&](int it) { return px_item<KT, NT>(p, gq, gk, gp, gb, it, lane); };
+  // A wait that gives up in any lane makes the whole warp leave its loop.
+  auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status));
+  };
+  int g_prod = 0, qi_prod = 0;   // producer: K/V tiles and Q loads issued
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- producer
+    const bool leader = (lane == 0);
+    if (leader) {
+      tma_prefetch_desc(&tmQ);
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+    }
+    const uint64_t policy = policy_evict_last();   // the row blocks of a group re-read the keys
+    const uint32_t q_bytes = static_cast<uint32_t>(C::NSUB * 128 * p.G * p.QB);
+    const int nbox = KT / p.box_rows;
+    const int skip_tile = hook_skip_tile();
+    int g = 0, qi = 0;
+    bool ok = true;
+    for (int it = blockIdx.x; ok && it < n_items; it += step) {
+      const PxItem t = item(it);
+      if (leader && t.keys > t.pages * p.page_size) atomicExch(status, SINKATTN_BAD_LENGTHS);
+      if (t.n == 0) continue;
+      if (qi > 0 && !wwait(q_empty, (qi - 1) & 1)) break;
+      if (leader) {
+        mbar_arrive_expect_tx(q_full, q_bytes * t.tiles);
+        for (int tt = 0; tt < t.tiles; ++tt)
+#pragma unroll
+          for (int sub = 0; sub < C::NSUB; ++sub)
+            tc::tma_load_3d(smem + tt * C::Q_TILE + sub * C::QSUB, &tmQ, sub * 64, t.kvh * p.G,
+                            t.tok0 + tt * p.QB, q_full);
+      }
+      ++qi;
+      PageCursor pc;
+      pc.start(p.page_indices + t.list0, t.pages, t.first / p.page_size, lane);
+      for (int j = 0; j < t.n; ++j, ++g) {
+        const int st = g % (FP8 ? C::NSTF_MOD : NST);
+        uint64_t* full = FP8 ? &c_full[st] : &kv_full[st];
+        if (!wwait(FP8 ? &c_empty[st] : &kv_empty[st],
+                   ((g / (FP8 ? C::NSTF_MOD : NST)) & 1) ^ 1)) {
+          ok = false;
+          break;
+        }
+        if (g == skip_tile) continue;   // test hook: the waits for this tile run out
+        if (leader) mbar_arrive_expect_tx(full, FP8 ? C::CODE_STAGE : C::STAGE);
+        // one box per page segment, lane i issuing box i: rows (page, head, slot) of the pool
+        const int j0 = t.first + j * KT;
+        const int a = j0 + min(lane, nbox - 1) * p.box_rows;
+        const int page = pc.get(j0 / p.page_size, a / p.page_size, lane);
+        __syncwarp();   // (the expected bytes are announced before any lane's copy)
+        if (lane < nbox) {
+          const int row = (page * p.Hkv + t.kvh) * p.page_size + a % p.page_size;
+          if constexpr (FP8) {
+            uint8_t* codes = smem + C::OFF_CODE + st * C::CODE_STAGE + (a - j0) * D;
+            tma_load_2d_hint(codes, &tmK, 0, row, full, policy);
+            tma_load_2d_hint(codes + KT * D, &tmV, 0, row, full, policy);
+          } else {
+            uint8_t* kt = smem + C::OFF_KV + st * C::STAGE + (a - j0) * 128;
+#pragma unroll
+            for (int sub = 0; sub < C::NSUB; ++sub) {
+              tma_load_2d_hint(kt + sub * C::KVSUB, &tmK, sub * 64, row, full, policy);
+              tma_load_2d_hint(kt + C::KV_TILE + sub * C::KVSUB, &tmV, sub * 64, row, full, policy);
+            }
+          }
+        }
+      }
+    }
+    g_prod = g;
+    qi_prod = qi;
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA issuer
+    // The whole warp runs the schedule; one elected lane issues.
+    const bool leader = tc::elect_one();
+    constexpr uint32_t idesc_s =
+        FP8 ? tc::idesc_f16_f32(128, KT, false) : tc::idesc_bf16_f32(128, KT, false);
+    constexpr uint32_t idesc_o =
+        FP8 ? tc::idesc_f16_f32(128, D, true) : tc::idesc_bf16_f32(128, D, true);
+    constexpr uint64_t STAGE16 = C::STAGE >> 4, QSUB16 = C::QSUB >> 4, KVSUB16 = C::KVSUB >> 4;
+    const uint64_t qd0 = tc::smem_desc_sw128(smem_u32(smem), 16, 1024);
+    const uint64_t kd0 = tc::smem_desc_sw128(smem_u32(smem + C::OFF_KV), 16, 1024);
+    const uint64_t vd0 = tc::smem_desc_sw128(smem_u32(smem + C::OFF_KV + C::KV_TILE),
+                                             static_cast<uint32_t>(C::KVSUB), 1024);
+    auto commit1 = [&](uint64_t* bar) {
+      if (leader) tc::commit(bar);
+      __syncwarp();
+    };
+    auto issue_s = [&](int t, int g) {
+      const uint64_t kd = kd0 + static_cast<uint64_t>(g % NST) * STAGE16;
+      const uint64_t qd = qd0 + static_cast<uint64_t>(t) * (C::Q_TILE >> 4);
+      if (leader) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint64_t s = static_cast<uint64_t>(kk & 3) * 2;
+          tc::mma_ss(tmem + C::col_s(t), qd + static_cast<uint64_t>(kk >> 2) * QSUB16 + s,
+                     kd + static_cast<uint64_t>(kk >> 2) * KVSUB16 + s, idesc_s, kk > 0 ? 1u : 0u);
+        }
+        tc::commit(&s_full[t]);
+      }
+      __syncwarp();
+    };
+    auto issue_pv = [&](int t, int g, bool first) {
+      const uint64_t vd = vd0 + static_cast<uint64_t>(g % NST) * STAGE16;
+      if (leader) {
+#pragma unroll
+        for (int kk = 0; kk < KT / 16; ++kk)
+          tc::mma_ts(tmem + C::col_o(t), tmem + C::col_s(t) + kk * 8,
+                     vd + static_cast<uint64_t>(kk) * 128u, idesc_o, (!first || kk > 0) ? 1u : 0u);
+        tc::commit(&pv_done[t]);
+      }
+      __syncwarp();
+    };
+    int g = 0, qi = 0;
+    int steps[NT];   // steps of each tile so far: the phase of its barriers
+#pragma unroll
+    for (int tt = 0; tt < NT; ++tt) steps[tt] = 0;
+    bool ok = true;
+    for (int it = blockIdx.x; ok && it < n_items; it += step) {
+      const PxItem t = item(it);
+      if (t.n == 0) continue;
+      // S_t of the first K/V tile for every row tile, then per K/V tile and
+      // row tile: PV_t, then the next S_t into the same buffer once that
+      // PV_t has completed (S overwrites P).
+      ok = wwait(FP8 ? q_cvt : q_full, qi & 1) && wwait(&kv_full[g % NST], (g / NST) & 1);
+#pragma unroll
+      for (int tt = 0; tt < NT; ++tt) {
+        if (!ok || tt >= t.tiles) break;
+        // the previous item's last PV of this tile has completed
+        if (steps[tt] > 0 && !wwait(&pv_done[tt], (steps[tt] - 1) & 1)) { ok = false; break; }
+        tc::fence_after_sync();
+        issue_s(tt, g);
+      }
+      if (!ok) break;
+      if (t.n == 1) commit1(q_empty);
+      for (int j = 0; ok && j < t.n; ++j) {
+        const int gg = g + j;
+#pragma unroll
+        for (int tt = 0; tt < NT; ++tt) {
+          if (tt >= t.tiles) break;
+          if (!wwait(&p_full[tt], steps[tt] & 1)) { ok = false; break; }
+          tc::fence_after_sync();
+          issue_pv(tt, gg, j == 0);
+          if (tt == t.tiles - 1) commit1(&kv_empty[gg % NST]);
+          if (j + 1 < t.n) {
+            if (tt == 0 && !wwait(&kv_full[(gg + 1) % NST], ((gg + 1) / NST) & 1)) { ok = false; break; }
+            if (!wwait(&pv_done[tt], steps[tt] & 1)) { ok = false; break; }
+            tc::fence_after_sync();
+            issue_s(tt, gg + 1);
+            if (j + 2 == t.n && tt == t.tiles - 1) commit1(q_empty);
+          }
+          ++steps[tt];
+        }
+      }
+      g += t.n;
+      ++qi;
+    }
+    // every MMA this warp issued has completed before the block frees TMEM
+    commit1(drain);
+    mbar_drain(drain, 0);
+  } else if (FP8 && warp >= C::W_CVT) {
+    // ------------------------------------------------------------ converters
+    // Per item Q in place, bf16 -> f16; per K/V tile 16-byte runs of codes ->
+    // f16 in the tile ring. Generic-proxy writes that the tensor core reads:
+    // fenced before each hand-over.
+    constexpr int N = C::N_CVT * 32;
+    constexpr int RUNS_ROW = D / 16, RUNS = 2 * KT * RUNS_ROW, PER = RUNS / N;
+    static_assert(RUNS % N == 0, "whole runs per converter thread");
+    const int ct = static_cast<int>(threadIdx.x) - C::W_CVT * 32;
+    int g = 0, qi = 0;
+    bool ok = true;
+    for (int it = blockIdx.x; ok && it < n_items; it += step) {
+      const PxItem t = item(it);
+      if (t.n == 0) continue;
+      if (!wwait(q_full, qi & 1)) break;
+      for (int c = ct; c < t.tiles * C::Q_TILE / 16; c += N) {
+        uint4 w = *reinterpret_cast<const uint4*>(smem + c * 16);
+        w.x = pack_f16x2(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u));
+        w.y = pack_f16x2(__uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
+        w.z = pack_f16x2(__uint_as_float(w.z << 16), __uint_as_float(w.z & 0xffff0000u));
+        w.w = pack_f16x2(__uint_as_float(w.w << 16), __uint_as_float(w.w & 0xffff0000u));
+        *reinterpret_cast<uint4*>(smem + c * 16) = w;
+      }
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_cvt);
+      ++qi;
+      for (int j = 0; j < t.n; ++j, ++g) {
+        const int sc = g % C::NSTF_MOD, st = g % NST;
+        if (!wwait(&c_full[sc], (g / C::NSTF_MOD) & 1)) { ok = false; break; }
+        const uint8_t* codes = smem + C::OFF_CODE + sc * C::CODE_STAGE;
+        uint8_t* dst = smem + C::OFF_KV + st * C::STAGE;
+        uint4 w[PER];
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+          w[i] = *reinterpret_cast<const uint4*>(codes + (ct + i * N) * 16);   // [K | V][KT][D]
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c_empty[sc]);
+        if (!wwait(&kv_empty[st], ((g / NST) & 1) ^ 1)) { ok = false; break; }
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          const int c = ct + i * N;
+          const int tensor = c / (KT * RUNS_ROW);   // 0: K, 1: V
+          const int rem = c - tensor * (KT * RUNS_ROW);
+          const int row = rem / RUNS_ROW, cb = rem % RUNS_ROW;
+          uint4 h0, h1;
+          h0.x = e4m3x2_to_f16x2(static_cast<uint16_t>(w[i].x));
+          h0.y = e4m3x2_to_f16x2(static_cast<uint16_t>(w[i].x >> 16));
+          h0.z = e4m3x2_to_f16x2(static_cast<uint16_t>(w[i].y));
+          h0.w = e4m3x2_to_f16x2(static_cast<uint16_t>(w[i].y >> 16));
+          h1.x = e4m3x2_to_f16x2(static_cast<uint16_t>(w[i].z));
+          h1.y = e4m3x2_to_f16x2(static_cast<uint16_t>(w[i].z >> 16));
+          h1.z = e4m3x2_to_f16x2(static_cast<uint16_t>(w[i].w));
+          h1.w = e4m3x2_to_f16x2(static_cast<uint16_t>(w[i].w >> 16));
+          uint8_t* sub = dst + tensor * C::KV_TILE + (cb >> 2) * C::KVSUB;
+          const int ch = (cb & 3) * 2;
+          *reinterpret_cast<uint4*>(sub + sw128_offset(row, ch)) = h0;
+          *reinterpret_cast<uint4*>(sub + sw128_offset(row, ch + 1)) = h1;
+        }
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&kv_full[st]);
+      }
+    }
+  } else {
+    // ---------------------------------------------------------------- softmax
+    const int tt = (warp - 2) >> 2;  // row tile
+    const int quad = warp & 3;       // TMEM lane quadrant this warp may access
+    const int row = quad * 32 + lane;
+    const int G = p.G;
+    const int rg = row / G;          // token within the tile
+    const int hig = row - rg * G;    // head within the group
+    const int tl = tt * p.QB + rg;   // token within the block
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const uint32_t s_addr = lane_base + C::col_s(tt);
+    const uint32_t o_addr = lane_base + C::col_o(tt);
+    constexpr int NCH = KT / 32;     // 32-column pieces of a score row
+    int steps = 0;
+    bool ok = true;
+    for (int it = blockIdx.x; ok && it < n_items; it += step) {
+      const PxItem t = item(it);
+      if (tt >= t.tiles) continue;
+      const bool valid = rg < p.QB && tl < t.nq;
+      const float kscale = FP8 ? p.k_scale[t.kvh] : 1.f;
+      const float c2 = p.scale_log2 * kscale;   // raw logits -> base-2 exponents
+      int lo_r = 0;
+      if (p.window > 0 && valid) lo_r = max(0, p.row_pos[t.tok0 + tl] - p.window + 1);
+      const int hi_r = t.keys - 1;
+      float m_used = kNegInf, l = 0.f;
+      for (int j = 0; j < t.n; ++j, ++steps) {
+        if (!wwait(&s_full[tt], steps & 1)) { ok = false; break; }
+        tc::fence_after_sync();
+        const int j0 = t.first + j * KT;
+        const int clo = lo_r - j0, chi = hi_r - j0;
+        float v[NCH][32];
+#pragma unroll
+        for (int c = 0; c < NCH; ++c) tc::tmem_ld32(s_addr + 32 * c, v[c]);
+        tc::tmem_wait_ld();
+        if (clo > 0 || chi < KT - 1) {
+#pragma unroll
+          for (int c = 0; c < NCH; ++c) {
+            const int lo_c = clo - c * 32, hi_c = chi - c * 32;
+            if (lo_c <= 0 && hi_c >= 31) continue;
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (e < lo_c || e > hi_c) v[c][e] = kNegInf;
+          }
+        }
+        // row maximum: 2 NCH independent chains of three-input maxima
+        float mxc[2 * NCH];
+#pragma unroll
+        for (int i = 0; i < 2 * NCH; ++i)
+          mxc[i] = fmaxf(v[i >> 1][(i & 1) * 16], v[i >> 1][(i & 1) * 16 + 1]);
+#pragma unroll
+        for (int c = 0; c < NCH; ++c)
+#pragma unroll
+          for (int e = 2; e < 16; e += 2) {
+            mxc[2 * c] = fmax3(mxc[2 * c], v[c][e], v[c][e + 1]);
+            mxc[2 * c + 1] = fmax3(mxc[2 * c + 1], v[c][16 + e], v[c][16 + e + 1]);
+          }
+        float mx = fmax3(mxc[0], mxc[1], mxc[2]);
+#pragma unroll
+        for (int i = 3; i < 2 * NCH; i += 2)
+          mx = (i + 1 < 2 * NCH) ? fmax3(mx, mxc[i], mxc[i + 1]) : fmaxf(mx, mxc[i]);
+
+        float alpha = 1.f;
+        bool rescale = false;
+        if (mx > m_used) {
+          alpha = (m_used == kNegInf) ? 0.f : ex2((m_used - mx) * c2);
+          m_used = mx;
+          rescale = true;
+        }
+        const float mb = (m_used == kNegInf) ? 0.f : m_used * c2;
+
+        // P = 2^(s c2 - mb) into the first KT / 2 columns of this S buffer
+        // (all scores are in registers); scale-subtract and the exact sum
+        // run two lanes per instruction.
+        const float2 c2x2 = make_float2(c2, c2), nmb2 = make_float2(-mb, -mb);
+        float2 rs2[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                         make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int c = 0; c < NCH; ++c)
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            uint32_t pk[8];
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              const int k = hh * 16 + e;
+              const float2 x = __ffma2_rn(make_float2(v[c][k], v[c][k + 1]), c2x2, nmb2);
+              const float2 a = make_float2(ex2(x.x), ex2(x.y));
+              rs2[(e >> 1) & 3] = __fadd2_rn(rs2[(e >> 1) & 3], a);
+              pk[e >> 1] = FP8 ? pack_f16x2(a.x, a.y) : pack_bf16x2(a.x, a.y);
+            }
+            tc::tmem_st8(s_addr + 16 * c + 8 * hh, pk);
+          }
+        const float2 rsa = __fadd2_rn(__fadd2_rn(rs2[0], rs2[1]), __fadd2_rn(rs2[2], rs2[3]));
+
+        // S_t was issued after the tile's previous PV_t had completed, so O_t
+        // is free to touch. Rescale it when some row of this warp moved its
+        // maximum (warp-uniform branch).
+        if (j >= 1 && __any_sync(0xffffffffu, rescale)) {
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            float o[32];
+            tc::tmem_ld32(o_addr + c * 32, o);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] *= alpha;
+            tc::tmem_st32(o_addr + c * 32, o);
+          }
+        }
+        tc::tmem_wait_st();
+        l = l * alpha + (rsa.x + rsa.y);
+        tc::fence_before_sync();
+        mbar_arrive(&p_full[tt]);
+      }
+      if (!ok) break;
+      // O_t is read out before this thread hands over P of the next item, so
+      // the next item's first PV (which overwrites O_t) comes after it.
+      if (t.n >= 1) {
+        if (!wwait(&pv_done[tt], (steps - 1) & 1)) { ok = false; break; }
+        tc::fence_after_sync();
+      }
+      const bool some = l > 0.f;   // the row sees a key of the chunk
+      const size_t slot =
+          (static_cast<size_t>(t.tok0 + tl) * p.Hq + t.kvh * G + hig) * p.part_slots + t.chunk;
+      store_partial<D>(o_addr, t.n < 1, FP8 ? p.v_scale[t.kvh] : 1.f, p.part_acc + slot * D, valid,
+                       lane);
+      tc::fence_before_sync();
+      if (valid)
+        *reinterpret_cast<float2*>(p.part_md + slot * 2) =
+            make_float2(some ? m_used * (p.sm_scale * kscale) : kNegInf, some ? l : 0.f);
+    }
+  }
+
+  // a warp that left its loop early may still have TMEM loads or stores in flight
+  tc::tmem_wait_ld();
+  tc::tmem_wait_st();
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 0 && lane == 0 && *abort_flag) {
+    // a wait gave up: let every issued copy land before the block's shared
+    // memory goes away (a left-out tile's phase never completes: bounded)
+    if (qi_prod > 0) mbar_drain(q_full, (qi_prod - 1) & 1);
+    constexpr int R = FP8 ? C::NSTF_MOD : NST;
+    for (int i = max(0, g_prod - R); i < g_prod; ++i)
+      mbar_drain(FP8 ? &c_full[i % R] : &kv_full[i % R], (i / R) & 1);
+  }
+  if (warp == 1) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+template <int D, bool FP8>
+int launch(const AttnArgs& a, const SharedPlan& plan, cudaStream_t stream) {
+  using C = PxCfg<D, FP8>;
+  const int G = a.Hq / a.Hkv, QB = 128 / G;
+  CUtensorMap tmQ, tmK, tmV;
+  int rc = make_q_tmap(&tmQ, a.q, static_cast<uint64_t>(a.total_q), a.Hq, D, G, QB);
+  if (rc) return rc;
+  const uint64_t rows = kv_map_rows(a);
+  const int box = kv_box_rows(a, C::KT);
+  rc = FP8 ? make_rows_tmap_u8(&tmK, a.k, rows, D, box) : make_rows_tmap(&tmK, a.k, rows, D, box, 128);
+  if (rc) return rc;
+  rc = FP8 ? make_rows_tmap_u8(&tmV, a.v, rows, D, box) : make_rows_tmap(&tmV, a.v, rows, D, box, 128);
+  if (rc) return rc;
+  PxParams p{};
+  p.grp_q = plan.grp_q;
+  p.grp_k = plan.grp_k;
+  p.grp_pages = plan.grp_pages;
+  p.grp_blk = plan.grp_blk;
+  p.row_pos = plan.row_pos;
+  p.page_indices = a.page_indices;
+  p.groups = a.batch;
+  p.Hq = a.Hq;
+  p.Hkv = a.Hkv;
+  p.G = G;
+  p.QB = QB;
+  p.num_splits = a.num_splits;
+  p.window = a.window;
+  p.sm_scale = a.sm_scale;
+  p.scale_log2 = a.sm_scale * kLog2e;
+  p.page_size = a.page_size;
+  p.box_rows = box;
+  p.k_scale = a.k_scale;
+  p.v_scale = a.v_scale;
+  p.part_acc = a.part_acc;
+  p.part_md = a.part_md;
+  p.part_slots = part_slots(a);
+  // blocks of rows: at most one per group more than its full ones
+  const int64_t blocks = a.batch + a.total_q / (C::NT * QB);
+  const int64_t items = blocks * a.Hkv * a.num_splits;
+  if (items >= (int64_t{1} << 31)) {
+    set_error("too many work items");
+    return SINKATTN_UNSUPPORTED;
+  }
+  auto kern = prefix_tc_kernel<D, FP8>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e == cudaSuccess) {
+    kern<<<static_cast<unsigned>(std::min<int64_t>(items, sm_count())), C::THREADS, C::SMEM, stream>>>(
+        tmQ, tmK, tmV, p);
+    e = cudaGetLastError();
+  }
+  if (e != cudaSuccess) {
+    set_error("shared-prefix kernel launch: %s", cudaGetErrorString(e));
+    return SINKATTN_CUDA_ERROR;
+  }
+  return SINKATTN_OK;
+}
+
+}  // namespace
+
+int prefix_block_tokens(int G) { return 2 * (128 / G); }
+int prefix_tile_keys(int d, bool fp8) {
+  if (d == 64) return PxCfg<64, false>::KT;
+  return fp8 ? PxCfg<128, true>::KT : PxCfg<128, false>::KT;
+}
+
+int launch_prefix_tc(const AttnArgs& a, const SharedPlan& plan, cudaStream_t stream) {
+  if (a.d == 64) return a.kv_fp8 ? launch<64, true>(a, plan, stream) : launch<64, false>(a, plan, stream);
+  return a.kv_fp8 ? launch<128, true>(a, plan, stream) : launch<128, false>(a, plan, stream);
+}
+
+SINKATTN_DEFINE_SET_HOOKS(set_hooks_prefix_tc)
+
+int read_status_prefix_tc(cudaStream_t s, int* status) {
+  int zero = 0;
+  if (cudaMemcpyFromSymbolAsync(status, g_status_prefix_tc, sizeof(int), 0,
+                                cudaMemcpyDeviceToHost, s) != cudaSuccess)
+    return SINKATTN_CUDA_ERROR;
+  if (cudaStreamSynchronize(s) != cudaSuccess) return SINKATTN_CUDA_ERROR;
+  if (cudaMemcpyToSymbolAsync(g_status_prefix_tc, &zero, sizeof(int), 0, cudaMemcpyHostToDevice,
+                              s) != cudaSuccess)
+    return SINKATTN_CUDA_ERROR;
+  if (cudaStreamSynchronize(s) != cudaSuccess) return SINKATTN_CUDA_ERROR;
+  return SINKATTN_OK;
+}
+
+}  // namespace sinkattn

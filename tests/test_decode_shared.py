@@ -22,7 +22,8 @@ import torch
 
 import oracle
 import gqa_attention_softmax_gb300 as sa
-from gqa_attention_softmax_gb300._binding import BAD_LENGTHS, INVALID_ARG, UNSUPPORTED
+from gqa_attention_softmax_gb300._binding import (BAD_LENGTHS, INVALID_ARG, TIMEOUT,
+                                                  UNSUPPORTED)
 
 gpu = pytest.mark.gpu
 
@@ -168,14 +169,56 @@ IDS = ["b%d_g%d_q%d_h%d-%d_d%d_p%d_w%d_s%d-%d" % (sum(len(g[1]) for g in c[0]), 
 
 
 @gpu
+@pytest.mark.parametrize("kernel", ["auto", "warp"])
 @pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
 @pytest.mark.parametrize("case", CASES, ids=IDS)
-def test_shared_decode_matches_oracle(case, fp8):
+def test_shared_decode_matches_oracle(case, fp8, kernel):
     groups, q_len, Hq, Hkv, d, page, window, ps, ss, qs = case
     x, h = make(groups, q_len, Hq, Hkv, d, page, seed=page + q_len, q_scale=qs, fp8=fp8)
     g = {k: v.cuda() for k, v in x.items()}
-    out, lse = call(g, h, window=window, prefix_splits=ps, num_splits=ss)
+    sa.sinkattn_set_decode_kernel(kernel)
+    try:
+        out, lse = call(g, h, window=window, prefix_splits=ps, num_splits=ss)
+    finally:
+        sa.sinkattn_set_decode_kernel("auto")
     check(out, lse, x, h, window=window)
+
+
+@gpu
+@pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+def test_row_blocks_and_tiles_of_every_page_size(fp8, d, page):
+    """Groups that fill whole row blocks, one tile of a block, and a part of one; prefixes
+    that end inside a K/V tile; more items than SMs."""
+    G = 8 if d == 64 else 16
+    per = 128 // G   # tokens of a tile
+    n = max(1, 512 // page)
+    groups = [(n, [1] * (2 * per)), (n + 1, [2] * (per - 1)), (2 * n, [1] * (4 * per + 3)),
+              (1, [5] * per)]
+    x, h = make(groups, 1, 2 * G, 2, d, page, seed=page, fp8=fp8)
+    g = {k: v.cuda() for k, v in x.items()}
+    for ps in (1, 3, 40):
+        out, lse = call(g, h, prefix_splits=ps, num_splits=1)
+        check(out, lse, x, h)
+
+
+@gpu
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+def test_a_wait_that_runs_out_is_recorded(fp8):
+    """The first block's producer leaves one tile's copies out: its waits give up after about
+    10 ms, the call ends with SINKATTN_TIMEOUT, and the next one is right."""
+    x, h = make([(20, [5] * 40)], 1, 64, 8, 64, 16, seed=9, fp8=fp8)
+    g = {k: v.cuda() for k, v in x.items()}
+    assert sa.sinkattn_debug_status() == 0
+    sa.sinkattn_debug_set_hooks(20_000_000, 1)
+    try:
+        call(g, h, prefix_splits=1, num_splits=1)
+        assert sa.sinkattn_debug_status() == TIMEOUT
+    finally:
+        sa.sinkattn_debug_set_hooks(0, -1)
+    out, lse = call(g, h)
+    check(out, lse, x, h)
 
 
 @gpu
