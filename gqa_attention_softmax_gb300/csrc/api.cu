@@ -513,8 +513,8 @@ int decode_shared_impl(const void* q, const void* k_pages, const void* v_pages, 
   plan.grp_q = plan.pages + batch + 1;
   plan.grp_k = plan.grp_q + num_groups + 1;
   plan.grp_pages = plan.grp_k + num_groups + 1;
-  plan.grp_blk = plan.grp_pages + num_groups + 1;
-  plan.row_pos = plan.grp_blk + num_groups + 1;
+  plan.grp_unit = plan.grp_pages + num_groups + 1;
+  plan.row_pos = plan.grp_unit + num_groups + 1;
   const size_t rows = static_cast<size_t>(batch) * q_len;
   const size_t plan_bytes = shared_plan_bytes(batch, q_len, num_groups);
   float* part_acc = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan_bytes);
@@ -523,7 +523,8 @@ int decode_shared_impl(const void* q, const void* k_pages, const void* v_pages, 
       ((rows * num_qo_heads * slots * head_dim * 4 + 255) & ~static_cast<size_t>(255)));
   rc = launch_shared_plan(kv_indptr, pg.page_indptr, group_indptr, prefix_lens, num_groups,
                           pg.page_size, batch, q_len, max_prefix_len, max_suffix_len,
-                          prefix_block_tokens(num_qo_heads / num_kv_heads), plan, s);
+                          prefix_block_tokens(num_qo_heads / num_kv_heads),
+                          prefix_tile_keys(head_dim, f8 != nullptr), num_kv_heads, plan, s);
   if (rc) return rc;
 
   a.part_acc = part_acc;
@@ -554,8 +555,8 @@ int decode_shared_impl(const void* q, const void* k_pages, const void* v_pages, 
   a.cu_k = plan.kv;
   a.part_first = prefix_splits;
   if ((rc = launch_partials(a, s))) return rc;
-  return launch_merge(part_acc, part_md, sinks, static_cast<int32_t>(rows), num_qo_heads, head_dim,
-                      slots, out, lse, s, true);
+  return launch_merge_sparse(part_acc, part_md, sinks, static_cast<int32_t>(rows), num_qo_heads,
+                             head_dim, slots, out, lse, s);
 }
 
 }  // namespace
@@ -672,26 +673,16 @@ int sinkattn_decode_shared_default_splits(int32_t batch, int32_t q_len, int32_t 
   const int G = num_qo_heads / num_kv_heads;
   const int64_t tokens = static_cast<int64_t>(batch) * q_len;
   if (G >= 1 && G <= 64 && prefix_on_tc(tokens, G, num_groups)) {
-    // rounds of work items over the SMs x (tiles of an item + its start and
-    // end), plus what the merge pays for one more partial of every row
-    const int kt = prefix_tile_keys(head_dim, false);
+    // partials that let the kernel deal its units out evenly (prefixes of
+    // several groups about half as long as the longest), at most 16
+    const int64_t tiles = (max_prefix_len + prefix_tile_keys(head_dim, false) - 1) /
+                          prefix_tile_keys(head_dim, false);
     const int64_t bt = prefix_block_tokens(G);
-    const int64_t items = num_groups * ((tokens / num_groups + bt - 1) / bt) * num_kv_heads;
-    const int64_t tiles = (static_cast<int64_t>(max_prefix_len) + kt - 1) / kt;
-    const double step_us = head_dim == 64 ? 1.0 : 1.9;
-    const double part_us = static_cast<double>(tokens) * num_qo_heads * head_dim * 8 / 6e6;
-    const int sms = sm_count();
-    double best = 0;
-    *prefix_splits = 1;
-    for (int64_t s = 1; s <= 64 && s <= std::max<int64_t>(tiles, 1); ++s) {
-      const double us = static_cast<double>((items * s + sms - 1) / sms) *
-                            static_cast<double>((tiles + s - 1) / s + 3) * step_us +
-                        static_cast<double>(s) * part_us;
-      if (s == 1 || us < best) {
-        best = us;
-        *prefix_splits = static_cast<int32_t>(s);
-      }
-    }
+    const int64_t units = num_groups * ((tokens / num_groups + bt - 1) / bt) * num_kv_heads *
+                          (num_groups > 1 ? (tiles + 1) / 2 : tiles);
+    const int64_t quota = std::max<int64_t>(1, (units + sm_count() - 1) / sm_count());
+    const int64_t n = tiles > 1 ? (tiles - 1 + quota - 1) / quota + 1 : 1;
+    *prefix_splits = static_cast<int32_t>(std::min<int64_t>(n, 16));
     return SINKATTN_OK;
   }
   // the warp-level kernel's blocks of up to 64 query rows

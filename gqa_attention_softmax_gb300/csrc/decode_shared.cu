@@ -23,7 +23,7 @@ struct PlanParams {
   const int32_t* page_indptr;
   const int32_t* group_indptr;
   const int32_t* prefix_lens;
-  int groups, page_size, batch, q_len, max_prefix, max_suffix, block_tokens;
+  int groups, page_size, batch, q_len, max_prefix, max_suffix, block_tokens, tile_keys, Hkv;
   SharedPlan out;
 };
 
@@ -70,10 +70,10 @@ __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const PlanParams 
               (g == p.groups - 1 && b1 != p.batch);
   }
   broken = __syncthreads_or(broken);
-  int run = 0, run_blk = 0, total;
+  int run = 0, run_unit = 0, total;
   for (int base = 0; base < p.groups; base += kThreads) {
     const int g = base + tid;
-    int len = 0, blocks = 0;
+    int len = 0, units = 0;
     if (g < p.groups && !broken) {
       const int b0 = p.group_indptr[g], b1 = p.group_indptr[g + 1];
       len = prefix_of(g, &bad);
@@ -82,7 +82,9 @@ __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const PlanParams 
         bad = true;
         len = 0;
       }
-      blocks = ((b1 - b0) * p.q_len + p.block_tokens - 1) / p.block_tokens;
+      // row blocks x KV heads x key tiles (below 2^31: checked on the host)
+      units = ((b1 - b0) * p.q_len + p.block_tokens - 1) / p.block_tokens * p.Hkv *
+              ((len + p.tile_keys - 1) / p.tile_keys);
       p.out.grp_q[g] = b0 * p.q_len;
       p.out.grp_pages[g] = p.page_indptr[b0];
     } else if (g < p.groups) {
@@ -91,17 +93,17 @@ __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const PlanParams 
     }
     const int upto = run + block_sum_scan(len, &total, sums);
     run += total;
-    const int upto_blk = run_blk + block_sum_scan(blocks, &total, sums);
-    run_blk += total;
+    const int upto_unit = run_unit + block_sum_scan(units, &total, sums);
+    run_unit += total;
     if (g < p.groups) {
       p.out.grp_k[g + 1] = upto;
-      p.out.grp_blk[g + 1] = upto_blk;
+      p.out.grp_unit[g + 1] = upto_unit;
     }
   }
   if (tid == 0) {
     p.out.grp_q[p.groups] = p.batch * p.q_len;
     p.out.grp_pages[p.groups] = p.page_indptr[p.batch];
-    p.out.grp_blk[0] = 0;
+    p.out.grp_unit[0] = 0;
   }
   if (tid == 0) p.out.grp_k[0] = p.out.kv[0] = 0;
   run = 0;
@@ -139,10 +141,10 @@ __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const PlanParams 
 int launch_shared_plan(const int32_t* kv_indptr, const int32_t* page_indptr,
                        const int32_t* group_indptr, const int32_t* prefix_lens, int32_t groups,
                        int32_t page_size, int32_t batch, int32_t q_len, int32_t max_prefix,
-                       int32_t max_suffix, int32_t block_tokens, const SharedPlan& plan,
-                       cudaStream_t stream) {
-  const PlanParams p{kv_indptr, page_indptr, group_indptr, prefix_lens, groups,       page_size,
-                     batch,     q_len,       max_prefix,   max_suffix,  block_tokens, plan};
+                       int32_t max_suffix, int32_t block_tokens, int32_t tile_keys, int32_t Hkv,
+                       const SharedPlan& plan, cudaStream_t stream) {
+  const PlanParams p{kv_indptr,  page_indptr, group_indptr, prefix_lens, groups, page_size, batch,
+                     q_len,      max_prefix,  max_suffix,   block_tokens, tile_keys, Hkv,   plan};
   shared_plan_kernel<<<1, kThreads, 0, stream>>>(p);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) {

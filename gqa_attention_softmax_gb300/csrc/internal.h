@@ -106,6 +106,11 @@ int launch_prefill_tc(const AttnArgs& a, int kind, cudaStream_t stream);
 int launch_merge(const float* part_acc, const float* part_md, const float* sinks, int32_t rows,
                  int32_t Hq, int32_t d, int32_t num_splits, void* out, float* lse,
                  cudaStream_t stream, bool drop_partials);
+// The same for partials of which many are empty (d = 0): those slots'
+// accumulators are not read and need not have been written.
+int launch_merge_sparse(const float* part_acc, const float* part_md, const float* sinks,
+                        int32_t rows, int32_t Hq, int32_t d, int32_t num_slots, void* out,
+                        float* lse, cudaStream_t stream);
 
 // Shared-prefix decode: what the prefix and the per-sequence passes read,
 // derived on the device from the page lists and the groups. All int32.
@@ -115,7 +120,7 @@ struct SharedPlan {
   int32_t* grp_q;     // [groups + 1] first query token of each group
   int32_t* grp_k;     // [groups + 1] running sum of the prefixes' keys
   int32_t* grp_pages; // [groups + 1] first entry of the prefixes' pages
-  int32_t* grp_blk;   // [groups + 1] running sum of the tcgen05 kernel's row blocks
+  int32_t* grp_unit;  // [groups + 1] running sum of the tcgen05 kernel's units of work
   int32_t* row_pos;   // [batch * q_len] position of each query token
 };
 inline size_t shared_plan_ints(int64_t batch, int64_t q_len, int64_t groups) {
@@ -124,8 +129,8 @@ inline size_t shared_plan_ints(int64_t batch, int64_t q_len, int64_t groups) {
 int launch_shared_plan(const int32_t* kv_indptr, const int32_t* page_indptr,
                        const int32_t* group_indptr, const int32_t* prefix_lens, int32_t groups,
                        int32_t page_size, int32_t batch, int32_t q_len, int32_t max_prefix,
-                       int32_t max_suffix, int32_t block_tokens, const SharedPlan& plan,
-                       cudaStream_t stream);
+                       int32_t max_suffix, int32_t block_tokens, int32_t tile_keys, int32_t Hkv,
+                       const SharedPlan& plan, cudaStream_t stream);
 
 // The groups' prefixes on the tcgen05/TMEM path: partials of every query row
 // over its group's prefix (a.batch: groups, a.total_q: query tokens).

@@ -33,6 +33,49 @@ __global__ void __launch_bounds__(256)
   }
 }
 
+template <int D>
+__global__ void __launch_bounds__(256)
+    merge_sparse_kernel(const float* __restrict__ part_acc, const float* __restrict__ part_md,
+                        const float* __restrict__ sinks, int n_rows, int Hq, int S,
+                        __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x & 31;
+  const long long n = static_cast<long long>(n_rows) * Hq;
+  const long long w0 = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+  if (w0 >= n) return;
+  const long long w = n - 1 - w0;   // newest rows first, as above
+  const int h = static_cast<int>(w % Hq);
+  merge_row_sparse<D>(part_md + w * S * 2, part_acc + w * S * D, sinks ? sinks[h] : kNegInf, S,
+                      lane, out + w * D, lse != nullptr ? lse + w : nullptr);
+}
+
+int launch_merge_sparse(const float* part_acc, const float* part_md, const float* sinks,
+                        int32_t rows, int32_t Hq, int32_t d, int32_t num_slots, void* out,
+                        float* lse, cudaStream_t stream) {
+  const long long warps = static_cast<long long>(rows) * Hq;
+  if (warps == 0) return SINKATTN_OK;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((warps + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  auto* o = static_cast<__nv_bfloat16*>(out);
+  const cudaError_t e =
+      d == 64 ? cudaLaunchKernelEx(&cfg, merge_sparse_kernel<64>, part_acc, part_md, sinks, rows,
+                                   Hq, num_slots, o, lse)
+              : cudaLaunchKernelEx(&cfg, merge_sparse_kernel<128>, part_acc, part_md, sinks, rows,
+                                   Hq, num_slots, o, lse);
+  if (e != cudaSuccess) {
+    set_error("merge kernel launch: %s", cudaGetErrorString(e));
+    return SINKATTN_CUDA_ERROR;
+  }
+  return SINKATTN_OK;
+}
+
 int launch_merge(const float* part_acc, const float* part_md, const float* sinks, int32_t rows,
                  int32_t Hq, int32_t d, int32_t num_splits, void* out, float* lse,
                  cudaStream_t stream, bool drop_partials) {

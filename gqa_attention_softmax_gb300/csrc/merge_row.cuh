@@ -116,4 +116,76 @@ __device__ __forceinline__ void merge_row(const float* md, const float* acc, flo
   if (lse_out != nullptr && lane == 0) *lse_out = dsum > 0.f ? M + lg2(dsum) * kLn2 : NEG_INF;
 }
 
+// The same fold for rows of which many slots are empty (d_s = 0): one pass
+// over the (m, d) pairs, 32 slots at a time, then only the accumulators that
+// have a weight, four in flight. Slots are taken in order.
+template <int D>
+__device__ __forceinline__ void merge_row_sparse(const float* md, const float* acc, float sink,
+                                                 int S, int lane, __nv_bfloat16* orow,
+                                                 float* lse_out) {
+  constexpr int VEC = D / 32;
+  float o[VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) o[e] = 0.f;
+  float M = sink, total = (sink == kNegInf) ? 0.f : 1.f;   // relative to M
+  for (int s0 = 0; s0 < S; s0 += 32) {
+    const float2 mine = s0 + lane < S ? __ldcg(reinterpret_cast<const float2*>(md + 2 * (s0 + lane)))
+                                      : make_float2(kNegInf, 0.f);
+    const bool some = mine.y > 0.f;
+    float top = some ? mine.x : kNegInf;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    const float m1 = fmaxf(M, top);
+    if (m1 == kNegInf) continue;   // no slot so far holds a key
+    const float keep = (M == kNegInf) ? 0.f : ex2((M - m1) * kLog2e);
+    M = m1;
+    const float w = some ? ex2((mine.x - M) * kLog2e) : 0.f;
+    float sum = w * mine.y;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    total = total * keep + sum;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) o[e] *= keep;
+    uint32_t left = __ballot_sync(0xffffffffu, some);
+    while (left) {   // warp-uniform
+      float a[4][VEC], wu[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int s = left ? __ffs(left) - 1 : -1;
+        left &= left - 1;   // (0 stays 0)
+        wu[u] = __shfl_sync(0xffffffffu, w, s < 0 ? 0 : s);
+        if (s >= 0) {
+          const float* src = acc + static_cast<size_t>(s0 + s) * D + lane * VEC;
+          if constexpr (VEC == 4) {
+            const float4 t = __ldcg(reinterpret_cast<const float4*>(src));
+            a[u][0] = t.x; a[u][1] = t.y; a[u][2] = t.z; a[u][3] = t.w;
+          } else {
+            const float2 t = __ldcg(reinterpret_cast<const float2*>(src));
+            a[u][0] = t.x; a[u][1] = t.y;
+          }
+        } else {
+          wu[u] = 0.f;
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) a[u][e] = 0.f;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) o[e] = fmaf(a[u][e], wu[u], o[e]);
+    }
+  }
+  const float inv = total > 0.f ? 1.f / total : 0.f;
+  __nv_bfloat16* op = orow + lane * VEC;
+  if constexpr (VEC == 4) {
+    uint2 pk;
+    pk.x = pack_bf16x2(o[0] * inv, o[1] * inv);
+    pk.y = pack_bf16x2(o[2] * inv, o[3] * inv);
+    *reinterpret_cast<uint2*>(op) = pk;
+  } else {
+    *reinterpret_cast<uint32_t*>(op) = pack_bf16x2(o[0] * inv, o[1] * inv);
+  }
+  if (lse_out != nullptr && lane == 0) *lse_out = total > 0.f ? M + lg2(total) * kLn2 : kNegInf;
+}
+
 }  // namespace sinkattn

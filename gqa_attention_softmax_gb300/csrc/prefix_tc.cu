@@ -4,7 +4,7 @@
 //
 // Rows are (query token, head in group) pairs of one KV head, 128 to a tile;
 // a block has NT tiles that share each K/V tile in shared memory. A work item
-// is (row block, KV head, chunk of the keys); it leaves the rows' partials
+// is (row block, KV head, run of its key tiles); it leaves the rows' partials
 // (m, d, acc) WITHOUT the sink for the merge, like the split-KV kernels:
 //
 //   S_t = Q_t K^T     M 128 rows, N KT keys, K d   (operands in shared memory)
@@ -17,7 +17,14 @@
 // per block (three would not divide 512 rows, the gpt-oss-shaped batch of 64
 // sequences, and TMEM holds no more at d 128); the tiles' chains S -> softmax
 // -> P V interleave on the tensor core. A tile whose rows all lie behind the
-// group's last token is left out. Chunks fill the SMs when row blocks are few.
+// group's last token is left out.
+//
+// The work is cut evenly: a unit is one K/V tile of one (row block, KV head),
+// block c takes the c-th run of Q units in a fixed order, and a row block's
+// partial number is that of its block of units. So few row blocks, ragged
+// groups and prefixes of any mix of lengths fill the SMs alike, and a row
+// block has as many partials as thread blocks worked on it; the merge reads
+// only those.
 //
 // e4m3 pools: the producer copies codes into a ring of their own, four
 // converter warps widen each tile to f16 in the layout the MMAs read (exact:
@@ -44,10 +51,12 @@ struct PxParams {
   const int32_t* grp_q;      // [groups + 1] first query token
   const int32_t* grp_k;      // [groups + 1] running sum of the prefixes' keys
   const int32_t* grp_pages;  // [groups + 1] first entry in page_indices
-  const int32_t* grp_blk;    // [groups + 1] running sum of row blocks
+  const int32_t* grp_unit;   // [groups + 1] running sum of units
   const int32_t* row_pos;    // [tokens] position of each query token (windows)
   const int32_t* page_indices;
-  int groups, Hq, Hkv, G, QB, num_splits;
+  int groups, Hq, Hkv, G, QB;
+  int splits;                // partials a row block may have
+  int quota_min;             // units per block that keep to it
   int window;
   float sm_scale, scale_log2;
   int page_size, box_rows;
@@ -97,38 +106,61 @@ struct PxCfg {
 };
 
 struct PxItem {
-  int kvh, chunk, tok0, nq, tiles, keys, first, n, list0, pages;
+  int kvh, slot, tok0, nq, tiles, keys, first, n, list0, pages;
+  int next;    // the unit behind the item
+  bool last;   // the item ends its row block's keys
 };
 
-// Item `it` of the list ordered by chunk, KV head, row block (blocks of the
-// same keys run side by side and find them in L2). Whole warp: with a window
-// the keys before the block's earliest visible one are left out, which takes
-// a minimum over its tokens.
-template <int KT, int NT>
-__device__ __forceinline__ PxItem px_item(const PxParams& p, const int32_t* gq, const int32_t* gk,
-                                          const int32_t* gp, const int32_t* gb, int it, int lane) {
-  PxItem t;
-  const int blocks = gb[p.groups];
-  const int r = it / blocks;
-  const int blk = it - r * blocks;
-  t.chunk = r / p.Hkv;
-  t.kvh = r - t.chunk * p.Hkv;
-  int lo = 0, hi = p.groups;
-  while (hi - lo > 1) {   // the group with gb[g] <= blk < gb[g + 1]
+// The group with gu[g] <= u < gu[g + 1].
+__device__ __forceinline__ int px_group(const int32_t* gu, int groups, int u) {
+  int lo = 0, hi = groups;
+  while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (gb[mid] <= blk) lo = mid;
+    if (gu[mid] <= u) lo = mid;
     else hi = mid;
   }
-  t.tok0 = gq[lo] + (blk - gb[lo]) * NT * p.QB;
-  t.nq = min(NT * p.QB, gq[lo + 1] - t.tok0);
+  return lo;
+}
+
+// The start of the first row block at or behind unit u (one partial per row:
+// row blocks are not cut).
+template <int KT>
+__device__ __forceinline__ int px_whole(const PxParams& p, const int32_t* gk, const int32_t* gu,
+                                        int u, int all) {
+  if (u >= all) return all;
+  const int g = px_group(gu, p.groups, u);
+  const int T = (gk[g + 1] - gk[g] + KT - 1) / KT;
+  return gu[g] + (u - gu[g] + T - 1) / T * T;
+}
+
+// The item that starts at unit u, of a thread block whose units end at `end`.
+// Row blocks of the same keys are neighbours in the order and find them in
+// L2. Whole warp: with a window the keys before the block's earliest visible
+// one are left out, which takes a minimum over its tokens.
+template <int KT, int NT>
+__device__ __forceinline__ PxItem px_item(const PxParams& p, const int32_t* gq, const int32_t* gk,
+                                          const int32_t* gp, const int32_t* gu, int u, int end,
+                                          int quota, int lane) {
+  PxItem t;
+  const int g = px_group(gu, p.groups, u);
+  t.keys = gk[g + 1] - gk[g];
+  t.list0 = gp[g];
+  t.pages = gp[g + 1] - gp[g];
+  const int T = (t.keys + KT - 1) / KT;
+  const int toks = gq[g + 1] - gq[g];
+  const int blocks = (toks + NT * p.QB - 1) / (NT * p.QB);
+  const int pair = (u - gu[g]) / T;
+  const int start = gu[g] + pair * T;     // the row block's first unit
+  t.kvh = pair / blocks;
+  const int at = (pair - t.kvh * blocks) * NT * p.QB;
+  t.tok0 = gq[g] + at;
+  t.nq = min(NT * p.QB, toks - at);
   t.tiles = (t.nq + p.QB - 1) / p.QB;
-  t.keys = gk[lo + 1] - gk[lo];
-  t.list0 = gp[lo];
-  t.pages = gp[lo + 1] - gp[lo];
-  const int all = (t.keys + KT - 1) / KT;
-  const int per = (all + p.num_splits - 1) / p.num_splits;
-  int t0 = min(t.chunk * per, all);
-  const int t1 = min(t0 + per, all);
+  t.next = min(end, start + T);
+  t.last = t.next == start + T;
+  t.slot = p.splits > 1 ? u / quota - start / quota : 0;
+  int t0 = u - start;
+  const int t1 = t.next - start;
   if (p.window > 0) {
     int pos = INT32_MAX;
     for (int i = lane; i < t.nq; i += 32) pos = min(pos, p.row_pos[t.tok0 + i]);
@@ -143,22 +175,17 @@ __device__ __forceinline__ PxItem px_item(const PxParams& p, const int32_t* gq, 
 // A tile row's accumulator from TMEM to its fp32 partial row, 32 columns at a
 // time: the eight 16-byte pieces of a lane's row are transposed within groups
 // of eight lanes, so that a store instruction writes four whole 128-byte rows.
-// Warp-collective; `zero` (warp-uniform) stores zeros without reading TMEM.
+// Warp-collective.
 template <int D>
-__device__ __forceinline__ void store_partial(uint32_t o_addr, bool zero, float scale, float* row,
-                                              bool valid, int lane) {
+__device__ __forceinline__ void store_partial(uint32_t o_addr, float scale, float* row, bool valid,
+                                              int lane) {
   const int i = lane & 7;
   const unsigned long long mine = valid ? reinterpret_cast<unsigned long long>(row) : 0ull;
 #pragma unroll
   for (int blk = 0; blk < D / 32; ++blk) {
     float o[32];
-    if (!zero) {
-      tc::tmem_ld32(o_addr + blk * 32, o);
-      tc::tmem_wait_ld();
-    } else {
-#pragma unroll
-      for (int e = 0; e < 32; ++e) o[e] = 0.f;
-    }
+    tc::tmem_ld32(o_addr + blk * 32, o);
+    tc::tmem_wait_ld();
     float4 ch[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e)
@@ -205,18 +232,18 @@ __global__ void __launch_bounds__(PxCfg<D, FP8>::LB_THREADS, 1)
   // the groups' tables in shared memory: every role looks every item up
   int32_t* gs = reinterpret_cast<int32_t*>(smem + C::OFF_GRP);
   const bool staged = p.groups <= C::GRP_CAP;
-  const int32_t *gq = p.grp_q, *gk = p.grp_k, *gp = p.grp_pages, *gb = p.grp_blk;
+  const int32_t *gq = p.grp_q, *gk = p.grp_k, *gp = p.grp_pages, *gu = p.grp_unit;
   if (staged) {
     for (int i = threadIdx.x; i <= p.groups; i += blockDim.x) {
       gs[i] = gq[i];
       gs[C::GRP_CAP + 1 + i] = gk[i];
       gs[2 * (C::GRP_CAP + 1) + i] = gp[i];
-      gs[3 * (C::GRP_CAP + 1) + i] = gb[i];
+      gs[3 * (C::GRP_CAP + 1) + i] = gu[i];
     }
     gq = gs;
     gk = gs + C::GRP_CAP + 1;
     gp = gs + 2 * (C::GRP_CAP + 1);
-    gb = gs + 3 * (C::GRP_CAP + 1);
+    gu = gs + 3 * (C::GRP_CAP + 1);
   }
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
@@ -247,9 +274,17 @@ __global__ void __launch_bounds__(PxCfg<D, FP8>::LB_THREADS, 1)
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  const int n_items = gb[p.groups] * p.Hkv * p.num_splits;
-  const int step = static_cast<int>(gridDim.x);
-  auto item = [&](int it) { return px_item<KT, NT>(p, gq, gk, gp, gb, it, lane); };
+  // this block's units [u0, u1)
+  const int all = gu[p.groups];
+  const int quota = max((all + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x),
+                        p.quota_min);
+  int u0 = static_cast<int>(min(static_cast<long long>(blockIdx.x) * quota, static_cast<long long>(all)));
+  int u1 = static_cast<int>(min(static_cast<long long>(u0) + quota, static_cast<long long>(all)));
+  if (p.splits == 1) {
+    u0 = px_whole<KT>(p, gk, gu, u0, all);
+    u1 = px_whole<KT>(p, gk, gu, u1, all);
+  }
+  auto item = [&](int u) { return px_item<KT, NT>(p, gq, gk, gp, gu, u, u1, quota, lane); };
   // A wait that gives up in any lane makes the whole warp leave its loop.
   auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status));
@@ -270,8 +305,9 @@ __global__ void __launch_bounds__(PxCfg<D, FP8>::LB_THREADS, 1)
     const int skip_tile = hook_skip_tile();
     int g = 0, qi = 0;
     bool ok = true;
-    for (int it = blockIdx.x; ok && it < n_items; it += step) {
-      const PxItem t = item(it);
+    for (int u = u0; ok && u < u1;) {
+      const PxItem t = item(u);
+      u = t.next;
       if (leader && t.keys > t.pages * p.page_size) atomicExch(status, SINKATTN_BAD_LENGTHS);
       if (t.n == 0) continue;
       if (qi > 0 && !wwait(q_empty, (qi - 1) & 1)) break;
@@ -367,8 +403,9 @@ __global__ void __launch_bounds__(PxCfg<D, FP8>::LB_THREADS, 1)
 #pragma unroll
     for (int tt = 0; tt < NT; ++tt) steps[tt] = 0;
     bool ok = true;
-    for (int it = blockIdx.x; ok && it < n_items; it += step) {
-      const PxItem t = item(it);
+    for (int u = u0; ok && u < u1;) {
+      const PxItem t = item(u);
+      u = t.next;
       if (t.n == 0) continue;
       // S_t of the first K/V tile for every row tile, then per K/V tile and
       // row tile: PV_t, then the next S_t into the same buffer once that
@@ -420,8 +457,9 @@ __global__ void __launch_bounds__(PxCfg<D, FP8>::LB_THREADS, 1)
     const int ct = static_cast<int>(threadIdx.x) - C::W_CVT * 32;
     int g = 0, qi = 0;
     bool ok = true;
-    for (int it = blockIdx.x; ok && it < n_items; it += step) {
-      const PxItem t = item(it);
+    for (int u = u0; ok && u < u1;) {
+      const PxItem t = item(u);
+      u = t.next;
       if (t.n == 0) continue;
       if (!wwait(q_full, qi & 1)) break;
       for (int c = ct; c < t.tiles * C::Q_TILE / 16; c += N) {
@@ -488,8 +526,9 @@ __global__ void __launch_bounds__(PxCfg<D, FP8>::LB_THREADS, 1)
     constexpr int NCH = KT / 32;     // 32-column pieces of a score row
     int steps = 0;
     bool ok = true;
-    for (int it = blockIdx.x; ok && it < n_items; it += step) {
-      const PxItem t = item(it);
+    for (int u = u0; ok && u < u1;) {
+      const PxItem t = item(u);
+      u = t.next;
       if (tt >= t.tiles) continue;
       const bool valid = rg < p.QB && tl < t.nq;
       const float kscale = FP8 ? p.k_scale[t.kvh] : 1.f;
@@ -594,13 +633,31 @@ __global__ void __launch_bounds__(PxCfg<D, FP8>::LB_THREADS, 1)
       }
       const bool some = l > 0.f;   // the row sees a key of the chunk
       const size_t slot =
-          (static_cast<size_t>(t.tok0 + tl) * p.Hq + t.kvh * G + hig) * p.part_slots + t.chunk;
-      store_partial<D>(o_addr, t.n < 1, FP8 ? p.v_scale[t.kvh] : 1.f, p.part_acc + slot * D, valid,
-                       lane);
+          (static_cast<size_t>(t.tok0 + tl) * p.Hq + t.kvh * G + hig) * p.part_slots + t.slot;
+      if (t.n >= 1)
+        store_partial<D>(o_addr, FP8 ? p.v_scale[t.kvh] : 1.f, p.part_acc + slot * D, valid, lane);
       tc::fence_before_sync();
-      if (valid)
-        *reinterpret_cast<float2*>(p.part_md + slot * 2) =
-            make_float2(some ? m_used * (p.sm_scale * kscale) : kNegInf, some ? l : 0.f);
+      if (valid) {
+        float2* md = reinterpret_cast<float2*>(p.part_md + slot * 2);
+        *md = make_float2(some ? m_used * (p.sm_scale * kscale) : kNegInf, some ? l : 0.f);
+        if (t.last)   // the partials that no block writes
+          for (int s = t.slot + 1; s < p.splits; ++s) md[s - t.slot] = make_float2(kNegInf, 0.f);
+      }
+    }
+    // rows of groups without a prefix: no block has units of theirs. All
+    // blocks share the rows of each group, or with many groups the groups.
+    const int nb = static_cast<int>(gridDim.x);
+    const bool many = p.groups > nb;
+    const int width = (many ? 1 : nb) * NT * 128;
+    const int mine = (many ? 0 : static_cast<int>(blockIdx.x)) * NT * 128 + tt * 128 + row;
+    for (int g = many ? blockIdx.x : 0; g < p.groups; g += many ? nb : 1) {
+      if (gk[g + 1] > gk[g]) continue;
+      const long long n = static_cast<long long>(gq[g + 1] - gq[g]) * p.Hq * p.splits;
+      for (long long i = mine; i < n; i += width) {
+        const long long r = static_cast<long long>(gq[g]) * p.Hq + i / p.splits;
+        *reinterpret_cast<float2*>(p.part_md + (r * p.part_slots + i % p.splits) * 2) =
+            make_float2(kNegInf, 0.f);
+      }
     }
   }
 
@@ -640,7 +697,7 @@ int launch(const AttnArgs& a, const SharedPlan& plan, cudaStream_t stream) {
   p.grp_q = plan.grp_q;
   p.grp_k = plan.grp_k;
   p.grp_pages = plan.grp_pages;
-  p.grp_blk = plan.grp_blk;
+  p.grp_unit = plan.grp_unit;
   p.row_pos = plan.row_pos;
   p.page_indices = a.page_indices;
   p.groups = a.batch;
@@ -648,7 +705,7 @@ int launch(const AttnArgs& a, const SharedPlan& plan, cudaStream_t stream) {
   p.Hkv = a.Hkv;
   p.G = G;
   p.QB = QB;
-  p.num_splits = a.num_splits;
+  p.splits = a.num_splits;
   p.window = a.window;
   p.sm_scale = a.sm_scale;
   p.scale_log2 = a.sm_scale * kLog2e;
@@ -659,17 +716,21 @@ int launch(const AttnArgs& a, const SharedPlan& plan, cudaStream_t stream) {
   p.part_acc = a.part_acc;
   p.part_md = a.part_md;
   p.part_slots = part_slots(a);
-  // blocks of rows: at most one per group more than its full ones
-  const int64_t blocks = a.batch + a.total_q / (C::NT * QB);
-  const int64_t items = blocks * a.Hkv * a.num_splits;
-  if (items >= (int64_t{1} << 31)) {
+  // row blocks: at most one per group more than its full ones; a row block of
+  // T tiles meets at most (T - 1) / quota + 2 runs of units
+  const int64_t tiles = (a.max_kv + C::KT - 1) / C::KT;
+  const int64_t units = (a.batch + a.total_q / (C::NT * QB)) * a.Hkv * tiles;
+  if (units >= (int64_t{1} << 31)) {
     set_error("too many work items");
     return SINKATTN_UNSUPPORTED;
   }
+  p.quota_min = a.num_splits > 1
+                    ? static_cast<int>(std::max<int64_t>(1, (tiles - 1 + a.num_splits - 2) / (a.num_splits - 1)))
+                    : 1;
   auto kern = prefix_tc_kernel<D, FP8>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e == cudaSuccess) {
-    kern<<<static_cast<unsigned>(std::min<int64_t>(items, sm_count())), C::THREADS, C::SMEM, stream>>>(
+    kern<<<static_cast<unsigned>(std::min<int64_t>(units, sm_count())), C::THREADS, C::SMEM, stream>>>(
         tmQ, tmK, tmV, p);
     e = cudaGetLastError();
   }
