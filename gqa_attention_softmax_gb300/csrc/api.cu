@@ -670,6 +670,13 @@ int sinkattn_decode_shared_default_splits(int32_t batch, int32_t q_len, int32_t 
   int rc = sinkattn_decode_default_splits(batch, q_len, num_qo_heads, num_kv_heads, head_dim,
                                           max_suffix_len, num_splits);
   if (rc) return rc;
+  // own keys: only as many chunks as fill two blocks per SM (each further one
+  // costs its partials: 64 sequences of up to 1024 own keys at d 64 take 55,
+  // 56, 60 and 64 us in 1, 2, 3 and 4 chunks, 256 x 3 drafts at d 128 take
+  // 186, 202, 234 and 270 us)
+  const int64_t fill = std::max<int64_t>(1, static_cast<int64_t>(batch) * num_kv_heads);
+  *num_splits = static_cast<int32_t>(
+      std::min<int64_t>(*num_splits, (2 * sm_count() + fill - 1) / fill));
   const int G = num_qo_heads / num_kv_heads;
   const int64_t tokens = static_cast<int64_t>(batch) * q_len;
   if (G >= 1 && G <= 64 && prefix_on_tc(tokens, G, num_groups)) {

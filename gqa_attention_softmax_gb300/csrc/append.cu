@@ -5,8 +5,15 @@
 // K and the same run in V, so a row (head_dim elements of one head of one
 // token) is written in full 16-byte lanes, and consecutive lanes read
 // consecutive heads of the token. With codes a thread reads two 16-byte runs
-// per pool instead of one. Quotients are IEEE divisions (the code is then the
-// one nearest to the fp32 quotient, whatever the scale), which the loads hide.
+// per pool instead of one.
+//
+// The code is the one nearest to the correctly rounded quotient x / s. 32 IEEE
+// divisions a thread would take longer than its bytes, so the quotient comes
+// from r = RN(1 / s) by one residual step, q0 = RN(x r), q = RN(q0 + r (x -
+// q0 s)) with the residual exact in an fma: Markstein's theorem ("Computation
+// of elementary functions on the IBM RISC System/6000", 1990) makes q the
+// correctly rounded quotient where nothing over- or underflows. Scales
+// outside [2^-100, 2^100] take IEEE divisions.
 #include <algorithm>
 
 #include "common.cuh"
@@ -29,21 +36,47 @@ struct AppendParams {
   long long n_slots;
 };
 
-// Sixteen bf16 (two 16-byte vectors) -> sixteen e4m3 codes of x / scale.
-__device__ __forceinline__ uint32_t codes4(uint32_t lo, uint32_t hi, float scale) {
-  const float a = __fdiv_rn(__uint_as_float(lo << 16), scale);
-  const float b = __fdiv_rn(__uint_as_float(lo & 0xffff0000u), scale);
-  const float c = __fdiv_rn(__uint_as_float(hi << 16), scale);
-  const float d = __fdiv_rn(__uint_as_float(hi & 0xffff0000u), scale);
-  uint16_t x, y;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(x) : "f"(b), "f"(a));
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(y) : "f"(d), "f"(c));
-  return static_cast<uint32_t>(x) | (static_cast<uint32_t>(y) << 16);
+struct Scale {
+  float s, r;   // the scale and RN(1 / s)
+  bool plain;   // s is in the range of the residual step
+};
+
+__device__ __forceinline__ Scale make_scale(float s) {
+  const float a = fabsf(s);
+  return {s, __frcp_rn(s), a >= 0x1p-100f && a <= 0x1p100f};
 }
 
+template <bool PLAIN>
+__device__ __forceinline__ float quotient(float x, const Scale& c) {
+  if constexpr (!PLAIN) return __fdiv_rn(x, c.s);
+  const float q0 = x * c.r;
+  const float q = fmaf(fmaf(-q0, c.s, x), c.r, q0);
+  // (an infinity, or a value that saturates, stays as it is; so does NaN)
+  return fabsf(q0) < 1024.f ? q : q0;
+}
+
+template <bool PLAIN>
+__device__ __forceinline__ uint32_t codes4(uint32_t lo, uint32_t hi, const Scale& c) {
+  const float x0 = quotient<PLAIN>(__uint_as_float(lo << 16), c);
+  const float x1 = quotient<PLAIN>(__uint_as_float(lo & 0xffff0000u), c);
+  const float x2 = quotient<PLAIN>(__uint_as_float(hi << 16), c);
+  const float x3 = quotient<PLAIN>(__uint_as_float(hi & 0xffff0000u), c);
+  uint16_t a, b;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(a) : "f"(x1), "f"(x0));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b) : "f"(x3), "f"(x2));
+  return static_cast<uint32_t>(a) | (static_cast<uint32_t>(b) << 16);
+}
+
+template <bool PLAIN>
+__device__ __forceinline__ uint4 codes16_t(uint4 a, uint4 b, const Scale& c) {
+  return make_uint4(codes4<PLAIN>(a.x, a.y, c), codes4<PLAIN>(a.z, a.w, c),
+                    codes4<PLAIN>(b.x, b.y, c), codes4<PLAIN>(b.z, b.w, c));
+}
+
+// Sixteen bf16 (two 16-byte vectors) -> sixteen e4m3 codes of x / scale.
 __device__ __forceinline__ uint4 codes16(uint4 a, uint4 b, float scale) {
-  return make_uint4(codes4(a.x, a.y, scale), codes4(a.z, a.w, scale), codes4(b.x, b.y, scale),
-                    codes4(b.z, b.w, scale));
+  const Scale c = make_scale(scale);
+  return c.plain ? codes16_t<true>(a, b, c) : codes16_t<false>(a, b, c);
 }
 
 template <int D, bool FP8>

@@ -7,9 +7,9 @@
 // by cluster barriers of a fraction of a microsecond, where separate launches
 // would cost two microseconds each, and nothing has to be read back by the
 // host, so every call can be captured into a graph. A call with up to
-// kOneBlock entries runs as a cluster of one block, larger ones as kCluster
-// blocks. Phase 1 only checks and writes scratch; a call that cannot be
-// served as a whole ends there, with the table unchanged.
+// kOneBlock entries runs as one block, larger ones as a cluster of kCluster.
+// Before the first barrier a call only checks and writes scratch; one that
+// cannot be served as a whole ends there, with the table unchanged.
 //
 // No result depends on the order in which atomics arrive: they only count,
 // or elect a page's first writer or first appearance by its position (a
@@ -17,8 +17,7 @@
 //
 // Page copies follow as a second launch over the whole GPU that reads the
 // pairs the first one found (a programmatic dependent, so its start-up
-// overlaps the first launch's end). They move 16 bytes per lane, and each
-// lane has four loads in flight.
+// overlaps the first launch's end).
 #include <algorithm>
 
 #include "common.cuh"
@@ -31,12 +30,14 @@ __device__ int g_status_pages;
 namespace {
 
 constexpr int kThreads = 1024;
-constexpr int kCluster = 8;          // blocks of a large call (the portable limit)
+constexpr int kCluster = 16;         // blocks of a large call (the hardware's limit)
 constexpr int kOneBlock = 4096;      // entries that one block takes alone
 constexpr int kHeader = 16;
+constexpr int kRun = 8;              // list entries of a thread, whose loads are in flight together
+constexpr int kKept = 1024;          // sequences of a call whose ranges stay in shared memory
 
 // Header words besides the free count (scratch of one call).
-enum { H_FREE = 0, H_OK = 1, H_COUNT = 2, H_PAIRS = 3, H_MOST = 4, H_RANK = 8 };
+enum { H_FREE = 0, H_OK = 1, H_COUNT = 2, H_PAIRS = 3 };
 
 struct PageTab {
   int32_t* base;
@@ -46,12 +47,11 @@ struct PageTab {
   __device__ __forceinline__ int32_t* list() const { return lens() + S; }
   __device__ __forceinline__ int32_t* rc() const { return list() + static_cast<size_t>(S) * M; }
   __device__ __forceinline__ int32_t* free_list() const { return rc() + N; }
-  __device__ __forceinline__ int32_t* mark() const { return free_list() + N; }
-  __device__ __forceinline__ int32_t* aux(int k) const {   // k < 6: one word per sequence
-    return mark() + static_cast<size_t>(S) * (1 + k);
+  __device__ __forceinline__ int32_t* aux(int k) const {   // k < 7: one word per sequence
+    return free_list() + N + static_cast<size_t>(S) * k;
   }
   __device__ __forceinline__ int32_t* work(int k) const {  // k < 2: one word per page
-    return mark() + static_cast<size_t>(S) * 7 + static_cast<size_t>(N) * k;
+    return aux(7) + static_cast<size_t>(N) * k;
   }
   __device__ __forceinline__ int pages(int tokens) const { return (tokens + P - 1) >> shift; }
   __device__ __forceinline__ bool seq_ok(int id) const {
@@ -96,6 +96,38 @@ __device__ __forceinline__ int block_scan(int v, int* total, int* sums) {
   *total = __shfl_sync(0xffffffffu, w, 31);
   const int upto = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
   return (warp > 0 ? upto : 0) + x - v;
+}
+
+// Which sequences a call names: one bit each in dynamic shared memory.
+extern __shared__ uint32_t seen_s[];
+
+__device__ __forceinline__ void seen_clear(const PageTab& t) {
+  for (int i = threadIdx.x; i < (t.S + 31) / 32; i += kThreads) seen_s[i] = 0u;
+}
+// Marks `id` (in range); true if it was marked before.
+__device__ __forceinline__ bool seen_twice(int id) {
+  const uint32_t bit = 1u << (id & 31);
+  return atomicOr(&seen_s[id >> 5], bit) & bit;
+}
+__device__ __forceinline__ bool seen(int id) { return seen_s[id >> 5] >> (id & 31) & 1u; }
+
+// Sum of *word (one per block of the cluster, written before the last cluster
+// barrier) over all blocks and over those before this one. The words must
+// stay until a later cluster barrier.
+__device__ __forceinline__ int cluster_sum(const int* word, int rank, int nr, int* before) {
+  int all = 0, low = 0;
+  if (nr == 1) {
+    *before = 0;
+    __syncthreads();
+    return *word;
+  }
+  for (int r = 0; r < nr; ++r) {
+    const int x = __float_as_int(ld_dsmem(reinterpret_cast<const float*>(word), r));
+    low += r < rank ? x : 0;
+    all += x;
+  }
+  *before = low;
+  return all;
 }
 
 // ---------------------------------------------------------------------------
@@ -158,31 +190,34 @@ __global__ void __launch_bounds__(kThreads)
     // the first item of each thread stays in registers
     ReserveItem mine{};
     if (tid < n) mine = reserve_item(t, ids, cu, tid);
-    for (int i = tid; i < n; i += kThreads) {
-      const ReserveItem r = i == tid ? mine : reserve_item(t, ids, cu, i);
-      if (t.seq_ok(r.id)) t.mark()[r.id] = 0;
-      if (r.tail >= 0) t.work(0)[r.tail] = t.work(1)[r.tail] = 0;
-    }
+    seen_clear(t);
     __syncthreads();
+    bool bad = false, shared = false;
     for (int i = tid; i < n; i += kThreads) {
       const ReserveItem r = i == tid ? mine : reserve_item(t, ids, cu, i);
-      if (t.seq_ok(r.id)) atomicAdd(&t.mark()[r.id], 1);
+      if (!r.ok || seen_twice(r.id)) bad = true;
       if (r.tail >= 0) {
-        atomicAdd(&t.work(0)[r.tail], 1);       // writers of the page in this call
-        atomicMax(&t.work(1)[r.tail], n - i);   // the first of them
+        shared = true;
+        t.work(0)[r.tail] = t.work(1)[r.tail] = 0;
       }
     }
-    __syncthreads();
-    bool bad = false;
+    if (__syncthreads_or(shared)) {
+      for (int i = tid; i < n; i += kThreads) {
+        const ReserveItem r = i == tid ? mine : reserve_item(t, ids, cu, i);
+        if (r.tail >= 0) {
+          atomicAdd(&t.work(0)[r.tail], 1);       // writers of the page in this call
+          atomicMax(&t.work(1)[r.tail], n - i);   // the first of them
+        }
+      }
+      __syncthreads();
+    }
     long long need = 0;
     for (int base = 0; base < n; base += kThreads) {
       const int i = base + tid;
       int want = 0, copies = 0;
       if (i < n) {
         const ReserveItem r = base == 0 ? mine : reserve_item(t, ids, cu, i);
-        if (!r.ok || __ldcg(&t.mark()[r.id]) != 1) {
-          bad = true;
-        } else {
+        if (r.ok) {
           copies = r.tail >= 0 && !(__ldcg(&t.work(0)[r.tail]) == r.rc &&
                                     __ldcg(&t.work(1)[r.tail]) == n - i);
           want = t.pages(r.len + r.grow) - t.pages(r.len) + copies;
@@ -262,165 +297,235 @@ __global__ void __launch_bounds__(kThreads)
 // ---------------------------------------------------------------------------
 // fork
 // ---------------------------------------------------------------------------
+// Every block checks the whole request, so none has to wait for another.
 __global__ void __launch_bounds__(kThreads)
     pages_fork_kernel(const PageTab t, const int32_t* __restrict__ src,
                       const int32_t* __restrict__ dst, int n) {
   __shared__ int most_s;
   const int tid = threadIdx.x;
-  int32_t* hdr = t.hdr();
-  if (cluster_rank() == 0) {
-    if (tid == 0) most_s = 0;
-    for (int i = tid; i < n; i += kThreads) {
-      if (t.seq_ok(src[i])) t.mark()[src[i]] = 0;
-      if (t.seq_ok(dst[i])) t.mark()[dst[i]] = 0;
-    }
-    __syncthreads();
-    for (int i = tid; i < n; i += kThreads)
-      if (t.seq_ok(dst[i])) atomicAdd(&t.mark()[dst[i]], 1);
-    __syncthreads();
-    bool bad = false;
-    for (int i = tid; i < n; i += kThreads) {
-      const int a = src[i], b = dst[i];
-      if (!t.seq_ok(a) || !t.seq_ok(b) || __ldcg(&t.mark()[b]) != 1 || __ldcg(&t.mark()[a]) != 0 ||
-          t.lens()[b] != 0) {
-        bad = true;
-        continue;
-      }
-      const int len = t.lens()[a];
-      if (len < 0 || t.pages(len) > t.M) bad = true;
-      else atomicMax(&most_s, t.pages(len));
-      t.aux(0)[i] = len;
-    }
-    bad = __syncthreads_or(bad);
-    if (tid == 0) {
-      if (bad) atomicExch(&g_status_pages, SINKATTN_BAD_PAGES);
-      hdr[H_OK] = !bad;
-      hdr[H_MOST] = most_s;
-    }
+  if (tid == 0) most_s = 0;
+  seen_clear(t);
+  __syncthreads();
+  bool bad = false;
+  for (int i = tid; i < n; i += kThreads) {
+    const int b = dst[i];
+    if (!t.seq_ok(b) || seen_twice(b) || t.lens()[b] != 0) bad = true;
   }
-  cluster_sync_all();
-  if (!__ldcg(&hdr[H_OK])) return;
-  const int most = __ldcg(&hdr[H_MOST]);
+  __syncthreads();
+  for (int i = tid; i < n; i += kThreads) {
+    const int a = src[i];
+    if (!t.seq_ok(a) || seen(a)) {
+      bad = true;
+      continue;
+    }
+    const int len = t.lens()[a];
+    if (len < 0 || t.pages(len) > t.M) bad = true;
+    else atomicMax(&most_s, t.pages(len));
+  }
+  if (__syncthreads_or(bad)) {
+    if (cluster_rank() == 0 && tid == 0) atomicExch(&g_status_pages, SINKATTN_BAD_PAGES);
+    return;   // every block of the cluster
+  }
+  cluster_sync_all();   // every block has seen the dst sequences empty
+  const int most = most_s;
   const int nt = cluster_size() * kThreads;
   const int t0 = cluster_rank() * kThreads + tid;
-  for (int i = t0; i < n; i += nt) t.lens()[dst[i]] = __ldcg(&t.aux(0)[i]);
+  for (int i = t0; i < n; i += nt) t.lens()[dst[i]] = t.lens()[src[i]];   // (no src is a dst)
   // (item, entry) pairs over the rectangle n x (longest list)
   const int cells = n * most;   // < max_seqs * max_pages
-  for (int c = t0; c < cells; c += nt) {
-    const int i = c / most, e = c - i * most;
-    if (e >= t.pages(__ldcg(&t.aux(0)[i]))) continue;
-    const int p = t.list()[static_cast<size_t>(src[i]) * t.M + e];
-    t.list()[static_cast<size_t>(dst[i]) * t.M + e] = p;
-    if (t.page_ok(p)) atomicAdd(&t.rc()[p], 1);
+  for (int c0 = t0; c0 < cells; c0 += kRun * nt) {
+    int p[kRun];
+    int32_t* to[kRun];
+#pragma unroll
+    for (int k = 0; k < kRun; ++k) {
+      const int c = c0 + k * nt;
+      to[k] = nullptr;
+      if (c >= cells) continue;
+      const int i = c / most, e = c - i * most;
+      if (e >= t.pages(t.lens()[src[i]])) continue;
+      p[k] = t.list()[static_cast<size_t>(src[i]) * t.M + e];
+      to[k] = &t.list()[static_cast<size_t>(dst[i]) * t.M + e];
+    }
+#pragma unroll
+    for (int k = 0; k < kRun; ++k) {
+      if (!to[k]) continue;
+      *to[k] = p[k];
+      if (t.page_ok(p[k])) atomicAdd(&t.rc()[p[k]], 1);
+    }
   }
 }
 
 // ---------------------------------------------------------------------------
 // truncate
 // ---------------------------------------------------------------------------
-// aux(0): entries the item keeps, aux(1): entries it drops. A dropped page is
-// given back by its first appearance in the request (its position is elected
-// in work(0)) if its count has come to zero.
+// A dropped page is given back by its first appearance in the request (its
+// position is elected in work(0)) if its count has come to zero. Every block
+// checks the whole request and keeps what each item keeps and drops, in
+// shared memory for calls of up to kKept sequences, else in aux(0) and aux(1),
+// where all blocks write the same words. A thread takes runs of kRun
+// consecutive cells (item, entry) of the rectangle n x (longest drop), a
+// block a run of those, so that positions follow the request's order with one
+// scan per kRun * kThreads cells.
 __global__ void __launch_bounds__(kThreads)
     pages_truncate_kernel(const PageTab t, const int32_t* __restrict__ ids,
                           const int32_t* __restrict__ new_lens, int n) {
   __shared__ int sums[32];
-  __shared__ int most_s;
+  __shared__ int most_s, found_s;
+  __shared__ int keep_s[kKept], drop_s[kKept];
   const int tid = threadIdx.x, rank = cluster_rank(), nr = cluster_size();
   int32_t* hdr = t.hdr();
-  if (rank == 0) {
-    if (tid == 0) most_s = 0;
-    for (int i = tid; i < n; i += kThreads)
-      if (t.seq_ok(ids[i])) t.mark()[ids[i]] = 0;
-    __syncthreads();
-    for (int i = tid; i < n; i += kThreads)
-      if (t.seq_ok(ids[i])) atomicAdd(&t.mark()[ids[i]], 1);
-    __syncthreads();
-    bool bad = false;
-    for (int i = tid; i < n; i += kThreads) {
-      const int id = ids[i], to = new_lens ? new_lens[i] : 0;
-      if (!t.seq_ok(id) || __ldcg(&t.mark()[id]) != 1) {
-        bad = true;
-        continue;
-      }
-      const int len = t.lens()[id];
-      if (to < 0 || to > len || t.pages(len) > t.M) {
-        bad = true;
-        continue;
-      }
-      const int keep = t.pages(to), drop = t.pages(len) - keep;
-      t.aux(0)[i] = keep;
-      t.aux(1)[i] = drop;
-      if (drop > 0) atomicMax(&most_s, drop);
+  int* keep = n <= kKept ? keep_s : t.aux(0);
+  int* drop = n <= kKept ? drop_s : t.aux(1);
+  if (tid == 0) most_s = 0;
+  seen_clear(t);
+  const int count = __ldcg(&hdr[H_FREE]);
+  __syncthreads();
+  bool bad = false;
+  for (int i = tid; i < n; i += kThreads) {
+    const int id = ids[i], to = new_lens ? new_lens[i] : 0;
+    if (!t.seq_ok(id) || seen_twice(id)) {
+      bad = true;
+      continue;
     }
-    bad = __syncthreads_or(bad);
-    if (tid == 0) {
-      if (bad) atomicExch(&g_status_pages, SINKATTN_BAD_PAGES);
-      hdr[H_OK] = !bad;
-      hdr[H_COUNT] = hdr[H_FREE];
-      hdr[H_MOST] = most_s;
+    const int len = __ldcg(&t.lens()[id]);
+    if (to < 0 || to > len || t.pages(len) > t.M) {
+      bad = true;
+      continue;
     }
+    const int k = t.pages(to), d = t.pages(len) - k;
+    keep[i] = k;
+    drop[i] = d;
+    if (d > 0) atomicMax(&most_s, d);
   }
-  cluster_sync_all();
-  if (!__ldcg(&hdr[H_OK])) return;   // uniform over the cluster
-  const int most = __ldcg(&hdr[H_MOST]), count = __ldcg(&hdr[H_COUNT]);
+  if (__syncthreads_or(bad)) {
+    if (rank == 0 && tid == 0) atomicExch(&g_status_pages, SINKATTN_BAD_PAGES);
+    return;   // every block of the cluster
+  }
+  const int most = most_s;
+  // cells in request order: a block's run, and the thread's first cells in registers
+  const int cells = n * most;        // < max_seqs * max_pages
+  constexpr int kStep = kRun * kThreads;
+  const int per = static_cast<int>((static_cast<long long>(cells) + nr - 1) / nr + kStep - 1) / kStep * kStep;
+  const int c0 = static_cast<int>(min(static_cast<long long>(cells), static_cast<long long>(rank) * per));
+  const int c1 = static_cast<int>(min(static_cast<long long>(cells), static_cast<long long>(c0) + per));
+  // addresses (in words from the first list) of the cells [c, c + kRun), -1 where nothing is dropped
+  auto entries = [&](int c, long long (&at)[kRun]) {
+    int i = c / max(most, 1), e = c - i * most;
+#pragma unroll
+    for (int k = 0; k < kRun; ++k) {
+      at[k] = -1;
+      if (c + k < c1 && e < drop[i]) at[k] = static_cast<long long>(ids[i]) * t.M + keep[i] + e;
+      if (++e == most) {
+        e = 0;
+        ++i;
+      }
+    }
+  };
+  auto load = [&](const long long (&at)[kRun], int (&p)[kRun]) {
+#pragma unroll
+    for (int k = 0; k < kRun; ++k) p[k] = at[k] >= 0 ? t.list()[at[k]] : -1;
+#pragma unroll
+    for (int k = 0; k < kRun; ++k) p[k] = t.page_ok(p[k]) ? p[k] : -1;
+  };
+  const int first = c0 + tid * kRun;
+  long long at0[kRun];
+  int page0[kRun];
+  if (first < c1) {
+    entries(first, at0);
+    load(at0, page0);
+  }
+  // runs f(first cell, addresses, pages) over the thread's cells
+  auto each = [&](auto&& f) {
+    for (int c = first; c < c1; c += kStep) {
+      if (c == first) {
+        f(c, at0, page0);
+      } else {
+        long long at[kRun];
+        int p[kRun];
+        entries(c, at);
+        load(at, p);
+        f(c, at, p);
+      }
+    }
+  };
+  each([&](int, const long long (&)[kRun], const int (&p)[kRun]) {
+#pragma unroll
+    for (int k = 0; k < kRun; ++k)
+      if (p[k] >= 0) t.work(0)[p[k]] = 0;
+  });
+  cluster_sync_all();   // every block has read the lengths; work(0) is clear
   for (int i = rank * kThreads + tid; i < n; i += nr * kThreads)
     t.lens()[ids[i]] = new_lens ? new_lens[i] : 0;
-  if (most == 0) return;             // uniform: no page leaves a list
-  // cells (item, entry) in request order; each block takes a run of them
-  const int cells = n * most;        // < max_seqs * max_pages
-  const int per = ((cells + nr - 1) / nr + kThreads - 1) / kThreads * kThreads;
-  const int c0 = min(cells, rank * per), c1 = min(cells, c0 + per);
-  auto entry = [&](int c) -> int32_t* {
-    const int i = c / most, e = c - i * most;
-    if (e >= __ldcg(&t.aux(1)[i])) return nullptr;
-    return &t.list()[static_cast<size_t>(ids[i]) * t.M + __ldcg(&t.aux(0)[i]) + e];
-  };
-  auto page_of = [&](int32_t* at) -> int { return at && t.page_ok(*at) ? *at : -1; };
-  int32_t* mine = c0 + tid < c1 ? entry(c0 + tid) : nullptr;   // the thread's first cell
-  const int page0 = page_of(mine);
-  for (int c = c0 + tid; c < c1; c += kThreads) {
-    const int p = c == c0 + tid ? page0 : page_of(entry(c));
-    if (p >= 0) t.work(0)[p] = 0;
-  }
+  if (most == 0) return;   // uniform over the cluster: no page leaves a list
+  each([&](int c, const long long (&)[kRun], const int (&p)[kRun]) {
+#pragma unroll
+    for (int k = 0; k < kRun; ++k)
+      if (p[k] >= 0) {
+        atomicSub(&t.rc()[p[k]], 1);
+        atomicMax(&t.work(0)[p[k]], INT32_MAX - (c + k));
+      }
+  });
   cluster_sync_all();
-  for (int c = c0 + tid; c < c1; c += kThreads) {
-    const int p = c == c0 + tid ? page0 : page_of(entry(c));
-    if (p >= 0) {
-      atomicSub(&t.rc()[p], 1);
-      atomicMax(&t.work(0)[p], INT32_MAX - c);
+  auto backs = [&](int c, const int (&p)[kRun]) -> uint32_t {   // which cells give their page back
+    int r[kRun], w[kRun];
+#pragma unroll
+    for (int k = 0; k < kRun; ++k) {
+      r[k] = p[k] >= 0 ? __ldcg(&t.rc()[p[k]]) : 1;
+      w[k] = p[k] >= 0 ? __ldcg(&t.work(0)[p[k]]) : 0;
+    }
+    uint32_t m = 0;
+#pragma unroll
+    for (int k = 0; k < kRun; ++k)
+      if (r[k] == 0 && w[k] == INT32_MAX - (c + k)) m |= 1u << k;
+    return m;
+  };
+  uint32_t back0 = 0;
+  int found = 0, total;
+  each([&](int c, const long long (&)[kRun], const int (&p)[kRun]) {
+    const uint32_t m = backs(c, p);
+    if (c == first) back0 = m;
+    found += __popc(m);
+  });
+  block_scan(found, &total, sums);
+  if (tid == 0) found_s = total;
+  cluster_sync_all();
+  int before;
+  const int all = cluster_sum(&found_s, rank, nr, &before);
+  if (rank == 0 && tid == 0) hdr[H_FREE] = count + all;
+  for (int base = c0; base < c1; base += kStep) {
+    const int c = base + tid * kRun;
+    long long at[kRun];
+    int p[kRun];
+    uint32_t m = 0;
+#pragma unroll
+    for (int k = 0; k < kRun; ++k) {
+      at[k] = -1;
+      p[k] = -1;
+    }
+    if (base == c0 && c < c1) {
+#pragma unroll
+      for (int k = 0; k < kRun; ++k) {
+        at[k] = at0[k];
+        p[k] = page0[k];
+      }
+      m = back0;
+    } else if (c < c1) {
+      entries(c, at);
+      load(at, p);
+      m = backs(c, p);
+    }
+    int r = before + block_scan(__popc(m), &total, sums);
+    before += total;
+#pragma unroll
+    for (int k = 0; k < kRun; ++k) {
+      if (at[k] >= 0) t.list()[at[k]] = -1;
+      if (m >> k & 1u) {
+        if (count + all <= t.N) t.free_list()[count + all - 1 - r] = p[k];
+        ++r;
+      }
     }
   }
-  cluster_sync_all();
-  auto gives_back = [&](int p, int c) -> bool {
-    return p >= 0 && __ldcg(&t.rc()[p]) == 0 && __ldcg(&t.work(0)[p]) == INT32_MAX - c;
-  };
-  int found = 0;
-  for (int c = c0 + tid; c < c1; c += kThreads) {
-    const int p = c == c0 + tid ? page0 : page_of(entry(c));
-    found += gives_back(p, c);
-  }
-  int total;
-  block_scan(found, &total, sums);
-  if (tid == 0) hdr[H_RANK + rank] = total;
-  cluster_sync_all();
-  int before = 0, all = 0;
-  for (int r = 0; r < nr; ++r) {
-    const int x = __ldcg(&hdr[H_RANK + r]);
-    before += r < rank ? x : 0;
-    all += x;
-  }
-  if (rank == 0 && tid == 0) hdr[H_FREE] = count + all;
-  for (int base = c0; base < c1; base += kThreads) {
-    const int c = base + tid;
-    int32_t* at = c < c1 ? (base == c0 ? mine : entry(c)) : nullptr;
-    const int p = base == c0 ? page0 : page_of(at);
-    const bool back = c < c1 && gives_back(p, c);
-    const int r = before + block_scan(back, &total, sums);
-    if (back && count + all <= t.N) t.free_list()[count + all - 1 - r] = p;
-    before += total;
-    if (at) *at = -1;
-  }
+  cluster_sync_all();   // the other blocks have read this one's sum
 }
 
 // ---------------------------------------------------------------------------
@@ -432,22 +537,19 @@ __global__ void __launch_bounds__(kThreads)
 __global__ void __launch_bounds__(kThreads)
     pages_compact_kernel(const PageTab t, int32_t* __restrict__ page_map) {
   __shared__ int sums[32];
+  __shared__ int live_s;
   const int tid = threadIdx.x, rank = cluster_rank(), nr = cluster_size();
   int32_t* hdr = t.hdr();
   const int per = ((t.N + nr - 1) / nr + kThreads - 1) / kThreads * kThreads;
   const int p0 = min(t.N, rank * per), p1 = min(t.N, p0 + per);
   int live = 0;
+#pragma unroll 4
   for (int p = p0 + tid; p < p1; p += kThreads) live += t.rc()[p] > 0;
-  int total;
+  int total, before;
   block_scan(live, &total, sums);
-  if (tid == 0) hdr[H_RANK + rank] = total;
+  if (tid == 0) live_s = total;
   cluster_sync_all();
-  int before = 0, kept = 0;
-  for (int r = 0; r < nr; ++r) {
-    const int x = __ldcg(&hdr[H_RANK + r]);
-    before += r < rank ? x : 0;
-    kept += x;
-  }
+  const int kept = cluster_sum(&live_s, rank, nr, &before);
   if (rank == 0 && tid == 0) {
     hdr[H_FREE] = t.N - kept;
     if (kept == t.N) hdr[H_PAIRS] = 0;
@@ -516,29 +618,101 @@ __global__ void __launch_bounds__(256) pages_cow_kernel(const PageTab t, const P
   }
 }
 
-// Compaction: whole pages, 2 KB per warp and step; then the lists follow the
-// map and the free list is written anew.
+// Compaction. Whole pages move through shared memory by bulk copies, one
+// thread per block: a ring of kStages pieces of up to kPiece bytes, so that a
+// block always has several reads and writes in flight and no registers hold
+// data. Then the lists follow the map and the free list is written anew.
+constexpr int kStages = 6, kPiece = 16384;
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
+               "r"(smem_u32(src)), "r"(bytes)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
 __global__ void __launch_bounds__(256)
     pages_move_kernel(const PageTab t, const Pools b, const int32_t* __restrict__ page_map) {
+  extern __shared__ __align__(128) uint8_t ring[];   // [kStages][kPiece]
+  __shared__ uint64_t full[kStages];
+  __shared__ int abort_s;
+  const int tid = threadIdx.x;
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) mbar_init(&full[i], 1);
+    abort_s = 0;
+    fence_barrier_init();
+  }
+  __syncthreads();
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int lane = threadIdx.x & 31;
-  const long long warps = static_cast<long long>(gridDim.x) * (blockDim.x >> 5);
-  const long long w0 = static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  const int pairs = __ldcg(&t.hdr()[H_PAIRS]);
-  const long long page_bytes = static_cast<long long>(b.Hkv) * t.P * b.row_bytes;
-  const int per_page = static_cast<int>((page_bytes + 2047) / 2048);
-  const long long per = 2LL * b.layers * per_page;
-  for (long long w = w0; w < pairs * per; w += warps) {
-    const int k = static_cast<int>(w / per);
-    const long long r = w - k * per;
-    const int x = static_cast<int>(r / per_page), c = static_cast<int>(r - static_cast<long long>(x) * per_page);
-    uint8_t* pool = (x & 1 ? b.v : b.k) + (x >> 1) * b.layer_stride + c * 2048LL;
-    warp_copy(pool + __ldcg(&t.work(0)[k]) * page_bytes,
-              pool + __ldcg(&t.work(1)[pairs - 1 - k]) * page_bytes,
-              static_cast<int>(min(2048LL, page_bytes - c * 2048LL)), lane);
+  if (tid == 0) {
+    const int pairs = __ldcg(&t.hdr()[H_PAIRS]);
+    const long long page_bytes = static_cast<long long>(b.Hkv) * t.P * b.row_bytes;
+    const int per_page = static_cast<int>((page_bytes + kPiece - 1) / kPiece);
+    // pieces in the order pair, layer, K or V, part of the page; this block
+    // takes every gridDim.x-th
+    const int per = 2 * b.layers * per_page;
+    const long long pieces = static_cast<long long>(pairs) * per;
+    struct Piece {
+      uint8_t *src, *dst;
+      uint32_t bytes;
+    };
+    auto piece = [&](long long w) -> Piece {
+      const int k = static_cast<int>(w / per), r = static_cast<int>(w - static_cast<long long>(k) * per);
+      const int x = r / per_page, c = r - x * per_page;
+      uint8_t* pool = (x & 1 ? b.v : b.k) + (x >> 1) * b.layer_stride + static_cast<long long>(c) * kPiece;
+      return {pool + __ldcg(&t.work(1)[pairs - 1 - k]) * page_bytes,
+              pool + __ldcg(&t.work(0)[k]) * page_bytes,
+              static_cast<uint32_t>(min(static_cast<long long>(kPiece),
+                                        page_bytes - static_cast<long long>(c) * kPiece))};
+    };
+    uint8_t* to[kStages];
+    uint32_t size[kStages];
+    long long w = blockIdx.x;
+    int issued = 0, done = 0;
+    bool ok = true;
+    auto issue = [&](int st) {
+      const Piece q = piece(w);
+      to[st] = q.dst;
+      size[st] = q.bytes;
+      mbar_arrive_expect_tx(&full[st], q.bytes);
+      bulk_load(ring + st * kPiece, q.src, q.bytes, &full[st]);
+      ++issued;
+      w += gridDim.x;
+    };
+    // loads run kStages - 1 ahead of the stores; a stage is loaded again once
+    // all but the newest store have read theirs
+    for (; ok && (done < issued || w < pieces);) {
+#pragma unroll
+      for (int st = 0; st < kStages; ++st) {
+        if (done == 0 && st == 0)
+          for (int i = 0; i < kStages - 1 && w < pieces; ++i) issue(i);
+        if (!ok || done >= issued) break;
+        if (!mbar_wait(&full[st], (done / kStages) & 1, &abort_s, &g_status_pages)) {
+          ok = false;
+          break;
+        }
+        bulk_store(to[st], ring + st * kPiece, size[st]);
+        ++done;
+        if (w < pieces) {
+          asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+          issue((st + kStages - 1) % kStages);
+        }
+      }
+    }
+    if (!ok)   // a wait gave up: the loads in flight land before the block's shared memory goes
+      for (int i = done; i < issued; ++i) mbar_drain(&full[i % kStages], (i / kStages) & 1);
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
   const long long step = static_cast<long long>(gridDim.x) * blockDim.x;
-  const long long t0 = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
+  const long long t0 = static_cast<long long>(blockIdx.x) * blockDim.x + tid;
   const long long cells = static_cast<long long>(t.S) * t.M;
   for (long long i = t0; i < cells; i += step) {
     const int p = t.list()[i];
@@ -611,31 +785,40 @@ int launched(cudaError_t e, const char* what) {
 }
 
 template <typename... Params, typename... Args>
-int launch_table(const char* what, long long entries, cudaStream_t stream,
+int launch_table(const char* what, long long entries, const PageTab& t, cudaStream_t stream,
                  void (*kern)(Params...), Args... args) {
   const unsigned blocks = entries <= kOneBlock ? 1 : kCluster;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(blocks);
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>((t.S + 31) / 32) * 4;   // one bit per sequence
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = blocks;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  if (blocks > 1) {
+    if (blocks > 8) {
+      const int rc = launched(cudaFuncSetAttribute(
+          kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1), what);
+      if (rc) return rc;
+    }
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = blocks;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+  }
   return launched(cudaLaunchKernelEx(&cfg, kern, args...), what);
 }
 
 // A launch that may start while the one before it ends (it waits for that
 // one's results itself).
 template <typename... Params, typename... Args>
-int launch_after(const char* what, unsigned blocks, cudaStream_t stream, void (*kern)(Params...),
-                 Args... args) {
+int launch_after(const char* what, unsigned blocks, size_t smem, cudaStream_t stream,
+                 void (*kern)(Params...), Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(blocks);
   cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -655,8 +838,9 @@ bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(
 int check_sizes(int32_t num_pages, int32_t max_seqs, int32_t max_pages) {
   if (num_pages < 1 || max_seqs < 1 || max_pages < 1)
     return refuse(SINKATTN_INVALID_ARG, "num_pages, max_seqs and max_pages must be positive");
-  if (static_cast<int64_t>(max_seqs) * max_pages >= (int64_t{1} << 31))
-    return refuse(SINKATTN_UNSUPPORTED, "max_seqs * max_pages reaches 2^31");
+  if (static_cast<int64_t>(max_seqs) * max_pages >= (int64_t{1} << 30))
+    return refuse(SINKATTN_UNSUPPORTED, "max_seqs * max_pages reaches 2^30");
+  if (max_seqs > (1 << 18)) return refuse(SINKATTN_UNSUPPORTED, "max_seqs exceeds 2^18");
   return SINKATTN_OK;
 }
 
@@ -776,12 +960,12 @@ int sinkattn_pages_reserve(int32_t* table, int32_t num_pages, int32_t page_size,
   if (!cu_new || !slots || !aligned(cu_new, 4) || !aligned(slots, 4))
     return refuse(SINKATTN_INVALID_ARG, "cu_new and slots must be non-null and 4-byte aligned");
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  rc = launch_table("page reserve launch", std::max(n, total_new), s, pages_reserve_kernel, t,
+  rc = launch_table("page reserve launch", std::max(n, total_new), t, s, pages_reserve_kernel, t,
                     seq_ids, cu_new, n, total_new, slots);
   if (rc) return rc;
   const int64_t warps = static_cast<int64_t>(n) * 2 * num_layers * num_kv_heads;
   const unsigned blocks = static_cast<unsigned>(std::min<int64_t>((warps + 7) / 8, copy_blocks()));
-  return launch_after("page copy launch", blocks, s, pages_cow_kernel, t, b);
+  return launch_after("page copy launch", blocks, 0, s, pages_cow_kernel, t, b);
 }
 
 int sinkattn_pages_fork(int32_t* table, int32_t num_pages, int32_t page_size, int32_t max_seqs,
@@ -793,7 +977,7 @@ int sinkattn_pages_fork(int32_t* table, int32_t num_pages, int32_t page_size, in
   if (!rc) rc = check_ids(t, dst_ids, n);
   if (rc) return rc;
   if (n == 0) return SINKATTN_OK;
-  return launch_table("page fork launch", static_cast<long long>(n) * max_pages,
+  return launch_table("page fork launch", static_cast<long long>(n) * max_pages, t,
                       static_cast<cudaStream_t>(stream), pages_fork_kernel, t, src_ids, dst_ids, n);
 }
 
@@ -806,7 +990,7 @@ int sinkattn_pages_truncate(int32_t* table, int32_t num_pages, int32_t page_size
   if (rc) return rc;
   if (!aligned(new_lens, 4)) return refuse(SINKATTN_INVALID_ARG, "new_lens must be 4-byte aligned");
   if (n == 0) return SINKATTN_OK;
-  return launch_table("page truncate launch", static_cast<long long>(n) * max_pages,
+  return launch_table("page truncate launch", static_cast<long long>(n) * max_pages, t,
                       static_cast<cudaStream_t>(stream), pages_truncate_kernel, t, seq_ids,
                       new_lens, n);
 }
@@ -824,10 +1008,14 @@ int sinkattn_pages_compact(int32_t* table, int32_t num_pages, int32_t page_size,
   if (!page_map || !aligned(page_map, 4))
     return refuse(SINKATTN_INVALID_ARG, "page_map must be non-null and 4-byte aligned");
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  rc = launch_table("page compact launch", num_pages, s, pages_compact_kernel, t, page_map);
+  rc = launch_table("page compact launch", num_pages, t, s, pages_compact_kernel, t, page_map);
   if (rc) return rc;
-  return launch_after("page move launch", copy_blocks(), s, pages_move_kernel, t, b,
-                      static_cast<const int32_t*>(page_map));
+  constexpr int smem = kStages * kPiece;   // two blocks per SM
+  rc = launched(cudaFuncSetAttribute(pages_move_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     smem), "page move launch");
+  if (rc) return rc;
+  return launch_after("page move launch", static_cast<unsigned>(sm_count()) * 2u, smem, s,
+                      pages_move_kernel, t, b, static_cast<const int32_t*>(page_map));
 }
 
 int sinkattn_pages_lists(const int32_t* table, int32_t num_pages, int32_t page_size,

@@ -458,8 +458,8 @@ SINKATTN_API int sinkattn_append_paged_fp8(const void* k, const void* v, int64_t
  * SINKATTN_OUT_OF_PAGES, SINKATTN_BAD_PAGES (an id outside [0, max_seqs), an
  * id twice, a length the table cannot hold) or SINKATTN_BAD_LENGTHS (cu_new
  * contradicts total_new); see sinkattn_debug_status. Calls on one table must
- * be ordered (one stream, or events); max_seqs * max_pages < 2^31, page_size
- * as for the paged attention.
+ * be ordered (one stream, or events); max_seqs <= 2^18, max_seqs * max_pages
+ * < 2^30, page_size as for the paged attention.
  * Where a call copies pages it takes the pools of all layers:
  *   k_pages, v_pages [num_layers][num_pages][Hkv][page_size] rows of
  *   row_bytes bytes (d * 2, or d for codes; a multiple of 16), one layer
