@@ -337,7 +337,7 @@ int launch_partials(const AttnArgs& a, cudaStream_t stream) {
                   "the tcgen05 FP8 decode needs head_dim 128 and at most 64 heads per group");
     if (kind == SINKATTN_DECODE_TCGEN05 || (kind == SINKATTN_DECODE_AUTO && tc8))
       return launch_decode_tc(a, stream);
-    return launch_attn_mma(a, stream);
+    return a.part_slots > 0 ? launch_attn_mma_shared(a, stream) : launch_attn_mma(a, stream);
   }
   const bool tc_ok = decode_tc_supported(a);
   if (kind == SINKATTN_DECODE_TCGEN05 && !tc_ok)
@@ -345,7 +345,7 @@ int launch_partials(const AttnArgs& a, cudaStream_t stream) {
                 "the tcgen05 decode kernel needs head_dim 128");
   if (kind == SINKATTN_DECODE_TCGEN05 || (kind == SINKATTN_DECODE_AUTO && tc_ok))
     return launch_decode_tc(a, stream);
-  return launch_attn_mma(a, stream);
+  return a.part_slots > 0 ? launch_attn_mma_shared(a, stream) : launch_attn_mma(a, stream);
 }
 
 int decode_split_impl(const void* q, const void* k, const void* v, const int32_t* kv_indptr,
@@ -547,13 +547,16 @@ int decode_shared_impl(const void* q, const void* k_pages, const void* v_pages, 
     pa.free_rows = 1;
     pa.row_pos = window > 0 ? plan.row_pos : nullptr;
     const bool tc = prefix_on_tc(rows, num_qo_heads / num_kv_heads, num_groups);
-    if ((rc = tc ? launch_prefix_tc(pa, plan, s) : launch_attn_mma(pa, s))) return rc;
+    pa.chain = kChainWaitFirst;
+    if ((rc = tc ? launch_prefix_tc(pa, plan, s) : launch_attn_mma_shared(pa, s))) return rc;
   }
   PagedKv own = pg;
   own.page_indptr = plan.pages;
   set_paged(&a, &own);
   a.cu_k = plan.kv;
   a.part_first = prefix_splits;
+  // behind a prefix pass, the plan is complete (that pass waited for it)
+  a.chain = prefix_splits > 0 ? kChainWaitLast : kChainWaitFirst;
   if ((rc = launch_partials(a, s))) return rc;
   return launch_merge_sparse(part_acc, part_md, sinks, static_cast<int32_t>(rows), num_qo_heads,
                              head_dim, slots, out, lse, s);

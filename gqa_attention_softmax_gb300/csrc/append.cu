@@ -33,6 +33,7 @@ struct AppendParams {
   uint8_t* k_pages;
   uint8_t* v_pages;
   int tokens, Hkv, shift;         // page size = 1 << shift
+  int per_block;                  // tokens of a thread block
   long long n_slots;
 };
 
@@ -79,32 +80,50 @@ __device__ __forceinline__ uint4 codes16(uint4 a, uint4 b, float scale) {
   return c.plain ? codes16_t<true>(a, b, c) : codes16_t<false>(a, b, c);
 }
 
+// A block takes p.per_block tokens; a thread takes its runs kIlp at a time,
+// with all loads of a step in flight before the first store.
 template <int D, bool FP8>
 __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
   constexpr int EL = FP8 ? 16 : 8;         // elements of a thread's 16-byte run in a pool
   constexpr int RUNS = D / EL;
   constexpr int ROW = D * (FP8 ? 1 : 2);   // bytes of a pool row
+  constexpr int kIlp = 2;
   const int per = p.Hkv * RUNS;
-  const long long n = static_cast<long long>(p.tokens) * per;
-  const long long step = static_cast<long long>(gridDim.x) * blockDim.x;
-  for (long long u = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; u < n;
-       u += step) {
-    const int tok = static_cast<int>(u / per), r = static_cast<int>(u - static_cast<long long>(tok) * per);
-    const int h = r / RUNS, c = r % RUNS;
-    const int slot = p.slots[tok];
-    const uint4* ks = reinterpret_cast<const uint4*>(p.k + tok * p.k_stride + r * EL);
-    const uint4* vs = reinterpret_cast<const uint4*>(p.v + tok * p.v_stride + r * EL);
-    uint4 k = __ldcs(ks), v = __ldcs(vs);
-    if constexpr (FP8) {
-      const uint4 k2 = __ldcs(ks + 1), v2 = __ldcs(vs + 1);
-      k = codes16(k, k2, p.k_scale[h]);
-      v = codes16(v, v2, p.v_scale[h]);
+  const int tok0 = blockIdx.x * p.per_block;
+  const int n = min(p.per_block, p.tokens - tok0) * per;
+  for (int u0 = threadIdx.x; u0 < n; u0 += kIlp * 256) {
+    uint4 k[kIlp], v[kIlp], k2[kIlp], v2[kIlp];
+    int slot[kIlp], run[kIlp];
+#pragma unroll
+    for (int i = 0; i < kIlp; ++i) {
+      const int u = u0 + i * 256;
+      slot[i] = -1;
+      if (u >= n) continue;
+      const int tok = tok0 + u / per;
+      run[i] = u % per;
+      slot[i] = p.slots[tok];
+      const uint4* ks = reinterpret_cast<const uint4*>(p.k + tok * p.k_stride + run[i] * EL);
+      const uint4* vs = reinterpret_cast<const uint4*>(p.v + tok * p.v_stride + run[i] * EL);
+      k[i] = __ldcs(ks);
+      v[i] = __ldcs(vs);
+      if constexpr (FP8) {
+        k2[i] = __ldcs(ks + 1);
+        v2[i] = __ldcs(vs + 1);
+      }
     }
-    if (slot < 0 || slot >= p.n_slots) continue;   // a padding token
-    const long long row =
-        ((static_cast<long long>(slot >> p.shift) * p.Hkv + h) << p.shift) + (slot & ((1 << p.shift) - 1));
-    *reinterpret_cast<uint4*>(p.k_pages + row * ROW + c * 16) = k;
-    *reinterpret_cast<uint4*>(p.v_pages + row * ROW + c * 16) = v;
+#pragma unroll
+    for (int i = 0; i < kIlp; ++i) {
+      if (slot[i] < 0 || slot[i] >= p.n_slots) continue;   // a padding token
+      const int h = run[i] / RUNS, c = run[i] % RUNS;
+      if constexpr (FP8) {
+        k[i] = codes16(k[i], k2[i], p.k_scale[h]);
+        v[i] = codes16(v[i], v2[i], p.v_scale[h]);
+      }
+      const long long row = ((static_cast<long long>(slot[i] >> p.shift) * p.Hkv + h) << p.shift) +
+                            (slot[i] & ((1 << p.shift) - 1));
+      *reinterpret_cast<uint4*>(p.k_pages + row * ROW + c * 16) = k[i];
+      *reinterpret_cast<uint4*>(p.v_pages + row * ROW + c * 16) = v[i];
+    }
   }
 }
 
@@ -154,9 +173,13 @@ int append(const void* k, const void* v, int64_t k_stride, int64_t v_stride, con
   p.Hkv = Hkv;
   while ((1 << p.shift) < page_size) ++p.shift;
   p.n_slots = static_cast<long long>(num_pages) * page_size;
-  const int64_t units = tokens * (width / (fp8 ? 16 : 8));
-  const unsigned blocks =
-      static_cast<unsigned>(std::min<int64_t>((units + 255) / 256, int64_t{1} << 30));
+  const int64_t per = width / (fp8 ? 16 : 8);   // runs of a token
+  if (per > (1 << 20)) return refuse(SINKATTN_UNSUPPORTED, "more than 2^20 runs in a token");
+  // two runs a thread, but one while that leaves SMs without a block
+  const int64_t blocks1 = (tokens * per + 255) / 256;
+  const int64_t runs = blocks1 >= 8LL * sm_count() ? 512 : 256;
+  p.per_block = static_cast<int>(std::max<int64_t>(1, runs / per));
+  const unsigned blocks = static_cast<unsigned>((tokens + p.per_block - 1) / p.per_block);
   auto kern = d == 64 ? (fp8 ? append_kernel<64, true> : append_kernel<64, false>)
                       : (fp8 ? append_kernel<128, true> : append_kernel<128, false>);
   kern<<<blocks, 256, 0, static_cast<cudaStream_t>(stream)>>>(p);

@@ -64,9 +64,12 @@ struct MmaParams {
   int causal, window;
   float* part_acc;
   float* part_md;
+  // SHARED: partials at their place among another pass's, rows that are not
+  // the last queries of the keys, the launch's place in its chain
   int part_slots, part_first;
   int free_rows;
   const int32_t* row_pos;
+  int chain;
   const float* sinks;     // fused mode
   __nv_bfloat16* out;     // fused mode
   float* lse;             // fused mode
@@ -79,7 +82,7 @@ struct MmaParams {
   const float* v_scale;
 };
 
-template <int D, int RT, int TG, int KT, int NST, bool FP8 = false>
+template <int D, int RT, int TG, int KT, int NST, bool FP8 = false, bool SHARED = false>
 struct MmaCfg {
   static constexpr int NW = RT * TG;               // consumer warps
   static constexpr int THREADS = (NW + 1) * 32;    // + producer warp
@@ -95,7 +98,12 @@ struct MmaCfg {
   static constexpr int XCHG_FLOATS_PER_LANE = D / 2 + 4;
   static constexpr int XCHG_BYTES = (TG - 1) * RT * 32 * XCHG_FLOATS_PER_LANE * 4;
   static constexpr int BAR_BYTES = 2 * NST * 8 + 16;
-  static constexpr int SMEM_BYTES = 1024 + OFF_BAR + BAR_BYTES + XCHG_BYTES;
+  // SHARED with one row tile: a token group's exchange slot lies in its own
+  // first ring stage (no other warp reads it, and every copy into it has been
+  // consumed), so that three CTAs fit an SM: sequences' own keys are short,
+  // and a CTA's start-up is a good part of its life
+  static constexpr bool XCHG_IN_RING = SHARED && RT == 1 && D == 64;
+  static constexpr int SMEM_BYTES = 1024 + OFF_BAR + BAR_BYTES + (XCHG_IN_RING ? 0 : XCHG_BYTES);
   // fused mode: one CTA's partial, [16 RT rows][m, d, pad, pad, acc[D]], over the tile ring
   static constexpr int XOUT_STRIDE = D + 4;
   static_assert(FP8 || 16 * RT * XOUT_STRIDE * 4 <= NST * STAGE_BYTES,
@@ -108,15 +116,15 @@ struct MmaCfg {
   static_assert(NST % TG == 0, "every ring stage serves one token group");
   // Two resident CTAs per SM: one CTA's prologue (barrier set-up, first TMA
   // round trip, Q fragments) and epilogue overlap the other's streaming.
-  static constexpr int MIN_CTAS = 2;
+  static constexpr int MIN_CTAS = XCHG_IN_RING ? 3 : 2;
 };
 
-template <int D, int RT, int TG, int KT, int NST, bool FUSED, bool FP8>
-__global__ void __launch_bounds__(MmaCfg<D, RT, TG, KT, NST, FP8>::THREADS,
-                                  MmaCfg<D, RT, TG, KT, NST, FP8>::MIN_CTAS)
+template <int D, int RT, int TG, int KT, int NST, bool FUSED, bool FP8, bool SHARED>
+__global__ void __launch_bounds__(MmaCfg<D, RT, TG, KT, NST, FP8, SHARED>::THREADS,
+                                  MmaCfg<D, RT, TG, KT, NST, FP8, SHARED>::MIN_CTAS)
     attn_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                     const MmaParams p) {
-  using C = MmaCfg<D, RT, TG, KT, NST, FP8>;
+  using C = MmaCfg<D, RT, TG, KT, NST, FP8, SHARED>;
   constexpr int NW = C::NW;
   constexpr float NEG_INF = kNegInf;
 
@@ -135,6 +143,8 @@ __global__ void __launch_bounds__(MmaCfg<D, RT, TG, KT, NST, FP8>::THREADS,
   const int lane = threadIdx.x & 31;
   const int b = blockIdx.z;
   const int kvh = blockIdx.y;
+  if constexpr (SHARED)
+    if (p.chain & kChainWaitFirst) grid_dependency_wait();
   const int S = p.num_splits;
   const int split = blockIdx.x % S;
   const int qb = p.nqb - 1 - static_cast<int>(blockIdx.x / S);   // longest query blocks first
@@ -146,7 +156,7 @@ __global__ void __launch_bounds__(MmaCfg<D, RT, TG, KT, NST, FP8>::THREADS,
   const int q0 = qb * p.QB;
   if (q0 >= Lq) return;   // uniform over the CTA (and the cluster), before any barrier
   const int nq = min(p.QB, Lq - q0);
-  if (threadIdx.x == 0 && ((Lk < Lq && !p.free_rows) || Lk > p.max_kv || Lq < 0))
+  if (threadIdx.x == 0 && ((Lk < Lq && !(SHARED && p.free_rows)) || Lk > p.max_kv || Lq < 0))
     atomicExch(&g_status_attn_mma, SINKATTN_BAD_LENGTHS);
 
   // Positions of the CTA's first and last query (queries are the last Lq keys).
@@ -158,7 +168,7 @@ __global__ void __launch_bounds__(MmaCfg<D, RT, TG, KT, NST, FP8>::THREADS,
   int k_lo = min(split * chunk, Lk);
   int k_hi = min(k_lo + chunk, Lk);
   if (p.causal) k_hi = min(k_hi, posN + 1);
-  if (p.window > 0 && !p.row_pos) k_lo = max(k_lo, pos0 - p.window + 1);
+  if (p.window > 0 && !(SHARED && p.row_pos)) k_lo = max(k_lo, pos0 - p.window + 1);
   // Tiles end at k_hi (contiguous: no copy reads past the last key needed),
   // or start on a multiple of KT (paged: no box straddles a page).
   const bool paged = p.page_size > 0;
@@ -288,7 +298,7 @@ __global__ void __launch_bounds__(MmaCfg<D, RT, TG, KT, NST, FP8>::THREADS,
     const int tl = r / G;
     valid[i] = tl < nq;
     tok[i] = q_start + q0 + tl;
-    pos[i] = p.row_pos && valid[i] ? p.row_pos[tok[i]] : pos0 + tl;
+    pos[i] = SHARED && p.row_pos && valid[i] ? p.row_pos[tok[i]] : pos0 + tl;
     head[i] = kvh * G + (r - tl * G);
   }
 
@@ -400,7 +410,7 @@ __global__ void __launch_bounds__(MmaCfg<D, RT, TG, KT, NST, FP8>::THREADS,
 
     // Mask (skipped for tiles that every row sees whole).
     const bool whole = (j0 >= k_lo) && (j0 + KT <= k_hi) && (!p.causal || j0 + KT - 1 <= pos0) &&
-                       (p.window <= 0 || (j0 > posN - p.window && !p.row_pos));
+                       (p.window <= 0 || (j0 > posN - p.window && !(SHARED && p.row_pos)));
     if (!whole) {
 #pragma unroll
       for (int j = 0; j < KT / 8; ++j) {
@@ -510,10 +520,15 @@ __global__ void __launch_bounds__(MmaCfg<D, RT, TG, KT, NST, FP8>::THREADS,
   }
 
   // Combine the token groups of each row tile.
+  auto slot_of = [&](int group) -> float* {
+    float* base = C::XCHG_IN_RING
+                      ? reinterpret_cast<float*>(smem + group * (FP8 ? C::F8_STAGE : C::STAGE_BYTES))
+                      : xchg + ((group - 1) * RT + rt) * 32 * C::XCHG_FLOATS_PER_LANE;
+    return base + lane * C::XCHG_FLOATS_PER_LANE;
+  };
   if (TG > 1) {
     if (tg > 0) {
-      float* slot = xchg + ((tg - 1) * RT + rt) * 32 * C::XCHG_FLOATS_PER_LANE +
-                    lane * C::XCHG_FLOATS_PER_LANE;
+      float* slot = slot_of(tg);
 #pragma unroll
       for (int jd = 0; jd < D / 8; ++jd)
 #pragma unroll
@@ -529,8 +544,7 @@ __global__ void __launch_bounds__(MmaCfg<D, RT, TG, KT, NST, FP8>::THREADS,
   if (TG > 1 && writer) {
 #pragma unroll 1
     for (int t = 1; t < TG; ++t) {
-      const float* slot = xchg + ((t - 1) * RT + rt) * 32 * C::XCHG_FLOATS_PER_LANE +
-                          lane * C::XCHG_FLOATS_PER_LANE;
+      const float* slot = slot_of(t);
       float a0[2], a1[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -560,7 +574,8 @@ __global__ void __launch_bounds__(MmaCfg<D, RT, TG, KT, NST, FP8>::THREADS,
     for (int i = 0; i < 2; ++i) {
       if (!valid[i]) continue;
       const size_t rowid = static_cast<size_t>(tok[i]) * p.Hq + head[i];
-      const size_t slot = rowid * p.part_slots + p.part_first + split;
+      const size_t slot =
+          SHARED ? rowid * p.part_slots + p.part_first + split : rowid * S + split;
       float* arow = p.part_acc + slot * D;
 #pragma unroll
       for (int jd = 0; jd < D / 8; ++jd) {
@@ -659,14 +674,16 @@ __global__ void __launch_bounds__(MmaCfg<D, RT, TG, KT, NST, FP8>::THREADS,
   // split mode: this thread's partial writes are issued; a dependent merge
   // may start launching (it waits for the whole grid before reading)
   if (!FUSED) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if constexpr (SHARED)
+    if (p.chain & kChainWaitLast) grid_dependency_wait();
 }
 
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-template <int D, int RT, int TG, int KT, int NST, bool FUSED, bool FP8>
+template <int D, int RT, int TG, int KT, int NST, bool FUSED, bool FP8, bool SHARED>
 static int launch_cfg(const AttnArgs& a, cudaStream_t stream) {
-  using C = MmaCfg<D, RT, TG, KT, NST, FP8>;
+  using C = MmaCfg<D, RT, TG, KT, NST, FP8, SHARED>;
   CUtensorMap tmK, tmV;
   const uint64_t rows = kv_map_rows(a);
   const int box = kv_box_rows(a, KT);
@@ -701,6 +718,7 @@ static int launch_cfg(const AttnArgs& a, cudaStream_t stream) {
   p.part_first = a.part_first;
   p.free_rows = a.free_rows;
   p.row_pos = a.row_pos;
+  p.chain = a.chain;
   p.page_size = a.page_size;
   p.box_rows = box;
   p.page_indptr = a.page_indptr;
@@ -711,7 +729,7 @@ static int launch_cfg(const AttnArgs& a, cudaStream_t stream) {
   p.k_scale = a.k_scale;
   p.v_scale = a.v_scale;
 
-  auto kern = attn_mma_kernel<D, RT, TG, KT, NST, FUSED, FP8>;
+  auto kern = attn_mma_kernel<D, RT, TG, KT, NST, FUSED, FP8, SHARED>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        C::SMEM_BYTES);
   if (e != cudaSuccess) {
@@ -742,6 +760,8 @@ static int launch_cfg(const AttnArgs& a, cudaStream_t stream) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, kern, tmK, tmV, p);
+  } else if (SHARED) {
+    e = launch_chained(kern, grid, C::THREADS, C::SMEM_BYTES, stream, tmK, tmV, p);
   } else {
     kern<<<grid, C::THREADS, C::SMEM_BYTES, stream>>>(tmK, tmV, p);
     e = cudaGetLastError();
@@ -753,7 +773,7 @@ static int launch_cfg(const AttnArgs& a, cudaStream_t stream) {
   return SINKATTN_OK;
 }
 
-template <bool FUSED, bool FP8>
+template <bool FUSED, bool FP8, bool SHARED>
 static int launch_attn_mma_t(const AttnArgs& a, cudaStream_t stream) {
   const int G = a.Hq / a.Hkv;
   const int64_t rows = static_cast<int64_t>(G) * (a.cu_q ? a.max_q : a.q_len);
@@ -766,24 +786,29 @@ static int launch_attn_mma_t(const AttnArgs& a, cudaStream_t stream) {
   // twice as many keep the same bytes in flight per SM
   constexpr int NS = FP8 ? 8 : 4;
   if (a.d == 64) {
-    if (rt_needed <= 1) return launch_cfg<64, 1, 4, 64, NS, FUSED, FP8>(a, stream);
-    if (rt_needed <= 2) return launch_cfg<64, 2, 2, 64, NS, FUSED, FP8>(a, stream);
-    if (rt_needed <= 3) return launch_cfg<64, 3, 2, 64, NS, FUSED, FP8>(a, stream);
-    return launch_cfg<64, 4, 2, 64, NS, FUSED, FP8>(a, stream);
+    if (rt_needed <= 1) return launch_cfg<64, 1, 4, 64, NS, FUSED, FP8, SHARED>(a, stream);
+    if (rt_needed <= 2) return launch_cfg<64, 2, 2, 64, NS, FUSED, FP8, SHARED>(a, stream);
+    if (rt_needed <= 3) return launch_cfg<64, 3, 2, 64, NS, FUSED, FP8, SHARED>(a, stream);
+    return launch_cfg<64, 4, 2, 64, NS, FUSED, FP8, SHARED>(a, stream);
   }
-  if (rt_needed <= 1) return launch_cfg<128, 1, 4, 32, NS, FUSED, FP8>(a, stream);
-  if (rt_needed <= 2) return launch_cfg<128, 2, 2, 32, NS, FUSED, FP8>(a, stream);
-  if (rt_needed <= 3) return launch_cfg<128, 3, 2, 32, NS, FUSED, FP8>(a, stream);
-  return launch_cfg<128, 4, 2, 32, NS, FUSED, FP8>(a, stream);
+  if (rt_needed <= 1) return launch_cfg<128, 1, 4, 32, NS, FUSED, FP8, SHARED>(a, stream);
+  if (rt_needed <= 2) return launch_cfg<128, 2, 2, 32, NS, FUSED, FP8, SHARED>(a, stream);
+  if (rt_needed <= 3) return launch_cfg<128, 3, 2, 32, NS, FUSED, FP8, SHARED>(a, stream);
+  return launch_cfg<128, 4, 2, 32, NS, FUSED, FP8, SHARED>(a, stream);
 }
 
 int launch_attn_mma(const AttnArgs& a, cudaStream_t stream) {
-  return a.kv_fp8 ? launch_attn_mma_t<false, true>(a, stream)
-                  : launch_attn_mma_t<false, false>(a, stream);
+  return a.kv_fp8 ? launch_attn_mma_t<false, true, false>(a, stream)
+                  : launch_attn_mma_t<false, false, false>(a, stream);
+}
+
+int launch_attn_mma_shared(const AttnArgs& a, cudaStream_t stream) {
+  return a.kv_fp8 ? launch_attn_mma_t<false, true, true>(a, stream)
+                  : launch_attn_mma_t<false, false, true>(a, stream);
 }
 
 int launch_attn_mma_fused(const AttnArgs& a, cudaStream_t stream) {
-  return launch_attn_mma_t<true, false>(a, stream);
+  return launch_attn_mma_t<true, false, false>(a, stream);
 }
 
 SINKATTN_DEFINE_SET_HOOKS(set_hooks_attn_mma)

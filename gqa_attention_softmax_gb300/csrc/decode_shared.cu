@@ -54,6 +54,7 @@ __device__ __forceinline__ int block_sum_scan(int v, int* total, int* sums) {
 __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const PlanParams p) {
   __shared__ int sums[32];
   const int tid = threadIdx.x;
+  grid_launch_dependents();   // the next launch sets itself up meanwhile, and waits for this one
   bool bad = false;
   // the keys of group g's prefix that can be used
   auto prefix_of = [&](int g, bool* wrong) -> int {

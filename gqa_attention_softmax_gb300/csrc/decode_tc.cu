@@ -37,7 +37,8 @@ struct DtcParams {
   int causal, window;
   float* part_acc;
   float* part_md;
-  int part_slots, part_first;
+  int part_slots, part_first;   // SHARED: partials at their place among another pass's
+  int chain;                    // SHARED: the launch's place in its chain
   // paged KV (page_size > 0): page-pool rows, boxes of box_rows keys
   int page_size, box_rows;
   const int32_t* page_indptr;
@@ -176,7 +177,7 @@ struct DtcCfg {
 // key scale joins the item's logit scale, the value scale multiplies the
 // staged accumulator. Rows are normalised by the exact weight sum: f16
 // weights are within 2^-11 of it.
-template <int RR, bool PAGED, bool FP8>
+template <int RR, bool PAGED, bool FP8, bool SHARED>
 __global__ void __launch_bounds__(DtcCfg<RR, FP8>::THREADS, 1)
     decode_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
                      const __grid_constant__ CUtensorMap tmK,
@@ -212,6 +213,8 @@ __global__ void __launch_bounds__(DtcCfg<RR, FP8>::THREADS, 1)
   const int lane = threadIdx.x & 31;
   const int n_mine = (p.n_items - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) /
                      static_cast<int>(gridDim.x);
+  if constexpr (SHARED)
+    if (p.chain & kChainWaitFirst) grid_dependency_wait();
   // kv_indptr in shared memory (global-memory loads under a saturated HBM
   // stream take microseconds, and every role needs every item's keys)
   int32_t* cu_s = reinterpret_cast<int32_t*>(smem + C::OFF_CU);
@@ -641,6 +644,7 @@ __global__ void __launch_bounds__(DtcCfg<RR, FP8>::THREADS, 1)
     const int tl = row / G;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     float* stage = reinterpret_cast<float*>(smem + C::OFF_STG);
+    const int S = p.num_splits;
     const uint64_t keep_policy = policy_evict_last();
     for (int k = 0; k < n_mine; ++k) {
       const DtcItem t = item_of(k);
@@ -680,7 +684,7 @@ __global__ void __launch_bounds__(DtcCfg<RR, FP8>::THREADS, 1)
           md.x = mlr.x * lscale + (lg2(mlr.y) - lg2(mlr.z)) * kLn2;
           md.y = mlr.z;
         }
-        *reinterpret_cast<float2*>(p.part_md + (rowid * p.part_slots + p.part_first + t.split) * 2) = md;
+        *reinterpret_cast<float2*>(p.part_md + (SHARED ? rowid * p.part_slots + p.part_first + t.split : rowid * S + t.split) * 2) = md;
       }
       named_barrier_sync(1, 128);   // staging written
       const int nrows = t.nq * G;
@@ -691,7 +695,7 @@ __global__ void __launch_bounds__(DtcCfg<RR, FP8>::THREADS, 1)
         const float4 val = *reinterpret_cast<const float4*>(stage + r * C::XS + lane * 4);
         // kept in L2 as long as possible: the merge reads the newest partials first
         asm volatile("st.global.L2::cache_hint.v4.f32 [%0], {%1, %2, %3, %4}, %5;" ::"l"(
-                         p.part_acc + (rowid * p.part_slots + p.part_first + t.split) * D + lane * 4),
+                         p.part_acc + (SHARED ? rowid * p.part_slots + p.part_first + t.split : rowid * S + t.split) * D + lane * 4),
                      "f"(val.x), "f"(val.y), "f"(val.z), "f"(val.w), "l"(keep_policy)
                      : "memory");
       }
@@ -718,6 +722,8 @@ __global__ void __launch_bounds__(DtcCfg<RR, FP8>::THREADS, 1)
   }
   // this CTA's partials are written: a dependent merge may start launching
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if constexpr (SHARED)
+    if (p.chain & kChainWaitLast) grid_dependency_wait();
   if (warp == C::W_MMA) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, C::TMEM_COLS);
@@ -725,7 +731,7 @@ __global__ void __launch_bounds__(DtcCfg<RR, FP8>::THREADS, 1)
 }
 
 // ---------------------------------------------------------------------------
-template <int RR, bool PAGED, bool FP8 = false>
+template <int RR, bool PAGED, bool FP8 = false, bool SHARED = false>
 static int launch_dtc(const AttnArgs& a, int QB, cudaStream_t stream) {
   using C = DtcCfg<RR, FP8>;
   const int G = a.Hq / a.Hkv;
@@ -771,7 +777,8 @@ static int launch_dtc(const AttnArgs& a, int QB, cudaStream_t stream) {
   p.part_md = a.part_md;
   p.part_slots = part_slots(a);
   p.part_first = a.part_first;
-  auto kern = decode_tc_kernel<RR, PAGED, FP8>;
+  p.chain = a.chain;
+  auto kern = decode_tc_kernel<RR, PAGED, FP8, SHARED>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) {
     set_error("cudaFuncSetAttribute: %s", cudaGetErrorString(e));
@@ -779,8 +786,12 @@ static int launch_dtc(const AttnArgs& a, int QB, cudaStream_t stream) {
   }
   if (p.n_items == 0) return SINKATTN_OK;
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(items, sm_count()));
-  kern<<<grid, C::THREADS, C::SMEM, stream>>>(tmQ, tmK, tmV, p);
-  e = cudaGetLastError();
+  if (SHARED) {
+    e = launch_chained(kern, dim3(grid), C::THREADS, C::SMEM, stream, tmQ, tmK, tmV, p);
+  } else {
+    kern<<<grid, C::THREADS, C::SMEM, stream>>>(tmQ, tmK, tmV, p);
+    e = cudaGetLastError();
+  }
   if (e != cudaSuccess) {
     set_error("decode kernel launch: %s", cudaGetErrorString(e));
     return SINKATTN_CUDA_ERROR;
@@ -811,6 +822,13 @@ int launch_decode_tc(const AttnArgs& a, cudaStream_t stream) {
   }
   const int QB = min(a.q_len, 128 / G);   // query tokens per CTA
   const int R = G * QB;                   // real rows of the 128-row tile
+  if (a.part_slots > 0) {   // a part of shared-prefix decode (paged, bf16)
+    if (R <= 16) return launch_dtc<16, true, false, true>(a, QB, stream);
+    if (R <= 32) return launch_dtc<32, true, false, true>(a, QB, stream);
+    if (R <= 48) return launch_dtc<48, true, false, true>(a, QB, stream);
+    if (R <= 64) return launch_dtc<64, true, false, true>(a, QB, stream);
+    return launch_dtc<128, true, false, true>(a, QB, stream);
+  }
   if (a.page_size > 0) {
     if (R <= 16) return launch_dtc<16, true>(a, QB, stream);
     if (R <= 32) return launch_dtc<32, true>(a, QB, stream);

@@ -35,6 +35,7 @@ struct AttnArgs {
   // token counted from the first key (nullptr: no window)
   int32_t free_rows;
   const int32_t* row_pos;
+  int32_t chain;            // kChain*: its place in a chain of dependent launches
   // paged KV (page_size > 0): k and v are page pools [num_pages, Hkv, page_size, d];
   // sequence b's keys [e * page_size, (e + 1) * page_size) live in page
   // page_indices[page_indptr[b] + e]; cu_k still gives the key counts
@@ -64,6 +65,30 @@ inline int kv_box_rows(const AttnArgs& a, int tile_keys) {
   return a.page_size < pow2 ? a.page_size : pow2;
 }
 
+// A chain of launches, each a programmatic dependent of the one before: a
+// launch may start while the one before it still runs. kChainWaitFirst: it
+// waits for that one's results before it reads anything. kChainWaitLast: it
+// needs none of them (the one before waited for what it does need), but ends
+// only after it, so that whoever waits for this launch has waited for both.
+constexpr int32_t kChainWaitFirst = 1, kChainWaitLast = 2;
+
+// Launches `kern` as a programmatic dependent of the launch before it.
+template <typename... Params, typename... Args>
+inline cudaError_t launch_chained(void (*kern)(Params...), dim3 grid, int threads, size_t smem,
+                                  cudaStream_t stream, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // Partials of a row, this call's or shared with another call's.
 inline int part_slots(const AttnArgs& a) { return a.part_slots > 0 ? a.part_slots : a.num_splits; }
 
@@ -84,6 +109,8 @@ int make_q_tmap(CUtensorMap* map, const void* q, uint64_t total_q, int Hq, int d
 // Split-KV decode (per-chunk partial outputs) on the warp-level tensor-core
 // path. Returns a SINKATTN_* status.
 int launch_attn_mma(const AttnArgs& a, cudaStream_t stream);
+// The same as a part of shared-prefix decode (a.part_slots, a.chain, ...).
+int launch_attn_mma_shared(const AttnArgs& a, cudaStream_t stream);
 
 // Split-KV decode with the merge done on chip: the num_splits (<= 16) chunks
 // of one (sequence, KV head) form a thread-block cluster that folds its

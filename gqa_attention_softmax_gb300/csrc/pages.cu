@@ -184,8 +184,15 @@ __global__ void __launch_bounds__(kThreads)
                          const int32_t* __restrict__ cu, int n, int total_new,
                          int32_t* __restrict__ slots) {
   __shared__ int sums[32];
+  __shared__ int kept_s[3][kKept];
+  __shared__ int ok_s, count_s;
   const int tid = threadIdx.x;
   int32_t* hdr = t.hdr();
+  // one block: what the second half reads of an item stays in shared memory
+  const bool alone = cluster_size() == 1;
+  int* first_of = alone && n <= kKept ? kept_s[0] : t.aux(0);
+  int* len_of = alone && n <= kKept ? kept_s[1] : t.aux(1);
+  int* copy_of = alone && n <= kKept ? kept_s[2] : t.aux(2);
   if (cluster_rank() == 0) {
     // the first item of each thread stays in registers
     ReserveItem mine{};
@@ -221,14 +228,14 @@ __global__ void __launch_bounds__(kThreads)
           copies = r.tail >= 0 && !(__ldcg(&t.work(0)[r.tail]) == r.rc &&
                                     __ldcg(&t.work(1)[r.tail]) == n - i);
           want = t.pages(r.len + r.grow) - t.pages(r.len) + copies;
-          t.aux(1)[i] = r.len;
-          t.aux(2)[i] = copies;
+          len_of[i] = r.len;
+          copy_of[i] = copies;
         }
       }
       int total;
       const int before = block_scan(want, &total, sums);
       // (a call that needs 2^31 pages has failed long before: need is exact)
-      if (i < n) t.aux(0)[i] = static_cast<int>(need) + before + copies;
+      if (i < n) first_of[i] = static_cast<int>(need) + before + copies;
       need += total;
     }
     bad = __syncthreads_or(bad);
@@ -239,27 +246,28 @@ __global__ void __launch_bounds__(kThreads)
       else if (bad) status = SINKATTN_BAD_PAGES;
       else if (need > count) status = SINKATTN_OUT_OF_PAGES;
       if (status) atomicExch(&g_status_pages, status);
-      hdr[H_OK] = status == SINKATTN_OK;
-      hdr[H_COUNT] = count;
+      ok_s = hdr[H_OK] = status == SINKATTN_OK;
+      count_s = hdr[H_COUNT] = count;
       hdr[H_PAIRS] = 0;
       if (!status) hdr[H_FREE] = count - static_cast<int>(need);
     }
   }
-  cluster_sync_all();
+  if (alone) __syncthreads();
+  else cluster_sync_all();
   const int nt = cluster_size() * kThreads;
   const int t0 = cluster_rank() * kThreads + tid;
-  if (!__ldcg(&hdr[H_OK])) {
+  if (!(alone ? ok_s : __ldcg(&hdr[H_OK]))) {
     for (int i = t0; i < total_new; i += nt) slots[i] = -1;
     return;
   }
-  const int count = __ldcg(&hdr[H_COUNT]);
+  const int count = alone ? count_s : __ldcg(&hdr[H_COUNT]);
   int32_t* list = t.list();
   for (int i = t0; i < n; i += nt) {
-    const int id = ids[i], len = __ldcg(&t.aux(1)[i]);
+    const int id = ids[i], len = len_of[i];
     t.lens()[id] = len + (cu[i + 1] - cu[i]);
-    if (__ldcg(&t.aux(2)[i])) {
+    if (copy_of[i]) {
       int32_t* entry = &list[static_cast<size_t>(id) * t.M + (len >> t.shift)];
-      const int src = *entry, dst = t.free_list()[count - __ldcg(&t.aux(0)[i])];
+      const int src = *entry, dst = t.free_list()[count - first_of[i]];
       if (!t.page_ok(dst)) continue;   // (a table that was written over: nothing to copy to)
       *entry = dst;
       atomicSub(&t.rc()[src], 1);
@@ -277,12 +285,12 @@ __global__ void __launch_bounds__(kThreads)
       if (cu[mid] <= k) lo = mid;
       else hi = mid;
     }
-    const int len = __ldcg(&t.aux(1)[lo]), first = __ldcg(&t.aux(0)[lo]);
+    const int len = len_of[lo], first = first_of[lo];
     const int pos = len + (k - cu[lo]), e = pos >> t.shift, have = t.pages(len);
     int32_t* row = list + static_cast<size_t>(ids[lo]) * t.M;
     int page;
     if (e < have) {
-      page = __ldcg(&t.aux(2)[lo]) ? t.free_list()[count - first] : row[e];
+      page = copy_of[lo] ? t.free_list()[count - first] : row[e];
     } else {
       page = t.free_list()[count - 1 - first - (e - have)];
       if ((pos & (t.P - 1)) == 0 && t.page_ok(page)) {   // a new page's first slot is a new token's
@@ -358,21 +366,29 @@ __global__ void __launch_bounds__(kThreads)
 // ---------------------------------------------------------------------------
 // truncate
 // ---------------------------------------------------------------------------
-// A dropped page is given back by its first appearance in the request (its
-// position is elected in work(0)) if its count has come to zero. Every block
-// checks the whole request and keeps what each item keeps and drops, in
-// shared memory for calls of up to kKept sequences, else in aux(0) and aux(1),
-// where all blocks write the same words. A thread takes runs of kRun
-// consecutive cells (item, entry) of the rectangle n x (longest drop), a
-// block a run of those, so that positions follow the request's order with one
-// scan per kRun * kThreads cells.
+// A dropped page that only this list held is free at once. One that other
+// lists hold too is counted down, and if nothing is left its first appearance
+// in the request (its position is elected in work(0)) gives it back. Scattered
+// words are what a block can touch least often (a few per ten cycles), so
+// pages of one holder cost one read and one write of their count, shared
+// pages five.
+//
+// Every block checks the whole request and keeps what each item keeps and
+// drops, in shared memory for calls of up to kKept sequences, else in aux(0)
+// and aux(1), where all blocks write the same words. Cells (item, entry) of the
+// rectangle n x (longest drop) are taken in request order: a block has a run
+// of them, a warp kRun * 32 consecutive ones at a time, lane by lane, so list
+// and free-list accesses are contiguous and ranks are ballots and one scan.
+// Where one block's step holds all cells, block 0 goes on alone.
 __global__ void __launch_bounds__(kThreads)
     pages_truncate_kernel(const PageTab t, const int32_t* __restrict__ ids,
                           const int32_t* __restrict__ new_lens, int n) {
+  constexpr int kStep = kRun * kThreads;
   __shared__ int sums[32];
   __shared__ int most_s, found_s;
   __shared__ int keep_s[kKept], drop_s[kKept];
-  const int tid = threadIdx.x, rank = cluster_rank(), nr = cluster_size();
+  const int tid = threadIdx.x, lane = tid & 31, rank = cluster_rank();
+  int nr = cluster_size();
   int32_t* hdr = t.hdr();
   int* keep = n <= kKept ? keep_s : t.aux(0);
   int* drop = n <= kKept ? drop_s : t.aux(1);
@@ -402,130 +418,122 @@ __global__ void __launch_bounds__(kThreads)
     return;   // every block of the cluster
   }
   const int most = most_s;
-  // cells in request order: a block's run, and the thread's first cells in registers
   const int cells = n * most;        // < max_seqs * max_pages
-  constexpr int kStep = kRun * kThreads;
-  const int per = static_cast<int>((static_cast<long long>(cells) + nr - 1) / nr + kStep - 1) / kStep * kStep;
+  const bool alone = cells <= kStep;
+  if (nr > 1 && alone) {
+    cluster_sync_all();              // every block has read the lengths
+    if (rank > 0) return;
+    nr = 1;
+  }
+  const int per = ((cells + nr - 1) / nr + kStep - 1) / kStep * kStep;
   const int c0 = static_cast<int>(min(static_cast<long long>(cells), static_cast<long long>(rank) * per));
-  const int c1 = static_cast<int>(min(static_cast<long long>(cells), static_cast<long long>(c0) + per));
-  // addresses (in words from the first list) of the cells [c, c + kRun), -1 where nothing is dropped
-  auto entries = [&](int c, long long (&at)[kRun]) {
-    int i = c / max(most, 1), e = c - i * most;
+  const int c1 = min(cells, c0 + per);
+  // A block with one step keeps its cells in registers over the phases, one
+  // with more loads them again and takes the shared way for every page.
+  const bool single = c1 - c0 <= kStep;
+  int at[kRun], page[kRun];   // the entry in words from the first list, its page; -1: none
+  uint32_t shared = 0, back = 0;
+  int found = 0, before = 0, all = 0, total;
+#pragma unroll 1
+  for (int phase = 0; phase < 4; ++phase) {
+#pragma unroll 1
+    for (int base = c0; base < c1; base += kStep) {
+      // the thread's cells: its warp's run, lane by lane
+      const int first = base + (tid >> 5) * (kRun * 32) + lane;
+      if (phase == 0 || !single) {
 #pragma unroll
-    for (int k = 0; k < kRun; ++k) {
-      at[k] = -1;
-      if (c + k < c1 && e < drop[i]) at[k] = static_cast<long long>(ids[i]) * t.M + keep[i] + e;
-      if (++e == most) {
-        e = 0;
-        ++i;
+        for (int k = 0; k < kRun; ++k) {
+          const int c = first + k * 32;
+          at[k] = -1;
+          if (c >= c1) continue;
+          const int i = c / most, e = c - i * most;
+          if (e < drop[i]) at[k] = ids[i] * t.M + keep[i] + e;
+        }
+#pragma unroll
+        for (int k = 0; k < kRun; ++k) page[k] = at[k] >= 0 ? t.list()[at[k]] : -1;
+#pragma unroll
+        for (int k = 0; k < kRun; ++k) page[k] = t.page_ok(page[k]) ? page[k] : -1;
+      }
+      if (phase == 0) {          // which pages other lists hold too, before any count changes
+        shared = 0xffu;
+        if (single) {
+          int r[kRun];
+#pragma unroll
+          for (int k = 0; k < kRun; ++k) r[k] = page[k] >= 0 ? __ldcg(&t.rc()[page[k]]) : 1;
+          shared = 0;
+#pragma unroll
+          for (int k = 0; k < kRun; ++k) shared |= r[k] != 1 ? 1u << k : 0u;
+        }
+#pragma unroll
+        for (int k = 0; k < kRun; ++k)
+          if ((shared >> k & 1u) && page[k] >= 0) t.work(0)[page[k]] = 0;
+      } else if (phase == 1) {   // count down, elect
+#pragma unroll
+        for (int k = 0; k < kRun; ++k) {
+          if (page[k] < 0) continue;
+          if (shared >> k & 1u) {
+            atomicSub(&t.rc()[page[k]], 1);
+            atomicMax(&t.work(0)[page[k]], INT32_MAX - (first + k * 32));
+          } else {
+            t.rc()[page[k]] = 0;
+          }
+        }
+      } else {                   // who gives a page back (counted in phase 2, written in phase 3)
+        if (phase == 2 || !single) {
+          int r[kRun], w[kRun];
+#pragma unroll
+          for (int k = 0; k < kRun; ++k) {
+            const bool look = page[k] >= 0 && (shared >> k & 1u);
+            r[k] = look ? __ldcg(&t.rc()[page[k]]) : 1;
+            w[k] = look ? __ldcg(&t.work(0)[page[k]]) : 0;
+          }
+          back = 0;
+#pragma unroll
+          for (int k = 0; k < kRun; ++k) {
+            const bool yes = shared >> k & 1u ? r[k] == 0 && w[k] == INT32_MAX - (first + k * 32)
+                                              : page[k] >= 0;
+            if (yes) back |= 1u << k;
+          }
+        }
+        // ranks: the warps' sums by a scan (lane 0 carries them), then by lanes within 32 cells
+        uint32_t vote[kRun];
+        int sum = 0;
+#pragma unroll
+        for (int k = 0; k < kRun; ++k) {
+          vote[k] = __ballot_sync(0xffffffffu, back >> k & 1u);
+          sum += __popc(vote[k]);
+        }
+        int r = block_scan(lane == 0 ? sum : 0, &total, sums);
+        if (phase == 2) {
+          found += total;
+        } else {
+          r = before + __shfl_sync(0xffffffffu, r, 0);
+          before += total;
+#pragma unroll
+          for (int k = 0; k < kRun; ++k) {
+            if (at[k] >= 0) t.list()[at[k]] = -1;
+            if ((back >> k & 1u) && count + all <= t.N)
+              t.free_list()[count + all - 1 - r - __popc(vote[k] & ((1u << lane) - 1u))] = page[k];
+            r += __popc(vote[k]);
+          }
+        }
       }
     }
-  };
-  auto load = [&](const long long (&at)[kRun], int (&p)[kRun]) {
-#pragma unroll
-    for (int k = 0; k < kRun; ++k) p[k] = at[k] >= 0 ? t.list()[at[k]] : -1;
-#pragma unroll
-    for (int k = 0; k < kRun; ++k) p[k] = t.page_ok(p[k]) ? p[k] : -1;
-  };
-  const int first = c0 + tid * kRun;
-  long long at0[kRun];
-  int page0[kRun];
-  if (first < c1) {
-    entries(first, at0);
-    load(at0, page0);
-  }
-  // runs f(first cell, addresses, pages) over the thread's cells
-  auto each = [&](auto&& f) {
-    for (int c = first; c < c1; c += kStep) {
-      if (c == first) {
-        f(c, at0, page0);
-      } else {
-        long long at[kRun];
-        int p[kRun];
-        entries(c, at);
-        load(at, p);
-        f(c, at, p);
-      }
+    if (phase == 2 && tid == 0) found_s = found;
+    if (phase < 3) {
+      if (alone) __syncthreads();
+      else cluster_sync_all();
     }
-  };
-  each([&](int, const long long (&)[kRun], const int (&p)[kRun]) {
-#pragma unroll
-    for (int k = 0; k < kRun; ++k)
-      if (p[k] >= 0) t.work(0)[p[k]] = 0;
-  });
-  cluster_sync_all();   // every block has read the lengths; work(0) is clear
-  for (int i = rank * kThreads + tid; i < n; i += nr * kThreads)
-    t.lens()[ids[i]] = new_lens ? new_lens[i] : 0;
-  if (most == 0) return;   // uniform over the cluster: no page leaves a list
-  each([&](int c, const long long (&)[kRun], const int (&p)[kRun]) {
-#pragma unroll
-    for (int k = 0; k < kRun; ++k)
-      if (p[k] >= 0) {
-        atomicSub(&t.rc()[p[k]], 1);
-        atomicMax(&t.work(0)[p[k]], INT32_MAX - (c + k));
-      }
-  });
-  cluster_sync_all();
-  auto backs = [&](int c, const int (&p)[kRun]) -> uint32_t {   // which cells give their page back
-    int r[kRun], w[kRun];
-#pragma unroll
-    for (int k = 0; k < kRun; ++k) {
-      r[k] = p[k] >= 0 ? __ldcg(&t.rc()[p[k]]) : 1;
-      w[k] = p[k] >= 0 ? __ldcg(&t.work(0)[p[k]]) : 0;
-    }
-    uint32_t m = 0;
-#pragma unroll
-    for (int k = 0; k < kRun; ++k)
-      if (r[k] == 0 && w[k] == INT32_MAX - (c + k)) m |= 1u << k;
-    return m;
-  };
-  uint32_t back0 = 0;
-  int found = 0, total;
-  each([&](int c, const long long (&)[kRun], const int (&p)[kRun]) {
-    const uint32_t m = backs(c, p);
-    if (c == first) back0 = m;
-    found += __popc(m);
-  });
-  block_scan(found, &total, sums);
-  if (tid == 0) found_s = total;
-  cluster_sync_all();
-  int before;
-  const int all = cluster_sum(&found_s, rank, nr, &before);
-  if (rank == 0 && tid == 0) hdr[H_FREE] = count + all;
-  for (int base = c0; base < c1; base += kStep) {
-    const int c = base + tid * kRun;
-    long long at[kRun];
-    int p[kRun];
-    uint32_t m = 0;
-#pragma unroll
-    for (int k = 0; k < kRun; ++k) {
-      at[k] = -1;
-      p[k] = -1;
-    }
-    if (base == c0 && c < c1) {
-#pragma unroll
-      for (int k = 0; k < kRun; ++k) {
-        at[k] = at0[k];
-        p[k] = page0[k];
-      }
-      m = back0;
-    } else if (c < c1) {
-      entries(c, at);
-      load(at, p);
-      m = backs(c, p);
-    }
-    int r = before + block_scan(__popc(m), &total, sums);
-    before += total;
-#pragma unroll
-    for (int k = 0; k < kRun; ++k) {
-      if (at[k] >= 0) t.list()[at[k]] = -1;
-      if (m >> k & 1u) {
-        if (count + all <= t.N) t.free_list()[count + all - 1 - r] = p[k];
-        ++r;
-      }
+    if (phase == 0) {   // every block has read the lengths and the counts
+      for (int i = rank * kThreads + tid; i < n; i += nr * kThreads)
+        t.lens()[ids[i]] = new_lens ? new_lens[i] : 0;
+      if (most == 0) return;   // uniform: no page leaves a list
+    } else if (phase == 2) {
+      all = cluster_sum(&found_s, rank, nr, &before);
+      if (rank == 0 && tid == 0) hdr[H_FREE] = count + all;
     }
   }
-  cluster_sync_all();   // the other blocks have read this one's sum
+  if (!alone) cluster_sync_all();   // the other blocks have read this one's sum
 }
 
 // ---------------------------------------------------------------------------

@@ -229,22 +229,6 @@ __global__ void __launch_bounds__(PxCfg<D, FP8>::LB_THREADS, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
-  // the groups' tables in shared memory: every role looks every item up
-  int32_t* gs = reinterpret_cast<int32_t*>(smem + C::OFF_GRP);
-  const bool staged = p.groups <= C::GRP_CAP;
-  const int32_t *gq = p.grp_q, *gk = p.grp_k, *gp = p.grp_pages, *gu = p.grp_unit;
-  if (staged) {
-    for (int i = threadIdx.x; i <= p.groups; i += blockDim.x) {
-      gs[i] = gq[i];
-      gs[C::GRP_CAP + 1 + i] = gk[i];
-      gs[2 * (C::GRP_CAP + 1) + i] = gp[i];
-      gs[3 * (C::GRP_CAP + 1) + i] = gu[i];
-    }
-    gq = gs;
-    gk = gs + C::GRP_CAP + 1;
-    gp = gs + 2 * (C::GRP_CAP + 1);
-    gu = gs + 3 * (C::GRP_CAP + 1);
-  }
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
@@ -265,10 +249,33 @@ __global__ void __launch_bounds__(PxCfg<D, FP8>::LB_THREADS, 1)
     }
     *abort_flag = 0;
     fence_barrier_init();
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
   }
   if (warp == 1) {
     tc::tmem_alloc(tmem_slot, C::TMEM_COLS);
     tc::tmem_relinquish();
+  }
+  // all of the above overlaps the plan's launch; the next launch of the chain
+  // may start as this one's blocks end
+  grid_dependency_wait();
+  grid_launch_dependents();
+  // the groups' tables in shared memory: every role looks every item up
+  int32_t* gs = reinterpret_cast<int32_t*>(smem + C::OFF_GRP);
+  const bool staged = p.groups <= C::GRP_CAP;
+  const int32_t *gq = p.grp_q, *gk = p.grp_k, *gp = p.grp_pages, *gu = p.grp_unit;
+  if (staged) {
+    for (int i = threadIdx.x; i <= p.groups; i += blockDim.x) {
+      gs[i] = gq[i];
+      gs[C::GRP_CAP + 1 + i] = gk[i];
+      gs[2 * (C::GRP_CAP + 1) + i] = gp[i];
+      gs[3 * (C::GRP_CAP + 1) + i] = gu[i];
+    }
+    gq = gs;
+    gk = gs + C::GRP_CAP + 1;
+    gp = gs + 2 * (C::GRP_CAP + 1);
+    gu = gs + 3 * (C::GRP_CAP + 1);
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -294,11 +301,6 @@ __global__ void __launch_bounds__(PxCfg<D, FP8>::LB_THREADS, 1)
   if (warp == 0) {
     // ---------------------------------------------------------------- producer
     const bool leader = (lane == 0);
-    if (leader) {
-      tma_prefetch_desc(&tmQ);
-      tma_prefetch_desc(&tmK);
-      tma_prefetch_desc(&tmV);
-    }
     const uint64_t policy = policy_evict_last();   // the row blocks of a group re-read the keys
     const uint32_t q_bytes = static_cast<uint32_t>(C::NSUB * 128 * p.G * p.QB);
     const int nbox = KT / p.box_rows;
@@ -730,9 +732,8 @@ int launch(const AttnArgs& a, const SharedPlan& plan, cudaStream_t stream) {
   auto kern = prefix_tc_kernel<D, FP8>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e == cudaSuccess) {
-    kern<<<static_cast<unsigned>(std::min<int64_t>(units, sm_count())), C::THREADS, C::SMEM, stream>>>(
-        tmQ, tmK, tmV, p);
-    e = cudaGetLastError();
+    e = launch_chained(kern, dim3(static_cast<unsigned>(std::min<int64_t>(units, sm_count()))),
+                       C::THREADS, C::SMEM, stream, tmQ, tmK, tmV, p);
   }
   if (e != cudaSuccess) {
     set_error("shared-prefix kernel launch: %s", cudaGetErrorString(e));
