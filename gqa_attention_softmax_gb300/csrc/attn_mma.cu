@@ -116,7 +116,7 @@ struct MmaCfg {
   static_assert(NST % TG == 0, "every ring stage serves one token group");
   // Two resident CTAs per SM: one CTA's prologue (barrier set-up, first TMA
   // round trip, Q fragments) and epilogue overlap the other's streaming.
-  static constexpr int MIN_CTAS = XCHG_IN_RING ? 3 : 2;
+  static constexpr int MIN_CTAS = XCHG_IN_RING ? 4 : 2;
 };
 
 template <int D, int RT, int TG, int KT, int NST, bool FUSED, bool FP8, bool SHARED>
@@ -786,7 +786,12 @@ static int launch_attn_mma_t(const AttnArgs& a, cudaStream_t stream) {
   // twice as many keep the same bytes in flight per SM
   constexpr int NS = FP8 ? 8 : 4;
   if (a.d == 64) {
-    if (rt_needed <= 1) return launch_cfg<64, 1, 4, 64, NS, FUSED, FP8, SHARED>(a, stream);
+    if constexpr (SHARED) {
+      if (rt_needed <= 1)
+        return launch_cfg<64, 1, 3, 64, FP8 ? 6 : 3, FUSED, FP8, SHARED>(a, stream);
+    } else {
+      if (rt_needed <= 1) return launch_cfg<64, 1, 4, 64, NS, FUSED, FP8, SHARED>(a, stream);
+    }
     if (rt_needed <= 2) return launch_cfg<64, 2, 2, 64, NS, FUSED, FP8, SHARED>(a, stream);
     if (rt_needed <= 3) return launch_cfg<64, 3, 2, 64, NS, FUSED, FP8, SHARED>(a, stream);
     return launch_cfg<64, 4, 2, 64, NS, FUSED, FP8, SHARED>(a, stream);

@@ -72,8 +72,8 @@ struct PxCfg {
   static constexpr int NT = 2;
   static constexpr int NSUB = D / 64;
   static constexpr int KT = D == 64 ? 96 : (FP8 ? 64 : 128);   // keys per tile
-  static constexpr int NST = D == 64 ? 4 : (FP8 ? 3 : 2);      // K/V stages
-  static constexpr int NSTF = FP8 ? (D == 64 ? 4 : 3) : 0;     // code stages
+  static constexpr int NST = D == 64 ? (FP8 ? 3 : 4) : (FP8 ? 3 : 2);   // K/V stages
+  static constexpr int NSTF = FP8 ? 3 : 0;     // code stages
   static constexpr int NSTF_MOD = FP8 ? NSTF : 1;
   static constexpr int QSUB = 128 * 128;                       // [128 rows][64], 128-byte swizzle
   static constexpr int KVSUB = KT * 128;
@@ -88,12 +88,12 @@ struct PxCfg {
   static constexpr int OFF_BAR = OFF_GRP + (4 * (GRP_CAP + 1) * 4 + 15) / 16 * 16;
   static constexpr int N_BARS = 3 + 2 * NST + 3 * NT + 1 + 2 * NSTF;
   static constexpr int SMEM = 1024 + OFF_BAR + N_BARS * 8 + 64;
-  static constexpr int N_CVT = 4;
+  static constexpr int N_CVT = D == 64 ? 2 : 4;
   static constexpr int W_CVT = 2 + 4 * NT;                     // first converter warp
   static constexpr int THREADS = (2 + 4 * NT + (FP8 ? N_CVT : 0)) * 32;
   // registers: 10 warps put 3 on two SM sub-partitions (168 a thread), 14
   // warps put 4 there (128, bounded by a 512-thread launch)
-  static constexpr int LB_THREADS = FP8 ? 512 : 320;
+  static constexpr int LB_THREADS = FP8 || D == 64 ? 512 : 320;
   static constexpr uint32_t TMEM_COLS = 512;
   __host__ __device__ static constexpr uint32_t col_s(int t) { return static_cast<uint32_t>(KT * t); }
   __host__ __device__ static constexpr uint32_t col_o(int t) {
