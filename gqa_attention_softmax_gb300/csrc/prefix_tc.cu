@@ -32,9 +32,15 @@
 // converted once per row block, not once per sequence. The key scale joins
 // the logit scale, the value scale the written accumulator.
 //
-// The running maximum is exact, so a row's largest weight is exactly 1 and
-// the others are rounded by at most half a step of bf16 (f16) for P V; the
-// row sum is kept in fp32 from the unrounded weights. Every wait is bounded.
+// Weights are taken relative to a reference maximum that lies at most 2^8
+// below the true one; each is rounded by at most half a step of bf16 (f16) for
+// P V, and the row sum is kept in fp32 from the unrounded weights. Every wait
+// is bounded.
+//
+// At d 64 (and with codes) each row tile has two S buffers: the issuer sends
+// the next S while the softmax of the present one runs, so that a step is the
+// softmax warps' 1.4k cycles and not also P V, S and their latencies (2.8k
+// cycles with one buffer, which is what TMEM leaves at d 128).
 #include <algorithm>
 
 #include "common.cuh"
@@ -72,6 +78,7 @@ struct PxCfg {
   static constexpr int NT = 2;
   static constexpr int NSUB = D / 64;
   static constexpr int KT = D == 64 ? 96 : (FP8 ? 64 : 128);   // keys per tile
+  static constexpr int NSB = D == 64 || FP8 ? 2 : 1;           // S buffers per row tile (TMEM)
   static constexpr int NST = D == 64 ? (FP8 ? 3 : 4) : (FP8 ? 3 : 2);   // K/V stages
   static constexpr int NSTF = FP8 ? 3 : 0;     // code stages
   static constexpr int NSTF_MOD = FP8 ? NSTF : 1;
@@ -85,8 +92,10 @@ struct PxCfg {
   static constexpr int OFF_CODE = OFF_KV + NST * STAGE;
   static constexpr int GRP_CAP = 512;                          // groups staged in shared memory
   static constexpr int OFF_GRP = OFF_CODE + NSTF * CODE_STAGE;
-  static constexpr int OFF_BAR = OFF_GRP + (4 * (GRP_CAP + 1) * 4 + 15) / 16 * 16;
-  static constexpr int N_BARS = 3 + 2 * NST + 3 * NT + 1 + 2 * NSTF;
+  static constexpr int NIT = 4;                                // items in the ring
+  static constexpr int OFF_ITEM = OFF_GRP + (4 * (GRP_CAP + 1) * 4 + 15) / 16 * 16;
+  static constexpr int OFF_BAR = OFF_ITEM + NIT * 48;
+  static constexpr int N_BARS = 3 + 2 * NST + (2 * NSB + 1) * NT + 1 + 2 * NSTF + 2 * NIT;
   static constexpr int SMEM = 1024 + OFF_BAR + N_BARS * 8 + 64;
   static constexpr int N_CVT = D == 64 ? 2 : 4;
   static constexpr int W_CVT = 2 + 4 * NT;                     // first converter warp
@@ -95,20 +104,24 @@ struct PxCfg {
   // warps put 4 there (128, bounded by a 512-thread launch)
   static constexpr int LB_THREADS = FP8 || D == 64 ? 512 : 320;
   static constexpr uint32_t TMEM_COLS = 512;
-  __host__ __device__ static constexpr uint32_t col_s(int t) { return static_cast<uint32_t>(KT * t); }
-  __host__ __device__ static constexpr uint32_t col_o(int t) {
-    return static_cast<uint32_t>(KT * NT + D * t);
+  __host__ __device__ static constexpr uint32_t col_s(int t, int buf) {
+    return static_cast<uint32_t>(KT * (NSB * t + buf));
   }
-  static_assert(NT * (KT + D) <= 512, "TMEM budget");
+  __host__ __device__ static constexpr uint32_t col_o(int t) {
+    return static_cast<uint32_t>(KT * NSB * NT + D * t);
+  }
+  static_assert(NT * (NSB * KT + D) <= 512, "TMEM budget");
   static_assert(KVSUB % 1024 == 0 && KT % 32 == 0, "tile shape");
   // one block per SM, so the 512-column TMEM allocation always succeeds
   static_assert(SMEM <= 232448 && 2 * (SMEM + 1024) > 233472, "one block per SM");
 };
 
 struct PxItem {
-  int kvh, slot, tok0, nq, tiles, keys, first, n, list0, pages;
-  int next;    // the unit behind the item
-  bool last;   // the item ends its row block's keys
+  int kvh, slot, tok0, nq, tiles, keys, first;
+  int n;       // K/V tiles; -1: no more items
+  int list0, pages;
+  int last;    // the item ends its row block's keys
+  int pad;
 };
 
 // The group with gu[g] <= u < gu[g + 1].
@@ -122,55 +135,104 @@ __device__ __forceinline__ int px_group(const int32_t* gu, int groups, int u) {
   return lo;
 }
 
-// The start of the first row block at or behind unit u (one partial per row:
-// row blocks are not cut).
-template <int KT>
-__device__ __forceinline__ int px_whole(const PxParams& p, const int32_t* gk, const int32_t* gu,
-                                        int u, int all) {
-  if (u >= all) return all;
-  const int g = px_group(gu, p.groups, u);
-  const int T = (gk[g + 1] - gk[g] + KT - 1) / KT;
-  return gu[g] + (u - gu[g] + T - 1) / T * T;
-}
-
-// The item that starts at unit u, of a thread block whose units end at `end`.
-// Row blocks of the same keys are neighbours in the order and find them in
-// L2. Whole warp: with a window the keys before the block's earliest visible
-// one are left out, which takes a minimum over its tokens.
+// Walks a thread block's units item by item: (group, KV head, row block),
+// neighbouring row blocks of the same keys finding them in L2. The producer
+// warp walks and hands the items to the other warps through a ring in shared
+// memory, which keeps the walk's registers out of theirs.
 template <int KT, int NT>
-__device__ __forceinline__ PxItem px_item(const PxParams& p, const int32_t* gq, const int32_t* gk,
-                                          const int32_t* gp, const int32_t* gu, int u, int end,
-                                          int quota, int lane) {
-  PxItem t;
-  const int g = px_group(gu, p.groups, u);
-  t.keys = gk[g + 1] - gk[g];
-  t.list0 = gp[g];
-  t.pages = gp[g + 1] - gp[g];
-  const int T = (t.keys + KT - 1) / KT;
-  const int toks = gq[g + 1] - gq[g];
-  const int blocks = (toks + NT * p.QB - 1) / (NT * p.QB);
-  const int pair = (u - gu[g]) / T;
-  const int start = gu[g] + pair * T;     // the row block's first unit
-  t.kvh = pair / blocks;
-  const int at = (pair - t.kvh * blocks) * NT * p.QB;
-  t.tok0 = gq[g] + at;
-  t.nq = min(NT * p.QB, toks - at);
-  t.tiles = (t.nq + p.QB - 1) / p.QB;
-  t.next = min(end, start + T);
-  t.last = t.next == start + T;
-  t.slot = p.splits > 1 ? u / quota - start / quota : 0;
-  int t0 = u - start;
-  const int t1 = t.next - start;
-  if (p.window > 0) {
-    int pos = INT32_MAX;
-    for (int i = lane; i < t.nq; i += 32) pos = min(pos, p.row_pos[t.tok0 + i]);
-    pos = __reduce_min_sync(0xffffffffu, pos);
-    t0 = min(max(t0, max(0, pos - p.window + 1) / KT), t1);
+struct PxCursor {
+  const int32_t *gq, *gk, *gp, *gu;
+  int u, end;                       // next unit, and the block's last but one
+  int g, kvh, blk, t0, slot;        // where u is
+  int T, blocks, keys, tok, toks;   // of group g
+
+  __device__ __forceinline__ void group(const PxParams& p) {
+    keys = gk[g + 1] - gk[g];
+    T = (keys + KT - 1) / KT;
+    tok = gq[g];
+    toks = gq[g + 1] - tok;
+    blocks = (toks + NT * p.QB - 1) / (NT * p.QB);
   }
-  t.first = t0 * KT;
-  t.n = t1 - t0;
-  return t;
-}
+
+  // This thread block's run of units. One partial per row: row blocks are not
+  // cut, a run starts and ends at the next row block's first unit.
+  __device__ __forceinline__ void start(const PxParams& p, const int32_t* gq_, const int32_t* gk_,
+                                        const int32_t* gp_, const int32_t* gu_) {
+    gq = gq_;
+    gk = gk_;
+    gp = gp_;
+    gu = gu_;
+    const int all = gu[p.groups];
+    const int quota = max((all + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x),
+                          p.quota_min);
+    const long long from = static_cast<long long>(blockIdx.x) * quota;
+    u = static_cast<int>(min(from, static_cast<long long>(all)));
+    end = static_cast<int>(min(from + quota, static_cast<long long>(all)));
+    if (p.splits == 1) {
+      u = whole(p, u, all);
+      end = whole(p, end, all);
+    }
+    if (u >= end) return;
+    g = px_group(gu, p.groups, u);
+    group(p);
+    const int pair = (u - gu[g]) / T;
+    t0 = u - gu[g] - pair * T;
+    kvh = pair / blocks;
+    blk = pair - kvh * blocks;
+    slot = p.splits > 1 ? static_cast<int>(blockIdx.x) - (u - t0) / quota : 0;
+  }
+
+  __device__ __forceinline__ int whole(const PxParams& p, int v, int all) const {
+    if (v >= all) return all;
+    const int h = px_group(gu, p.groups, v);
+    const int n = (gk[h + 1] - gk[h] + KT - 1) / KT;
+    return gu[h] + (v - gu[h] + n - 1) / n * n;
+  }
+
+  __device__ __forceinline__ bool more() const { return u < end; }
+
+  // The item at u, and on to the next. Whole warp: with a window the keys
+  // before the block's earliest visible one are left out, which takes a
+  // minimum over its tokens.
+  __device__ __forceinline__ PxItem next(const PxParams& p, int lane) {
+    PxItem t;
+    t.kvh = kvh;
+    t.slot = slot;
+    const int at = blk * NT * p.QB;
+    t.tok0 = tok + at;
+    t.nq = min(NT * p.QB, toks - at);
+    t.tiles = t.nq > p.QB ? 2 : 1;
+    t.keys = keys;
+    t.list0 = gp[g];
+    t.pages = gp[g + 1] - t.list0;
+    int from = t0;
+    const int to = min(T, t0 + end - u);
+    t.last = to == T;
+    u += to - t0;
+    if (p.window > 0) {
+      int pos = INT32_MAX;
+      for (int i = lane; i < t.nq; i += 32) pos = min(pos, p.row_pos[t.tok0 + i]);
+      pos = __reduce_min_sync(0xffffffffu, pos);
+      from = min(max(from, max(0, pos - p.window + 1) / KT), to);
+    }
+    t.first = from * KT;
+    t.n = to - from;
+    t0 = 0;   // (only a block's last item ends inside a row block)
+    slot = 0;
+    if (++blk == blocks) {
+      blk = 0;
+      if (++kvh == p.Hkv) {
+        kvh = 0;
+        if (u < end) {
+          do ++g;
+          while (gu[g + 1] == gu[g]);
+          group(p);
+        }
+      }
+    }
+    return t;
+  }
+};
 
 // A tile row's accumulator from TMEM to its fp32 partial row, 32 columns at a
 // time: the eight 16-byte pieces of a lane's row are transposed within groups
@@ -181,6 +243,10 @@ __device__ __forceinline__ void store_partial(uint32_t o_addr, float scale, floa
                                               int lane) {
   const int i = lane & 7;
   const unsigned long long mine = valid ? reinterpret_cast<unsigned long long>(row) : 0ull;
+  float* to[8];   // the rows of the lane's group of eight
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    to[e] = reinterpret_cast<float*>(__shfl_sync(0xffffffffu, mine, (lane & ~7) + e));
 #pragma unroll
   for (int blk = 0; blk < D / 32; ++blk) {
     float o[32];
@@ -193,10 +259,8 @@ __device__ __forceinline__ void store_partial(uint32_t o_addr, float scale, floa
                           o[4 * e + 3] * scale);
     transpose8_chunks(ch, lane);   // ch[e] of lane i: piece i of the group's row e
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const unsigned long long to = __shfl_sync(0xffffffffu, mine, (lane & ~7) + e);
-      if (to) *reinterpret_cast<float4*>(reinterpret_cast<float*>(to) + blk * 32 + i * 4) = ch[e];
-    }
+    for (int e = 0; e < 8; ++e)
+      if (to[e]) *reinterpret_cast<float4*>(to[e] + blk * 32 + i * 4) = ch[e];
   }
 }
 
@@ -206,7 +270,7 @@ __global__ void __launch_bounds__(PxCfg<D, FP8>::LB_THREADS, 1)
                      const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const PxParams p) {
   using C = PxCfg<D, FP8>;
-  constexpr int KT = C::KT, NST = C::NST, NT = C::NT;
+  constexpr int KT = C::KT, NST = C::NST, NT = C::NT, NSB = C::NSB;
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -216,13 +280,17 @@ __global__ void __launch_bounds__(PxCfg<D, FP8>::LB_THREADS, 1)
   uint64_t* q_cvt = q_empty + 1;        // FP8: Q is f16
   uint64_t* kv_full = q_cvt + 1;        // [NST] by K/V tile
   uint64_t* kv_empty = kv_full + NST;
-  uint64_t* s_full = kv_empty + NST;    // [NT] by the tile's own steps
-  uint64_t* p_full = s_full + NT;       // [NT] P_t written and O_t rescaled (128 arrivals)
-  uint64_t* pv_done = p_full + NT;      // [NT]
+  uint64_t* s_full = kv_empty + NST;    // [NT][NSB] by the row tile's own steps
+  uint64_t* p_full = s_full + NT * NSB; // [NT][NSB] P_t written and O_t rescaled (128 arrivals)
+  uint64_t* pv_done = p_full + NT * NSB;   // [NT]
   uint64_t* drain = pv_done + NT;
   uint64_t* c_full = drain + 1;         // FP8: [NSTF] codes landed
   uint64_t* c_empty = c_full + C::NSTF;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(c_empty + C::NSTF);
+  uint64_t* i_full = c_empty + C::NSTF; // [NIT] item written
+  uint64_t* i_empty = i_full + C::NIT;  // [NIT] every other warp is done with it
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(i_empty + C::NIT);
+  PxItem* items = reinterpret_cast<PxItem*>(smem + C::OFF_ITEM);
+  static_assert(sizeof(PxItem) == 48, "ring of items");
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
   int* status = &g_status_prefix_tc;
 
@@ -237,15 +305,19 @@ __global__ void __launch_bounds__(PxCfg<D, FP8>::LB_THREADS, 1)
       mbar_init(&kv_full[i], FP8 ? C::N_CVT : 1);
       mbar_init(&kv_empty[i], 1);
     }
-    for (int t = 0; t < NT; ++t) {
+    for (int t = 0; t < NT * NSB; ++t) {
       mbar_init(&s_full[t], 1);
       mbar_init(&p_full[t], 128);
-      mbar_init(&pv_done[t], 1);
     }
+    for (int t = 0; t < NT; ++t) mbar_init(&pv_done[t], 1);
     mbar_init(drain, 1);
     for (int i = 0; i < C::NSTF; ++i) {
       mbar_init(&c_full[i], 1);
       mbar_init(&c_empty[i], C::N_CVT);
+    }
+    for (int i = 0; i < C::NIT; ++i) {
+      mbar_init(&i_full[i], 1);
+      mbar_init(&i_empty[i], C::THREADS / 32 - 1);
     }
     *abort_flag = 0;
     fence_barrier_init();
@@ -281,20 +353,15 @@ __global__ void __launch_bounds__(PxCfg<D, FP8>::LB_THREADS, 1)
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  // this block's units [u0, u1)
-  const int all = gu[p.groups];
-  const int quota = max((all + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x),
-                        p.quota_min);
-  int u0 = static_cast<int>(min(static_cast<long long>(blockIdx.x) * quota, static_cast<long long>(all)));
-  int u1 = static_cast<int>(min(static_cast<long long>(u0) + quota, static_cast<long long>(all)));
-  if (p.splits == 1) {
-    u0 = px_whole<KT>(p, gk, gu, u0, all);
-    u1 = px_whole<KT>(p, gk, gu, u1, all);
-  }
-  auto item = [&](int u) { return px_item<KT, NT>(p, gq, gk, gp, gu, u, u1, quota, lane); };
   // A wait that gives up in any lane makes the whole warp leave its loop.
   auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status));
+  };
+  // Item number k of the ring; its n is -1 behind the last one.
+  auto item_wait = [&](int k) -> bool { return wwait(&i_full[k % C::NIT], (k / C::NIT) & 1); };
+  auto item_done = [&](int k) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&i_empty[k % C::NIT]);
   };
   int g_prod = 0, qi_prod = 0;   // producer: K/V tiles and Q loads issued
 
@@ -307,11 +374,24 @@ __global__ void __launch_bounds__(PxCfg<D, FP8>::LB_THREADS, 1)
     const int skip_tile = hook_skip_tile();
     int g = 0, qi = 0;
     bool ok = true;
-    for (int u = u0; ok && u < u1;) {
-      const PxItem t = item(u);
-      u = t.next;
+    PxCursor<KT, NT> cur;
+    cur.start(p, gq, gk, gp, gu);
+    for (int k = 0; ok; ++k) {
+      PxItem t{};
+      const bool more = cur.more();
+      if (more) t = cur.next(p, lane);
+      else t.n = -1;
+      if (!wwait(&i_empty[k % C::NIT], ((k / C::NIT) & 1) ^ 1)) break;
+      if (leader) {
+        items[k % C::NIT] = t;
+        mbar_arrive(&i_full[k % C::NIT]);
+      }
+      __syncwarp();
+      if (!more) break;
       if (leader && t.keys > t.pages * p.page_size) atomicExch(status, SINKATTN_BAD_LENGTHS);
       if (t.n == 0) continue;
+      PageCursor pc;   // (its loads are in flight while Q's turn comes)
+      pc.start(p.page_indices + t.list0, t.pages, t.first / p.page_size, lane);
       if (qi > 0 && !wwait(q_empty, (qi - 1) & 1)) break;
       if (leader) {
         mbar_arrive_expect_tx(q_full, q_bytes * t.tiles);
@@ -322,8 +402,6 @@ __global__ void __launch_bounds__(PxCfg<D, FP8>::LB_THREADS, 1)
                             t.tok0 + tt * p.QB, q_full);
       }
       ++qi;
-      PageCursor pc;
-      pc.start(p.page_indices + t.list0, t.pages, t.first / p.page_size, lane);
       for (int j = 0; j < t.n; ++j, ++g) {
         const int st = g % (FP8 ? C::NSTF_MOD : NST);
         uint64_t* full = FP8 ? &c_full[st] : &kv_full[st];
@@ -375,51 +453,55 @@ __global__ void __launch_bounds__(PxCfg<D, FP8>::LB_THREADS, 1)
       if (leader) tc::commit(bar);
       __syncwarp();
     };
-    auto issue_s = [&](int t, int g) {
+    // S_t of K/V tile g into buffer b of the row tile
+    auto issue_s = [&](int t, int b, int g) {
       const uint64_t kd = kd0 + static_cast<uint64_t>(g % NST) * STAGE16;
       const uint64_t qd = qd0 + static_cast<uint64_t>(t) * (C::Q_TILE >> 4);
+      const uint32_t d_tm = tmem + C::col_s(t, 0) + static_cast<uint32_t>(b * KT);
       if (leader) {
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint64_t s = static_cast<uint64_t>(kk & 3) * 2;
-          tc::mma_ss(tmem + C::col_s(t), qd + static_cast<uint64_t>(kk >> 2) * QSUB16 + s,
+          tc::mma_ss(d_tm, qd + static_cast<uint64_t>(kk >> 2) * QSUB16 + s,
                      kd + static_cast<uint64_t>(kk >> 2) * KVSUB16 + s, idesc_s, kk > 0 ? 1u : 0u);
         }
-        tc::commit(&s_full[t]);
+        tc::commit(&s_full[t * NSB + b]);
       }
       __syncwarp();
     };
-    auto issue_pv = [&](int t, int g, bool first) {
+    auto issue_pv = [&](int t, int b, int g, bool first) {
       const uint64_t vd = vd0 + static_cast<uint64_t>(g % NST) * STAGE16;
+      const uint32_t a_tm = tmem + C::col_s(t, 0) + static_cast<uint32_t>(b * KT);
       if (leader) {
 #pragma unroll
         for (int kk = 0; kk < KT / 16; ++kk)
-          tc::mma_ts(tmem + C::col_o(t), tmem + C::col_s(t) + kk * 8,
-                     vd + static_cast<uint64_t>(kk) * 128u, idesc_o, (!first || kk > 0) ? 1u : 0u);
+          tc::mma_ts(tmem + C::col_o(t), a_tm + kk * 8, vd + static_cast<uint64_t>(kk) * 128u,
+                     idesc_o, (!first || kk > 0) ? 1u : 0u);
         tc::commit(&pv_done[t]);
       }
       __syncwarp();
     };
     int g = 0, qi = 0;
-    int steps[NT];   // steps of each tile so far: the phase of its barriers
+    int steps[NT];   // P V steps of each row tile so far: buffers and phases go by it
 #pragma unroll
     for (int tt = 0; tt < NT; ++tt) steps[tt] = 0;
+    // all P V up to step s - 1 of the row tile have completed
+    auto pv_before = [&](int tt, int s) -> bool {
+      return s <= 0 || wwait(&pv_done[tt], (s - 1) & 1);
+    };
     bool ok = true;
-    for (int u = u0; ok && u < u1;) {
-      const PxItem t = item(u);
-      u = t.next;
+    for (int k = 0; ok && item_wait(k); ++k) {
+      struct { int n, tiles; } t{items[k % C::NIT].n, items[k % C::NIT].tiles};
+      item_done(k);
+      if (t.n < 0) break;
       if (t.n == 0) continue;
-      // S_t of the first K/V tile for every row tile, then per K/V tile and
-      // row tile: PV_t, then the next S_t into the same buffer once that
-      // PV_t has completed (S overwrites P).
       ok = wwait(FP8 ? q_cvt : q_full, qi & 1) && wwait(&kv_full[g % NST], (g / NST) & 1);
 #pragma unroll
       for (int tt = 0; tt < NT; ++tt) {
         if (!ok || tt >= t.tiles) break;
-        // the previous item's last PV of this tile has completed
-        if (steps[tt] > 0 && !wwait(&pv_done[tt], (steps[tt] - 1) & 1)) { ok = false; break; }
+        if (!pv_before(tt, steps[tt])) { ok = false; break; }
         tc::fence_after_sync();
-        issue_s(tt, g);
+        issue_s(tt, steps[tt] % NSB, g);
       }
       if (!ok) break;
       if (t.n == 1) commit1(q_empty);
@@ -428,17 +510,25 @@ __global__ void __launch_bounds__(PxCfg<D, FP8>::LB_THREADS, 1)
 #pragma unroll
         for (int tt = 0; tt < NT; ++tt) {
           if (tt >= t.tiles) break;
-          if (!wwait(&p_full[tt], steps[tt] & 1)) { ok = false; break; }
-          tc::fence_after_sync();
-          issue_pv(tt, gg, j == 0);
-          if (tt == t.tiles - 1) commit1(&kv_empty[gg % NST]);
-          if (j + 1 < t.n) {
-            if (tt == 0 && !wwait(&kv_full[(gg + 1) % NST], ((gg + 1) / NST) & 1)) { ok = false; break; }
-            if (!wwait(&pv_done[tt], steps[tt] & 1)) { ok = false; break; }
+          const int b = steps[tt] % NSB;
+          // the next K/V tile's S: with two buffers before this step's P is
+          // there (it goes where the step before left its P), else after its
+          // P V, which reads P from the one buffer
+          auto ahead = [&]() -> bool {
+            if (j + 1 >= t.n) return true;
+            if (tt == 0 && !wwait(&kv_full[(gg + 1) % NST], ((gg + 1) / NST) & 1)) return false;
+            if (!pv_before(tt, NSB == 2 ? steps[tt] : steps[tt] + 1)) return false;
             tc::fence_after_sync();
-            issue_s(tt, gg + 1);
+            issue_s(tt, (steps[tt] + 1) % NSB, gg + 1);
             if (j + 2 == t.n && tt == t.tiles - 1) commit1(q_empty);
-          }
+            return true;
+          };
+          if (NSB == 2 && !ahead()) { ok = false; break; }
+          if (!wwait(&p_full[tt * NSB + b], (steps[tt] / NSB) & 1)) { ok = false; break; }
+          tc::fence_after_sync();
+          issue_pv(tt, b, gg, j == 0);
+          if (tt == t.tiles - 1) commit1(&kv_empty[gg % NST]);
+          if (NSB == 1 && !ahead()) { ok = false; break; }
           ++steps[tt];
         }
       }
@@ -459,9 +549,10 @@ __global__ void __launch_bounds__(PxCfg<D, FP8>::LB_THREADS, 1)
     const int ct = static_cast<int>(threadIdx.x) - C::W_CVT * 32;
     int g = 0, qi = 0;
     bool ok = true;
-    for (int u = u0; ok && u < u1;) {
-      const PxItem t = item(u);
-      u = t.next;
+    for (int k = 0; ok && item_wait(k); ++k) {
+      struct { int n, tiles; } t{items[k % C::NIT].n, items[k % C::NIT].tiles};
+      item_done(k);
+      if (t.n < 0) break;
       if (t.n == 0) continue;
       if (!wwait(q_full, qi & 1)) break;
       for (int c = ct; c < t.tiles * C::Q_TILE / 16; c += N) {
@@ -523,27 +614,32 @@ __global__ void __launch_bounds__(PxCfg<D, FP8>::LB_THREADS, 1)
     const int hig = row - rg * G;    // head within the group
     const int tl = tt * p.QB + rg;   // token within the block
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    const uint32_t s_addr = lane_base + C::col_s(tt);
+    const uint32_t s_addr0 = lane_base + C::col_s(tt, 0);
     const uint32_t o_addr = lane_base + C::col_o(tt);
     constexpr int NCH = KT / 32;     // 32-column pieces of a score row
     int steps = 0;
     bool ok = true;
-    for (int u = u0; ok && u < u1;) {
-      const PxItem t = item(u);
-      u = t.next;
-      if (tt >= t.tiles) continue;
+    for (int k = 0; ok && item_wait(k); ++k) {
+      const PxItem& t = items[k % C::NIT];   // (shared memory: read where needed)
+      const int n = t.n;
+      if (n < 0 || tt >= t.tiles) {
+        item_done(k);
+        if (n < 0) break;
+        continue;
+      }
       const bool valid = rg < p.QB && tl < t.nq;
       const float kscale = FP8 ? p.k_scale[t.kvh] : 1.f;
       const float c2 = p.scale_log2 * kscale;   // raw logits -> base-2 exponents
       int lo_r = 0;
       if (p.window > 0 && valid) lo_r = max(0, p.row_pos[t.tok0 + tl] - p.window + 1);
-      const int hi_r = t.keys - 1;
+      // the row's first and last visible key, from the first column of the tile
+      int clo = lo_r - t.first, chi = t.keys - 1 - t.first;
       float m_used = kNegInf, l = 0.f;
-      for (int j = 0; j < t.n; ++j, ++steps) {
-        if (!wwait(&s_full[tt], steps & 1)) { ok = false; break; }
+      for (int j = 0; j < n; ++j, ++steps, clo -= KT, chi -= KT) {
+        const int b = steps % NSB;
+        if (!wwait(&s_full[tt * NSB + b], (steps / NSB) & 1)) { ok = false; break; }
         tc::fence_after_sync();
-        const int j0 = t.first + j * KT;
-        const int clo = lo_r - j0, chi = hi_r - j0;
+        const uint32_t s_addr = s_addr0 + static_cast<uint32_t>(b * KT);
         float v[NCH][32];
 #pragma unroll
         for (int c = 0; c < NCH; ++c) tc::tmem_ld32(s_addr + 32 * c, v[c]);
@@ -575,9 +671,12 @@ __global__ void __launch_bounds__(PxCfg<D, FP8>::LB_THREADS, 1)
         for (int i = 3; i < 2 * NCH; i += 2)
           mx = (i + 1 < 2 * NCH) ? fmax3(mx, mxc[i], mxc[i + 1]) : fmaxf(mx, mxc[i]);
 
+        // the reference moves only when the maximum is past it by more than
+        // 2^8, or O_t, which the tensor core holds, would be rescaled in
+        // almost every step by one row or another of the warp
         float alpha = 1.f;
         bool rescale = false;
-        if (mx > m_used) {
+        if (m_used == kNegInf ? mx > m_used : (mx - m_used) * c2 > 8.f) {
           alpha = (m_used == kNegInf) ? 0.f : ex2((m_used - mx) * c2);
           m_used = mx;
           rescale = true;
@@ -607,10 +706,11 @@ __global__ void __launch_bounds__(PxCfg<D, FP8>::LB_THREADS, 1)
           }
         const float2 rsa = __fadd2_rn(__fadd2_rn(rs2[0], rs2[1]), __fadd2_rn(rs2[2], rs2[3]));
 
-        // S_t was issued after the tile's previous PV_t had completed, so O_t
-        // is free to touch. Rescale it when some row of this warp moved its
-        // maximum (warp-uniform branch).
+        // Rescale O_t when some row of this warp moved its reference
+        // (warp-uniform branch), once the previous step's PV_t has completed.
         if (j >= 1 && __any_sync(0xffffffffu, rescale)) {
+          if (!wwait(&pv_done[tt], (steps - 1) & 1)) { ok = false; break; }
+          tc::fence_after_sync();
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
             float o[32];
@@ -624,19 +724,19 @@ __global__ void __launch_bounds__(PxCfg<D, FP8>::LB_THREADS, 1)
         tc::tmem_wait_st();
         l = l * alpha + (rsa.x + rsa.y);
         tc::fence_before_sync();
-        mbar_arrive(&p_full[tt]);
+        mbar_arrive(&p_full[tt * NSB + b]);
       }
       if (!ok) break;
       // O_t is read out before this thread hands over P of the next item, so
       // the next item's first PV (which overwrites O_t) comes after it.
-      if (t.n >= 1) {
+      if (n >= 1) {
         if (!wwait(&pv_done[tt], (steps - 1) & 1)) { ok = false; break; }
         tc::fence_after_sync();
       }
       const bool some = l > 0.f;   // the row sees a key of the chunk
       const size_t slot =
           (static_cast<size_t>(t.tok0 + tl) * p.Hq + t.kvh * G + hig) * p.part_slots + t.slot;
-      if (t.n >= 1)
+      if (n >= 1)
         store_partial<D>(o_addr, FP8 ? p.v_scale[t.kvh] : 1.f, p.part_acc + slot * D, valid, lane);
       tc::fence_before_sync();
       if (valid) {
@@ -645,6 +745,7 @@ __global__ void __launch_bounds__(PxCfg<D, FP8>::LB_THREADS, 1)
         if (t.last)   // the partials that no block writes
           for (int s = t.slot + 1; s < p.splits; ++s) md[s - t.slot] = make_float2(kNegInf, 0.f);
       }
+      item_done(k);
     }
     // rows of groups without a prefix: no block has units of theirs. All
     // blocks share the rows of each group, or with many groups the groups.
