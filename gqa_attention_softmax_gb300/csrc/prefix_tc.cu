@@ -12,8 +12,8 @@
 //
 // With hundreds of rows per KV head the prefix is compute-bound (4 d
 // operations per row and key against 4 d / rows bytes), so the kernel follows
-// the persistent prefill: one block per SM, a TMA producer warp, an MMA
-// issuer warp, and per tile four softmax warps, one thread per row. Two tiles
+// the persistent prefill: one block per SM, a TMA producer warp, MMA issuer
+// warps, and per tile four softmax warps, one thread per row. Two tiles
 // per block (three would not divide 512 rows, the gpt-oss-shaped batch of 64
 // sequences, and TMEM holds no more at d 128); the tiles' chains S -> softmax
 // -> P V interleave on the tensor core. A tile whose rows all lie behind the
@@ -37,10 +37,11 @@
 // P V, and the row sum is kept in fp32 from the unrounded weights. Every wait
 // is bounded.
 //
-// At d 64 (and with codes) each row tile has two S buffers: the issuer sends
-// the next S while the softmax of the present one runs, so that a step is the
-// softmax warps' 1.4k cycles and not also P V, S and their latencies (2.8k
-// cycles with one buffer, which is what TMEM leaves at d 128).
+// At d 64 (and with codes) each row tile has two S buffers and an issuer of
+// its own, which sends the next S while the softmax of the present one runs.
+// A step of 96 keys took 2.8k cycles with one buffer (softmax 1.4k, then P V,
+// S and their latencies; what TMEM leaves at d 128), 2.25k with two and one
+// issuer.
 #include <algorithm>
 
 #include "common.cuh"
@@ -95,13 +96,17 @@ struct PxCfg {
   static constexpr int NIT = 4;                                // items in the ring
   static constexpr int OFF_ITEM = OFF_GRP + (4 * (GRP_CAP + 1) * 4 + 15) / 16 * 16;
   static constexpr int OFF_BAR = OFF_ITEM + NIT * 48;
-  static constexpr int N_BARS = 3 + 2 * NST + (2 * NSB + 1) * NT + 1 + 2 * NSTF + 2 * NIT;
+  // MMA issuers: with two S buffers a step is bound by the issue of its MMAs,
+  // about 1.0k cycles per row tile with their waits, so each tile has its own
+  static constexpr int NI = NSB == 2 ? NT : 1;
+  static constexpr int N_BARS = 3 + 2 * NST + (2 * NSB + 1) * NT + NI + 2 * NSTF + 2 * NIT;
   static constexpr int SMEM = 1024 + OFF_BAR + N_BARS * 8 + 64;
+  static constexpr int W_MMA1 = 2 + 4 * NT;                    // the second tile's issuer
   static constexpr int N_CVT = D == 64 ? 2 : 4;
-  static constexpr int W_CVT = 2 + 4 * NT;                     // first converter warp
-  static constexpr int THREADS = (2 + 4 * NT + (FP8 ? N_CVT : 0)) * 32;
-  // registers: 10 warps put 3 on two SM sub-partitions (168 a thread), 14
-  // warps put 4 there (128, bounded by a 512-thread launch)
+  static constexpr int W_CVT = W_MMA1 + NI - 1;                // first converter warp
+  static constexpr int THREADS = (W_CVT + (FP8 ? N_CVT : 0)) * 32;
+  // registers: 10 warps put 3 on two SM sub-partitions (168 a thread), 13
+  // warps and more put 4 on one (128, bounded by a 512-thread launch)
   static constexpr int LB_THREADS = FP8 || D == 64 ? 512 : 320;
   static constexpr uint32_t TMEM_COLS = 512;
   __host__ __device__ static constexpr uint32_t col_s(int t, int buf) {
@@ -283,8 +288,8 @@ __global__ void __launch_bounds__(PxCfg<D, FP8>::LB_THREADS, 1)
   uint64_t* s_full = kv_empty + NST;    // [NT][NSB] by the row tile's own steps
   uint64_t* p_full = s_full + NT * NSB; // [NT][NSB] P_t written and O_t rescaled (128 arrivals)
   uint64_t* pv_done = p_full + NT * NSB;   // [NT]
-  uint64_t* drain = pv_done + NT;
-  uint64_t* c_full = drain + 1;         // FP8: [NSTF] codes landed
+  uint64_t* drain = pv_done + NT;       // [NI]
+  uint64_t* c_full = drain + C::NI;     // FP8: [NSTF] codes landed
   uint64_t* c_empty = c_full + C::NSTF;
   uint64_t* i_full = c_empty + C::NSTF; // [NIT] item written
   uint64_t* i_empty = i_full + C::NIT;  // [NIT] every other warp is done with it
@@ -299,18 +304,18 @@ __global__ void __launch_bounds__(PxCfg<D, FP8>::LB_THREADS, 1)
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
+    mbar_init(q_empty, C::NI);
     mbar_init(q_cvt, C::N_CVT);
     for (int i = 0; i < NST; ++i) {
       mbar_init(&kv_full[i], FP8 ? C::N_CVT : 1);
-      mbar_init(&kv_empty[i], 1);
+      mbar_init(&kv_empty[i], C::NI);
     }
     for (int t = 0; t < NT * NSB; ++t) {
       mbar_init(&s_full[t], 1);
       mbar_init(&p_full[t], 128);
     }
     for (int t = 0; t < NT; ++t) mbar_init(&pv_done[t], 1);
-    mbar_init(drain, 1);
+    for (int i = 0; i < C::NI; ++i) mbar_init(&drain[i], 1);
     for (int i = 0; i < C::NSTF; ++i) {
       mbar_init(&c_full[i], 1);
       mbar_init(&c_empty[i], C::N_CVT);
@@ -436,9 +441,11 @@ __global__ void __launch_bounds__(PxCfg<D, FP8>::LB_THREADS, 1)
     }
     g_prod = g;
     qi_prod = qi;
-  } else if (warp == 1) {
-    // ---------------------------------------------------------------- MMA issuer
-    // The whole warp runs the schedule; one elected lane issues.
+  } else if (warp == 1 || (C::NI == 2 && warp == C::W_MMA1)) {
+    // --------------------------------------------------------------- MMA issuers
+    // The whole warp runs the schedule; one elected lane issues. Issuer i has
+    // row tile i, or the one issuer both.
+    const int me = warp == 1 ? 0 : 1;
     const bool leader = tc::elect_one();
     constexpr uint32_t idesc_s =
         FP8 ? tc::idesc_f16_f32(128, KT, false) : tc::idesc_bf16_f32(128, KT, false);
@@ -457,7 +464,7 @@ __global__ void __launch_bounds__(PxCfg<D, FP8>::LB_THREADS, 1)
     auto issue_s = [&](int t, int b, int g) {
       const uint64_t kd = kd0 + static_cast<uint64_t>(g % NST) * STAGE16;
       const uint64_t qd = qd0 + static_cast<uint64_t>(t) * (C::Q_TILE >> 4);
-      const uint32_t d_tm = tmem + C::col_s(t, 0) + static_cast<uint32_t>(b * KT);
+      const uint32_t d_tm = tmem + C::col_s(0, 0) + static_cast<uint32_t>((t * NSB + b) * KT);
       if (leader) {
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
@@ -471,73 +478,110 @@ __global__ void __launch_bounds__(PxCfg<D, FP8>::LB_THREADS, 1)
     };
     auto issue_pv = [&](int t, int b, int g, bool first) {
       const uint64_t vd = vd0 + static_cast<uint64_t>(g % NST) * STAGE16;
-      const uint32_t a_tm = tmem + C::col_s(t, 0) + static_cast<uint32_t>(b * KT);
+      const uint32_t a_tm = tmem + C::col_s(0, 0) + static_cast<uint32_t>((t * NSB + b) * KT);
+      const uint32_t d_tm = tmem + C::col_o(0) + static_cast<uint32_t>(t * D);
       if (leader) {
 #pragma unroll
         for (int kk = 0; kk < KT / 16; ++kk)
-          tc::mma_ts(tmem + C::col_o(t), a_tm + kk * 8, vd + static_cast<uint64_t>(kk) * 128u,
-                     idesc_o, (!first || kk > 0) ? 1u : 0u);
+          tc::mma_ts(d_tm, a_tm + kk * 8, vd + static_cast<uint64_t>(kk) * 128u, idesc_o,
+                     (!first || kk > 0) ? 1u : 0u);
         tc::commit(&pv_done[t]);
       }
       __syncwarp();
     };
-    int g = 0, qi = 0;
-    int steps[NT];   // P V steps of each row tile so far: buffers and phases go by it
-#pragma unroll
-    for (int tt = 0; tt < NT; ++tt) steps[tt] = 0;
     // all P V up to step s - 1 of the row tile have completed
-    auto pv_before = [&](int tt, int s) -> bool {
-      return s <= 0 || wwait(&pv_done[tt], (s - 1) & 1);
+    auto pv_before = [&](int t, int s) -> bool {
+      return s <= 0 || wwait(&pv_done[t], (s - 1) & 1);
     };
+    auto kv_wait = [&](int g) -> bool { return wwait(&kv_full[g % NST], (g / NST) & 1); };
+    int g = 0, qi = 0;
     bool ok = true;
-    for (int k = 0; ok && item_wait(k); ++k) {
-      struct { int n, tiles; } t{items[k % C::NIT].n, items[k % C::NIT].tiles};
-      item_done(k);
-      if (t.n < 0) break;
-      if (t.n == 0) continue;
-      ok = wwait(FP8 ? q_cvt : q_full, qi & 1) && wwait(&kv_full[g % NST], (g / NST) & 1);
-#pragma unroll
-      for (int tt = 0; tt < NT; ++tt) {
-        if (!ok || tt >= t.tiles) break;
-        if (!pv_before(tt, steps[tt])) { ok = false; break; }
+    if constexpr (C::NI == 2) {
+      // Two S buffers: S of the next K/V tile goes out before this step's P
+      // is there, into the buffer where the step before left its P.
+      int steps = 0;   // P V steps of the row tile so far: buffers and phases go by it
+      for (int k = 0; ok && item_wait(k); ++k) {
+        const int n = items[k % C::NIT].n, tiles = items[k % C::NIT].tiles;
+        item_done(k);
+        if (n < 0) break;
+        if (n == 0) continue;
+        ok = wwait(FP8 ? q_cvt : q_full, qi & 1);
+        ++qi;
+        if (me >= tiles) {
+          // no rows: this issuer's share of the barriers, in step with the tiles
+          if (ok && lane == 0) mbar_arrive(q_empty);
+          __syncwarp();
+          for (int j = 0; ok && j < n; ++j) {
+            ok = kv_wait(g + j);
+            if (ok && lane == 0) mbar_arrive(&kv_empty[(g + j) % NST]);
+            __syncwarp();
+          }
+          g += n;
+          continue;
+        }
+        if (!ok || !kv_wait(g) || !pv_before(me, steps)) { ok = false; break; }
         tc::fence_after_sync();
-        issue_s(tt, steps[tt] % NSB, g);
-      }
-      if (!ok) break;
-      if (t.n == 1) commit1(q_empty);
-      for (int j = 0; ok && j < t.n; ++j) {
-        const int gg = g + j;
-#pragma unroll
-        for (int tt = 0; tt < NT; ++tt) {
-          if (tt >= t.tiles) break;
-          const int b = steps[tt] % NSB;
-          // the next K/V tile's S: with two buffers before this step's P is
-          // there (it goes where the step before left its P), else after its
-          // P V, which reads P from the one buffer
-          auto ahead = [&]() -> bool {
-            if (j + 1 >= t.n) return true;
-            if (tt == 0 && !wwait(&kv_full[(gg + 1) % NST], ((gg + 1) / NST) & 1)) return false;
-            if (!pv_before(tt, NSB == 2 ? steps[tt] : steps[tt] + 1)) return false;
+        issue_s(me, steps % NSB, g);
+        if (n == 1) commit1(q_empty);
+        for (int j = 0; j < n; ++j, ++g, ++steps) {
+          if (j + 1 < n) {
+            if (!kv_wait(g + 1) || !pv_before(me, steps)) { ok = false; break; }
             tc::fence_after_sync();
-            issue_s(tt, (steps[tt] + 1) % NSB, gg + 1);
-            if (j + 2 == t.n && tt == t.tiles - 1) commit1(q_empty);
-            return true;
-          };
-          if (NSB == 2 && !ahead()) { ok = false; break; }
-          if (!wwait(&p_full[tt * NSB + b], (steps[tt] / NSB) & 1)) { ok = false; break; }
+            issue_s(me, (steps + 1) % NSB, g + 1);
+            if (j + 2 == n) commit1(q_empty);
+          }
+          if (!wwait(&p_full[me * NSB + steps % NSB], (steps / NSB) & 1)) { ok = false; break; }
           tc::fence_after_sync();
-          issue_pv(tt, b, gg, j == 0);
-          if (tt == t.tiles - 1) commit1(&kv_empty[gg % NST]);
-          if (NSB == 1 && !ahead()) { ok = false; break; }
-          ++steps[tt];
+          issue_pv(me, steps % NSB, g, j == 0);
+          commit1(&kv_empty[g % NST]);
         }
       }
-      g += t.n;
-      ++qi;
+    } else {
+      // One S buffer: per K/V tile and row tile P V, then the next S into the
+      // same buffer once that P V has completed (S overwrites P).
+      int steps[NT];
+#pragma unroll
+      for (int tt = 0; tt < NT; ++tt) steps[tt] = 0;
+      for (int k = 0; ok && item_wait(k); ++k) {
+        const int n = items[k % C::NIT].n, tiles = items[k % C::NIT].tiles;
+        item_done(k);
+        if (n < 0) break;
+        if (n == 0) continue;
+        ok = wwait(FP8 ? q_cvt : q_full, qi & 1) && kv_wait(g);
+        ++qi;
+#pragma unroll
+        for (int tt = 0; tt < NT; ++tt) {
+          if (!ok || tt >= tiles) break;
+          if (!pv_before(tt, steps[tt])) { ok = false; break; }
+          tc::fence_after_sync();
+          issue_s(tt, 0, g);
+        }
+        if (!ok) break;
+        if (n == 1) commit1(q_empty);
+        for (int j = 0; ok && j < n; ++j) {
+          const int gg = g + j;
+#pragma unroll
+          for (int tt = 0; tt < NT; ++tt) {
+            if (tt >= tiles) break;
+            if (!wwait(&p_full[tt], steps[tt] & 1)) { ok = false; break; }
+            tc::fence_after_sync();
+            issue_pv(tt, 0, gg, j == 0);
+            if (tt == tiles - 1) commit1(&kv_empty[gg % NST]);
+            ++steps[tt];
+            if (j + 1 < n) {
+              if ((tt == 0 && !kv_wait(gg + 1)) || !pv_before(tt, steps[tt])) { ok = false; break; }
+              tc::fence_after_sync();
+              issue_s(tt, 0, gg + 1);
+              if (j + 2 == n && tt == tiles - 1) commit1(q_empty);
+            }
+          }
+        }
+        g += n;
+      }
     }
     // every MMA this warp issued has completed before the block frees TMEM
-    commit1(drain);
-    mbar_drain(drain, 0);
+    commit1(&drain[me]);
+    mbar_drain(&drain[me], 0);
   } else if (FP8 && warp >= C::W_CVT) {
     // ------------------------------------------------------------ converters
     // Per item Q in place, bf16 -> f16; per K/V tile 16-byte runs of codes ->
@@ -550,12 +594,12 @@ __global__ void __launch_bounds__(PxCfg<D, FP8>::LB_THREADS, 1)
     int g = 0, qi = 0;
     bool ok = true;
     for (int k = 0; ok && item_wait(k); ++k) {
-      struct { int n, tiles; } t{items[k % C::NIT].n, items[k % C::NIT].tiles};
+      const int n = items[k % C::NIT].n, tiles = items[k % C::NIT].tiles;
       item_done(k);
-      if (t.n < 0) break;
-      if (t.n == 0) continue;
+      if (n < 0) break;
+      if (n == 0) continue;
       if (!wwait(q_full, qi & 1)) break;
-      for (int c = ct; c < t.tiles * C::Q_TILE / 16; c += N) {
+      for (int c = ct; c < tiles * C::Q_TILE / 16; c += N) {
         uint4 w = *reinterpret_cast<const uint4*>(smem + c * 16);
         w.x = pack_f16x2(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u));
         w.y = pack_f16x2(__uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
@@ -567,7 +611,7 @@ __global__ void __launch_bounds__(PxCfg<D, FP8>::LB_THREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(q_cvt);
       ++qi;
-      for (int j = 0; j < t.n; ++j, ++g) {
+      for (int j = 0; j < n; ++j, ++g) {
         const int sc = g % C::NSTF_MOD, st = g % NST;
         if (!wwait(&c_full[sc], (g / C::NSTF_MOD) & 1)) { ok = false; break; }
         const uint8_t* codes = smem + C::OFF_CODE + sc * C::CODE_STAGE;
