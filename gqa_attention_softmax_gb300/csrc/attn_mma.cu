@@ -675,7 +675,8 @@ __global__ void __launch_bounds__(MmaCfg<D, RT, TG, KT, NST, FP8, SHARED>::THREA
   // may start launching (it waits for the whole grid before reading)
   if (!FUSED) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if constexpr (SHARED)
-    if (p.chain & kChainWaitLast) grid_dependency_wait();
+    if ((p.chain & kChainWaitLast) && (blockIdx.x | blockIdx.y | blockIdx.z) == 0)
+      grid_dependency_wait();
 }
 
 // ---------------------------------------------------------------------------
@@ -730,8 +731,9 @@ static int launch_cfg(const AttnArgs& a, cudaStream_t stream) {
   p.v_scale = a.v_scale;
 
   auto kern = attn_mma_kernel<D, RT, TG, KT, NST, FUSED, FP8, SHARED>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       C::SMEM_BYTES);
+  cudaError_t e = SHARED ? set_chained_smem(kern, C::SMEM_BYTES)
+                         : cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                C::SMEM_BYTES);
   if (e != cudaSuccess) {
     set_error("cudaFuncSetAttribute: %s", cudaGetErrorString(e));
     return SINKATTN_CUDA_ERROR;

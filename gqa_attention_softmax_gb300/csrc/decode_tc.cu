@@ -723,7 +723,7 @@ __global__ void __launch_bounds__(DtcCfg<RR, FP8>::THREADS, 1)
   // this CTA's partials are written: a dependent merge may start launching
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if constexpr (SHARED)
-    if (p.chain & kChainWaitLast) grid_dependency_wait();
+    if ((p.chain & kChainWaitLast) && blockIdx.x == 0) grid_dependency_wait();
   if (warp == C::W_MMA) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, C::TMEM_COLS);

@@ -68,9 +68,22 @@ inline int kv_box_rows(const AttnArgs& a, int tile_keys) {
 // A chain of launches, each a programmatic dependent of the one before: a
 // launch may start while the one before it still runs. kChainWaitFirst: it
 // waits for that one's results before it reads anything. kChainWaitLast: it
-// needs none of them (the one before waited for what it does need), but ends
-// only after it, so that whoever waits for this launch has waited for both.
+// needs none of them (the one before waited for what it does need), but its
+// first block ends only after it, so that whoever waits for this launch has
+// waited for both (one block, as a block that waits keeps its place on the SM).
 constexpr int32_t kChainWaitFirst = 1, kChainWaitLast = 2;
+
+// Sets a kernel of a chain up: its dynamic shared memory, and the largest
+// shared-memory share of the SM, without which the next launch's blocks could
+// not start beside its own.
+template <typename Kern>
+inline cudaError_t set_chained_smem(Kern kern, int smem) {
+  const cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
+                              cudaSharedmemCarveoutMaxShared);
+}
 
 // Launches `kern` as a programmatic dependent of the launch before it.
 template <typename... Params, typename... Args>

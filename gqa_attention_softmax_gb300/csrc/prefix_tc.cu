@@ -875,7 +875,7 @@ int launch(const AttnArgs& a, const SharedPlan& plan, cudaStream_t stream) {
                     ? static_cast<int>(std::max<int64_t>(1, (tiles - 1 + a.num_splits - 2) / (a.num_splits - 1)))
                     : 1;
   auto kern = prefix_tc_kernel<D, FP8>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  cudaError_t e = set_chained_smem(kern, C::SMEM);
   if (e == cudaSuccess) {
     e = launch_chained(kern, dim3(static_cast<unsigned>(std::min<int64_t>(units, sm_count()))),
                        C::THREADS, C::SMEM, stream, tmQ, tmK, tmV, p);
