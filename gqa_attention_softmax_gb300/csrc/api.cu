@@ -508,23 +508,32 @@ int decode_shared_impl(const void* q, const void* k_pages, const void* v_pages, 
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
 
   SharedPlan plan;
-  plan.kv = static_cast<int32_t*>(workspace);
-  plan.pages = plan.kv + batch + 1;
-  plan.grp_q = plan.pages + batch + 1;
+  plan.own_seq = static_cast<int32_t*>(workspace);
+  plan.own_len = plan.own_seq + batch;
+  plan.own_page = plan.own_len + batch;
+  plan.grp_q = plan.own_page + batch;
   plan.grp_k = plan.grp_q + num_groups + 1;
   plan.grp_pages = plan.grp_k + num_groups + 1;
   plan.grp_unit = plan.grp_pages + num_groups + 1;
-  plan.row_pos = plan.grp_unit + num_groups + 1;
+  plan.quota = plan.grp_unit + num_groups + 1;
+  plan.row_pos = plan.quota + 1;
   const size_t rows = static_cast<size_t>(batch) * q_len;
   const size_t plan_bytes = shared_plan_bytes(batch, q_len, num_groups);
   float* part_acc = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan_bytes);
   float* part_md = reinterpret_cast<float*>(
       reinterpret_cast<char*>(part_acc) +
       ((rows * num_qo_heads * slots * head_dim * 4 + 255) & ~static_cast<size_t>(255)));
+  // (at d 128 a block of either pass fills its SM)
+  SharedCost cost;
+  cost.unit = head_dim == 64 ? 1.05f : 1.9f;
+  cost.own_key = head_dim == 64 ? 0.5f / 64 * num_kv_heads : 0.f;
+  cost.ramp = 8.f;
+  cost.sms = sm_count();
   rc = launch_shared_plan(kv_indptr, pg.page_indptr, group_indptr, prefix_lens, num_groups,
                           pg.page_size, batch, q_len, max_prefix_len, max_suffix_len,
                           prefix_block_tokens(num_qo_heads / num_kv_heads),
-                          prefix_tile_keys(head_dim, f8 != nullptr), num_kv_heads, plan, s);
+                          prefix_tile_keys(head_dim, f8 != nullptr), num_kv_heads,
+                          window, prefix_splits, cost, plan, s);
   if (rc) return rc;
 
   a.part_acc = part_acc;
@@ -551,9 +560,10 @@ int decode_shared_impl(const void* q, const void* k_pages, const void* v_pages, 
     if ((rc = tc ? launch_prefix_tc(pa, plan, s) : launch_attn_mma_shared(pa, s))) return rc;
   }
   PagedKv own = pg;
-  own.page_indptr = plan.pages;
+  own.page_indptr = plan.own_page;
   set_paged(&a, &own);
-  a.cu_k = plan.kv;
+  a.cu_k = plan.own_len;
+  a.seq = plan.own_seq;
   a.part_first = prefix_splits;
   // behind a prefix pass, the plan is complete (that pass waited for it)
   a.chain = prefix_splits > 0 ? kChainWaitLast : kChainWaitFirst;

@@ -69,6 +69,7 @@ struct MmaParams {
   int part_slots, part_first;
   int free_rows;
   const int32_t* row_pos;
+  const int32_t* seq;
   int chain;
   const float* sinks;     // fused mode
   __nv_bfloat16* out;     // fused mode
@@ -149,10 +150,11 @@ __global__ void __launch_bounds__(MmaCfg<D, RT, TG, KT, NST, FP8, SHARED>::THREA
   const int split = blockIdx.x % S;
   const int qb = p.nqb - 1 - static_cast<int>(blockIdx.x / S);   // longest query blocks first
 
-  const int q_start = p.cu_q ? p.cu_q[b] : b * p.q_len;
+  const bool own = SHARED && p.seq != nullptr;   // an own pass: lengths instead of running sums
+  const int q_start = p.cu_q ? p.cu_q[b] : (own ? p.seq[b] : b) * p.q_len;
   const int Lq = p.cu_q ? p.cu_q[b + 1] - q_start : p.q_len;
   const int k_start = p.cu_k[b];
-  const int Lk = p.cu_k[b + 1] - k_start;
+  const int Lk = own ? k_start : p.cu_k[b + 1] - k_start;
   const int q0 = qb * p.QB;
   if (q0 >= Lq) return;   // uniform over the CTA (and the cluster), before any barrier
   const int nq = min(p.QB, Lq - q0);
@@ -204,7 +206,7 @@ __global__ void __launch_bounds__(MmaCfg<D, RT, TG, KT, NST, FP8, SHARED>::THREA
       PageCursor pc;
       if (paged) {
         const int e0 = p.page_indptr[b];
-        const int np = p.page_indptr[b + 1] - e0;
+        const int np = own ? (Lk + p.page_size - 1) / p.page_size : p.page_indptr[b + 1] - e0;
         if (leader && Lk > np * p.page_size) atomicExch(&g_status_attn_mma, SINKATTN_BAD_LENGTHS);
         pc.start(p.page_indices + e0, np, first / p.page_size, lane);
       }
@@ -719,6 +721,7 @@ static int launch_cfg(const AttnArgs& a, cudaStream_t stream) {
   p.part_first = a.part_first;
   p.free_rows = a.free_rows;
   p.row_pos = a.row_pos;
+  p.seq = a.seq;
   p.chain = a.chain;
   p.page_size = a.page_size;
   p.box_rows = box;

@@ -9,6 +9,8 @@
 // same P keys, read once; the own part is a split-KV decode whose page lists
 // start behind the prefix. One small launch derives both parts' lengths and
 // page-list starts from the caller's arrays, so the call needs no host copy.
+#include <algorithm>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -23,7 +25,11 @@ struct PlanParams {
   const int32_t* page_indptr;
   const int32_t* group_indptr;
   const int32_t* prefix_lens;
-  int groups, page_size, batch, q_len, max_prefix, max_suffix, block_tokens, tile_keys, Hkv;
+  int groups, page_shift, batch, q_len, max_prefix, max_suffix, block_tokens, tile_keys, Hkv;
+  int window;
+  int quota_min;       // units per block that keep to the splits
+  float class_scale;   // own keys -> class
+  SharedCost cost;
   SharedPlan out;
 };
 
@@ -51,15 +57,27 @@ __device__ __forceinline__ int block_sum_scan(int v, int* total, int* sums) {
   return v + (warp > 0 ? before : 0);
 }
 
-__global__ void __launch_bounds__(kThreads) shared_plan_kernel(const PlanParams p) {
+constexpr int kClasses = 64;   // of own lengths
+
+__global__ void __launch_bounds__(kThreads, 1) shared_plan_kernel(const PlanParams p) {
   __shared__ int sums[32];
+  __shared__ int count_s[kClasses], place_s[kClasses];
+  __shared__ float own_s[32];
   const int tid = threadIdx.x;
   grid_launch_dependents();   // the next launch sets itself up meanwhile, and waits for this one
+  if (tid < kClasses) count_s[tid] = 0;
+  // the first sequence of each thread: loads that depend on nothing
+  int len0 = 0, page0 = 0, held0 = 0;
+  if (tid < p.batch) {
+    len0 = p.kv_indptr[tid + 1] - p.kv_indptr[tid];
+    page0 = p.page_indptr[tid];
+    held0 = p.page_indptr[tid + 1] - page0;
+  }
   bool bad = false;
   // the keys of group g's prefix that can be used
   auto prefix_of = [&](int g, bool* wrong) -> int {
     const int len = p.prefix_lens[g];
-    const bool ok = len >= 0 && len <= p.max_prefix && len % p.page_size == 0;
+    const bool ok = len >= 0 && len <= p.max_prefix && (len & ((1 << p.page_shift) - 1)) == 0;
     if (!ok) *wrong = true;
     return ok ? len : 0;
   };
@@ -78,8 +96,9 @@ __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const PlanParams 
     if (g < p.groups && !broken) {
       const int b0 = p.group_indptr[g], b1 = p.group_indptr[g + 1];
       len = prefix_of(g, &bad);
+      const int first = p.page_indptr[b0];
       // the first sequence's list holds the prefix
-      if (b1 > b0 && len > (p.page_indptr[b0 + 1] - p.page_indptr[b0]) * p.page_size) {
+      if (b1 > b0 && len > (p.page_indptr[b0 + 1] - first) << p.page_shift) {
         bad = true;
         len = 0;
       }
@@ -87,7 +106,7 @@ __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const PlanParams 
       units = ((b1 - b0) * p.q_len + p.block_tokens - 1) / p.block_tokens * p.Hkv *
               ((len + p.tile_keys - 1) / p.tile_keys);
       p.out.grp_q[g] = b0 * p.q_len;
-      p.out.grp_pages[g] = p.page_indptr[b0];
+      p.out.grp_pages[g] = first;
     } else if (g < p.groups) {
       p.out.grp_q[g] = p.batch * p.q_len;
       p.out.grp_pages[g] = p.page_indptr[p.batch];
@@ -101,38 +120,82 @@ __global__ void __launch_bounds__(kThreads) shared_plan_kernel(const PlanParams 
       p.out.grp_unit[g + 1] = upto_unit;
     }
   }
+  // The sequences: own keys and where their pages start. A sequence's class
+  // goes by its length, longest first; the order within a class is whoever
+  // comes first, which moves work between SMs and no result.
+  struct Own {
+    int len, page, kind;
+  };
+  auto own_of = [&](int b) -> Own {
+    int lo = 0, hi = broken ? 1 : p.groups;   // the group with group_indptr[g] <= b < group_indptr[g + 1]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (p.group_indptr[mid] <= b) lo = mid;
+      else hi = mid;
+    }
+    const int len = b == tid ? len0 : p.kv_indptr[b + 1] - p.kv_indptr[b];
+    const int first = b == tid ? page0 : p.page_indptr[b];
+    const int held = b == tid ? held0 : p.page_indptr[b + 1] - first;
+    int prefix = broken ? 0 : prefix_of(lo, &bad);
+    int own = len - prefix;
+    if (own < p.q_len || own > p.max_suffix || len > held << p.page_shift) {
+      bad = true;
+      own = prefix = 0;
+    }
+    const int kind = kClasses - 1 - min(kClasses - 1, static_cast<int>(static_cast<float>(own) * p.class_scale));
+    return {own, first + (prefix >> p.page_shift), kind};
+  };
+  Own mine{};
+  float keys = 0.f;   // own keys of the batch (for the quota only)
+  for (int b = tid; b < p.batch; b += kThreads) {
+    const Own o = own_of(b);
+    if (b == tid) mine = o;
+    atomicAdd(&count_s[o.kind], 1);
+    keys += static_cast<float>(o.len);
+    if (p.window > 0) {
+      const int len = b == tid ? len0 : p.kv_indptr[b + 1] - p.kv_indptr[b];
+      for (int t = 0; t < p.q_len; ++t) p.out.row_pos[b * p.q_len + t] = len - p.q_len + t;
+    }
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) keys += __shfl_xor_sync(0xffffffffu, keys, off);
+  if ((tid & 31) == 0) own_s[tid >> 5] = keys;
+  __syncthreads();
+  if (tid < 32) {   // where each class starts
+    const int c0 = count_s[2 * tid], c1 = count_s[2 * tid + 1];
+    int x = c0 + c1;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, off);
+      if (tid >= off) x += y;
+    }
+    place_s[2 * tid] = x - c0 - c1;
+    place_s[2 * tid + 1] = x - c1;
+  }
+  __syncthreads();
+  for (int b = tid; b < p.batch; b += kThreads) {
+    const Own o = b == tid ? mine : own_of(b);
+    const int at = atomicAdd(&place_s[o.kind], 1);
+    p.out.own_seq[at] = b;
+    p.out.own_len[at] = o.len;
+    p.out.own_page[at] = o.page;
+  }
   if (tid == 0) {
+    p.out.grp_k[0] = 0;
     p.out.grp_q[p.groups] = p.batch * p.q_len;
     p.out.grp_pages[p.groups] = p.page_indptr[p.batch];
     p.out.grp_unit[0] = 0;
-  }
-  if (tid == 0) p.out.grp_k[0] = p.out.kv[0] = 0;
-  run = 0;
-  for (int base = 0; base < p.batch; base += kThreads) {
-    const int b = base + tid;
-    int own = 0;
-    if (b < p.batch) {
-      int lo = 0, hi = broken ? 1 : p.groups;   // the group with group_indptr[g] <= b < group_indptr[g + 1]
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (p.group_indptr[mid] <= b) lo = mid;
-        else hi = mid;
-      }
-      const int len = p.kv_indptr[b + 1] - p.kv_indptr[b];
-      const int first = p.page_indptr[b], held = p.page_indptr[b + 1] - first;
-      int prefix = broken ? 0 : prefix_of(lo, &bad);
-      own = len - prefix;
-      if (own < p.q_len || own > p.max_suffix || len > held * p.page_size) {
-        bad = true;
-        own = prefix = 0;
-      }
-      p.out.pages[b] = first + prefix / p.page_size;
-      for (int t = 0; t < p.q_len; ++t) p.out.row_pos[b * p.q_len + t] = len - p.q_len + t;
-      if (b == p.batch - 1) p.out.pages[p.batch] = p.page_indptr[p.batch];
+    // units of one thread block: an even share, or, where the own pass runs
+    // beside the prefix, what keeps a block busy for as long as all work takes
+    int quota = (run_unit + p.cost.sms - 1) / p.cost.sms;
+    if (p.cost.own_key > 0.f) {
+      float own = 0.f;
+      for (int w = 0; w < 32; ++w) own += own_s[w];
+      const float all = (static_cast<float>(run_unit) * p.cost.unit + own * p.cost.own_key) /
+                        static_cast<float>(p.cost.sms);
+      quota = max(quota, static_cast<int>((all - p.cost.ramp) / p.cost.unit));
     }
-    const int upto = run + block_sum_scan(own, &total, sums);
-    if (b < p.batch) p.out.kv[b + 1] = upto;
-    run += total;
+    *p.out.quota = max(max(quota, p.quota_min), 1);
   }
   if (__syncthreads_or(bad || broken) && tid == 0) atomicExch(&g_status_shared, SINKATTN_BAD_LENGTHS);
 }
@@ -143,9 +206,31 @@ int launch_shared_plan(const int32_t* kv_indptr, const int32_t* page_indptr,
                        const int32_t* group_indptr, const int32_t* prefix_lens, int32_t groups,
                        int32_t page_size, int32_t batch, int32_t q_len, int32_t max_prefix,
                        int32_t max_suffix, int32_t block_tokens, int32_t tile_keys, int32_t Hkv,
-                       const SharedPlan& plan, cudaStream_t stream) {
-  const PlanParams p{kv_indptr,  page_indptr, group_indptr, prefix_lens, groups, page_size, batch,
-                     q_len,      max_prefix,  max_suffix,   block_tokens, tile_keys, Hkv,   plan};
+                       int32_t window, int32_t splits, const SharedCost& cost, const SharedPlan& plan,
+                       cudaStream_t stream) {
+  // a row block of T tiles meets at most (T - 1) / quota + 2 runs of units
+  const int64_t tiles = (static_cast<int64_t>(max_prefix) + tile_keys - 1) / tile_keys;
+  const int quota_min =
+      splits > 1 ? static_cast<int>(std::max<int64_t>(1, (tiles - 1 + splits - 2) / (splits - 1))) : 1;
+  PlanParams p{};
+  p.kv_indptr = kv_indptr;
+  p.page_indptr = page_indptr;
+  p.group_indptr = group_indptr;
+  p.prefix_lens = prefix_lens;
+  p.groups = groups;
+  while ((1 << p.page_shift) < page_size) ++p.page_shift;
+  p.batch = batch;
+  p.q_len = q_len;
+  p.max_prefix = max_prefix;
+  p.max_suffix = max_suffix;
+  p.block_tokens = block_tokens;
+  p.tile_keys = tile_keys;
+  p.Hkv = Hkv;
+  p.window = window;
+  p.quota_min = quota_min;
+  p.class_scale = static_cast<float>(kClasses) / (static_cast<float>(max_suffix) + 1.f);
+  p.cost = cost;
+  p.out = plan;
   shared_plan_kernel<<<1, kThreads, 0, stream>>>(p);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) {

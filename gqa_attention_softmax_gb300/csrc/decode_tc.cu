@@ -39,6 +39,7 @@ struct DtcParams {
   float* part_md;
   int part_slots, part_first;   // SHARED: partials at their place among another pass's
   int chain;                    // SHARED: the launch's place in its chain
+  const int32_t* seq;           // SHARED: the items' sequences; cu_k holds their lengths
   // paged KV (page_size > 0): page-pool rows, boxes of box_rows keys
   int page_size, box_rows;
   const int32_t* page_indptr;
@@ -57,7 +58,7 @@ struct DtcItem {
 
 // cu_k is read from `cu` (a shared-memory copy when the batch fits, else
 // global memory): every role derives every item's keys from it.
-template <int KT, bool PAGED, bool ROTATE>
+template <int KT, bool PAGED, bool ROTATE, bool SHARED>
 __device__ __forceinline__ DtcItem dtc_item(const DtcParams& p, const int32_t* cu, int it) {
   DtcItem t;
   const int S = p.num_splits;
@@ -75,7 +76,7 @@ __device__ __forceinline__ DtcItem dtc_item(const DtcParams& p, const int32_t* c
   t.q0 = qb * p.QB;
   t.nq = min(p.QB, p.q_len - t.q0);
   t.k_start = cu[t.b];
-  t.Lk = cu[t.b + 1] - t.k_start;
+  t.Lk = SHARED ? t.k_start : cu[t.b + 1] - t.k_start;
   t.pos0 = t.Lk - p.q_len + t.q0;
   const int posN = t.pos0 + t.nq - 1;
   const int chunk = split_chunk(t.Lk, S);
@@ -218,13 +219,13 @@ __global__ void __launch_bounds__(DtcCfg<RR, FP8>::THREADS, 1)
   // kv_indptr in shared memory (global-memory loads under a saturated HBM
   // stream take microseconds, and every role needs every item's keys)
   int32_t* cu_s = reinterpret_cast<int32_t*>(smem + C::OFF_CU);
-  const int n_cu = p.batch + 1;
+  const int n_cu = SHARED ? p.batch : p.batch + 1;
   const bool cu_in_smem = n_cu <= C::CU_CAP + 1;
   if (cu_in_smem)
     for (int i = threadIdx.x; i < n_cu; i += blockDim.x) cu_s[i] = p.cu_k[i];
   const int32_t* cu = cu_in_smem ? cu_s : p.cu_k;
   auto item_of = [&](int k) {
-    return dtc_item<KT, PAGED, !FP8>(p, cu, static_cast<int>(blockIdx.x) + k * static_cast<int>(gridDim.x));
+    return dtc_item<KT, PAGED, !FP8, SHARED>(p, cu, static_cast<int>(blockIdx.x) + k * static_cast<int>(gridDim.x));
   };
 
   if (threadIdx.x == 0) {
@@ -295,14 +296,15 @@ __global__ void __launch_bounds__(DtcCfg<RR, FP8>::THREADS, 1)
         if (!pwait(&q_empty[qi & 1], ((qi >> 1) & 1) ^ 1)) { ok = false; break; }
         if (leader) {
           mbar_arrive_expect_tx(&q_full[qi & 1], static_cast<uint32_t>(2 * 128 * p.G * p.QB));
+          const int q_start = SHARED ? p.seq[t.b] * p.q_len : t.q_start;
           for (int sub = 0; sub < 2; ++sub)
             tc::tma_load_3d(smem + C::OFF_Q + (qi & 1) * C::Q_BUF + sub * C::Q_SUB, &tmQ,
-                            sub * 64, t.kvh * p.G, t.q_start + t.q0, &q_full[qi & 1]);
+                            sub * 64, t.kvh * p.G, q_start + t.q0, &q_full[qi & 1]);
         }
         ++qi;
         if constexpr (PAGED) {
           const int e0 = p.page_indptr[t.b];
-          const int np = p.page_indptr[t.b + 1] - e0;
+          const int np = SHARED ? (t.Lk + p.page_size - 1) / p.page_size : p.page_indptr[t.b + 1] - e0;
           if (leader && t.Lk > np * p.page_size) atomicExch(status, SINKATTN_BAD_LENGTHS);
           pc.start(p.page_indices + e0, np, t.first / p.page_size, lane);
         }
@@ -648,6 +650,7 @@ __global__ void __launch_bounds__(DtcCfg<RR, FP8>::THREADS, 1)
     const uint64_t keep_policy = policy_evict_last();
     for (int k = 0; k < n_mine; ++k) {
       const DtcItem t = item_of(k);
+      const int q_start = SHARED ? p.seq[t.b] * p.q_len : t.q_start;
       if (!wwait(&o_full[k & 1], (k >> 1) & 1) || !wwait(&ml_full[k & 1], (k >> 1) & 1)) break;
       tc::fence_after_sync();
       const float4 mlr = ml[(k & 1) * 128 + row];
@@ -675,7 +678,7 @@ __global__ void __launch_bounds__(DtcCfg<RR, FP8>::THREADS, 1)
       mbar_arrive(&o_free[k & 1]);
       if (tl < t.nq) {
         const size_t rowid =
-            static_cast<size_t>(t.q_start + t.q0 + tl) * p.Hq + t.kvh * G + (row - tl * G);
+            static_cast<size_t>(q_start + t.q0 + tl) * p.Hq + t.kvh * G + (row - tl * G);
         // (m', lr): m' + ln lr = m + ln l, the chunk's exact log-sum-exp
         float2 md;
         if (mlr.x == NEG_INF || !(mlr.z > 0.f)) {
@@ -691,7 +694,7 @@ __global__ void __launch_bounds__(DtcCfg<RR, FP8>::THREADS, 1)
       for (int r = quad; r < nrows; r += 4) {
         const int t2 = r / G;
         const size_t rowid =
-            static_cast<size_t>(t.q_start + t.q0 + t2) * p.Hq + t.kvh * G + (r - t2 * G);
+            static_cast<size_t>(q_start + t.q0 + t2) * p.Hq + t.kvh * G + (r - t2 * G);
         const float4 val = *reinterpret_cast<const float4*>(stage + r * C::XS + lane * 4);
         // kept in L2 as long as possible: the merge reads the newest partials first
         asm volatile("st.global.L2::cache_hint.v4.f32 [%0], {%1, %2, %3, %4}, %5;" ::"l"(
@@ -778,6 +781,7 @@ static int launch_dtc(const AttnArgs& a, int QB, cudaStream_t stream) {
   p.part_slots = part_slots(a);
   p.part_first = a.part_first;
   p.chain = a.chain;
+  p.seq = a.seq;
   auto kern = decode_tc_kernel<RR, PAGED, FP8, SHARED>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) {

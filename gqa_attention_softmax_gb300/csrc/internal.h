@@ -35,6 +35,9 @@ struct AttnArgs {
   // token counted from the first key (nullptr: no window)
   int32_t free_rows;
   const int32_t* row_pos;
+  // an own pass: cu_k holds lengths, page_indptr first entries, both of
+  // sequence seq[b] (nullptr: none of this)
+  const int32_t* seq;
   int32_t chain;            // kChain*: its place in a chain of dependent launches
   // paged KV (page_size > 0): k and v are page pools [num_pages, Hkv, page_size, d];
   // sequence b's keys [e * page_size, (e + 1) * page_size) live in page
@@ -155,22 +158,34 @@ int launch_merge_sparse(const float* part_acc, const float* part_md, const float
 // Shared-prefix decode: what the prefix and the per-sequence passes read,
 // derived on the device from the page lists and the groups. All int32.
 struct SharedPlan {
-  int32_t* kv;        // [batch + 1] running sum of the sequences' own keys
-  int32_t* pages;     // [batch + 1] first entry of their own pages in page_indices
+  // the sequences, longest own keys first (to 64 classes of length): an own
+  // pass whose blocks take them in this order ends with its short ones
+  int32_t* own_seq;   // [batch] sequence
+  int32_t* own_len;   // [batch] its own keys
+  int32_t* own_page;  // [batch] first entry of its own pages in page_indices
   int32_t* grp_q;     // [groups + 1] first query token of each group
   int32_t* grp_k;     // [groups + 1] running sum of the prefixes' keys
   int32_t* grp_pages; // [groups + 1] first entry of the prefixes' pages
   int32_t* grp_unit;  // [groups + 1] running sum of the tcgen05 kernel's units of work
+  int32_t* quota;     // [1] units of one thread block
   int32_t* row_pos;   // [batch * q_len] position of each query token
 };
 inline size_t shared_plan_ints(int64_t batch, int64_t q_len, int64_t groups) {
-  return static_cast<size_t>(2 * (batch + 1) + 4 * (groups + 1) + batch * q_len);
+  return static_cast<size_t>(3 * batch + 4 * (groups + 1) + 1 + batch * q_len);
 }
+// What the plan's choice of the quota goes by, in microseconds of one SM: a
+// unit, an own key (of all its KV heads; 0: the own pass does not run beside
+// the prefix's), and a row block's start and end.
+struct SharedCost {
+  float unit, own_key, ramp;
+  int sms;
+};
 int launch_shared_plan(const int32_t* kv_indptr, const int32_t* page_indptr,
                        const int32_t* group_indptr, const int32_t* prefix_lens, int32_t groups,
                        int32_t page_size, int32_t batch, int32_t q_len, int32_t max_prefix,
                        int32_t max_suffix, int32_t block_tokens, int32_t tile_keys, int32_t Hkv,
-                       const SharedPlan& plan, cudaStream_t stream);
+                       int32_t window, int32_t splits, const SharedCost& cost, const SharedPlan& plan,
+                       cudaStream_t stream);
 
 // The groups' prefixes on the tcgen05/TMEM path: partials of every query row
 // over its group's prefix (a.batch: groups, a.total_q: query tokens).

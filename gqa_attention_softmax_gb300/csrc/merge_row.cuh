@@ -118,7 +118,7 @@ __device__ __forceinline__ void merge_row(const float* md, const float* acc, flo
 
 // The same fold for rows of which many slots are empty (d_s = 0): one pass
 // over the (m, d) pairs, 32 slots at a time, then only the accumulators that
-// have a weight, four in flight. Slots are taken in order.
+// have a weight, eight in flight. Slots are taken in order.
 template <int D>
 __device__ __forceinline__ void merge_row_sparse(const float* md, const float* acc, float sink,
                                                  int S, int lane, __nv_bfloat16* orow,
@@ -148,9 +148,9 @@ __device__ __forceinline__ void merge_row_sparse(const float* md, const float* a
     for (int e = 0; e < VEC; ++e) o[e] *= keep;
     uint32_t left = __ballot_sync(0xffffffffu, some);
     while (left) {   // warp-uniform
-      float a[4][VEC], wu[4];
+      float a[8][VEC], wu[8];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < 8; ++u) {
         const int s = left ? __ffs(left) - 1 : -1;
         left &= left - 1;   // (0 stays 0)
         wu[u] = __shfl_sync(0xffffffffu, w, s < 0 ? 0 : s);
@@ -170,7 +170,7 @@ __device__ __forceinline__ void merge_row_sparse(const float* md, const float* a
         }
       }
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
+      for (int u = 0; u < 8; ++u)
 #pragma unroll
         for (int e = 0; e < VEC; ++e) o[e] = fmaf(a[u][e], wu[u], o[e]);
     }

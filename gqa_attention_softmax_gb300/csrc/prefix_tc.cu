@@ -19,8 +19,10 @@
 // -> P V interleave on the tensor core. A tile whose rows all lie behind the
 // group's last token is left out.
 //
-// The work is cut evenly: a unit is one K/V tile of one (row block, KV head),
-// block c takes the c-th run of Q units in a fixed order, and a row block's
+// The work is cut into equal runs: a unit is one K/V tile of one (row block,
+// KV head), block c takes the c-th run of units in a fixed order (their number
+// is the plan's: with own keys to read beside the prefix, fewer blocks with
+// longer runs leave SMs to those and partials out), and a row block's
 // partial number is that of its block of units. So few row blocks, ragged
 // groups and prefixes of any mix of lengths fill the SMs alike, and a row
 // block has as many partials as thread blocks worked on it; the merge reads
@@ -59,11 +61,11 @@ struct PxParams {
   const int32_t* grp_k;      // [groups + 1] running sum of the prefixes' keys
   const int32_t* grp_pages;  // [groups + 1] first entry in page_indices
   const int32_t* grp_unit;   // [groups + 1] running sum of units
+  const int32_t* quota;      // [1] units of one thread block
   const int32_t* row_pos;    // [tokens] position of each query token (windows)
   const int32_t* page_indices;
   int groups, Hq, Hkv, G, QB;
   int splits;                // partials a row block may have
-  int quota_min;             // units per block that keep to it
   int window;
   float sm_scale, scale_log2;
   int page_size, box_rows;
@@ -99,7 +101,7 @@ struct PxCfg {
   // MMA issuers: with two S buffers a step is bound by the issue of its MMAs,
   // about 1.0k cycles per row tile with their waits, so each tile has its own
   static constexpr int NI = NSB == 2 ? NT : 1;
-  static constexpr int N_BARS = 3 + 2 * NST + (2 * NSB + 1) * NT + NI + 2 * NSTF + 2 * NIT;
+  static constexpr int N_BARS = 3 + 2 * NST + 3 * NSB * NT + NI + 2 * NSTF + 2 * NIT;
   static constexpr int SMEM = 1024 + OFF_BAR + N_BARS * 8 + 64;
   static constexpr int W_MMA1 = 2 + 4 * NT;                    // the second tile's issuer
   static constexpr int N_CVT = D == 64 ? 2 : 4;
@@ -168,8 +170,7 @@ struct PxCursor {
     gp = gp_;
     gu = gu_;
     const int all = gu[p.groups];
-    const int quota = max((all + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x),
-                          p.quota_min);
+    const int quota = *p.quota;
     const long long from = static_cast<long long>(blockIdx.x) * quota;
     u = static_cast<int>(min(from, static_cast<long long>(all)));
     end = static_cast<int>(min(from + quota, static_cast<long long>(all)));
@@ -287,8 +288,8 @@ __global__ void __launch_bounds__(PxCfg<D, FP8>::LB_THREADS, 1)
   uint64_t* kv_empty = kv_full + NST;
   uint64_t* s_full = kv_empty + NST;    // [NT][NSB] by the row tile's own steps
   uint64_t* p_full = s_full + NT * NSB; // [NT][NSB] P_t written and O_t rescaled (128 arrivals)
-  uint64_t* pv_done = p_full + NT * NSB;   // [NT]
-  uint64_t* drain = pv_done + NT;       // [NI]
+  uint64_t* pv_done = p_full + NT * NSB;   // [NT][NSB] by the step's buffer
+  uint64_t* drain = pv_done + NT * NSB; // [NI]
   uint64_t* c_full = drain + C::NI;     // FP8: [NSTF] codes landed
   uint64_t* c_empty = c_full + C::NSTF;
   uint64_t* i_full = c_empty + C::NSTF; // [NIT] item written
@@ -313,8 +314,8 @@ __global__ void __launch_bounds__(PxCfg<D, FP8>::LB_THREADS, 1)
     for (int t = 0; t < NT * NSB; ++t) {
       mbar_init(&s_full[t], 1);
       mbar_init(&p_full[t], 128);
+      mbar_init(&pv_done[t], 1);
     }
-    for (int t = 0; t < NT; ++t) mbar_init(&pv_done[t], 1);
     for (int i = 0; i < C::NI; ++i) mbar_init(&drain[i], 1);
     for (int i = 0; i < C::NSTF; ++i) {
       mbar_init(&c_full[i], 1);
@@ -361,6 +362,12 @@ __global__ void __launch_bounds__(PxCfg<D, FP8>::LB_THREADS, 1)
   // A wait that gives up in any lane makes the whole warp leave its loop.
   auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status));
+  };
+  // P V of row tile t's step s has completed. One barrier per S buffer: whoever
+  // waits for step s knows that step s - NSB has completed, which is what a
+  // wait by parity needs to know.
+  auto pv_wait = [&](int t, int s) -> bool {
+    return wwait(&pv_done[t * NSB + s % NSB], (s / NSB) & 1);
   };
   // Item number k of the ring; its n is -1 behind the last one.
   auto item_wait = [&](int k) -> bool { return wwait(&i_full[k % C::NIT], (k / C::NIT) & 1); };
@@ -485,13 +492,13 @@ __global__ void __launch_bounds__(PxCfg<D, FP8>::LB_THREADS, 1)
         for (int kk = 0; kk < KT / 16; ++kk)
           tc::mma_ts(d_tm, a_tm + kk * 8, vd + static_cast<uint64_t>(kk) * 128u, idesc_o,
                      (!first || kk > 0) ? 1u : 0u);
-        tc::commit(&pv_done[t]);
+        tc::commit(&pv_done[t * NSB + b]);
       }
       __syncwarp();
     };
     // all P V up to step s - 1 of the row tile have completed
     auto pv_before = [&](int t, int s) -> bool {
-      return s <= 0 || wwait(&pv_done[t], (s - 1) & 1);
+      return s <= 0 || pv_wait(t, s - 1);
     };
     auto kv_wait = [&](int g) -> bool { return wwait(&kv_full[g % NST], (g / NST) & 1); };
     int g = 0, qi = 0;
@@ -753,7 +760,7 @@ __global__ void __launch_bounds__(PxCfg<D, FP8>::LB_THREADS, 1)
         // Rescale O_t when some row of this warp moved its reference
         // (warp-uniform branch), once the previous step's PV_t has completed.
         if (j >= 1 && __any_sync(0xffffffffu, rescale)) {
-          if (!wwait(&pv_done[tt], (steps - 1) & 1)) { ok = false; break; }
+          if (!pv_wait(tt, steps - 1)) { ok = false; break; }
           tc::fence_after_sync();
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
@@ -774,7 +781,7 @@ __global__ void __launch_bounds__(PxCfg<D, FP8>::LB_THREADS, 1)
       // O_t is read out before this thread hands over P of the next item, so
       // the next item's first PV (which overwrites O_t) comes after it.
       if (n >= 1) {
-        if (!wwait(&pv_done[tt], (steps - 1) & 1)) { ok = false; break; }
+        if (!pv_wait(tt, steps - 1)) { ok = false; break; }
         tc::fence_after_sync();
       }
       const bool some = l > 0.f;   // the row sees a key of the chunk
@@ -845,6 +852,7 @@ int launch(const AttnArgs& a, const SharedPlan& plan, cudaStream_t stream) {
   p.grp_k = plan.grp_k;
   p.grp_pages = plan.grp_pages;
   p.grp_unit = plan.grp_unit;
+  p.quota = plan.quota;
   p.row_pos = plan.row_pos;
   p.page_indices = a.page_indices;
   p.groups = a.batch;
@@ -863,17 +871,13 @@ int launch(const AttnArgs& a, const SharedPlan& plan, cudaStream_t stream) {
   p.part_acc = a.part_acc;
   p.part_md = a.part_md;
   p.part_slots = part_slots(a);
-  // row blocks: at most one per group more than its full ones; a row block of
-  // T tiles meets at most (T - 1) / quota + 2 runs of units
+  // row blocks: at most one per group more than its full ones
   const int64_t tiles = (a.max_kv + C::KT - 1) / C::KT;
   const int64_t units = (a.batch + a.total_q / (C::NT * QB)) * a.Hkv * tiles;
   if (units >= (int64_t{1} << 31)) {
     set_error("too many work items");
     return SINKATTN_UNSUPPORTED;
   }
-  p.quota_min = a.num_splits > 1
-                    ? static_cast<int>(std::max<int64_t>(1, (tiles - 1 + a.num_splits - 2) / (a.num_splits - 1)))
-                    : 1;
   auto kern = prefix_tc_kernel<D, FP8>;
   cudaError_t e = set_chained_smem(kern, C::SMEM);
   if (e == cudaSuccess) {

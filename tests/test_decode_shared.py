@@ -433,3 +433,25 @@ def test_refuses_tensors_that_would_be_misread(name, change):
     with pytest.raises(sa.SinkAttnError) as e:
         call(g, h)
     assert e.value.status == INVALID_ARG
+
+
+@gpu
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_short_items_repeat_bit_for_bit(d, fp8):
+    """Row blocks cut into items of two or three key tiles, several per thread block: every
+    repetition gives the same bits as the first (a partial read before its last product
+    shows here as rows that change)."""
+    G = 8 if d == 64 else 16
+    per = 128 // G
+    groups = [(32, [1] * (2 * per)), (33, [2] * (per - 1)), (64, [1] * (4 * per + 3)), (1, [5] * per)]
+    x, h = make(groups, 1, 2 * G, 2, d, 16, seed=16, fp8=fp8)
+    g = {k: v.cuda() for k, v in x.items()}
+    first = {}
+    for rep in range(40):
+        for ps in (2, 3, 5, 16):
+            out, lse = call(g, h, prefix_splits=ps, num_splits=1)
+            if rep == 0:
+                check(out, lse, x, h)
+                first[ps] = out, lse
+            assert torch.equal(out, first[ps][0]) and torch.equal(lse, first[ps][1])
