@@ -556,7 +556,7 @@ int decode_shared_impl(const void* q, const void* k_pages, const void* v_pages, 
     pa.free_rows = 1;
     pa.row_pos = window > 0 ? plan.row_pos : nullptr;
     const bool tc = prefix_on_tc(rows, num_qo_heads / num_kv_heads, num_groups);
-    pa.chain = kChainWaitFirst;
+    pa.chain = kChainWaitFirst | kChainFollow;
     if ((rc = tc ? launch_prefix_tc(pa, plan, s) : launch_attn_mma_shared(pa, s))) return rc;
   }
   PagedKv own = pg;

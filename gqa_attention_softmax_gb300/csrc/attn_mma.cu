@@ -144,8 +144,12 @@ __global__ void __launch_bounds__(MmaCfg<D, RT, TG, KT, NST, FP8, SHARED>::THREA
   const int lane = threadIdx.x & 31;
   const int b = blockIdx.z;
   const int kvh = blockIdx.y;
-  if constexpr (SHARED)
-    if (p.chain & kChainWaitFirst) grid_dependency_wait();
+  if constexpr (SHARED) {
+    if (p.chain & kChainWaitFirst) {
+      grid_dependency_wait();
+      if (p.chain & kChainFollow) grid_launch_dependents();
+    }
+  }
   const int S = p.num_splits;
   const int split = blockIdx.x % S;
   const int qb = p.nqb - 1 - static_cast<int>(blockIdx.x / S);   // longest query blocks first

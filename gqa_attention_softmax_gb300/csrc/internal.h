@@ -74,7 +74,8 @@ inline int kv_box_rows(const AttnArgs& a, int tile_keys) {
 // needs none of them (the one before waited for what it does need), but its
 // first block ends only after it, so that whoever waits for this launch has
 // waited for both (one block, as a block that waits keeps its place on the SM).
-constexpr int32_t kChainWaitFirst = 1, kChainWaitLast = 2;
+// kChainFollow: the next launch may start as soon as this one has waited.
+constexpr int32_t kChainWaitFirst = 1, kChainWaitLast = 2, kChainFollow = 4;
 
 // Sets a kernel of a chain up: its dynamic shared memory, and the largest
 // shared-memory share of the SM, without which the next launch's blocks could

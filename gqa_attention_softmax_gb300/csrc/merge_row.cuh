@@ -116,9 +116,92 @@ __device__ __forceinline__ void merge_row(const float* md, const float* acc, flo
   if (lse_out != nullptr && lane == 0) *lse_out = dsum > 0.f ? M + lg2(dsum) * kLn2 : NEG_INF;
 }
 
-// The same fold for rows of which many slots are empty (d_s = 0): one pass
-// over the (m, d) pairs, 32 slots at a time, then only the accumulators that
-// have a weight, eight in flight. Slots are taken in order.
+// The same fold for rows of which many slots are empty (d_s = 0): R rows per
+// warp, 32 / R lanes each for the (m, d) pairs (S <= 32 / R), and then only the
+// accumulators that have a weight. A row's loads depend on its weights, two
+// memory round trips, so the rows of a warp take theirs together: eight
+// accumulator loads are in flight. Slots are taken in order.
+template <int D, int R>
+__device__ __forceinline__ void merge_rows_sparse(const float* part_md, const float* part_acc,
+                                                  const float* sinks, long long row0, int rows,
+                                                  int Hq, int S, int lane, __nv_bfloat16* out,
+                                                  float* lse) {
+  constexpr int VEC = D / 32, W = 32 / R, U = 8 / R;
+  const int r = lane / W, s = lane % W;   // the lane's row and slot
+  const bool real = r < rows;
+  const long long row = row0 + r;
+  const float2 mine = real && s < S
+                          ? __ldcg(reinterpret_cast<const float2*>(part_md + (row * S + s) * 2))
+                          : make_float2(kNegInf, 0.f);
+  const float sink = real && sinks ? sinks[static_cast<int>(row % Hq)] : kNegInf;
+  const bool some = mine.y > 0.f;
+  float M = fmaxf(sink, some ? mine.x : kNegInf);
+#pragma unroll
+  for (int off = W / 2; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  float w = some ? ex2((mine.x - M) * kLog2e) : 0.f;
+  float total = w * mine.y;
+#pragma unroll
+  for (int off = W / 2; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
+  if (sink != kNegInf) total += ex2((sink - M) * kLog2e);
+  w *= total > 0.f ? 1.f / total : 0.f;
+  if (lse != nullptr && real && s == 0) lse[row] = total > 0.f ? M + lg2(total) * kLn2 : kNegInf;
+  const uint32_t vote = __ballot_sync(0xffffffffu, some);
+  uint32_t left[R];
+  float o[R][VEC];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    left[i] = R == 1 ? vote : (vote >> (i * W)) & ((1u << (W & 31)) - 1u);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) o[i][e] = 0.f;
+  }
+  for (uint32_t any = vote; any;) {   // warp-uniform
+    float a[U][R][VEC], wu[U][R];
+    any = 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const int slot = left[i] ? __ffs(left[i]) - 1 : -1;
+        left[i] &= left[i] - 1;   // (0 stays 0)
+        const float t = __shfl_sync(0xffffffffu, w, i * W + max(slot, 0));
+        wu[u][i] = slot >= 0 ? t : 0.f;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) a[u][i][e] = 0.f;
+        if (slot >= 0) {
+          const float* src = part_acc + ((row0 + i) * S + slot) * D + lane * VEC;
+          if constexpr (VEC == 4) {
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
+            a[u][i][0] = v.x; a[u][i][1] = v.y; a[u][i][2] = v.z; a[u][i][3] = v.w;
+          } else {
+            const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
+            a[u][i][0] = v.x; a[u][i][1] = v.y;
+          }
+        }
+        if (u == U - 1) any |= left[i];
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) o[i][e] = fmaf(a[u][i][e], wu[u][i], o[i][e]);
+  }
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    if (i >= rows) break;
+    __nv_bfloat16* op = out + (row0 + i) * D + lane * VEC;
+    if constexpr (VEC == 4) {
+      uint2 pk;
+      pk.x = pack_bf16x2(o[i][0], o[i][1]);
+      pk.y = pack_bf16x2(o[i][2], o[i][3]);
+      *reinterpret_cast<uint2*>(op) = pk;
+    } else {
+      *reinterpret_cast<uint32_t*>(op) = pack_bf16x2(o[i][0], o[i][1]);
+    }
+  }
+}
+
+// One row of any number of slots, 32 at a time.
 template <int D>
 __device__ __forceinline__ void merge_row_sparse(const float* md, const float* acc, float sink,
                                                  int S, int lane, __nv_bfloat16* orow,
@@ -146,45 +229,19 @@ __device__ __forceinline__ void merge_row_sparse(const float* md, const float* a
     total = total * keep + sum;
 #pragma unroll
     for (int e = 0; e < VEC; ++e) o[e] *= keep;
-    uint32_t left = __ballot_sync(0xffffffffu, some);
-    while (left) {   // warp-uniform
-      float a[8][VEC], wu[8];
+    for (uint32_t left = __ballot_sync(0xffffffffu, some); left; left &= left - 1) {
+      const int s = __ffs(left) - 1;
+      const float wu = __shfl_sync(0xffffffffu, w, s);
+      const float* src = acc + static_cast<size_t>(s0 + s) * D + lane * VEC;
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int s = left ? __ffs(left) - 1 : -1;
-        left &= left - 1;   // (0 stays 0)
-        wu[u] = __shfl_sync(0xffffffffu, w, s < 0 ? 0 : s);
-        if (s >= 0) {
-          const float* src = acc + static_cast<size_t>(s0 + s) * D + lane * VEC;
-          if constexpr (VEC == 4) {
-            const float4 t = __ldcg(reinterpret_cast<const float4*>(src));
-            a[u][0] = t.x; a[u][1] = t.y; a[u][2] = t.z; a[u][3] = t.w;
-          } else {
-            const float2 t = __ldcg(reinterpret_cast<const float2*>(src));
-            a[u][0] = t.x; a[u][1] = t.y;
-          }
-        } else {
-          wu[u] = 0.f;
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) a[u][e] = 0.f;
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < 8; ++u)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) o[e] = fmaf(a[u][e], wu[u], o[e]);
+      for (int e = 0; e < VEC; ++e) o[e] = fmaf(__ldcg(src + e), wu, o[e]);
     }
   }
   const float inv = total > 0.f ? 1.f / total : 0.f;
   __nv_bfloat16* op = orow + lane * VEC;
-  if constexpr (VEC == 4) {
-    uint2 pk;
-    pk.x = pack_bf16x2(o[0] * inv, o[1] * inv);
-    pk.y = pack_bf16x2(o[2] * inv, o[3] * inv);
-    *reinterpret_cast<uint2*>(op) = pk;
-  } else {
-    *reinterpret_cast<uint32_t*>(op) = pack_bf16x2(o[0] * inv, o[1] * inv);
-  }
+#pragma unroll
+  for (int e = 0; e < VEC; e += 2)
+    *reinterpret_cast<uint32_t*>(op + e) = pack_bf16x2(o[e] * inv, o[e + 1] * inv);
   if (lse_out != nullptr && lane == 0) *lse_out = total > 0.f ? M + lg2(total) * kLn2 : kNegInf;
 }
 
