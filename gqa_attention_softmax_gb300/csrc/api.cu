@@ -526,8 +526,8 @@ int decode_shared_impl(const void* q, const void* k_pages, const void* v_pages, 
   // (at d 128 a block of either pass fills its SM)
   SharedCost cost;
   cost.unit = head_dim == 64 ? 1.05f : 1.9f;
-  cost.own_key = head_dim == 64 ? 0.5f / 64 * num_kv_heads : 0.f;
-  cost.ramp = 8.f;
+  cost.own_key = head_dim == 64 ? 0.35f / 64 * num_kv_heads : 0.f;
+  cost.ramp = 4.f;
   cost.sms = sm_count();
   rc = launch_shared_plan(kv_indptr, pg.page_indptr, group_indptr, prefix_lens, num_groups,
                           pg.page_size, batch, q_len, max_prefix_len, max_suffix_len,
@@ -680,16 +680,20 @@ int sinkattn_decode_shared_default_splits(int32_t batch, int32_t q_len, int32_t 
   if (!prefix_splits || !num_splits)
     return fail(SINKATTN_INVALID_ARG, "prefix_splits and num_splits must be non-null");
   if (num_groups < 1 || max_prefix_len < 0) return fail(SINKATTN_INVALID_ARG, "bad sizes");
-  int rc = sinkattn_decode_default_splits(batch, q_len, num_qo_heads, num_kv_heads, head_dim,
-                                          max_suffix_len, num_splits);
-  if (rc) return rc;
-  // own keys: only as many chunks as fill two blocks per SM (each further one
-  // costs its partials: 64 sequences of up to 1024 own keys at d 64 take 55,
-  // 56, 60 and 64 us in 1, 2, 3 and 4 chunks, 256 x 3 drafts at d 128 take
-  // 186, 202, 234 and 270 us)
-  const int64_t fill = std::max<int64_t>(1, static_cast<int64_t>(batch) * num_kv_heads);
-  *num_splits = static_cast<int32_t>(
-      std::min<int64_t>(*num_splits, (2 * sm_count() + fill - 1) / fill));
+  if (batch < 0 || q_len < 1 || num_qo_heads <= 0 || num_kv_heads <= 0 || max_suffix_len < 0)
+    return fail(SINKATTN_INVALID_ARG, "bad sizes");
+  if (head_dim != 64 && head_dim != 128)
+    return fail(SINKATTN_UNSUPPORTED, "head_dim %d is not 64 or 128", head_dim);
+  // Own keys: chunks of about 1024 keys while they are needed to fill the SMs
+  // (the warp-level kernel's four blocks per SM twice over, the tcgen05
+  // kernel's one block twice over). Each further chunk costs its partials: 64
+  // sequences behind 8192 keys at d 64 take 33, 35 and 38 us in 1, 2 and 3
+  // chunks with up to 1024 own keys, 76, 59 and 59 us with up to 4000; 16
+  // sequences of up to 8000 own keys 96, 45, 40 and 37 us in 1, 3, 4 and 8.
+  const int64_t items = std::max<int64_t>(1, static_cast<int64_t>(batch) * num_kv_heads);
+  const int64_t fill = (head_dim == 64 ? 8 : 2) * static_cast<int64_t>(sm_count());
+  *num_splits = static_cast<int32_t>(std::max<int64_t>(
+      1, std::min<int64_t>((fill + items - 1) / items, (max_suffix_len + 1023) / 1024)));
   const int G = num_qo_heads / num_kv_heads;
   const int64_t tokens = static_cast<int64_t>(batch) * q_len;
   if (G >= 1 && G <= 64 && prefix_on_tc(tokens, G, num_groups)) {
