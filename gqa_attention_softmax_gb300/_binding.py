@@ -456,6 +456,16 @@ def _stream_of(dev, stream):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _made(t, stream):
+    """A tensor allocated here, on the current stream's account, for kernels on
+    `stream`: its memory is not handed out again before they are done."""
+    if stream is not None:
+        t.record_stream(stream if isinstance(stream, torch.cuda.Stream)
+                        else torch.cuda.ExternalStream(_stream_of(t.device, stream),
+                                                       device=t.device))
+    return t
+
+
 def _launch(dev, entry, *args):
     """Calls a C entry point with `dev` current; raises on a non-zero status."""
     if dev.index == torch.cuda.current_device():
@@ -529,11 +539,11 @@ def _decode_shared(entry, pool_dtype, scales, q, k_pages, v_pages, kv_indptr, pa
         dev.index, int(prefix_splits), int(num_splits), batch, q_len, Hq, Hkv, d, groups,
         max_prefix_len, max_suffix_len)
     if workspace is None:
-        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+        workspace = _made(torch.empty((need,), dtype=torch.uint8, device=dev), stream)
     elif not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
         raise SinkAttnError(INVALID_ARG, "workspace must be contiguous and on %s" % dev)
     if out is None:
-        out = torch.empty_like(q)
+        out = _made(torch.empty_like(q), stream)
         out_p = out.data_ptr()
     else:
         out_p = _need(out, "out", torch.bfloat16, dev, q.shape)
@@ -541,7 +551,7 @@ def _decode_shared(entry, pool_dtype, scales, q, k_pages, v_pages, kv_indptr, pa
     if lse is not None:
         lse_p = _need(lse, "lse", f32, dev, (rows, Hq))
     elif return_lse:
-        lse = torch.empty((rows, Hq), dtype=f32, device=dev)
+        lse = _made(torch.empty((rows, Hq), dtype=f32, device=dev), stream)
         lse_p = lse.data_ptr()
     if batch == 0:   # (an empty tensor has no address to check)
         return out, lse
@@ -643,8 +653,8 @@ class PageTable:
         need = 16 + max_seqs * (8 + max_pages) + 4 * num_pages
         new = state is None
         if new:
-            state = torch.empty((sinkattn_pages_table_ints(num_pages, max_seqs, max_pages),),
-                                dtype=torch.int32, device=device)
+            state = _made(torch.empty((sinkattn_pages_table_ints(num_pages, max_seqs, max_pages),),
+                                      dtype=torch.int32, device=device), stream)
         self.device = _need_cuda(state, "state")
         ptr = _need(state, "state", torch.int32, self.device, 1)
         if state.shape[0] < need:
@@ -723,7 +733,7 @@ def sinkattn_pages_reserve(table, seq_ids, cu_new, total_new, k_pages, v_pages, 
     cu_p = _need(cu_new, "cu_new", torch.int32, dev, (n + 1,))
     total_new = int(total_new)
     if slots is None:
-        slots = torch.empty((max(total_new, 0),), dtype=torch.int32, device=dev)
+        slots = _made(torch.empty((max(total_new, 0),), dtype=torch.int32, device=dev), stream)
         slots_p = slots.data_ptr()
     else:
         slots_p = _need(slots, "slots", torch.int32, dev, (total_new,))
@@ -758,7 +768,7 @@ def sinkattn_pages_compact(table, k_pages, v_pages, page_map=None, stream=None):
     page_map, int32 [num_pages]: each old page's new index, -1 where it was free."""
     dev = table.device
     if page_map is None:
-        page_map = torch.empty((table.num_pages,), dtype=torch.int32, device=dev)
+        page_map = _made(torch.empty((table.num_pages,), dtype=torch.int32, device=dev), stream)
         map_p = page_map.data_ptr()
     else:
         map_p = _need(page_map, "page_map", torch.int32, dev, (table.num_pages,))
@@ -776,11 +786,11 @@ def sinkattn_pages_lists(table, seq_ids, kv_indptr=None, page_indptr=None, page_
     n = seq_ids.shape[0]
     make = torch.empty if n > 0 else torch.zeros   # an empty batch writes nothing
     if kv_indptr is None:
-        kv_indptr = make((n + 1,), dtype=torch.int32, device=dev)
+        kv_indptr = _made(make((n + 1,), dtype=torch.int32, device=dev), stream)
     if page_indptr is None:
-        page_indptr = make((n + 1,), dtype=torch.int32, device=dev)
+        page_indptr = _made(make((n + 1,), dtype=torch.int32, device=dev), stream)
     if page_indices is None:
-        page_indices = make((n * table.max_pages,), dtype=torch.int32, device=dev)
+        page_indices = _made(make((n * table.max_pages,), dtype=torch.int32, device=dev), stream)
     kv_p = _need(kv_indptr, "kv_indptr", torch.int32, dev, (n + 1,))
     pp_p = _need(page_indptr, "page_indptr", torch.int32, dev, (n + 1,))
     pi_p = _need(page_indices, "page_indices", torch.int32, dev, 1)

@@ -439,6 +439,7 @@ int decode_impl(const void* q, const void* k, const void* v, const int32_t* kv_i
 // Whether the prefixes take the tcgen05 kernel, which works on row blocks of
 // 256 (128 at least), or the warp-level one, which takes up to 64 rows at a
 // time and re-reads the keys for each.
+// (A group's sequences come as one run of rows: 4 samples of 8 heads are 32.)
 bool prefix_on_tc(int64_t tokens, int G, int64_t groups) {
   const int kind = g_decode_kernel.load(std::memory_order_relaxed);
   if (kind != SINKATTN_DECODE_AUTO) return kind == SINKATTN_DECODE_TCGEN05;
@@ -523,6 +524,8 @@ int decode_shared_impl(const void* q, const void* k_pages, const void* v_pages, 
   float* part_md = reinterpret_cast<float*>(
       reinterpret_cast<char*>(part_acc) +
       ((rows * num_qo_heads * slots * head_dim * 4 + 255) & ~static_cast<size_t>(255)));
+  const int G = num_qo_heads / num_kv_heads;
+  const bool tc = prefix_on_tc(static_cast<int64_t>(rows), G, num_groups);
   // (at d 128 a block of either pass fills its SM)
   SharedCost cost;
   cost.unit = head_dim == 64 ? 1.05f : 1.9f;
@@ -531,8 +534,8 @@ int decode_shared_impl(const void* q, const void* k_pages, const void* v_pages, 
   cost.sms = sm_count();
   rc = launch_shared_plan(kv_indptr, pg.page_indptr, group_indptr, prefix_lens, num_groups,
                           pg.page_size, batch, q_len, max_prefix_len, max_suffix_len,
-                          prefix_block_tokens(num_qo_heads / num_kv_heads),
-                          prefix_tile_keys(head_dim, f8 != nullptr), num_kv_heads,
+                          tc ? prefix_block_tokens(G) : attn_mma_block_tokens(G, rows),
+                          tc ? prefix_tile_keys(head_dim, f8 != nullptr) : 0, num_kv_heads,
                           window, prefix_splits, cost, plan, s);
   if (rc) return rc;
 
@@ -555,7 +558,7 @@ int decode_shared_impl(const void* q, const void* k_pages, const void* v_pages, 
     pa.num_splits = prefix_splits;
     pa.free_rows = 1;
     pa.row_pos = window > 0 ? plan.row_pos : nullptr;
-    const bool tc = prefix_on_tc(rows, num_qo_heads / num_kv_heads, num_groups);
+    pa.blk = tc ? nullptr : plan.grp_unit;
     pa.chain = kChainWaitFirst | kChainFollow;
     if ((rc = tc ? launch_prefix_tc(pa, plan, s) : launch_attn_mma_shared(pa, s))) return rc;
   }
@@ -870,7 +873,8 @@ int sinkattn_debug_set_hooks(long long wait_limit_cycles, int skip_tile) {
   if (set_hooks_attn_mma(wait_limit_cycles, skip_tile) ||
       set_hooks_prefill_tc(wait_limit_cycles, skip_tile) ||
       set_hooks_decode_tc(wait_limit_cycles, skip_tile) ||
-      set_hooks_prefix_tc(wait_limit_cycles, skip_tile))
+      set_hooks_prefix_tc(wait_limit_cycles, skip_tile) ||
+      set_hooks_pages(wait_limit_cycles, skip_tile))
     return fail(SINKATTN_CUDA_ERROR, "setting the test hooks failed: %s",
                 cudaGetErrorString(cudaGetLastError()));
   return SINKATTN_OK;

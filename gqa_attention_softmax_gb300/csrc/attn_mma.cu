@@ -70,6 +70,8 @@ struct MmaParams {
   int free_rows;
   const int32_t* row_pos;
   const int32_t* seq;
+  const int32_t* blk;   // a prefix pass: running sum of row blocks over the `groups`
+  int groups;
   int chain;
   const float* sinks;     // fused mode
   __nv_bfloat16* out;     // fused mode
@@ -142,7 +144,7 @@ __global__ void __launch_bounds__(MmaCfg<D, RT, TG, KT, NST, FP8, SHARED>::THREA
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int b = blockIdx.z;
+  int b = blockIdx.z;
   const int kvh = blockIdx.y;
   if constexpr (SHARED) {
     if (p.chain & kChainWaitFirst) {
@@ -152,7 +154,19 @@ __global__ void __launch_bounds__(MmaCfg<D, RT, TG, KT, NST, FP8, SHARED>::THREA
   }
   const int S = p.num_splits;
   const int split = blockIdx.x % S;
-  const int qb = p.nqb - 1 - static_cast<int>(blockIdx.x / S);   // longest query blocks first
+  int qb = p.nqb - 1 - static_cast<int>(blockIdx.x / S);   // longest query blocks first
+  if (SHARED && p.blk) {   // row block blockIdx.x / S of all groups' blocks
+    const int x = static_cast<int>(blockIdx.x / S);
+    if (x >= p.blk[p.groups]) return;
+    int lo = 0, hi = p.groups;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (p.blk[mid] <= x) lo = mid;
+      else hi = mid;
+    }
+    b = lo;
+    qb = x - p.blk[lo];
+  }
 
   const bool own = SHARED && p.seq != nullptr;   // an own pass: lengths instead of running sums
   const int q_start = p.cu_q ? p.cu_q[b] : (own ? p.seq[b] : b) * p.q_len;
@@ -712,7 +726,8 @@ static int launch_cfg(const AttnArgs& a, cudaStream_t stream) {
   p.G = a.Hq / a.Hkv;
   const int maxq = a.cu_q ? a.max_q : a.q_len;
   p.QB = std::min(maxq, (16 * RT) / p.G);
-  p.nqb = (maxq + p.QB - 1) / p.QB;
+  // (blk: at most one row block per group more than the full ones)
+  p.nqb = a.blk ? a.batch + maxq / p.QB : (maxq + p.QB - 1) / p.QB;
   p.num_splits = a.num_splits;
   p.max_kv = a.max_kv;
   p.sm_scale = a.sm_scale;
@@ -726,6 +741,8 @@ static int launch_cfg(const AttnArgs& a, cudaStream_t stream) {
   p.free_rows = a.free_rows;
   p.row_pos = a.row_pos;
   p.seq = a.seq;
+  p.blk = a.blk;
+  p.groups = a.batch;
   p.chain = a.chain;
   p.page_size = a.page_size;
   p.box_rows = box;
@@ -745,8 +762,12 @@ static int launch_cfg(const AttnArgs& a, cudaStream_t stream) {
     set_error("cudaFuncSetAttribute: %s", cudaGetErrorString(e));
     return SINKATTN_CUDA_ERROR;
   }
+  if (static_cast<int64_t>(p.nqb) * p.num_splits >= (int64_t{1} << 31)) {
+    set_error("too many blocks of query rows");
+    return SINKATTN_UNSUPPORTED;
+  }
   const dim3 grid(static_cast<unsigned>(p.nqb * p.num_splits), static_cast<unsigned>(a.Hkv),
-                  static_cast<unsigned>(a.batch));
+                  a.blk ? 1u : static_cast<unsigned>(a.batch));
   if (FUSED) {
     // the S chunks of one (sequence, KV head, query block) form a cluster
     if (p.num_splits > 8) {
@@ -814,6 +835,11 @@ static int launch_attn_mma_t(const AttnArgs& a, cudaStream_t stream) {
 int launch_attn_mma(const AttnArgs& a, cudaStream_t stream) {
   return a.kv_fp8 ? launch_attn_mma_t<false, true, false>(a, stream)
                   : launch_attn_mma_t<false, false, false>(a, stream);
+}
+
+int attn_mma_block_tokens(int G, int64_t tokens) {
+  const int64_t rt = std::min<int64_t>(4, (tokens * G + 15) / 16);
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(tokens, 16 * rt / G)));
 }
 
 int launch_attn_mma_shared(const AttnArgs& a, cudaStream_t stream) {

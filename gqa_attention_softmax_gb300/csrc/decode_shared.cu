@@ -103,8 +103,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_plan_kernel(const PlanPara
         len = 0;
       }
       // row blocks x KV heads x key tiles (below 2^31: checked on the host)
-      units = ((b1 - b0) * p.q_len + p.block_tokens - 1) / p.block_tokens * p.Hkv *
-              ((len + p.tile_keys - 1) / p.tile_keys);
+      units = ((b1 - b0) * p.q_len + p.block_tokens - 1) / p.block_tokens;
+      if (p.tile_keys > 0) units *= p.Hkv * ((len + p.tile_keys - 1) / p.tile_keys);
       p.out.grp_q[g] = b0 * p.q_len;
       p.out.grp_pages[g] = first;
     } else if (g < p.groups) {
@@ -211,7 +211,8 @@ int launch_shared_plan(const int32_t* kv_indptr, const int32_t* page_indptr,
                        int32_t window, int32_t splits, const SharedCost& cost, const SharedPlan& plan,
                        cudaStream_t stream) {
   // a row block of T tiles meets at most (T - 1) / quota + 2 runs of units
-  const int64_t tiles = (static_cast<int64_t>(max_prefix) + tile_keys - 1) / tile_keys;
+  const int64_t tiles =
+      tile_keys > 0 ? (static_cast<int64_t>(max_prefix) + tile_keys - 1) / tile_keys : 1;
   const int quota_min =
       splits > 1 ? static_cast<int>(std::max<int64_t>(1, (tiles - 1 + splits - 2) / (splits - 1))) : 1;
   PlanParams p{};

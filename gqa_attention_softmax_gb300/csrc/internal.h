@@ -38,6 +38,9 @@ struct AttnArgs {
   // an own pass: cu_k holds lengths, page_indptr first entries, both of
   // sequence seq[b] (nullptr: none of this)
   const int32_t* seq;
+  // a prefix pass: running sum of the groups' row blocks [batch + 1], each of
+  // attn_mma_block_tokens() query tokens (nullptr: blocks per sequence)
+  const int32_t* blk;
   int32_t chain;            // kChain*: its place in a chain of dependent launches
   // paged KV (page_size > 0): k and v are page pools [num_pages, Hkv, page_size, d];
   // sequence b's keys [e * page_size, (e + 1) * page_size) live in page
@@ -128,6 +131,7 @@ int make_q_tmap(CUtensorMap* map, const void* q, uint64_t total_q, int Hq, int d
 int launch_attn_mma(const AttnArgs& a, cudaStream_t stream);
 // The same as a part of shared-prefix decode (a.part_slots, a.chain, ...).
 int launch_attn_mma_shared(const AttnArgs& a, cudaStream_t stream);
+int attn_mma_block_tokens(int G, int64_t tokens);   // of `tokens` query tokens in all
 
 // Split-KV decode with the merge done on chip: the num_splits (<= 16) chunks
 // of one (sequence, KV head) form a thread-block cluster that folds its
@@ -167,7 +171,8 @@ struct SharedPlan {
   int32_t* grp_q;     // [groups + 1] first query token of each group
   int32_t* grp_k;     // [groups + 1] running sum of the prefixes' keys
   int32_t* grp_pages; // [groups + 1] first entry of the prefixes' pages
-  int32_t* grp_unit;  // [groups + 1] running sum of the tcgen05 kernel's units of work
+  int32_t* grp_unit;  // [groups + 1] running sum of the tcgen05 kernel's units of work, or
+                      // (tile_keys 0) of the warp-level kernel's row blocks
   int32_t* quota;     // [1] units of one thread block
   int32_t* row_pos;   // [batch * q_len] position of each query token
 };
@@ -210,6 +215,7 @@ int set_hooks_attn_mma(long long limit, int skip);
 int set_hooks_prefill_tc(long long limit, int skip);
 int set_hooks_decode_tc(long long limit, int skip);
 int set_hooks_prefix_tc(long long limit, int skip);
+int set_hooks_pages(long long limit, int skip);
 
 // Thread-local error text used by the C ABI.
 void set_error(const char* fmt, ...);

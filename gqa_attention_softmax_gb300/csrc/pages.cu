@@ -909,6 +909,9 @@ unsigned copy_blocks() { return static_cast<unsigned>(sm_count()) * 8u; }   // 6
 
 }  // namespace
 
+// (the move kernel has waits but no K/V tiles: the limit is all that counts here)
+SINKATTN_DEFINE_SET_HOOKS(set_hooks_pages)
+
 int read_status_pages(cudaStream_t s, int* status) {
   int zero = 0;
   if (cudaMemcpyFromSymbolAsync(status, g_status_pages, sizeof(int), 0, cudaMemcpyDeviceToHost,
@@ -963,6 +966,7 @@ int sinkattn_pages_reserve(int32_t* table, int32_t num_pages, int32_t page_size,
     rc = make_pools(t, k_pages, v_pages, num_layers, layer_stride, num_kv_heads, row_bytes, &b);
   if (rc) return rc;
   if (total_new < 0) return refuse(SINKATTN_INVALID_ARG, "total_new must be non-negative");
+  if (total_new >= (1 << 30)) return refuse(SINKATTN_UNSUPPORTED, "total_new reaches 2^30");
   if (n == 0 && total_new > 0) return refuse(SINKATTN_INVALID_ARG, "new tokens without sequences");
   if (n == 0 || total_new == 0) return SINKATTN_OK;
   if (!cu_new || !slots || !aligned(cu_new, 4) || !aligned(slots, 4))

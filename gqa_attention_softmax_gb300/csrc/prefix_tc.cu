@@ -799,12 +799,13 @@ __global__ void __launch_bounds__(PxCfg<D, FP8>::LB_THREADS, 1)
       item_done(k);
     }
     // rows of groups without a prefix: no block has units of theirs. All
-    // blocks share the rows of each group, or with many groups the groups.
-    const int nb = static_cast<int>(gridDim.x);
-    const bool many = p.groups > nb;
-    const int width = (many ? 1 : nb) * NT * 128;
-    const int mine = (many ? 0 : static_cast<int>(blockIdx.x)) * NT * 128 + tt * 128 + row;
-    for (int g = many ? blockIdx.x : 0; g < p.groups; g += many ? nb : 1) {
+    // warps share the rows of each group, or with many groups the groups.
+    const int warps = static_cast<int>(gridDim.x) * NT * 4;
+    const int me = static_cast<int>(blockIdx.x) * NT * 4 + (warp - 2);
+    const bool many = p.groups > warps;
+    const int width = (many ? 1 : warps) * 32;
+    const int mine = (many ? 0 : me) * 32 + lane;
+    for (int g = many ? me : 0; g < p.groups; g += many ? warps : 1) {
       if (gk[g + 1] > gk[g]) continue;
       const long long n = static_cast<long long>(gq[g + 1] - gq[g]) * p.Hq * p.splits;
       for (long long i = mine; i < n; i += width) {

@@ -455,3 +455,55 @@ def test_many_short_items_repeat_bit_for_bit(d, fp8):
                 check(out, lse, x, h)
                 first[ps] = out, lse
             assert torch.equal(out, first[ps][0]) and torch.equal(lse, first[ps][1])
+
+
+@gpu
+@pytest.mark.parametrize("kernel", ["auto", "warp"])
+@pytest.mark.parametrize("d,fp8", [(64, False), (128, False), (64, True)])
+def test_more_groups_than_are_staged(d, fp8, kernel):
+    """700 groups, a third of them without a prefix, more row blocks than groups in some."""
+    rng = random.Random(3)
+    groups = [(rng.choice([0, 1, 2]), [rng.randint(1, 20) for _ in range(rng.randint(0, 3))])
+              for _ in range(690)] + [(3, [2] * 40)] + [(1, [3])] * 9
+    x, h = make(groups, 1, 16, 2, d, 16, seed=2, fp8=fp8)
+    g = {k: v.cuda() for k, v in x.items()}
+    sa.sinkattn_set_decode_kernel(kernel)
+    try:
+        out, lse = call(g, h, prefix_splits=2)
+    finally:
+        sa.sinkattn_set_decode_kernel("auto")
+    check(out, lse, x, h)
+
+
+@gpu
+def test_more_sequences_than_are_staged():
+    """3000 sequences at d 128: the own pass reads lengths from memory, not from its copy."""
+    rng = random.Random(5)
+    x, h = make([(2, [rng.randint(1, 9) for _ in range(1700)]), (0, [rng.randint(1, 30) for _ in range(1300)])],
+                1, 2, 1, 128, 16, seed=4)
+    g = {k: v.cuda() for k, v in x.items()}
+    out, lse = call(g, h)
+    check(out, lse, x, h)
+
+
+@gpu
+def test_call_on_another_stream_keeps_its_workspace():
+    """The workspace that a call on a side stream allocates is not handed out to the current
+    stream while the side stream still runs."""
+    x, h = make([(40, [5] * 30)], 1, 64, 8, 64, 16, seed=9)
+    g = {k: v.cuda() for k, v in x.items()}
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    got = []
+    with torch.cuda.stream(st):
+        torch.cuda._sleep(20_000_000)   # the call waits behind this on its stream
+    for _ in range(4):
+        got.append(call(g, h, stream=st))
+        # the same sizes on the current stream, at once overwritten
+        n = sa.sinkattn_decode_shared_workspace_bytes(
+            30, 1, 64, 64, 1, *sa.sinkattn_decode_shared_default_splits(30, 1, 64, 8, 64, 1, 640, 5))
+        torch.empty(n, dtype=torch.uint8, device="cuda").fill_(0xff)
+    st.synchronize()
+    torch.cuda.synchronize()
+    for o, l in got:
+        check(o, l, x, h)
