@@ -363,6 +363,7 @@ def sinkattn_set_decode_kernel(kind) -> None:
     "tcgen05" (or the integer codes of include/sinkattn.h)."""
     code = DECODE_KERNELS[kind] if isinstance(kind, str) else int(kind)
     _check(lib().sinkattn_set_decode_kernel(code))
+    _shared_sizes.cache_clear()   # (the default split counts go by the kernel)
 
 
 def sinkattn_decode_split_fp8(q, k, v, k_scale, v_scale, kv_indptr, q_len, max_kv_len,
@@ -456,13 +457,19 @@ def _stream_of(dev, stream):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _made(t, stream):
-    """A tensor allocated here, on the current stream's account, for kernels on
-    `stream`: its memory is not handed out again before they are done."""
-    if stream is not None:
-        t.record_stream(stream if isinstance(stream, torch.cuda.Stream)
-                        else torch.cuda.ExternalStream(_stream_of(t.device, stream),
-                                                       device=t.device))
+def _new(shape, dtype, dev, stream, kept=True, make=torch.empty):
+    """A tensor for kernels on `stream`, taken from that stream's memory: what
+    its bytes held before may still be read on another stream. One that the
+    caller gets (`kept`) is used on the current stream too."""
+    if stream is None:
+        return make(shape, dtype=dtype, device=dev)
+    here = torch.cuda.current_stream(dev)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream_of(dev, stream), device=dev)
+    with torch.cuda.stream(stream):
+        t = make(shape, dtype=dtype, device=dev)
+    if kept and stream.cuda_stream != here.cuda_stream:
+        t.record_stream(here)
     return t
 
 
@@ -539,11 +546,11 @@ def _decode_shared(entry, pool_dtype, scales, q, k_pages, v_pages, kv_indptr, pa
         dev.index, int(prefix_splits), int(num_splits), batch, q_len, Hq, Hkv, d, groups,
         max_prefix_len, max_suffix_len)
     if workspace is None:
-        workspace = _made(torch.empty((need,), dtype=torch.uint8, device=dev), stream)
+        workspace = _new((need,), torch.uint8, dev, stream, kept=False)
     elif not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
         raise SinkAttnError(INVALID_ARG, "workspace must be contiguous and on %s" % dev)
     if out is None:
-        out = _made(torch.empty_like(q), stream)
+        out = _new(q.shape, torch.bfloat16, dev, stream)
         out_p = out.data_ptr()
     else:
         out_p = _need(out, "out", torch.bfloat16, dev, q.shape)
@@ -551,7 +558,7 @@ def _decode_shared(entry, pool_dtype, scales, q, k_pages, v_pages, kv_indptr, pa
     if lse is not None:
         lse_p = _need(lse, "lse", f32, dev, (rows, Hq))
     elif return_lse:
-        lse = _made(torch.empty((rows, Hq), dtype=f32, device=dev), stream)
+        lse = _new((rows, Hq), f32, dev, stream)
         lse_p = lse.data_ptr()
     if batch == 0:   # (an empty tensor has no address to check)
         return out, lse
@@ -644,30 +651,34 @@ class PageTable:
     least sinkattn_pages_table_ints() words that holds a table already; without
     one, a new buffer on ``device`` is allocated and initialised (every page
     free, every sequence empty). The parts are views of ``state``."""
-    __slots__ = ("state", "num_pages", "page_size", "max_seqs", "max_pages", "args", "device")
+    __slots__ = ("_args", "_state", "device")
 
     def __init__(self, state, num_pages, page_size, max_seqs, max_pages, device="cuda",
                  stream=None):
-        self.num_pages, self.page_size = num_pages, page_size
-        self.max_seqs, self.max_pages = max_seqs, max_pages
         need = 16 + max_seqs * (8 + max_pages) + 4 * num_pages
         new = state is None
         if new:
-            state = _made(torch.empty((sinkattn_pages_table_ints(num_pages, max_seqs, max_pages),),
-                                      dtype=torch.int32, device=device), stream)
+            words = sinkattn_pages_table_ints(num_pages, max_seqs, max_pages)
+            state = _new((words,), torch.int32, torch.device(device), stream)
         self.device = _need_cuda(state, "state")
         ptr = _need(state, "state", torch.int32, self.device, 1)
         if state.shape[0] < need:
             raise SinkAttnError(INVALID_ARG, "state has %d words, a table of these sizes %d" % (
                 state.shape[0], need))
-        self.state = state
-        # what every entry point takes first (the buffer stays where it is while `state` lives)
-        self.args = (ptr, num_pages, page_size, max_seqs, max_pages)
+        self._state = state
+        # what every entry point takes first (the buffer stays where it is while the table lives)
+        self._args = (ptr, num_pages, page_size, max_seqs, max_pages)
         if new:
             sinkattn_pages_init(self, stream=stream)
 
+    state = property(lambda self: self._state)
+    num_pages = property(lambda self: self._args[1])
+    page_size = property(lambda self: self._args[2])
+    max_seqs = property(lambda self: self._args[3])
+    max_pages = property(lambda self: self._args[4])
+
     def _part(self, at, n):
-        return self.state[at:at + n]
+        return self._state[at:at + n]
 
     @property
     def free_count(self):
@@ -718,7 +729,7 @@ def _pools(table, k_pages, v_pages):
 def sinkattn_pages_init(table, stream=None) -> None:
     """Every page free (page 0 is the first to be taken), every sequence empty."""
     dev = table.device
-    _launch(dev, lib().sinkattn_pages_init, *table.args, _stream_of(dev, stream))
+    _launch(dev, lib().sinkattn_pages_init, *table._args, _stream_of(dev, stream))
 
 
 def sinkattn_pages_reserve(table, seq_ids, cu_new, total_new, k_pages, v_pages, slots=None,
@@ -733,11 +744,11 @@ def sinkattn_pages_reserve(table, seq_ids, cu_new, total_new, k_pages, v_pages, 
     cu_p = _need(cu_new, "cu_new", torch.int32, dev, (n + 1,))
     total_new = int(total_new)
     if slots is None:
-        slots = _made(torch.empty((max(total_new, 0),), dtype=torch.int32, device=dev), stream)
+        slots = _new((max(total_new, 0),), torch.int32, dev, stream)
         slots_p = slots.data_ptr()
     else:
         slots_p = _need(slots, "slots", torch.int32, dev, (total_new,))
-    _launch(dev, lib().sinkattn_pages_reserve, *table.args, ids_p, cu_p, n, total_new,
+    _launch(dev, lib().sinkattn_pages_reserve, *table._args, ids_p, cu_p, n, total_new,
             *_pools(table, k_pages, v_pages), slots_p, _stream_of(dev, stream))
     return slots
 
@@ -748,7 +759,7 @@ def sinkattn_pages_fork(table, src_ids, dst_ids, stream=None) -> None:
     dev = table.device
     src_p = _need(src_ids, "src_ids", torch.int32, dev, 1)
     dst_p = _need(dst_ids, "dst_ids", torch.int32, dev, src_ids.shape)
-    _launch(dev, lib().sinkattn_pages_fork, *table.args, src_p, dst_p, src_ids.shape[0],
+    _launch(dev, lib().sinkattn_pages_fork, *table._args, src_p, dst_p, src_ids.shape[0],
             _stream_of(dev, stream))
 
 
@@ -759,7 +770,7 @@ def sinkattn_pages_truncate(table, seq_ids, new_lens=None, stream=None) -> None:
     ids_p = _need(seq_ids, "seq_ids", torch.int32, dev, 1)
     new_p = None if new_lens is None else _need(new_lens, "new_lens", torch.int32, dev,
                                                 seq_ids.shape)
-    _launch(dev, lib().sinkattn_pages_truncate, *table.args, ids_p, new_p, seq_ids.shape[0],
+    _launch(dev, lib().sinkattn_pages_truncate, *table._args, ids_p, new_p, seq_ids.shape[0],
             _stream_of(dev, stream))
 
 
@@ -768,11 +779,11 @@ def sinkattn_pages_compact(table, k_pages, v_pages, page_map=None, stream=None):
     page_map, int32 [num_pages]: each old page's new index, -1 where it was free."""
     dev = table.device
     if page_map is None:
-        page_map = _made(torch.empty((table.num_pages,), dtype=torch.int32, device=dev), stream)
+        page_map = _new((table.num_pages,), torch.int32, dev, stream)
         map_p = page_map.data_ptr()
     else:
         map_p = _need(page_map, "page_map", torch.int32, dev, (table.num_pages,))
-    _launch(dev, lib().sinkattn_pages_compact, *table.args, *_pools(table, k_pages, v_pages),
+    _launch(dev, lib().sinkattn_pages_compact, *table._args, *_pools(table, k_pages, v_pages),
             map_p, _stream_of(dev, stream))
     return page_map
 
@@ -786,15 +797,15 @@ def sinkattn_pages_lists(table, seq_ids, kv_indptr=None, page_indptr=None, page_
     n = seq_ids.shape[0]
     make = torch.empty if n > 0 else torch.zeros   # an empty batch writes nothing
     if kv_indptr is None:
-        kv_indptr = _made(make((n + 1,), dtype=torch.int32, device=dev), stream)
+        kv_indptr = _new((n + 1,), torch.int32, dev, stream, make=make)
     if page_indptr is None:
-        page_indptr = _made(make((n + 1,), dtype=torch.int32, device=dev), stream)
+        page_indptr = _new((n + 1,), torch.int32, dev, stream, make=make)
     if page_indices is None:
-        page_indices = _made(make((n * table.max_pages,), dtype=torch.int32, device=dev), stream)
+        page_indices = _new((n * table.max_pages,), torch.int32, dev, stream, make=make)
     kv_p = _need(kv_indptr, "kv_indptr", torch.int32, dev, (n + 1,))
     pp_p = _need(page_indptr, "page_indptr", torch.int32, dev, (n + 1,))
     pi_p = _need(page_indices, "page_indices", torch.int32, dev, 1)
-    _launch(dev, lib().sinkattn_pages_lists, *table.args, ids_p, n, kv_p, pp_p, pi_p,
+    _launch(dev, lib().sinkattn_pages_lists, *table._args, ids_p, n, kv_p, pp_p, pi_p,
             page_indices.shape[0], _stream_of(dev, stream))
     return kv_indptr, page_indptr, page_indices
 

@@ -179,7 +179,7 @@ int append(const void* k, const void* v, int64_t k_stride, int64_t v_stride, con
   const int64_t blocks1 = (tokens * per + 255) / 256;
   const int64_t runs = blocks1 >= 8LL * sm_count() ? 512 : 256;
   p.per_block = static_cast<int>(std::max<int64_t>(1, runs / per));
-  const unsigned blocks = static_cast<unsigned>((tokens + p.per_block - 1) / p.per_block);
+  const unsigned blocks = static_cast<unsigned>((int64_t{tokens} + p.per_block - 1) / p.per_block);
   auto kern = d == 64 ? (fp8 ? append_kernel<64, true> : append_kernel<64, false>)
                       : (fp8 ? append_kernel<128, true> : append_kernel<128, false>);
   kern<<<blocks, 256, 0, static_cast<cudaStream_t>(stream)>>>(p);

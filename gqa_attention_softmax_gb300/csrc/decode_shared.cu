@@ -210,7 +210,7 @@ int launch_shared_plan(const int32_t* kv_indptr, const int32_t* page_indptr,
                        int32_t max_suffix, int32_t block_tokens, int32_t tile_keys, int32_t Hkv,
                        int32_t window, int32_t splits, const SharedCost& cost, const SharedPlan& plan,
                        cudaStream_t stream) {
-  // a row block of T tiles meets at most (T - 1) / quota + 2 runs of units
+  // a row block of T tiles meets at most ceil((T - 1) / quota) + 1 runs of units
   const int64_t tiles =
       tile_keys > 0 ? (static_cast<int64_t>(max_prefix) + tile_keys - 1) / tile_keys : 1;
   const int quota_min =

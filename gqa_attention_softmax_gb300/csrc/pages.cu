@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(kThreads)
       const int count = hdr[H_FREE];
       int status = SINKATTN_OK;
       if (cu[0] != 0 || cu[n] != total_new) status = SINKATTN_BAD_LENGTHS;
-      else if (bad) status = SINKATTN_BAD_PAGES;
+      else if (bad || count < 0 || count > t.N) status = SINKATTN_BAD_PAGES;
       else if (need > count) status = SINKATTN_OUT_OF_PAGES;
       if (status) atomicExch(&g_status_pages, status);
       ok_s = hdr[H_OK] = status == SINKATTN_OK;
@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(kThreads)
   seen_clear(t);
   const int count = __ldcg(&hdr[H_FREE]);
   __syncthreads();
-  bool bad = false;
+  bool bad = count < 0 || count > t.N;   // (not a table)
   for (int i = tid; i < n; i += kThreads) {
     const int id = ids[i], to = new_lens ? new_lens[i] : 0;
     if (!t.seq_ok(id) || seen_twice(id)) {
@@ -770,12 +770,12 @@ __global__ void __launch_bounds__(256)
     pages += part[1][w];
   }
   const int len = len_of(i), mine = t.pages(max(0, len));
-  const bool fits = pages + mine <= capacity;
+  const bool fits = pages + mine <= capacity && tokens + max(0, len) <= INT32_MAX;
   if (tid == 0) {
     if (len < 0) atomicExch(&g_status_pages, SINKATTN_BAD_PAGES);
     else if (!fits) atomicExch(&g_status_pages, SINKATTN_BAD_LENGTHS);
     if (i == 0) kv_indptr[0] = page_indptr[0] = 0;
-    kv_indptr[i + 1] = static_cast<int>(tokens + max(0, len));
+    kv_indptr[i + 1] = static_cast<int>(min(tokens + max(0, len), static_cast<long long>(INT32_MAX)));
     page_indptr[i + 1] = static_cast<int>(min(pages + mine, static_cast<long long>(capacity)));
   }
   if (!fits || len < 0) return;

@@ -371,7 +371,11 @@ SINKATTN_API int sinkattn_decode_fp8(const void* q, const void* k, const void* v
  *   max_prefix_len / max_suffix_len (host) bound prefix_lens[g] and
  *   Lk_b - prefix_lens[g]; lengths that break one of these rules make the
  *   call record SINKATTN_BAD_LENGTHS and treat the sequence's or group's own
- *   part as empty (sinkattn_debug_status).
+ *   part as empty (sinkattn_debug_status); with a group_indptr that does not
+ *   cut the batch, no group has a prefix.
+ *   sinkattn_set_decode_kernel decides for the prefixes too: AUTO takes the
+ *   tcgen05 kernel where a group has more than 64 query rows per KV head on
+ *   average.
  *   prefix_splits / num_splits: KV chunks of a prefix and of a sequence's own
  *   keys; <= 0 selects sinkattn_decode_shared_default_splits().
  *   workspace: at least sinkattn_decode_shared_workspace_bytes() bytes for
@@ -456,10 +460,11 @@ SINKATTN_API int sinkattn_append_paged_fp8(const void* k, const void* v, int64_t
  * page taken is page 0) and every sequence empty.
  * A call that cannot be served as a whole changes nothing and records
  * SINKATTN_OUT_OF_PAGES, SINKATTN_BAD_PAGES (an id outside [0, max_seqs), an
- * id twice, a length the table cannot hold) or SINKATTN_BAD_LENGTHS (cu_new
- * contradicts total_new); see sinkattn_debug_status. Calls on one table must
+ * id twice, a length the table cannot hold, a free count outside
+ * [0, num_pages]) or SINKATTN_BAD_LENGTHS (cu_new contradicts total_new); see
+ * sinkattn_debug_status. Calls on one table must
  * be ordered (one stream, or events); max_seqs <= 2^18, max_seqs * max_pages
- * < 2^30, page_size as for the paged attention.
+ * < 2^30, total_new < 2^30, page_size as for the paged attention.
  * Where a call copies pages it takes the pools of all layers:
  *   k_pages, v_pages [num_layers][num_pages][Hkv][page_size] rows of
  *   row_bytes bytes (d * 2, or d for codes; a multiple of 16), one layer
@@ -480,6 +485,7 @@ SINKATTN_API int sinkattn_pages_init(int32_t* table, int32_t num_pages, int32_t 
  * its own, with the rows in use copied in every layer (copy on write): all
  * writers do, except that when every holder writes in this call the first of
  * them keeps the page. A call that cannot be served fills slots with -1.
+ * With total_new 0 nothing is read or written.
  */
 SINKATTN_API int sinkattn_pages_reserve(int32_t* table, int32_t num_pages, int32_t page_size,
                                         int32_t max_seqs, int32_t max_pages,
@@ -526,8 +532,8 @@ SINKATTN_API int sinkattn_pages_compact(int32_t* table, int32_t num_pages, int32
  * The paged attention's view of n sequences of a table: kv_indptr [n + 1] and
  * page_indptr [n + 1] (running sums of lengths and of page counts), and their
  * page lists one after the other in page_indices (capacity entries; what lies
- * past the last list stays as it was). Lists that do not fit record
- * SINKATTN_BAD_LENGTHS and are left out; an id outside the table counts as an
+ * past the last list stays as it was). Lists that do not fit, and lengths
+ * whose sum passes 2^31 - 1, record SINKATTN_BAD_LENGTHS and are left out; an id outside the table counts as an
  * empty sequence and records SINKATTN_BAD_PAGES.
  */
 SINKATTN_API int sinkattn_pages_lists(const int32_t* table, int32_t num_pages, int32_t page_size,

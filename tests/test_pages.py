@@ -295,6 +295,69 @@ def test_other_streams_and_empty_calls():
     p.check()
 
 
+@gpu
+@pytest.mark.parametrize("count", [-1, 31, 2 ** 31 - 1, -2 ** 31])
+def test_a_buffer_that_holds_no_table_is_refused(count):
+    """A free count that no table has would index before or behind the free list."""
+    p = Pair(30, 16, 4, 8)
+    p.reserve([1], [40])
+    free = p.table.free_count.item()
+    p.table.free_count.fill_(count)
+    before = p.used().copy()
+    slots = sa.sinkattn_pages_reserve(p.table, i32([2]), i32([0, 20]), 20, p.k, p.v)
+    assert sa.sinkattn_debug_status() == BAD_PAGES
+    assert (slots == -1).all()
+    sa.sinkattn_pages_truncate(p.table, i32([1]))
+    assert sa.sinkattn_debug_status() == BAD_PAGES
+    np.testing.assert_array_equal(np.delete(p.used(), range(1, 16)), np.delete(before, range(1, 16)))
+    p.table.free_count.fill_(free)
+    p.check()
+
+
+@gpu
+def test_lists_whose_lengths_pass_32_bits():
+    M = 1 << 20
+    table = sa.PageTable(None, 64, 256, 9, M)
+    table.page_list.fill_(7)
+    table.seq_lens.fill_(M * 256)
+    kv, ptr, pages = sa.sinkattn_pages_lists(table, torch.arange(9, dtype=torch.int32, device="cuda"))
+    assert sa.sinkattn_debug_status() == BAD_LENGTHS
+    assert kv.tolist() == [min(i * M * 256, 2 ** 31 - 1) for i in range(10)]
+    assert ptr.tolist() == [i * M for i in range(10)]
+    assert (pages[:7 * M] == 7).all()   # (the eighth and ninth are left out)
+
+
+@gpu
+def test_results_of_a_call_on_another_stream_come_from_its_memory():
+    """What a call on a side stream allocates does not lie where the current stream still
+    reads, and is not handed out again while the current stream still uses it."""
+    p = Pair(600, 16, 8, 80)
+    st = torch.cuda.Stream()
+    ids, cu = i32([0]), i32([0, 1000])
+    torch.cuda.synchronize()
+    old = torch.full((1000,), 5, dtype=torch.int32, device="cuda")
+    torch.cuda._sleep(20_000_000)
+    late = old + 1       # waits behind the sleep, reads what is given back next
+    del old
+    slots = sa.sinkattn_pages_reserve(p.table, ids, cu, 1000, p.k, p.v, stream=st)
+    st.synchronize()
+    assert (late == 6).all()
+    assert slots.tolist() == list(range(1000))
+    torch.cuda._sleep(20_000_000)
+    kept = slots + 0     # on the current stream, behind the sleep
+    del slots
+    with torch.cuda.stream(st):
+        torch.full((1000,), -9, dtype=torch.int32, device="cuda")
+    st.synchronize()
+    assert kept.tolist() == list(range(1000))
+
+
+def test_a_table_keeps_its_buffer_and_sizes():
+    for name in ("state", "num_pages", "page_size", "max_seqs", "max_pages"):
+        with pytest.raises(AttributeError):
+            setattr(sa.PageTable.__new__(sa.PageTable), name, 1)
+
+
 # -------------------------------------------------------------------- append
 @gpu
 @pytest.mark.parametrize("d", [64, 128])
