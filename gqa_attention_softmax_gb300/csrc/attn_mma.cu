@@ -228,6 +228,13 @@ __global__ void __launch_bounds__(MmaCfg<D, RT, TG, KT, NST, FP8, SHARED>::THREA
         if (leader && Lk > np * p.page_size) atomicExch(&g_status_attn_mma, SINKATTN_BAD_LENGTHS);
         pc.start(p.page_indices + e0, np, first / p.page_size, lane);
       }
+      // the pool row of key a in its page. SHARED: boxes behind the last key come
+      // as zeros, from a row before the pool (behind a prefix lies one
+      // sequence's own, and its infinities and NaN with it)
+      auto row_of = [&](int page, int a) -> int {
+        if (SHARED && a >= Lk) return -p.box_rows;
+        return (page * p.Hkv + kvh) * p.page_size + a % p.page_size;
+      };
       int issued = 0;
       const int skip_tile = hook_skip_tile();
       for (int i = 0; i < ntiles; ++i) {
@@ -253,7 +260,7 @@ __global__ void __launch_bounds__(MmaCfg<D, RT, TG, KT, NST, FP8, SHARED>::THREA
             const int a = j0 + min(lane, nbox - 1) * p.box_rows;
             const int page = pc.get(j0 / p.page_size, a / p.page_size, lane);
             if (lane < nbox) {
-              const int row = (page * p.Hkv + kvh) * p.page_size + a % p.page_size;
+              const int row = row_of(page, a);
               const int off = (a - j0) * D;
               tma_load_2d_hint(kc + off, &tmK, 0, row, &full[st], policy);
               tma_load_2d_hint(vc + off, &tmV, 0, row, &full[st], policy);
@@ -284,7 +291,7 @@ __global__ void __launch_bounds__(MmaCfg<D, RT, TG, KT, NST, FP8, SHARED>::THREA
           const int a = j0 + min(lane, nbox - 1) * p.box_rows;
           const int page = pc.get(j0 / p.page_size, a / p.page_size, lane);
           if (lane < nbox) {
-            const int row = (page * p.Hkv + kvh) * p.page_size + a % p.page_size;
+            const int row = row_of(page, a);
             const int off = (a - j0) * 128;
 #pragma unroll
             for (int sub = 0; sub < C::NSUB; ++sub) {

@@ -681,7 +681,8 @@ __global__ void __launch_bounds__(DtcCfg<RR, FP8>::THREADS, 1)
             static_cast<size_t>(q_start + t.q0 + tl) * p.Hq + t.kvh * G + (row - tl * G);
         // (m', lr): m' + ln lr = m + ln l, the chunk's exact log-sum-exp
         float2 md;
-        if (mlr.x == NEG_INF || !(mlr.z > 0.f)) {
+        // (SHARED: the merge leaves empty slots out, so a NaN sum is none)
+        if ((mlr.x == NEG_INF || !(mlr.z > 0.f)) && !(SHARED && mlr.z != mlr.z)) {
           md = make_float2(NEG_INF, 0.f);
         } else {
           md.x = mlr.x * lscale + (lg2(mlr.y) - lg2(mlr.z)) * kLn2;

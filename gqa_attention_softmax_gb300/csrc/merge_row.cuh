@@ -116,7 +116,8 @@ __device__ __forceinline__ void merge_row(const float* md, const float* acc, flo
   if (lse_out != nullptr && lane == 0) *lse_out = dsum > 0.f ? M + lg2(dsum) * kLn2 : NEG_INF;
 }
 
-// The same fold for rows of which many slots are empty (d_s = 0): R rows per
+// The same fold for rows of which many slots are empty (d_s = 0; a NaN sum is
+// a row's answer, and no empty slot): R rows per
 // warp, 32 / R lanes each for the (m, d) pairs (S <= 32 / R), and then only the
 // accumulators that have a weight. A row's loads depend on its weights, two
 // memory round trips, so the rows of a warp take theirs together: eight
@@ -134,7 +135,7 @@ __device__ __forceinline__ void merge_rows_sparse(const float* part_md, const fl
                           ? __ldcg(reinterpret_cast<const float2*>(part_md + (row * S + s) * 2))
                           : make_float2(kNegInf, 0.f);
   const float sink = real && sinks ? sinks[static_cast<int>(row % Hq)] : kNegInf;
-  const bool some = mine.y > 0.f;
+  const bool some = mine.y != 0.f;
   float M = fmaxf(sink, some ? mine.x : kNegInf);
 #pragma unroll
   for (int off = W / 2; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
@@ -142,9 +143,9 @@ __device__ __forceinline__ void merge_rows_sparse(const float* part_md, const fl
   float total = w * mine.y;
 #pragma unroll
   for (int off = W / 2; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
-  if (sink != kNegInf) total += ex2((sink - M) * kLog2e);
-  w *= total > 0.f ? 1.f / total : 0.f;
-  if (lse != nullptr && real && s == 0) lse[row] = total > 0.f ? M + lg2(total) * kLn2 : kNegInf;
+  if (sink != kNegInf) total += sink == M ? 1.f : ex2((sink - M) * kLog2e);
+  w *= total != 0.f ? 1.f / total : 0.f;
+  if (lse != nullptr && real && s == 0) lse[row] = total != 0.f ? M + lg2(total) * kLn2 : kNegInf;
   const uint32_t vote = __ballot_sync(0xffffffffu, some);
   uint32_t left[R];
   float o[R][VEC];
@@ -214,13 +215,14 @@ __device__ __forceinline__ void merge_row_sparse(const float* md, const float* a
   for (int s0 = 0; s0 < S; s0 += 32) {
     const float2 mine = s0 + lane < S ? __ldcg(reinterpret_cast<const float2*>(md + 2 * (s0 + lane)))
                                       : make_float2(kNegInf, 0.f);
-    const bool some = mine.y > 0.f;
+    const bool some = mine.y != 0.f;
+    const uint32_t vote = __ballot_sync(0xffffffffu, some);
+    if (vote == 0) continue;
     float top = some ? mine.x : kNegInf;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
     const float m1 = fmaxf(M, top);
-    if (m1 == kNegInf) continue;   // no slot so far holds a key
-    const float keep = (M == kNegInf) ? 0.f : ex2((M - m1) * kLog2e);
+    const float keep = M == m1 ? 1.f : (M == kNegInf ? 0.f : ex2((M - m1) * kLog2e));
     M = m1;
     const float w = some ? ex2((mine.x - M) * kLog2e) : 0.f;
     float sum = w * mine.y;
@@ -229,7 +231,7 @@ __device__ __forceinline__ void merge_row_sparse(const float* md, const float* a
     total = total * keep + sum;
 #pragma unroll
     for (int e = 0; e < VEC; ++e) o[e] *= keep;
-    for (uint32_t left = __ballot_sync(0xffffffffu, some); left; left &= left - 1) {
+    for (uint32_t left = vote; left; left &= left - 1) {
       const int s = __ffs(left) - 1;
       const float wu = __shfl_sync(0xffffffffu, w, s);
       const float* src = acc + static_cast<size_t>(s0 + s) * D + lane * VEC;
@@ -237,12 +239,12 @@ __device__ __forceinline__ void merge_row_sparse(const float* md, const float* a
       for (int e = 0; e < VEC; ++e) o[e] = fmaf(__ldcg(src + e), wu, o[e]);
     }
   }
-  const float inv = total > 0.f ? 1.f / total : 0.f;
+  const float inv = total != 0.f ? 1.f / total : 0.f;
   __nv_bfloat16* op = orow + lane * VEC;
 #pragma unroll
   for (int e = 0; e < VEC; e += 2)
     *reinterpret_cast<uint32_t*>(op + e) = pack_bf16x2(o[e] * inv, o[e + 1] * inv);
-  if (lse_out != nullptr && lane == 0) *lse_out = total > 0.f ? M + lg2(total) * kLn2 : kNegInf;
+  if (lse_out != nullptr && lane == 0) *lse_out = total != 0.f ? M + lg2(total) * kLn2 : kNegInf;
 }
 
 }  // namespace sinkattn

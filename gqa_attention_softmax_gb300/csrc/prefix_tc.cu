@@ -430,7 +430,10 @@ __global__ void __launch_bounds__(PxCfg<D, FP8>::LB_THREADS, 1)
         const int page = pc.get(j0 / p.page_size, a / p.page_size, lane);
         __syncwarp();   // (the expected bytes are announced before any lane's copy)
         if (lane < nbox) {
-          const int row = (page * p.Hkv + t.kvh) * p.page_size + a % p.page_size;
+          // (boxes behind the prefix come as zeros, from a row before the pool: what lies
+          // there is one sequence's own, and its infinities and NaN with it)
+          const int row = a < t.keys ? (page * p.Hkv + t.kvh) * p.page_size + a % p.page_size
+                                     : -p.box_rows;
           if constexpr (FP8) {
             uint8_t* codes = smem + C::OFF_CODE + st * C::CODE_STAGE + (a - j0) * D;
             tma_load_2d_hint(codes, &tmK, 0, row, full, policy);
@@ -784,7 +787,7 @@ __global__ void __launch_bounds__(PxCfg<D, FP8>::LB_THREADS, 1)
         if (!pv_wait(tt, steps - 1)) { ok = false; break; }
         tc::fence_after_sync();
       }
-      const bool some = l > 0.f;   // the row sees a key of the chunk
+      const bool some = l != 0.f;   // the row sees a key of the chunk (or a NaN)
       const size_t slot =
           (static_cast<size_t>(t.tok0 + tl) * p.Hq + t.kvh * G + hig) * p.part_slots + t.slot;
       if (n >= 1)

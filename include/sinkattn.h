@@ -381,6 +381,8 @@ SINKATTN_API int sinkattn_decode_fp8(const void* q, const void* k, const void* v
  *   workspace: at least sinkattn_decode_shared_workspace_bytes() bytes for
  *   the split counts in use, 256-byte aligned, device memory; contents on
  *   entry do not matter. Two calls that may overlap need two workspaces.
+ * A sequence whose own keys or values hold NaN gets NaN, in lse too where its
+ * keys do; the other sequences of its group do not.
  * Every other argument and rule is that of sinkattn_decode_paged
  * (num_kv_heads groups of at most 64 query heads). The _fp8 form reads pools
  * of e4m3 codes, uint8 [num_pages, Hkv, page_size, d], with the scales and
@@ -485,6 +487,8 @@ SINKATTN_API int sinkattn_pages_init(int32_t* table, int32_t num_pages, int32_t 
  * its own, with the rows in use copied in every layer (copy on write): all
  * writers do, except that when every holder writes in this call the first of
  * them keeps the page. A call that cannot be served fills slots with -1.
+ * A page keeps what it held before: the attention reads and masks the slots
+ * past a sequence's length, so rows that are written have to be finite.
  * With total_new 0 nothing is read or written.
  */
 SINKATTN_API int sinkattn_pages_reserve(int32_t* table, int32_t num_pages, int32_t page_size,

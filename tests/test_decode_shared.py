@@ -507,3 +507,66 @@ def test_call_on_another_stream_keeps_its_workspace():
     torch.cuda.synchronize()
     for o, l in got:
         check(o, l, x, h)
+
+
+@gpu
+@pytest.mark.parametrize("kernel", ["auto", "warp"])
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("groups,q_len,Hq,Hkv,d,page", [
+    ([(1, [20] + [5] * 9)], 1, 16, 2, 64, 16),            # tiles end behind the prefix
+    ([(3, [64] + [5] * 9), (4, [30, 7])], 1, 64, 8, 64, 32),
+    ([(1, [200, 3, 4])], 3, 64, 4, 128, 64),
+    ([(5, [17] * 12), (1, [40] * 6)], 2, 32, 4, 128, 16),
+    ([(1, [9, 8])], 1, 8, 8, 64, 16),
+    ([(1, [300, 8])], 1, 8, 8, 64, 16),
+])
+@pytest.mark.parametrize("where", ["k_pages", "v_pages"])
+def test_a_sequence_with_nan_keys_spoils_no_other(groups, q_len, Hq, Hkv, d, page, fp8, kernel,
+                                                     where):
+    """The own keys and values of each group's first sequence lie behind the prefix in the list
+    that the prefix is read from: NaN there are that sequence's alone, and its answer is NaN."""
+    x, h = make(groups, q_len, Hq, Hkv, d, page, seed=3, fp8=fp8)
+    g = {k: v.cuda() for k, v in x.items()}
+    firsts = [int(b) for b in x["group_indptr"][:-1]]
+    spoilt = []
+    for b, (pre, _) in zip(firsts, groups):
+        lo, hi = int(x["page_indptr"][b]) + pre, int(x["page_indptr"][b + 1])
+        spoilt += x["page_indices"][lo:hi].tolist()
+    g[where][torch.tensor(spoilt, device="cuda").long()] = 0x7f if fp8 else float("nan")
+    sa.sinkattn_set_decode_kernel(kernel)
+    try:
+        out, lse = call(g, h)
+    finally:
+        sa.sinkattn_set_decode_kernel("auto")
+    assert sa.sinkattn_debug_status() == 0
+    o, l, A = want(x, h)
+    o, A, got = (t.reshape(out.shape) for t in (o, A, out.float().cpu().numpy()))
+    l, gl = l.reshape(lse.shape), lse.cpu().numpy()
+    rest = np.ones(o.shape[0], dtype=bool)
+    for b in firsts:
+        rest[b * q_len:(b + 1) * q_len] = False
+        assert np.isnan(got[b * q_len:(b + 1) * q_len]).all()
+    o, l, A, got, gl = (t[rest] for t in (o, l, A, got, gl))
+    assert np.isfinite(got).all()
+    weight = 2.0 ** -11 if fp8 else 2.0 ** -8
+    low = 2.0 ** -25 * h["keys"] * 6.0 if fp8 else 0.0
+    room = 2.0 ** -8 * np.abs(o) + (weight + 2e-4) * A + low + 1e-6
+    assert (np.abs(got - o) <= room).all()
+    assert np.abs(gl - l).max() <= 1e-4
+
+
+@gpu
+@pytest.mark.parametrize("splits", [(2, 1), (30, 9)])   # several rows a warp; one row of many slots
+def test_a_sink_of_all_weight(splits):
+    x, h = make([(3, [9, 8, 1])], 1, 8, 2, 64, 16, seed=4)
+    x["sinks"][2] = float("inf")
+    x["sinks"][5] = float("-inf")
+    g = {k: v.cuda() for k, v in x.items()}
+    out, lse = call(g, h, prefix_splits=splits[0], num_splits=splits[1])
+    assert (out[:, 2] == 0).all() and (lse[:, 2] == float("inf")).all()
+    x["sinks"][2] = 0.0
+    o, l, A = want(x, h)
+    o, A, got = (t.reshape(out.shape) for t in (o, A, out.float().cpu().numpy()))
+    keep = [0, 1, 3, 4, 5, 6, 7]
+    assert (np.abs(got - o) <= 2.0 ** -8 * np.abs(o) + (2.0 ** -8 + 2e-4) * A + 1e-6)[:, keep].all()
+    assert np.abs(lse.cpu().numpy() - l.reshape(lse.shape))[:, keep].max() <= 1e-4
