@@ -9,8 +9,6 @@
 // same P keys, read once; the own part is a split-KV decode whose page lists
 // start behind the prefix. One small launch derives both parts' lengths and
 // page-list starts from the caller's arrays, so the call needs no host copy.
-#include <algorithm>
-
 #include "common.cuh"
 #include "internal.h"
 
@@ -27,7 +25,7 @@ struct PlanParams {
   const int32_t* prefix_lens;
   int groups, page_shift, batch, q_len, max_prefix, max_suffix, block_tokens, tile_keys, Hkv;
   int window;
-  int quota_min;       // units per block that keep to the splits
+  int splits;          // partials a row block may have
   float class_scale;   // own keys -> class
   SharedCost cost;
   SharedPlan out;
@@ -63,9 +61,11 @@ __global__ void __launch_bounds__(kThreads, 1) shared_plan_kernel(const PlanPara
   __shared__ int sums[32];
   __shared__ int count_s[kClasses], place_s[kClasses];
   __shared__ float own_s[32];
+  __shared__ int longest_s;   // tiles of the longest prefix
   const int tid = threadIdx.x;
   grid_launch_dependents();   // the next launch sets itself up meanwhile, and waits for this one
   if (tid < kClasses) count_s[tid] = 0;
+  if (tid == 0) longest_s = 0;
   // the first sequence of each thread: loads that depend on nothing
   int len0 = 0, page0 = 0, held0 = 0;
   if (tid < p.batch) {
@@ -104,11 +104,17 @@ __global__ void __launch_bounds__(kThreads, 1) shared_plan_kernel(const PlanPara
       }
       // row blocks x KV heads x key tiles (below 2^31: checked on the host)
       units = ((b1 - b0) * p.q_len + p.block_tokens - 1) / p.block_tokens;
-      if (p.tile_keys > 0) units *= p.Hkv * ((len + p.tile_keys - 1) / p.tile_keys);
+      if (p.tile_keys > 0) {
+        const int tiles = (len + p.tile_keys - 1) / p.tile_keys;
+        units *= p.Hkv * tiles;
+        if (b1 > b0) atomicMax(&longest_s, tiles);
+      }
       p.out.grp_q[g] = b0 * p.q_len;
       p.out.grp_pages[g] = first;
     } else if (g < p.groups) {
-      p.out.grp_q[g] = p.batch * p.q_len;
+      // all rows are the first group's, without a prefix
+      if (g == 0 && p.tile_keys == 0) units = (p.batch * p.q_len + p.block_tokens - 1) / p.block_tokens;
+      p.out.grp_q[g] = g == 0 ? 0 : p.batch * p.q_len;
       p.out.grp_pages[g] = p.page_indptr[p.batch];
     }
     const int upto = run + block_sum_scan(len, &total, sums);
@@ -197,7 +203,9 @@ __global__ void __launch_bounds__(kThreads, 1) shared_plan_kernel(const PlanPara
                         static_cast<float>(p.cost.sms);
       quota = max(quota, min(2 * quota, static_cast<int>((all - p.cost.ramp) / p.cost.unit)));
     }
-    *p.out.quota = max(max(quota, p.quota_min), 1);
+    // a row block of T tiles meets at most ceil((T - 1) / quota) + 1 runs of units
+    if (p.splits > 1) quota = max(quota, (longest_s - 1 + p.splits - 2) / (p.splits - 1));
+    *p.out.quota = max(quota, 1);
   }
   if (__syncthreads_or(bad || broken) && tid == 0) atomicExch(&g_status_shared, SINKATTN_BAD_LENGTHS);
 }
@@ -210,11 +218,6 @@ int launch_shared_plan(const int32_t* kv_indptr, const int32_t* page_indptr,
                        int32_t max_suffix, int32_t block_tokens, int32_t tile_keys, int32_t Hkv,
                        int32_t window, int32_t splits, const SharedCost& cost, const SharedPlan& plan,
                        cudaStream_t stream) {
-  // a row block of T tiles meets at most ceil((T - 1) / quota) + 1 runs of units
-  const int64_t tiles =
-      tile_keys > 0 ? (static_cast<int64_t>(max_prefix) + tile_keys - 1) / tile_keys : 1;
-  const int quota_min =
-      splits > 1 ? static_cast<int>(std::max<int64_t>(1, (tiles - 1 + splits - 2) / (splits - 1))) : 1;
   PlanParams p{};
   p.kv_indptr = kv_indptr;
   p.page_indptr = page_indptr;
@@ -230,7 +233,7 @@ int launch_shared_plan(const int32_t* kv_indptr, const int32_t* page_indptr,
   p.tile_keys = tile_keys;
   p.Hkv = Hkv;
   p.window = window;
-  p.quota_min = quota_min;
+  p.splits = splits;
   p.class_scale = static_cast<float>(kClasses) / (static_cast<float>(max_suffix) + 1.f);
   p.cost = cost;
   p.out = plan;

@@ -372,7 +372,7 @@ SINKATTN_API int sinkattn_decode_fp8(const void* q, const void* k, const void* v
  *   Lk_b - prefix_lens[g]; lengths that break one of these rules make the
  *   call record SINKATTN_BAD_LENGTHS and treat the sequence's or group's own
  *   part as empty (sinkattn_debug_status); with a group_indptr that does not
- *   cut the batch, no group has a prefix.
+ *   cut the batch, all keys count as own ones.
  *   sinkattn_set_decode_kernel decides for the prefixes too: AUTO takes the
  *   tcgen05 kernel where a group has more than 64 query rows per KV head on
  *   average.

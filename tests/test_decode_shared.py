@@ -522,7 +522,7 @@ def test_call_on_another_stream_keeps_its_workspace():
 ])
 @pytest.mark.parametrize("where", ["k_pages", "v_pages"])
 def test_a_sequence_with_nan_keys_spoils_no_other(groups, q_len, Hq, Hkv, d, page, fp8, kernel,
-                                                     where):
+                                                  where):
     """The own keys and values of each group's first sequence lie behind the prefix in the list
     that the prefix is read from: NaN there are that sequence's alone, and its answer is NaN."""
     x, h = make(groups, q_len, Hq, Hkv, d, page, seed=3, fp8=fp8)
@@ -570,3 +570,34 @@ def test_a_sink_of_all_weight(splits):
     keep = [0, 1, 3, 4, 5, 6, 7]
     assert (np.abs(got - o) <= 2.0 ** -8 * np.abs(o) + (2.0 ** -8 + 2e-4) * A + 1e-6)[:, keep].all()
     assert np.abs(lse.cpu().numpy() - l.reshape(lse.shape))[:, keep].max() <= 1e-4
+
+
+@gpu
+@pytest.mark.parametrize("d,fp8", [(64, False), (128, False), (64, True), (128, True)])
+def test_a_loose_bound_on_the_prefixes_changes_nothing(d, fp8):
+    x, h = make([(20, [5] * 12), (3, [9] * 7)], 1, 64, 8, d, 16, seed=6, fp8=fp8)
+    g = {k: v.cuda() for k, v in x.items()}
+    got = []
+    for bound in (h["max_prefix"], 1 << 20):
+        got.append(call(g, dict(h, max_prefix=bound), prefix_splits=4, num_splits=1))
+    check(*got[0], x, h)
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+@gpu
+@pytest.mark.parametrize("kernel", ["auto", "warp"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_groups_that_do_not_cut_the_batch_share_nothing(d, kernel):
+    x, h = make([(0, [5 + 3 * i for i in range(20)])], 1, 64, 8, d, 16, seed=8)
+    g = {k: v.cuda() for k, v in x.items()}
+    sa.sinkattn_set_decode_kernel(kernel)
+    try:
+        for cut in ([0, 21], [0, 7, 5, 20], [1, 20]):
+            g["group_indptr"] = torch.tensor(cut, dtype=torch.int32, device="cuda")
+            g["prefix_lens"] = torch.full((len(cut) - 1,), 16, dtype=torch.int32, device="cuda")
+            work = torch.full((1 << 23,), 0x7f, dtype=torch.uint8, device="cuda")
+            out, lse = call(g, dict(h, max_prefix=64), workspace=work)
+            assert sa.sinkattn_debug_status() == BAD_LENGTHS
+            check(out, lse, x, h)
+    finally:
+        sa.sinkattn_set_decode_kernel("auto")
