@@ -438,12 +438,15 @@ int decode_impl(const void* q, const void* k, const void* v, const int32_t* kv_i
 
 // Whether the prefixes take the tcgen05 kernel, which works on row blocks of
 // 256 (128 at least), or the warp-level one, which takes up to 64 rows at a
-// time and re-reads the keys for each.
+// time and re-reads the keys for each. Calls of one group behind 8192 keys,
+// warp-level against tcgen05: 48 rows 19.8 and 20.4 us at d 64, 23.5 and 25.7
+// at d 128; 64 rows 22.5 and 20.9, 37.5 and 25.6; behind 1024 keys 48 rows 13.2
+// and 14.5, 15.3 and 18.3; 64 rows 14.0 and 14.9, 20.0 and 18.4.
 // (A group's sequences come as one run of rows: 4 samples of 8 heads are 32.)
 bool prefix_on_tc(int64_t tokens, int G, int64_t groups) {
   const int kind = g_decode_kernel.load(std::memory_order_relaxed);
   if (kind != SINKATTN_DECODE_AUTO) return kind == SINKATTN_DECODE_TCGEN05;
-  return tokens * G > 64 * groups;
+  return tokens * G > 48 * groups;
 }
 
 // Shared-prefix decode: the sequences' own keys and the groups' prefixes as

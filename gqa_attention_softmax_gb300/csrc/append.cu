@@ -13,7 +13,9 @@
 // q0 s)) with the residual exact in an fma: Markstein's theorem ("Computation
 // of elementary functions on the IBM RISC System/6000", 1990) makes q the
 // correctly rounded quotient where nothing over- or underflows. Scales
-// outside [2^-100, 2^100] take IEEE divisions.
+// outside [2^-100, 2^100] take IEEE divisions. 22000 tokens of 4 heads of 128
+// take 14 us as codes (16.6 with divisions; the bytes alone are 8), bound by
+// the conversions: issue slots 54 %, ALU 50 % busy.
 #include <algorithm>
 
 #include "common.cuh"
@@ -175,7 +177,8 @@ int append(const void* k, const void* v, int64_t k_stride, int64_t v_stride, con
   p.n_slots = static_cast<long long>(num_pages) * page_size;
   const int64_t per = width / (fp8 ? 16 : 8);   // runs of a token
   if (per > (1 << 20)) return refuse(SINKATTN_UNSUPPORTED, "more than 2^20 runs in a token");
-  // two runs a thread, but one while that leaves SMs without a block
+  // two runs a thread, but one while that leaves SMs without a block (22000
+  // tokens as codes 23.2 us with two, 23.8 with one; 64 tokens 11.1 and 10.8)
   const int64_t blocks1 = (tokens * per + 255) / 256;
   const int64_t runs = blocks1 >= 8LL * sm_count() ? 512 : 256;
   p.per_block = static_cast<int>(std::max<int64_t>(1, runs / per));

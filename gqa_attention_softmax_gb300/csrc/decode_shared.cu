@@ -8,7 +8,8 @@
 // group is one attention of (sequences x drafts x query heads) rows over the
 // same P keys, read once; the own part is a split-KV decode whose page lists
 // start behind the prefix. One small launch derives both parts' lengths and
-// page-list starts from the caller's arrays, so the call needs no host copy.
+// page-list starts from the caller's arrays, so the call needs no host copy: a
+// block of 1024 threads, about 4 us of load, barrier and scan latency.
 #include "common.cuh"
 #include "internal.h"
 

@@ -28,8 +28,8 @@
 // block has as many partials as thread blocks worked on it; the merge reads
 // only those.
 //
-// e4m3 pools: the producer copies codes into a ring of their own, four
-// converter warps widen each tile to f16 in the layout the MMAs read (exact:
+// e4m3 pools: the producer copies codes into a ring of their own, two
+// converter warps (four at d 128) widen each tile to f16 in the layout the MMAs read (exact:
 // f16 holds every e4m3 value) and turn Q to f16 once per item; each code is
 // converted once per row block, not once per sequence. The key scale joins
 // the logit scale, the value scale the written accumulator.
@@ -43,7 +43,13 @@
 // its own, which sends the next S while the softmax of the present one runs.
 // A step of 96 keys took 2.8k cycles with one buffer (softmax 1.4k, then P V,
 // S and their latencies; what TMEM leaves at d 128), 2.25k with two and one
-// issuer.
+// issuer, 2.0k with two issuers.
+//
+// Measured: a unit (256 rows, 96 keys) at d 64 1.05 us, at d 128 (128 keys)
+// 1.75 us, the softmax warps' chain; a block's first P comes 6 us after the plan's
+// end, a run's end costs about 3 us at d 128. 512 rows of 8 KV heads behind 8192
+// keys: 22 us; 12288 rows of 4 behind 4032: 89 us, 1.15 PFLOP/s (tensor pipe 48 %
+// of the time, 57 % while blocks run).
 #include <algorithm>
 
 #include "common.cuh"

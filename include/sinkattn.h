@@ -374,7 +374,7 @@ SINKATTN_API int sinkattn_decode_fp8(const void* q, const void* k, const void* v
  *   part as empty (sinkattn_debug_status); with a group_indptr that does not
  *   cut the batch, all keys count as own ones.
  *   sinkattn_set_decode_kernel decides for the prefixes too: AUTO takes the
- *   tcgen05 kernel where a group has more than 64 query rows per KV head on
+ *   tcgen05 kernel where a group has more than 48 query rows per KV head on
  *   average.
  *   prefix_splits / num_splits: KV chunks of a prefix and of a sequence's own
  *   keys; <= 0 selects sinkattn_decode_shared_default_splits().
