@@ -449,6 +449,17 @@ bool prefix_on_tc(int64_t tokens, int G, int64_t groups) {
   return tokens * G > 48 * groups;
 }
 
+// So few keys that every sequence reads its own: two launches instead of four,
+// and what the sequences share comes from L2. By keys x KV heads x head_dim of
+// the whole batch, in millions, us per call shared | not, 4 to 64 sequences: at
+// d 64 2.2: 12.6 | 8.3, 4.4: 14.6 | 8.7, 8.5: 15 to 16.5 | 14.5 to 14.8, 9.7:
+// 16.4 | 15.5, 17: 17.7 to 19.6 | 20.3 to 24.4; at d 128 4.4: 18.5 | 10.0, 9.7:
+// 22.5 | 17.9, 17: 20.9 to 25.8 | 17.8 to 26.1.
+bool few_keys(int64_t batch, int64_t max_prefix, int64_t max_suffix, int64_t Hkv, int64_t d) {
+  return g_decode_kernel.load(std::memory_order_relaxed) == SINKATTN_DECODE_AUTO && batch > 0 &&
+         max_prefix + max_suffix <= (int64_t{10} << 20) / (batch * Hkv * d);
+}
+
 // Shared-prefix decode: the sequences' own keys and the groups' prefixes as
 // two sets of partials of the same rows, folded by one merge.
 size_t shared_plan_bytes(int64_t batch, int64_t q_len, int64_t groups) {
@@ -474,12 +485,15 @@ int decode_shared_impl(const void* q, const void* k_pages, const void* v_pages, 
                                                  num_groups, max_prefix_len, max_suffix_len, &ps,
                                                  &ss);
   if (rc) return rc;
+  const bool alone = prefix_splits <= 0 &&
+                     few_keys(batch, max_prefix_len, max_suffix_len, num_kv_heads, head_dim);
   if (prefix_splits <= 0) prefix_splits = ps;
   if (num_splits <= 0) num_splits = ss;
   if (max_prefix_len == 0) prefix_splits = 0;   // nothing is shared
   AttnArgs a;
-  rc = decode_args(q, k_pages, v_pages, kv_indptr, batch, q_len, max_suffix_len, num_qo_heads,
-                   num_kv_heads, head_dim, sm_scale, causal, window, num_splits, &a);
+  rc = decode_args(q, k_pages, v_pages, kv_indptr, batch, q_len,
+                   max_suffix_len + (alone ? max_prefix_len : 0), num_qo_heads, num_kv_heads,
+                   head_dim, sm_scale, causal, window, num_splits, &a);
   if (rc) return rc;
   if ((rc = check_paged(pg, num_kv_heads))) return rc;
   if (f8) {
@@ -510,6 +524,22 @@ int decode_shared_impl(const void* q, const void* k_pages, const void* v_pages, 
     return fail(SINKATTN_INVALID_ARG, "lse must be 4-byte aligned");
   if (batch == 0) return SINKATTN_OK;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const size_t rows = static_cast<size_t>(batch) * q_len;
+  const size_t plan_bytes = shared_plan_bytes(batch, q_len, num_groups);
+  float* part_acc = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan_bytes);
+  float* part_md = reinterpret_cast<float*>(
+      reinterpret_cast<char*>(part_acc) +
+      ((rows * num_qo_heads * slots * head_dim * 4 + 255) & ~static_cast<size_t>(255)));
+  a.part_acc = part_acc;
+  a.part_md = part_md;
+  if (alone) {
+    set_paged(&a, &pg);
+    if ((rc = launch_attn_mma(a, s))) return rc;
+    const SharedCheck check{kv_indptr,    pg.page_indptr, group_indptr, prefix_lens,    num_groups,
+                            pg.page_size, batch,          q_len,        max_prefix_len, max_suffix_len};
+    return launch_merge_sparse(part_acc, part_md, sinks, static_cast<int32_t>(rows), num_qo_heads,
+                               head_dim, slots, out, lse, &check, s);
+  }
 
   SharedPlan plan;
   plan.own_seq = static_cast<int32_t*>(workspace);
@@ -521,12 +551,6 @@ int decode_shared_impl(const void* q, const void* k_pages, const void* v_pages, 
   plan.grp_unit = plan.grp_pages + num_groups + 1;
   plan.quota = plan.grp_unit + num_groups + 1;
   plan.row_pos = plan.quota + 1;
-  const size_t rows = static_cast<size_t>(batch) * q_len;
-  const size_t plan_bytes = shared_plan_bytes(batch, q_len, num_groups);
-  float* part_acc = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan_bytes);
-  float* part_md = reinterpret_cast<float*>(
-      reinterpret_cast<char*>(part_acc) +
-      ((rows * num_qo_heads * slots * head_dim * 4 + 255) & ~static_cast<size_t>(255)));
   const int G = num_qo_heads / num_kv_heads;
   const bool tc = prefix_on_tc(static_cast<int64_t>(rows), G, num_groups);
   // (at d 128 a block of either pass fills its SM)
@@ -542,8 +566,6 @@ int decode_shared_impl(const void* q, const void* k_pages, const void* v_pages, 
                           window, prefix_splits, cost, plan, s);
   if (rc) return rc;
 
-  a.part_acc = part_acc;
-  a.part_md = part_md;
   a.part_slots = slots;
   if (prefix_splits > 0) {
     AttnArgs pa = a;
@@ -575,7 +597,7 @@ int decode_shared_impl(const void* q, const void* k_pages, const void* v_pages, 
   a.chain = prefix_splits > 0 ? kChainWaitLast : kChainWaitFirst;
   if ((rc = launch_partials(a, s))) return rc;
   return launch_merge_sparse(part_acc, part_md, sinks, static_cast<int32_t>(rows), num_qo_heads,
-                             head_dim, slots, out, lse, s);
+                             head_dim, slots, out, lse, nullptr, s);
 }
 
 }  // namespace
@@ -690,6 +712,11 @@ int sinkattn_decode_shared_default_splits(int32_t batch, int32_t q_len, int32_t 
     return fail(SINKATTN_INVALID_ARG, "bad sizes");
   if (head_dim != 64 && head_dim != 128)
     return fail(SINKATTN_UNSUPPORTED, "head_dim %d is not 64 or 128", head_dim);
+  if (few_keys(batch, max_prefix_len, max_suffix_len, num_kv_heads, head_dim)) {
+    *prefix_splits = 0;
+    return sinkattn_decode_default_splits(batch, q_len, num_qo_heads, num_kv_heads, head_dim,
+                                          max_prefix_len + max_suffix_len, num_splits);
+  }
   // Own keys: chunks of about 1024 keys while they are needed to fill the SMs
   // (the warp-level kernel's four blocks per SM twice over, the tcgen05
   // kernel's one block twice over). Each further chunk costs its partials: 64

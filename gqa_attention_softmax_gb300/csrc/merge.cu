@@ -33,6 +33,35 @@ __global__ void __launch_bounds__(256)
   }
 }
 
+__device__ int g_status_merge;
+
+// Records SINKATTN_BAD_LENGTHS where the arrays of a shared-prefix call break a
+// rule (the plan's own checks, for a call without one). One block.
+__device__ void check_shared(const SharedCheck& c) {
+  bool bad = false;
+  for (int g = threadIdx.x; g < c.groups; g += blockDim.x) {
+    const int b0 = c.group_indptr[g], b1 = c.group_indptr[g + 1], len = c.prefix_lens[g];
+    const bool cut = b0 >= 0 && b1 >= b0 && b1 <= c.batch && (g > 0 || b0 == 0) &&
+                     (g < c.groups - 1 || b1 == c.batch);
+    bad |= !cut || len < 0 || len > c.max_prefix || len % c.page_size != 0;
+    if (cut && b1 > b0)
+      bad |= len > static_cast<long long>(c.page_indptr[b0 + 1] - c.page_indptr[b0]) * c.page_size;
+  }
+  bad = __syncthreads_or(bad);
+  for (int b = threadIdx.x; b < c.batch && !bad; b += blockDim.x) {
+    int lo = 0, hi = c.groups;   // the group with group_indptr[g] <= b < group_indptr[g + 1]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (c.group_indptr[mid] <= b) lo = mid;
+      else hi = mid;
+    }
+    const int len = c.kv_indptr[b + 1] - c.kv_indptr[b], own = len - c.prefix_lens[lo];
+    bad = own < c.q_len || own > c.max_suffix ||
+          len > static_cast<long long>(c.page_indptr[b + 1] - c.page_indptr[b]) * c.page_size;
+  }
+  if (bad) atomicExch(&g_status_merge, SINKATTN_BAD_LENGTHS);
+}
+
 // The merge of shared-prefix decode: only the slots that hold keys are read, R
 // rows per warp (R = 0: one row of more than 32 slots). Bound by two dependent
 // reads per row and by HBM for partials that L2 no longer holds: 49152 rows of
@@ -41,7 +70,12 @@ template <int D, int R>
 __global__ void __launch_bounds__(256)
     merge_sparse_kernel(const float* __restrict__ part_acc, const float* __restrict__ part_md,
                         const float* __restrict__ sinks, int n_rows, int Hq, int S,
-                        __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
+                        __nv_bfloat16* __restrict__ out, float* __restrict__ lse,
+                        const SharedCheck check) {
+  if (check.groups > 0 && blockIdx.x == gridDim.x - 1) {   // (reads nothing of the launch before)
+    check_shared(check);
+    return;
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31;
   const long long n = static_cast<long long>(n_rows) * Hq;
@@ -61,7 +95,7 @@ __global__ void __launch_bounds__(256)
 
 int launch_merge_sparse(const float* part_acc, const float* part_md, const float* sinks,
                         int32_t rows, int32_t Hq, int32_t d, int32_t num_slots, void* out,
-                        float* lse, cudaStream_t stream) {
+                        float* lse, const SharedCheck* check, cudaStream_t stream) {
   const long long n = static_cast<long long>(rows) * Hq;
   if (n == 0) return SINKATTN_OK;
   auto* o = static_cast<__nv_bfloat16*>(out);
@@ -71,9 +105,10 @@ int launch_merge_sparse(const float* part_acc, const float* part_md, const float
   const int most = num_slots <= 8 ? 4 : num_slots <= 16 ? 2 : num_slots <= 32 ? 1 : 0;
   const int R = most > 1 && n / most < 64LL * sm_count() ? 1 : most;
   const unsigned blocks = static_cast<unsigned>((n + 8 * (R > 0 ? R : 1) - 1) / (8 * (R > 0 ? R : 1)));
+  const SharedCheck c = check ? *check : SharedCheck{};
   auto run = [&](auto kern) {
-    return launch_chained(kern, dim3(blocks), 256, 0, stream, part_acc, part_md, sinks, rows, Hq,
-                          num_slots, o, lse);
+    return launch_chained(kern, dim3(blocks + (check ? 1 : 0)), 256, 0, stream, part_acc, part_md,
+                          sinks, rows, Hq, num_slots, o, lse, c);
   };
   cudaError_t e;
   if (d == 64)
@@ -126,8 +161,15 @@ int launch_merge(const float* part_acc, const float* part_md, const float* sinks
 }
 
 int read_status_merge(cudaStream_t s, int* status) {
-  *status = SINKATTN_OK;   // the merge kernel has no waits and no length checks
-  (void)s;
+  int zero = 0;
+  if (cudaMemcpyFromSymbolAsync(status, g_status_merge, sizeof(int), 0, cudaMemcpyDeviceToHost,
+                                s) != cudaSuccess)
+    return SINKATTN_CUDA_ERROR;
+  if (cudaStreamSynchronize(s) != cudaSuccess) return SINKATTN_CUDA_ERROR;
+  if (cudaMemcpyToSymbolAsync(g_status_merge, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s) !=
+      cudaSuccess)
+    return SINKATTN_CUDA_ERROR;
+  if (cudaStreamSynchronize(s) != cudaSuccess) return SINKATTN_CUDA_ERROR;
   return SINKATTN_OK;
 }
 

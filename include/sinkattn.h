@@ -369,15 +369,16 @@ SINKATTN_API int sinkattn_decode_fp8(const void* q, const void* k, const void* v
  *   Each sequence needs Lk_b >= prefix_lens[g] + q_len (the drafts' own keys
  *   are not shared), so every query sees the whole prefix but for the window.
  *   max_prefix_len / max_suffix_len (host) bound prefix_lens[g] and
- *   Lk_b - prefix_lens[g]; lengths that break one of these rules make the
- *   call record SINKATTN_BAD_LENGTHS and treat the sequence's or group's own
- *   part as empty (sinkattn_debug_status); with a group_indptr that does not
- *   cut the batch, all keys count as own ones.
+ *   Lk_b - prefix_lens[g]; lengths and groups that break one of these rules
+ *   make the call record SINKATTN_BAD_LENGTHS (sinkattn_debug_status), and the
+ *   results of the sequences concerned are not defined.
  *   sinkattn_set_decode_kernel decides for the prefixes too: AUTO takes the
  *   tcgen05 kernel where a group has more than 48 query rows per KV head on
  *   average.
  *   prefix_splits / num_splits: KV chunks of a prefix and of a sequence's own
- *   keys; <= 0 selects sinkattn_decode_shared_default_splits().
+ *   keys; <= 0 selects sinkattn_decode_shared_default_splits(). Its
+ *   prefix_splits is 0 for a call of so few keys that it is faster to let every
+ *   sequence read all of its own (num_splits then cuts those).
  *   workspace: at least sinkattn_decode_shared_workspace_bytes() bytes for
  *   the split counts in use, 256-byte aligned, device memory; contents on
  *   entry do not matter. Two calls that may overlap need two workspaces.
@@ -412,7 +413,8 @@ SINKATTN_API int sinkattn_decode_shared_workspace_bytes(int32_t batch, int32_t q
                                                         int32_t num_groups, int32_t prefix_splits,
                                                         int32_t num_splits, size_t* bytes);
 
-/* The split counts the shared-prefix decode uses when given <= 0 (host only). */
+/* The split counts the shared-prefix decode uses when given <= 0 (host only);
+ * prefix_splits 0: every sequence reads its own keys. */
 SINKATTN_API int sinkattn_decode_shared_default_splits(
     int32_t batch, int32_t q_len, int32_t num_qo_heads, int32_t num_kv_heads, int32_t head_dim,
     int32_t num_groups, int32_t max_prefix_len, int32_t max_suffix_len, int32_t* prefix_splits,

@@ -106,6 +106,7 @@ def make(groups, q_len, Hq, Hkv, d, page, seed=0, q_scale=1.0, fp8=False):
 
 def call(x, h, sinks=True, **kw):
     s = x["sinks"] if sinks else None
+    kw.setdefault("prefix_splits", 4)   # (by default calls this small do not share)
     if h["fp8"]:
         return sa.sinkattn_decode_shared_paged_fp8(
             x["q"], x["k_pages"], x["v_pages"], x["k_scale"], x["v_scale"], x["kv_indptr"],
@@ -322,9 +323,10 @@ def test_outputs_of_an_empty_batch_are_left():
 
 
 @gpu
+@pytest.mark.parametrize("share", [4, 0])
 @pytest.mark.parametrize("bad", ["prefix_unaligned", "prefix_too_long", "suffix_short",
                                  "suffix_long", "groups_end", "groups_back", "pages_few"])
-def test_wrong_lengths_are_recorded(bad):
+def test_wrong_lengths_are_recorded(bad, share):
     """Device arrays that break a rule: recorded, and nothing is read outside
     the pools or the lists (the plan turns the part into an empty one)."""
     x, h = make([(3, [5, 70, 9]), (1, [4, 30])], 2, 16, 2, 64, 16, seed=1)
@@ -345,7 +347,7 @@ def test_wrong_lengths_are_recorded(bad):
         x["page_indices"] = x["page_indices"][1:].clone()
     g = {k: v.cuda() for k, v in x.items()}
     assert sa.sinkattn_debug_status() == 0
-    call(g, h)
+    call(g, h, prefix_splits=share)
     assert sa.sinkattn_debug_status() == BAD_LENGTHS
     assert sa.sinkattn_debug_status() == 0
 
@@ -407,7 +409,7 @@ def test_workspace_holds_plan_and_partials():
 def test_default_splits_are_positive():
     for B, ql, ng, mp, ms in ((1, 1, 1, 0, 1), (64, 1, 1, 8192, 512), (256, 3, 5, 4096, 9000)):
         ps, ss = sa.sinkattn_decode_shared_default_splits(B, ql, 64, 8, 64, ng, mp, ms)
-        assert ps >= 1 and ss >= 1 and ps + ss <= 4096
+        assert ps >= (0 if B == 1 else 1) and ss >= 1 and ps + ss <= 4096
 
 
 def test_refuses_tensors_of_another_kind():
@@ -501,7 +503,7 @@ def test_call_on_another_stream_keeps_its_workspace():
         got.append(call(g, h, stream=st))
         # the same sizes on the current stream, at once overwritten
         n = sa.sinkattn_decode_shared_workspace_bytes(
-            30, 1, 64, 64, 1, *sa.sinkattn_decode_shared_default_splits(30, 1, 64, 8, 64, 1, 640, 5))
+            30, 1, 64, 64, 1, 4, sa.sinkattn_decode_shared_default_splits(30, 1, 64, 8, 64, 1, 640, 5)[1])
         torch.empty(n, dtype=torch.uint8, device="cuda").fill_(0xff)
     st.synchronize()
     torch.cuda.synchronize()
@@ -601,3 +603,34 @@ def test_groups_that_do_not_cut_the_batch_share_nothing(d, kernel):
             check(out, lse, x, h)
     finally:
         sa.sinkattn_set_decode_kernel("auto")
+
+
+@gpu
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("case", CASES, ids=IDS)
+def test_calls_of_few_keys_read_each_sequence_alone(case, fp8):
+    groups, q_len, Hq, Hkv, d, page, window, _, ss, qs = case
+    x, h = make(groups, q_len, Hq, Hkv, d, page, seed=page + q_len + 1, q_scale=qs, fp8=fp8)
+    B = x["kv_indptr"].numel() - 1
+    alone = B * (h["max_prefix"] + h["max_suffix"]) * Hkv * d <= 10 << 20   # (all but one or two)
+    ps, _ = sa.sinkattn_decode_shared_default_splits(B, q_len, Hq, Hkv, d, len(groups),
+                                                     h["max_prefix"], h["max_suffix"])
+    assert (ps == 0) == alone
+    g = {k: v.cuda() for k, v in x.items()}
+    for splits in (0, ss):
+        out, lse = call(g, h, window=window, prefix_splits=0, num_splits=splits)
+        check(out, lse, x, h, window=window)
+    assert sa.sinkattn_debug_status() == 0
+
+
+@gpu
+@pytest.mark.parametrize("d,q_len,fp8", [(64, 1, False), (64, 2, True), (128, 3, False), (128, 1, True)])
+def test_calls_of_many_keys_share_by_default(d, q_len, fp8):
+    groups = [(150, [3 + 7 * i for i in range(30)]), (40, [9] * 11), (0, [50, 4])]
+    x, h = make(groups, q_len, 16, 4, d, 16, seed=d + q_len, fp8=fp8)
+    assert sa.sinkattn_decode_shared_default_splits(43, q_len, 16, 4, d, 3, h["max_prefix"],
+                                                    8 << 20)[0] > 0
+    g = {k: v.cuda() for k, v in x.items()}
+    for bound in (h["max_suffix"], 100000):
+        out, lse = call(g, dict(h, max_suffix=bound), prefix_splits=0)
+        check(out, lse, x, h)
