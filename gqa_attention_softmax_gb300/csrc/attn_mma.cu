@@ -42,7 +42,9 @@
 // writes out and lse; a second cluster barrier keeps every CTA's shared
 // memory alive until its peers have read it. No partials go to HBM.
 #include <algorithm>
+#include <type_traits>
 
+#include "chain.cuh"
 #include "common.cuh"
 #include "internal.h"
 
@@ -64,15 +66,6 @@ struct MmaParams {
   int causal, window;
   float* part_acc;
   float* part_md;
-  // SHARED: partials at their place among another pass's, rows that are not
-  // the last queries of the keys, the launch's place in its chain
-  int part_slots, part_first;
-  int free_rows;
-  const int32_t* row_pos;
-  const int32_t* seq;
-  const int32_t* blk;   // a prefix pass: running sum of row blocks over the `groups`
-  int groups;
-  int chain;
   const float* sinks;     // fused mode
   __nv_bfloat16* out;     // fused mode
   float* lse;             // fused mode
@@ -85,6 +78,20 @@ struct MmaParams {
   const float* v_scale;
 };
 
+// A part of shared-prefix decode: partials at their place among another pass's,
+// rows that are not the last queries of the keys, the launch's place in its chain.
+struct MmaSharedParams : MmaParams {
+  int part_slots, part_first;
+  int free_rows;
+  const int32_t* row_pos;
+  const int32_t* seq;
+  const int32_t* blk;   // a prefix pass: running sum of row blocks over the `groups`
+  int groups;
+  int chain;
+};
+template <bool SHARED>
+using MmaParamsOf = std::conditional_t<SHARED, MmaSharedParams, MmaParams>;
+
 template <int D, int RT, int TG, int KT, int NST, bool FP8 = false, bool SHARED = false>
 struct MmaCfg {
   static constexpr int NW = RT * TG;               // consumer warps
@@ -95,6 +102,7 @@ struct MmaCfg {
   static constexpr int STAGE_BYTES = 2 * TILE_BYTES;
   static constexpr int F8_TILE = KT * D;           // one K or V tile of e4m3 codes
   static constexpr int F8_STAGE = 2 * F8_TILE;
+  static constexpr int RING_STAGE = FP8 ? F8_STAGE : STAGE_BYTES;
   // bf16: the stage ring of tiles; FP8: the ring of e4m3 stages
   static constexpr int OFF_F8 = FP8 ? 0 : NST * STAGE_BYTES;
   static constexpr int OFF_BAR = OFF_F8 + (FP8 ? NST * F8_STAGE : 0);
@@ -130,7 +138,7 @@ template <int D, int RT, int TG, int KT, int NST, bool FUSED, bool FP8, bool SHA
 __global__ void __launch_bounds__(MmaCfg<D, RT, TG, KT, NST, FP8, SHARED>::THREADS,
                                   MmaCfg<D, RT, TG, KT, NST, FP8, SHARED>::MIN_CTAS)
     attn_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                    const MmaParams p) {
+                    const MmaParamsOf<SHARED> p) {
   using C = MmaCfg<D, RT, TG, KT, NST, FP8, SHARED>;
   constexpr int NW = C::NW;
   constexpr float NEG_INF = kNegInf;
@@ -159,28 +167,37 @@ __global__ void __launch_bounds__(MmaCfg<D, RT, TG, KT, NST, FP8, SHARED>::THREA
   const int S = p.num_splits;
   const int split = blockIdx.x % S;
   int qb = p.nqb - 1 - static_cast<int>(blockIdx.x / S);   // longest query blocks first
-  if (SHARED && p.blk) {   // row block blockIdx.x / S of all groups' blocks
-    const int x = static_cast<int>(blockIdx.x / S);
-    if (x >= p.blk[p.groups]) return;
-    int lo = 0, hi = p.groups;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (p.blk[mid] <= x) lo = mid;
-      else hi = mid;
+  bool own = false;         // an own pass: lengths instead of running sums
+  bool free_rows = false;
+  const int32_t* row_pos = nullptr;
+  int at = b;
+  if constexpr (SHARED) {
+    if (p.blk) {   // row block blockIdx.x / S of all groups' blocks
+      const int x = static_cast<int>(blockIdx.x / S);
+      if (x >= p.blk[p.groups]) return;
+      int lo = 0, hi = p.groups;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (p.blk[mid] <= x) lo = mid;
+        else hi = mid;
+      }
+      at = b = lo;
+      qb = x - p.blk[lo];
     }
-    b = lo;
-    qb = x - p.blk[lo];
+    own = p.seq != nullptr;
+    if (own) at = p.seq[b];
+    free_rows = p.free_rows != 0;
+    row_pos = p.row_pos;
   }
 
-  const bool own = SHARED && p.seq != nullptr;   // an own pass: lengths instead of running sums
-  const int q_start = p.cu_q ? p.cu_q[b] : (own ? p.seq[b] : b) * p.q_len;
+  const int q_start = p.cu_q ? p.cu_q[b] : at * p.q_len;
   const int Lq = p.cu_q ? p.cu_q[b + 1] - q_start : p.q_len;
   const int k_start = p.cu_k[b];
   const int Lk = own ? k_start : p.cu_k[b + 1] - k_start;
   const int q0 = qb * p.QB;
   if (q0 >= Lq) return;   // uniform over the CTA (and the cluster), before any barrier
   const int nq = min(p.QB, Lq - q0);
-  if (threadIdx.x == 0 && ((Lk < Lq && !(SHARED && p.free_rows)) || Lk > p.max_kv || Lq < 0))
+  if (threadIdx.x == 0 && ((Lk < Lq && !free_rows) || Lk > p.max_kv || Lq < 0))
     atomicExch(&g_status_attn_mma, SINKATTN_BAD_LENGTHS);
 
   // Positions of the CTA's first and last query (queries are the last Lq keys).
@@ -192,7 +209,7 @@ __global__ void __launch_bounds__(MmaCfg<D, RT, TG, KT, NST, FP8, SHARED>::THREA
   int k_lo = min(split * chunk, Lk);
   int k_hi = min(k_lo + chunk, Lk);
   if (p.causal) k_hi = min(k_hi, posN + 1);
-  if (p.window > 0 && !(SHARED && p.row_pos)) k_lo = max(k_lo, pos0 - p.window + 1);
+  if (p.window > 0 && !row_pos) k_lo = max(k_lo, pos0 - p.window + 1);
   // Tiles end at k_hi (contiguous: no copy reads past the last key needed),
   // or start on a multiple of KT (paged: no box straddles a page).
   const bool paged = p.page_size > 0;
@@ -329,7 +346,7 @@ __global__ void __launch_bounds__(MmaCfg<D, RT, TG, KT, NST, FP8, SHARED>::THREA
     const int tl = r / G;
     valid[i] = tl < nq;
     tok[i] = q_start + q0 + tl;
-    pos[i] = SHARED && p.row_pos && valid[i] ? p.row_pos[tok[i]] : pos0 + tl;
+    pos[i] = SHARED && row_pos && valid[i] ? row_pos[tok[i]] : pos0 + tl;
     head[i] = kvh * G + (r - tl * G);
   }
 
@@ -441,7 +458,7 @@ __global__ void __launch_bounds__(MmaCfg<D, RT, TG, KT, NST, FP8, SHARED>::THREA
 
     // Mask (skipped for tiles that every row sees whole).
     const bool whole = (j0 >= k_lo) && (j0 + KT <= k_hi) && (!p.causal || j0 + KT - 1 <= pos0) &&
-                       (p.window <= 0 || (j0 > posN - p.window && !(SHARED && p.row_pos)));
+                       (p.window <= 0 || (j0 > posN - p.window && !row_pos));
     if (!whole) {
 #pragma unroll
       for (int j = 0; j < KT / 8; ++j) {
@@ -551,15 +568,14 @@ __global__ void __launch_bounds__(MmaCfg<D, RT, TG, KT, NST, FP8, SHARED>::THREA
   }
 
   // Combine the token groups of each row tile.
-  auto slot_of = [&](int group) -> float* {
-    float* base = C::XCHG_IN_RING
-                      ? reinterpret_cast<float*>(smem + group * (FP8 ? C::F8_STAGE : C::STAGE_BYTES))
-                      : xchg + ((group - 1) * RT + rt) * 32 * C::XCHG_FLOATS_PER_LANE;
-    return base + lane * C::XCHG_FLOATS_PER_LANE;
-  };
   if (TG > 1) {
     if (tg > 0) {
-      float* slot = slot_of(tg);
+      float* slot;
+      if constexpr (C::XCHG_IN_RING)
+        slot = reinterpret_cast<float*>(smem + tg * C::RING_STAGE) + lane * C::XCHG_FLOATS_PER_LANE;
+      else
+        slot = xchg + ((tg - 1) * RT + rt) * 32 * C::XCHG_FLOATS_PER_LANE +
+               lane * C::XCHG_FLOATS_PER_LANE;
 #pragma unroll
       for (int jd = 0; jd < D / 8; ++jd)
 #pragma unroll
@@ -575,7 +591,12 @@ __global__ void __launch_bounds__(MmaCfg<D, RT, TG, KT, NST, FP8, SHARED>::THREA
   if (TG > 1 && writer) {
 #pragma unroll 1
     for (int t = 1; t < TG; ++t) {
-      const float* slot = slot_of(t);
+      const float* slot;
+      if constexpr (C::XCHG_IN_RING)
+        slot = reinterpret_cast<float*>(smem + t * C::RING_STAGE) + lane * C::XCHG_FLOATS_PER_LANE;
+      else
+        slot = xchg + ((t - 1) * RT + rt) * 32 * C::XCHG_FLOATS_PER_LANE +
+               lane * C::XCHG_FLOATS_PER_LANE;
       float a0[2], a1[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -605,8 +626,9 @@ __global__ void __launch_bounds__(MmaCfg<D, RT, TG, KT, NST, FP8, SHARED>::THREA
     for (int i = 0; i < 2; ++i) {
       if (!valid[i]) continue;
       const size_t rowid = static_cast<size_t>(tok[i]) * p.Hq + head[i];
-      const size_t slot =
-          SHARED ? rowid * p.part_slots + p.part_first + split : rowid * S + split;
+      size_t slot;
+      if constexpr (SHARED) slot = rowid * p.part_slots + p.part_first + split;
+      else slot = rowid * S + split;
       float* arow = p.part_acc + slot * D;
 #pragma unroll
       for (int jd = 0; jd < D / 8; ++jd) {
@@ -727,7 +749,7 @@ static int launch_cfg(const AttnArgs& a, cudaStream_t stream) {
   rc = FP8 ? make_rows_tmap_u8(&tmV, a.v, rows, D, box, D) : make_rows_tmap(&tmV, a.v, rows, D, box, 128);
   if (rc) return rc;
 
-  MmaParams p{};
+  MmaParamsOf<SHARED> p{};
   p.q = static_cast<const __nv_bfloat16*>(a.q);
   p.cu_q = a.cu_q;
   p.cu_k = a.cu_k;
@@ -747,14 +769,16 @@ static int launch_cfg(const AttnArgs& a, cudaStream_t stream) {
   p.window = a.window;
   p.part_acc = a.part_acc;
   p.part_md = a.part_md;
-  p.part_slots = part_slots(a);
-  p.part_first = a.part_first;
-  p.free_rows = a.free_rows;
-  p.row_pos = a.row_pos;
-  p.seq = a.seq;
-  p.blk = a.blk;
-  p.groups = a.batch;
-  p.chain = a.chain;
+  if constexpr (SHARED) {
+    p.part_slots = part_slots(a);
+    p.part_first = a.part_first;
+    p.free_rows = a.free_rows;
+    p.row_pos = a.row_pos;
+    p.seq = a.seq;
+    p.blk = a.blk;
+    p.groups = a.batch;
+    p.chain = a.chain;
+  }
   p.page_size = a.page_size;
   p.box_rows = box;
   p.page_indptr = a.page_indptr;

@@ -357,18 +357,6 @@ __device__ __forceinline__ void transpose8_chunks(V4 (&ch)[8], int lane) {
   }
 }
 
-// Waits until the launch this one programmatically depends on has completed
-// and its writes are visible (immediate without one).
-__device__ __forceinline__ void grid_dependency_wait() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
-// Lets the next launch of the chain start as SMs have room (it still waits
-// for this one where it has to).
-__device__ __forceinline__ void grid_launch_dependents() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
 __device__ __forceinline__ void named_barrier_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }

@@ -10,6 +10,7 @@
 // start behind the prefix. One small launch derives both parts' lengths and
 // page-list starts from the caller's arrays, so the call needs no host copy: a
 // block of 1024 threads, about 4 us of load, barrier and scan latency.
+#include "chain.cuh"
 #include "common.cuh"
 #include "internal.h"
 

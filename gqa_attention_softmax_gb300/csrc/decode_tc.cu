@@ -19,7 +19,9 @@
 // shared memory; the MMA's other 128 - RR rows read whatever follows, which
 // only reaches padding lanes. Every wait is bounded.
 #include <algorithm>
+#include <type_traits>
 
+#include "chain.cuh"
 #include "common.cuh"
 #include "internal.h"
 #include "tc.cuh"
@@ -37,9 +39,6 @@ struct DtcParams {
   int causal, window;
   float* part_acc;
   float* part_md;
-  int part_slots, part_first;   // SHARED: partials at their place among another pass's
-  int chain;                    // SHARED: the launch's place in its chain
-  const int32_t* seq;           // SHARED: the items' sequences; cu_k holds their lengths
   // paged KV (page_size > 0): page-pool rows, boxes of box_rows keys
   int page_size, box_rows;
   const int32_t* page_indptr;
@@ -48,6 +47,16 @@ struct DtcParams {
   const float* k_scale;
   const float* v_scale;
 };
+
+// The own pass of shared-prefix decode. (In one structure for both, the FP8
+// kernel's calls took 1.3 % longer.)
+struct DtcSharedParams : DtcParams {
+  int part_slots, part_first;   // partials at their place among another pass's
+  int chain;                    // the launch's place in its chain
+  const int32_t* seq;           // the items' sequences; cu_k holds their lengths
+};
+template <bool SHARED>
+using DtcParamsOf = std::conditional_t<SHARED, DtcSharedParams, DtcParams>;
 
 // One work item: (sequence b, KV head, query block, KV chunk) and its keys.
 struct DtcItem {
@@ -182,7 +191,7 @@ template <int RR, bool PAGED, bool FP8, bool SHARED>
 __global__ void __launch_bounds__(DtcCfg<RR, FP8>::THREADS, 1)
     decode_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
                      const __grid_constant__ CUtensorMap tmK,
-                     const __grid_constant__ CUtensorMap tmV, const DtcParams p) {
+                     const __grid_constant__ CUtensorMap tmV, const DtcParamsOf<SHARED> p) {
   using C = DtcCfg<RR, FP8>;
   constexpr int D = C::D, KT = C::KT, NST = C::NST;
   constexpr float NEG_INF = kNegInf;
@@ -226,6 +235,14 @@ __global__ void __launch_bounds__(DtcCfg<RR, FP8>::THREADS, 1)
   const int32_t* cu = cu_in_smem ? cu_s : p.cu_k;
   auto item_of = [&](int k) {
     return dtc_item<KT, PAGED, !FP8, SHARED>(p, cu, static_cast<int>(blockIdx.x) + k * static_cast<int>(gridDim.x));
+  };
+  auto q_start_of = [&](const DtcItem& t) -> int {
+    if constexpr (SHARED) return p.seq[t.b] * p.q_len;
+    else return t.q_start;
+  };
+  auto slot_of = [&](size_t rowid, int split) -> size_t {
+    if constexpr (SHARED) return rowid * p.part_slots + p.part_first + split;
+    else return rowid * p.num_splits + split;
   };
 
   if (threadIdx.x == 0) {
@@ -296,7 +313,7 @@ __global__ void __launch_bounds__(DtcCfg<RR, FP8>::THREADS, 1)
         if (!pwait(&q_empty[qi & 1], ((qi >> 1) & 1) ^ 1)) { ok = false; break; }
         if (leader) {
           mbar_arrive_expect_tx(&q_full[qi & 1], static_cast<uint32_t>(2 * 128 * p.G * p.QB));
-          const int q_start = SHARED ? p.seq[t.b] * p.q_len : t.q_start;
+          const int q_start = q_start_of(t);
           for (int sub = 0; sub < 2; ++sub)
             tc::tma_load_3d(smem + C::OFF_Q + (qi & 1) * C::Q_BUF + sub * C::Q_SUB, &tmQ,
                             sub * 64, t.kvh * p.G, q_start + t.q0, &q_full[qi & 1]);
@@ -650,7 +667,7 @@ __global__ void __launch_bounds__(DtcCfg<RR, FP8>::THREADS, 1)
     const uint64_t keep_policy = policy_evict_last();
     for (int k = 0; k < n_mine; ++k) {
       const DtcItem t = item_of(k);
-      const int q_start = SHARED ? p.seq[t.b] * p.q_len : t.q_start;
+      const int q_start = q_start_of(t);
       if (!wwait(&o_full[k & 1], (k >> 1) & 1) || !wwait(&ml_full[k & 1], (k >> 1) & 1)) break;
       tc::fence_after_sync();
       const float4 mlr = ml[(k & 1) * 128 + row];
@@ -688,7 +705,7 @@ __global__ void __launch_bounds__(DtcCfg<RR, FP8>::THREADS, 1)
           md.x = mlr.x * lscale + (lg2(mlr.y) - lg2(mlr.z)) * kLn2;
           md.y = mlr.z;
         }
-        *reinterpret_cast<float2*>(p.part_md + (SHARED ? rowid * p.part_slots + p.part_first + t.split : rowid * S + t.split) * 2) = md;
+        *reinterpret_cast<float2*>(p.part_md + slot_of(rowid, t.split) * 2) = md;
       }
       named_barrier_sync(1, 128);   // staging written
       const int nrows = t.nq * G;
@@ -699,7 +716,7 @@ __global__ void __launch_bounds__(DtcCfg<RR, FP8>::THREADS, 1)
         const float4 val = *reinterpret_cast<const float4*>(stage + r * C::XS + lane * 4);
         // kept in L2 as long as possible: the merge reads the newest partials first
         asm volatile("st.global.L2::cache_hint.v4.f32 [%0], {%1, %2, %3, %4}, %5;" ::"l"(
-                         p.part_acc + (SHARED ? rowid * p.part_slots + p.part_first + t.split : rowid * S + t.split) * D + lane * 4),
+                         p.part_acc + slot_of(rowid, t.split) * D + lane * 4),
                      "f"(val.x), "f"(val.y), "f"(val.z), "f"(val.w), "l"(keep_policy)
                      : "memory");
       }
@@ -750,7 +767,7 @@ static int launch_dtc(const AttnArgs& a, int QB, cudaStream_t stream) {
   rc = FP8 ? make_rows_tmap_u8(&tmV, a.v, rows, C::D, box)
            : make_rows_tmap(&tmV, a.v, rows, C::D, box, 128);
   if (rc) return rc;
-  DtcParams p{};
+  DtcParamsOf<SHARED> p{};
   p.k_scale = a.k_scale;
   p.v_scale = a.v_scale;
   p.page_size = a.page_size;
@@ -779,10 +796,12 @@ static int launch_dtc(const AttnArgs& a, int QB, cudaStream_t stream) {
   p.window = a.window;
   p.part_acc = a.part_acc;
   p.part_md = a.part_md;
-  p.part_slots = part_slots(a);
-  p.part_first = a.part_first;
-  p.chain = a.chain;
-  p.seq = a.seq;
+  if constexpr (SHARED) {
+    p.part_slots = part_slots(a);
+    p.part_first = a.part_first;
+    p.chain = a.chain;
+    p.seq = a.seq;
+  }
   auto kern = decode_tc_kernel<RR, PAGED, FP8, SHARED>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) {

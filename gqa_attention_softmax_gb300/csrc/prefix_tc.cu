@@ -52,6 +52,7 @@
 // of the time, 57 % while blocks run).
 #include <algorithm>
 
+#include "chain.cuh"
 #include "common.cuh"
 #include "internal.h"
 #include "tc.cuh"
