@@ -156,11 +156,12 @@ int launch_merge(const float* part_acc, const float* part_md, const float* sinks
                  cudaStream_t stream, bool drop_partials);
 // The same for partials of which many are empty (d = 0): those slots'
 // accumulators are not read and need not have been written.
-// `check` (nullptr: none): one more block holds the caller's lengths and groups
+// `check` (nullptr: none): a few more blocks hold the caller's lengths and groups
 // to the rules of shared-prefix decode, where no plan has.
 struct SharedCheck {
   const int32_t *kv_indptr, *page_indptr, *group_indptr, *prefix_lens;
   int groups, page_size, batch, q_len, max_prefix, max_suffix;
+  int blocks;   // (set by the launch)
 };
 int launch_merge_sparse(const float* part_acc, const float* part_md, const float* sinks,
                         int32_t rows, int32_t Hq, int32_t d, int32_t num_slots, void* out,

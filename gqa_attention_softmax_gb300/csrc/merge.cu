@@ -1,5 +1,7 @@
 // Merge of split-KV partials with the sink counted exactly once: one warp
 // per (row, query head) runs merge_row (merge_row.cuh).
+#include <algorithm>
+
 #include "common.cuh"
 #include "internal.h"
 #include "merge_row.cuh"
@@ -36,28 +38,29 @@ __global__ void __launch_bounds__(256)
 __device__ int g_status_merge;
 
 // Records SINKATTN_BAD_LENGTHS where the arrays of a shared-prefix call break a
-// rule (the plan's own checks, for a call without one). One block.
-__device__ void check_shared(const SharedCheck& c) {
+// rule (the plan's own checks, for a call without one). Thread i has group i
+// and sequence i.
+__device__ __forceinline__ void check_shared(const SharedCheck& c, int i) {
   bool bad = false;
-  for (int g = threadIdx.x; g < c.groups; g += blockDim.x) {
-    const int b0 = c.group_indptr[g], b1 = c.group_indptr[g + 1], len = c.prefix_lens[g];
-    const bool cut = b0 >= 0 && b1 >= b0 && b1 <= c.batch && (g > 0 || b0 == 0) &&
-                     (g < c.groups - 1 || b1 == c.batch);
-    bad |= !cut || len < 0 || len > c.max_prefix || len % c.page_size != 0;
+  if (i < c.groups) {
+    const int b0 = c.group_indptr[i], b1 = c.group_indptr[i + 1], len = c.prefix_lens[i];
+    const bool cut = b0 >= 0 && b1 >= b0 && b1 <= c.batch && (i > 0 || b0 == 0) &&
+                     (i < c.groups - 1 || b1 == c.batch);
+    bad = !cut || len < 0 || len > c.max_prefix || len % c.page_size != 0;
     if (cut && b1 > b0)
       bad |= len > static_cast<long long>(c.page_indptr[b0 + 1] - c.page_indptr[b0]) * c.page_size;
   }
-  bad = __syncthreads_or(bad);
-  for (int b = threadIdx.x; b < c.batch && !bad; b += blockDim.x) {
-    int lo = 0, hi = c.groups;   // the group with group_indptr[g] <= b < group_indptr[g + 1]
+  if (i < c.batch) {
+    int lo = 0, hi = c.groups;   // the group with group_indptr[g] <= i < group_indptr[g + 1]
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (c.group_indptr[mid] <= b) lo = mid;
+      if (c.group_indptr[mid] <= i) lo = mid;
       else hi = mid;
     }
-    const int len = c.kv_indptr[b + 1] - c.kv_indptr[b], own = len - c.prefix_lens[lo];
-    bad = own < c.q_len || own > c.max_suffix ||
-          len > static_cast<long long>(c.page_indptr[b + 1] - c.page_indptr[b]) * c.page_size;
+    const int len = c.kv_indptr[i + 1] - c.kv_indptr[i];
+    const long long own = static_cast<long long>(len) - c.prefix_lens[lo];
+    bad |= own < c.q_len || own > c.max_suffix ||
+           len > static_cast<long long>(c.page_indptr[i + 1] - c.page_indptr[i]) * c.page_size;
   }
   if (bad) atomicExch(&g_status_merge, SINKATTN_BAD_LENGTHS);
 }
@@ -72,8 +75,9 @@ __global__ void __launch_bounds__(256)
                         const float* __restrict__ sinks, int n_rows, int Hq, int S,
                         __nv_bfloat16* __restrict__ out, float* __restrict__ lse,
                         const SharedCheck check) {
-  if (check.groups > 0 && blockIdx.x == gridDim.x - 1) {   // (reads nothing of the launch before)
-    check_shared(check);
+  const int beyond = static_cast<int>(blockIdx.x) - static_cast<int>(gridDim.x) + check.blocks;
+  if (beyond >= 0) {   // (reads nothing of the launch before)
+    check_shared(check, beyond * 256 + static_cast<int>(threadIdx.x));
     return;
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -105,9 +109,10 @@ int launch_merge_sparse(const float* part_acc, const float* part_md, const float
   const int most = num_slots <= 8 ? 4 : num_slots <= 16 ? 2 : num_slots <= 32 ? 1 : 0;
   const int R = most > 1 && n / most < 64LL * sm_count() ? 1 : most;
   const unsigned blocks = static_cast<unsigned>((n + 8 * (R > 0 ? R : 1) - 1) / (8 * (R > 0 ? R : 1)));
-  const SharedCheck c = check ? *check : SharedCheck{};
+  SharedCheck c = check ? *check : SharedCheck{};
+  c.blocks = check ? (std::max(c.groups, c.batch) + 255) / 256 : 0;
   auto run = [&](auto kern) {
-    return launch_chained(kern, dim3(blocks + (check ? 1 : 0)), 256, 0, stream, part_acc, part_md,
+    return launch_chained(kern, dim3(blocks + c.blocks), 256, 0, stream, part_acc, part_md,
                           sinks, rows, Hq, num_slots, o, lse, c);
   };
   cudaError_t e;

@@ -634,3 +634,19 @@ def test_calls_of_many_keys_share_by_default(d, q_len, fp8):
     for bound in (h["max_suffix"], 100000):
         out, lse = call(g, dict(h, max_suffix=bound), prefix_splits=0)
         check(out, lse, x, h)
+
+
+@gpu
+@pytest.mark.parametrize("at", [0, 300, 1249])
+def test_wrong_lengths_of_many_short_sequences_are_recorded(at):
+    """1250 sequences in 417 groups, read alone: each one's length counts."""
+    x, h = make([(i % 2, [3, 5, 2]) for i in range(416)] + [(1, [4, 4])], 1, 2, 1, 64, 16, seed=7)
+    assert x["kv_indptr"].numel() == 1251
+    g = {k: v.cuda() for k, v in x.items()}
+    out, lse = call(g, h, prefix_splits=0)
+    assert sa.sinkattn_debug_status() == 0
+    check(out, lse, x, h)
+    own = int(x["kv_indptr"][at + 1] - x["kv_indptr"][at]) % 16   # (prefixes of 0 or 16 keys)
+    g["kv_indptr"][at + 1:] -= own   # no key of its own left, the others as they were
+    call(g, h, prefix_splits=0)
+    assert sa.sinkattn_debug_status() == BAD_LENGTHS
