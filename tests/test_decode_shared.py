@@ -258,8 +258,9 @@ def test_agrees_with_the_paged_decode():
 
 
 @gpu
+@pytest.mark.parametrize("share", [2, 0])
 @pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
-def test_captured_call_replays_on_new_inputs(fp8):
+def test_captured_call_replays_on_new_inputs(fp8, share):
     """One graph, two inputs with other lengths and groups of the same sizes."""
     first, h = make([(3, [5, 70, 9]), (1, [4, 30])], 2, 64, 8, 64, 16, seed=1, fp8=fp8)
     other, h2 = make([(2, [33, 6]), (2, [8, 2, 60])], 2, 64, 8, 64, 16, seed=2, fp8=fp8)
@@ -282,11 +283,11 @@ def test_captured_call_replays_on_new_inputs(fp8):
                 lse=torch.empty(g["q"].shape[:2], dtype=torch.float32, device="cuda"),
                 workspace=torch.empty(sa.sinkattn_decode_shared_workspace_bytes(
                     5, 2, 64, 64, 2, 2, 2), dtype=torch.uint8, device="cuda"))
-    call(g, h, num_splits=2, prefix_splits=2, **bufs)
+    call(g, h, num_splits=2, prefix_splits=share, **bufs)
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        call(g, h, num_splits=2, prefix_splits=2, **bufs)
+        call(g, h, num_splits=2, prefix_splits=share, **bufs)
     for x in (b, a, b):
         for k in g:
             g[k].copy_(x[k])
