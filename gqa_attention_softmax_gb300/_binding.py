@@ -580,7 +580,9 @@ def sinkattn_decode_shared_paged(q, k_pages, v_pages, kv_indptr, page_indptr, pa
     whose first prefix_lens[g] keys (int32, device; a multiple of the page
     size) are the same; they are read once, from the first sequence's page
     list. max_prefix_len bounds prefix_lens, max_suffix_len the keys of a
-    sequence past its prefix (at least q_len each). Returns (out, lse)."""
+    sequence past its prefix (at least q_len each). Where these say that the
+    call has few keys, every sequence reads its own, unless prefix_splits > 0.
+    Returns (out, lse)."""
     return _decode_shared(lib().sinkattn_decode_shared_paged, torch.bfloat16, (), q, k_pages,
                           v_pages, kv_indptr, page_indptr, page_indices, group_indptr, prefix_lens,
                           sinks, q_len, max_prefix_len, max_suffix_len, num_splits, prefix_splits,
