@@ -610,3 +610,56 @@ def test_refuses_tensors_that_would_be_misread():
             pytest.fail("call %d was taken" % i)
         assert e.value.status == INVALID_ARG
     p.check()
+
+
+@gpu
+def test_pools_past_32_bit_offsets():
+    """Pools of more than 2^31 elements (2^32 bytes): appends, copies on write, the attention
+    and moves at their far end."""
+    N, P, Hkv, d = 40000, 64, 8, 128
+    k = torch.zeros((N, Hkv, P, d), dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    assert k.numel() > 2 ** 31
+    table = sa.PageTable(None, N, P, 4, N)
+    sa.sinkattn_pages_reserve(table, i32([0]), i32([0, (N - 4) * P]), (N - 4) * P, k, v)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    new = [torch.randn((100, Hkv, d), generator=gen, device="cuda").to(torch.bfloat16)
+           for _ in range(2)]
+    slots = sa.sinkattn_pages_reserve(table, i32([1]), i32([0, 100]), 100, k, v)
+    assert slots.min().item() == (N - 4) * P
+    sa.sinkattn_append_paged(*new, slots, k, v)
+    sa.sinkattn_pages_truncate(table, i32([0]))
+    sa.sinkattn_pages_fork(table, i32([1]), i32([2]))
+    more = [torch.randn((2, Hkv, d), generator=gen, device="cuda").to(torch.bfloat16)
+            for _ in range(2)]
+    # both write behind the shared 100 tokens: the second gets a copy of the last page
+    slots = sa.sinkattn_pages_reserve(table, i32([1, 2]), i32([0, 1, 2]), 2, k, v)
+    sa.sinkattn_append_paged(*more, slots, k, v)
+
+    q = torch.randn((2, 16, d), generator=gen, device="cuda").to(torch.bfloat16)
+
+    def look(share):
+        kv, ptr, pages = sa.sinkattn_pages_lists(table, i32([1, 2]), page_indices=i32([0] * 8))
+        return sa.sinkattn_decode_shared_paged(
+            q, k, v, kv, ptr, pages, i32([0, 2]), i32([P]), None, 1, P, P, prefix_splits=share)
+
+    def want(i):
+        x, y = (torch.cat([a, b[i:i + 1]]).double().transpose(0, 1) for a, b in zip(new, more))
+        l = torch.einsum("hgd,hjd->hgj", q[i].double().view(Hkv, 2, d), x) / math.sqrt(d)
+        return torch.einsum("hgj,hjd->hgd", l.softmax(-1), y).reshape(16, d), l.logsumexp(-1).reshape(16)
+
+    def held():
+        for share in (1, 0):
+            out, lse = look(share)
+            for i in range(2):
+                o, l = want(i)
+                # weights to bf16, then the output: half a step each, relative to |v| <= 6
+                assert (out[i].double() - o).abs().max().item() <= 2 * 2.0 ** -8 * 6
+                assert (lse[i].double() - l).abs().max().item() <= 1e-4
+
+    held()
+    page_map = sa.sinkattn_pages_compact(table, k, v)
+    assert table.page_list[1:3, :2].max().item() == 2 and table.free_count.item() == N - 3
+    assert (page_map >= 0).sum().item() == 3
+    held()
+    assert sa.sinkattn_debug_status() == 0
