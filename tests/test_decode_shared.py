@@ -24,6 +24,7 @@ import oracle
 import gqa_attention_softmax_gb300 as sa
 from gqa_attention_softmax_gb300._binding import (BAD_LENGTHS, INVALID_ARG, TIMEOUT,
                                                   UNSUPPORTED)
+from _helpers import compare
 
 gpu = pytest.mark.gpu
 
@@ -651,3 +652,73 @@ def test_wrong_lengths_of_many_short_sequences_are_recorded(at):
     g["kv_indptr"][at + 1:] -= own   # no key of its own left, the others as they were
     call(g, h, prefix_splits=0)
     assert sa.sinkattn_debug_status() == BAD_LENGTHS
+
+
+def one_late_key(d, fp8, seed):
+    """40 sequences behind 768 shared keys, 8 rows per KV head each. All keys are zero but two of the
+    prefix: key 5, whose logit is 2^20 in weight, and key 700, whose weight is another 2^6 to 2^7.7 times
+    that. So a row's output is key 700's value but for less than 2^-6, and its weight, relative to a
+    reference maximum that stayed at key 5, is no power of two. Returns (x, h, mass outside key 700)."""
+    x, h = make([(48, [2] * 40)], 1, 64, 8, d, 16, seed=seed, fp8=fp8)
+    one = 0x70 if fp8 else 1.0   # (the code of 128)
+    x["k"].zero_()
+    x["k_pages"].zero_()
+    for key, dim in ((5, 0), (700, 1)):
+        x["k"].view(40, 8, 770, d)[:, :, key, dim] = one
+        x["k_pages"][x["page_indices"][key // 16].item(), :, key % 16, dim] = one
+    value = 128.0 * x["k_scale"] if fp8 else torch.ones(8)
+    unit = (math.log(2) * math.sqrt(d) / value).repeat_interleave(8)   # q of one bit of logit, by head
+    gen = torch.Generator().manual_seed(seed)
+    bits = 6.0 + 1.7 * torch.rand((40, 64), generator=gen)
+    x["q"].zero_()
+    x["q"][:, :, 0] = (20.0 * unit).to(torch.bfloat16)
+    x["q"][:, :, 1] = ((20.0 + bits) * unit).to(torch.bfloat16)
+    logits = x["q"][:, :, :2].double() / unit.double()[None, :, None]   # in bits
+    rest = torch.exp2(logits[..., 0] - logits[..., 1]) + 768 * torch.exp2(-logits[..., 1])
+    assert ((logits[..., 1] - logits[..., 0]) < 8).all() and (rest < 2.0 ** -5.8).all()
+    return x, h, rest.numpy().reshape(-1)
+
+
+@gpu
+@pytest.mark.parametrize("kernel", ["auto", "warp"])
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_weight_that_is_most_of_a_row_is_not_rounded_into_the_output(d, fp8, kernel):
+    """Rounded weights w (1 + r), |r| <= 2^-8, over a divisor that counts the dominant one as rounded leave
+    sum p_j r_j (v_j - out) for the counted weights and sum p_j r_j v_j for the rest: with e the mass outside
+    the dominant key and V the largest |v|, at most 2^-8 e 2 V + 2^-8 e 2 V, and e V 2^-7 more for logits
+    that are off by 2^-8 at most (products of one term, exact to 2^-22 of 28 bits). The output's own
+    rounding adds 2^-8 |out|; no 2^-8 |out| of the weight's own."""
+    x, h, rest = one_late_key(d, fp8, seed=d)
+    g = {k: v.cuda() for k, v in x.items()}
+    sa.sinkattn_set_decode_kernel(kernel)
+    try:
+        out, lse = call(g, h, sinks=False, prefix_splits=1, num_splits=1)
+    finally:
+        sa.sinkattn_set_decode_kernel("auto")
+    o, l, _ = want(x, h, sinks=False)
+    v = x["v"].view(torch.float8_e4m3fn).float() * x["v_scale"].max() if fp8 else x["v"].float()
+    room = 2.0 ** -8 * np.abs(o) + rest.reshape(*o.shape[:-1], 1) * (2.0 ** -6 + 2.0 ** -7) * v.abs().max().item()
+    err = np.abs(out.float().cpu().numpy().reshape(o.shape) - o)
+    assert (err <= room + 1e-6).all(), "off by %.3g of the room" % (err / (room + 1e-6)).max()
+    assert np.abs(lse.cpu().numpy().reshape(l.shape) - l).max() <= 1e-4
+
+
+@gpu
+@pytest.mark.parametrize("q_scale", [3.0, 6.0])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+def test_peaky_rows_meet_the_bounds_of_the_other_paths(fp8, d, q_scale):
+    """max-abs 1e-2, mean-abs 1e-3, as for prefill and decode, with |v| up to 1/2: a weight's half step
+    and the output's are below 2^-8 / 2 + 2^-10 together, their means a quarter of that."""
+    x, h = make([(40, [3, 17] * 16)], 1, 64, 8, d, 32, seed=d, q_scale=q_scale, fp8=fp8)
+    for name in ("v", "v_pages"):
+        if fp8:
+            f = x[name].view(torch.float8_e4m3fn).float().clamp(-90.0, 90.0) * 0.4
+            x[name] = f.to(torch.float8_e4m3fn).view(torch.uint8)
+        else:
+            x[name] = (x[name].float().clamp(-2.0, 2.0) * 0.25).to(torch.bfloat16)
+    g = {k: v.cuda() for k, v in x.items()}
+    out, lse = call(g, h, prefix_splits=2, num_splits=1)
+    o, l, _ = want(x, h)
+    compare(out, lse, o, l, "shared prefix, logits spread by %g" % q_scale)
