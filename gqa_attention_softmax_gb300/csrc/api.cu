@@ -456,8 +456,9 @@ bool prefix_on_tc(int64_t tokens, int G, int64_t groups) {
 // 16.4 | 15.5, 17: 17.7 to 19.6 | 20.3 to 24.4; at d 128 4.4: 18.5 | 10.0, 9.7:
 // 22.5 | 17.9, 17: 20.9 to 25.8 | 17.8 to 26.1.
 bool few_keys(int64_t batch, int64_t max_prefix, int64_t max_suffix, int64_t Hkv, int64_t d) {
+  // (one division at a time: the product of any sizes may pass 64 bits)
   return g_decode_kernel.load(std::memory_order_relaxed) == SINKATTN_DECODE_AUTO && batch > 0 &&
-         max_prefix + max_suffix <= (int64_t{10} << 20) / (batch * Hkv * d);
+         max_prefix + max_suffix <= (int64_t{10} << 20) / batch / Hkv / d;
 }
 
 // Shared-prefix decode: the sequences' own keys and the groups' prefixes as
@@ -728,22 +729,25 @@ int sinkattn_decode_shared_default_splits(int32_t batch, int32_t q_len, int32_t 
   *num_splits = static_cast<int32_t>(std::max<int64_t>(
       1, std::min<int64_t>((fill + items - 1) / items, (max_suffix_len + 1023) / 1024)));
   const int G = num_qo_heads / num_kv_heads;
-  const int64_t tokens = static_cast<int64_t>(batch) * q_len;
+  // (calls of 2^31 rows are refused: beyond, any answer does, within 64 bits)
+  const int64_t tokens = std::min<int64_t>(static_cast<int64_t>(batch) * q_len, int64_t{1} << 31);
   if (G >= 1 && G <= 64 && prefix_on_tc(tokens, G, num_groups)) {
     // partials that let the kernel deal its units out evenly (prefixes of
     // several groups about half as long as the longest), at most 16
     const int64_t tiles = (max_prefix_len + prefix_tile_keys(head_dim, false) - 1) /
                           prefix_tile_keys(head_dim, false);
     const int64_t bt = prefix_block_tokens(G);
-    const int64_t units = num_groups * ((tokens / num_groups + bt - 1) / bt) * num_kv_heads *
-                          (num_groups > 1 ? (tiles + 1) / 2 : tiles);
-    const int64_t quota = std::max<int64_t>(1, (units + sm_count() - 1) / sm_count());
+    const double units = static_cast<double>(num_groups * ((tokens / num_groups + bt - 1) / bt)) *
+                         num_kv_heads * (num_groups > 1 ? (tiles + 1) / 2 : tiles);
+    const int64_t quota = static_cast<int64_t>(
+        std::max(1.0, std::min(std::ceil(units / sm_count()), 0x1p40)));
     const int64_t n = tiles > 1 ? (tiles - 1 + quota - 1) / quota + 1 : 1;
     *prefix_splits = static_cast<int32_t>(std::min<int64_t>(n, 16));
     return SINKATTN_OK;
   }
   // the warp-level kernel's blocks of up to 64 query rows
-  const int64_t blocks = std::min<int64_t>(num_groups + tokens * G / 64, int64_t{1} << 20);
+  const int64_t blocks =
+      std::min<int64_t>(num_groups + tokens * std::min(G, 64) / 64, int64_t{1} << 20);
   return sinkattn_decode_default_splits(static_cast<int32_t>(blocks), 1, num_qo_heads, num_kv_heads,
                                         head_dim, max_prefix_len, prefix_splits);
 }

@@ -722,3 +722,16 @@ def test_peaky_rows_meet_the_bounds_of_the_other_paths(fp8, d, q_scale):
     out, lse = call(g, h, prefix_splits=2, num_splits=1)
     o, l, _ = want(x, h)
     compare(out, lse, o, l, "shared prefix, logits spread by %g" % q_scale)
+
+
+def test_split_counts_of_sizes_beyond_64_bits():
+    """batch x KV heads x head_dim of these wraps to zero in 64 bits."""
+    for B, ql, Hq, Hkv, ng in ((1 << 30, 1, 1 << 30, 1 << 30, 1),
+                               (2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1, 1),
+                               (2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1, 1, 2 ** 31 - 1),
+                               (2 ** 31 - 1, 2 ** 31 - 1, 64, 1, 2 ** 31 - 1)):
+        for mp in (0, 2 ** 31 - 1):
+            for d in (64, 128):
+                ps, ss = sa.sinkattn_decode_shared_default_splits(B, ql, Hq, Hkv, d, ng, mp, 2 ** 31 - 1)
+                assert 1 <= ps <= 16 and 1 <= ss <= 4096
+    assert raw(B=1 << 30, Hq=1 << 30, Hkv=1 << 30) == UNSUPPORTED
