@@ -328,8 +328,9 @@ struct Fp8Kv {
   const float* v_scale;
 };
 
-int launch_partials(const AttnArgs& a, cudaStream_t stream) {
-  const int kind = g_decode_kernel.load(std::memory_order_relaxed);
+int decode_kind() { return g_decode_kernel.load(std::memory_order_relaxed); }
+
+int launch_partials(const AttnArgs& a, int kind, cudaStream_t stream) {
   if (a.kv_fp8) {   // tcgen05 up to 64 rows per tile at head_dim 128, else the warp-level kernel
     const bool tc8 = decode_tc_supported(a);
     if (kind == SINKATTN_DECODE_TCGEN05 && !tc8)
@@ -373,7 +374,7 @@ int decode_split_impl(const void* q, const void* k, const void* v, const int32_t
   if (batch == 0) return SINKATTN_OK;
   a.part_acc = part_acc; a.part_md = part_md;
   set_paged(&a, pg);
-  return launch_partials(a, static_cast<cudaStream_t>(stream));
+  return launch_partials(a, decode_kind(), static_cast<cudaStream_t>(stream));
 }
 
 int decode_impl(const void* q, const void* k, const void* v, const int32_t* kv_indptr,
@@ -443,8 +444,7 @@ int decode_impl(const void* q, const void* k, const void* v, const int32_t* kv_i
 // at d 128; 64 rows 22.5 and 20.9, 37.5 and 25.6; behind 1024 keys 48 rows 13.2
 // and 14.5, 15.3 and 18.3; 64 rows 14.0 and 14.9, 20.0 and 18.4.
 // (A group's sequences come as one run of rows: 4 samples of 8 heads are 32.)
-bool prefix_on_tc(int64_t tokens, int G, int64_t groups) {
-  const int kind = g_decode_kernel.load(std::memory_order_relaxed);
+bool prefix_on_tc(int kind, int64_t tokens, int G, int64_t groups) {
   if (kind != SINKATTN_DECODE_AUTO) return kind == SINKATTN_DECODE_TCGEN05;
   return tokens * G > 48 * groups;
 }
@@ -455,10 +455,63 @@ bool prefix_on_tc(int64_t tokens, int G, int64_t groups) {
 // d 64 2.2: 12.6 | 8.3, 4.4: 14.6 | 8.7, 8.5: 15 to 16.5 | 14.5 to 14.8, 9.7:
 // 16.4 | 15.5, 17: 17.7 to 19.6 | 20.3 to 24.4; at d 128 4.4: 18.5 | 10.0, 9.7:
 // 22.5 | 17.9, 17: 20.9 to 25.8 | 17.8 to 26.1.
-bool few_keys(int64_t batch, int64_t max_prefix, int64_t max_suffix, int64_t Hkv, int64_t d) {
+bool few_keys(int kind, int64_t batch, int64_t max_prefix, int64_t max_suffix, int64_t Hkv,
+              int64_t d) {
   // (one division at a time: the product of any sizes may pass 64 bits)
-  return g_decode_kernel.load(std::memory_order_relaxed) == SINKATTN_DECODE_AUTO && batch > 0 &&
+  return kind == SINKATTN_DECODE_AUTO && batch > 0 &&
          max_prefix + max_suffix <= (int64_t{10} << 20) / batch / Hkv / d;
+}
+
+// The default split counts under a choice of kernel.
+int shared_splits(int kind, int32_t batch, int32_t q_len, int32_t num_qo_heads,
+                  int32_t num_kv_heads, int32_t head_dim, int32_t num_groups,
+                  int32_t max_prefix_len, int32_t max_suffix_len, int32_t* prefix_splits,
+                  int32_t* num_splits) {
+  g_last_error[0] = '\0';
+  if (!prefix_splits || !num_splits)
+    return fail(SINKATTN_INVALID_ARG, "prefix_splits and num_splits must be non-null");
+  if (num_groups < 1 || max_prefix_len < 0) return fail(SINKATTN_INVALID_ARG, "bad sizes");
+  if (batch < 0 || q_len < 1 || num_qo_heads <= 0 || num_kv_heads <= 0 || max_suffix_len < 0)
+    return fail(SINKATTN_INVALID_ARG, "bad sizes");
+  if (head_dim != 64 && head_dim != 128)
+    return fail(SINKATTN_UNSUPPORTED, "head_dim %d is not 64 or 128", head_dim);
+  if (few_keys(kind, batch, max_prefix_len, max_suffix_len, num_kv_heads, head_dim)) {
+    *prefix_splits = 0;
+    return sinkattn_decode_default_splits(batch, q_len, num_qo_heads, num_kv_heads, head_dim,
+                                          max_prefix_len + max_suffix_len, num_splits);
+  }
+  // Own keys: chunks of about 1024 keys while they are needed to fill the SMs
+  // (the warp-level kernel's four blocks per SM twice over, the tcgen05
+  // kernel's one block twice over). Each further chunk costs its partials: 64
+  // sequences behind 8192 keys at d 64 take 33, 35 and 38 us in 1, 2 and 3
+  // chunks with up to 1024 own keys, 76, 59 and 59 us with up to 4000; 16
+  // sequences of up to 8000 own keys 96, 45, 40 and 37 us in 1, 3, 4 and 8.
+  const int64_t items = std::max<int64_t>(1, static_cast<int64_t>(batch) * num_kv_heads);
+  const int64_t fill = (head_dim == 64 ? 8 : 2) * static_cast<int64_t>(sm_count());
+  *num_splits = static_cast<int32_t>(std::max<int64_t>(
+      1, std::min<int64_t>((fill + items - 1) / items, (int64_t{max_suffix_len} + 1023) / 1024)));
+  const int G = num_qo_heads / num_kv_heads;
+  // (calls of 2^31 rows are refused: beyond, any answer does, within 64 bits)
+  const int64_t tokens = std::min<int64_t>(static_cast<int64_t>(batch) * q_len, int64_t{1} << 31);
+  if (G >= 1 && G <= 64 && prefix_on_tc(kind, tokens, G, num_groups)) {
+    // partials that let the kernel deal its units out evenly (prefixes of
+    // several groups about half as long as the longest), at most 16
+    const int64_t tiles = (int64_t{max_prefix_len} + prefix_tile_keys(head_dim, false) - 1) /
+                          prefix_tile_keys(head_dim, false);
+    const int64_t bt = prefix_block_tokens(G);
+    const double units = static_cast<double>(num_groups * ((tokens / num_groups + bt - 1) / bt)) *
+                         num_kv_heads * (num_groups > 1 ? (tiles + 1) / 2 : tiles);
+    const int64_t quota = static_cast<int64_t>(
+        std::max(1.0, std::min(std::ceil(units / sm_count()), 0x1p40)));
+    const int64_t n = tiles > 1 ? (tiles - 1 + quota - 1) / quota + 1 : 1;
+    *prefix_splits = static_cast<int32_t>(std::min<int64_t>(n, 16));
+    return SINKATTN_OK;
+  }
+  // the warp-level kernel's blocks of up to 64 query rows
+  const int64_t blocks =
+      std::min<int64_t>(num_groups + tokens * std::min(G, 64) / 64, int64_t{1} << 20);
+  return sinkattn_decode_default_splits(static_cast<int32_t>(blocks), 1, num_qo_heads, num_kv_heads,
+                                        head_dim, max_prefix_len, prefix_splits);
 }
 
 // Shared-prefix decode: the sequences' own keys and the groups' prefixes as
@@ -482,12 +535,12 @@ int decode_shared_impl(const void* q, const void* k_pages, const void* v_pages, 
     return fail(SINKATTN_INVALID_ARG, "num_groups must be positive, max_prefix_len non-negative");
   if (num_groups > 65535) return fail(SINKATTN_UNSUPPORTED, "num_groups %d exceeds 65535", num_groups);
   int32_t ps = 0, ss = 0;
-  int rc = sinkattn_decode_shared_default_splits(batch, q_len, num_qo_heads, num_kv_heads, head_dim,
-                                                 num_groups, max_prefix_len, max_suffix_len, &ps,
-                                                 &ss);
+  const int kind = decode_kind();   // (read once: the passes of a call go by one choice)
+  int rc = shared_splits(kind, batch, q_len, num_qo_heads, num_kv_heads, head_dim, num_groups,
+                         max_prefix_len, max_suffix_len, &ps, &ss);
   if (rc) return rc;
   const bool alone = prefix_splits <= 0 &&
-                     few_keys(batch, max_prefix_len, max_suffix_len, num_kv_heads, head_dim);
+                     few_keys(kind, batch, max_prefix_len, max_suffix_len, num_kv_heads, head_dim);
   if (prefix_splits <= 0) prefix_splits = ps;
   if (num_splits <= 0) num_splits = ss;
   if (max_prefix_len == 0) prefix_splits = 0;   // nothing is shared
@@ -510,8 +563,9 @@ int decode_shared_impl(const void* q, const void* k_pages, const void* v_pages, 
   if (static_cast<int64_t>(max_prefix_len) + max_suffix_len >= (int64_t{1} << 31) ||
       static_cast<int64_t>(num_groups) * max_prefix_len >= (int64_t{1} << 31))
     return fail(SINKATTN_UNSUPPORTED, "prefixes reach 2^31 keys");
+  if (static_cast<int64_t>(prefix_splits) + num_splits > 4096)
+    return fail(SINKATTN_UNSUPPORTED, "the splits exceed 4096 in all");
   const int slots = prefix_splits + num_splits;
-  if (slots > 4096) return fail(SINKATTN_UNSUPPORTED, "%d splits in all exceed 4096", slots);
   size_t need = 0;
   rc = sinkattn_decode_shared_workspace_bytes(batch, q_len, num_qo_heads, head_dim, num_groups,
                                               prefix_splits, num_splits, &need);
@@ -523,9 +577,31 @@ int decode_shared_impl(const void* q, const void* k_pages, const void* v_pages, 
   if (!out || !aligned16(out)) return fail(SINKATTN_INVALID_ARG, "out must be non-null and 16-byte aligned");
   if (lse && (reinterpret_cast<uintptr_t>(lse) & 3u))
     return fail(SINKATTN_INVALID_ARG, "lse must be 4-byte aligned");
+  set_paged(&a, &pg);
+  const int G = num_qo_heads / num_kv_heads;
+  const size_t rows = static_cast<size_t>(batch) * q_len;
+  const bool tc = prefix_on_tc(kind, static_cast<int64_t>(rows), G, num_groups);
+  // what a launch would refuse is refused here, before the first one
+  const bool own_tc = kind != SINKATTN_DECODE_WARP && decode_tc_supported(a);
+  if (kind == SINKATTN_DECODE_TCGEN05 && !own_tc)
+    return fail(SINKATTN_UNSUPPORTED,
+                "the tcgen05 shared-prefix decode needs head_dim 128 and bf16 pools");
+  if (num_kv_heads > 65535)
+    return fail(SINKATTN_UNSUPPORTED, "num_kv_heads %d exceeds 65535", num_kv_heads);
+  // blocks of query tokens that a pass forms at most, and its work items
+  auto blocks_of = [](int64_t n, int64_t per) { return (n + per - 1) / per; };
+  const int tile = prefix_tile_keys(head_dim, f8 != nullptr);
+  const int64_t prefix_items =
+      tc ? (num_groups + static_cast<int64_t>(rows) / prefix_block_tokens(G)) * num_kv_heads *
+               blocks_of(max_prefix_len, tile)
+         : (num_groups + static_cast<int64_t>(rows) / attn_mma_block_tokens(G, rows)) * prefix_splits;
+  const int64_t own_items =
+      own_tc ? blocks_of(q_len, std::min(q_len, 128 / G)) * batch * num_kv_heads * num_splits
+             : blocks_of(q_len, attn_mma_block_tokens(G, q_len)) * num_splits;
+  if (std::max(prefix_items, own_items) >= (int64_t{1} << 31))
+    return fail(SINKATTN_UNSUPPORTED, "too many work items");
   if (batch == 0) return SINKATTN_OK;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const size_t rows = static_cast<size_t>(batch) * q_len;
   const size_t plan_bytes = shared_plan_bytes(batch, q_len, num_groups);
   float* part_acc = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan_bytes);
   float* part_md = reinterpret_cast<float*>(
@@ -534,7 +610,6 @@ int decode_shared_impl(const void* q, const void* k_pages, const void* v_pages, 
   a.part_acc = part_acc;
   a.part_md = part_md;
   if (alone) {
-    set_paged(&a, &pg);
     if ((rc = launch_attn_mma(a, s))) return rc;
     const SharedCheck check{kv_indptr,    pg.page_indptr, group_indptr, prefix_lens,    num_groups,
                             pg.page_size, batch,          q_len,        max_prefix_len, max_suffix_len};
@@ -552,8 +627,6 @@ int decode_shared_impl(const void* q, const void* k_pages, const void* v_pages, 
   plan.grp_unit = plan.grp_pages + num_groups + 1;
   plan.quota = plan.grp_unit + num_groups + 1;
   plan.row_pos = plan.quota + 1;
-  const int G = num_qo_heads / num_kv_heads;
-  const bool tc = prefix_on_tc(static_cast<int64_t>(rows), G, num_groups);
   // (at d 128 a block of either pass fills its SM)
   SharedCost cost;
   cost.unit = head_dim == 64 ? 1.05f : 1.9f;
@@ -596,7 +669,7 @@ int decode_shared_impl(const void* q, const void* k_pages, const void* v_pages, 
   a.part_first = prefix_splits;
   // behind a prefix pass, the plan is complete (that pass waited for it)
   a.chain = prefix_splits > 0 ? kChainWaitLast : kChainWaitFirst;
-  if ((rc = launch_partials(a, s))) return rc;
+  if ((rc = launch_partials(a, kind, s))) return rc;
   return launch_merge_sparse(part_acc, part_md, sinks, static_cast<int32_t>(rows), num_qo_heads,
                              head_dim, slots, out, lse, nullptr, s);
 }
@@ -705,51 +778,8 @@ int sinkattn_decode_shared_default_splits(int32_t batch, int32_t q_len, int32_t 
                                           int32_t num_groups, int32_t max_prefix_len,
                                           int32_t max_suffix_len, int32_t* prefix_splits,
                                           int32_t* num_splits) {
-  g_last_error[0] = '\0';
-  if (!prefix_splits || !num_splits)
-    return fail(SINKATTN_INVALID_ARG, "prefix_splits and num_splits must be non-null");
-  if (num_groups < 1 || max_prefix_len < 0) return fail(SINKATTN_INVALID_ARG, "bad sizes");
-  if (batch < 0 || q_len < 1 || num_qo_heads <= 0 || num_kv_heads <= 0 || max_suffix_len < 0)
-    return fail(SINKATTN_INVALID_ARG, "bad sizes");
-  if (head_dim != 64 && head_dim != 128)
-    return fail(SINKATTN_UNSUPPORTED, "head_dim %d is not 64 or 128", head_dim);
-  if (few_keys(batch, max_prefix_len, max_suffix_len, num_kv_heads, head_dim)) {
-    *prefix_splits = 0;
-    return sinkattn_decode_default_splits(batch, q_len, num_qo_heads, num_kv_heads, head_dim,
-                                          max_prefix_len + max_suffix_len, num_splits);
-  }
-  // Own keys: chunks of about 1024 keys while they are needed to fill the SMs
-  // (the warp-level kernel's four blocks per SM twice over, the tcgen05
-  // kernel's one block twice over). Each further chunk costs its partials: 64
-  // sequences behind 8192 keys at d 64 take 33, 35 and 38 us in 1, 2 and 3
-  // chunks with up to 1024 own keys, 76, 59 and 59 us with up to 4000; 16
-  // sequences of up to 8000 own keys 96, 45, 40 and 37 us in 1, 3, 4 and 8.
-  const int64_t items = std::max<int64_t>(1, static_cast<int64_t>(batch) * num_kv_heads);
-  const int64_t fill = (head_dim == 64 ? 8 : 2) * static_cast<int64_t>(sm_count());
-  *num_splits = static_cast<int32_t>(std::max<int64_t>(
-      1, std::min<int64_t>((fill + items - 1) / items, (max_suffix_len + 1023) / 1024)));
-  const int G = num_qo_heads / num_kv_heads;
-  // (calls of 2^31 rows are refused: beyond, any answer does, within 64 bits)
-  const int64_t tokens = std::min<int64_t>(static_cast<int64_t>(batch) * q_len, int64_t{1} << 31);
-  if (G >= 1 && G <= 64 && prefix_on_tc(tokens, G, num_groups)) {
-    // partials that let the kernel deal its units out evenly (prefixes of
-    // several groups about half as long as the longest), at most 16
-    const int64_t tiles = (max_prefix_len + prefix_tile_keys(head_dim, false) - 1) /
-                          prefix_tile_keys(head_dim, false);
-    const int64_t bt = prefix_block_tokens(G);
-    const double units = static_cast<double>(num_groups * ((tokens / num_groups + bt - 1) / bt)) *
-                         num_kv_heads * (num_groups > 1 ? (tiles + 1) / 2 : tiles);
-    const int64_t quota = static_cast<int64_t>(
-        std::max(1.0, std::min(std::ceil(units / sm_count()), 0x1p40)));
-    const int64_t n = tiles > 1 ? (tiles - 1 + quota - 1) / quota + 1 : 1;
-    *prefix_splits = static_cast<int32_t>(std::min<int64_t>(n, 16));
-    return SINKATTN_OK;
-  }
-  // the warp-level kernel's blocks of up to 64 query rows
-  const int64_t blocks =
-      std::min<int64_t>(num_groups + tokens * std::min(G, 64) / 64, int64_t{1} << 20);
-  return sinkattn_decode_default_splits(static_cast<int32_t>(blocks), 1, num_qo_heads, num_kv_heads,
-                                        head_dim, max_prefix_len, prefix_splits);
+  return shared_splits(decode_kind(), batch, q_len, num_qo_heads, num_kv_heads, head_dim, num_groups,
+                       max_prefix_len, max_suffix_len, prefix_splits, num_splits);
 }
 
 int sinkattn_set_prefill_kernel(int kind) {

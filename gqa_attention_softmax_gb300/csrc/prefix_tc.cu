@@ -900,13 +900,9 @@ int launch(const AttnArgs& a, const SharedPlan& plan, cudaStream_t stream) {
   p.part_acc = a.part_acc;
   p.part_md = a.part_md;
   p.part_slots = part_slots(a);
-  // row blocks: at most one per group more than its full ones
+  // row blocks: at most one per group more than its full ones (units below 2^31: the caller checks)
   const int64_t tiles = (a.max_kv + C::KT - 1) / C::KT;
   const int64_t units = (a.batch + a.total_q / (C::NT * QB)) * a.Hkv * tiles;
-  if (units >= (int64_t{1} << 31)) {
-    set_error("too many work items");
-    return SINKATTN_UNSUPPORTED;
-  }
   auto kern = prefix_tc_kernel<D, FP8>;
   cudaError_t e = set_chained_smem(kern, C::SMEM);
   if (e == cudaSuccess) {

@@ -374,7 +374,8 @@ SINKATTN_API int sinkattn_decode_fp8(const void* q, const void* k, const void* v
  *   results of the sequences concerned are not defined.
  *   sinkattn_set_decode_kernel decides for the prefixes too: AUTO takes the
  *   tcgen05 kernel where a group has more than 48 query rows per KV head on
- *   average.
+ *   average. TCGEN05 takes it for both parts, which needs head_dim 128 and bf16
+ *   pools (SINKATTN_UNSUPPORTED otherwise).
  *   prefix_splits / num_splits: KV chunks of a prefix and of a sequence's own
  *   keys; <= 0 selects sinkattn_decode_shared_default_splits(). Its
  *   prefix_splits is 0 for a call of so few keys that it is faster to let every

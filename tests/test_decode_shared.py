@@ -735,3 +735,70 @@ def test_split_counts_of_sizes_beyond_64_bits():
                 ps, ss = sa.sinkattn_decode_shared_default_splits(B, ql, Hq, Hkv, d, ng, mp, 2 ** 31 - 1)
                 assert 1 <= ps <= 16 and 1 <= ss <= 4096
     assert raw(B=1 << 30, Hq=1 << 30, Hkv=1 << 30) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("kw", [
+    dict(),                                       # head_dim 64
+    dict(d=128, fp8=True),                        # codes, whose own keys have the warp-level kernel only
+    dict(fp8=True),
+])
+def test_forced_tcgen05_is_refused_before_any_launch(kw):
+    """(Without a GPU a launch is a CUDA error, so the status says which came first.)"""
+    kw = dict(kw)
+    fp8 = kw.pop("fp8", False)
+    sa.sinkattn_set_decode_kernel("tcgen05")
+    try:
+        if fp8:
+            rc = sa.lib().sinkattn_decode_shared_paged_fp8(
+                A16, A16, A16, A16, A16, A16, A16, A16, A16, A16, 2, 8, 16, 4, 1, 64, 40, 8, 2,
+                kw.get("d", 64), 0.125, 1, 0, 2, 2, None, WS, 1 << 30, A16, None, None)
+        else:
+            rc = raw(**kw)
+        text = sa.sinkattn_last_error()
+    finally:
+        sa.sinkattn_set_decode_kernel("auto")
+    assert rc == UNSUPPORTED and "tcgen05" in text
+
+
+@pytest.mark.parametrize("kw", [
+    # units of the tcgen05 prefix pass (8191 full row blocks of 8 KV heads x 32768 tiles of 96)
+    dict(B=65535, ql=4, ng=1, Hq=64, Hkv=8, mp=32768 * 96, ms=4),
+    dict(B=65535, ql=2048, ng=65535, Hq=16, Hkv=16, mp=32000, ms=2048, psp=2, ss=1),
+    dict(B=1, Hq=65536, Hkv=65536, mp=16, ms=1),
+])
+def test_calls_of_too_many_items_are_refused_before_any_launch(kw):
+    assert raw(npg=8, ps=256 if kw["Hkv"] < 100 else 16, wsb=1 << 62, **kw) == UNSUPPORTED
+
+
+@gpu
+@pytest.mark.parametrize("d,fp8", [(64, False), (64, True), (128, True)])
+def test_a_refused_call_leaves_its_buffers(d, fp8):
+    x, h = make([(20, [5] * 40)], 1, 64, 8, d, 16, seed=2, fp8=fp8)
+    g = {k: v.cuda() for k, v in x.items()}
+    bufs = dict(out=torch.full_like(g["q"], 7.0), lse=torch.full(g["q"].shape[:2], 7.0, device="cuda"),
+                workspace=torch.full((sa.sinkattn_decode_shared_workspace_bytes(40, 1, 64, d, 1, 4, 2),),
+                                     7, dtype=torch.uint8, device="cuda"))
+    sa.sinkattn_set_decode_kernel("tcgen05")
+    try:
+        with pytest.raises(sa.SinkAttnError) as e:
+            call(g, h, num_splits=2, **bufs)
+    finally:
+        sa.sinkattn_set_decode_kernel("auto")
+    assert e.value.status == UNSUPPORTED
+    torch.cuda.synchronize()
+    assert all((t == 7).all() for t in bufs.values())
+
+
+@gpu
+@pytest.mark.parametrize("case", [i for i, c in enumerate(CASES) if c[4] == 128],
+                         ids=[n for n, c in zip(IDS, CASES) if c[4] == 128])
+def test_forced_tcgen05_matches_oracle(case):
+    groups, q_len, Hq, Hkv, d, page, window, ps, ss, qs = CASES[case]
+    x, h = make(groups, q_len, Hq, Hkv, d, page, seed=page, q_scale=qs)
+    g = {k: v.cuda() for k, v in x.items()}
+    sa.sinkattn_set_decode_kernel("tcgen05")
+    try:
+        out, lse = call(g, h, window=window, prefix_splits=ps, num_splits=ss)
+    finally:
+        sa.sinkattn_set_decode_kernel("auto")
+    check(out, lse, x, h, window=window)
