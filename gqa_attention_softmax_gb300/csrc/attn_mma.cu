@@ -185,14 +185,16 @@ __global__ void __launch_bounds__(MmaCfg<D, RT, TG, KT, NST, FP8, SHARED>::THREA
       qb = x - p.blk[lo];
     }
     own = p.seq != nullptr;
-    if (own) at = p.seq[b];
+    if (own) at = chain_load(&p.seq[b]);
     free_rows = p.free_rows != 0;
     row_pos = p.row_pos;
   }
 
   const int q_start = p.cu_q ? p.cu_q[b] : at * p.q_len;
   const int Lq = p.cu_q ? p.cu_q[b + 1] - q_start : p.q_len;
-  const int k_start = p.cu_k[b];
+  int k_start;
+  if constexpr (SHARED) k_start = chain_load(&p.cu_k[b]);
+  else k_start = p.cu_k[b];
   const int Lk = own ? k_start : p.cu_k[b + 1] - k_start;
   const int q0 = qb * p.QB;
   if (q0 >= Lq) return;   // uniform over the CTA (and the cluster), before any barrier
@@ -244,7 +246,9 @@ __global__ void __launch_bounds__(MmaCfg<D, RT, TG, KT, NST, FP8, SHARED>::THREA
       const int slab = k_start * p.Hkv + kvh * Lk;   // contiguous: tensor-map row of key 0
       PageCursor pc;
       if (paged) {
-        const int e0 = p.page_indptr[b];
+        int e0;
+        if constexpr (SHARED) e0 = chain_load(&p.page_indptr[b]);
+        else e0 = p.page_indptr[b];
         const int np = own ? (Lk + p.page_size - 1) / p.page_size : p.page_indptr[b + 1] - e0;
         if (leader && Lk > np * p.page_size) atomicExch(&g_status_attn_mma, SINKATTN_BAD_LENGTHS);
         pc.start(p.page_indices + e0, np, first / p.page_size, lane);

@@ -15,4 +15,9 @@ __device__ __forceinline__ void grid_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// A word that a launch further back in the chain wrote. The launch between has
+// waited for that one, so the word is in L2; a launch that does not wait itself
+// must not take it from its SM's L1.
+__device__ __forceinline__ int32_t chain_load(const int32_t* p) { return __ldcg(p); }
+
 }  // namespace sinkattn

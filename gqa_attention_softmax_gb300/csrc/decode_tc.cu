@@ -84,7 +84,8 @@ __device__ __forceinline__ DtcItem dtc_item(const DtcParams& p, const int32_t* c
   t.q_start = t.b * p.q_len;
   t.q0 = qb * p.QB;
   t.nq = min(p.QB, p.q_len - t.q0);
-  t.k_start = cu[t.b];
+  // (SHARED: shared memory, or the plan's words around L1)
+  t.k_start = SHARED ? *const_cast<const volatile int32_t*>(&cu[t.b]) : cu[t.b];
   t.Lk = SHARED ? t.k_start : cu[t.b + 1] - t.k_start;
   t.pos0 = t.Lk - p.q_len + t.q0;
   const int posN = t.pos0 + t.nq - 1;
@@ -231,13 +232,14 @@ __global__ void __launch_bounds__(DtcCfg<RR, FP8>::THREADS, 1)
   const int n_cu = SHARED ? p.batch : p.batch + 1;
   const bool cu_in_smem = n_cu <= C::CU_CAP + 1;
   if (cu_in_smem)
-    for (int i = threadIdx.x; i < n_cu; i += blockDim.x) cu_s[i] = p.cu_k[i];
+    for (int i = threadIdx.x; i < n_cu; i += blockDim.x)
+      cu_s[i] = SHARED ? chain_load(&p.cu_k[i]) : p.cu_k[i];
   const int32_t* cu = cu_in_smem ? cu_s : p.cu_k;
   auto item_of = [&](int k) {
     return dtc_item<KT, PAGED, !FP8, SHARED>(p, cu, static_cast<int>(blockIdx.x) + k * static_cast<int>(gridDim.x));
   };
   auto q_start_of = [&](const DtcItem& t) -> int {
-    if constexpr (SHARED) return p.seq[t.b] * p.q_len;
+    if constexpr (SHARED) return chain_load(&p.seq[t.b]) * p.q_len;
     else return t.q_start;
   };
   auto slot_of = [&](size_t rowid, int split) -> size_t {
@@ -320,7 +322,7 @@ __global__ void __launch_bounds__(DtcCfg<RR, FP8>::THREADS, 1)
         }
         ++qi;
         if constexpr (PAGED) {
-          const int e0 = p.page_indptr[t.b];
+          const int e0 = SHARED ? chain_load(&p.page_indptr[t.b]) : p.page_indptr[t.b];
           const int np = SHARED ? (t.Lk + p.page_size - 1) / p.page_size : p.page_indptr[t.b + 1] - e0;
           if (leader && t.Lk > np * p.page_size) atomicExch(status, SINKATTN_BAD_LENGTHS);
           pc.start(p.page_indices + e0, np, t.first / p.page_size, lane);

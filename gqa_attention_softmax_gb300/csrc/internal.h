@@ -74,10 +74,11 @@ inline int kv_box_rows(const AttnArgs& a, int tile_keys) {
 // A chain of launches, each a programmatic dependent of the one before: a
 // launch may start while the one before it still runs. kChainWaitFirst: it
 // waits for that one's results before it reads anything. kChainWaitLast: it
-// needs none of them (the one before waited for what it does need), but its
-// first block ends only after it, so that whoever waits for this launch has
-// waited for both (one block, as a block that waits keeps its place on the SM).
-// kChainFollow: the next launch may start as soon as this one has waited.
+// needs none of them (the one before waited for what it does need, which this
+// one loads around L1, chain_load), but its first block ends only after it, so
+// that whoever waits for this launch has waited for both (one block, as a block
+// that waits keeps its place on the SM). kChainFollow: the next launch may
+// start as soon as this one has waited.
 constexpr int32_t kChainWaitFirst = 1, kChainWaitLast = 2, kChainFollow = 4;
 
 // Sets a kernel of a chain up: its dynamic shared memory, and the largest
