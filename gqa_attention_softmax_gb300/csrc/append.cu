@@ -54,8 +54,9 @@ __device__ __forceinline__ float quotient(float x, const Scale& c) {
   if constexpr (!PLAIN) return __fdiv_rn(x, c.s);
   const float q0 = x * c.r;
   const float q = fmaf(fmaf(-q0, c.s, x), c.r, q0);
-  // (an infinity, or a value that saturates, stays as it is; so does NaN)
-  return fabsf(q0) < 1024.f ? q : q0;
+  // (an infinity, or a value that saturates, stays as it is; so does NaN, and a
+  // zero, whose sign the residual step would lose)
+  return fabsf(q0) < 1024.f && q0 != 0.f ? q : q0;
 }
 
 template <bool PLAIN>

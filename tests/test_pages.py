@@ -663,3 +663,31 @@ def test_pools_past_32_bit_offsets():
     assert (page_map >= 0).sum().item() == 3
     held()
     assert sa.sinkattn_debug_status() == 0
+
+
+def codes_of(x, scale):
+    """The e4m3 codes of x / scale, by torch: [tokens, Hkv, d] under one scale per head."""
+    quot = (x.float() / scale[None, :, None]).clamp(-448.0, 448.0)
+    return quot.to(torch.float8_e4m3fn).view(torch.uint8)
+
+
+def appended(x, scale):
+    """The codes that the append writes for x, in the order of x."""
+    tokens, Hkv, d = x.shape
+    pools = [torch.full((-(-tokens // 16), Hkv, 16, d), 0x55, dtype=torch.uint8, device="cuda")
+             for _ in range(2)]
+    slots = torch.arange(tokens, dtype=torch.int32, device="cuda")
+    sa.sinkattn_append_paged_fp8(x, x, slots, scale, scale, *pools)
+    got = [p.transpose(1, 2).reshape(-1, Hkv, d)[:tokens] for p in pools]
+    assert torch.equal(*got)
+    return got[0]
+
+
+@gpu
+@pytest.mark.parametrize("scale", [1.0, 0.7, -0.7, 2.0 ** -99, 2.0 ** -110])
+def test_append_fp8_keeps_the_sign_of_a_zero(scale):
+    x = torch.tensor([0.0, -0.0] * 32, device="cuda").to(torch.bfloat16).view(1, 1, 64)
+    s = torch.tensor([scale], device="cuda")
+    want = codes_of(x, s)
+    assert sorted(set(want.reshape(-1).tolist())) == [0x00, 0x80]
+    assert torch.equal(appended(x, s), want)
