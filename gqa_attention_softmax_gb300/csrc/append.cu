@@ -12,8 +12,10 @@
 // from r = RN(1 / s) by one residual step, q0 = RN(x r), q = RN(q0 + r (x -
 // q0 s)) with the residual exact in an fma: Markstein's theorem ("Computation
 // of elementary functions on the IBM RISC System/6000", 1990) makes q the
-// correctly rounded quotient where nothing over- or underflows. Scales
-// outside [2^-100, 2^100] take IEEE divisions. 22000 tokens of 4 heads of 128
+// correctly rounded quotient where nothing over- or underflows. The residual's
+// last bit is that of q0 s: with q0 >= 2^-11 (half the least quotient whose code
+// is not zero) and s >= 2^-90 at least 2^(-11-23-90-23) = 2^-147, above fp32's
+// 2^-149. Scales outside [2^-90, 2^100] take IEEE divisions. 22000 tokens of 4 heads of 128
 // take 14 us as codes (16.6 with divisions; the bytes alone are 8), bound by
 // the conversions: issue slots 54 %, ALU 50 % busy.
 #include <algorithm>
@@ -46,7 +48,7 @@ struct Scale {
 
 __device__ __forceinline__ Scale make_scale(float s) {
   const float a = fabsf(s);
-  return {s, __frcp_rn(s), a >= 0x1p-100f && a <= 0x1p100f};
+  return {s, __frcp_rn(s), a >= 0x1p-90f && a <= 0x1p100f};
 }
 
 template <bool PLAIN>

@@ -691,3 +691,29 @@ def test_append_fp8_keeps_the_sign_of_a_zero(scale):
     want = codes_of(x, s)
     assert sorted(set(want.reshape(-1).tolist())) == [0x00, 0x80]
     assert torch.equal(appended(x, s), want)
+
+
+@gpu
+@pytest.mark.parametrize("bits", [-127, -104, -101, -100, -99, -97, -95, -93, -92, -91, -90, -89, -60,
+                                  0, 60, 99, 100, 101, 110])
+def test_append_fp8_codes_under_scales_of_any_size(bits):
+    """Bit for bit the codes of the fp32 quotient, ties and their neighbours among them: x / s next
+    to the borders between codes for scales of every mantissa end, where the residual step would be
+    one bit short of exact. (s = (2 - 2^-23) 2^-97, x = 2^-106: the quotient is one step above the
+    border 2^-10, so its code is 1 and not 0.)"""
+    gen = torch.Generator().manual_seed(abs(bits))
+    ends = torch.tensor([1.0, 1.0 + 2.0 ** -23, 2.0 - 2.0 ** -23, 2.0 - 2.0 ** -22, 1.5, 1.0 / 0.7])
+    s = torch.cat([ends, 1.0 + torch.rand(10, generator=gen)]).double() * 2.0 ** bits
+    s = s.float()
+    codes = torch.arange(0, 127, dtype=torch.uint8).view(torch.float8_e4m3fn).double()
+    border = torch.cat([(codes[1:] + codes[:-1]) / 2, codes])[:252]
+    x = (border[:, None] * s.double()[None, :]).to(torch.bfloat16)          # [252, 16 heads]
+    x = torch.stack([x, -x, x * 1.0078125, x * 0.99609375], dim=-1).to(torch.bfloat16)
+    two = torch.exp2(torch.arange(-11, 4).double() + bits).to(torch.bfloat16)   # powers of two at s
+    x = torch.cat([x, two.view(15, 1, 1).expand(15, 16, 4)])                   # [267, 16, 4]
+    x = x.repeat_interleave(16, dim=-1).contiguous().cuda()
+    s = s.cuda()
+    got, want = appended(x, s), codes_of(x, s)
+    nan = (want & 0x7f) == 0x7f
+    assert torch.equal((got & 0x7f) == 0x7f, nan)
+    assert torch.equal(got[~nan], want[~nan])
