@@ -457,17 +457,17 @@ def _stream_of(dev, stream):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _new(shape, dtype, dev, stream, kept=True, make=torch.empty):
+def _new(shape, dtype, dev, stream, kept=True):
     """A tensor for kernels on `stream`, taken from that stream's memory: what
     its bytes held before may still be read on another stream. One that the
     caller gets (`kept`) is used on the current stream too."""
     if stream is None:
-        return make(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=dtype, device=dev)
     here = torch.cuda.current_stream(dev)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(_stream_of(dev, stream), device=dev)
     with torch.cuda.stream(stream):
-        t = make(shape, dtype=dtype, device=dev)
+        t = torch.empty(shape, dtype=dtype, device=dev)
     if kept and stream.cuda_stream != here.cuda_stream:
         t.record_stream(here)
     return t
@@ -797,13 +797,12 @@ def sinkattn_pages_lists(table, seq_ids, kv_indptr=None, page_indptr=None, page_
     dev = table.device
     ids_p = _need(seq_ids, "seq_ids", torch.int32, dev, 1)
     n = seq_ids.shape[0]
-    make = torch.empty if n > 0 else torch.zeros   # an empty batch writes nothing
     if kv_indptr is None:
-        kv_indptr = _new((n + 1,), torch.int32, dev, stream, make=make)
+        kv_indptr = _new((n + 1,), torch.int32, dev, stream)
     if page_indptr is None:
-        page_indptr = _new((n + 1,), torch.int32, dev, stream, make=make)
+        page_indptr = _new((n + 1,), torch.int32, dev, stream)
     if page_indices is None:
-        page_indices = _new((n * table.max_pages,), torch.int32, dev, stream, make=make)
+        page_indices = _new((n * table.max_pages,), torch.int32, dev, stream)
     kv_p = _need(kv_indptr, "kv_indptr", torch.int32, dev, (n + 1,))
     pp_p = _need(page_indptr, "page_indptr", torch.int32, dev, (n + 1,))
     pi_p = _need(page_indices, "page_indices", torch.int32, dev, 1)

@@ -749,6 +749,11 @@ __global__ void __launch_bounds__(256)
   __shared__ long long part[2][8];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int i = blockIdx.x;
+  if (n == 0) {   // no sequences: the running sums are their first zeros
+    if (tid == 0 && kv_indptr) kv_indptr[0] = 0;
+    if (tid == 0 && page_indptr) page_indptr[0] = 0;
+    return;
+  }
   auto len_of = [&](int j) -> int {
     const int id = ids[j];
     if (!t.seq_ok(id)) return -1;
@@ -1047,13 +1052,13 @@ int sinkattn_pages_lists(const int32_t* table, int32_t num_pages, int32_t page_s
   if (rc) return rc;
   if (n < 0 || capacity < 0)
     return refuse(SINKATTN_INVALID_ARG, "n and capacity must be non-negative");
-  if (n == 0) return SINKATTN_OK;
-  if (!seq_ids || !kv_indptr || !page_indptr || (capacity > 0 && !page_indices) ||
+  if (n == 0 && !kv_indptr && !page_indptr) return SINKATTN_OK;
+  if ((n > 0 && (!seq_ids || !kv_indptr || !page_indptr || (capacity > 0 && !page_indices))) ||
       !aligned(seq_ids, 4) || !aligned(kv_indptr, 4) || !aligned(page_indptr, 4) ||
       !aligned(page_indices, 4))
     return refuse(SINKATTN_INVALID_ARG,
                   "seq_ids, kv_indptr, page_indptr and page_indices must be non-null and 4-byte aligned");
-  pages_lists_kernel<<<static_cast<unsigned>(n), 256, 0, static_cast<cudaStream_t>(stream)>>>(
+  pages_lists_kernel<<<static_cast<unsigned>(std::max(n, 1)), 256, 0, static_cast<cudaStream_t>(stream)>>>(
       t, seq_ids, n, kv_indptr, page_indptr, page_indices, capacity);
   return launched(cudaGetLastError(), "page lists launch");
 }

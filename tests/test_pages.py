@@ -717,3 +717,19 @@ def test_append_fp8_codes_under_scales_of_any_size(bits):
     nan = (want & 0x7f) == 0x7f
     assert torch.equal((got & 0x7f) == 0x7f, nan)
     assert torch.equal(got[~nan], want[~nan])
+
+
+@gpu
+def test_lists_of_no_sequences_write_their_zeros():
+    p = Pair(8, 16, 4, 4)
+    kv, ptr, idx = i32([9]), i32([9]), i32([9, 9])
+    got = sa.sinkattn_pages_lists(p.table, i32([]), kv_indptr=kv, page_indptr=ptr, page_indices=idx)
+    assert got[0] is kv and kv.tolist() == [0] and ptr.tolist() == [0] and idx.tolist() == [9, 9]
+    kv, ptr, idx = sa.sinkattn_pages_lists(p.table, i32([]))
+    assert kv.tolist() == [0] and ptr.tolist() == [0] and idx.numel() == 0
+    L, none = sa.lib(), i32([9])
+    args = p.table._args
+    assert L.sinkattn_pages_lists(*args, None, 0, none.data_ptr(), None, None, 0, None) == 0
+    torch.cuda.synchronize()
+    assert none.tolist() == [0]
+    p.check()
