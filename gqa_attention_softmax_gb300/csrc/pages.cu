@@ -740,7 +740,8 @@ __global__ void __launch_bounds__(256)
 
 // ---------------------------------------------------------------------------
 // lists: one block per sequence; each block sums the lengths before its own
-// (n loads over 256 threads, from L2) rather than wait for a scan.
+// (n loads over 256 threads, from L2) rather than wait for a scan. That is n^2
+// loads in all, so n is bounded (a table has at most 2^18 sequences).
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(256)
     pages_lists_kernel(const PageTab t, const int32_t* __restrict__ ids, int n,
@@ -1052,6 +1053,7 @@ int sinkattn_pages_lists(const int32_t* table, int32_t num_pages, int32_t page_s
   if (rc) return rc;
   if (n < 0 || capacity < 0)
     return refuse(SINKATTN_INVALID_ARG, "n and capacity must be non-negative");
+  if (n > (1 << 18)) return refuse(SINKATTN_UNSUPPORTED, "n exceeds 2^18");
   if (n == 0 && !kv_indptr && !page_indptr) return SINKATTN_OK;
   if ((n > 0 && (!seq_ids || !kv_indptr || !page_indptr || (capacity > 0 && !page_indices))) ||
       !aligned(seq_ids, 4) || !aligned(kv_indptr, 4) || !aligned(page_indptr, 4) ||

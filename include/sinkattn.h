@@ -536,14 +536,14 @@ SINKATTN_API int sinkattn_pages_compact(int32_t* table, int32_t num_pages, int32
                                         int32_t* page_map, void* stream);
 
 /*
- * The paged attention's view of n sequences of a table: kv_indptr [n + 1] and
- * page_indptr [n + 1] (running sums of lengths and of page counts), and their
- * page lists one after the other in page_indices (capacity entries; what lies
- * past the last list stays as it was). Lists that do not fit, and lengths
- * whose sum passes 2^31 - 1, record SINKATTN_BAD_LENGTHS and are left out; an
- * id outside the table counts as an empty sequence and records
- * SINKATTN_BAD_PAGES. With n 0 the first entries, zero, are written where
- * the pointers are given.
+ * The paged attention's view of n <= 2^18 sequences of a table (an id may come
+ * more than once): kv_indptr [n + 1] and page_indptr [n + 1] (running sums of
+ * lengths and of page counts), and their page lists one after the other in
+ * page_indices (capacity entries; what lies past the last list stays as it
+ * was). Lists that do not fit, and lengths whose sum passes 2^31 - 1, record
+ * SINKATTN_BAD_LENGTHS and are left out; an id outside the table counts as an
+ * empty sequence and records SINKATTN_BAD_PAGES. With n 0 the first entries,
+ * zero, are written where the pointers are given.
  */
 SINKATTN_API int sinkattn_pages_lists(const int32_t* table, int32_t num_pages, int32_t page_size,
                                       int32_t max_seqs, int32_t max_pages,

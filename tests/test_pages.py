@@ -733,3 +733,10 @@ def test_lists_of_no_sequences_write_their_zeros():
     torch.cuda.synchronize()
     assert none.tolist() == [0]
     p.check()
+
+
+def test_lists_of_more_sequences_than_a_table_can_have_are_refused():
+    """(Each sequence's block sums the lengths before its own: 2^31 ids would keep a GPU for days.)"""
+    for n in ((1 << 18) + 1, 2 ** 31 - 1):
+        assert sa.lib().sinkattn_pages_lists(A, 8, 16, 4, 4, A, n, A, A, A, 8, None) == UNSUPPORTED
+        assert "2^18" in sa.sinkattn_last_error()
