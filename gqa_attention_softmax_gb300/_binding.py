@@ -447,6 +447,16 @@ def _need_cuda(t, what):
     return t.device
 
 
+def _i32(*sizes):
+    """The sizes as integers that the entry points' 32-bit arguments hold (ctypes would
+    drop the upper bits)."""
+    sizes = [int(x) for x in sizes]
+    for x in sizes:
+        if not -2 ** 31 <= x < 2 ** 31:
+            raise SinkAttnError(INVALID_ARG, "%d does not fit a 32-bit size" % x)
+    return sizes
+
+
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
@@ -489,9 +499,8 @@ def sinkattn_decode_shared_default_splits(batch, q_len, num_qo_heads, num_kv_hea
     """(prefix_splits, num_splits) the shared-prefix decode uses by default."""
     a, b = ctypes.c_int32(0), ctypes.c_int32(0)
     _check(lib().sinkattn_decode_shared_default_splits(
-        int(batch), int(q_len), int(num_qo_heads), int(num_kv_heads), int(head_dim),
-        int(num_groups), int(max_prefix_len), int(max_suffix_len), ctypes.byref(a),
-        ctypes.byref(b)))
+        *_i32(batch, q_len, num_qo_heads, num_kv_heads, head_dim, num_groups, max_prefix_len,
+              max_suffix_len), ctypes.byref(a), ctypes.byref(b)))
     return int(a.value), int(b.value)
 
 
@@ -499,8 +508,8 @@ def sinkattn_decode_shared_workspace_bytes(batch, q_len, num_qo_heads, head_dim,
                                            prefix_splits, num_splits) -> int:
     n = ctypes.c_size_t(0)
     _check(lib().sinkattn_decode_shared_workspace_bytes(
-        int(batch), int(q_len), int(num_qo_heads), int(head_dim), int(num_groups),
-        int(prefix_splits), int(num_splits), ctypes.byref(n)))
+        *_i32(batch, q_len, num_qo_heads, head_dim, num_groups, prefix_splits, num_splits),
+        ctypes.byref(n)))
     return int(n.value)
 
 
@@ -508,6 +517,7 @@ def sinkattn_decode_shared_workspace_bytes(batch, q_len, num_qo_heads, head_dim,
 def _shared_sizes(device_index, prefix_splits, num_splits, batch, q_len, Hq, Hkv, d, groups,
                   max_prefix_len, max_suffix_len):
     """(prefix_splits, num_splits, workspace bytes) of these sizes (host arithmetic only)."""
+    _i32(prefix_splits, num_splits, max_prefix_len, max_suffix_len)
     if num_splits <= 0 or prefix_splits <= 0:
         ps, ss = sinkattn_decode_shared_default_splits(batch, q_len, Hq, Hkv, d, groups,
                                                        max_prefix_len, max_suffix_len)
@@ -564,8 +574,8 @@ def _decode_shared(entry, pool_dtype, scales, q, k_pages, v_pages, kv_indptr, pa
         return out, lse
     _launch(dev, entry, q_p, k_p, v_p, *scale_p, kv_p, pp_p, pi_p, gp_p, pl_p, groups, num_pages,
             page_size, batch, q_len, max_prefix_len, max_suffix_len, Hq, Hkv, d,
-            _scale(sm_scale, d), 1 if causal else 0, int(window), prefix_splits, num_splits,
-            sinks_p, workspace.data_ptr(), workspace.numel() * workspace.element_size(), out_p,
+            _scale(sm_scale, d), 1 if causal else 0, min(int(window), 2 ** 31 - 1), prefix_splits,
+            num_splits, sinks_p, workspace.data_ptr(), workspace.numel() * workspace.element_size(), out_p,
             lse_p, _stream_of(dev, stream))
     return out, lse
 
@@ -643,8 +653,7 @@ def sinkattn_append_paged_fp8(k, v, slots, k_scale, v_scale, k_pages, v_pages, s
 
 def sinkattn_pages_table_ints(num_pages, max_seqs, max_pages) -> int:
     n = ctypes.c_int64(0)
-    _check(lib().sinkattn_pages_table_ints(int(num_pages), int(max_seqs), int(max_pages),
-                                           ctypes.byref(n)))
+    _check(lib().sinkattn_pages_table_ints(*_i32(num_pages, max_seqs, max_pages), ctypes.byref(n)))
     return int(n.value)
 
 
@@ -657,6 +666,7 @@ class PageTable:
 
     def __init__(self, state, num_pages, page_size, max_seqs, max_pages, device="cuda",
                  stream=None):
+        num_pages, page_size, max_seqs, max_pages = _i32(num_pages, page_size, max_seqs, max_pages)
         need = 16 + max_seqs * (8 + max_pages) + 4 * num_pages
         new = state is None
         if new:
@@ -744,7 +754,7 @@ def sinkattn_pages_reserve(table, seq_ids, cu_new, total_new, k_pages, v_pages, 
     ids_p = _need(seq_ids, "seq_ids", torch.int32, dev, 1)
     n = seq_ids.shape[0]
     cu_p = _need(cu_new, "cu_new", torch.int32, dev, (n + 1,))
-    total_new = int(total_new)
+    total_new, = _i32(total_new)
     if slots is None:
         slots = _new((max(total_new, 0),), torch.int32, dev, stream)
         slots_p = slots.data_ptr()

@@ -802,3 +802,34 @@ def test_forced_tcgen05_matches_oracle(case):
     finally:
         sa.sinkattn_set_decode_kernel("auto")
     check(out, lse, x, h, window=window)
+
+
+def test_sizes_beyond_32_bits_are_refused():
+    """(As 32-bit arguments they would be other sizes: 2^32 + 64 keys would be 64.)"""
+    with pytest.raises(sa.SinkAttnError) as e:
+        sa.sinkattn_decode_shared_workspace_bytes(2 ** 32 + 4, 1, 8, 64, 1, 2, 2)
+    assert e.value.status == INVALID_ARG
+    with pytest.raises(sa.SinkAttnError) as e:
+        sa.sinkattn_decode_shared_default_splits(4, 1, 8, 2, 64, 1, 2 ** 32 + 64, 40)
+    assert e.value.status == INVALID_ARG
+
+
+@gpu
+@pytest.mark.parametrize("name", ["max_prefix", "max_suffix"])
+def test_key_bounds_beyond_32_bits_are_refused(name):
+    x, h = make([(4, [5, 9])], 1, 8, 1, 64, 16)
+    g = {k: v.cuda() for k, v in x.items()}
+    for n in (2 ** 32 + h[name], 2 ** 31):
+        with pytest.raises(sa.SinkAttnError) as e:
+            call(g, dict(h, **{name: n}))
+        assert e.value.status == INVALID_ARG
+
+
+@gpu
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31, 2 ** 32 + 5])
+def test_a_window_wider_than_any_sequence_hides_nothing(window):
+    x, h = make([(4, [5, 9, 60])], 2, 64, 8, 64, 16, seed=4)
+    g = {k: v.cuda() for k, v in x.items()}
+    for share in (4, 0):
+        out, lse = call(g, h, window=window, prefix_splits=share)
+        check(out, lse, x, h)

@@ -740,3 +740,23 @@ def test_lists_of_more_sequences_than_a_table_can_have_are_refused():
     for n in ((1 << 18) + 1, 2 ** 31 - 1):
         assert sa.lib().sinkattn_pages_lists(A, 8, 16, 4, 4, A, n, A, A, A, 8, None) == UNSUPPORTED
         assert "2^18" in sa.sinkattn_last_error()
+
+
+def test_sizes_beyond_32_bits_are_refused():
+    """(As 32-bit arguments they would be other sizes: 2^32 + 8 pages would be 8.)"""
+    for call in (lambda: sa.sinkattn_pages_table_ints(2 ** 32 + 8, 4, 4),
+                 lambda: sa.sinkattn_pages_table_ints(8, 4, -2 ** 31 - 1),
+                 lambda: sa.PageTable(None, 2 ** 32 + 8, 16, 4, 4),
+                 lambda: sa.PageTable(None, 8, 2 ** 32 + 16, 4, 4)):
+        with pytest.raises(sa.SinkAttnError) as e:
+            call()
+        assert e.value.status == INVALID_ARG and "32-bit" in str(e.value)
+
+
+@gpu
+def test_a_reserve_of_2_to_the_32_tokens_is_refused():
+    p = Pair(8, 16, 4, 4)
+    with pytest.raises(sa.SinkAttnError) as e:
+        sa.sinkattn_pages_reserve(p.table, i32([0]), i32([0, 0]), 2 ** 32, p.k, p.v)
+    assert e.value.status == INVALID_ARG
+    p.check()
