@@ -760,3 +760,28 @@ def test_a_reserve_of_2_to_the_32_tokens_is_refused():
         sa.sinkattn_pages_reserve(p.table, i32([0]), i32([0, 0]), 2 ** 32, p.k, p.v)
     assert e.value.status == INVALID_ARG
     p.check()
+
+
+@gpu
+def test_a_table_of_the_most_sequences():
+    """2^18 sequences of one table in every call, one token each at first."""
+    S, N = 1 << 18, (1 << 18) + 8
+    table = sa.PageTable(None, N, 16, S, 4)
+    k, v = (torch.zeros((N, 1, 16, 8), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    ids = torch.arange(S, dtype=torch.int32, device="cuda")
+    cu = torch.arange(S + 1, dtype=torch.int32, device="cuda")
+    low, high = ids[:S // 2], ids[S // 2:]
+    assert torch.equal(sa.sinkattn_pages_reserve(table, ids, cu, S, k, v), 16 * ids)
+    kv, ptr, pages = sa.sinkattn_pages_lists(table, ids)
+    assert torch.equal(kv, cu) and torch.equal(ptr, cu) and torch.equal(pages[:S], ids)
+    sa.sinkattn_pages_truncate(table, high)
+    assert table.free_count.item() == S // 2 + 8
+    sa.sinkattn_pages_fork(table, low, high)
+    assert (table.refcount[:S // 2] == 2).all() and torch.equal(table.page_list[S // 2:, 0], low)
+    # every holder writes: the first keeps its page, the other takes a copy
+    slots = sa.sinkattn_pages_reserve(table, ids, cu, S, k, v)
+    assert torch.equal(slots[:S // 2], 16 * low + 1) and (slots[S // 2:] % 16 == 1).all()
+    assert table.free_count.item() == 8 and (table.seq_lens == 2).all()
+    sa.sinkattn_pages_truncate(table, ids)
+    assert table.free_count.item() == N and (table.page_list == -1).all()
+    assert torch.equal(table.free_list.sort().values, torch.arange(N, dtype=torch.int32, device="cuda"))
