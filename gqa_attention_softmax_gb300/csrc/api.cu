@@ -444,6 +444,7 @@ int decode_impl(const void* q, const void* k, const void* v, const int32_t* kv_i
 // at d 128; 64 rows 22.5 and 20.9, 37.5 and 25.6; behind 1024 keys 48 rows 13.2
 // and 14.5, 15.3 and 18.3; 64 rows 14.0 and 14.9, 20.0 and 18.4.
 // (A group's sequences come as one run of rows: 4 samples of 8 heads are 32.)
+// Measured with bf16 pools; codes go by the same border.
 bool prefix_on_tc(int kind, int64_t tokens, int G, int64_t groups) {
   if (kind != SINKATTN_DECODE_AUTO) return kind == SINKATTN_DECODE_TCGEN05;
   return tokens * G > 48 * groups;
@@ -454,7 +455,9 @@ bool prefix_on_tc(int kind, int64_t tokens, int G, int64_t groups) {
 // the whole batch, in millions, us per call shared | not, 4 to 64 sequences: at
 // d 64 2.2: 12.6 | 8.3, 4.4: 14.6 | 8.7, 8.5: 15 to 16.5 | 14.5 to 14.8, 9.7:
 // 16.4 | 15.5, 17: 17.7 to 19.6 | 20.3 to 24.4; at d 128 4.4: 18.5 | 10.0, 9.7:
-// 22.5 | 17.9, 17: 20.9 to 25.8 | 17.8 to 26.1.
+// 22.5 | 17.9, 17: 20.9 to 25.8 | 17.8 to 26.1. (bf16 pools; codes go by the same
+// border. A window does not count here: with one of 128 behind 8192 keys, 64
+// sequences at d 64 take 17.6 us shared and 20.0 each for itself, 4 16.3 and 9.1.)
 bool few_keys(int kind, int64_t batch, int64_t max_prefix, int64_t max_suffix, int64_t Hkv,
               int64_t d) {
   // (one division at a time: the product of any sizes may pass 64 bits)
@@ -627,7 +630,7 @@ int decode_shared_impl(const void* q, const void* k_pages, const void* v_pages, 
   plan.grp_unit = plan.grp_pages + num_groups + 1;
   plan.quota = plan.grp_unit + num_groups + 1;
   plan.row_pos = plan.quota + 1;
-  // (at d 128 a block of either pass fills its SM)
+  // (at d 128 a block of either pass fills its SM; bf16 figures, for codes too)
   SharedCost cost;
   cost.unit = head_dim == 64 ? 1.05f : 1.9f;
   cost.own_key = head_dim == 64 ? 0.35f / 64 * num_kv_heads : 0.f;

@@ -1,8 +1,8 @@
 // Writes new keys and values into the pages of a paged cache, as bf16 or as
 // e4m3 codes under one scale per KV head (rules: sinkattn.h).
 //
-// One pass, bound by HBM: each thread takes one 16-byte run of a pool row in
-// K and the same run in V, so a row (head_dim elements of one head of one
+// One pass: each thread takes one 16-byte run of a pool row in K and the same
+// run in V, so a row (head_dim elements of one head of one
 // token) is written in full 16-byte lanes, and consecutive lanes read
 // consecutive heads of the token. With codes a thread reads two 16-byte runs
 // per pool instead of one.
@@ -16,9 +16,12 @@
 // last bit is that of q0 s: with q0 >= 2^-11 (half the least quotient whose code
 // is not zero) and s >= 2^-90 at least 2^(-11-23-90-23) = 2^-147, above fp32's
 // 2^-149. Scales outside [2^-90, 2^100] (negative ones, whose zeros it would
-// give the wrong sign) take IEEE divisions. 22000 tokens of 4 heads of 128
-// take 14 us as codes (16.6 with divisions; the bytes alone are 8), bound by
-// the conversions: issue slots 54 %, ALU 50 % busy.
+// give the wrong sign) take IEEE divisions.
+//
+// 22000 tokens of 4 heads of 128 (68 MB) take 10.4 us as codes with all of it in
+// L2, 17 from DRAM, where the bytes alone are 10 and the latency of the loads binds:
+// 64 registers a thread leave 40 % of the warps resident, and what an
+// instruction waits for is a load (5 cycles of 9; issue slots 54 %, ALU 50 %).
 #include <algorithm>
 
 #include "common.cuh"
@@ -181,7 +184,8 @@ int append(const void* k, const void* v, int64_t k_stride, int64_t v_stride, con
   p.n_slots = static_cast<long long>(num_pages) * page_size;
   const int64_t per = width / (fp8 ? 16 : 8);   // runs of a token
   if (per > (1 << 20)) return refuse(SINKATTN_UNSUPPORTED, "more than 2^20 runs in a token");
-  // two runs a thread, but one while that leaves SMs without a block (22000
+  // two runs a thread, but one while that leaves SMs without a block (with the
+  // reserve and the lists of the same tokens and a copy of the table: 22000
   // tokens as codes 23.2 us with two, 23.8 with one; 64 tokens 11.1 and 10.8)
   const int64_t blocks1 = (tokens * per + 255) / 256;
   const int64_t runs = blocks1 >= 8LL * sm_count() ? 512 : 256;

@@ -8,8 +8,9 @@
 // would cost two microseconds each, and nothing has to be read back by the
 // host, so every call can be captured into a graph. A call with up to
 // kOneBlock entries runs as one block, larger ones as a cluster of kCluster.
-// Before the first barrier a call only checks and writes scratch; one that
-// cannot be served as a whole ends there, with the table unchanged.
+// Before the first barrier a call checks and writes scratch; one that cannot
+// be served as a whole ends there, with the table unchanged. (Reserve takes its
+// pages off the free count there, by the thread that has the check's result.)
 //
 // No result depends on the order in which atomics arrive: they only count,
 // or elect a page's first writer or first appearance by its position (a
