@@ -19,9 +19,10 @@
 // give the wrong sign) take IEEE divisions.
 //
 // 22000 tokens of 4 heads of 128 (68 MB) take 10.4 us as codes with all of it in
-// L2, 17 from DRAM, where the bytes alone are 10 and the latency of the loads binds:
-// 64 registers a thread leave 40 % of the warps resident, and what an
-// instruction waits for is a load (5 cycles of 9; issue slots 54 %, ALU 50 %).
+// L2, 17.6 from DRAM, where the bytes alone are 10 and the latency of the loads
+// binds: 64 registers a thread leave 41 % of the warps resident, and 5 of the 12
+// cycles from a warp's instruction to its next are a load's (issue slots 53 %,
+// ALU 50 %).
 #include <algorithm>
 
 #include "common.cuh"
