@@ -580,6 +580,7 @@ int decode_shared_impl(const void* q, const void* k_pages, const void* v_pages, 
   if (!out || !aligned16(out)) return fail(SINKATTN_INVALID_ARG, "out must be non-null and 16-byte aligned");
   if (lse && (reinterpret_cast<uintptr_t>(lse) & 3u))
     return fail(SINKATTN_INVALID_ARG, "lse must be 4-byte aligned");
+  if (batch == 0) return SINKATTN_OK;
   set_paged(&a, &pg);
   const int G = num_qo_heads / num_kv_heads;
   const size_t rows = static_cast<size_t>(batch) * q_len;
@@ -603,7 +604,6 @@ int decode_shared_impl(const void* q, const void* k_pages, const void* v_pages, 
              : blocks_of(q_len, attn_mma_block_tokens(G, q_len)) * num_splits;
   if (std::max(prefix_items, own_items) >= (int64_t{1} << 31))
     return fail(SINKATTN_UNSUPPORTED, "too many work items");
-  if (batch == 0) return SINKATTN_OK;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const size_t plan_bytes = shared_plan_bytes(batch, q_len, num_groups);
   float* part_acc = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan_bytes);

@@ -833,3 +833,12 @@ def test_a_window_wider_than_any_sequence_hides_nothing(window):
     for share in (4, 0):
         out, lse = call(g, h, window=window, prefix_splits=share)
         check(out, lse, x, h)
+
+
+@pytest.mark.parametrize("kernel", ["auto", "warp", "tcgen05"])
+def test_empty_batch_is_a_no_op_under_any_kernel(kernel):
+    sa.sinkattn_set_decode_kernel(kernel)
+    try:
+        assert raw(B=0) == 0
+    finally:
+        sa.sinkattn_set_decode_kernel("auto")
