@@ -14,7 +14,13 @@ decode of sequences that share prefixes) with
 ``PageTable`` with ``sinkattn_pages_table_ints``, ``sinkattn_pages_init``,
 ``sinkattn_pages_reserve``, ``sinkattn_pages_fork``, ``sinkattn_pages_truncate``,
 ``sinkattn_pages_compact``, ``sinkattn_pages_lists`` (which sequence holds which
-pages),
+pages), ``sinkattn_prefill_backward`` with
+``sinkattn_prefill_backward_workspace_bytes`` (gradients of the prefill),
+``Rope`` with ``sinkattn_rope_frequencies`` and ``sinkattn_rope_turns`` (rotary
+positions), ``sinkattn_rope_qkv`` (norms and rotation on the way to the
+prefill), ``sinkattn_rope_qkv_backward`` with
+``sinkattn_rope_qkv_backward_workspace_bytes``, ``sinkattn_rope_append_paged``,
+``sinkattn_rope_append_paged_fp8`` (the same on the way into the pages),
 ``sinkattn_status_string``,
 ``sinkattn_last_error``, ``sinkattn_debug_status``, ``sinkattn_debug_set_hooks`` (tests),
 ``sinkattn_set_decode_kernel``,
@@ -25,6 +31,7 @@ call raises (there is no CPU fallback).
 """
 from ._binding import (  # noqa: F401
     PageTable,
+    Rope,
     SinkAttnError,
     lib,
     sinkattn_append_paged,
@@ -55,7 +62,16 @@ from ._binding import (  # noqa: F401
     sinkattn_pages_table_ints,
     sinkattn_pages_truncate,
     sinkattn_prefill,
+    sinkattn_prefill_backward,
+    sinkattn_prefill_backward_workspace_bytes,
     sinkattn_prefill_paged,
+    sinkattn_rope_append_paged,
+    sinkattn_rope_append_paged_fp8,
+    sinkattn_rope_frequencies,
+    sinkattn_rope_qkv,
+    sinkattn_rope_qkv_backward,
+    sinkattn_rope_qkv_backward_workspace_bytes,
+    sinkattn_rope_turns,
     sinkattn_set_decode_kernel,
     sinkattn_set_prefill_kernel,
     sinkattn_status_string,

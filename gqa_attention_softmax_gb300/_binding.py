@@ -96,6 +96,22 @@ def lib() -> ctypes.CDLL:
             L.sinkattn_pages_truncate.argtypes = T + [P, P, I32, P]
             L.sinkattn_pages_compact.argtypes = T + [P, P, I32, I64, I32, I32, P, P]
             L.sinkattn_pages_lists.argtypes = T + [P, I32, P, P, P, I32, P]
+            L.sinkattn_prefill_backward.argtypes = (
+                [P] * 10 + [I32] * 8 + [F] + [I32] * 2 + [P] * 5 + [SZ, P])
+            L.sinkattn_prefill_backward_workspace_bytes.argtypes = [I32, I32, ctypes.POINTER(SZ)]
+            D = ctypes.c_double
+            L.sinkattn_rope_frequencies.argtypes = [I32, D, I32, D, I32, D, D, P, P]
+            L.sinkattn_rope_turns.argtypes = [P, I32, P]
+            R = [P, I32, I32, F, P, P, F]   # turns .. eps
+            L.sinkattn_rope_qkv.argtypes = [P] * 3 + [I64] * 3 + [P] * 2 + [I32] * 5 + R + [P] * 4
+            L.sinkattn_rope_qkv_backward.argtypes = (
+                [P] * 5 + [I64] * 2 + [P] * 2 + [I32] * 5 + R + [P] * 3 + [I64] * 3 + [P] * 3
+                + [SZ, P])
+            L.sinkattn_rope_qkv_backward_workspace_bytes.argtypes = [I32, I32, ctypes.POINTER(SZ)]
+            L.sinkattn_rope_append_paged.argtypes = (
+                [P] * 3 + [I64] * 3 + [P] * 2 + [I32] * 4 + R + [P] * 3 + [I32] * 2 + [P])
+            L.sinkattn_rope_append_paged_fp8.argtypes = (
+                [P] * 3 + [I64] * 3 + [P] * 2 + [I32] * 4 + R + [P] * 5 + [I32] * 2 + [P])
             for name in ("sinkattn_prefill", "sinkattn_decode_split", "sinkattn_merge",
                          "sinkattn_decode", "sinkattn_decode_fused", "sinkattn_decode_noalloc",
                          "sinkattn_decode_workspace_bytes", "sinkattn_decode_default_splits",
@@ -111,7 +127,12 @@ def lib() -> ctypes.CDLL:
                          "sinkattn_append_paged_fp8", "sinkattn_pages_table_ints",
                          "sinkattn_pages_init", "sinkattn_pages_reserve", "sinkattn_pages_fork",
                          "sinkattn_pages_truncate", "sinkattn_pages_compact",
-                         "sinkattn_pages_lists"):
+                         "sinkattn_pages_lists", "sinkattn_prefill_backward",
+                         "sinkattn_prefill_backward_workspace_bytes",
+                         "sinkattn_rope_frequencies", "sinkattn_rope_turns", "sinkattn_rope_qkv",
+                         "sinkattn_rope_qkv_backward",
+                         "sinkattn_rope_qkv_backward_workspace_bytes",
+                         "sinkattn_rope_append_paged", "sinkattn_rope_append_paged_fp8"):
                 getattr(L, name).restype = ctypes.c_int
             _lib = L
     return _lib
@@ -819,6 +840,309 @@ def sinkattn_pages_lists(table, seq_ids, kv_indptr=None, page_indptr=None, page_
     _launch(dev, lib().sinkattn_pages_lists, *table._args, ids_p, n, kv_p, pp_p, pi_p,
             page_indices.shape[0], _stream_of(dev, stream))
     return kv_indptr, page_indptr, page_indices
+
+
+def sinkattn_prefill_backward_workspace_bytes(total_q, num_qo_heads) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().sinkattn_prefill_backward_workspace_bytes(*_i32(total_q, num_qo_heads),
+                                                           ctypes.byref(n)))
+    return int(n.value)
+
+
+def _given_or_new(t, what, shape, dtype, dev, stream):
+    if t is None:
+        return _new(shape, dtype, dev, stream)
+    _need(t, what, dtype, dev, tuple(shape))
+    return t
+
+
+def _workspace(t, need, dev, stream):
+    if t is None:
+        return _new((max(need, 256),), torch.uint8, dev, stream, kept=False)
+    if not torch.is_tensor(t) or t.device != dev or not t.is_contiguous():
+        raise SinkAttnError(INVALID_ARG, "workspace must be contiguous and on %s" % dev)
+    return t
+
+
+def sinkattn_prefill_backward(dout, q, k, v, out, lse, sinks, cu_seqlens_q, cu_seqlens_k,
+                              max_seqlen_q, max_seqlen_k, num_kv_heads, sm_scale=None, causal=True,
+                              window=0, dlse=None, dq=None, dk=None, dv=None, dsinks=None,
+                              workspace=None, stream=None):
+    """Gradients of sinkattn_prefill: dout bf16 [total_q, Hq, d] is that of
+    out, dlse fp32 [total_q, Hq] (or None) that of lse; out and lse are what
+    the forward call returned for the same q, k, v, sinks. Returns (dq, dk, dv,
+    dsinks), bf16 in the inputs' layouts and fp32 [Hq] (None without sinks)."""
+    dev = _need_cuda(q, "q")
+    bf16, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    _need(q, "q", bf16, dev, 3)
+    total_q, Hq, d = q.shape
+    _need(k, "k", bf16, dev, 2)
+    Hkv, = _i32(num_kv_heads)
+    if Hkv < 1 or k.shape[1] != d or k.shape[0] % Hkv:
+        raise SinkAttnError(INVALID_ARG, "k must have shape [%d * total_k, %d], not %s" % (
+            Hkv, d, tuple(k.shape)))
+    total_k = k.shape[0] // Hkv
+    _need(v, "v", bf16, dev, k.shape)
+    _need(dout, "dout", bf16, dev, q.shape)
+    _need(out, "out", bf16, dev, q.shape)
+    _need(lse, "lse", f32, dev, (total_q, Hq))
+    if sinks is not None:
+        _need(sinks, "sinks", f32, dev, (Hq,))
+    elif dsinks is not None:
+        raise SinkAttnError(INVALID_ARG, "dsinks without sinks")
+    if dlse is not None:
+        _need(dlse, "dlse", f32, dev, (total_q, Hq))
+    _need(cu_seqlens_q, "cu_seqlens_q", i32, dev, 1)
+    _need(cu_seqlens_k, "cu_seqlens_k", i32, dev, cu_seqlens_q.shape)
+    batch = cu_seqlens_q.shape[0] - 1
+    if batch < 0:
+        raise SinkAttnError(INVALID_ARG, "cu_seqlens_q must have an entry at least")
+    max_seqlen_q, max_seqlen_k = _i32(max_seqlen_q, max_seqlen_k)
+    dq = _given_or_new(dq, "dq", q.shape, bf16, dev, stream)
+    dk = _given_or_new(dk, "dk", k.shape, bf16, dev, stream)
+    dv = _given_or_new(dv, "dv", k.shape, bf16, dev, stream)
+    if sinks is not None:
+        dsinks = _given_or_new(dsinks, "dsinks", (Hq,), f32, dev, stream)
+    need = sinkattn_prefill_backward_workspace_bytes(total_q, Hq)
+    workspace = _workspace(workspace, need, dev, stream)
+    _launch(dev, lib().sinkattn_prefill_backward, dout.data_ptr(), q.data_ptr(), k.data_ptr(),
+            v.data_ptr(), out.data_ptr(), lse.data_ptr(),
+            None if sinks is None else sinks.data_ptr(),
+            None if dlse is None else dlse.data_ptr(), cu_seqlens_q.data_ptr(),
+            cu_seqlens_k.data_ptr(), batch, total_q, total_k, max_seqlen_q, max_seqlen_k, Hq, Hkv,
+            d, _scale(sm_scale, d), 1 if causal else 0, min(int(window), 2 ** 31 - 1),
+            dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+            None if dsinks is None else dsinks.data_ptr(), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), _stream_of(dev, stream))
+    return dq, dk, dv, dsinks
+
+
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+def sinkattn_rope_frequencies(rotary_dim, base=10000.0, scaling="none", factor=1.0,
+                              original_len=0, beta_fast=32.0, beta_slow=1.0):
+    """(angles per position of the rotary_dim / 2 pairs, attention factor) of
+    plain, "linear", "ntk" or "yarn" scaled rotary positions; host arithmetic only."""
+    if isinstance(scaling, str) and scaling not in ROPE_SCALINGS:
+        raise SinkAttnError(INVALID_ARG, "scaling must be one of %s" % ", ".join(ROPE_SCALINGS))
+    code = ROPE_SCALINGS[scaling] if isinstance(scaling, str) else scaling
+    rotary_dim, original_len, code = _i32(rotary_dim, original_len, code)
+    inv = (ctypes.c_double * max(rotary_dim // 2, 1))()
+    att = ctypes.c_float(0.0)
+    _check(lib().sinkattn_rope_frequencies(rotary_dim, float(base), code, float(factor),
+                                           original_len, float(beta_fast), float(beta_slow), inv,
+                                           ctypes.addressof(att)))
+    return list(inv)[:rotary_dim // 2], float(att.value)
+
+
+def sinkattn_rope_turns(inv_freq):
+    """Frequencies as the kernels take them: turns per position in units of
+    2^-64, as a list of integers in [0, 2^64)."""
+    n = len(inv_freq)
+    freq = (ctypes.c_double * max(n, 1))(*[float(x) for x in inv_freq])
+    turns = (ctypes.c_uint64 * max(n, 1))()
+    _check(lib().sinkattn_rope_turns(freq, n, turns))
+    return list(turns)[:n]
+
+
+class Rope:
+    """Rotary positions of a head's first ``rotary_dim`` elements, in the half
+    layout (pairs (i, i + rotary_dim / 2)) or the ``interleaved`` one (pairs
+    (2i, 2i + 1)). The frequencies are those of sinkattn_rope_frequencies, or
+    ``inv_freq`` (a sequence of rotary_dim / 2 angles per position) with
+    ``attention_factor``, which overrides the scaling's own where given. They
+    live on ``device``, so make the object once and keep it."""
+    __slots__ = ("_turns", "rotary_dim", "interleaved", "attention_factor", "inv_freq", "device")
+
+    def __init__(self, rotary_dim, base=10000.0, interleaved=False, scaling="none", factor=1.0,
+                 original_len=0, beta_fast=32.0, beta_slow=1.0, inv_freq=None,
+                 attention_factor=None, device="cuda"):
+        self.rotary_dim, = _i32(rotary_dim)
+        if inv_freq is None:
+            inv_freq, own = sinkattn_rope_frequencies(rotary_dim, base, scaling, factor,
+                                                      original_len, beta_fast, beta_slow)
+        else:
+            inv_freq, own = [float(x) for x in inv_freq], 1.0
+            if self.rotary_dim < 0 or 2 * len(inv_freq) != self.rotary_dim:
+                raise SinkAttnError(INVALID_ARG, "inv_freq must have rotary_dim / 2 entries")
+        self.attention_factor = float(own if attention_factor is None else attention_factor)
+        if not math.isfinite(self.attention_factor):
+            raise SinkAttnError(INVALID_ARG, "attention_factor must be finite")
+        self.interleaved = bool(interleaved)
+        self.inv_freq = tuple(inv_freq)
+        # (int64 holds the unsigned words)
+        words = [t - 2 ** 64 if t >= 2 ** 63 else t for t in sinkattn_rope_turns(inv_freq)]
+        self._turns = torch.tensor(words or [0], dtype=torch.int64).to(device)
+        self.device = _need_cuda(self._turns, "device")
+
+    turns = property(lambda self: self._turns)
+
+
+def _rope_rows(t, what, dev, heads, d, tokens):
+    """(address, token stride) of rows [tokens, heads, d] bf16."""
+    if (not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or t.device != dev
+            or t.dim() != 3 or t.shape != (tokens, heads, d)):
+        raise SinkAttnError(INVALID_ARG, "%s must be bfloat16 %s on %s" % (
+            what, (tokens, heads, d), dev))
+    at, head, el = t.stride()
+    if tokens > 0 and (el != 1 or (head != d and heads > 1)):
+        raise SinkAttnError(INVALID_ARG, "the rows of a token of %s must be contiguous" % what)
+    return t.data_ptr(), at if tokens > 1 else heads * d
+
+
+def _rope_common(q, k, v, rope, q_weight, k_weight, positions):
+    """(device, tokens, Hq, Hkv, d, addresses and strides, positions, rotation arguments without eps)."""
+    dev = _need_cuda(q, "q")
+    if q.dim() != 3 or not torch.is_tensor(k) or k.dim() != 3:
+        raise SinkAttnError(INVALID_ARG, "q and k must have 3 dimensions")
+    tokens, Hq, d = q.shape
+    Hkv = k.shape[1]
+    rows = [_rope_rows(t, what, dev, heads, d, tokens)
+            for t, what, heads in ((q, "q", Hq), (k, "k", Hkv), (v, "v", Hkv))]
+    return dev, tokens, Hq, Hkv, d, rows, *_rope_args(rope, q_weight, k_weight, positions, dev, d,
+                                                      tokens)
+
+
+def _rope_args(rope, q_weight, k_weight, positions, dev, d, tokens):
+    if not isinstance(rope, Rope) or rope.device != dev:
+        raise SinkAttnError(INVALID_ARG, "rope must be a Rope on %s" % dev)
+    qw, kw = [None if t is None else _need(t, what, torch.float32, dev, (d,))
+              for t, what in ((q_weight, "q_weight"), (k_weight, "k_weight"))]
+    pos = None if positions is None else _need(positions, "positions", torch.int32, dev, (tokens,))
+    return pos, (rope._turns.data_ptr(), rope.rotary_dim, 1 if rope.interleaved else 0,
+                 rope.attention_factor, qw, kw)
+
+
+def sinkattn_rope_qkv(q, k, v, cu_seqlens, rope, q_weight=None, k_weight=None, eps=1e-6,
+                      positions=None, q_out=None, k_out=None, v_out=None, stream=None):
+    """From a fused projection's rows to what sinkattn_prefill reads: q bf16
+    [tokens, Hq, d], k and v [tokens, Hkv, d] (heads of a token contiguous, any
+    token stride that is a multiple of 8) are normed per head (q_weight,
+    k_weight fp32 [d]; None: not), q and k rotated by ``rope`` at ``positions``
+    (int32 [tokens]; None: the index in the sequence). Returns (q [tokens, Hq,
+    d], k, v ragged HND [Hkv * tokens, d])."""
+    dev, tokens, Hq, Hkv, d, rows, pos, args = _rope_common(q, k, v, rope, q_weight, k_weight,
+                                                            positions)
+    cu = _need(cu_seqlens, "cu_seqlens", torch.int32, dev, 1)
+    if cu_seqlens.shape[0] < 1:
+        raise SinkAttnError(INVALID_ARG, "cu_seqlens must have an entry at least")
+    bf16 = torch.bfloat16
+    q_out = _given_or_new(q_out, "q_out", (tokens, Hq, d), bf16, dev, stream)
+    k_out = _given_or_new(k_out, "k_out", (Hkv * tokens, d), bf16, dev, stream)
+    v_out = _given_or_new(v_out, "v_out", (Hkv * tokens, d), bf16, dev, stream)
+    _launch(dev, lib().sinkattn_rope_qkv, *[r[0] for r in rows], *[r[1] for r in rows], cu, pos,
+            cu_seqlens.shape[0] - 1, tokens, Hq, Hkv, d, *args, float(eps), q_out.data_ptr(),
+            k_out.data_ptr(), v_out.data_ptr(), _stream_of(dev, stream))
+    return q_out, k_out, v_out
+
+
+def sinkattn_rope_qkv_backward_workspace_bytes(tokens, head_dim) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().sinkattn_rope_qkv_backward_workspace_bytes(*_i32(tokens, head_dim),
+                                                            ctypes.byref(n)))
+    return int(n.value)
+
+
+def sinkattn_rope_qkv_backward(dq, dk, dv, cu_seqlens, rope, q=None, k=None, q_weight=None,
+                               k_weight=None, eps=1e-6, positions=None, dq_in=None, dk_in=None,
+                               dv_in=None, dq_weight=None, dk_weight=None, workspace=None,
+                               stream=None):
+    """Gradients of sinkattn_rope_qkv from those of its outputs: dq bf16
+    [tokens, Hq, d], dk and dv ragged HND. q and k, its inputs, are read where
+    they are normed. Returns (dq_in, dk_in, dv_in, dq_weight, dk_weight); by default the
+    first three are slices of one [tokens, (Hq + 2 Hkv) * d] gradient of the
+    projection's output."""
+    dev = _need_cuda(dq, "dq")
+    bf16, f32 = torch.bfloat16, torch.float32
+    _need(dq, "dq", bf16, dev, 3)
+    tokens, Hq, d = dq.shape
+    _need(dk, "dk", bf16, dev, 2)
+    if dk.shape[1] != d or (tokens > 0 and (dk.shape[0] % tokens or dk.shape[0] == 0)):
+        raise SinkAttnError(INVALID_ARG, "dk must have shape [Hkv * %d, %d], not %s" % (
+            tokens, d, tuple(dk.shape)))
+    _need(dv, "dv", bf16, dev, dk.shape)
+    if tokens > 0:
+        Hkv = dk.shape[0] // tokens
+    else:   # (the layout of no rows does not tell)
+        Hkv = next((t.shape[1] for t in (k, dk_in, dv_in) if torch.is_tensor(t) and t.dim() == 3), 1)
+    cu = _need(cu_seqlens, "cu_seqlens", torch.int32, dev, 1)
+    if cu_seqlens.shape[0] < 1:
+        raise SinkAttnError(INVALID_ARG, "cu_seqlens must have an entry at least")
+    pos, args = _rope_args(rope, q_weight, k_weight, positions, dev, d, tokens)
+    ins = [(None, 0), (None, 0)]
+    if q_weight is not None:
+        ins[0] = _rope_rows(q, "q", dev, Hq, d, tokens)
+    if k_weight is not None:
+        ins[1] = _rope_rows(k, "k", dev, Hkv, d, tokens)
+    if dq_in is None or dk_in is None or dv_in is None:
+        rows = _new((tokens, Hq + 2 * Hkv, d), bf16, dev, stream)
+        dq_in = rows[:, :Hq] if dq_in is None else dq_in
+        dk_in = rows[:, Hq:Hq + Hkv] if dk_in is None else dk_in
+        dv_in = rows[:, Hq + Hkv:] if dv_in is None else dv_in
+    outs = [_rope_rows(t, what, dev, heads, d, tokens) for t, what, heads in (
+        (dq_in, "dq_in", Hq), (dk_in, "dk_in", Hkv), (dv_in, "dv_in", Hkv))]
+    if q_weight is not None:
+        dq_weight = _given_or_new(dq_weight, "dq_weight", (d,), f32, dev, stream)
+    elif dq_weight is not None:
+        raise SinkAttnError(INVALID_ARG, "dq_weight without q_weight")
+    if k_weight is not None:
+        dk_weight = _given_or_new(dk_weight, "dk_weight", (d,), f32, dev, stream)
+    elif dk_weight is not None:
+        raise SinkAttnError(INVALID_ARG, "dk_weight without k_weight")
+    ws_p, ws_n = None, 0
+    if q_weight is not None or k_weight is not None:
+        need = sinkattn_rope_qkv_backward_workspace_bytes(tokens, d)
+        workspace = _workspace(workspace, need, dev, stream)
+        ws_p, ws_n = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _launch(dev, lib().sinkattn_rope_qkv_backward, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+            ins[0][0], ins[1][0], ins[0][1], ins[1][1], cu, pos, cu_seqlens.shape[0] - 1, tokens,
+            Hq, Hkv, d, *args, float(eps), *[o[0] for o in outs], *[o[1] for o in outs],
+            None if dq_weight is None else dq_weight.data_ptr(),
+            None if dk_weight is None else dk_weight.data_ptr(), ws_p, ws_n,
+            _stream_of(dev, stream))
+    return dq_in, dk_in, dv_in, dq_weight, dk_weight
+
+
+def _rope_append(entry, pool_dtype, scales, q, k, v, positions, slots, rope, k_pages, v_pages,
+                 q_weight, k_weight, eps, q_out, stream):
+    dev, tokens, Hq, Hkv, d, rows, pos, args = _rope_common(q, k, v, rope, q_weight, k_weight,
+                                                            positions)
+    if pos is None:
+        raise SinkAttnError(INVALID_ARG, "positions must be a tensor")
+    s_p = _need(slots, "slots", torch.int32, dev, (tokens,))
+    kp_p = _need(k_pages, "k_pages", pool_dtype, dev, 4)
+    num_pages, pool_heads, page_size, pool_d = k_pages.shape
+    if pool_heads != Hkv or pool_d != d:
+        raise SinkAttnError(INVALID_ARG, "k has %d heads of %d, the pools %d of %d" % (
+            Hkv, d, pool_heads, pool_d))
+    vp_p = _need(v_pages, "v_pages", pool_dtype, dev, k_pages.shape)
+    scale_p = [_need(t, what, torch.float32, dev, (Hkv,))
+               for t, what in zip(scales, ("k_scale", "v_scale"))]
+    q_out = _given_or_new(q_out, "q_out", (tokens, Hq, d), torch.bfloat16, dev, stream)
+    _launch(dev, entry, *[r[0] for r in rows], *[r[1] for r in rows], pos, s_p, tokens, Hq, Hkv, d,
+            *args, float(eps), *scale_p, q_out.data_ptr(), kp_p, vp_p, num_pages, page_size,
+            _stream_of(dev, stream))
+    return q_out
+
+
+def sinkattn_rope_append_paged(q, k, v, positions, slots, rope, k_pages, v_pages, q_weight=None,
+                               k_weight=None, eps=1e-6, q_out=None, stream=None):
+    """sinkattn_append_paged with the norm and rotation of sinkattn_rope_qkv on
+    the way: q, k, v are a fused projection's rows, positions and slots int32
+    [tokens]. k and v go to the pools; returns the rotated q, [tokens, Hq, d]."""
+    return _rope_append(lib().sinkattn_rope_append_paged, torch.bfloat16, (), q, k, v, positions,
+                        slots, rope, k_pages, v_pages, q_weight, k_weight, eps, q_out, stream)
+
+
+def sinkattn_rope_append_paged_fp8(q, k, v, positions, slots, rope, k_scale, v_scale, k_pages,
+                                   v_pages, q_weight=None, k_weight=None, eps=1e-6, q_out=None,
+                                   stream=None):
+    """sinkattn_rope_append_paged into pools of e4m3 codes (uint8): the code
+    nearest to the rotated key / scale[head] (ties to even, saturating at 448)."""
+    return _rope_append(lib().sinkattn_rope_append_paged_fp8, torch.uint8, (k_scale, v_scale), q, k,
+                        v, positions, slots, rope, k_pages, v_pages, q_weight, k_weight, eps,
+                        q_out, stream)
 
 
 PREFILL_KERNELS = {"auto": 0, "one_block": 1, "persistent": 2}

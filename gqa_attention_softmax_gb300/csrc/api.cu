@@ -290,6 +290,101 @@ int sinkattn_prefill_paged(const void* q, const void* k_pages, const void* v_pag
 
 namespace {
 
+// Workspace of the backward pass: delta, then the blocks' sums of the sinks' gradients.
+size_t back_delta_bytes(int32_t total_q, int32_t Hq) {
+  return (static_cast<size_t>(total_q) * Hq * 4 + 255) & ~static_cast<size_t>(255);
+}
+
+}  // namespace
+
+extern "C" {
+
+int sinkattn_prefill_backward_workspace_bytes(int32_t total_q, int32_t num_qo_heads,
+                                              size_t* bytes) {
+  g_last_error[0] = '\0';
+  if (!bytes) return fail(SINKATTN_INVALID_ARG, "bytes must be non-null");
+  if (total_q < 0 || num_qo_heads <= 0) return fail(SINKATTN_INVALID_ARG, "bad sizes");
+  if (static_cast<int64_t>(total_q) * num_qo_heads >= (int64_t{1} << 31))
+    return fail(SINKATTN_UNSUPPORTED, "problem exceeds 2^31 rows");
+  *bytes = back_delta_bytes(total_q, num_qo_heads) +
+           static_cast<size_t>(back_blocks(total_q, num_qo_heads)) * num_qo_heads * 4;
+  return SINKATTN_OK;
+}
+
+int sinkattn_prefill_backward(const void* dout, const void* q, const void* k, const void* v,
+                              const void* out, const float* lse, const float* sinks,
+                              const float* dlse, const int32_t* cu_seqlens_q,
+                              const int32_t* cu_seqlens_k, int32_t batch, int32_t total_q,
+                              int32_t total_k, int32_t max_seqlen_q, int32_t max_seqlen_k,
+                              int32_t num_qo_heads, int32_t num_kv_heads, int32_t head_dim,
+                              float sm_scale, int32_t causal, int32_t window, void* dq, void* dk,
+                              void* dv, float* dsinks, void* workspace, size_t workspace_bytes,
+                              void* stream) {
+  g_last_error[0] = '\0';
+  if (batch < 0 || total_q < 0 || total_k < 0 || max_seqlen_q < 0 || max_seqlen_k < 0)
+    return fail(SINKATTN_INVALID_ARG, "sizes must be non-negative");
+  const bool none = batch == 0 || total_k == 0;   // (each sequence has Lq <= Lk: no queries either)
+  // an empty tensor has no address to check
+  static const int unused __attribute__((aligned(16))) = 0;
+  const bool no_q = none || total_q == 0;
+  int rc = check_common(no_q ? &unused : q, none ? &unused : k, none ? &unused : v, num_qo_heads,
+                        num_kv_heads, head_dim, sm_scale, causal, window);
+  if (rc) return rc;
+  if (batch > 65535) return fail(SINKATTN_UNSUPPORTED, "batch %d exceeds 65535", batch);
+  if (num_kv_heads > 65535)
+    return fail(SINKATTN_UNSUPPORTED, "num_kv_heads %d exceeds 65535", num_kv_heads);
+  if (num_qo_heads / num_kv_heads > 128)
+    return fail(SINKATTN_UNSUPPORTED, "GQA group of %d heads exceeds 128",
+                num_qo_heads / num_kv_heads);
+  if (max_seqlen_q > max_seqlen_k)
+    return fail(SINKATTN_INVALID_ARG, "max_seqlen_q (%d) exceeds max_seqlen_k (%d)", max_seqlen_q,
+                max_seqlen_k);
+  if (static_cast<int64_t>(num_kv_heads) * total_k >= (int64_t{1} << 31) ||
+      static_cast<int64_t>(total_q) * num_qo_heads >= (int64_t{1} << 31))
+    return fail(SINKATTN_UNSUPPORTED, "problem exceeds 2^31 rows");
+  if ((sinks == nullptr) != (dsinks == nullptr))
+    return fail(SINKATTN_INVALID_ARG, "sinks and dsinks must be both given or both NULL");
+  if ((reinterpret_cast<uintptr_t>(sinks) | reinterpret_cast<uintptr_t>(dsinks) |
+       reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(dlse)) & 3u)
+    return fail(SINKATTN_INVALID_ARG, "lse, dlse, sinks and dsinks must be 4-byte aligned");
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (none) {
+    if (dsinks && cudaMemsetAsync(dsinks, 0, sizeof(float) * num_qo_heads, s) != cudaSuccess)
+      return fail(SINKATTN_CUDA_ERROR, "cudaMemsetAsync: %s", cudaGetErrorString(cudaGetLastError()));
+    return SINKATTN_OK;
+  }
+  if (!dk || !dv || !aligned16(dk) || !aligned16(dv))
+    return fail(SINKATTN_INVALID_ARG, "dk and dv must be non-null and 16-byte aligned");
+  if (!cu_seqlens_q || !cu_seqlens_k)
+    return fail(SINKATTN_INVALID_ARG, "cu_seqlens must be non-null");
+  if (!no_q && (!dout || !out || !dq || !aligned16(dout) || !aligned16(out) || !aligned16(dq)))
+    return fail(SINKATTN_INVALID_ARG, "dout, out and dq must be non-null and 16-byte aligned");
+  if (!no_q && !lse) return fail(SINKATTN_INVALID_ARG, "lse must be non-null");
+  size_t need = 0;
+  if ((rc = sinkattn_prefill_backward_workspace_bytes(total_q, num_qo_heads, &need))) return rc;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return fail(SINKATTN_INVALID_ARG, "workspace must be non-null and 256-byte aligned");
+  if (workspace_bytes < need)
+    return fail(SINKATTN_INVALID_ARG, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
+  BackArgs a{};
+  a.dout = dout; a.q = q; a.k = k; a.v = v; a.out = out;
+  a.lse = lse; a.sinks = sinks; a.dlse = dlse;
+  a.cu_q = cu_seqlens_q; a.cu_k = cu_seqlens_k;
+  a.batch = batch; a.total_q = total_q; a.total_k = total_k;
+  a.max_q = max_seqlen_q; a.max_kv = max_seqlen_k;
+  a.Hq = num_qo_heads; a.Hkv = num_kv_heads; a.d = head_dim;
+  a.sm_scale = sm_scale; a.causal = causal; a.window = window;
+  a.dq = dq; a.dk = dk; a.dv = dv; a.dsinks = dsinks;
+  a.delta = static_cast<float*>(workspace);
+  a.sink_part = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                         back_delta_bytes(total_q, num_qo_heads));
+  return launch_prefill_back(a, s);
+}
+
+}  // extern "C"
+
+namespace {
+
 // Validation shared by the split-KV decode entry points; fills `a` (without
 // the output pointers). Returns SINKATTN_OK or the failing status.
 int decode_args(const void* q, const void* k, const void* v, const int32_t* kv_indptr,
@@ -924,13 +1019,13 @@ int sinkattn_debug_status(void* stream, int* status) {
   g_last_error[0] = '\0';
   if (!status) return fail(SINKATTN_INVALID_ARG, "status must be non-null");
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  int a = 0, m = 0, t = 0, dt = 0, sh = 0, pg = 0, px = 0;
+  int a = 0, m = 0, t = 0, dt = 0, sh = 0, pg = 0, px = 0, ro = 0, pb = 0;
   if (read_status_attn_mma(s, &a) || read_status_merge(s, &m) || read_status_prefill_tc(s, &t) ||
       read_status_decode_tc(s, &dt) || read_status_shared(s, &sh) || read_status_pages(s, &pg) ||
-      read_status_prefix_tc(s, &px))
+      read_status_prefix_tc(s, &px) || read_status_rope(s, &ro) || read_status_prefill_back(s, &pb))
     return fail(SINKATTN_CUDA_ERROR, "reading the device status failed: %s",
                 cudaGetErrorString(cudaGetLastError()));
-  *status = a ? a : (dt ? dt : (t ? t : (m ? m : (px ? px : (sh ? sh : pg)))));
+  *status = a ? a : (dt ? dt : (t ? t : (m ? m : (px ? px : (sh ? sh : (pg ? pg : (pb ? pb : ro)))))));
   return SINKATTN_OK;
 }
 

@@ -207,7 +207,31 @@ int launch_prefix_tc(const AttnArgs& a, const SharedPlan& plan, cudaStream_t str
 int prefix_block_tokens(int G);            // query tokens of one row block
 int prefix_tile_keys(int d, bool fp8);     // keys of one K/V tile
 
+// The backward pass of the prefill.
+struct BackArgs {
+  const void *dout, *q, *k, *v, *out;   // bf16; q, dout, out [total_q, Hq, d], k, v ragged HND
+  const float *lse, *sinks, *dlse;      // sinks, dlse: or nullptr
+  const int32_t *cu_q, *cu_k;
+  int32_t batch, total_q, total_k, max_q, max_kv, Hq, Hkv, d;
+  float sm_scale;
+  int32_t causal, window;
+  void *dq, *dk, *dv;
+  float* dsinks;                        // nullptr where sinks is
+  // workspace
+  float* delta;                         // [total_q, Hq]
+  float* sink_part;                     // [back_blocks(), Hq]
+};
+// Rows of sink_part: blocks of query tokens of the pass that computes delta.
+int back_block_tokens(int32_t Hq);
+inline int64_t back_blocks(int32_t total_q, int32_t Hq) {
+  const int64_t per = back_block_tokens(Hq);
+  return (total_q + per - 1) / per;
+}
+int launch_prefill_back(const BackArgs& a, cudaStream_t stream);
+
 // Reads and clears the device status word of one translation unit.
+int read_status_rope(cudaStream_t s, int* status);
+int read_status_prefill_back(cudaStream_t s, int* status);
 int read_status_pages(cudaStream_t s, int* status);
 int read_status_shared(cudaStream_t s, int* status);
 int read_status_prefix_tc(cudaStream_t s, int* status);

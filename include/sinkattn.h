@@ -551,6 +551,140 @@ SINKATTN_API int sinkattn_pages_lists(const int32_t* table, int32_t num_pages, i
                                       int32_t* page_indptr, int32_t* page_indices,
                                       int32_t capacity, void* stream);
 
+/*
+ * Gradients of sinkattn_prefill. With P_ij = e^{l_ij - lse_i} over the visible
+ * keys, delta_i = dout_i . out_i - dlse_i and dS_ij = P_ij (dout_i . v_j - delta_i):
+ *   dq_i = sm_scale sum_j dS_ij k_j        dk_j = sm_scale sum_i dS_ij q_i
+ *   dv_j = sum_i P_ij dout_i               dsinks_h = -sum_i e^{s_h - lse_i} delta_i
+ * with the sums over i also over the query heads of the KV head's group. The
+ * derivation is that of the softmax with the sink as one more column whose
+ * value row is zero; the pages hold no training.
+ *   dout, out, q, dq: bf16 [total_q, Hq, d]; k, v, dk, dv: bf16 ragged HND,
+ *     [Hkv * total_k, d]; lse fp32 [total_q, Hq]; sinks, dsinks fp32 [Hq] or
+ *     NULL, both or neither; dlse fp32 [total_q, Hq] or NULL: the gradient of lse.
+ *     out and lse are what sinkattn_prefill gave for these q, k, v and sinks.
+ *   cu_seqlens_*, batch, max_seqlen_*, the masks: as there; total_q =
+ *     cu_seqlens_q[batch], total_k = cu_seqlens_k[batch] (host).
+ *   workspace: sinkattn_prefill_backward_workspace_bytes() bytes, 256-byte
+ *     aligned, device memory; contents on entry do not matter. Two calls that
+ *     may overlap need two workspaces.
+ * Every element of dq, dk, dv and dsinks up to the last sequence's end is
+ * written (zeros where nothing is visible); rows behind it stay as they are.
+ * Sums are fp32; P and dS are rounded to bf16 for the products. Results do not
+ * depend on timing. A sequence whose inputs hold NaN or infinities gets NaN; the
+ * other sequences do not. Lengths that contradict the host sizes record
+ * SINKATTN_BAD_LENGTHS and leave that sequence's gradients undefined.
+ */
+SINKATTN_API int sinkattn_prefill_backward(
+    const void* dout, const void* q, const void* k, const void* v, const void* out,
+    const float* lse, const float* sinks, const float* dlse, const int32_t* cu_seqlens_q,
+    const int32_t* cu_seqlens_k, int32_t batch, int32_t total_q, int32_t total_k,
+    int32_t max_seqlen_q, int32_t max_seqlen_k, int32_t num_qo_heads, int32_t num_kv_heads,
+    int32_t head_dim, float sm_scale, int32_t causal, int32_t window, void* dq, void* dk, void* dv,
+    float* dsinks, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of the backward pass for these sizes (host only, no CUDA call). */
+SINKATTN_API int sinkattn_prefill_backward_workspace_bytes(int32_t total_q, int32_t num_qo_heads,
+                                                           size_t* bytes);
+
+/*
+ * Rotary positions. A head's first rotary_dim elements are cut into pairs, in
+ * the interleaved layout (2i, 2i + 1), else (i, i + rotary_dim / 2); pair i is
+ * turned by the angle position * f_i and scaled by attention_factor; the other
+ * elements stay as they are. The frequencies are passed as
+ *   turns: uint64 [rotary_dim / 2] (device), f_i / (2 pi) modulo 1 in units of 2^-64,
+ * so that an angle is exact at any int32 position (sinkattn_rope_turns makes
+ * them from f_i in host memory).
+ * sinkattn_rope_frequencies (host only) gives f_i = base^(-2i / rotary_dim) and
+ * the factor of cosine and sine, scaled for contexts beyond the trained ones:
+ *   SINKATTN_ROPE_PLAIN: as they are, attention_factor 1;
+ *   SINKATTN_ROPE_LINEAR: f_i / factor;
+ *   SINKATTN_ROPE_NTK: base times factor^(r / (r - 2)), r = rotary_dim, which divides the
+ *     lowest frequency by factor;
+ *   SINKATTN_ROPE_YARN ("YaRN: Efficient Context Window Extension of Large
+ *     Language Models", Peng et al., 2023): pairs that turn more than beta_fast
+ *     times within original_len positions keep f_i, those that turn less than
+ *     beta_slow times get f_i / factor, with a linear ramp over i between, and
+ *     attention_factor = 0.1 ln(factor) + 1.
+ */
+#define SINKATTN_ROPE_PLAIN 0
+#define SINKATTN_ROPE_LINEAR 1
+#define SINKATTN_ROPE_NTK 2
+#define SINKATTN_ROPE_YARN 3
+SINKATTN_API int sinkattn_rope_frequencies(int32_t rotary_dim, double base, int32_t scaling,
+                                           double factor, int32_t original_len, double beta_fast,
+                                           double beta_slow, double* inv_freq,
+                                           float* attention_factor);
+SINKATTN_API int sinkattn_rope_turns(const double* inv_freq, int32_t n, uint64_t* turns);
+
+/*
+ * From a fused projection's rows to what sinkattn_prefill reads: per-head norm
+ * and rotation of queries and keys, and the ragged HND layout, in one pass.
+ *   q [tokens, Hq, d], k, v [tokens, Hkv, d] bf16 (device), the heads of a
+ *     token contiguous, token i at element i * q_stride (k_stride, v_stride):
+ *     multiples of 8, so slices of one projection's output need no copy;
+ *   cu_seqlens int32 [batch + 1] (device), tokens = cu_seqlens[batch] (rows
+ *     behind it are neither read nor written);
+ *   positions int32 [tokens] (device), or NULL: the index in the sequence;
+ *   q_weight, k_weight fp32 [d] (device) or NULL: y = w * x * rsqrt(mean x^2 +
+ *     eps) over the head's d elements before the rotation; NULL: no norm;
+ *   q_out bf16 [tokens, Hq, d]; k_out, v_out bf16 ragged HND [Hkv * tokens, d].
+ * Arithmetic is fp32, each output is rounded once. cu_seqlens that leave
+ * [0, tokens] record SINKATTN_BAD_LENGTHS; the tokens concerned are left out.
+ */
+SINKATTN_API int sinkattn_rope_qkv(const void* q, const void* k, const void* v, int64_t q_stride,
+                                   int64_t k_stride, int64_t v_stride, const int32_t* cu_seqlens,
+                                   const int32_t* positions, int32_t batch, int32_t tokens,
+                                   int32_t num_qo_heads, int32_t num_kv_heads, int32_t head_dim,
+                                   const uint64_t* turns, int32_t rotary_dim, int32_t interleaved,
+                                   float attention_factor, const float* q_weight,
+                                   const float* k_weight, float eps, void* q_out, void* k_out,
+                                   void* v_out, void* stream);
+
+/*
+ * Gradients of sinkattn_rope_qkv. dq bf16 [tokens, Hq, d] and dk, dv bf16
+ * ragged HND are those of its outputs; q and k its inputs, read only where there is
+ * a norm (NULL otherwise). dq_in, dk_in, dv_in with their token strides get
+ * the gradients of q, k, v (rows behind the last sequence stay as they are);
+ * dq_weight, dk_weight fp32 [d] those of the weights, summed in an order that
+ * does not depend on timing. workspace: sinkattn_rope_qkv_backward_workspace_bytes()
+ * bytes, 256-byte aligned, needed where there is a norm. With no tokens the weights'
+ * gradients are zero.
+ */
+SINKATTN_API int sinkattn_rope_qkv_backward(
+    const void* dq, const void* dk, const void* dv, const void* q, const void* k, int64_t q_stride,
+    int64_t k_stride, const int32_t* cu_seqlens, const int32_t* positions, int32_t batch,
+    int32_t tokens, int32_t num_qo_heads, int32_t num_kv_heads, int32_t head_dim,
+    const uint64_t* turns, int32_t rotary_dim, int32_t interleaved, float attention_factor,
+    const float* q_weight, const float* k_weight, float eps, void* dq_in, void* dk_in, void* dv_in,
+    int64_t dq_stride, int64_t dk_stride, int64_t dv_stride, float* dq_weight, float* dk_weight,
+    void* workspace, size_t workspace_bytes, void* stream);
+SINKATTN_API int sinkattn_rope_qkv_backward_workspace_bytes(int32_t tokens, int32_t head_dim,
+                                                            size_t* bytes);
+
+/*
+ * sinkattn_append_paged with the norm and the rotation of sinkattn_rope_qkv on
+ * the way: q goes to q_out [tokens, Hq, d], k and v to their slots in the
+ * pools. positions int32 [tokens] (device) as the rotation takes them; slots,
+ * pools, scales and padding (a slot outside the pool: k and v are left out, q
+ * is written) as there. The _fp8 form rounds the fp32 quotient of the rotated
+ * key, not rounded to bf16 before, and its scale.
+ */
+SINKATTN_API int sinkattn_rope_append_paged(
+    const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
+    int64_t v_stride, const int32_t* positions, const int32_t* slots, int32_t tokens,
+    int32_t num_qo_heads, int32_t num_kv_heads, int32_t head_dim, const uint64_t* turns,
+    int32_t rotary_dim, int32_t interleaved, float attention_factor, const float* q_weight,
+    const float* k_weight, float eps, void* q_out, void* k_pages, void* v_pages, int32_t num_pages,
+    int32_t page_size, void* stream);
+SINKATTN_API int sinkattn_rope_append_paged_fp8(
+    const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
+    int64_t v_stride, const int32_t* positions, const int32_t* slots, int32_t tokens,
+    int32_t num_qo_heads, int32_t num_kv_heads, int32_t head_dim, const uint64_t* turns,
+    int32_t rotary_dim, int32_t interleaved, float attention_factor, const float* q_weight,
+    const float* k_weight, float eps, const float* k_scale, const float* v_scale, void* q_out,
+    void* k_pages, void* v_pages, int32_t num_pages, int32_t page_size, void* stream);
+
 /* Human-readable name of a status code (static string). */
 SINKATTN_API const char* sinkattn_status_string(int status);
 
