@@ -1036,7 +1036,8 @@ int sinkattn_debug_set_hooks(long long wait_limit_cycles, int skip_tile) {
       set_hooks_prefill_tc(wait_limit_cycles, skip_tile) ||
       set_hooks_decode_tc(wait_limit_cycles, skip_tile) ||
       set_hooks_prefix_tc(wait_limit_cycles, skip_tile) ||
-      set_hooks_pages(wait_limit_cycles, skip_tile))
+      set_hooks_pages(wait_limit_cycles, skip_tile) ||
+      set_hooks_prefill_back(wait_limit_cycles, skip_tile))
     return fail(SINKATTN_CUDA_ERROR, "setting the test hooks failed: %s",
                 cudaGetErrorString(cudaGetLastError()));
   return SINKATTN_OK;

@@ -248,6 +248,7 @@ int set_hooks_prefill_tc(long long limit, int skip);
 int set_hooks_decode_tc(long long limit, int skip);
 int set_hooks_prefix_tc(long long limit, int skip);
 int set_hooks_pages(long long limit, int skip);
+int set_hooks_prefill_back(long long limit, int skip);
 
 // Thread-local error text used by the C ABI.
 void set_error(const char* fmt, ...);

@@ -209,5 +209,54 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
+// Epilogue: out row = O_t row times inv, as bf16. Each lane owns one row of the
+// tile; D / 64 blocks of 64 columns (128 bytes) are read from TMEM, scaled
+// and packed into eight 16-byte chunks. An 8 x 8 transpose of the chunks
+// within each group of 8 lanes leaves lane i with chunk i of each of the
+// group's rows, so a store instruction writes 4 whole 128-byte rows per warp
+// rather than 16 bytes of each of 32 rows: 4 L1 wavefronts instead of 32,
+// which keeps the load/store unit free for the next item's copies into
+// shared memory.
+// Warp-collective; `zero` (warp-uniform) stores zeros without reading TMEM.
+template <int D>
+__device__ __forceinline__ void store_o_rows(uint32_t o_addr, bool zero, float inv,
+                                             __nv_bfloat16* orow, bool valid, int lane) {
+  const int i = lane & 7;
+#pragma unroll
+  for (int blk = 0; blk < D / 64; ++blk) {
+    uint4 ch[8];
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      float o[32];
+      if (!zero) {
+        tmem_ld32(o_addr + blk * 64 + half * 32, o);
+        tmem_wait_ld();
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = 0.f;
+      }
+#pragma unroll
+      for (int q4 = 0; q4 < 4; ++q4) {
+        uint4& pk = ch[half * 4 + q4];
+        pk.x = pack_bf16x2(o[q4 * 8 + 0] * inv, o[q4 * 8 + 1] * inv);
+        pk.y = pack_bf16x2(o[q4 * 8 + 2] * inv, o[q4 * 8 + 3] * inv);
+        pk.z = pack_bf16x2(o[q4 * 8 + 4] * inv, o[q4 * 8 + 5] * inv);
+        pk.w = pack_bf16x2(o[q4 * 8 + 6] * inv, o[q4 * 8 + 7] * inv);
+      }
+    }
+    transpose8_chunks(ch, lane);   // now ch[e] of lane i: chunk i of the group's row e
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int src = (lane & ~7) + e;
+      const unsigned long long row =
+          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(orow), src);
+      const int v = __shfl_sync(0xffffffffu, valid ? 1 : 0, src);
+      if (v)
+        *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(row) + blk * 64 + i * 8) =
+            ch[e];
+    }
+  }
+}
+
 }  // namespace tc
 }  // namespace sinkattn

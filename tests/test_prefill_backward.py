@@ -6,7 +6,8 @@ import torch
 
 import gqa_attention_softmax_gb300 as sa
 from gqa_attention_softmax_gb300 import _build
-from gqa_attention_softmax_gb300._binding import BAD_LENGTHS, INVALID_ARG, UNSUPPORTED
+from gqa_attention_softmax_gb300._binding import (BAD_LENGTHS, INVALID_ARG, TIMEOUT,
+                                                  UNSUPPORTED)
 from _gradient_model import attention, attention_gradients
 
 gpu = pytest.mark.gpu
@@ -278,6 +279,25 @@ def test_lengths_that_contradict_the_sizes_are_recorded():
     back = torch.tensor([0, 50, 10], dtype=torch.int32, device="cuda")
     sa.sinkattn_prefill_backward(*args, back, back, 60, 60, 2)
     assert sa.sinkattn_debug_status() == BAD_LENGTHS
+    assert sa.sinkattn_debug_status() == 0
+
+
+@gpu
+@pytest.mark.parametrize("shape", [(8, 1, 64), (8, 1, 128)])
+@pytest.mark.parametrize("tile", [0, 3])
+def test_a_wait_that_runs_out_is_recorded(shape, tile):
+    """A test hook shortens the waits to about 10 ms and leaves one tile's copies out."""
+    x, h = make([700], [700], *shape)
+    want = [t.clone() for t in call(x, h)]
+    assert sa.sinkattn_debug_status() == 0
+    sa.sinkattn_debug_set_hooks(20_000_000, tile)
+    try:
+        call(x, h)
+        assert sa.sinkattn_debug_status() == TIMEOUT
+    finally:
+        sa.sinkattn_debug_set_hooks(0, -1)
+    for a, b in zip(want, call(x, h)):
+        assert torch.equal(a, b)
     assert sa.sinkattn_debug_status() == 0
 
 
