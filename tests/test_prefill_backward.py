@@ -73,7 +73,7 @@ def test_causal(shape, lens):
 
 
 @gpu
-@pytest.mark.parametrize("shape", [(64, 8, 64), (24, 8, 64), (32, 8, 128), (128, 1, 64)])
+@pytest.mark.parametrize("shape", [(64, 8, 64), (24, 8, 64), (32, 8, 128), (128, 1, 64), (70, 1, 128)])
 @pytest.mark.parametrize("causal,window", [(False, 0), (True, 1), (True, 17), (True, 128), (True, 1000)])
 @pytest.mark.parametrize("sinks", [False, True])
 def test_masks(shape, causal, window, sinks):
