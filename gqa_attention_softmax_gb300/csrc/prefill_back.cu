@@ -12,12 +12,9 @@
 // no fp32 buffer of dq in memory, and the group's heads add up in the
 // accumulators.
 //
-// Both kernels: warp 0 stages tiles by TMA and issues the products that take P
-// and dS, warp 1 those that make S and dP, then a warpgroup per stream computes P and dS, one thread per TMEM lane. A tile's way
-// is a chain (product, weights, product), so two streams of tiles share an SM:
-// at d 64 two CTAs of one stream, whose starts and ends overlap too; at d 128,
-// where the accumulators leave no room for a second CTA, one CTA of two streams that
-// take alternate tiles and add to the same accumulators.
+// Both kernels: warp 0 stages tiles by TMA and issues the products that make S
+// and dP, warp 1 those that take P and dS, warps 2 .. compute P and dS, one
+// thread per TMEM lane and 64 columns.
 // P and dS are rounded to bf16 for the products that take them; P enters dS
 // unrounded. Every wait is bounded; on a timeout the CTA records
 // SINKATTN_TIMEOUT, drains its copies and MMAs, frees TMEM and exits.
@@ -45,7 +42,6 @@ struct BackParams {
   int per;       // tokens of a block of the delta pass
   int delta_blocks, sink_blocks;
   int QB, nqb;   // query tokens of a tile of 128 rows, tiles of the longest sequence
-  int GT, chunks, QB2;   // heads and tokens of a tile of 64 rows, tiles of a token
 };
 
 __device__ __forceinline__ float dot8(uint4 x, uint4 y, float s) {
@@ -113,11 +109,10 @@ __global__ void __launch_bounds__(256) back_delta_kernel(const BackParams p) {
 }
 
 // dsinks of 32 heads: the blocks' sums added in a fixed order, by all threads
-// of a block. These are the first blocks of the pass that computes dq.
+// of a block (s: shared memory, 32 words a warp). These are the first blocks of the pass that computes dq.
 template <int kThreads>
-__device__ __forceinline__ void reduce_sinks(const BackParams& p, int chunk) {
+__device__ __forceinline__ void reduce_sinks(const BackParams& p, int chunk, float (*s)[32]) {
   constexpr int kSlices = kThreads / 32;
-  __shared__ float s[kSlices][32];
   const int h = chunk * 32 + threadIdx.x % 32, slice = threadIdx.x / 32;
   float x = 0.f;
   if (h < p.Hq) {
@@ -191,6 +186,12 @@ __device__ __forceinline__ void scores2(float& a, float& b, float p0, float p1, 
   b = x.y;
 }
 
+// The A operand of a TS product: bf16 pairs that replaced fp32 columns, each
+// 64 elements in the first 32 columns of their 64. K step kk covers elements 16 kk ...
+__device__ __forceinline__ uint32_t half_packed(uint32_t base, int kk) {
+  return base + static_cast<uint32_t>(8 * kk + (kk >= 4 ? 32 : 0));
+}
+
 // 32 fp32 columns as bf16 pairs into 16 columns.
 __device__ __forceinline__ void store_packed(uint32_t addr, const float (&v)[32]) {
   uint32_t pk[16];
@@ -199,60 +200,54 @@ __device__ __forceinline__ void store_packed(uint32_t addr, const float (&v)[32]
   tc::tmem_st16(addr, pk);
 }
 
-// dK, dV. S^T = K Q^T and dP^T = V dO^T (M 128 keys, N 64 query rows, K d; all
-// from shared memory), dV += P^T dO and dK += dS^T Q (M 128 keys, N d, K 64; P^T
+// dK, dV. S^T = K Q^T and dP^T = V dO^T (M 128 keys, N 128 query rows, K d; all
+// from shared memory), dV += P^T dO and dK += dS^T Q (M 128 keys, N d, K 128; P^T
 // and dS^T from TMEM, where they replace S^T and dP^T). Keys in the TMEM lanes
-// make P^T and dS^T the MMA's A operand as they are. 64 rows a tile are what TMEM
-// holds of two streams beside the accumulators.
+// make P^T and dS^T the MMA's A operand as they are.
 template <int D>
 struct DkvCfg {
-  static constexpr int NS = D / 64;                 // streams of a CTA
-  static constexpr int CTAS = 2 / NS;               // CTAs of an SM
-  static constexpr int THREADS = 64 + 128 * NS;
+  static constexpr int THREADS = 64 + 256;
   static constexpr int NSUB = D / 64;
-  static constexpr int QT = 64;                     // query rows of a tile
-  static constexpr int KSUB = 128 * 128;            // [128 keys][64 bf16], 128B-swizzled
-  static constexpr int QSUB = QT * 128;
-  static constexpr int K_TILE = NSUB * KSUB;
-  static constexpr int Q_TILE = NSUB * QSUB;
-  static constexpr int NST = 4;                     // stages of Q and dO
-  static constexpr int STAGE = 2 * Q_TILE;
+  static constexpr int SUB = 128 * 128;             // [128 rows][64 bf16], 128B-swizzled
+  static constexpr int TILE = NSUB * SUB;
+  static constexpr int NQ = D == 64 ? 4 : 3;        // stages of Q
+  static constexpr int ND = D == 64 ? 4 : 2;        // stages of dO, which is wanted later
+  static constexpr int NSB = D == 64 ? 2 : 1;       // S^T buffers (TMEM holds no more at d 128)
   static constexpr int OFF_K = 0;
-  static constexpr int OFF_V = K_TILE;
-  static constexpr int OFF_Q = 2 * K_TILE;          // stage s: Q, then dO
-  static constexpr int OFF_ROW = OFF_Q + NST * STAGE;   // [NS][2][-lse log2 e, -delta][QT]
-  static constexpr int OFF_BAR = OFF_ROW + NS * 2 * 2 * QT * 4;
-  static constexpr int N_BARS = 1 + NST + 6 * NS + 7;
-  static constexpr int SMEM = 1024 + OFF_BAR + N_BARS * 8 + 64;
-  static constexpr uint32_t COLS = 512 / CTAS;
-  __host__ __device__ static constexpr uint32_t col_s(int st) { return static_cast<uint32_t>(2 * QT * st); }
-  __host__ __device__ static constexpr uint32_t col_dp(int st) { return col_s(st) + QT; }
-  static constexpr uint32_t COL_DV = 2 * QT * NS;
+  static constexpr int OFF_V = TILE;
+  static constexpr int OFF_Q = 2 * TILE;
+  static constexpr int OFF_DO = OFF_Q + NQ * TILE;
+  static constexpr int OFF_ROW = OFF_DO + ND * TILE;   // [2][-lse log2 e, -delta][128]
+  static constexpr int OFF_BAR = OFF_ROW + 2 * 2 * 128 * 4;
+  static constexpr int N_BARS = 1 + NQ + ND + 2 * NSB + 2 + 2 + 2 + 2 + 1 + 2;
+  static constexpr int SMEM = OFF_BAR + N_BARS * 8 + 16;
+  static constexpr uint32_t COL_S = 0;
+  static constexpr uint32_t COL_DP = 128 * NSB;
+  static constexpr uint32_t COL_DV = COL_DP + 128;
   static constexpr uint32_t COL_DK = COL_DV + D;
-  static_assert(COL_DK + D <= COLS, "TMEM budget");
-  static_assert((SMEM + 1024) * CTAS <= 233472, "shared memory budget");
+  static_assert(COL_DK + D <= 512, "TMEM budget");
+  static_assert(SMEM <= 232448, "shared memory budget");
 };
 
 template <int D>
-__global__ void __launch_bounds__(DkvCfg<D>::THREADS, DkvCfg<D>::CTAS)
+__global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
     back_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmDo,
                     const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                     const BackParams p) {
   using C = DkvCfg<D>;
-  constexpr int NST = C::NST, NS = C::NS, NSUB = C::NSUB, QT = C::QT;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
+  constexpr int NQ = C::NQ, ND = C::ND, NSB = C::NSB, NSUB = C::NSUB;
+  extern __shared__ __align__(1024) uint8_t smem[];   // (swizzled tiles start on 1024 bytes)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* kv_full = bars;
-  uint64_t* q_full = kv_full + 1;      // [NST]
-  uint64_t* s_full = q_full + NST;     // [NS] S^T written
-  uint64_t* p_full = s_full + NS;      // [NS] P^T written (128 arrivals)
-  uint64_t* dp_full = p_full + NS;     // [NS] dP^T written
-  uint64_t* ds_full = dp_full + NS;    // [NS] dS^T written (128 arrivals)
-  uint64_t* row_full = ds_full + NS;   // [NS][2] the rows' lse and delta staged (128 arrivals)
-  uint64_t* dv_done = row_full + 2 * NS;
-  uint64_t* dk_done = dv_done + 2;     // [2] (and dv_done[2]) of even and odd tiles: another warp waits
+  uint64_t* q_full = kv_full + 1;      // [NQ]
+  uint64_t* do_full = q_full + NQ;     // [ND]
+  uint64_t* s_full = do_full + ND;     // [NSB] S^T written
+  uint64_t* p_full = s_full + NSB;     // [NSB] P^T written (256 arrivals)
+  uint64_t* dp_full = p_full + NSB;    // dP^T written
+  uint64_t* ds_full = dp_full + 1;     // dS^T written (256 arrivals)
+  uint64_t* row_full = ds_full + 1;    // [2] the rows' lse and delta staged (256 arrivals)
+  uint64_t* dv_done = row_full + 2;    // [2] of even and odd tiles
+  uint64_t* dk_done = dv_done + 2;     // [2]
   uint64_t* all_done = dk_done + 2;    // every product
   uint64_t* drain = all_done + 1;      // [2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
@@ -278,23 +273,21 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, DkvCfg<D>::CTAS)
   // queries [i0, i1) see some key of the tile
   const int i0 = p.causal ? max(0, k0 - off) : 0;
   const int i1 = p.window > 0 ? max(0, min(s.lq, k0 + nk - 1 + p.window - off)) : s.lq;
-  // a tile is QB2 tokens times GT heads; groups of more than 64 heads come in two chunks
-  const int GT = p.GT, cs = p.chunks - 1, QB2 = p.QB2;
-  const int n = i1 > i0 ? (i1 - i0 + QB2 - 1) / QB2 << cs : 0;
-  const int rows = GT * QB2;
+  const int n = i1 > i0 ? (i1 - i0 + p.QB - 1) / p.QB : 0;
+  const int G = p.G, rows = G * p.QB;
 
   if (threadIdx.x == 0) {
     mbar_init(kv_full, 1);
-    for (int i = 0; i < NST; ++i) mbar_init(&q_full[i], 1);
-    for (int i = 0; i < NS; ++i) {
+    for (int i = 0; i < NQ; ++i) mbar_init(&q_full[i], 1);
+    for (int i = 0; i < ND; ++i) mbar_init(&do_full[i], 1);
+    for (int i = 0; i < NSB; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 128);
-      mbar_init(&dp_full[i], 1);
-      mbar_init(&ds_full[i], 128);
-      mbar_init(&row_full[2 * i], 128);
-      mbar_init(&row_full[2 * i + 1], 128);
+      mbar_init(&p_full[i], 256);
     }
+    mbar_init(dp_full, 1);
+    mbar_init(ds_full, 256);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&row_full[i], 256);
       mbar_init(&dv_done[i], 1);
       mbar_init(&dk_done[i], 1);
       mbar_init(&drain[i], 1);
@@ -303,87 +296,93 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, DkvCfg<D>::CTAS)
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (rows < QT) {   // rows that no copy writes
-    for (int i = 0; i < 2 * NST; ++i)
-      zero_rows<NSUB>(smem + C::OFF_Q + i * C::Q_TILE, C::QSUB, rows, QT, threadIdx.x, C::THREADS);
+  if (rows < 128) {   // rows that no copy writes
+    for (int i = 0; i < NQ + ND; ++i)
+      zero_rows<NSUB>(smem + C::OFF_Q + i * C::TILE, C::SUB, rows, 128, threadIdx.x, C::THREADS);
     tc::fence_proxy_async_smem();
   }
   if (warp == 1) {
-    tc::tmem_alloc(tmem_slot, C::COLS);
+    tc::tmem_alloc(tmem_slot, 512);
     tc::tmem_relinquish();
   }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  int issued = 0;   // tiles whose copies were issued (or left out by the test hook)
+  int issued_q = 0, issued_do = 0;   // tiles whose copies were issued (or left out by the test hook)
   auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
     return warp_wait(bar, parity, abort_flag, status);
   };
-  const uint64_t qt = tc::smem_desc_sw128(smem_u32(smem + C::OFF_Q), C::QSUB, 1024);   // MN-major
-  auto stage = [&](int j) { return static_cast<uint64_t>(j % NST) * (C::STAGE >> 4); };
 
   if (warp == 0) {
-    // ------------------------------------------ copies; dV += P^T dO and dK += dS^T Q
+    // ------------------------------------------ copies; S^T = K Q^T and dP^T = V dO^T
     const bool leader = tc::elect_one();
     const int skip_tile = hook_skip_tile();
-    auto load = [&](int j) {   // of a stage that is free
-      issued = j + 1;
+    auto load = [&](const CUtensorMap* map, int j, uint8_t* to, uint64_t* bar) {   // into a free stage
       if (j != skip_tile && leader) {   // test hook: the waits for this tile run out
-        uint8_t* to = smem + C::OFF_Q + (j % NST) * C::STAGE;
-        uint64_t* bar = &q_full[j % NST];
-        mbar_arrive_expect_tx(bar, static_cast<uint32_t>(2 * NSUB * 128 * rows));
-        const int tok = s.q0 + i0 + (j >> cs) * QB2;
-        const int head = kvh * p.G + (j & cs) * GT;
+        mbar_arrive_expect_tx(bar, static_cast<uint32_t>(NSUB * 128 * rows));
 #pragma unroll
         for (int sub = 0; sub < NSUB; ++sub)
-          tc::tma_load_3d(to + sub * C::QSUB, &tmQ, sub * 64, head, tok, bar);
-#pragma unroll
-        for (int sub = 0; sub < NSUB; ++sub)
-          tc::tma_load_3d(to + C::Q_TILE + sub * C::QSUB, &tmDo, sub * 64, head, tok, bar);
+          tc::tma_load_3d(to + sub * C::SUB, map, sub * 64, kvh * G, s.q0 + i0 + j * p.QB, bar);
       }
       __syncwarp();
     };
+    auto load_q = [&](int j) {
+      issued_q = j + 1;
+      load(&tmQ, j, smem + C::OFF_Q + j % NQ * C::TILE, &q_full[j % NQ]);
+    };
+    auto load_do = [&](int j) {
+      issued_do = j + 1;
+      load(&tmDo, j, smem + C::OFF_DO + j % ND * C::TILE, &do_full[j % ND]);
+    };
     if (n > 0) {
       if (leader) {
-        mbar_arrive_expect_tx(kv_full, 2 * C::K_TILE);
+        mbar_arrive_expect_tx(kv_full, 2 * C::TILE);
         const int slab = p.Hkv * s.k0 + kvh * s.lk + k0;
 #pragma unroll
         for (int sub = 0; sub < NSUB; ++sub) {
-          tma_load_2d(smem + C::OFF_K + sub * C::KSUB, &tmK, sub * 64, slab, kv_full);
-          tma_load_2d(smem + C::OFF_V + sub * C::KSUB, &tmV, sub * 64, slab, kv_full);
+          tma_load_2d(smem + C::OFF_K + sub * C::SUB, &tmK, sub * 64, slab, kv_full);
+          tma_load_2d(smem + C::OFF_V + sub * C::SUB, &tmV, sub * 64, slab, kv_full);
         }
       }
-      for (int j = 0; j < min(NST, n); ++j) load(j);
+      __syncwarp();
+      for (int j = 0; j < min(NQ, n); ++j) load_q(j);
+      for (int j = 0; j < min(ND, n); ++j) load_do(j);
     }
-    constexpr uint32_t idesc_o = tc::idesc_bf16_f32(128, D, true);
-    // D += A B over the tile's rows; A in TMEM
-    auto ts = [&](uint32_t d_tm, uint32_t a, uint64_t bq, bool first, uint64_t* bar) {
+    constexpr uint32_t idesc_s = tc::idesc_bf16_f32(128, 128, false);
+    const uint64_t kd = tc::smem_desc_sw128(smem_u32(smem + C::OFF_K), 16, 1024);
+    const uint64_t vd = tc::smem_desc_sw128(smem_u32(smem + C::OFF_V), 16, 1024);
+    const uint64_t qd = tc::smem_desc_sw128(smem_u32(smem + C::OFF_Q), 16, 1024);
+    const uint64_t dod = tc::smem_desc_sw128(smem_u32(smem + C::OFF_DO), 16, 1024);
+    // D = A B^T over d; both K-major
+    auto ss = [&](uint32_t d_tm, uint64_t a, uint64_t bq, uint64_t* bar) {
       if (leader) {
 #pragma unroll
-        for (int kk = 0; kk < QT / 16; ++kk)
-          tc::mma_ts(d_tm, a + 8 * kk, bq + static_cast<uint64_t>(kk) * 128u, idesc_o,
-                     first && kk == 0 ? 0u : 1u);
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint64_t at = static_cast<uint64_t>(kk >> 2) * (C::SUB >> 4) + (kk & 3) * 2;
+          tc::mma_ss(d_tm, a + at, bq + at, idesc_s, kk > 0 ? 1u : 0u);
+        }
         tc::commit(bar);
       }
       __syncwarp();
     };
-    for (int j = 0; j < n; ++j) {
-      const int st = j % NS;
-      if (!wwait(&p_full[st], (j / NS) & 1)) break;
-      tc::fence_after_sync();
-      ts(tmem + C::COL_DV, tmem + C::col_s(st), qt + stage(j) + (C::Q_TILE >> 4), j == 0, &dv_done[j & 1]);
-      if (!wwait(&ds_full[st], (j / NS) & 1)) break;
-      tc::fence_after_sync();
-      ts(tmem + C::COL_DK, tmem + C::col_dp(st), qt + stage(j), j == 0, &dk_done[j & 1]);
-      if (j + 1 == n) {
-        if (leader) tc::commit(all_done);
-        __syncwarp();
-      }
-      // the stage of the tile before is free when its dK, the last of its four products, is done
-      if (j >= 1 && j - 1 + NST < n) {
-        if (!wwait(&dk_done[(j - 1) & 1], ((j - 1) >> 1) & 1)) break;
-        load(j - 1 + NST);
+    if (n > 0 && wwait(kv_full, 0)) {
+      for (int j = 0; j < n; ++j) {
+        // S^T(j) overwrites the P^T that dV(j - NSB) reads
+        if (!wwait(&q_full[j % NQ], j / NQ & 1) ||
+            (j >= NSB && !wwait(&dv_done[(j - NSB) & 1], ((j - NSB) >> 1) & 1))) break;
+        tc::fence_after_sync();
+        ss(tmem + C::COL_S + 128 * (j % NSB), kd, qd + static_cast<uint64_t>(j % NQ) * (C::TILE >> 4),
+           &s_full[j % NSB]);
+        // dP^T(j) overwrites the dS^T that dK(j - 1) reads, the last of that tile's products
+        if (j >= 1) {
+          if (!wwait(&dk_done[(j - 1) & 1], ((j - 1) >> 1) & 1)) break;
+          if (j - 1 + NQ < n) load_q(j - 1 + NQ);
+          if (j - 1 + ND < n) load_do(j - 1 + ND);
+        }
+        if (!wwait(&do_full[j % ND], j / ND & 1)) break;
+        tc::fence_after_sync();
+        ss(tmem + C::COL_DP, vd, dod + static_cast<uint64_t>(j % ND) * (C::TILE >> 4), dp_full);
       }
     }
     // every MMA this warp issued has completed before the CTA frees TMEM
@@ -391,91 +390,88 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, DkvCfg<D>::CTAS)
     __syncwarp();
     mbar_drain(&drain[0], 0);
   } else if (warp == 1) {
-    // ------------------------------------------ S^T = K Q^T and dP^T = V dO^T
+    // ------------------------------------------ dV += P^T dO and dK += dS^T Q
     // (a warp of its own: an issuer that waits for the weights of one tile would
     // leave the tensor core without the next tile's scores)
     const bool leader = tc::elect_one();
-    constexpr uint32_t idesc_s = tc::idesc_bf16_f32(128, QT, false);
-    const uint64_t kd = tc::smem_desc_sw128(smem_u32(smem + C::OFF_K), 16, 1024);
-    const uint64_t vd = tc::smem_desc_sw128(smem_u32(smem + C::OFF_V), 16, 1024);
-    const uint64_t qd = tc::smem_desc_sw128(smem_u32(smem + C::OFF_Q), 16, 1024);
-    // D = A B^T over d; both K-major
-    auto ss = [&](uint32_t d_tm, uint64_t a, uint64_t bq, uint64_t* bar) {
+    constexpr uint32_t idesc_o = tc::idesc_bf16_f32(128, D, true);
+    const uint64_t qt = tc::smem_desc_sw128(smem_u32(smem + C::OFF_Q), C::SUB, 1024);   // MN-major
+    const uint64_t dot = tc::smem_desc_sw128(smem_u32(smem + C::OFF_DO), C::SUB, 1024);
+    // D += A B over the tile's rows; A in TMEM
+    auto ts = [&](uint32_t d_tm, uint32_t a, uint64_t bq, bool first, uint64_t* bar) {
       if (leader) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          tc::mma_ss(d_tm, a + static_cast<uint64_t>(kk >> 2) * (C::KSUB >> 4) + (kk & 3) * 2,
-                     bq + static_cast<uint64_t>(kk >> 2) * (C::QSUB >> 4) + (kk & 3) * 2, idesc_s,
-                     kk > 0 ? 1u : 0u);
+        for (int kk = 0; kk < 8; ++kk)
+          tc::mma_ts(d_tm, half_packed(a, kk), bq + static_cast<uint64_t>(kk) * 128u, idesc_o,
+                     first && kk == 0 ? 0u : 1u);
         tc::commit(bar);
       }
       __syncwarp();
     };
-    if (n > 0 && wwait(kv_full, 0)) {
-      for (int j = 0; j < n; ++j) {
-        const int st = j % NS;
-        // S^T(j) overwrites the P^T that dV(j - NS) reads, dP^T(j) the dS^T that dK(j - NS) reads
-        if (!wwait(&q_full[j % NST], (j / NST) & 1) || (j >= NS && !wwait(&dv_done[(j - NS) & 1], ((j - NS) >> 1) & 1))) break;
-        tc::fence_after_sync();
-        ss(tmem + C::col_s(st), kd, qd + stage(j), &s_full[st]);
-        if (j >= NS && !wwait(&dk_done[(j - NS) & 1], ((j - NS) >> 1) & 1)) break;
-        tc::fence_after_sync();
-        ss(tmem + C::col_dp(st), vd, qd + stage(j) + (C::Q_TILE >> 4), &dp_full[st]);
-      }
+    for (int j = 0; j < n; ++j) {
+      if (!wwait(&p_full[j % NSB], j / NSB & 1)) break;
+      tc::fence_after_sync();
+      ts(tmem + C::COL_DV, tmem + C::COL_S + 128 * (j % NSB),
+         dot + static_cast<uint64_t>(j % ND) * (C::TILE >> 4), j == 0, &dv_done[j & 1]);
+      if (!wwait(ds_full, j & 1)) break;
+      tc::fence_after_sync();
+      ts(tmem + C::COL_DK, tmem + C::COL_DP, qt + static_cast<uint64_t>(j % NQ) * (C::TILE >> 4),
+         j == 0, &dk_done[j & 1]);
     }
-    if (leader) tc::commit(&drain[1]);
+    if (leader) {
+      tc::commit(all_done);
+      tc::commit(&drain[1]);
+    }
     __syncwarp();
     mbar_drain(&drain[1], 0);
   } else {
     // ---------------------------------------------------------------- P and dS
-    const int st = (warp - 2) >> 2;            // stream
-    const int tid = threadIdx.x - 64 - 128 * st;
+    const int tid = threadIdx.x - 64;
+    const int half = (warp - 2) >> 2;          // columns 64 half ...
     const int quad = warp & 3;                 // TMEM lane quadrant this warp may access
     const int key = quad * 32 + lane;          // key of the tile
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    const uint32_t s_addr = lane_base + C::col_s(0) + 2 * QT * st;
-    const uint32_t dp_addr = s_addr + QT;
-    float* row_s = reinterpret_cast<float*>(smem + C::OFF_ROW) + st * 4 * QT;   // [2][2][QT]
-    uint64_t* rows_in = row_full + 2 * st;
-    // thread tid stages -lse log2(e) (tid < QT) or -delta of row tid % QT; a row outside
+    float* row_s = reinterpret_cast<float*>(smem + C::OFF_ROW);   // [2][2][128]
+    // thread tid stages -lse log2(e) (tid < 128) or -delta of row tid % 128; a row outside
     // the tile, and one that sees nothing, gets lse = +inf: P = 0
-    const int r = tid % QT, rt = r / GT;
+    const int r = tid & 127, rt = r / G;
+    const float* from = (tid < 128 ? p.lse : p.delta) + kvh * G + (r - rt * G);
     auto fetch = [&](int j) -> float {
-      const int i = i0 + (j >> cs) * QB2 + rt;
-      const int hh = (j & cs) * GT + (r - rt * GT);
-      if (r >= rows || i >= i1 || hh >= p.G) return tid < QT ? INFINITY : 0.f;
-      const long long at = static_cast<long long>(s.q0 + i) * p.Hq + kvh * p.G + hh;
-      return (tid < QT ? p.lse : p.delta)[at];
+      const int i = i0 + j * p.QB + rt;
+      if (r >= rows || i >= i1) return tid < 128 ? INFINITY : 0.f;
+      return from[static_cast<long long>(s.q0 + i) * p.Hq];
     };
     // (what was fetched is first looked at here, half a tile later)
-    auto put = [&](int u, float x) {   // of the stream's u-th tile
-      row_s[(u & 1) * 2 * QT + tid] = tid >= QT ? -x : x == kNegInf ? kNegInf : -x * kLog2e;
-      mbar_arrive(&rows_in[u & 1]);
+    auto put = [&](int j, float x) {
+      row_s[(j & 1) * 256 + tid] = tid >= 128 ? -x : x == kNegInf ? kNegInf : -x * kLog2e;
+      mbar_arrive(&row_full[j & 1]);
     };
     const float2 cc = make_float2(p.scale_log2, p.scale_log2);
     bool ok = true;
-    if (st < n) put(0, fetch(st));
-    for (int j = st, u = 0; j < n; j += NS, ++u) {
+    if (n > 0) put(0, fetch(0));
+    for (int j = 0; j < n; ++j) {
       float next = 0.f;
-      if (j + NS < n) next = fetch(j + NS);
-      const int t0 = i0 + (j >> cs) * QB2;      // first query of the tile
-      const int nt = min(QB2, i1 - t0);
+      if (j + 1 < n) next = fetch(j + 1);
+      const int t0 = i0 + j * p.QB;              // first query of the tile
+      const int nt = min(p.QB, i1 - t0);
       const int pos0 = off + t0;
-      // columns [lo, hi) of this key's row are visible
-      int lo = 0, hi = nt * GT;
-      bool masked = nt < QB2;   // (the rows past rows are zeros of weight 0)
+      // columns [lo, hi) of this thread's 64 are visible to the key
+      int lo = -64 * half, hi = lo + nt * G;
+      bool masked = nt < p.QB;   // (the rows past rows are zeros of weight 0)
       if (p.causal) {
         masked = masked || k0 + 127 > pos0;
-        lo = max(0, min(nt, k0 + key - pos0)) * GT;
+        lo += max(0, min(nt, k0 + key - pos0)) * G;
       }
       if (p.window > 0) {
-        masked = masked || k0 + p.window < pos0 + QB2;
-        hi = max(0, min(nt, k0 + key + p.window - pos0)) * GT;
+        masked = masked || k0 + p.window < pos0 + p.QB;
+        hi = max(0, min(nt, k0 + key + p.window - pos0)) * G - 64 * half;
       }
-      if (!wwait(&rows_in[u & 1], (u >> 1) & 1) || !wwait(&s_full[st], u & 1)) { ok = false; break; }
+      if (!wwait(&row_full[j & 1], j >> 1 & 1) || !wwait(&s_full[j % NSB], j / NSB & 1)) { ok = false; break; }
       tc::fence_after_sync();
-      const float4* lse4 = reinterpret_cast<const float4*>(row_s + (u & 1) * 2 * QT);
-      const float4* del4 = lse4 + QT / 4;
+      const uint32_t s_addr = lane_base + C::COL_S + 128 * (j % NSB) + 64 * half;
+      const uint32_t dp_addr = lane_base + C::COL_DP + 64 * half;
+      const float4* lse4 = reinterpret_cast<const float4*>(row_s + (j & 1) * 256 + 64 * half);
+      const float4* del4 = lse4 + 32;
       float v[2][32];
       tc::tmem_ld32(s_addr, v[0]);
       tc::tmem_ld32(s_addr + 32, v[1]);
@@ -495,21 +491,20 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, DkvCfg<D>::CTAS)
         }
         store_packed(s_addr + 16 * c, v[c]);
       }
-      if (nt < QB2) {
+      if (nt < p.QB) {
         // The visible rows end inside the tile: those behind them may be another
         // sequence's, whose NaN would pass through zero weights. Both products
         // that read the tile along d are done.
-        if (!wwait(&dp_full[st], u & 1)) { ok = false; break; }
-        uint8_t* tile = smem + C::OFF_Q + (j % NST) * C::STAGE;
-        zero_rows<NSUB>(tile, C::QSUB, nt * GT, QT, tid, 128);
-        zero_rows<NSUB>(tile + C::Q_TILE, C::QSUB, nt * GT, QT, tid, 128);
+        if (!wwait(dp_full, j & 1)) { ok = false; break; }
+        zero_rows<NSUB>(smem + C::OFF_Q + j % NQ * C::TILE, C::SUB, nt * G, 128, tid, 256);
+        zero_rows<NSUB>(smem + C::OFF_DO + j % ND * C::TILE, C::SUB, nt * G, 128, tid, 256);
         tc::fence_proxy_async_smem();
       }
       tc::tmem_wait_st();
       tc::fence_before_sync();
-      mbar_arrive(&p_full[st]);
+      mbar_arrive(&p_full[j % NSB]);
 
-      if (!wwait(&dp_full[st], u & 1)) { ok = false; break; }
+      if (!wwait(dp_full, j & 1)) { ok = false; break; }
       tc::fence_after_sync();
       float w[2][32];
       tc::tmem_ld32(dp_addr, w[0]);
@@ -532,18 +527,16 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, DkvCfg<D>::CTAS)
       }
       tc::tmem_wait_st();
       tc::fence_before_sync();
-      mbar_arrive(&ds_full[st]);
-      if (j + NS < n) put(u + 1, next);
+      mbar_arrive(ds_full);
+      if (j + 1 < n) put(j + 1, next);
     }
     // ------------------------------------------------------------ epilogue
     if (ok && n > 0) ok = wwait(all_done, 0);
     tc::fence_after_sync();
     const long long row = static_cast<long long>(p.Hkv) * s.k0 + static_cast<long long>(kvh) * s.lk + k0 + key;
-    // two streams: the first stores dV, the second dK
-    if (NS == 1 || st == 0)
-      tc::store_o_rows<D>(lane_base + C::COL_DV, !(ok && n > 0), 1.f, p.dv + row * D, key < nk, lane);
-    if (NS == 1 || st == 1)
-      tc::store_o_rows<D>(lane_base + C::COL_DK, !(ok && n > 0), p.sm_scale, p.dk + row * D, key < nk, lane);
+    // the first four warps store dV, the others dK
+    tc::store_o_rows<D>(lane_base + (half ? C::COL_DK : C::COL_DV), !(ok && n > 0),
+                        half ? p.sm_scale : 1.f, (half ? p.dk : p.dv) + row * D, key < nk, lane);
   }
 
   // a warp that left its loop early may still have TMEM loads or stores in flight
@@ -555,40 +548,44 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, DkvCfg<D>::CTAS)
     // a wait gave up: let every issued copy land before the CTA's shared
     // memory goes away (a left-out tile's phase never completes: bounded)
     if (n > 0) mbar_drain(kv_full, 0);
-    for (int i = max(0, issued - NST); i < issued; ++i) mbar_drain(&q_full[i % NST], (i / NST) & 1);
+    for (int i = max(0, issued_q - NQ); i < issued_q; ++i) mbar_drain(&q_full[i % NQ], i / NQ & 1);
+    for (int i = max(0, issued_do - ND); i < issued_do; ++i) mbar_drain(&do_full[i % ND], i / ND & 1);
   }
   if (warp == 1) {
     tc::fence_after_sync();
-    tc::tmem_dealloc(tmem, C::COLS);
+    tc::tmem_dealloc(tmem, 512);
   }
 }
 
-// dQ. S = Q K^T and dP = dO V^T (M 128 query rows, N 96 keys, K d; from shared
-// memory), dQ += dS K (N d, K 96; dS from TMEM, where it replaces S). 96 keys a
-// tile fill what TMEM holds of two streams beside the accumulators.
+// dQ. S = Q K^T and dP = dO V^T (M 128 query rows, N KT keys, K d; from shared
+// memory), dQ += dS K (N d, K KT; dS from TMEM, where it replaces S). Two S
+// buffers: S(j + 1) is there when the weights of tile j are done. At d 64 two
+// CTAs share an SM, so that one starts or ends while the other computes.
 template <int D>
 struct DqCfg {
-  static constexpr int NS = D / 64;                 // streams of a CTA
-  static constexpr int CTAS = 2 / NS;               // CTAs of an SM
-  static constexpr int THREADS = 64 + 128 * NS;
+  static constexpr int CTAS = D == 64 ? 2 : 1;      // CTAs of an SM
+  static constexpr int KT = D;                      // keys of a tile
+  static constexpr int HALVES = KT / 64;            // warpgroups that share a tile's columns
+  static constexpr int SOFT = 128 * HALVES;
+  static constexpr int THREADS = 64 + SOFT;
   static constexpr int NSUB = D / 64;
-  static constexpr int KT = 96;                     // keys of a tile
   static constexpr int KSUB = KT * 128;
   static constexpr int QSUB = 128 * 128;
   static constexpr int K_TILE = NSUB * KSUB;
   static constexpr int Q_TILE = NSUB * QSUB;
-  static constexpr int NST = 3;                     // stages of K, and of V
+  static constexpr int NK = D == 64 ? 4 : 3;        // stages of K
+  static constexpr int NV = D == 64 ? 4 : 2;        // stages of V, which one product reads
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_DO = Q_TILE;
   static constexpr int OFF_K = 2 * Q_TILE;
-  static constexpr int OFF_V = OFF_K + NST * K_TILE;
-  static constexpr int OFF_BAR = OFF_V + NST * K_TILE;
-  static constexpr int N_BARS = 1 + 2 * NST + 3 * NS + 5;
-  static constexpr int SMEM = 1024 + OFF_BAR + N_BARS * 8 + 64;
+  static constexpr int OFF_V = OFF_K + NK * K_TILE;
+  static constexpr int OFF_BAR = OFF_V + NV * K_TILE;
+  static constexpr int N_BARS = 1 + NK + NV + 2 + 2 + 1 + 1 + 2 + 1 + 2;
+  static constexpr int SMEM = 1024 + OFF_BAR + N_BARS * 8 + 16;
   static constexpr uint32_t COLS = 512 / CTAS;
-  __host__ __device__ static constexpr uint32_t col_s(int st) { return static_cast<uint32_t>(2 * KT * st); }
-  __host__ __device__ static constexpr uint32_t col_dp(int st) { return col_s(st) + KT; }
-  static constexpr uint32_t COL_DQ = 2 * KT * NS;
+  static constexpr uint32_t COL_S = 0;
+  static constexpr uint32_t COL_DP = 2 * KT;
+  static constexpr uint32_t COL_DQ = 3 * KT;
   static_assert(COL_DQ + D <= COLS, "TMEM budget");
   static_assert((SMEM + 1024) * CTAS <= 233472, "shared memory budget");
 };
@@ -599,22 +596,23 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, DqCfg<D>::CTAS)
                    const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                    const BackParams p) {
   using C = DqCfg<D>;
-  constexpr int NST = C::NST, NS = C::NS, NSUB = C::NSUB, KT = C::KT;
+  constexpr int NK = C::NK, NV = C::NV, NSUB = C::NSUB, KT = C::KT;
+  extern __shared__ uint8_t smem_raw[];
   if (static_cast<int>(blockIdx.x) < p.sink_blocks) {
-    reduce_sinks<C::THREADS>(p, blockIdx.x);
+    reduce_sinks<C::THREADS>(p, blockIdx.x, reinterpret_cast<float(*)[32]>(smem_raw));
     return;
   }
-  extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* q_full = bars;
-  uint64_t* k_full = q_full + 1;       // [NST]
-  uint64_t* v_full = k_full + NST;     // [NST]
-  uint64_t* s_full = v_full + NST;     // [NS] S written
-  uint64_t* dp_full = s_full + NS;     // [NS] dP written
-  uint64_t* ds_full = dp_full + NS;    // [NS] dS written, dP read (128 arrivals)
-  uint64_t* dq_done = ds_full + NS;    // [2] of even and odd tiles (two warps wait for it)
+  uint64_t* k_full = q_full + 1;       // [NK]
+  uint64_t* v_full = k_full + NK;      // [NV]
+  uint64_t* s_full = v_full + NV;      // [2] S written
+  uint64_t* ds_full = s_full + 2;      // [2] dS written (all softmax threads)
+  uint64_t* dp_full = ds_full + 2;     // dP written
+  uint64_t* dp_free = dp_full + 1;     // dP read (all softmax threads)
+  uint64_t* dq_done = dp_free + 1;     // [2] of even and odd tiles
   uint64_t* all_done = dq_done + 2;    // every product
   uint64_t* drain = all_done + 1;      // [2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
@@ -645,16 +643,13 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, DqCfg<D>::CTAS)
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
-    for (int i = 0; i < NST; ++i) {
-      mbar_init(&k_full[i], 1);
-      mbar_init(&v_full[i], 1);
-    }
-    for (int i = 0; i < NS; ++i) {
-      mbar_init(&s_full[i], 1);
-      mbar_init(&dp_full[i], 1);
-      mbar_init(&ds_full[i], 128);
-    }
+    for (int i = 0; i < NK; ++i) mbar_init(&k_full[i], 1);
+    for (int i = 0; i < NV; ++i) mbar_init(&v_full[i], 1);
+    mbar_init(dp_full, 1);
+    mbar_init(dp_free, C::SOFT);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&ds_full[i], C::SOFT);
       mbar_init(&dq_done[i], 1);
       mbar_init(&drain[i], 1);
     }
@@ -674,35 +669,29 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, DqCfg<D>::CTAS)
   auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
     return warp_wait(bar, parity, abort_flag, status);
   };
-  auto stage = [&](int j) { return static_cast<uint64_t>(j % NST) * (C::K_TILE >> 4); };
 
   if (warp == 0) {
-    // ------------------------------------------ copies; dQ += dS K
+    // ------------------------------------------ copies; S = Q K^T and dP = dO V^T
     const bool leader = tc::elect_one();
     const uint64_t policy = policy_evict_last();   // K and V are re-read by every query block
     const int slab = p.Hkv * s.k0 + kvh * s.lk + k_lo;
     const int skip_tile = hook_skip_tile();
-    auto load_k = [&](int j) {   // into a stage that is free
-      issued_k = j + 1;
+    auto load = [&](const CUtensorMap* map, int j, uint8_t* to, uint64_t* bar) {   // into a free stage
       if (j != skip_tile && leader) {   // test hook: the waits for this tile run out
-        mbar_arrive_expect_tx(&k_full[j % NST], C::K_TILE);
+        mbar_arrive_expect_tx(bar, C::K_TILE);
 #pragma unroll
         for (int sub = 0; sub < NSUB; ++sub)
-          tma_load_2d_hint(smem + C::OFF_K + (j % NST) * C::K_TILE + sub * C::KSUB, &tmK, sub * 64,
-                           slab + j * KT, &k_full[j % NST], policy);
+          tma_load_2d_hint(to + sub * C::KSUB, map, sub * 64, slab + j * KT, bar, policy);
       }
       __syncwarp();
     };
+    auto load_k = [&](int j) {
+      issued_k = j + 1;
+      load(&tmK, j, smem + C::OFF_K + j % NK * C::K_TILE, &k_full[j % NK]);
+    };
     auto load_v = [&](int j) {
       issued_v = j + 1;
-      if (j != skip_tile && leader) {
-        mbar_arrive_expect_tx(&v_full[j % NST], C::K_TILE);
-#pragma unroll
-        for (int sub = 0; sub < NSUB; ++sub)
-          tma_load_2d_hint(smem + C::OFF_V + (j % NST) * C::K_TILE + sub * C::KSUB, &tmV, sub * 64,
-                           slab + j * KT, &v_full[j % NST], policy);
-      }
-      __syncwarp();
+      load(&tmV, j, smem + C::OFF_V + j % NV * C::K_TILE, &v_full[j % NV]);
     };
     if (leader) {
       // (rows that no copy writes are lanes whose results are not stored)
@@ -713,40 +702,9 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, DqCfg<D>::CTAS)
         tc::tma_load_3d(smem + C::OFF_DO + sub * C::QSUB, &tmDo, sub * 64, kvh * G, s.q0 + t0, q_full);
       }
     }
-    for (int j = 0; j < min(NST, n); ++j) {
-      load_k(j);
-      load_v(j);
-    }
-    constexpr uint32_t idesc_o = tc::idesc_bf16_f32(128, D, true);
-    const uint64_t kt = tc::smem_desc_sw128(smem_u32(smem + C::OFF_K), C::KSUB, 1024);   // MN-major
-    for (int j = 0; j < n; ++j) {
-      const int st = j % NS;
-      if (!wwait(&ds_full[st], (j / NS) & 1)) break;
-      tc::fence_after_sync();
-      if (leader) {
-        const uint64_t bk = kt + stage(j);
-#pragma unroll
-        for (int kk = 0; kk < KT / 16; ++kk)
-          tc::mma_ts(tmem + C::COL_DQ, tmem + C::col_s(st) + 8 * kk,
-                     bk + static_cast<uint64_t>(kk) * 128u, idesc_o, j == 0 && kk == 0 ? 0u : 1u);
-        tc::commit(&dq_done[j & 1]);
-        if (j + 1 == n) tc::commit(all_done);
-      }
-      __syncwarp();
-      // dS(j) came after dP(j), the only product that reads V's tile j
-      if (j + NST < n) load_v(j + NST);
-      if (j >= 1 && j - 1 + NST < n) {
-        if (!wwait(&dq_done[(j - 1) & 1], ((j - 1) >> 1) & 1)) break;
-        load_k(j - 1 + NST);
-      }
-    }
-    // every MMA this warp issued has completed before the CTA frees TMEM
-    if (leader) tc::commit(&drain[0]);
     __syncwarp();
-    mbar_drain(&drain[0], 0);
-  } else if (warp == 1) {
-    // ------------------------------------------ S = Q K^T and dP = dO V^T
-    const bool leader = tc::elect_one();
+    for (int j = 0; j < min(NK, n); ++j) load_k(j);
+    for (int j = 0; j < min(NV, n); ++j) load_v(j);
     constexpr uint32_t idesc_s = tc::idesc_bf16_f32(128, KT, false);
     const uint64_t qd = tc::smem_desc_sw128(smem_u32(smem + C::OFF_Q), 16, 1024);
     const uint64_t dod = tc::smem_desc_sw128(smem_u32(smem + C::OFF_DO), 16, 1024);
@@ -765,26 +723,57 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, DqCfg<D>::CTAS)
     };
     if (wwait(q_full, 0)) {
       for (int j = 0; j < n; ++j) {
-        const int st = j % NS;
-        // dP(j) overwrites a dP that has been read when its dS is there, S(j)
-        // the dS(j - NS) that dQ reads: dP runs while that ends
-        if (!wwait(&v_full[j % NST], (j / NST) & 1) ||
-            (j >= NS && !wwait(&ds_full[st], (j / NS - 1) & 1))) break;
+        // S(j) overwrites the dS(j - 2) that dQ reads
+        if (!wwait(&k_full[j % NK], j / NK & 1)) break;
+        if (j >= 2) {
+          if (!wwait(&dq_done[j & 1], (j - 2) >> 1 & 1)) break;
+          if (j - 2 + NK < n) load_k(j - 2 + NK);
+        }
         tc::fence_after_sync();
-        ss(tmem + C::col_dp(st), dod, vd + stage(j), &dp_full[st]);
-        if (!wwait(&k_full[j % NST], (j / NST) & 1) ||
-            (j >= NS && !wwait(&dq_done[(j - NS) & 1], ((j - NS) >> 1) & 1))) break;
+        ss(tmem + C::COL_S + KT * (j & 1), qd, kd + static_cast<uint64_t>(j % NK) * (C::K_TILE >> 4),
+           &s_full[j & 1]);
+        // dP(j) overwrites dP(j - 1)
+        if (j >= 1) {
+          if (!wwait(dp_free, (j - 1) & 1)) break;
+          if (j - 1 + NV < n) load_v(j - 1 + NV);
+        }
+        if (!wwait(&v_full[j % NV], j / NV & 1)) break;
         tc::fence_after_sync();
-        ss(tmem + C::col_s(st), qd, kd + stage(j), &s_full[st]);
+        ss(tmem + C::COL_DP, dod, vd + static_cast<uint64_t>(j % NV) * (C::K_TILE >> 4), dp_full);
       }
     }
-    if (leader) tc::commit(&drain[1]);
+    // every MMA this warp issued has completed before the CTA frees TMEM
+    if (leader) tc::commit(&drain[0]);
+    __syncwarp();
+    mbar_drain(&drain[0], 0);
+  } else if (warp == 1) {
+    // ------------------------------------------ dQ += dS K
+    const bool leader = tc::elect_one();
+    constexpr uint32_t idesc_o = tc::idesc_bf16_f32(128, D, true);
+    const uint64_t kt = tc::smem_desc_sw128(smem_u32(smem + C::OFF_K), C::KSUB, 1024);   // MN-major
+    for (int j = 0; j < n; ++j) {
+      if (!wwait(&ds_full[j & 1], j >> 1 & 1)) break;
+      tc::fence_after_sync();
+      if (leader) {
+        const uint64_t bk = kt + static_cast<uint64_t>(j % NK) * (C::K_TILE >> 4);
+#pragma unroll
+        for (int kk = 0; kk < KT / 16; ++kk)
+          tc::mma_ts(tmem + C::COL_DQ, half_packed(tmem + C::COL_S + KT * (j & 1), kk),
+                     bk + static_cast<uint64_t>(kk) * 128u, idesc_o, j == 0 && kk == 0 ? 0u : 1u);
+        tc::commit(&dq_done[j & 1]);
+      }
+      __syncwarp();
+    }
+    if (leader) {
+      tc::commit(all_done);
+      tc::commit(&drain[1]);
+    }
     __syncwarp();
     mbar_drain(&drain[1], 0);
   } else {
     // ---------------------------------------------------------------- P and dS
-    const int st = (warp - 2) >> 2;            // stream
-    const int tid = threadIdx.x - 64 - 128 * st;
+    const int tid = threadIdx.x - 64;
+    const int half = (warp - 2) >> 2;          // columns 64 half ... of a tile
     const int quad = warp & 3;
     const int row = quad * 32 + lane;
     const int rt = row / G;
@@ -802,58 +791,60 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, DqCfg<D>::CTAS)
       ndel = -p.delta[at];
     }
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    const uint32_t s_addr = lane_base + C::col_s(0) + 2 * KT * st;
-    const uint32_t dp_addr = s_addr + KT;
+    const uint32_t dp_addr = lane_base + C::COL_DP + 64 * half;
     const float2 cc = make_float2(p.scale_log2, p.scale_log2);
     const float2 nl = make_float2(nlse, nlse), nd = make_float2(ndel, ndel);
     bool ok = true;
-    for (int j = st, u = 0; j < n; j += NS, ++u) {
+    for (int j = 0; j < n; ++j) {
       const int j0 = k_lo + j * KT;
       // (rows that are not stored need no mask)
       const bool masked = j0 + KT > s.lk || (p.causal && j0 + KT - 1 > pos0) ||
                           (p.window > 0 && j0 + p.window <= pos0 + nt - 1);
-      const int lo = lo_r - j0, hi = hi_r - j0;
-      if (!wwait(&s_full[st], u & 1)) { ok = false; break; }
+      const int lo = lo_r - j0 - 64 * half, hi = hi_r - j0 - 64 * half;
+      const uint32_t s_addr = lane_base + C::COL_S + KT * (j & 1) + 64 * half;
+      if (!wwait(&s_full[j & 1], j >> 1 & 1)) { ok = false; break; }
       tc::fence_after_sync();
-      float v[KT / 32][32];
-#pragma unroll
-      for (int c = 0; c < KT / 32; ++c) tc::tmem_ld32(s_addr + 32 * c, v[c]);
+      float v[2][32], w[2][32];
+      tc::tmem_ld32(s_addr, v[0]);
+      tc::tmem_ld32(s_addr + 32, v[1]);
       tc::tmem_wait_ld();
 #pragma unroll
-      for (int c = 0; c < KT / 32; ++c)
+      for (int c = 0; c < 2; ++c)
 #pragma unroll
         for (int e = 0; e < 32; e += 2) weights2(v[c][e], v[c][e + 1], cc, nl);
       if (j0 + KT > s.lk) {
         // The keys end inside the tile: the rows behind them are another head's or sequence's,
         // whose NaN would pass through zero weights. (S(j), the other reader, is done.)
-        zero_rows<NSUB>(smem + C::OFF_K + (j % NST) * C::K_TILE, C::KSUB, s.lk - j0, KT, tid, 128);
+        zero_rows<NSUB>(smem + C::OFF_K + j % NK * C::K_TILE, C::KSUB, s.lk - j0, KT, tid, C::SOFT);
         tc::fence_proxy_async_smem();
       }
-      if (!wwait(&dp_full[st], u & 1)) { ok = false; break; }
+      if (!wwait(dp_full, j & 1)) { ok = false; break; }
       tc::fence_after_sync();
+      tc::tmem_ld32(dp_addr, w[0]);
+      tc::tmem_ld32(dp_addr + 32, w[1]);
+      tc::tmem_wait_ld();
+      tc::fence_before_sync();
+      mbar_arrive(dp_free);
 #pragma unroll
-      for (int c = 0; c < KT / 32; ++c) {
-        float w[32];
-        tc::tmem_ld32(dp_addr + 32 * c, w);
-        tc::tmem_wait_ld();
+      for (int c = 0; c < 2; ++c) {
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) scores2(w[e], w[e + 1], v[c][e], v[c][e + 1], nd);
+        for (int e = 0; e < 32; e += 2) scores2(w[c][e], w[c][e + 1], v[c][e], v[c][e + 1], nd);
         if (masked) {
 #pragma unroll
           for (int e = 0; e < 32; ++e)
-            if (c * 32 + e < lo || c * 32 + e >= hi) w[e] = 0.f;
+            if (c * 32 + e < lo || c * 32 + e >= hi) w[c][e] = 0.f;
         }
-        store_packed(s_addr + 16 * c, w);
+        store_packed(s_addr + 16 * c, w[c]);
       }
       tc::tmem_wait_st();
       tc::fence_before_sync();
-      mbar_arrive(&ds_full[st]);
+      mbar_arrive(&ds_full[j & 1]);
     }
     // ------------------------------------------------------------ epilogue
     if (ok) ok = wwait(all_done, 0);
     tc::fence_after_sync();
-    // stream s stores the 64-column block s
-    tc::store_o_rows<64>(lane_base + C::COL_DQ + 64 * st, !ok, p.sm_scale, p.dq + at * D + 64 * st,
+    // half h stores the 64-column block h
+    tc::store_o_rows<64>(lane_base + C::COL_DQ + 64 * half, !ok, p.sm_scale, p.dq + at * D + 64 * half,
                          valid, lane);
   }
 
@@ -863,8 +854,8 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, DqCfg<D>::CTAS)
   __syncthreads();
   if (warp == 0 && lane == 0 && *abort_flag) {
     mbar_drain(q_full, 0);
-    for (int i = max(0, issued_k - NST); i < issued_k; ++i) mbar_drain(&k_full[i % NST], (i / NST) & 1);
-    for (int i = max(0, issued_v - NST); i < issued_v; ++i) mbar_drain(&v_full[i % NST], (i / NST) & 1);
+    for (int i = max(0, issued_k - NK); i < issued_k; ++i) mbar_drain(&k_full[i % NK], i / NK & 1);
+    for (int i = max(0, issued_v - NV); i < issued_v; ++i) mbar_drain(&v_full[i % NV], i / NV & 1);
   }
   if (warp == 1) {
     tc::fence_after_sync();
@@ -898,7 +889,7 @@ int launch_back(BackParams& p, cudaStream_t stream) {
     set_error("too many work items");
     return SINKATTN_UNSUPPORTED;
   }
-  CUtensorMap tmQ, tmDo, tmQ2, tmDo2, tmK, tmV, tmK2, tmV2;
+  CUtensorMap tmQ, tmDo, tmK, tmV, tmK2, tmV2;
   const uint64_t kv_rows = static_cast<uint64_t>(p.Hkv) * p.total_k;
   const uint64_t q_rows = static_cast<uint64_t>(p.total_q);
   // (with no query rows nothing is copied through the maps of q and dout)
@@ -907,8 +898,6 @@ int launch_back(BackParams& p, cudaStream_t stream) {
   int rc;
   if ((rc = make_q_tmap(&tmQ, q, q_rows, p.Hq, D, p.G, p.QB)) ||
       (rc = make_q_tmap(&tmDo, dout, q_rows, p.Hq, D, p.G, p.QB)) ||
-      (rc = make_q_tmap(&tmQ2, q, q_rows, p.Hq, D, p.GT, p.QB2)) ||
-      (rc = make_q_tmap(&tmDo2, dout, q_rows, p.Hq, D, p.GT, p.QB2)) ||
       (rc = make_rows_tmap(&tmK, p.k, kv_rows, D, DQ::KT, 128)) ||
       (rc = make_rows_tmap(&tmV, p.v, kv_rows, D, DQ::KT, 128)) ||
       (rc = make_rows_tmap(&tmK2, p.k, kv_rows, D, 128, 128)) ||
@@ -924,7 +913,7 @@ int launch_back(BackParams& p, cudaStream_t stream) {
   }
   if (dkv_items > 0) {
     back_dkv_kernel<D><<<static_cast<unsigned>(dkv_items), KV::THREADS, KV::SMEM, stream>>>(
-        tmQ2, tmDo2, tmK2, tmV2, p);
+        tmQ, tmDo, tmK2, tmV2, p);
     if ((rc = launched("dk, dv"))) return rc;
   }
   if (dq_items > 0) {
@@ -966,9 +955,6 @@ int launch_prefill_back(const BackArgs& a, cudaStream_t stream) {
   p.dsinks = a.dsinks; p.delta = a.delta; p.sink_part = a.sink_part;
   p.per = back_block_tokens(a.total_q, a.Hq);
   p.delta_blocks = static_cast<int>(back_blocks(a.total_q, a.Hq));
-  p.chunks = p.G > 64 ? 2 : 1;
-  p.GT = (p.G + p.chunks - 1) / p.chunks;
-  p.QB2 = 64 / p.GT;
   return a.d == 64 ? launch_back<64>(p, stream) : launch_back<128>(p, stream);
 }
 
