@@ -162,6 +162,15 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return true;
 }
 
+// The same for two barriers: where both are done, which is the rule here, they
+// cost about as much as one (100 cycles each, one after the other).
+__device__ __forceinline__ bool warp_wait2(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb,
+                                           volatile int* abort_flag, int* status) {
+  const bool ra = mbar_try_wait(a, pa), rb = mbar_try_wait(b, pb);
+  if (__all_sync(0xffffffffu, ra && rb)) return true;
+  return warp_wait(a, pa, abort_flag, status) && warp_wait(b, pb, abort_flag, status);
+}
+
 // Zeros rows [from, to) of a tile of NSUB swizzled sub-tiles in shared memory.
 template <int NSUB>
 __device__ __forceinline__ void zero_rows(uint8_t* tile, int sub_bytes, int from, int to, int tid,
@@ -186,10 +195,10 @@ __device__ __forceinline__ void scores2(float& a, float& b, float p0, float p1, 
   b = x.y;
 }
 
-// The A operand of a TS product: bf16 pairs that replaced fp32 columns, each
-// 64 elements in the first 32 columns of their 64. K step kk covers elements 16 kk ...
-__device__ __forceinline__ uint32_t half_packed(uint32_t base, int kk) {
-  return base + static_cast<uint32_t>(8 * kk + (kk >= 4 ? 32 : 0));
+// The A operand of a TS product: bf16 pairs that replaced fp32 columns, each 32
+// elements in 16 of their 32 columns. K step kk covers elements 16 kk ...
+__device__ __forceinline__ uint32_t packed_step(uint32_t base, int kk) {
+  return base + static_cast<uint32_t>(32 * (kk >> 1) + 8 * (kk & 1));
 }
 
 // 32 fp32 columns as bf16 pairs into 16 columns.
@@ -202,8 +211,14 @@ __device__ __forceinline__ void store_packed(uint32_t addr, const float (&v)[32]
 
 // dK, dV. S^T = K Q^T and dP^T = V dO^T (M 128 keys, N 128 query rows, K d; all
 // from shared memory), dV += P^T dO and dK += dS^T Q (M 128 keys, N d, K 128; P^T
-// and dS^T from TMEM, where they replace S^T and dP^T). Keys in the TMEM lanes
-// make P^T and dS^T the MMA's A operand as they are.
+// and dS^T from TMEM). Keys in the TMEM lanes make P^T and dS^T the MMA's A
+// operand as they are.
+// At d 64 TMEM holds two S^T buffers. P^T and dS^T, computed in one step, both
+// replace S^T, dP^T is free as soon as it has been read, and the scores of the
+// next tile are there when a tile's weights are done (one step keeps the
+// exponentials' unit and the others busy at once). At d 128 there is one
+// buffer: P^T replaces S^T and dS^T replaces dP^T, so that the next S^T follows dV
+// while dS^T is computed, and the next dP^T follows dK.
 template <int D>
 struct DkvCfg {
   static constexpr int THREADS = 64 + 256;
@@ -236,15 +251,16 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
                     const BackParams p) {
   using C = DkvCfg<D>;
   constexpr int NQ = C::NQ, ND = C::ND, NSB = C::NSB, NSUB = C::NSUB;
+  constexpr bool kOneStep = NSB == 2;
   extern __shared__ __align__(1024) uint8_t smem[];   // (swizzled tiles start on 1024 bytes)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* kv_full = bars;
   uint64_t* q_full = kv_full + 1;      // [NQ]
   uint64_t* do_full = q_full + NQ;     // [ND]
   uint64_t* s_full = do_full + ND;     // [NSB] S^T written
-  uint64_t* p_full = s_full + NSB;     // [NSB] P^T written (256 arrivals)
+  uint64_t* p_full = s_full + NSB;     // [NSB] P^T, in one step dS^T too, written (256 arrivals)
   uint64_t* dp_full = p_full + NSB;    // dP^T written
-  uint64_t* ds_full = dp_full + 1;     // dS^T written (256 arrivals)
+  uint64_t* ds_full = dp_full + 1;     // dS^T written, or in one step dP^T read (256 arrivals)
   uint64_t* row_full = ds_full + 1;    // [2] the rows' lse and delta staged (256 arrivals)
   uint64_t* dv_done = row_full + 2;    // [2] of even and odd tiles
   uint64_t* dk_done = dv_done + 2;     // [2]
@@ -368,21 +384,28 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
     };
     if (n > 0 && wwait(kv_full, 0)) {
       for (int j = 0; j < n; ++j) {
-        // S^T(j) overwrites the P^T that dV(j - NSB) reads
-        if (!wwait(&q_full[j % NQ], j / NQ & 1) ||
-            (j >= NSB && !wwait(&dv_done[(j - NSB) & 1], ((j - NSB) >> 1) & 1))) break;
+        // S^T(j) overwrites the P^T that dV(j - NSB) reads, in one step also dK's dS^T
+        if (!wwait(&q_full[j % NQ], j / NQ & 1)) break;
+        if (j >= NSB) {
+          uint64_t* done = kOneStep ? dk_done : dv_done;
+          if (!wwait(&done[(j - NSB) & 1], (j - NSB) >> 1 & 1)) break;
+        }
         tc::fence_after_sync();
         ss(tmem + C::COL_S + 128 * (j % NSB), kd, qd + static_cast<uint64_t>(j % NQ) * (C::TILE >> 4),
            &s_full[j % NSB]);
-        // dP^T(j) overwrites the dS^T that dK(j - 1) reads, the last of that tile's products
+        // dP^T(j) overwrites dP^T(j - 1), or the dS^T that dK(j - 1) reads
         if (j >= 1) {
-          if (!wwait(&dk_done[(j - 1) & 1], ((j - 1) >> 1) & 1)) break;
-          if (j - 1 + NQ < n) load_q(j - 1 + NQ);
-          if (j - 1 + ND < n) load_do(j - 1 + ND);
+          if (!(kOneStep ? wwait(ds_full, (j - 1) & 1) : wwait(&dk_done[(j - 1) & 1], (j - 1) >> 1 & 1))) break;
         }
         if (!wwait(&do_full[j % ND], j / ND & 1)) break;
         tc::fence_after_sync();
         ss(tmem + C::COL_DP, vd, dod + static_cast<uint64_t>(j % ND) * (C::TILE >> 4), dp_full);
+        // dK of a tile is the last of its four products: its stages are free
+        const int f = kOneStep ? j - 2 : j - 1;
+        if (f >= 0) {
+          if (f + NQ < n) load_q(f + NQ);
+          if (f + ND < n) load_do(f + ND);
+        }
       }
     }
     // every MMA this warp issued has completed before the CTA frees TMEM
@@ -402,21 +425,23 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
       if (leader) {
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
-          tc::mma_ts(d_tm, half_packed(a, kk), bq + static_cast<uint64_t>(kk) * 128u, idesc_o,
+          tc::mma_ts(d_tm, packed_step(a, kk), bq + static_cast<uint64_t>(kk) * 128u, idesc_o,
                      first && kk == 0 ? 0u : 1u);
         tc::commit(bar);
       }
       __syncwarp();
     };
     for (int j = 0; j < n; ++j) {
+      const uint32_t pt = tmem + C::COL_S + 128 * (j % NSB);
       if (!wwait(&p_full[j % NSB], j / NSB & 1)) break;
       tc::fence_after_sync();
-      ts(tmem + C::COL_DV, tmem + C::COL_S + 128 * (j % NSB),
-         dot + static_cast<uint64_t>(j % ND) * (C::TILE >> 4), j == 0, &dv_done[j & 1]);
-      if (!wwait(ds_full, j & 1)) break;
-      tc::fence_after_sync();
-      ts(tmem + C::COL_DK, tmem + C::COL_DP, qt + static_cast<uint64_t>(j % NQ) * (C::TILE >> 4),
-         j == 0, &dk_done[j & 1]);
+      ts(tmem + C::COL_DV, pt, dot + static_cast<uint64_t>(j % ND) * (C::TILE >> 4), j == 0, &dv_done[j & 1]);
+      if (!kOneStep) {
+        if (!wwait(ds_full, j & 1)) break;
+        tc::fence_after_sync();
+      }
+      ts(tmem + C::COL_DK, kOneStep ? pt + 16 : tmem + C::COL_DP,
+         qt + static_cast<uint64_t>(j % NQ) * (C::TILE >> 4), j == 0, &dk_done[j & 1]);
     }
     if (leader) {
       tc::commit(all_done);
@@ -466,68 +491,103 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
         masked = masked || k0 + p.window < pos0 + p.QB;
         hi = max(0, min(nt, k0 + key + p.window - pos0)) * G - 64 * half;
       }
-      if (!wwait(&row_full[j & 1], j >> 1 & 1) || !wwait(&s_full[j % NSB], j / NSB & 1)) { ok = false; break; }
-      tc::fence_after_sync();
       const uint32_t s_addr = lane_base + C::COL_S + 128 * (j % NSB) + 64 * half;
       const uint32_t dp_addr = lane_base + C::COL_DP + 64 * half;
+      const uint32_t ds_addr = kOneStep ? s_addr + 16 : dp_addr;
       const float4* lse4 = reinterpret_cast<const float4*>(row_s + (j & 1) * 256 + 64 * half);
       const float4* del4 = lse4 + 32;
-      float v[2][32];
-      tc::tmem_ld32(s_addr, v[0]);
-      tc::tmem_ld32(s_addr + 32, v[1]);
-      tc::tmem_wait_ld();
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
+      if (!warp_wait2(&row_full[j & 1], j >> 1 & 1, &s_full[j % NSB], j / NSB & 1, abort_flag, status)) {
+        ok = false;
+        break;
+      }
+      if (kOneStep && !wwait(dp_full, j & 1)) { ok = false; break; }
+      tc::fence_after_sync();
+      auto weights = [&](float (&v)[32], int c) {   // P of columns 32 c ..
 #pragma unroll
         for (int e = 0; e < 32; e += 4) {
           const float4 l = lse4[c * 8 + e / 4];
-          weights2(v[c][e], v[c][e + 1], cc, make_float2(l.x, l.y));
-          weights2(v[c][e + 2], v[c][e + 3], cc, make_float2(l.z, l.w));
+          weights2(v[e], v[e + 1], cc, make_float2(l.x, l.y));
+          weights2(v[e + 2], v[e + 3], cc, make_float2(l.z, l.w));
         }
         if (masked) {
 #pragma unroll
           for (int e = 0; e < 32; ++e)
-            if (c * 32 + e < lo || c * 32 + e >= hi) v[c][e] = 0.f;
+            if (c * 32 + e < lo || c * 32 + e >= hi) v[e] = 0.f;
         }
-        store_packed(s_addr + 16 * c, v[c]);
-      }
-      if (nt < p.QB) {
-        // The visible rows end inside the tile: those behind them may be another
-        // sequence's, whose NaN would pass through zero weights. Both products
-        // that read the tile along d are done.
-        if (!wwait(dp_full, j & 1)) { ok = false; break; }
-        zero_rows<NSUB>(smem + C::OFF_Q + j % NQ * C::TILE, C::SUB, nt * G, 128, tid, 256);
-        zero_rows<NSUB>(smem + C::OFF_DO + j % ND * C::TILE, C::SUB, nt * G, 128, tid, 256);
-        tc::fence_proxy_async_smem();
-      }
-      tc::tmem_wait_st();
-      tc::fence_before_sync();
-      mbar_arrive(&p_full[j % NSB]);
-
-      if (!wwait(dp_full, j & 1)) { ok = false; break; }
-      tc::fence_after_sync();
-      float w[2][32];
-      tc::tmem_ld32(dp_addr, w[0]);
-      tc::tmem_ld32(dp_addr + 32, w[1]);
-      tc::tmem_wait_ld();
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
+      };
+      auto scores = [&](float (&w)[32], const float (&v)[32], int c) {   // their dS
 #pragma unroll
         for (int e = 0; e < 32; e += 4) {
           const float4 d = del4[c * 8 + e / 4];
-          scores2(w[c][e], w[c][e + 1], v[c][e], v[c][e + 1], make_float2(d.x, d.y));
-          scores2(w[c][e + 2], w[c][e + 3], v[c][e + 2], v[c][e + 3], make_float2(d.z, d.w));
+          scores2(w[e], w[e + 1], v[e], v[e + 1], make_float2(d.x, d.y));
+          scores2(w[e + 2], w[e + 3], v[e + 2], v[e + 3], make_float2(d.z, d.w));
         }
         if (masked) {   // (0 x NaN of another row is not 0)
 #pragma unroll
           for (int e = 0; e < 32; ++e)
-            if (c * 32 + e < lo || c * 32 + e >= hi) w[c][e] = 0.f;
+            if (c * 32 + e < lo || c * 32 + e >= hi) w[e] = 0.f;
         }
-        store_packed(dp_addr + 16 * c, w[c]);
+      };
+      // The sequence ends inside the tile: the rows behind it are another
+      // one's, whose NaN would pass through zero weights. Both products that
+      // read the tile along d are done.
+      auto zero_behind = [&]() {
+        if (nt == p.QB) return;
+        zero_rows<NSUB>(smem + C::OFF_Q + j % NQ * C::TILE, C::SUB, nt * G, 128, tid, 256);
+        zero_rows<NSUB>(smem + C::OFF_DO + j % ND * C::TILE, C::SUB, nt * G, 128, tid, 256);
+        tc::fence_proxy_async_smem();
+      };
+      if constexpr (kOneStep) {
+        zero_behind();
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float v[32], w[32];
+          tc::tmem_ld32(s_addr + 32 * c, v);
+          tc::tmem_ld32(dp_addr + 32 * c, w);
+          tc::tmem_wait_ld();
+          if (c == 1) {
+            tc::fence_before_sync();
+            mbar_arrive(ds_full);
+          }
+          weights(v, c);
+          scores(w, v, c);
+          store_packed(s_addr + 32 * c, v);
+          store_packed(ds_addr + 32 * c, w);
+        }
+        tc::tmem_wait_st();
+        tc::fence_before_sync();
+        mbar_arrive(&p_full[j % NSB]);
+      } else {
+        float v[2][32];
+        tc::tmem_ld32(s_addr, v[0]);
+        tc::tmem_ld32(s_addr + 32, v[1]);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          weights(v[c], c);
+          store_packed(s_addr + 32 * c, v[c]);
+        }
+        if (nt < p.QB) {
+          if (!wwait(dp_full, j & 1)) { ok = false; break; }
+          zero_behind();
+        }
+        tc::tmem_wait_st();
+        tc::fence_before_sync();
+        mbar_arrive(&p_full[j % NSB]);
+        if (!wwait(dp_full, j & 1)) { ok = false; break; }
+        tc::fence_after_sync();
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float w[32];
+          tc::tmem_ld32(dp_addr + 32 * c, w);
+          tc::tmem_wait_ld();
+          scores(w, v[c], c);
+          store_packed(ds_addr + 32 * c, w);
+        }
+        tc::tmem_wait_st();
+        tc::fence_before_sync();
+        mbar_arrive(ds_full);
       }
-      tc::tmem_wait_st();
-      tc::fence_before_sync();
-      mbar_arrive(ds_full);
       if (j + 1 < n) put(j + 1, next);
     }
     // ------------------------------------------------------------ epilogue
@@ -758,7 +818,7 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, DqCfg<D>::CTAS)
         const uint64_t bk = kt + static_cast<uint64_t>(j % NK) * (C::K_TILE >> 4);
 #pragma unroll
         for (int kk = 0; kk < KT / 16; ++kk)
-          tc::mma_ts(tmem + C::COL_DQ, half_packed(tmem + C::COL_S + KT * (j & 1), kk),
+          tc::mma_ts(tmem + C::COL_DQ, packed_step(tmem + C::COL_S + KT * (j & 1), kk),
                      bk + static_cast<uint64_t>(kk) * 128u, idesc_o, j == 0 && kk == 0 ? 0u : 1u);
         tc::commit(&dq_done[j & 1]);
       }
@@ -802,39 +862,35 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, DqCfg<D>::CTAS)
                           (p.window > 0 && j0 + p.window <= pos0 + nt - 1);
       const int lo = lo_r - j0 - 64 * half, hi = hi_r - j0 - 64 * half;
       const uint32_t s_addr = lane_base + C::COL_S + KT * (j & 1) + 64 * half;
-      if (!wwait(&s_full[j & 1], j >> 1 & 1)) { ok = false; break; }
+      if (!warp_wait2(&s_full[j & 1], j >> 1 & 1, dp_full, j & 1, abort_flag, status)) { ok = false; break; }
       tc::fence_after_sync();
-      float v[2][32], w[2][32];
-      tc::tmem_ld32(s_addr, v[0]);
-      tc::tmem_ld32(s_addr + 32, v[1]);
-      tc::tmem_wait_ld();
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
-#pragma unroll
-        for (int e = 0; e < 32; e += 2) weights2(v[c][e], v[c][e + 1], cc, nl);
       if (j0 + KT > s.lk) {
         // The keys end inside the tile: the rows behind them are another head's or sequence's,
         // whose NaN would pass through zero weights. (S(j), the other reader, is done.)
         zero_rows<NSUB>(smem + C::OFF_K + j % NK * C::K_TILE, C::KSUB, s.lk - j0, KT, tid, C::SOFT);
         tc::fence_proxy_async_smem();
       }
-      if (!wwait(dp_full, j & 1)) { ok = false; break; }
-      tc::fence_after_sync();
-      tc::tmem_ld32(dp_addr, w[0]);
-      tc::tmem_ld32(dp_addr + 32, w[1]);
-      tc::tmem_wait_ld();
-      tc::fence_before_sync();
-      mbar_arrive(dp_free);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
+        float v[32], w[32];
+        tc::tmem_ld32(s_addr + 32 * c, v);
+        tc::tmem_ld32(dp_addr + 32 * c, w);
+        tc::tmem_wait_ld();
+        if (c == 1) {
+          tc::fence_before_sync();
+          mbar_arrive(dp_free);
+        }
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) scores2(w[c][e], w[c][e + 1], v[c][e], v[c][e + 1], nd);
+        for (int e = 0; e < 32; e += 2) {
+          weights2(v[e], v[e + 1], cc, nl);
+          scores2(w[e], w[e + 1], v[e], v[e + 1], nd);
+        }
         if (masked) {
 #pragma unroll
           for (int e = 0; e < 32; ++e)
-            if (c * 32 + e < lo || c * 32 + e >= hi) w[c][e] = 0.f;
+            if (c * 32 + e < lo || c * 32 + e >= hi) w[e] = 0.f;
         }
-        store_packed(s_addr + 16 * c, w[c]);
+        store_packed(s_addr + 32 * c, w);
       }
       tc::tmem_wait_st();
       tc::fence_before_sync();
