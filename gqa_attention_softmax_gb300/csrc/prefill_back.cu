@@ -12,9 +12,11 @@
 // no fp32 buffer of dq in memory, and the group's heads add up in the
 // accumulators.
 //
-// Both kernels: warp 0 stages tiles by TMA and issues the products that make S
-// and dP, warp 1 those that take P and dS, warps 2 .. compute P and dS, one
-// thread per TMEM lane and 64 columns.
+// Both kernels: warp 0 stages tiles by TMA, warp 1 issues the product that makes
+// S, warp 2 that of dP, warp 3 those that take P and dS, and the others compute
+// these, one thread per TMEM lane and 64 columns. An issuing warp's wait that is already over, its
+// MMAs and its commits take 100 to 250 cycles each, one after the other: one
+// warp for all products needed 2000 a tile pair, twice what the tensor core does.
 // P and dS are rounded to bf16 for the products that take them; P enters dS
 // unrounded. Every wait is bounded; on a timeout the CTA records
 // SINKATTN_TIMEOUT, drains its copies and MMAs, frees TMEM and exits.
@@ -144,14 +146,18 @@ __device__ __forceinline__ Seq load_seq(const BackParams& p, int b) {
 }
 
 // ---------------------------------------------------------------------------
-// A warp's bounded wait (mbar_wait by all lanes, as one uniform branch: the
-// lanes leave together, so the warp-collective TMEM accesses that follow never
-// run with some of them missing).
+// A warp's bounded wait, as one uniform branch: the lanes leave together, so the
+// warp-collective TMEM accesses that follow never run with some of them missing.
+// The time and the abort flag are looked at every 64th time only: reading the
+// limit from memory each time kept a waiting warp about 600 cycles from seeing
+// that its wait was over.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                           int* status) {
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   const long long t0 = clock64();
-  while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
+  while (true) {
+    for (int i = 0; i < 64; ++i)
+      if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
     if (__any_sync(0xffffffffu, *abort_flag)) return false;
     if (__any_sync(0xffffffffu, clock64() - t0 > g_wait_limit_cycles)) {
       *abort_flag = 1;
@@ -159,16 +165,23 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
       return false;
     }
   }
-  return true;
 }
 
-// The same for two barriers: where both are done, which is the rule here, they
-// cost about as much as one (100 cycles each, one after the other).
+// The same for two or three barriers: where all are done, which is the rule here,
+// they cost about as much as one.
 __device__ __forceinline__ bool warp_wait2(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb,
                                            volatile int* abort_flag, int* status) {
   const bool ra = mbar_try_wait(a, pa), rb = mbar_try_wait(b, pb);
   if (__all_sync(0xffffffffu, ra && rb)) return true;
   return warp_wait(a, pa, abort_flag, status) && warp_wait(b, pb, abort_flag, status);
+}
+__device__ __forceinline__ bool warp_wait3(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb,
+                                           uint64_t* c, uint32_t pc, volatile int* abort_flag,
+                                           int* status) {
+  const bool ra = mbar_try_wait(a, pa), rb = mbar_try_wait(b, pb), rc = mbar_try_wait(c, pc);
+  if (__all_sync(0xffffffffu, ra && rb && rc)) return true;
+  return warp_wait(a, pa, abort_flag, status) && warp_wait(b, pb, abort_flag, status) &&
+         warp_wait(c, pc, abort_flag, status);
 }
 
 // Zeros rows [from, to) of a tile of NSUB swizzled sub-tiles in shared memory.
@@ -201,6 +214,28 @@ __device__ __forceinline__ uint32_t packed_step(uint32_t base, int kk) {
   return base + static_cast<uint32_t>(32 * (kk >> 1) + 8 * (kk & 1));
 }
 
+// The products, by one lane of a warp. ss: D = A B^T over d, both in shared memory
+// and K-major, in 64-column sub-tiles of a_sub and b_sub bytes. ts: D += A B over
+// STEPS steps of 16 rows of B; A in TMEM (packed_step), B MN-major.
+template <int D, int N>
+__device__ __forceinline__ void issue_ss(bool leader, uint32_t d_tm, uint64_t a, uint64_t b, int a_sub,
+                                         int b_sub) {
+  if (!leader) return;
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk)
+    tc::mma_ss(d_tm, a + static_cast<uint64_t>(kk >> 2) * (a_sub >> 4) + (kk & 3) * 2,
+               b + static_cast<uint64_t>(kk >> 2) * (b_sub >> 4) + (kk & 3) * 2,
+               tc::idesc_bf16_f32(128, N, false), kk > 0 ? 1u : 0u);
+}
+template <int D, int STEPS>
+__device__ __forceinline__ void issue_ts(bool leader, uint32_t d_tm, uint32_t a, uint64_t b, bool first) {
+  if (!leader) return;
+#pragma unroll
+  for (int kk = 0; kk < STEPS; ++kk)
+    tc::mma_ts(d_tm, packed_step(a, kk), b + static_cast<uint64_t>(kk) * 128u,
+               tc::idesc_bf16_f32(128, D, true), first && kk == 0 ? 0u : 1u);
+}
+
 // 32 fp32 columns as bf16 pairs into 16 columns.
 __device__ __forceinline__ void store_packed(uint32_t addr, const float (&v)[32]) {
   uint32_t pk[16];
@@ -221,7 +256,9 @@ __device__ __forceinline__ void store_packed(uint32_t addr, const float (&v)[32]
 // while dS^T is computed, and the next dP^T follows dK.
 template <int D>
 struct DkvCfg {
-  static constexpr int THREADS = 64 + 256;
+  static constexpr int SOFT0 = 4;                   // first warp of P and dS
+  static constexpr int SOFT = 256;                  // their threads
+  static constexpr int THREADS = SOFT0 * 32 + SOFT;
   static constexpr int NSUB = D / 64;
   static constexpr int SUB = 128 * 128;             // [128 rows][64 bf16], 128B-swizzled
   static constexpr int TILE = NSUB * SUB;
@@ -234,7 +271,7 @@ struct DkvCfg {
   static constexpr int OFF_DO = OFF_Q + NQ * TILE;
   static constexpr int OFF_ROW = OFF_DO + ND * TILE;   // [2][-lse log2 e, -delta][128]
   static constexpr int OFF_BAR = OFF_ROW + 2 * 2 * 128 * 4;
-  static constexpr int N_BARS = 1 + NQ + ND + 2 * NSB + 2 + 2 + 2 + 2 + 1 + 2;
+  static constexpr int N_BARS = 1 + 2 * NQ + 2 * ND + 3 * NSB + 3 + 2 + 1 + 3;
   static constexpr int SMEM = OFF_BAR + N_BARS * 8 + 16;
   static constexpr uint32_t COL_S = 0;
   static constexpr uint32_t COL_DP = 128 * NSB;
@@ -256,17 +293,19 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* kv_full = bars;
   uint64_t* q_full = kv_full + 1;      // [NQ]
-  uint64_t* do_full = q_full + NQ;     // [ND]
-  uint64_t* s_full = do_full + ND;     // [NSB] S^T written
-  uint64_t* p_full = s_full + NSB;     // [NSB] P^T, in one step dS^T too, written (256 arrivals)
+  uint64_t* q_empty = q_full + NQ;     // [NQ] dK, the last that reads the stage, done
+  uint64_t* do_full = q_empty + NQ;    // [ND]
+  uint64_t* do_empty = do_full + ND;   // [ND] dP^T and dV done
+  uint64_t* s_full = do_empty + ND;    // [NSB] S^T written
+  uint64_t* s_free = s_full + NSB;     // [NSB] the P^T (in one step and dS^T) in it read
+  uint64_t* p_full = s_free + NSB;     // [NSB] P^T (in one step and dS^T) written (256 arrivals)
   uint64_t* dp_full = p_full + NSB;    // dP^T written
-  uint64_t* ds_full = dp_full + 1;     // dS^T written, or in one step dP^T read (256 arrivals)
+  uint64_t* dp_free = dp_full + 1;     // dP^T read (256 arrivals), or the dS^T in its place (by dK)
+  uint64_t* ds_full = dp_free + 1;     // dS^T written (256 arrivals; not in one step)
   uint64_t* row_full = ds_full + 1;    // [2] the rows' lse and delta staged (256 arrivals)
-  uint64_t* dv_done = row_full + 2;    // [2] of even and odd tiles
-  uint64_t* dk_done = dv_done + 2;     // [2]
-  uint64_t* all_done = dk_done + 2;    // every product
-  uint64_t* drain = all_done + 1;      // [2]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
+  uint64_t* all_done = row_full + 2;   // dV and dK
+  uint64_t* drain = all_done + 1;      // [3]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 3);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
   int* status = &g_status_prefill_back;
   const int warp = threadIdx.x >> 5;
@@ -294,21 +333,25 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
 
   if (threadIdx.x == 0) {
     mbar_init(kv_full, 1);
-    for (int i = 0; i < NQ; ++i) mbar_init(&q_full[i], 1);
-    for (int i = 0; i < ND; ++i) mbar_init(&do_full[i], 1);
+    for (int i = 0; i < NQ; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 1);
+    }
+    for (int i = 0; i < ND; ++i) {
+      mbar_init(&do_full[i], 1);
+      mbar_init(&do_empty[i], 2);
+    }
     for (int i = 0; i < NSB; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 256);
+      mbar_init(&s_free[i], 1);
+      mbar_init(&p_full[i], C::SOFT);
     }
     mbar_init(dp_full, 1);
-    mbar_init(ds_full, 256);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&row_full[i], 256);
-      mbar_init(&dv_done[i], 1);
-      mbar_init(&dk_done[i], 1);
-      mbar_init(&drain[i], 1);
-    }
+    mbar_init(dp_free, kOneStep ? C::SOFT : 1);
+    mbar_init(ds_full, C::SOFT);
+    for (int i = 0; i < 2; ++i) mbar_init(&row_full[i], C::SOFT);
     mbar_init(all_done, 1);
+    for (int i = 0; i < 3; ++i) mbar_init(&drain[i], 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -329,10 +372,20 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
   auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
     return warp_wait(bar, parity, abort_flag, status);
   };
+  auto wwait2 = [&](uint64_t* x, uint32_t px, uint64_t* y, uint32_t py) -> bool {
+    return warp_wait2(x, px, y, py, abort_flag, status);
+  };
+  const bool leader = tc::elect_one();
+  // an issuing warp's end: every MMA of it has completed before the CTA frees TMEM
+  auto finish = [&](uint64_t* bar) {
+    if (leader) tc::commit(bar);
+    __syncwarp();
+    mbar_drain(bar, 0);
+  };
+  const uint32_t tile16 = C::TILE >> 4;   // a stage, in descriptor units
 
   if (warp == 0) {
-    // ------------------------------------------ copies; S^T = K Q^T and dP^T = V dO^T
-    const bool leader = tc::elect_one();
+    // ---------------------------------------------------------------- copies
     const int skip_tile = hook_skip_tile();
     auto load = [&](const CUtensorMap* map, int j, uint8_t* to, uint64_t* bar) {   // into a free stage
       if (j != skip_tile && leader) {   // test hook: the waits for this tile run out
@@ -343,116 +396,97 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
       }
       __syncwarp();
     };
-    auto load_q = [&](int j) {
-      issued_q = j + 1;
-      load(&tmQ, j, smem + C::OFF_Q + j % NQ * C::TILE, &q_full[j % NQ]);
-    };
-    auto load_do = [&](int j) {
-      issued_do = j + 1;
-      load(&tmDo, j, smem + C::OFF_DO + j % ND * C::TILE, &do_full[j % ND]);
-    };
-    if (n > 0) {
-      if (leader) {
-        mbar_arrive_expect_tx(kv_full, 2 * C::TILE);
-        const int slab = p.Hkv * s.k0 + kvh * s.lk + k0;
+    if (n > 0 && leader) {
+      mbar_arrive_expect_tx(kv_full, 2 * C::TILE);
+      const int slab = p.Hkv * s.k0 + kvh * s.lk + k0;
 #pragma unroll
-        for (int sub = 0; sub < NSUB; ++sub) {
-          tma_load_2d(smem + C::OFF_K + sub * C::SUB, &tmK, sub * 64, slab, kv_full);
-          tma_load_2d(smem + C::OFF_V + sub * C::SUB, &tmV, sub * 64, slab, kv_full);
-        }
+      for (int sub = 0; sub < NSUB; ++sub) {
+        tma_load_2d(smem + C::OFF_K + sub * C::SUB, &tmK, sub * 64, slab, kv_full);
+        tma_load_2d(smem + C::OFF_V + sub * C::SUB, &tmV, sub * 64, slab, kv_full);
       }
-      __syncwarp();
-      for (int j = 0; j < min(NQ, n); ++j) load_q(j);
-      for (int j = 0; j < min(ND, n); ++j) load_do(j);
     }
-    constexpr uint32_t idesc_s = tc::idesc_bf16_f32(128, 128, false);
+    __syncwarp();
+    // tile x's dO is wanted after its Q, and its stage is free before
+    for (int x = 0; x < n; ++x) {
+      if (x >= NQ && !wwait(&q_empty[x % NQ], (x / NQ - 1) & 1)) break;
+      issued_q = x + 1;
+      load(&tmQ, x, smem + C::OFF_Q + x % NQ * C::TILE, &q_full[x % NQ]);
+      // dO lags by the stages that Q has more
+      const int y = x - (NQ - ND);
+      if (y < 0) continue;
+      if (y >= ND && !wwait(&do_empty[y % ND], (y / ND - 1) & 1)) break;
+      issued_do = y + 1;
+      load(&tmDo, y, smem + C::OFF_DO + y % ND * C::TILE, &do_full[y % ND]);
+    }
+    for (int y = max(0, n - (NQ - ND)); y < n; ++y) {
+      if (y >= ND && !wwait(&do_empty[y % ND], (y / ND - 1) & 1)) break;
+      issued_do = y + 1;
+      load(&tmDo, y, smem + C::OFF_DO + y % ND * C::TILE, &do_full[y % ND]);
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- S^T = K Q^T
     const uint64_t kd = tc::smem_desc_sw128(smem_u32(smem + C::OFF_K), 16, 1024);
-    const uint64_t vd = tc::smem_desc_sw128(smem_u32(smem + C::OFF_V), 16, 1024);
     const uint64_t qd = tc::smem_desc_sw128(smem_u32(smem + C::OFF_Q), 16, 1024);
-    const uint64_t dod = tc::smem_desc_sw128(smem_u32(smem + C::OFF_DO), 16, 1024);
-    // D = A B^T over d; both K-major
-    auto ss = [&](uint32_t d_tm, uint64_t a, uint64_t bq, uint64_t* bar) {
-      if (leader) {
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint64_t at = static_cast<uint64_t>(kk >> 2) * (C::SUB >> 4) + (kk & 3) * 2;
-          tc::mma_ss(d_tm, a + at, bq + at, idesc_s, kk > 0 ? 1u : 0u);
-        }
-        tc::commit(bar);
-      }
-      __syncwarp();
-    };
     if (n > 0 && wwait(kv_full, 0)) {
       for (int j = 0; j < n; ++j) {
-        // S^T(j) overwrites the P^T that dV(j - NSB) reads, in one step also dK's dS^T
-        if (!wwait(&q_full[j % NQ], j / NQ & 1)) break;
-        if (j >= NSB) {
-          uint64_t* done = kOneStep ? dk_done : dv_done;
-          if (!wwait(&done[(j - NSB) & 1], (j - NSB) >> 1 & 1)) break;
-        }
+        if (j < NSB ? !wwait(&q_full[j % NQ], 0)
+                    : !wwait2(&s_free[j % NSB], (j / NSB - 1) & 1, &q_full[j % NQ], j / NQ & 1)) break;
         tc::fence_after_sync();
-        ss(tmem + C::COL_S + 128 * (j % NSB), kd, qd + static_cast<uint64_t>(j % NQ) * (C::TILE >> 4),
-           &s_full[j % NSB]);
-        // dP^T(j) overwrites dP^T(j - 1), or the dS^T that dK(j - 1) reads
-        if (j >= 1) {
-          if (!(kOneStep ? wwait(ds_full, (j - 1) & 1) : wwait(&dk_done[(j - 1) & 1], (j - 1) >> 1 & 1))) break;
-        }
-        if (!wwait(&do_full[j % ND], j / ND & 1)) break;
-        tc::fence_after_sync();
-        ss(tmem + C::COL_DP, vd, dod + static_cast<uint64_t>(j % ND) * (C::TILE >> 4), dp_full);
-        // dK of a tile is the last of its four products: its stages are free
-        const int f = kOneStep ? j - 2 : j - 1;
-        if (f >= 0) {
-          if (f + NQ < n) load_q(f + NQ);
-          if (f + ND < n) load_do(f + ND);
-        }
+        issue_ss<D, 128>(leader, tmem + C::COL_S + 128 * (j % NSB), kd, qd + j % NQ * tile16, C::SUB, C::SUB);
+        if (leader) tc::commit(&s_full[j % NSB]);
+        __syncwarp();
       }
     }
-    // every MMA this warp issued has completed before the CTA frees TMEM
-    if (leader) tc::commit(&drain[0]);
-    __syncwarp();
-    mbar_drain(&drain[0], 0);
-  } else if (warp == 1) {
-    // ------------------------------------------ dV += P^T dO and dK += dS^T Q
-    // (a warp of its own: an issuer that waits for the weights of one tile would
-    // leave the tensor core without the next tile's scores)
-    const bool leader = tc::elect_one();
-    constexpr uint32_t idesc_o = tc::idesc_bf16_f32(128, D, true);
-    const uint64_t qt = tc::smem_desc_sw128(smem_u32(smem + C::OFF_Q), C::SUB, 1024);   // MN-major
-    const uint64_t dot = tc::smem_desc_sw128(smem_u32(smem + C::OFF_DO), C::SUB, 1024);
-    // D += A B over the tile's rows; A in TMEM
-    auto ts = [&](uint32_t d_tm, uint32_t a, uint64_t bq, bool first, uint64_t* bar) {
-      if (leader) {
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          tc::mma_ts(d_tm, packed_step(a, kk), bq + static_cast<uint64_t>(kk) * 128u, idesc_o,
-                     first && kk == 0 ? 0u : 1u);
-        tc::commit(bar);
+    finish(&drain[0]);
+  } else if (warp == 2) {
+    // ---------------------------------------------------------------- dP^T = V dO^T
+    const uint64_t vd = tc::smem_desc_sw128(smem_u32(smem + C::OFF_V), 16, 1024);
+    const uint64_t dod = tc::smem_desc_sw128(smem_u32(smem + C::OFF_DO), 16, 1024);
+    if (n > 0 && wwait(kv_full, 0)) {
+      for (int j = 0; j < n; ++j) {
+        if (j == 0 ? !wwait(&do_full[0], 0)
+                   : !wwait2(dp_free, (j - 1) & 1, &do_full[j % ND], j / ND & 1)) break;
+        tc::fence_after_sync();
+        issue_ss<D, 128>(leader, tmem + C::COL_DP, vd, dod + j % ND * tile16, C::SUB, C::SUB);
+        if (leader) {
+          tc::commit(dp_full);
+          tc::commit(&do_empty[j % ND]);
+        }
+        __syncwarp();
       }
-      __syncwarp();
-    };
+    }
+    finish(&drain[1]);
+  } else if (warp == 3) {
+    // ------------------------------------------ dV += P^T dO and dK += dS^T Q
+    const uint64_t dot = tc::smem_desc_sw128(smem_u32(smem + C::OFF_DO), C::SUB, 1024);   // MN-major
+    const uint64_t qt = tc::smem_desc_sw128(smem_u32(smem + C::OFF_Q), C::SUB, 1024);
     for (int j = 0; j < n; ++j) {
       const uint32_t pt = tmem + C::COL_S + 128 * (j % NSB);
       if (!wwait(&p_full[j % NSB], j / NSB & 1)) break;
       tc::fence_after_sync();
-      ts(tmem + C::COL_DV, pt, dot + static_cast<uint64_t>(j % ND) * (C::TILE >> 4), j == 0, &dv_done[j & 1]);
+      issue_ts<D, 8>(leader, tmem + C::COL_DV, pt, dot + j % ND * tile16, j == 0);
+      if (leader) {
+        if (!kOneStep) tc::commit(&s_free[0]);
+        tc::commit(&do_empty[j % ND]);
+      }
+      __syncwarp();
       if (!kOneStep) {
         if (!wwait(ds_full, j & 1)) break;
         tc::fence_after_sync();
       }
-      ts(tmem + C::COL_DK, kOneStep ? pt + 16 : tmem + C::COL_DP,
-         qt + static_cast<uint64_t>(j % NQ) * (C::TILE >> 4), j == 0, &dk_done[j & 1]);
+      issue_ts<D, 8>(leader, tmem + C::COL_DK, kOneStep ? pt + 16 : tmem + C::COL_DP, qt + j % NQ * tile16, j == 0);
+      if (leader) {
+        tc::commit(kOneStep ? &s_free[j % NSB] : dp_free);
+        tc::commit(&q_empty[j % NQ]);
+      }
+      __syncwarp();
     }
-    if (leader) {
-      tc::commit(all_done);
-      tc::commit(&drain[1]);
-    }
-    __syncwarp();
-    mbar_drain(&drain[1], 0);
+    if (leader) tc::commit(all_done);
+    finish(&drain[2]);
   } else {
     // ---------------------------------------------------------------- P and dS
-    const int tid = threadIdx.x - 64;
-    const int half = (warp - 2) >> 2;          // columns 64 half ...
+    const int tid = threadIdx.x - 32 * C::SOFT0;
+    const int half = tid >> 7;                 // columns 64 half ...
     const int quad = warp & 3;                 // TMEM lane quadrant this warp may access
     const int key = quad * 32 + lane;          // key of the tile
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
@@ -471,37 +505,45 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
       row_s[(j & 1) * 256 + tid] = tid >= 128 ? -x : x == kNegInf ? kNegInf : -x * kLog2e;
       mbar_arrive(&row_full[j & 1]);
     };
+    // every key of the tile sees every row of tiles [j_lo, j_hi)
+    int j_lo = 0, j_hi = (i1 - i0) % p.QB ? n - 1 : n;
+    if (p.causal) j_lo = max(0, (k0 + 127 - off - i0 + p.QB - 1) / p.QB);
+    if (p.window > 0) j_hi = min(j_hi, (k0 + p.window - off - i0) / p.QB);
     const float2 cc = make_float2(p.scale_log2, p.scale_log2);
+    const uint32_t dp_addr = lane_base + C::COL_DP + 64 * half;
     bool ok = true;
     if (n > 0) put(0, fetch(0));
     for (int j = 0; j < n; ++j) {
       float next = 0.f;
       if (j + 1 < n) next = fetch(j + 1);
-      const int t0 = i0 + j * p.QB;              // first query of the tile
-      const int nt = min(p.QB, i1 - t0);
-      const int pos0 = off + t0;
-      // columns [lo, hi) of this thread's 64 are visible to the key
-      int lo = -64 * half, hi = lo + nt * G;
-      bool masked = nt < p.QB;   // (the rows past rows are zeros of weight 0)
-      if (p.causal) {
-        masked = masked || k0 + 127 > pos0;
-        lo += max(0, min(nt, k0 + key - pos0)) * G;
-      }
-      if (p.window > 0) {
-        masked = masked || k0 + p.window < pos0 + p.QB;
-        hi = max(0, min(nt, k0 + key + p.window - pos0)) * G - 64 * half;
+      const bool masked = j < j_lo || j >= j_hi;
+      int lo = -128, hi = 128, nt = p.QB;        // this thread's visible columns
+      if (masked) {
+        const int t0 = i0 + j * p.QB;            // first query of the tile
+        const int pos0 = off + t0;
+        nt = min(p.QB, i1 - t0);
+        lo = (p.causal ? max(0, min(nt, k0 + key - pos0)) * G : 0) - 64 * half;
+        hi = (p.window > 0 ? max(0, min(nt, k0 + key + p.window - pos0)) : nt) * G - 64 * half;
       }
       const uint32_t s_addr = lane_base + C::COL_S + 128 * (j % NSB) + 64 * half;
-      const uint32_t dp_addr = lane_base + C::COL_DP + 64 * half;
-      const uint32_t ds_addr = kOneStep ? s_addr + 16 : dp_addr;
       const float4* lse4 = reinterpret_cast<const float4*>(row_s + (j & 1) * 256 + 64 * half);
       const float4* del4 = lse4 + 32;
-      if (!warp_wait2(&row_full[j & 1], j >> 1 & 1, &s_full[j % NSB], j / NSB & 1, abort_flag, status)) {
+      if (kOneStep ? !warp_wait3(&row_full[j & 1], j >> 1 & 1, &s_full[j % NSB], j / NSB & 1, dp_full, j & 1,
+                                 abort_flag, status)
+                   : !wwait2(&row_full[j & 1], j >> 1 & 1, &s_full[0], j & 1)) {
         ok = false;
         break;
       }
-      if (kOneStep && !wwait(dp_full, j & 1)) { ok = false; break; }
       tc::fence_after_sync();
+      if (nt < p.QB) {
+        // The visible rows end inside the tile: those behind them may be another
+        // sequence's, whose NaN would pass through zero weights. Both products
+        // that read the tile along d have to be done.
+        if (!kOneStep && !wwait(dp_full, j & 1)) { ok = false; break; }
+        zero_rows<NSUB>(smem + C::OFF_Q + j % NQ * C::TILE, C::SUB, nt * G, 128, tid, C::SOFT);
+        zero_rows<NSUB>(smem + C::OFF_DO + j % ND * C::TILE, C::SUB, nt * G, 128, tid, C::SOFT);
+        tc::fence_proxy_async_smem();
+      }
       auto weights = [&](float (&v)[32], int c) {   // P of columns 32 c ..
 #pragma unroll
         for (int e = 0; e < 32; e += 4) {
@@ -528,17 +570,7 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
             if (c * 32 + e < lo || c * 32 + e >= hi) w[e] = 0.f;
         }
       };
-      // The sequence ends inside the tile: the rows behind it are another
-      // one's, whose NaN would pass through zero weights. Both products that
-      // read the tile along d are done.
-      auto zero_behind = [&]() {
-        if (nt == p.QB) return;
-        zero_rows<NSUB>(smem + C::OFF_Q + j % NQ * C::TILE, C::SUB, nt * G, 128, tid, 256);
-        zero_rows<NSUB>(smem + C::OFF_DO + j % ND * C::TILE, C::SUB, nt * G, 128, tid, 256);
-        tc::fence_proxy_async_smem();
-      };
       if constexpr (kOneStep) {
-        zero_behind();
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           float v[32], w[32];
@@ -547,16 +579,13 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
           tc::tmem_wait_ld();
           if (c == 1) {
             tc::fence_before_sync();
-            mbar_arrive(ds_full);
+            mbar_arrive(dp_free);   // the next tile's dP^T may come
           }
           weights(v, c);
           scores(w, v, c);
           store_packed(s_addr + 32 * c, v);
-          store_packed(ds_addr + 32 * c, w);
+          store_packed(s_addr + 32 * c + 16, w);
         }
-        tc::tmem_wait_st();
-        tc::fence_before_sync();
-        mbar_arrive(&p_full[j % NSB]);
       } else {
         float v[2][32];
         tc::tmem_ld32(s_addr, v[0]);
@@ -567,13 +596,9 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
           weights(v[c], c);
           store_packed(s_addr + 32 * c, v[c]);
         }
-        if (nt < p.QB) {
-          if (!wwait(dp_full, j & 1)) { ok = false; break; }
-          zero_behind();
-        }
         tc::tmem_wait_st();
         tc::fence_before_sync();
-        mbar_arrive(&p_full[j % NSB]);
+        mbar_arrive(&p_full[0]);
         if (!wwait(dp_full, j & 1)) { ok = false; break; }
         tc::fence_after_sync();
 #pragma unroll
@@ -582,12 +607,12 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
           tc::tmem_ld32(dp_addr + 32 * c, w);
           tc::tmem_wait_ld();
           scores(w, v[c], c);
-          store_packed(ds_addr + 32 * c, w);
+          store_packed(dp_addr + 32 * c, w);
         }
-        tc::tmem_wait_st();
-        tc::fence_before_sync();
-        mbar_arrive(ds_full);
       }
+      tc::tmem_wait_st();
+      tc::fence_before_sync();
+      mbar_arrive(kOneStep ? &p_full[j % NSB] : ds_full);
       if (j + 1 < n) put(j + 1, next);
     }
     // ------------------------------------------------------------ epilogue
@@ -625,22 +650,22 @@ template <int D>
 struct DqCfg {
   static constexpr int CTAS = D == 64 ? 2 : 1;      // CTAs of an SM
   static constexpr int KT = D;                      // keys of a tile
-  static constexpr int HALVES = KT / 64;            // warpgroups that share a tile's columns
-  static constexpr int SOFT = 128 * HALVES;
-  static constexpr int THREADS = 64 + SOFT;
+  static constexpr int SOFT0 = 4;                   // first warp of dS
+  static constexpr int SOFT = 2 * KT;               // their threads
+  static constexpr int THREADS = SOFT0 * 32 + SOFT;
   static constexpr int NSUB = D / 64;
   static constexpr int KSUB = KT * 128;
   static constexpr int QSUB = 128 * 128;
   static constexpr int K_TILE = NSUB * KSUB;
   static constexpr int Q_TILE = NSUB * QSUB;
-  static constexpr int NK = D == 64 ? 4 : 3;        // stages of K
+  static constexpr int NK = D == 64 ? 5 : 3;        // stages of K
   static constexpr int NV = D == 64 ? 4 : 2;        // stages of V, which one product reads
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_DO = Q_TILE;
   static constexpr int OFF_K = 2 * Q_TILE;
   static constexpr int OFF_V = OFF_K + NK * K_TILE;
   static constexpr int OFF_BAR = OFF_V + NV * K_TILE;
-  static constexpr int N_BARS = 1 + NK + NV + 2 + 2 + 1 + 1 + 2 + 1 + 2;
+  static constexpr int N_BARS = 1 + 2 * NK + 2 * NV + 2 + 2 + 2 + 1 + 1 + 1 + 3;
   static constexpr int SMEM = 1024 + OFF_BAR + N_BARS * 8 + 16;
   static constexpr uint32_t COLS = 512 / CTAS;
   static constexpr uint32_t COL_S = 0;
@@ -667,15 +692,17 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, DqCfg<D>::CTAS)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* q_full = bars;
   uint64_t* k_full = q_full + 1;       // [NK]
-  uint64_t* v_full = k_full + NK;      // [NV]
-  uint64_t* s_full = v_full + NV;      // [2] S written
-  uint64_t* ds_full = s_full + 2;      // [2] dS written (all softmax threads)
+  uint64_t* k_empty = k_full + NK;     // [NK] dQ, the last that reads the stage, done
+  uint64_t* v_full = k_empty + NK;     // [NV]
+  uint64_t* v_empty = v_full + NV;     // [NV] dP done
+  uint64_t* s_full = v_empty + NV;     // [2] S written
+  uint64_t* s_free = s_full + 2;       // [2] the dS in it read by dQ
+  uint64_t* ds_full = s_free + 2;      // [2] dS written (all softmax threads)
   uint64_t* dp_full = ds_full + 2;     // dP written
   uint64_t* dp_free = dp_full + 1;     // dP read (all softmax threads)
-  uint64_t* dq_done = dp_free + 1;     // [2] of even and odd tiles
-  uint64_t* all_done = dq_done + 2;    // every product
-  uint64_t* drain = all_done + 1;      // [2]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
+  uint64_t* all_done = dp_free + 1;    // dQ
+  uint64_t* drain = all_done + 1;      // [3]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 3);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
   int* status = &g_status_prefill_back;
   const int warp = threadIdx.x >> 5;
@@ -703,17 +730,23 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, DqCfg<D>::CTAS)
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
-    for (int i = 0; i < NK; ++i) mbar_init(&k_full[i], 1);
-    for (int i = 0; i < NV; ++i) mbar_init(&v_full[i], 1);
-    mbar_init(dp_full, 1);
-    mbar_init(dp_free, C::SOFT);
+    for (int i = 0; i < NK; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+    }
+    for (int i = 0; i < NV; ++i) {
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_empty[i], 1);
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
+      mbar_init(&s_free[i], 1);
       mbar_init(&ds_full[i], C::SOFT);
-      mbar_init(&dq_done[i], 1);
-      mbar_init(&drain[i], 1);
     }
+    mbar_init(dp_full, 1);
+    mbar_init(dp_free, C::SOFT);
     mbar_init(all_done, 1);
+    for (int i = 0; i < 3; ++i) mbar_init(&drain[i], 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -730,9 +763,20 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, DqCfg<D>::CTAS)
     return warp_wait(bar, parity, abort_flag, status);
   };
 
+  auto wwait2 = [&](uint64_t* x, uint32_t px, uint64_t* y, uint32_t py) -> bool {
+    return warp_wait2(x, px, y, py, abort_flag, status);
+  };
+  const bool leader = tc::elect_one();
+  // an issuing warp's end: every MMA of it has completed before the CTA frees TMEM
+  auto finish = [&](uint64_t* bar) {
+    if (leader) tc::commit(bar);
+    __syncwarp();
+    mbar_drain(bar, 0);
+  };
+  const uint32_t tile16 = C::K_TILE >> 4;   // a stage, in descriptor units
+
   if (warp == 0) {
-    // ------------------------------------------ copies; S = Q K^T and dP = dO V^T
-    const bool leader = tc::elect_one();
+    // ---------------------------------------------------------------- copies
     const uint64_t policy = policy_evict_last();   // K and V are re-read by every query block
     const int slab = p.Hkv * s.k0 + kvh * s.lk + k_lo;
     const int skip_tile = hook_skip_tile();
@@ -745,14 +789,6 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, DqCfg<D>::CTAS)
       }
       __syncwarp();
     };
-    auto load_k = [&](int j) {
-      issued_k = j + 1;
-      load(&tmK, j, smem + C::OFF_K + j % NK * C::K_TILE, &k_full[j % NK]);
-    };
-    auto load_v = [&](int j) {
-      issued_v = j + 1;
-      load(&tmV, j, smem + C::OFF_V + j % NV * C::K_TILE, &v_full[j % NV]);
-    };
     if (leader) {
       // (rows that no copy writes are lanes whose results are not stored)
       mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(2 * NSUB * 128 * G * p.QB));
@@ -763,77 +799,70 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, DqCfg<D>::CTAS)
       }
     }
     __syncwarp();
-    for (int j = 0; j < min(NK, n); ++j) load_k(j);
-    for (int j = 0; j < min(NV, n); ++j) load_v(j);
-    constexpr uint32_t idesc_s = tc::idesc_bf16_f32(128, KT, false);
-    const uint64_t qd = tc::smem_desc_sw128(smem_u32(smem + C::OFF_Q), 16, 1024);
-    const uint64_t dod = tc::smem_desc_sw128(smem_u32(smem + C::OFF_DO), 16, 1024);
-    const uint64_t kd = tc::smem_desc_sw128(smem_u32(smem + C::OFF_K), 16, 1024);
-    const uint64_t vd = tc::smem_desc_sw128(smem_u32(smem + C::OFF_V), 16, 1024);
-    auto ss = [&](uint32_t d_tm, uint64_t a, uint64_t bk, uint64_t* bar) {
-      if (leader) {
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          tc::mma_ss(d_tm, a + static_cast<uint64_t>(kk >> 2) * (C::QSUB >> 4) + (kk & 3) * 2,
-                     bk + static_cast<uint64_t>(kk >> 2) * (C::KSUB >> 4) + (kk & 3) * 2, idesc_s,
-                     kk > 0 ? 1u : 0u);
-        tc::commit(bar);
+    for (int x = 0; x < n + NK - NV; ++x) {
+      if (x < n) {
+        if (x >= NK && !wwait(&k_empty[x % NK], (x / NK - 1) & 1)) break;
+        issued_k = x + 1;
+        load(&tmK, x, smem + C::OFF_K + x % NK * C::K_TILE, &k_full[x % NK]);
       }
-      __syncwarp();
-    };
+      const int y = x - (NK - NV);   // V lags by the stages that K has more
+      if (y < 0) continue;
+      if (y >= NV && !wwait(&v_empty[y % NV], (y / NV - 1) & 1)) break;
+      issued_v = y + 1;
+      load(&tmV, y, smem + C::OFF_V + y % NV * C::K_TILE, &v_full[y % NV]);
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- S = Q K^T
+    const uint64_t qd = tc::smem_desc_sw128(smem_u32(smem + C::OFF_Q), 16, 1024);
+    const uint64_t kd = tc::smem_desc_sw128(smem_u32(smem + C::OFF_K), 16, 1024);
     if (wwait(q_full, 0)) {
       for (int j = 0; j < n; ++j) {
-        // S(j) overwrites the dS(j - 2) that dQ reads
-        if (!wwait(&k_full[j % NK], j / NK & 1)) break;
-        if (j >= 2) {
-          if (!wwait(&dq_done[j & 1], (j - 2) >> 1 & 1)) break;
-          if (j - 2 + NK < n) load_k(j - 2 + NK);
-        }
+        if (j < 2 ? !wwait(&k_full[j % NK], 0)
+                  : !wwait2(&s_free[j & 1], ((j >> 1) - 1) & 1, &k_full[j % NK], j / NK & 1)) break;
         tc::fence_after_sync();
-        ss(tmem + C::COL_S + KT * (j & 1), qd, kd + static_cast<uint64_t>(j % NK) * (C::K_TILE >> 4),
-           &s_full[j & 1]);
-        // dP(j) overwrites dP(j - 1)
-        if (j >= 1) {
-          if (!wwait(dp_free, (j - 1) & 1)) break;
-          if (j - 1 + NV < n) load_v(j - 1 + NV);
-        }
-        if (!wwait(&v_full[j % NV], j / NV & 1)) break;
-        tc::fence_after_sync();
-        ss(tmem + C::COL_DP, dod, vd + static_cast<uint64_t>(j % NV) * (C::K_TILE >> 4), dp_full);
+        issue_ss<D, KT>(leader, tmem + C::COL_S + KT * (j & 1), qd, kd + j % NK * tile16, C::QSUB, C::KSUB);
+        if (leader) tc::commit(&s_full[j & 1]);
+        __syncwarp();
       }
     }
-    // every MMA this warp issued has completed before the CTA frees TMEM
-    if (leader) tc::commit(&drain[0]);
-    __syncwarp();
-    mbar_drain(&drain[0], 0);
-  } else if (warp == 1) {
-    // ------------------------------------------ dQ += dS K
-    const bool leader = tc::elect_one();
-    constexpr uint32_t idesc_o = tc::idesc_bf16_f32(128, D, true);
+    finish(&drain[0]);
+  } else if (warp == 2) {
+    // ---------------------------------------------------------------- dP = dO V^T
+    const uint64_t dod = tc::smem_desc_sw128(smem_u32(smem + C::OFF_DO), 16, 1024);
+    const uint64_t vd = tc::smem_desc_sw128(smem_u32(smem + C::OFF_V), 16, 1024);
+    if (wwait(q_full, 0)) {
+      for (int j = 0; j < n; ++j) {
+        if (j < 1 ? !wwait(&v_full[0], 0)
+                  : !wwait2(dp_free, (j - 1) & 1, &v_full[j % NV], j / NV & 1)) break;
+        tc::fence_after_sync();
+        issue_ss<D, KT>(leader, tmem + C::COL_DP, dod, vd + j % NV * tile16, C::QSUB, C::KSUB);
+        if (leader) {
+          tc::commit(dp_full);
+          tc::commit(&v_empty[j % NV]);
+        }
+        __syncwarp();
+      }
+    }
+    finish(&drain[1]);
+  } else if (warp == 3) {
+    // ---------------------------------------------------------------- dQ += dS K
     const uint64_t kt = tc::smem_desc_sw128(smem_u32(smem + C::OFF_K), C::KSUB, 1024);   // MN-major
     for (int j = 0; j < n; ++j) {
       if (!wwait(&ds_full[j & 1], j >> 1 & 1)) break;
       tc::fence_after_sync();
+      issue_ts<D, KT / 16>(leader, tmem + C::COL_DQ, tmem + C::COL_S + KT * (j & 1), kt + j % NK * tile16, j == 0);
       if (leader) {
-        const uint64_t bk = kt + static_cast<uint64_t>(j % NK) * (C::K_TILE >> 4);
-#pragma unroll
-        for (int kk = 0; kk < KT / 16; ++kk)
-          tc::mma_ts(tmem + C::COL_DQ, packed_step(tmem + C::COL_S + KT * (j & 1), kk),
-                     bk + static_cast<uint64_t>(kk) * 128u, idesc_o, j == 0 && kk == 0 ? 0u : 1u);
-        tc::commit(&dq_done[j & 1]);
+        tc::commit(&s_free[j & 1]);
+        tc::commit(&k_empty[j % NK]);
       }
       __syncwarp();
     }
-    if (leader) {
-      tc::commit(all_done);
-      tc::commit(&drain[1]);
-    }
-    __syncwarp();
-    mbar_drain(&drain[1], 0);
+    if (leader) tc::commit(all_done);
+    finish(&drain[2]);
   } else {
     // ---------------------------------------------------------------- P and dS
-    const int tid = threadIdx.x - 64;
-    const int half = (warp - 2) >> 2;          // columns 64 half ... of a tile
+    const int tid = threadIdx.x - 32 * C::SOFT0;
+    const int half = tid >> 7;                 // columns 64 half ... of a tile
     const int quad = warp & 3;
     const int row = quad * 32 + lane;
     const int rt = row / G;
@@ -854,15 +883,17 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, DqCfg<D>::CTAS)
     const uint32_t dp_addr = lane_base + C::COL_DP + 64 * half;
     const float2 cc = make_float2(p.scale_log2, p.scale_log2);
     const float2 nl = make_float2(nlse, nlse), nd = make_float2(ndel, ndel);
+    // every row of the block sees every key of tiles [j_lo, j_hi) (rows that are not stored need no mask)
+    int j_lo = 0;
+    const int j_hi = ((p.causal ? min(s.lk, pos0 + 1) : s.lk) - k_lo) / KT;
+    if (p.window > 0) j_lo = max(0, (pos0 + nt - p.window - k_lo + KT - 1) / KT);
     bool ok = true;
     for (int j = 0; j < n; ++j) {
+      const bool masked = j < j_lo || j >= j_hi;
       const int j0 = k_lo + j * KT;
-      // (rows that are not stored need no mask)
-      const bool masked = j0 + KT > s.lk || (p.causal && j0 + KT - 1 > pos0) ||
-                          (p.window > 0 && j0 + p.window <= pos0 + nt - 1);
       const int lo = lo_r - j0 - 64 * half, hi = hi_r - j0 - 64 * half;
       const uint32_t s_addr = lane_base + C::COL_S + KT * (j & 1) + 64 * half;
-      if (!warp_wait2(&s_full[j & 1], j >> 1 & 1, dp_full, j & 1, abort_flag, status)) { ok = false; break; }
+      if (!wwait2(&s_full[j & 1], j >> 1 & 1, dp_full, j & 1)) { ok = false; break; }
       tc::fence_after_sync();
       if (j0 + KT > s.lk) {
         // The keys end inside the tile: the rows behind them are another head's or sequence's,
