@@ -146,18 +146,28 @@ __device__ __forceinline__ Seq load_seq(const BackParams& p, int b) {
 }
 
 // ---------------------------------------------------------------------------
+// One try of a wait, suspended for up to `ns` while the phase is not complete.
+__device__ __forceinline__ bool try_wait_for(uint64_t* bar, uint32_t parity, uint32_t ns) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(ns)
+      : "memory");
+  return ok != 0;
+}
+
 // A warp's bounded wait, as one uniform branch: the lanes leave together, so the
 // warp-collective TMEM accesses that follow never run with some of them missing.
-// The time and the abort flag are looked at every 64th time only: reading the
-// limit from memory each time kept a waiting warp about 600 cycles from seeing
-// that its wait was over.
+// A try is suspended for up to 20 us, because a warp that polls takes issue slots
+// from the ones that compute; the time and the abort flag are looked at between tries.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                           int* status) {
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   const long long t0 = clock64();
-  while (true) {
-    for (int i = 0; i < 64; ++i)
-      if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  while (!__all_sync(0xffffffffu, try_wait_for(bar, parity, 20000u))) {
     if (__any_sync(0xffffffffu, *abort_flag)) return false;
     if (__any_sync(0xffffffffu, clock64() - t0 > g_wait_limit_cycles)) {
       *abort_flag = 1;
@@ -165,6 +175,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
       return false;
     }
   }
+  return true;
 }
 
 // The same for two or three barriers: where all are done, which is the rule here,
