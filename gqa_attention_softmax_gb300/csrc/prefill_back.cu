@@ -582,20 +582,22 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
         }
       };
       if constexpr (kOneStep) {
+        float w[2][32];
+        tc::tmem_ld32(dp_addr, w[0]);
+        tc::tmem_ld32(dp_addr + 32, w[1]);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          float v[32], w[32];
+          float v[32];
           tc::tmem_ld32(s_addr + 32 * c, v);
-          tc::tmem_ld32(dp_addr + 32 * c, w);
           tc::tmem_wait_ld();
-          if (c == 1) {
+          if (c == 0) {
             tc::fence_before_sync();
             mbar_arrive(dp_free);   // the next tile's dP^T may come
           }
           weights(v, c);
-          scores(w, v, c);
+          scores(w[c], v, c);
           store_packed(s_addr + 32 * c, v);
-          store_packed(s_addr + 32 * c + 16, w);
+          store_packed(s_addr + 32 * c + 16, w[c]);
         }
       } else {
         float v[2][32];
@@ -912,27 +914,29 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, DqCfg<D>::CTAS)
         zero_rows<NSUB>(smem + C::OFF_K + j % NK * C::K_TILE, C::KSUB, s.lk - j0, KT, tid, C::SOFT);
         tc::fence_proxy_async_smem();
       }
+      float w[2][32];
+      tc::tmem_ld32(dp_addr, w[0]);
+      tc::tmem_ld32(dp_addr + 32, w[1]);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        float v[32], w[32];
+        float v[32];
         tc::tmem_ld32(s_addr + 32 * c, v);
-        tc::tmem_ld32(dp_addr + 32 * c, w);
         tc::tmem_wait_ld();
-        if (c == 1) {
+        if (c == 0) {
           tc::fence_before_sync();
-          mbar_arrive(dp_free);
+          mbar_arrive(dp_free);   // the next tile's dP may come
         }
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
           weights2(v[e], v[e + 1], cc, nl);
-          scores2(w[e], w[e + 1], v[e], v[e + 1], nd);
+          scores2(w[c][e], w[c][e + 1], v[e], v[e + 1], nd);
         }
         if (masked) {
 #pragma unroll
           for (int e = 0; e < 32; ++e)
-            if (c * 32 + e < lo || c * 32 + e >= hi) w[e] = 0.f;
+            if (c * 32 + e < lo || c * 32 + e >= hi) w[c][e] = 0.f;
         }
-        store_packed(s_addr + 32 * c, w);
+        store_packed(s_addr + 32 * c, w[c]);
       }
       tc::tmem_wait_st();
       tc::fence_before_sync();
