@@ -219,10 +219,10 @@ __device__ __forceinline__ void scores2(float& a, float& b, float p0, float p1, 
   b = x.y;
 }
 
-// The A operand of a TS product: bf16 pairs that replaced fp32 columns, each 32
-// elements in 16 of their 32 columns. K step kk covers elements 16 kk ...
+// The A operand of a TS product: bf16 pairs that replaced fp32 columns, each 16
+// elements in 8 of their 16 columns. K step kk covers elements 16 kk ...
 __device__ __forceinline__ uint32_t packed_step(uint32_t base, int kk) {
-  return base + static_cast<uint32_t>(32 * (kk >> 1) + 8 * (kk & 1));
+  return base + static_cast<uint32_t>(16 * kk);
 }
 
 // The products, by one lane of a warp. ss: D = A B^T over d, both in shared memory
@@ -247,12 +247,12 @@ __device__ __forceinline__ void issue_ts(bool leader, uint32_t d_tm, uint32_t a,
                tc::idesc_bf16_f32(128, D, true), first && kk == 0 ? 0u : 1u);
 }
 
-// 32 fp32 columns as bf16 pairs into 16 columns.
-__device__ __forceinline__ void store_packed(uint32_t addr, const float (&v)[32]) {
-  uint32_t pk[16];
+// 16 fp32 columns as bf16 pairs into 8 columns.
+__device__ __forceinline__ void store_packed(uint32_t addr, const float (&v)[16]) {
+  uint32_t pk[8];
 #pragma unroll
-  for (int e = 0; e < 16; ++e) pk[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
-  tc::tmem_st16(addr, pk);
+  for (int e = 0; e < 8; ++e) pk[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
+  tc::tmem_st8(addr, pk);
 }
 
 // dK, dV. S^T = K Q^T and dP^T = V dO^T (M 128 keys, N 128 query rows, K d; all
@@ -268,7 +268,7 @@ __device__ __forceinline__ void store_packed(uint32_t addr, const float (&v)[32]
 template <int D>
 struct DkvCfg {
   static constexpr int SOFT0 = 4;                   // first warp of P and dS
-  static constexpr int SOFT = 256;                  // their threads
+  static constexpr int SOFT = 512;                  // their threads: 32 columns of a key each
   static constexpr int THREADS = SOFT0 * 32 + SOFT;
   static constexpr int NSUB = D / 64;
   static constexpr int SUB = 128 * 128;             // [128 rows][64 bf16], 128B-swizzled
@@ -309,11 +309,11 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
   uint64_t* do_empty = do_full + ND;   // [ND] dP^T and dV done
   uint64_t* s_full = do_empty + ND;    // [NSB] S^T written
   uint64_t* s_free = s_full + NSB;     // [NSB] the P^T (in one step and dS^T) in it read
-  uint64_t* p_full = s_free + NSB;     // [NSB] P^T (in one step and dS^T) written (256 arrivals)
+  uint64_t* p_full = s_free + NSB;     // [NSB] P^T (in one step and dS^T) written (512 arrivals)
   uint64_t* dp_full = p_full + NSB;    // dP^T written
-  uint64_t* dp_free = dp_full + 1;     // dP^T read (256 arrivals), or the dS^T in its place (by dK)
-  uint64_t* ds_full = dp_free + 1;     // dS^T written (256 arrivals; not in one step)
-  uint64_t* row_full = ds_full + 1;    // [2] the rows' lse and delta staged (256 arrivals)
+  uint64_t* dp_free = dp_full + 1;     // dP^T read (512 arrivals), or the dS^T in its place (by dK)
+  uint64_t* ds_full = dp_free + 1;     // dS^T written (512 arrivals; not in one step)
+  uint64_t* row_full = ds_full + 1;    // [2] the rows' lse and delta staged (32 arrivals)
   uint64_t* all_done = row_full + 2;   // dV and dK
   uint64_t* drain = all_done + 1;      // [3]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 3);
@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
     mbar_init(dp_full, 1);
     mbar_init(dp_free, kOneStep ? C::SOFT : 1);
     mbar_init(ds_full, C::SOFT);
-    for (int i = 0; i < 2; ++i) mbar_init(&row_full[i], C::SOFT);
+    for (int i = 0; i < 2; ++i) mbar_init(&row_full[i], 32);
     mbar_init(all_done, 1);
     for (int i = 0; i < 3; ++i) mbar_init(&drain[i], 1);
     *abort_flag = 0;
@@ -435,9 +435,31 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
       load(&tmDo, y, smem + C::OFF_DO + y % ND * C::TILE, &do_full[y % ND]);
     }
   } else if (warp == 1) {
-    // ---------------------------------------------------------------- S^T = K Q^T
+    // ------------------------------------------ S^T = K Q^T; the rows' lse and delta
     const uint64_t kd = tc::smem_desc_sw128(smem_u32(smem + C::OFF_K), 16, 1024);
     const uint64_t qd = tc::smem_desc_sw128(smem_u32(smem + C::OFF_Q), 16, 1024);
+    // Lane l holds rows 4 l .. 4 l + 3 of the next tile: -lse log2(e) and -delta. A row
+    // outside the tile, and one that sees nothing, gets lse = +inf: P = 0. (The tile that used
+    // the slot before is done where S^T's buffer is free.)
+    float lse[4], del[4];
+    long long at[4];
+    int rt[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int r = 4 * lane + e;
+      rt[e] = r < rows ? r / G : 1 << 30;
+      at[e] = static_cast<long long>(s.q0 + i0 + r / G) * p.Hq + kvh * G + r % G;
+    }
+    auto fetch = [&](int j) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const bool in = rt[e] < i1 - i0 - j * p.QB;
+        const long long x = at[e] + static_cast<long long>(j) * p.QB * p.Hq;
+        lse[e] = in ? p.lse[x] : kNegInf;
+        del[e] = in ? p.delta[x] : 0.f;
+      }
+    };
+    if (n > 0) fetch(0);
     if (n > 0 && wwait(kv_full, 0)) {
       for (int j = 0; j < n; ++j) {
         if (j < NSB ? !wwait(&q_full[j % NQ], 0)
@@ -446,6 +468,14 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
         issue_ss<D, 128>(leader, tmem + C::COL_S + 128 * (j % NSB), kd, qd + j % NQ * tile16, C::SUB, C::SUB);
         if (leader) tc::commit(&s_full[j % NSB]);
         __syncwarp();
+        float* to = reinterpret_cast<float*>(smem + C::OFF_ROW) + (j & 1) * 256 + 4 * lane;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          to[e] = lse[e] == kNegInf ? kNegInf : -lse[e] * kLog2e;
+          to[128 + e] = -del[e];
+        }
+        mbar_arrive(&row_full[j & 1]);
+        if (j + 1 < n) fetch(j + 1);
       }
     }
     finish(&drain[0]);
@@ -485,7 +515,7 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
         if (!wwait(ds_full, j & 1)) break;
         tc::fence_after_sync();
       }
-      issue_ts<D, 8>(leader, tmem + C::COL_DK, kOneStep ? pt + 16 : tmem + C::COL_DP, qt + j % NQ * tile16, j == 0);
+      issue_ts<D, 8>(leader, tmem + C::COL_DK, kOneStep ? pt + 8 : tmem + C::COL_DP, qt + j % NQ * tile16, j == 0);
       if (leader) {
         tc::commit(kOneStep ? &s_free[j % NSB] : dp_free);
         tc::commit(&q_empty[j % NQ]);
@@ -497,47 +527,30 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
   } else {
     // ---------------------------------------------------------------- P and dS
     const int tid = threadIdx.x - 32 * C::SOFT0;
-    const int half = tid >> 7;                 // columns 64 half ...
+    const int cols = 32 * (tid >> 7);          // first of this thread's columns
     const int quad = warp & 3;                 // TMEM lane quadrant this warp may access
     const int key = quad * 32 + lane;          // key of the tile
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    float* row_s = reinterpret_cast<float*>(smem + C::OFF_ROW);   // [2][2][128]
-    // thread tid stages -lse log2(e) (tid < 128) or -delta of row tid % 128; a row outside
-    // the tile, and one that sees nothing, gets lse = +inf: P = 0
-    const int r = tid & 127, rt = r / G;
-    const float* from = (tid < 128 ? p.lse : p.delta) + kvh * G + (r - rt * G);
-    auto fetch = [&](int j) -> float {
-      const int i = i0 + j * p.QB + rt;
-      if (r >= rows || i >= i1) return tid < 128 ? INFINITY : 0.f;
-      return from[static_cast<long long>(s.q0 + i) * p.Hq];
-    };
-    // (what was fetched is first looked at here, half a tile later)
-    auto put = [&](int j, float x) {
-      row_s[(j & 1) * 256 + tid] = tid >= 128 ? -x : x == kNegInf ? kNegInf : -x * kLog2e;
-      mbar_arrive(&row_full[j & 1]);
-    };
+    const float* row_s = reinterpret_cast<const float*>(smem + C::OFF_ROW) + cols;   // [2][2][128]
     // every key of the tile sees every row of tiles [j_lo, j_hi)
     int j_lo = 0, j_hi = (i1 - i0) % p.QB ? n - 1 : n;
     if (p.causal) j_lo = max(0, (k0 + 127 - off - i0 + p.QB - 1) / p.QB);
     if (p.window > 0) j_hi = min(j_hi, (k0 + p.window - off - i0) / p.QB);
     const float2 cc = make_float2(p.scale_log2, p.scale_log2);
-    const uint32_t dp_addr = lane_base + C::COL_DP + 64 * half;
+    const uint32_t dp_addr = lane_base + C::COL_DP + cols;
     bool ok = true;
-    if (n > 0) put(0, fetch(0));
     for (int j = 0; j < n; ++j) {
-      float next = 0.f;
-      if (j + 1 < n) next = fetch(j + 1);
       const bool masked = j < j_lo || j >= j_hi;
       int lo = -128, hi = 128, nt = p.QB;        // this thread's visible columns
       if (masked) {
         const int t0 = i0 + j * p.QB;            // first query of the tile
         const int pos0 = off + t0;
         nt = min(p.QB, i1 - t0);
-        lo = (p.causal ? max(0, min(nt, k0 + key - pos0)) * G : 0) - 64 * half;
-        hi = (p.window > 0 ? max(0, min(nt, k0 + key + p.window - pos0)) : nt) * G - 64 * half;
+        lo = (p.causal ? max(0, min(nt, k0 + key - pos0)) * G : 0) - cols;
+        hi = (p.window > 0 ? max(0, min(nt, k0 + key + p.window - pos0)) : nt) * G - cols;
       }
-      const uint32_t s_addr = lane_base + C::COL_S + 128 * (j % NSB) + 64 * half;
-      const float4* lse4 = reinterpret_cast<const float4*>(row_s + (j & 1) * 256 + 64 * half);
+      const uint32_t s_addr = lane_base + C::COL_S + 128 * (j % NSB) + cols;
+      const float4* lse4 = reinterpret_cast<const float4*>(row_s + (j & 1) * 256);
       const float4* del4 = lse4 + 32;
       if (kOneStep ? !warp_wait3(&row_full[j & 1], j >> 1 & 1, &s_full[j % NSB], j / NSB & 1, dp_full, j & 1,
                                  abort_flag, status)
@@ -555,86 +568,88 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
         zero_rows<NSUB>(smem + C::OFF_DO + j % ND * C::TILE, C::SUB, nt * G, 128, tid, C::SOFT);
         tc::fence_proxy_async_smem();
       }
-      auto weights = [&](float (&v)[32], int c) {   // P of columns 32 c ..
+      auto weights = [&](float (&v)[16], int c) {   // P of columns 16 c ..
 #pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-          const float4 l = lse4[c * 8 + e / 4];
+        for (int e = 0; e < 16; e += 4) {
+          const float4 l = lse4[c * 4 + e / 4];
           weights2(v[e], v[e + 1], cc, make_float2(l.x, l.y));
           weights2(v[e + 2], v[e + 3], cc, make_float2(l.z, l.w));
         }
         if (masked) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (c * 32 + e < lo || c * 32 + e >= hi) v[e] = 0.f;
+          for (int e = 0; e < 16; ++e)
+            if (c * 16 + e < lo || c * 16 + e >= hi) v[e] = 0.f;
         }
       };
-      auto scores = [&](float (&w)[32], const float (&v)[32], int c) {   // their dS
+      auto scores = [&](float (&w)[16], const float (&v)[16], int c) {   // their dS
 #pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-          const float4 d = del4[c * 8 + e / 4];
+        for (int e = 0; e < 16; e += 4) {
+          const float4 d = del4[c * 4 + e / 4];
           scores2(w[e], w[e + 1], v[e], v[e + 1], make_float2(d.x, d.y));
           scores2(w[e + 2], w[e + 3], v[e + 2], v[e + 3], make_float2(d.z, d.w));
         }
         if (masked) {   // (0 x NaN of another row is not 0)
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (c * 32 + e < lo || c * 32 + e >= hi) w[e] = 0.f;
+          for (int e = 0; e < 16; ++e)
+            if (c * 16 + e < lo || c * 16 + e >= hi) w[e] = 0.f;
         }
       };
+      float v[2][16], w[2][16];
+      tc::tmem_ld16(s_addr, v[0]);
       if constexpr (kOneStep) {
-        float w[2][32];
-        tc::tmem_ld32(dp_addr, w[0]);
-        tc::tmem_ld32(dp_addr + 32, w[1]);
+        tc::tmem_ld16(dp_addr, w[0]);
+        tc::tmem_ld16(dp_addr + 16, w[1]);
+        tc::tmem_wait_ld();
+        tc::fence_before_sync();
+        mbar_arrive(dp_free);   // the next tile's dP^T may come
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          float v[32];
-          tc::tmem_ld32(s_addr + 32 * c, v);
-          tc::tmem_wait_ld();
-          if (c == 0) {
-            tc::fence_before_sync();
-            mbar_arrive(dp_free);   // the next tile's dP^T may come
+          if (c == 1) {
+            tc::tmem_ld16(s_addr + 16, v[1]);
+            tc::tmem_wait_ld();
           }
-          weights(v, c);
-          scores(w[c], v, c);
-          store_packed(s_addr + 32 * c, v);
-          store_packed(s_addr + 32 * c + 16, w[c]);
+          weights(v[c], c);
+          scores(w[c], v[c], c);
+          store_packed(s_addr + 16 * c, v[c]);
+          store_packed(s_addr + 16 * c + 8, w[c]);
         }
       } else {
-        float v[2][32];
-        tc::tmem_ld32(s_addr, v[0]);
-        tc::tmem_ld32(s_addr + 32, v[1]);
+        tc::tmem_ld16(s_addr + 16, v[1]);
         tc::tmem_wait_ld();
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           weights(v[c], c);
-          store_packed(s_addr + 32 * c, v[c]);
+          store_packed(s_addr + 16 * c, v[c]);
         }
         tc::tmem_wait_st();
         tc::fence_before_sync();
         mbar_arrive(&p_full[0]);
         if (!wwait(dp_full, j & 1)) { ok = false; break; }
         tc::fence_after_sync();
+        tc::tmem_ld16(dp_addr, w[0]);
+        tc::tmem_ld16(dp_addr + 16, w[1]);
+        tc::tmem_wait_ld();
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          float w[32];
-          tc::tmem_ld32(dp_addr + 32 * c, w);
-          tc::tmem_wait_ld();
-          scores(w, v[c], c);
-          store_packed(dp_addr + 32 * c, w);
+          scores(w[c], v[c], c);
+          store_packed(dp_addr + 16 * c, w[c]);
         }
       }
       tc::tmem_wait_st();
       tc::fence_before_sync();
       mbar_arrive(kOneStep ? &p_full[j % NSB] : ds_full);
-      if (j + 1 < n) put(j + 1, next);
     }
     // ------------------------------------------------------------ epilogue
     if (ok && n > 0) ok = wwait(all_done, 0);
     tc::fence_after_sync();
     const long long row = static_cast<long long>(p.Hkv) * s.k0 + static_cast<long long>(kvh) * s.lk + k0 + key;
-    // the first four warps store dV, the others dK
-    tc::store_o_rows<D>(lane_base + (half ? C::COL_DK : C::COL_DV), !(ok && n > 0),
-                        half ? p.sm_scale : 1.f, (half ? p.dk : p.dv) + row * D, key < nk, lane);
+    // four warps store 64 columns: dV's, then dK's
+    const int blk = tid >> 7;
+    const bool is_dk = blk >= NSUB;
+    if (blk < 2 * NSUB)
+      tc::store_o_rows<64>(lane_base + C::COL_DV + 64 * blk, !(ok && n > 0), is_dk ? p.sm_scale : 1.f,
+                           (is_dk ? p.dk : p.dv) + row * D + 64 * (is_dk ? blk - NSUB : blk), key < nk,
+                           lane);
   }
 
   // a warp that left its loop early may still have TMEM loads or stores in flight
@@ -664,7 +679,7 @@ struct DqCfg {
   static constexpr int CTAS = D == 64 ? 2 : 1;      // CTAs of an SM
   static constexpr int KT = D;                      // keys of a tile
   static constexpr int SOFT0 = 4;                   // first warp of dS
-  static constexpr int SOFT = 2 * KT;               // their threads
+  static constexpr int SOFT = 4 * KT;               // their threads: 32 columns of a row each
   static constexpr int THREADS = SOFT0 * 32 + SOFT;
   static constexpr int NSUB = D / 64;
   static constexpr int KSUB = KT * 128;
@@ -875,7 +890,7 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, DqCfg<D>::CTAS)
   } else {
     // ---------------------------------------------------------------- P and dS
     const int tid = threadIdx.x - 32 * C::SOFT0;
-    const int half = tid >> 7;                 // columns 64 half ... of a tile
+    const int cols = 32 * (tid >> 7);          // first of this thread's columns
     const int quad = warp & 3;
     const int row = quad * 32 + lane;
     const int rt = row / G;
@@ -893,7 +908,7 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, DqCfg<D>::CTAS)
       ndel = -p.delta[at];
     }
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    const uint32_t dp_addr = lane_base + C::COL_DP + 64 * half;
+    const uint32_t dp_addr = lane_base + C::COL_DP + cols;
     const float2 cc = make_float2(p.scale_log2, p.scale_log2);
     const float2 nl = make_float2(nlse, nlse), nd = make_float2(ndel, ndel);
     // every row of the block sees every key of tiles [j_lo, j_hi) (rows that are not stored need no mask)
@@ -904,8 +919,8 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, DqCfg<D>::CTAS)
     for (int j = 0; j < n; ++j) {
       const bool masked = j < j_lo || j >= j_hi;
       const int j0 = k_lo + j * KT;
-      const int lo = lo_r - j0 - 64 * half, hi = hi_r - j0 - 64 * half;
-      const uint32_t s_addr = lane_base + C::COL_S + KT * (j & 1) + 64 * half;
+      const int lo = lo_r - j0 - cols, hi = hi_r - j0 - cols;
+      const uint32_t s_addr = lane_base + C::COL_S + KT * (j & 1) + cols;
       if (!wwait2(&s_full[j & 1], j >> 1 & 1, dp_full, j & 1)) { ok = false; break; }
       tc::fence_after_sync();
       if (j0 + KT > s.lk) {
@@ -914,29 +929,29 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, DqCfg<D>::CTAS)
         zero_rows<NSUB>(smem + C::OFF_K + j % NK * C::K_TILE, C::KSUB, s.lk - j0, KT, tid, C::SOFT);
         tc::fence_proxy_async_smem();
       }
-      float w[2][32];
-      tc::tmem_ld32(dp_addr, w[0]);
-      tc::tmem_ld32(dp_addr + 32, w[1]);
+      float w[2][16];
+      tc::tmem_ld16(dp_addr, w[0]);
+      tc::tmem_ld16(dp_addr + 16, w[1]);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        float v[32];
-        tc::tmem_ld32(s_addr + 32 * c, v);
+        float v[16];
+        tc::tmem_ld16(s_addr + 16 * c, v);
         tc::tmem_wait_ld();
         if (c == 0) {
           tc::fence_before_sync();
           mbar_arrive(dp_free);   // the next tile's dP may come
         }
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) {
+        for (int e = 0; e < 16; e += 2) {
           weights2(v[e], v[e + 1], cc, nl);
           scores2(w[c][e], w[c][e + 1], v[e], v[e + 1], nd);
         }
         if (masked) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (c * 32 + e < lo || c * 32 + e >= hi) w[c][e] = 0.f;
+          for (int e = 0; e < 16; ++e)
+            if (c * 16 + e < lo || c * 16 + e >= hi) w[c][e] = 0.f;
         }
-        store_packed(s_addr + 32 * c, w[c]);
+        store_packed(s_addr + 16 * c, w[c]);
       }
       tc::tmem_wait_st();
       tc::fence_before_sync();
@@ -945,9 +960,10 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, DqCfg<D>::CTAS)
     // ------------------------------------------------------------ epilogue
     if (ok) ok = wwait(all_done, 0);
     tc::fence_after_sync();
-    // half h stores the 64-column block h
-    tc::store_o_rows<64>(lane_base + C::COL_DQ + 64 * half, !ok, p.sm_scale, p.dq + at * D + 64 * half,
-                         valid, lane);
+    const int blk = tid >> 7;   // four warps store 64 columns
+    if (blk < NSUB)
+      tc::store_o_rows<64>(lane_base + C::COL_DQ + 64 * blk, !ok, p.sm_scale, p.dq + at * D + 64 * blk,
+                           valid, lane);
   }
 
   tc::tmem_wait_ld();
