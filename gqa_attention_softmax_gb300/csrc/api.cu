@@ -290,8 +290,9 @@ int sinkattn_prefill_paged(const void* q, const void* k_pages, const void* v_pag
 
 namespace {
 
-// Workspace of the backward pass: delta, then the blocks' sums of the sinks' gradients.
-size_t back_delta_bytes(int32_t total_q, int32_t Hq) {
+// Workspace of the backward pass: two arrays of a value per row, then the
+// blocks' sums of the sinks' gradients.
+size_t back_row_bytes(int32_t total_q, int32_t Hq) {
   return (static_cast<size_t>(total_q) * Hq * 4 + 255) & ~static_cast<size_t>(255);
 }
 
@@ -306,7 +307,7 @@ int sinkattn_prefill_backward_workspace_bytes(int32_t total_q, int32_t num_qo_he
   if (total_q < 0 || num_qo_heads <= 0) return fail(SINKATTN_INVALID_ARG, "bad sizes");
   if (static_cast<int64_t>(total_q) * num_qo_heads >= (int64_t{1} << 31))
     return fail(SINKATTN_UNSUPPORTED, "problem exceeds 2^31 rows");
-  *bytes = back_delta_bytes(total_q, num_qo_heads) +
+  *bytes = 2 * back_row_bytes(total_q, num_qo_heads) +
            static_cast<size_t>(back_blocks(total_q, num_qo_heads)) * num_qo_heads * 4;
   return SINKATTN_OK;
 }
@@ -375,9 +376,10 @@ int sinkattn_prefill_backward(const void* dout, const void* q, const void* k, co
   a.Hq = num_qo_heads; a.Hkv = num_kv_heads; a.d = head_dim;
   a.sm_scale = sm_scale; a.causal = causal; a.window = window;
   a.dq = dq; a.dk = dk; a.dv = dv; a.dsinks = dsinks;
-  a.delta = static_cast<float*>(workspace);
-  a.sink_part = reinterpret_cast<float*>(static_cast<char*>(workspace) +
-                                         back_delta_bytes(total_q, num_qo_heads));
+  char* ws = static_cast<char*>(workspace);
+  a.nlse = reinterpret_cast<float*>(ws);
+  a.ndelta = reinterpret_cast<float*>(ws + back_row_bytes(total_q, num_qo_heads));
+  a.sink_part = reinterpret_cast<float*>(ws + 2 * back_row_bytes(total_q, num_qo_heads));
   return launch_prefill_back(a, s);
 }
 

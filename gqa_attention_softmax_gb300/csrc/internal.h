@@ -218,7 +218,7 @@ struct BackArgs {
   void *dq, *dk, *dv;
   float* dsinks;                        // nullptr where sinks is
   // workspace
-  float* delta;                         // [total_q, Hq]
+  float *nlse, *ndelta;                 // [total_q, Hq]
   float* sink_part;                     // [back_blocks(), Hq]
 };
 // Rows of sink_part: blocks of query tokens of the pass that computes delta.

@@ -13,10 +13,13 @@
 // accumulators.
 //
 // Both kernels: warp 0 stages tiles by TMA, warp 1 issues the product that makes
-// S, warp 2 that of dP, warp 3 those that take P and dS, and the others compute
-// these, one thread per TMEM lane and 64 columns. An issuing warp's wait that is already over, its
-// MMAs and its commits take 100 to 250 cycles each, one after the other: one
-// warp for all products needed 2000 a tile pair, twice what the tensor core does.
+// S, warp 2 that of dP, warp 3 those that take P and dS, and groups of eight
+// warps compute these, one thread per TMEM lane and 32 columns. A product is
+// seen by those who wait for it about 500 cycles after the tensor core has
+// done it, and a tile goes through three of them in turn. So tiles are small (64
+// columns), and TMEM holds as many of them on their way as fit beside the
+// accumulators; each kind of product has a warp of its own, because an issuing
+// warp's waits, MMAs and commits take 100 to 250 cycles each, one after the other.
 // P and dS are rounded to bf16 for the products that take them; P enters dS
 // unrounded. Every wait is bounded; on a timeout the CTA records
 // SINKATTN_TIMEOUT, drains its copies and MMAs, frees TMEM and exits.
@@ -40,10 +43,11 @@ struct BackParams {
   float sm_scale, scale_log2;
   int causal, window;
   __nv_bfloat16 *dq, *dk, *dv;
-  float *dsinks, *delta, *sink_part;
+  float *dsinks, *nlse, *ndelta, *sink_part;   // (workspace: [total_q, Hq] -lse log2 e, -delta)
   int per;       // tokens of a block of the delta pass
   int delta_blocks, sink_blocks;
   int QB, nqb;   // query tokens of a tile of 128 rows, tiles of the longest sequence
+  int GT, chunks, QB2;   // heads and tokens of a tile of 64 rows, tiles of a token
 };
 
 __device__ __forceinline__ float dot8(uint4 x, uint4 y, float s) {
@@ -59,8 +63,8 @@ __device__ __forceinline__ float dot8(uint4 x, uint4 y, float s) {
 constexpr int kDeltaRows = 1024;   // rows (token, head) of a block of the delta pass at most
 constexpr int kDeltaHeads = 256;   // heads of a block
 
-// delta of p.per tokens and up to kDeltaHeads heads, d / 8 threads a row, and
-// those rows' sum of the sinks' gradients, in the order of the tokens.
+// -delta and -lse log2 e of p.per tokens and up to kDeltaHeads heads, d / 8 threads a
+// row, and those rows' sum of the sinks' gradients, in the order of the tokens.
 template <int D>
 __global__ void __launch_bounds__(256) back_delta_kernel(const BackParams p) {
   constexpr int C = D / 8;
@@ -95,9 +99,12 @@ __global__ void __launch_bounds__(256) back_delta_kernel(const BackParams p) {
       for (int m = 1; m < C; m <<= 1) s[i] += __shfl_xor_sync(0xffffffffu, s[i], m);
       if (r < rows && c == 0) {
         if (p.dlse) s[i] -= p.dlse[at[i]];
-        p.delta[at[i]] = s[i];
-        // a row with no visible key and no sink has lse -inf, but then there are no sinks
-        if (p.sinks) term[r] = -expf(p.sinks[h0 + r % nh] - p.lse[at[i]]) * s[i];
+        const float lse = p.lse[at[i]];
+        p.ndelta[at[i]] = -s[i];
+        // a row that sees nothing (lse -inf) has P = 0, as for lse +inf
+        p.nlse[at[i]] = lse == kNegInf ? kNegInf : -lse * kLog2e;
+        // (then there is no sink)
+        if (p.sinks) term[r] = -expf(p.sinks[h0 + r % nh] - lse) * s[i];
       }
     }
   }
@@ -205,6 +212,16 @@ __device__ __forceinline__ void zero_rows(uint8_t* tile, int sub_bytes, int from
         make_uint4(0, 0, 0, 0);
 }
 
+// Four bytes from global to shared memory, asynchronously; an arrival on a barrier
+// when the thread's copies so far have landed; the end of all of them.
+__device__ __forceinline__ void copy4_async(float* to, const float* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void arrive_after_copies(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void wait_copies() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // Two of P's elements: 2^(s c2 - lse log2 e).
 __device__ __forceinline__ void weights2(float& a, float& b, float2 cc, float2 nl) {
   const float2 x = __ffma2_rn(make_float2(a, b), cc, nl);
@@ -255,38 +272,40 @@ __device__ __forceinline__ void store_packed(uint32_t addr, const float (&v)[16]
   tc::tmem_st8(addr, pk);
 }
 
-// dK, dV. S^T = K Q^T and dP^T = V dO^T (M 128 keys, N 128 query rows, K d; all
-// from shared memory), dV += P^T dO and dK += dS^T Q (M 128 keys, N d, K 128; P^T
-// and dS^T from TMEM). Keys in the TMEM lanes make P^T and dS^T the MMA's A
-// operand as they are.
-// At d 64 TMEM holds two S^T buffers. P^T and dS^T, computed in one step, both
-// replace S^T, dP^T is free as soon as it has been read, and the scores of the
-// next tile are there when a tile's weights are done (one step keeps the
-// exponentials' unit and the others busy at once). At d 128 there is one
-// buffer: P^T replaces S^T and dS^T replaces dP^T, so that the next S^T follows dV
-// while dS^T is computed, and the next dP^T follows dK.
+// dK, dV. S^T = K Q^T and dP^T = V dO^T (M 128 keys, N 64 query rows, K d; all
+// from shared memory), dV += P^T dO and dK += dS^T Q (M 128 keys, N d, K 64; P^T and
+// dS^T from TMEM, where both replace S^T). Keys in the TMEM lanes make P^T and
+// dS^T the MMA's A operand as they are. dP^T is free as soon as it has been read.
+// A tile is QB2 tokens times GT heads; groups of more than 64 heads come in two chunks.
 template <int D>
 struct DkvCfg {
   static constexpr int SOFT0 = 4;                   // first warp of P and dS
-  static constexpr int SOFT = 512;                  // their threads: 32 columns of a key each
-  static constexpr int THREADS = SOFT0 * 32 + SOFT;
+  static constexpr int GROUP = 256;                 // threads of a group; two groups take alternate tiles
+  static constexpr int THREADS = SOFT0 * 32 + 2 * GROUP;
   static constexpr int NSUB = D / 64;
-  static constexpr int SUB = 128 * 128;             // [128 rows][64 bf16], 128B-swizzled
-  static constexpr int TILE = NSUB * SUB;
-  static constexpr int NQ = D == 64 ? 4 : 3;        // stages of Q
-  static constexpr int ND = D == 64 ? 4 : 2;        // stages of dO, which is wanted later
-  static constexpr int NSB = D == 64 ? 2 : 1;       // S^T buffers (TMEM holds no more at d 128)
+  static constexpr int QT = 64;                     // query rows of a tile
+  static constexpr int KSUB = 128 * 128;            // [128 keys][64 bf16], 128B-swizzled
+  static constexpr int QSUB = QT * 128;
+  static constexpr int K_TILE = NSUB * KSUB;
+  static constexpr int Q_TILE = NSUB * QSUB;
+  static constexpr int NSB = D == 64 ? 4 : 3;       // S^T buffers
+  static constexpr int NDP = D == 64 ? 2 : 1;       // dP^T buffers
+  static constexpr int NB = D == 64 ? 4 : 6;        // tiles after which buffer and group repeat
+  static constexpr int NQ = D == 64 ? 8 : 6;        // stages of Q
+  static constexpr int ND = D == 64 ? 8 : 4;        // stages of dO, which is held for a shorter time
   static constexpr int OFF_K = 0;
-  static constexpr int OFF_V = TILE;
-  static constexpr int OFF_Q = 2 * TILE;
-  static constexpr int OFF_DO = OFF_Q + NQ * TILE;
-  static constexpr int OFF_ROW = OFF_DO + ND * TILE;   // [2][-lse log2 e, -delta][128]
-  static constexpr int OFF_BAR = OFF_ROW + 2 * 2 * 128 * 4;
-  static constexpr int N_BARS = 1 + 2 * NQ + 2 * ND + 3 * NSB + 3 + 2 + 1 + 3;
+  static constexpr int OFF_V = K_TILE;
+  static constexpr int OFF_Q = 2 * K_TILE;
+  static constexpr int OFF_DO = OFF_Q + NQ * Q_TILE;
+  static constexpr int NR = 4;                      // slots of the rows' lse and delta
+  static constexpr int OFF_ROW = OFF_DO + ND * Q_TILE;   // [NR][-lse log2 e, -delta][QT]
+  static constexpr int OFF_BAR = OFF_ROW + NR * 2 * QT * 4;
+  static constexpr int N_BARS = 1 + 2 * NQ + 2 * ND + NB + NR + 2 * NSB + 2 + NDP + 1 + 3;
+  static_assert(NR % 2 == 0 && NR <= ND && ND <= NQ, "order of the copies");
   static constexpr int SMEM = OFF_BAR + N_BARS * 8 + 16;
   static constexpr uint32_t COL_S = 0;
-  static constexpr uint32_t COL_DP = 128 * NSB;
-  static constexpr uint32_t COL_DV = COL_DP + 128;
+  static constexpr uint32_t COL_DP = QT * NSB;
+  static constexpr uint32_t COL_DV = COL_DP + QT * NDP;
   static constexpr uint32_t COL_DK = COL_DV + D;
   static_assert(COL_DK + D <= 512, "TMEM budget");
   static_assert(SMEM <= 232448, "shared memory budget");
@@ -298,8 +317,8 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
                     const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                     const BackParams p) {
   using C = DkvCfg<D>;
-  constexpr int NQ = C::NQ, ND = C::ND, NSB = C::NSB, NSUB = C::NSUB;
-  constexpr bool kOneStep = NSB == 2;
+  constexpr int NQ = C::NQ, ND = C::ND, NSB = C::NSB, NDP = C::NDP, NB = C::NB, NR = C::NR, NSUB = C::NSUB,
+                QT = C::QT;
   extern __shared__ __align__(1024) uint8_t smem[];   // (swizzled tiles start on 1024 bytes)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* kv_full = bars;
@@ -307,14 +326,13 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
   uint64_t* q_empty = q_full + NQ;     // [NQ] dK, the last that reads the stage, done
   uint64_t* do_full = q_empty + NQ;    // [ND]
   uint64_t* do_empty = do_full + ND;   // [ND] dP^T and dV done
-  uint64_t* s_full = do_empty + ND;    // [NSB] S^T written
-  uint64_t* s_free = s_full + NSB;     // [NSB] the P^T (in one step and dS^T) in it read
-  uint64_t* p_full = s_free + NSB;     // [NSB] P^T (in one step and dS^T) written (512 arrivals)
-  uint64_t* dp_full = p_full + NSB;    // dP^T written
-  uint64_t* dp_free = dp_full + 1;     // dP^T read (512 arrivals), or the dS^T in its place (by dK)
-  uint64_t* ds_full = dp_free + 1;     // dS^T written (512 arrivals; not in one step)
-  uint64_t* row_full = ds_full + 1;    // [2] the rows' lse and delta staged (32 arrivals)
-  uint64_t* all_done = row_full + 2;   // dV and dK
+  uint64_t* s_full = do_empty + ND;    // [NB] S^T written
+  uint64_t* row_full = s_full + NB;    // [NR] the rows' lse and delta staged (64 arrivals)
+  uint64_t* s_free = row_full + NR;    // [NSB] the P^T and dS^T in it read
+  uint64_t* p_full = s_free + NSB;     // [NSB] P^T and dS^T written (the group's arrivals)
+  uint64_t* dp_full = p_full + NSB;    // [2] of even and odd tiles: dP^T written
+  uint64_t* dp_free = dp_full + 2;     // [NDP] dP^T read (the group's arrivals)
+  uint64_t* all_done = dp_free + NDP;  // dV and dK
   uint64_t* drain = all_done + 1;      // [3]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 3);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
@@ -339,8 +357,8 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
   // queries [i0, i1) see some key of the tile
   const int i0 = p.causal ? max(0, k0 - off) : 0;
   const int i1 = p.window > 0 ? max(0, min(s.lq, k0 + nk - 1 + p.window - off)) : s.lq;
-  const int n = i1 > i0 ? (i1 - i0 + p.QB - 1) / p.QB : 0;
-  const int G = p.G, rows = G * p.QB;
+  const int GT = p.GT, cs = p.chunks - 1, QB2 = p.QB2, rows = GT * QB2;
+  const int n = i1 > i0 ? (i1 - i0 + QB2 - 1) / QB2 << cs : 0;
 
   if (threadIdx.x == 0) {
     mbar_init(kv_full, 1);
@@ -350,25 +368,24 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
     }
     for (int i = 0; i < ND; ++i) {
       mbar_init(&do_full[i], 1);
-      mbar_init(&do_empty[i], 2);
+      mbar_init(&do_empty[i], 1);
     }
+    for (int i = 0; i < NB; ++i) mbar_init(&s_full[i], 1);
+    for (int i = 0; i < NR; ++i) mbar_init(&row_full[i], 64);
     for (int i = 0; i < NSB; ++i) {
-      mbar_init(&s_full[i], 1);
       mbar_init(&s_free[i], 1);
-      mbar_init(&p_full[i], C::SOFT);
+      mbar_init(&p_full[i], C::GROUP);
     }
-    mbar_init(dp_full, 1);
-    mbar_init(dp_free, kOneStep ? C::SOFT : 1);
-    mbar_init(ds_full, C::SOFT);
-    for (int i = 0; i < 2; ++i) mbar_init(&row_full[i], 32);
+    for (int i = 0; i < 2; ++i) mbar_init(&dp_full[i], 1);
+    for (int i = 0; i < NDP; ++i) mbar_init(&dp_free[i], C::GROUP);
     mbar_init(all_done, 1);
     for (int i = 0; i < 3; ++i) mbar_init(&drain[i], 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (rows < 128) {   // rows that no copy writes
+  if (rows < QT) {   // rows that no copy writes
     for (int i = 0; i < NQ + ND; ++i)
-      zero_rows<NSUB>(smem + C::OFF_Q + i * C::TILE, C::SUB, rows, 128, threadIdx.x, C::THREADS);
+      zero_rows<NSUB>(smem + C::OFF_Q + i * C::Q_TILE, C::QSUB, rows, QT, threadIdx.x, C::THREADS);
     tc::fence_proxy_async_smem();
   }
   if (warp == 1) {
@@ -393,7 +410,7 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
     __syncwarp();
     mbar_drain(bar, 0);
   };
-  const uint32_t tile16 = C::TILE >> 4;   // a stage, in descriptor units
+  const uint32_t tile16 = C::Q_TILE >> 4;   // a stage, in descriptor units
 
   if (warp == 0) {
     // ---------------------------------------------------------------- copies
@@ -401,81 +418,77 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
     auto load = [&](const CUtensorMap* map, int j, uint8_t* to, uint64_t* bar) {   // into a free stage
       if (j != skip_tile && leader) {   // test hook: the waits for this tile run out
         mbar_arrive_expect_tx(bar, static_cast<uint32_t>(NSUB * 128 * rows));
+        const int tok = s.q0 + i0 + (j >> cs) * QB2, head = kvh * p.G + (j & cs) * GT;
 #pragma unroll
         for (int sub = 0; sub < NSUB; ++sub)
-          tc::tma_load_3d(to + sub * C::SUB, map, sub * 64, kvh * G, s.q0 + i0 + j * p.QB, bar);
+          tc::tma_load_3d(to + sub * C::QSUB, map, sub * 64, head, tok, bar);
       }
       __syncwarp();
     };
     if (n > 0 && leader) {
-      mbar_arrive_expect_tx(kv_full, 2 * C::TILE);
+      mbar_arrive_expect_tx(kv_full, 2 * C::K_TILE);
       const int slab = p.Hkv * s.k0 + kvh * s.lk + k0;
 #pragma unroll
       for (int sub = 0; sub < NSUB; ++sub) {
-        tma_load_2d(smem + C::OFF_K + sub * C::SUB, &tmK, sub * 64, slab, kv_full);
-        tma_load_2d(smem + C::OFF_V + sub * C::SUB, &tmV, sub * 64, slab, kv_full);
+        tma_load_2d(smem + C::OFF_K + sub * C::KSUB, &tmK, sub * 64, slab, kv_full);
+        tma_load_2d(smem + C::OFF_V + sub * C::KSUB, &tmV, sub * 64, slab, kv_full);
       }
     }
     __syncwarp();
-    // tile x's dO is wanted after its Q, and its stage is free before
-    for (int x = 0; x < n; ++x) {
+    // -lse log2(e) and -delta of rows 2 l and 2 l + 1 of a tile, by lane l. A row outside the tile
+    // gets lse = +inf: P = 0. Both kinds of writes arrive, the copies when they have landed.
+    int rt[2], rh[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      rt[e] = (2 * lane + e) / GT;
+      rh[e] = (2 * lane + e) % GT;
+    }
+    auto load_rows = [&](int j) {
+      float* to = reinterpret_cast<float*>(smem + C::OFF_ROW) + j % NR * 2 * QT + 2 * lane;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int i = i0 + (j >> cs) * QB2 + rt[e], h = (j & cs) * GT + rh[e];
+        if (2 * lane + e < rows && i < i1 && h < p.G) {
+          const long long at = static_cast<long long>(s.q0 + i) * p.Hq + kvh * p.G + h;
+          copy4_async(to + e, p.nlse + at);
+          copy4_async(to + QT + e, p.ndelta + at);
+        } else {
+          to[e] = kNegInf;
+          to[QT + e] = 0.f;
+        }
+      }
+      mbar_arrive(&row_full[j % NR]);
+      arrive_after_copies(&row_full[j % NR]);
+    };
+    // Q of tile x, and the tiles whose dO and rows take the places of the same tile x - NQ
+    for (int x = 0; x < n + NQ - NR; ++x) {
       if (x >= NQ && !wwait(&q_empty[x % NQ], (x / NQ - 1) & 1)) break;
-      issued_q = x + 1;
-      load(&tmQ, x, smem + C::OFF_Q + x % NQ * C::TILE, &q_full[x % NQ]);
-      // dO lags by the stages that Q has more
-      const int y = x - (NQ - ND);
-      if (y < 0) continue;
-      if (y >= ND && !wwait(&do_empty[y % ND], (y / ND - 1) & 1)) break;
-      issued_do = y + 1;
-      load(&tmDo, y, smem + C::OFF_DO + y % ND * C::TILE, &do_full[y % ND]);
+      if (x < n) {
+        issued_q = x + 1;
+        load(&tmQ, x, smem + C::OFF_Q + x % NQ * C::Q_TILE, &q_full[x % NQ]);
+      }
+      const int y = x - (NQ - ND), z = x - (NQ - NR);
+      if (y >= 0 && y < n) {
+        if (y >= ND && !wwait(&do_empty[y % ND], (y / ND - 1) & 1)) break;
+        issued_do = y + 1;
+        load(&tmDo, y, smem + C::OFF_DO + y % ND * C::Q_TILE, &do_full[y % ND]);
+      }
+      if (z >= 0) load_rows(z);
     }
-    for (int y = max(0, n - (NQ - ND)); y < n; ++y) {
-      if (y >= ND && !wwait(&do_empty[y % ND], (y / ND - 1) & 1)) break;
-      issued_do = y + 1;
-      load(&tmDo, y, smem + C::OFF_DO + y % ND * C::TILE, &do_full[y % ND]);
-    }
+    wait_copies();   // (before the CTA's shared memory goes away)
   } else if (warp == 1) {
-    // ------------------------------------------ S^T = K Q^T; the rows' lse and delta
+    // ---------------------------------------------------------------- S^T = K Q^T
     const uint64_t kd = tc::smem_desc_sw128(smem_u32(smem + C::OFF_K), 16, 1024);
     const uint64_t qd = tc::smem_desc_sw128(smem_u32(smem + C::OFF_Q), 16, 1024);
-    // Lane l holds rows 4 l .. 4 l + 3 of the next tile: -lse log2(e) and -delta. A row
-    // outside the tile, and one that sees nothing, gets lse = +inf: P = 0. (The tile that used
-    // the slot before is done where S^T's buffer is free.)
-    float lse[4], del[4];
-    long long at[4];
-    int rt[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int r = 4 * lane + e;
-      rt[e] = r < rows ? r / G : 1 << 30;
-      at[e] = static_cast<long long>(s.q0 + i0 + r / G) * p.Hq + kvh * G + r % G;
-    }
-    auto fetch = [&](int j) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const bool in = rt[e] < i1 - i0 - j * p.QB;
-        const long long x = at[e] + static_cast<long long>(j) * p.QB * p.Hq;
-        lse[e] = in ? p.lse[x] : kNegInf;
-        del[e] = in ? p.delta[x] : 0.f;
-      }
-    };
-    if (n > 0) fetch(0);
     if (n > 0 && wwait(kv_full, 0)) {
       for (int j = 0; j < n; ++j) {
+        const int sb = j % NSB;
         if (j < NSB ? !wwait(&q_full[j % NQ], 0)
-                    : !wwait2(&s_free[j % NSB], (j / NSB - 1) & 1, &q_full[j % NQ], j / NQ & 1)) break;
+                    : !wwait2(&s_free[sb], (j / NSB - 1) & 1, &q_full[j % NQ], j / NQ & 1)) break;
         tc::fence_after_sync();
-        issue_ss<D, 128>(leader, tmem + C::COL_S + 128 * (j % NSB), kd, qd + j % NQ * tile16, C::SUB, C::SUB);
-        if (leader) tc::commit(&s_full[j % NSB]);
+        issue_ss<D, QT>(leader, tmem + C::COL_S + QT * sb, kd, qd + j % NQ * tile16, C::KSUB, C::QSUB);
+        if (leader) tc::commit(&s_full[j % NB]);
         __syncwarp();
-        float* to = reinterpret_cast<float*>(smem + C::OFF_ROW) + (j & 1) * 256 + 4 * lane;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          to[e] = lse[e] == kNegInf ? kNegInf : -lse[e] * kLog2e;
-          to[128 + e] = -del[e];
-        }
-        mbar_arrive(&row_full[j & 1]);
-        if (j + 1 < n) fetch(j + 1);
       }
     }
     finish(&drain[0]);
@@ -485,39 +498,29 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
     const uint64_t dod = tc::smem_desc_sw128(smem_u32(smem + C::OFF_DO), 16, 1024);
     if (n > 0 && wwait(kv_full, 0)) {
       for (int j = 0; j < n; ++j) {
-        if (j == 0 ? !wwait(&do_full[0], 0)
-                   : !wwait2(dp_free, (j - 1) & 1, &do_full[j % ND], j / ND & 1)) break;
+        if (j < NDP ? !wwait(&do_full[j % ND], 0)
+                    : !wwait2(&dp_free[j % NDP], (j / NDP - 1) & 1, &do_full[j % ND], j / ND & 1)) break;
         tc::fence_after_sync();
-        issue_ss<D, 128>(leader, tmem + C::COL_DP, vd, dod + j % ND * tile16, C::SUB, C::SUB);
-        if (leader) {
-          tc::commit(dp_full);
-          tc::commit(&do_empty[j % ND]);
-        }
+        issue_ss<D, QT>(leader, tmem + C::COL_DP + QT * (j % NDP), vd, dod + j % ND * tile16, C::KSUB, C::QSUB);
+        if (leader) tc::commit(&dp_full[j & 1]);
         __syncwarp();
       }
     }
     finish(&drain[1]);
   } else if (warp == 3) {
     // ------------------------------------------ dV += P^T dO and dK += dS^T Q
-    const uint64_t dot = tc::smem_desc_sw128(smem_u32(smem + C::OFF_DO), C::SUB, 1024);   // MN-major
-    const uint64_t qt = tc::smem_desc_sw128(smem_u32(smem + C::OFF_Q), C::SUB, 1024);
+    const uint64_t dot = tc::smem_desc_sw128(smem_u32(smem + C::OFF_DO), C::QSUB, 1024);   // MN-major
+    const uint64_t qt = tc::smem_desc_sw128(smem_u32(smem + C::OFF_Q), C::QSUB, 1024);
     for (int j = 0; j < n; ++j) {
-      const uint32_t pt = tmem + C::COL_S + 128 * (j % NSB);
-      if (!wwait(&p_full[j % NSB], j / NSB & 1)) break;
+      const int sb = j % NSB;
+      const uint32_t pt = tmem + C::COL_S + QT * sb;
+      if (!wwait(&p_full[sb], j / NSB & 1)) break;
       tc::fence_after_sync();
-      issue_ts<D, 8>(leader, tmem + C::COL_DV, pt, dot + j % ND * tile16, j == 0);
+      issue_ts<D, QT / 16>(leader, tmem + C::COL_DV, pt, dot + j % ND * tile16, j == 0);
+      if (leader) tc::commit(&do_empty[j % ND]);
+      issue_ts<D, QT / 16>(leader, tmem + C::COL_DK, pt + 8, qt + j % NQ * tile16, j == 0);
       if (leader) {
-        if (!kOneStep) tc::commit(&s_free[0]);
-        tc::commit(&do_empty[j % ND]);
-      }
-      __syncwarp();
-      if (!kOneStep) {
-        if (!wwait(ds_full, j & 1)) break;
-        tc::fence_after_sync();
-      }
-      issue_ts<D, 8>(leader, tmem + C::COL_DK, kOneStep ? pt + 8 : tmem + C::COL_DP, qt + j % NQ * tile16, j == 0);
-      if (leader) {
-        tc::commit(kOneStep ? &s_free[j % NSB] : dp_free);
+        tc::commit(&s_free[sb]);
         tc::commit(&q_empty[j % NQ]);
       }
       __syncwarp();
@@ -526,125 +529,86 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
     finish(&drain[2]);
   } else {
     // ---------------------------------------------------------------- P and dS
-    const int tid = threadIdx.x - 32 * C::SOFT0;
+    const int grp = (threadIdx.x - 32 * C::SOFT0) / C::GROUP;   // tiles grp, grp + 2 ...
+    const int tid = threadIdx.x - 32 * C::SOFT0 - grp * C::GROUP;
     const int cols = 32 * (tid >> 7);          // first of this thread's columns
     const int quad = warp & 3;                 // TMEM lane quadrant this warp may access
     const int key = quad * 32 + lane;          // key of the tile
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    const float* row_s = reinterpret_cast<const float*>(smem + C::OFF_ROW) + cols;   // [2][2][128]
-    // every key of the tile sees every row of tiles [j_lo, j_hi)
-    int j_lo = 0, j_hi = (i1 - i0) % p.QB ? n - 1 : n;
-    if (p.causal) j_lo = max(0, (k0 + 127 - off - i0 + p.QB - 1) / p.QB);
-    if (p.window > 0) j_hi = min(j_hi, (k0 + p.window - off - i0) / p.QB);
+    const float* row_s = reinterpret_cast<const float*>(smem + C::OFF_ROW) + cols;   // [NR][2][QT]
+    // every key of the tile sees every row of the token blocks [b_lo, b_hi)
+    int b_lo = 0, b_hi = (i1 - i0) / QB2;
+    if (p.causal) b_lo = max(0, (k0 + 127 - off - i0 + QB2 - 1) / QB2);
+    if (p.window > 0) b_hi = min(b_hi, (k0 + p.window - off - i0) / QB2);
     const float2 cc = make_float2(p.scale_log2, p.scale_log2);
-    const uint32_t dp_addr = lane_base + C::COL_DP + cols;
     bool ok = true;
-    for (int j = 0; j < n; ++j) {
-      const bool masked = j < j_lo || j >= j_hi;
-      int lo = -128, hi = 128, nt = p.QB;        // this thread's visible columns
+    for (int j = grp; j < n; j += 2) {
+      const int sb = j % NSB;
+      const bool masked = (j >> cs) < b_lo || (j >> cs) >= b_hi;
+      int lo = -128, hi = 128, nt = QB2;         // this thread's visible columns
       if (masked) {
-        const int t0 = i0 + j * p.QB;            // first query of the tile
+        const int t0 = i0 + (j >> cs) * QB2;     // first query of the tile
         const int pos0 = off + t0;
-        nt = min(p.QB, i1 - t0);
-        lo = (p.causal ? max(0, min(nt, k0 + key - pos0)) * G : 0) - cols;
-        hi = (p.window > 0 ? max(0, min(nt, k0 + key + p.window - pos0)) : nt) * G - cols;
+        nt = min(QB2, i1 - t0);
+        lo = (p.causal ? max(0, min(nt, k0 + key - pos0)) * GT : 0) - cols;
+        hi = (p.window > 0 ? max(0, min(nt, k0 + key + p.window - pos0)) : nt) * GT - cols;
       }
-      const uint32_t s_addr = lane_base + C::COL_S + 128 * (j % NSB) + cols;
-      const float4* lse4 = reinterpret_cast<const float4*>(row_s + (j & 1) * 256);
-      const float4* del4 = lse4 + 32;
-      if (kOneStep ? !warp_wait3(&row_full[j & 1], j >> 1 & 1, &s_full[j % NSB], j / NSB & 1, dp_full, j & 1,
-                                 abort_flag, status)
-                   : !wwait2(&row_full[j & 1], j >> 1 & 1, &s_full[0], j & 1)) {
+      const uint32_t s_addr = lane_base + C::COL_S + QT * sb + cols;
+      const uint32_t dp_addr = lane_base + C::COL_DP + QT * (j % NDP) + cols;
+      const float4* lse4 = reinterpret_cast<const float4*>(row_s + j % NR * 2 * QT);
+      const float4* del4 = lse4 + QT / 4;
+      if (!warp_wait3(&row_full[j % NR], j / NR & 1, &s_full[j % NB], j / NB & 1, &dp_full[grp], j >> 1 & 1,
+                      abort_flag, status)) {
         ok = false;
         break;
       }
       tc::fence_after_sync();
-      if (nt < p.QB) {
-        // The visible rows end inside the tile: those behind them may be another
-        // sequence's, whose NaN would pass through zero weights. Both products
-        // that read the tile along d have to be done.
-        if (!kOneStep && !wwait(dp_full, j & 1)) { ok = false; break; }
-        zero_rows<NSUB>(smem + C::OFF_Q + j % NQ * C::TILE, C::SUB, nt * G, 128, tid, C::SOFT);
-        zero_rows<NSUB>(smem + C::OFF_DO + j % ND * C::TILE, C::SUB, nt * G, 128, tid, C::SOFT);
-        tc::fence_proxy_async_smem();
-      }
-      auto weights = [&](float (&v)[16], int c) {   // P of columns 16 c ..
+      float w[2][16];
+      tc::tmem_ld16(dp_addr, w[0]);
+      tc::tmem_ld16(dp_addr + 16, w[1]);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float v[16];
+        tc::tmem_ld16(s_addr + 16 * c, v);
+        tc::tmem_wait_ld();
+        if (c == 0) {
+          tc::fence_before_sync();
+          mbar_arrive(&dp_free[j % NDP]);   // a later tile's dP^T may come
+        }
 #pragma unroll
         for (int e = 0; e < 16; e += 4) {
-          const float4 l = lse4[c * 4 + e / 4];
+          const float4 l = lse4[c * 4 + e / 4], d = del4[c * 4 + e / 4];
           weights2(v[e], v[e + 1], cc, make_float2(l.x, l.y));
           weights2(v[e + 2], v[e + 3], cc, make_float2(l.z, l.w));
-        }
-        if (masked) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (c * 16 + e < lo || c * 16 + e >= hi) v[e] = 0.f;
-        }
-      };
-      auto scores = [&](float (&w)[16], const float (&v)[16], int c) {   // their dS
-#pragma unroll
-        for (int e = 0; e < 16; e += 4) {
-          const float4 d = del4[c * 4 + e / 4];
-          scores2(w[e], w[e + 1], v[e], v[e + 1], make_float2(d.x, d.y));
-          scores2(w[e + 2], w[e + 3], v[e + 2], v[e + 3], make_float2(d.z, d.w));
+          scores2(w[c][e], w[c][e + 1], v[e], v[e + 1], make_float2(d.x, d.y));
+          scores2(w[c][e + 2], w[c][e + 3], v[e + 2], v[e + 3], make_float2(d.z, d.w));
         }
         if (masked) {   // (0 x NaN of another row is not 0)
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            if (c * 16 + e < lo || c * 16 + e >= hi) w[e] = 0.f;
+            if (c * 16 + e < lo || c * 16 + e >= hi) v[e] = w[c][e] = 0.f;
         }
-      };
-      float v[2][16], w[2][16];
-      tc::tmem_ld16(s_addr, v[0]);
-      if constexpr (kOneStep) {
-        tc::tmem_ld16(dp_addr, w[0]);
-        tc::tmem_ld16(dp_addr + 16, w[1]);
-        tc::tmem_wait_ld();
-        tc::fence_before_sync();
-        mbar_arrive(dp_free);   // the next tile's dP^T may come
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          if (c == 1) {
-            tc::tmem_ld16(s_addr + 16, v[1]);
-            tc::tmem_wait_ld();
-          }
-          weights(v[c], c);
-          scores(w[c], v[c], c);
-          store_packed(s_addr + 16 * c, v[c]);
-          store_packed(s_addr + 16 * c + 8, w[c]);
-        }
-      } else {
-        tc::tmem_ld16(s_addr + 16, v[1]);
-        tc::tmem_wait_ld();
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          weights(v[c], c);
-          store_packed(s_addr + 16 * c, v[c]);
-        }
-        tc::tmem_wait_st();
-        tc::fence_before_sync();
-        mbar_arrive(&p_full[0]);
-        if (!wwait(dp_full, j & 1)) { ok = false; break; }
-        tc::fence_after_sync();
-        tc::tmem_ld16(dp_addr, w[0]);
-        tc::tmem_ld16(dp_addr + 16, w[1]);
-        tc::tmem_wait_ld();
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          scores(w[c], v[c], c);
-          store_packed(dp_addr + 16 * c, w[c]);
-        }
+        store_packed(s_addr + 16 * c, v);
+        store_packed(s_addr + 16 * c + 8, w[c]);
+      }
+      if (nt < QB2) {
+        // The visible rows end inside the tile: those behind them may be another
+        // sequence's, whose NaN would pass through zero weights. Both products
+        // that read the tile along d are done.
+        zero_rows<NSUB>(smem + C::OFF_Q + j % NQ * C::Q_TILE, C::QSUB, nt * GT, QT, tid, C::GROUP);
+        zero_rows<NSUB>(smem + C::OFF_DO + j % ND * C::Q_TILE, C::QSUB, nt * GT, QT, tid, C::GROUP);
+        tc::fence_proxy_async_smem();
       }
       tc::tmem_wait_st();
       tc::fence_before_sync();
-      mbar_arrive(kOneStep ? &p_full[j % NSB] : ds_full);
+      mbar_arrive(&p_full[sb]);
     }
     // ------------------------------------------------------------ epilogue
     if (ok && n > 0) ok = wwait(all_done, 0);
     tc::fence_after_sync();
     const long long row = static_cast<long long>(p.Hkv) * s.k0 + static_cast<long long>(kvh) * s.lk + k0 + key;
     // four warps store 64 columns: dV's, then dK's
-    const int blk = tid >> 7;
+    const int blk = (warp - C::SOFT0) >> 2;
     const bool is_dk = blk >= NSUB;
     if (blk < 2 * NSUB)
       tc::store_o_rows<64>(lane_base + C::COL_DV + 64 * blk, !(ok && n > 0), is_dk ? p.sm_scale : 1.f,
@@ -670,35 +634,39 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
   }
 }
 
-// dQ. S = Q K^T and dP = dO V^T (M 128 query rows, N KT keys, K d; from shared
-// memory), dQ += dS K (N d, K KT; dS from TMEM, where it replaces S). Two S
-// buffers: S(j + 1) is there when the weights of tile j are done. At d 64 two
-// CTAs share an SM, so that one starts or ends while the other computes.
+// dQ. S = Q K^T and dP = dO V^T (M 128 query rows, N 64 keys, K d; from shared
+// memory), dQ += dS K (N d, K 64; dS from TMEM, where it replaces S). At d 64 two
+// CTAs of one group share an SM: one starts or ends while the other computes. At
+// d 128, where shared memory holds one CTA, it has two groups, which take
+// alternate tiles.
 template <int D>
 struct DqCfg {
   static constexpr int CTAS = D == 64 ? 2 : 1;      // CTAs of an SM
-  static constexpr int KT = D;                      // keys of a tile
+  static constexpr int NG = D / 64;                 // groups of a CTA
+  static constexpr int KT = 64;                     // keys of a tile
   static constexpr int SOFT0 = 4;                   // first warp of dS
-  static constexpr int SOFT = 4 * KT;               // their threads: 32 columns of a row each
-  static constexpr int THREADS = SOFT0 * 32 + SOFT;
+  static constexpr int GROUP = 256;                 // threads of a group: 32 columns of a row each
+  static constexpr int THREADS = SOFT0 * 32 + NG * GROUP;
   static constexpr int NSUB = D / 64;
   static constexpr int KSUB = KT * 128;
   static constexpr int QSUB = 128 * 128;
   static constexpr int K_TILE = NSUB * KSUB;
   static constexpr int Q_TILE = NSUB * QSUB;
-  static constexpr int NK = D == 64 ? 5 : 3;        // stages of K
-  static constexpr int NV = D == 64 ? 4 : 2;        // stages of V, which one product reads
+  static constexpr int NSB = 2 * NG;                // S buffers
+  static constexpr int NDP = NG;                    // dP buffers
+  static constexpr int NK = D == 64 ? 5 : 6;        // stages of K
+  static constexpr int NV = 4;                      // stages of V, which one product reads
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_DO = Q_TILE;
   static constexpr int OFF_K = 2 * Q_TILE;
   static constexpr int OFF_V = OFF_K + NK * K_TILE;
   static constexpr int OFF_BAR = OFF_V + NV * K_TILE;
-  static constexpr int N_BARS = 1 + 2 * NK + 2 * NV + 2 + 2 + 2 + 1 + 1 + 1 + 3;
+  static constexpr int N_BARS = 1 + 2 * NK + 2 * NV + 3 * NSB + 2 + NDP + 1 + 3;
   static constexpr int SMEM = 1024 + OFF_BAR + N_BARS * 8 + 16;
   static constexpr uint32_t COLS = 512 / CTAS;
   static constexpr uint32_t COL_S = 0;
-  static constexpr uint32_t COL_DP = 2 * KT;
-  static constexpr uint32_t COL_DQ = 3 * KT;
+  static constexpr uint32_t COL_DP = NSB * KT;
+  static constexpr uint32_t COL_DQ = COL_DP + NDP * KT;
   static_assert(COL_DQ + D <= COLS, "TMEM budget");
   static_assert((SMEM + 1024) * CTAS <= 233472, "shared memory budget");
 };
@@ -709,7 +677,7 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, DqCfg<D>::CTAS)
                    const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                    const BackParams p) {
   using C = DqCfg<D>;
-  constexpr int NK = C::NK, NV = C::NV, NSUB = C::NSUB, KT = C::KT;
+  constexpr int NK = C::NK, NV = C::NV, NSB = C::NSB, NDP = C::NDP, NG = C::NG, NSUB = C::NSUB, KT = C::KT;
   extern __shared__ uint8_t smem_raw[];
   if (static_cast<int>(blockIdx.x) < p.sink_blocks) {
     reduce_sinks<C::THREADS>(p, blockIdx.x, reinterpret_cast<float(*)[32]>(smem_raw));
@@ -723,12 +691,12 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, DqCfg<D>::CTAS)
   uint64_t* k_empty = k_full + NK;     // [NK] dQ, the last that reads the stage, done
   uint64_t* v_full = k_empty + NK;     // [NV]
   uint64_t* v_empty = v_full + NV;     // [NV] dP done
-  uint64_t* s_full = v_empty + NV;     // [2] S written
-  uint64_t* s_free = s_full + 2;       // [2] the dS in it read by dQ
-  uint64_t* ds_full = s_free + 2;      // [2] dS written (all softmax threads)
-  uint64_t* dp_full = ds_full + 2;     // dP written
-  uint64_t* dp_free = dp_full + 1;     // dP read (all softmax threads)
-  uint64_t* all_done = dp_free + 1;    // dQ
+  uint64_t* s_full = v_empty + NV;     // [NSB] S written
+  uint64_t* s_free = s_full + NSB;     // [NSB] the dS in it read by dQ
+  uint64_t* ds_full = s_free + NSB;    // [NSB] dS written (the group's arrivals)
+  uint64_t* dp_full = ds_full + NSB;   // [2] of even and odd tiles: dP written
+  uint64_t* dp_free = dp_full + 2;     // [NDP] dP read (the group's arrivals)
+  uint64_t* all_done = dp_free + NDP;  // dQ
   uint64_t* drain = all_done + 1;      // [3]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 3);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
@@ -766,13 +734,13 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, DqCfg<D>::CTAS)
       mbar_init(&v_full[i], 1);
       mbar_init(&v_empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < NSB; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&s_free[i], 1);
-      mbar_init(&ds_full[i], C::SOFT);
+      mbar_init(&ds_full[i], C::GROUP);
     }
-    mbar_init(dp_full, 1);
-    mbar_init(dp_free, C::SOFT);
+    for (int i = 0; i < 2; ++i) mbar_init(&dp_full[i], 1);
+    for (int i = 0; i < NDP; ++i) mbar_init(&dp_free[i], C::GROUP);
     mbar_init(all_done, 1);
     for (int i = 0; i < 3; ++i) mbar_init(&drain[i], 1);
     *abort_flag = 0;
@@ -845,11 +813,11 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, DqCfg<D>::CTAS)
     const uint64_t kd = tc::smem_desc_sw128(smem_u32(smem + C::OFF_K), 16, 1024);
     if (wwait(q_full, 0)) {
       for (int j = 0; j < n; ++j) {
-        if (j < 2 ? !wwait(&k_full[j % NK], 0)
-                  : !wwait2(&s_free[j & 1], ((j >> 1) - 1) & 1, &k_full[j % NK], j / NK & 1)) break;
+        if (j < NSB ? !wwait(&k_full[j % NK], j / NK & 1)
+                    : !wwait2(&s_free[j % NSB], (j / NSB - 1) & 1, &k_full[j % NK], j / NK & 1)) break;
         tc::fence_after_sync();
-        issue_ss<D, KT>(leader, tmem + C::COL_S + KT * (j & 1), qd, kd + j % NK * tile16, C::QSUB, C::KSUB);
-        if (leader) tc::commit(&s_full[j & 1]);
+        issue_ss<D, KT>(leader, tmem + C::COL_S + KT * (j % NSB), qd, kd + j % NK * tile16, C::QSUB, C::KSUB);
+        if (leader) tc::commit(&s_full[j % NSB]);
         __syncwarp();
       }
     }
@@ -860,12 +828,12 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, DqCfg<D>::CTAS)
     const uint64_t vd = tc::smem_desc_sw128(smem_u32(smem + C::OFF_V), 16, 1024);
     if (wwait(q_full, 0)) {
       for (int j = 0; j < n; ++j) {
-        if (j < 1 ? !wwait(&v_full[0], 0)
-                  : !wwait2(dp_free, (j - 1) & 1, &v_full[j % NV], j / NV & 1)) break;
+        if (j < NDP ? !wwait(&v_full[j % NV], 0)
+                    : !wwait2(&dp_free[j % NDP], (j / NDP - 1) & 1, &v_full[j % NV], j / NV & 1)) break;
         tc::fence_after_sync();
-        issue_ss<D, KT>(leader, tmem + C::COL_DP, dod, vd + j % NV * tile16, C::QSUB, C::KSUB);
+        issue_ss<D, KT>(leader, tmem + C::COL_DP + KT * (j % NDP), dod, vd + j % NV * tile16, C::QSUB, C::KSUB);
         if (leader) {
-          tc::commit(dp_full);
+          tc::commit(&dp_full[j & 1]);
           tc::commit(&v_empty[j % NV]);
         }
         __syncwarp();
@@ -876,11 +844,12 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, DqCfg<D>::CTAS)
     // ---------------------------------------------------------------- dQ += dS K
     const uint64_t kt = tc::smem_desc_sw128(smem_u32(smem + C::OFF_K), C::KSUB, 1024);   // MN-major
     for (int j = 0; j < n; ++j) {
-      if (!wwait(&ds_full[j & 1], j >> 1 & 1)) break;
+      if (!wwait(&ds_full[j % NSB], j / NSB & 1)) break;
       tc::fence_after_sync();
-      issue_ts<D, KT / 16>(leader, tmem + C::COL_DQ, tmem + C::COL_S + KT * (j & 1), kt + j % NK * tile16, j == 0);
+      issue_ts<D, KT / 16>(leader, tmem + C::COL_DQ, tmem + C::COL_S + KT * (j % NSB), kt + j % NK * tile16,
+                           j == 0);
       if (leader) {
-        tc::commit(&s_free[j & 1]);
+        tc::commit(&s_free[j % NSB]);
         tc::commit(&k_empty[j % NK]);
       }
       __syncwarp();
@@ -889,7 +858,8 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, DqCfg<D>::CTAS)
     finish(&drain[2]);
   } else {
     // ---------------------------------------------------------------- P and dS
-    const int tid = threadIdx.x - 32 * C::SOFT0;
+    const int grp = NG == 1 ? 0 : (threadIdx.x - 32 * C::SOFT0) / C::GROUP;   // tiles grp, grp + NG ...
+    const int tid = threadIdx.x - 32 * C::SOFT0 - grp * C::GROUP;
     const int cols = 32 * (tid >> 7);          // first of this thread's columns
     const int quad = warp & 3;
     const int row = quad * 32 + lane;
@@ -903,12 +873,11 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, DqCfg<D>::CTAS)
     const int lo_r = p.window > 0 ? max(0, pos - p.window + 1) : 0;
     float nlse = kNegInf, ndel = 0.f;
     if (valid) {
-      const float l = p.lse[at];
-      if (l != kNegInf) nlse = -l * kLog2e;   // (a row that sees nothing: P = 0)
-      ndel = -p.delta[at];
+      nlse = p.nlse[at];
+      ndel = p.ndelta[at];
     }
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    const uint32_t dp_addr = lane_base + C::COL_DP + cols;
+    const uint32_t dp_addr = lane_base + C::COL_DP + KT * grp + cols;
     const float2 cc = make_float2(p.scale_log2, p.scale_log2);
     const float2 nl = make_float2(nlse, nlse), nd = make_float2(ndel, ndel);
     // every row of the block sees every key of tiles [j_lo, j_hi) (rows that are not stored need no mask)
@@ -916,17 +885,17 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, DqCfg<D>::CTAS)
     const int j_hi = ((p.causal ? min(s.lk, pos0 + 1) : s.lk) - k_lo) / KT;
     if (p.window > 0) j_lo = max(0, (pos0 + nt - p.window - k_lo + KT - 1) / KT);
     bool ok = true;
-    for (int j = 0; j < n; ++j) {
+    for (int j = grp; j < n; j += NG) {
       const bool masked = j < j_lo || j >= j_hi;
       const int j0 = k_lo + j * KT;
       const int lo = lo_r - j0 - cols, hi = hi_r - j0 - cols;
-      const uint32_t s_addr = lane_base + C::COL_S + KT * (j & 1) + cols;
-      if (!wwait2(&s_full[j & 1], j >> 1 & 1, dp_full, j & 1)) { ok = false; break; }
+      const uint32_t s_addr = lane_base + C::COL_S + KT * (j % NSB) + cols;
+      if (!wwait2(&s_full[j % NSB], j / NSB & 1, &dp_full[j & 1], j >> 1 & 1)) { ok = false; break; }
       tc::fence_after_sync();
       if (j0 + KT > s.lk) {
         // The keys end inside the tile: the rows behind them are another head's or sequence's,
         // whose NaN would pass through zero weights. (S(j), the other reader, is done.)
-        zero_rows<NSUB>(smem + C::OFF_K + j % NK * C::K_TILE, C::KSUB, s.lk - j0, KT, tid, C::SOFT);
+        zero_rows<NSUB>(smem + C::OFF_K + j % NK * C::K_TILE, C::KSUB, s.lk - j0, KT, tid, C::GROUP);
         tc::fence_proxy_async_smem();
       }
       float w[2][16];
@@ -939,7 +908,7 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, DqCfg<D>::CTAS)
         tc::tmem_wait_ld();
         if (c == 0) {
           tc::fence_before_sync();
-          mbar_arrive(dp_free);   // the next tile's dP may come
+          mbar_arrive(&dp_free[grp]);   // a later tile's dP may come
         }
 #pragma unroll
         for (int e = 0; e < 16; e += 2) {
@@ -955,12 +924,12 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, DqCfg<D>::CTAS)
       }
       tc::tmem_wait_st();
       tc::fence_before_sync();
-      mbar_arrive(&ds_full[j & 1]);
+      mbar_arrive(&ds_full[j % NSB]);
     }
     // ------------------------------------------------------------ epilogue
     if (ok) ok = wwait(all_done, 0);
     tc::fence_after_sync();
-    const int blk = tid >> 7;   // four warps store 64 columns
+    const int blk = (warp - C::SOFT0) >> 2;   // four warps store 64 columns
     if (blk < NSUB)
       tc::store_o_rows<64>(lane_base + C::COL_DQ + 64 * blk, !ok, p.sm_scale, p.dq + at * D + 64 * blk,
                            valid, lane);
@@ -1007,7 +976,7 @@ int launch_back(BackParams& p, cudaStream_t stream) {
     set_error("too many work items");
     return SINKATTN_UNSUPPORTED;
   }
-  CUtensorMap tmQ, tmDo, tmK, tmV, tmK2, tmV2;
+  CUtensorMap tmQ, tmDo, tmQ2, tmDo2, tmK, tmV, tmK2, tmV2;
   const uint64_t kv_rows = static_cast<uint64_t>(p.Hkv) * p.total_k;
   const uint64_t q_rows = static_cast<uint64_t>(p.total_q);
   // (with no query rows nothing is copied through the maps of q and dout)
@@ -1016,6 +985,8 @@ int launch_back(BackParams& p, cudaStream_t stream) {
   int rc;
   if ((rc = make_q_tmap(&tmQ, q, q_rows, p.Hq, D, p.G, p.QB)) ||
       (rc = make_q_tmap(&tmDo, dout, q_rows, p.Hq, D, p.G, p.QB)) ||
+      (rc = make_q_tmap(&tmQ2, q, q_rows, p.Hq, D, p.GT, p.QB2)) ||
+      (rc = make_q_tmap(&tmDo2, dout, q_rows, p.Hq, D, p.GT, p.QB2)) ||
       (rc = make_rows_tmap(&tmK, p.k, kv_rows, D, DQ::KT, 128)) ||
       (rc = make_rows_tmap(&tmV, p.v, kv_rows, D, DQ::KT, 128)) ||
       (rc = make_rows_tmap(&tmK2, p.k, kv_rows, D, 128, 128)) ||
@@ -1031,7 +1002,7 @@ int launch_back(BackParams& p, cudaStream_t stream) {
   }
   if (dkv_items > 0) {
     back_dkv_kernel<D><<<static_cast<unsigned>(dkv_items), KV::THREADS, KV::SMEM, stream>>>(
-        tmQ, tmDo, tmK2, tmV2, p);
+        tmQ2, tmDo2, tmK2, tmV2, p);
     if ((rc = launched("dk, dv"))) return rc;
   }
   if (dq_items > 0) {
@@ -1067,10 +1038,13 @@ int launch_prefill_back(const BackArgs& a, cudaStream_t stream) {
   p.window = a.window < std::min(a.max_kv, a.total_k) ? a.window : 0;   // (one of all keys cuts nothing)
   p.QB = 128 / p.G;
   p.nqb = (a.max_q + p.QB - 1) / p.QB;
+  p.chunks = p.G > 64 ? 2 : 1;
+  p.GT = (p.G + p.chunks - 1) / p.chunks;
+  p.QB2 = 64 / p.GT;
   p.dq = static_cast<__nv_bfloat16*>(a.dq);
   p.dk = static_cast<__nv_bfloat16*>(a.dk);
   p.dv = static_cast<__nv_bfloat16*>(a.dv);
-  p.dsinks = a.dsinks; p.delta = a.delta; p.sink_part = a.sink_part;
+  p.dsinks = a.dsinks; p.nlse = a.nlse; p.ndelta = a.ndelta; p.sink_part = a.sink_part;
   p.per = back_block_tokens(a.total_q, a.Hq);
   p.delta_blocks = static_cast<int>(back_blocks(a.total_q, a.Hq));
   return a.d == 64 ? launch_back<64>(p, stream) : launch_back<128>(p, stream);
