@@ -47,7 +47,7 @@ struct BackParams {
   int per;       // tokens of a block of the delta pass
   int delta_blocks, sink_blocks;
   int QB, nqb;   // query tokens of a tile of 128 rows, tiles of the longest sequence
-  int GT, chunks, QB2;   // heads and tokens of a tile of 64 rows, tiles of a token
+  int GT, chunks, QB2;   // heads and tokens of a tile of the dk, dv pass, tiles of a token
 };
 
 __device__ __forceinline__ float dot8(uint4 x, uint4 y, float s) {
@@ -166,40 +166,50 @@ __device__ __forceinline__ bool try_wait_for(uint64_t* bar, uint32_t parity, uin
   return ok != 0;
 }
 
+// Between two tries of a wait that began at `since` (0: now): -1 where it is to be
+// given up, because another warp has, or because its time is over, else when it
+// began. (Out of line: the loops of the issuing warps are short, and what they
+// fetch of their instructions is what they cost.)
+__device__ __noinline__ long long give_up(long long since, volatile int* abort_flag, int* status) {
+  if (*abort_flag) return -1;
+  const long long now = clock64();
+  if (since == 0) return now;
+  if (now - since <= g_wait_limit_cycles) return since;
+  *abort_flag = 1;
+  atomicExch(status, SINKATTN_TIMEOUT);
+  return -1;
+}
+
 // A warp's bounded wait, as one uniform branch: the lanes leave together, so the
 // warp-collective TMEM accesses that follow never run with some of them missing.
 // A try is suspended for up to 20 us, because a warp that polls takes issue slots
-// from the ones that compute; the time and the abort flag are looked at between tries.
+// from the ones that compute.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                           int* status) {
-  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-  const long long t0 = clock64();
-  while (!__all_sync(0xffffffffu, try_wait_for(bar, parity, 20000u))) {
-    if (__any_sync(0xffffffffu, *abort_flag)) return false;
-    if (__any_sync(0xffffffffu, clock64() - t0 > g_wait_limit_cycles)) {
-      *abort_flag = 1;
-      atomicExch(status, SINKATTN_TIMEOUT);
-      return false;
-    }
-  }
+  long long since = 0;
+  while (!__all_sync(0xffffffffu, try_wait_for(bar, parity, 20000u)))
+    if (__any_sync(0xffffffffu, (since = give_up(since, abort_flag, status)) < 0)) return false;
   return true;
 }
-
-// The same for two or three barriers: where all are done, which is the rule here,
-// they cost about as much as one.
 __device__ __forceinline__ bool warp_wait2(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb,
                                            volatile int* abort_flag, int* status) {
-  const bool ra = mbar_try_wait(a, pa), rb = mbar_try_wait(b, pb);
-  if (__all_sync(0xffffffffu, ra && rb)) return true;
-  return warp_wait(a, pa, abort_flag, status) && warp_wait(b, pb, abort_flag, status);
+  long long since = 0;
+  while (true) {
+    const bool ra = try_wait_for(a, pa, 20000u), rb = try_wait_for(b, pb, 20000u);
+    if (__all_sync(0xffffffffu, ra && rb)) return true;
+    if (__any_sync(0xffffffffu, (since = give_up(since, abort_flag, status)) < 0)) return false;
+  }
 }
 __device__ __forceinline__ bool warp_wait3(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb,
                                            uint64_t* c, uint32_t pc, volatile int* abort_flag,
                                            int* status) {
-  const bool ra = mbar_try_wait(a, pa), rb = mbar_try_wait(b, pb), rc = mbar_try_wait(c, pc);
-  if (__all_sync(0xffffffffu, ra && rb && rc)) return true;
-  return warp_wait(a, pa, abort_flag, status) && warp_wait(b, pb, abort_flag, status) &&
-         warp_wait(c, pc, abort_flag, status);
+  long long since = 0;
+  while (true) {
+    const bool ra = try_wait_for(a, pa, 20000u), rb = try_wait_for(b, pb, 20000u),
+               rc = try_wait_for(c, pc, 20000u);
+    if (__all_sync(0xffffffffu, ra && rb && rc)) return true;
+    if (__any_sync(0xffffffffu, (since = give_up(since, abort_flag, status)) < 0)) return false;
+  }
 }
 
 // Zeros rows [from, to) of a tile of NSUB swizzled sub-tiles in shared memory.
@@ -272,27 +282,28 @@ __device__ __forceinline__ void store_packed(uint32_t addr, const float (&v)[16]
   tc::tmem_st8(addr, pk);
 }
 
-// dK, dV. S^T = K Q^T and dP^T = V dO^T (M 128 keys, N 64 query rows, K d; all
-// from shared memory), dV += P^T dO and dK += dS^T Q (M 128 keys, N d, K 64; P^T and
+// dK, dV. S^T = K Q^T and dP^T = V dO^T (M 128 keys, N QT query rows, K d; all from
+// shared memory), dV += P^T dO and dK += dS^T Q (M 128 keys, N d, K QT; P^T and
 // dS^T from TMEM, where both replace S^T). Keys in the TMEM lanes make P^T and
 // dS^T the MMA's A operand as they are. dP^T is free as soon as it has been read.
-// A tile is QB2 tokens times GT heads; groups of more than 64 heads come in two chunks.
+// A tile is QB2 tokens times GT heads; groups of more heads than it has rows come
+// in two chunks.
 template <int D>
 struct DkvCfg {
   static constexpr int SOFT0 = 4;                   // first warp of P and dS
-  static constexpr int GROUP = 256;                 // threads of a group; two groups take alternate tiles
-  static constexpr int THREADS = SOFT0 * 32 + 2 * GROUP;
+  static constexpr int NG = D / 64;                 // groups of warps, which take alternate tiles
+  static constexpr int QT = D == 64 ? 128 : 64;     // query rows of a tile
+  static constexpr int GROUP = 128 * QT / 32;       // threads of a group
+  static constexpr int THREADS = SOFT0 * 32 + NG * GROUP;
   static constexpr int NSUB = D / 64;
-  static constexpr int QT = 64;                     // query rows of a tile
   static constexpr int KSUB = 128 * 128;            // [128 keys][64 bf16], 128B-swizzled
   static constexpr int QSUB = QT * 128;
   static constexpr int K_TILE = NSUB * KSUB;
   static constexpr int Q_TILE = NSUB * QSUB;
-  static constexpr int NSB = D == 64 ? 4 : 3;       // S^T buffers
-  static constexpr int NDP = D == 64 ? 2 : 1;       // dP^T buffers
-  static constexpr int NB = D == 64 ? 4 : 6;        // tiles after which buffer and group repeat
-  static constexpr int NQ = D == 64 ? 8 : 6;        // stages of Q
-  static constexpr int ND = D == 64 ? 8 : 4;        // stages of dO, which is held for a shorter time
+  static constexpr int NSB = D == 64 ? 2 : 3;       // S^T buffers
+  static constexpr int NB = D == 64 ? 2 : 6;        // tiles after which buffer and group repeat
+  static constexpr int NQ = D == 64 ? 5 : 6;        // stages of Q
+  static constexpr int ND = 4;                      // stages of dO, which is held for a shorter time
   static constexpr int OFF_K = 0;
   static constexpr int OFF_V = K_TILE;
   static constexpr int OFF_Q = 2 * K_TILE;
@@ -300,12 +311,12 @@ struct DkvCfg {
   static constexpr int NR = 4;                      // slots of the rows' lse and delta
   static constexpr int OFF_ROW = OFF_DO + ND * Q_TILE;   // [NR][-lse log2 e, -delta][QT]
   static constexpr int OFF_BAR = OFF_ROW + NR * 2 * QT * 4;
-  static constexpr int N_BARS = 1 + 2 * NQ + 2 * ND + NB + NR + 2 * NSB + 2 + NDP + 1 + 3;
-  static_assert(NR % 2 == 0 && NR <= ND && ND <= NQ, "order of the copies");
+  static constexpr int N_BARS = 1 + 2 * NQ + 2 * ND + NB + NR + 2 * NSB + 2 + 1 + 1 + 3;
+  static_assert(NR % NG == 0 && NR <= ND && ND <= NQ, "order of the copies");
   static constexpr int SMEM = OFF_BAR + N_BARS * 8 + 16;
   static constexpr uint32_t COL_S = 0;
   static constexpr uint32_t COL_DP = QT * NSB;
-  static constexpr uint32_t COL_DV = COL_DP + QT * NDP;
+  static constexpr uint32_t COL_DV = COL_DP + QT;
   static constexpr uint32_t COL_DK = COL_DV + D;
   static_assert(COL_DK + D <= 512, "TMEM budget");
   static_assert(SMEM <= 232448, "shared memory budget");
@@ -317,7 +328,7 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
                     const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                     const BackParams p) {
   using C = DkvCfg<D>;
-  constexpr int NQ = C::NQ, ND = C::ND, NSB = C::NSB, NDP = C::NDP, NB = C::NB, NR = C::NR, NSUB = C::NSUB,
+  constexpr int NQ = C::NQ, ND = C::ND, NSB = C::NSB, NG = C::NG, NB = C::NB, NR = C::NR, NSUB = C::NSUB,
                 QT = C::QT;
   extern __shared__ __align__(1024) uint8_t smem[];   // (swizzled tiles start on 1024 bytes)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
@@ -331,8 +342,8 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
   uint64_t* s_free = row_full + NR;    // [NSB] the P^T and dS^T in it read
   uint64_t* p_full = s_free + NSB;     // [NSB] P^T and dS^T written (the group's arrivals)
   uint64_t* dp_full = p_full + NSB;    // [2] of even and odd tiles: dP^T written
-  uint64_t* dp_free = dp_full + 2;     // [NDP] dP^T read (the group's arrivals)
-  uint64_t* all_done = dp_free + NDP;  // dV and dK
+  uint64_t* dp_free = dp_full + 2;     // dP^T read (the group's arrivals)
+  uint64_t* all_done = dp_free + 1;    // dV and dK
   uint64_t* drain = all_done + 1;      // [3]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 3);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
@@ -377,7 +388,7 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
       mbar_init(&p_full[i], C::GROUP);
     }
     for (int i = 0; i < 2; ++i) mbar_init(&dp_full[i], 1);
-    for (int i = 0; i < NDP; ++i) mbar_init(&dp_free[i], C::GROUP);
+    mbar_init(dp_free, C::GROUP);
     mbar_init(all_done, 1);
     for (int i = 0; i < 3; ++i) mbar_init(&drain[i], 1);
     *abort_flag = 0;
@@ -435,26 +446,27 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
       }
     }
     __syncwarp();
-    // -lse log2(e) and -delta of rows 2 l and 2 l + 1 of a tile, by lane l. A row outside the tile
+    // -lse log2(e) and -delta of a tile's rows, QT / 32 a lane. A row outside the tile
     // gets lse = +inf: P = 0. Both kinds of writes arrive, the copies when they have landed.
-    int rt[2], rh[2];
+    constexpr int kRows = QT / 32;
+    int rt[kRows], rh[kRows];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      rt[e] = (2 * lane + e) / GT;
-      rh[e] = (2 * lane + e) % GT;
+    for (int e = 0; e < kRows; ++e) {
+      rt[e] = (lane + 32 * e) / GT;
+      rh[e] = (lane + 32 * e) % GT;
     }
     auto load_rows = [&](int j) {
-      float* to = reinterpret_cast<float*>(smem + C::OFF_ROW) + j % NR * 2 * QT + 2 * lane;
+      float* to = reinterpret_cast<float*>(smem + C::OFF_ROW) + j % NR * 2 * QT + lane;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
+      for (int e = 0; e < kRows; ++e) {
         const int i = i0 + (j >> cs) * QB2 + rt[e], h = (j & cs) * GT + rh[e];
-        if (2 * lane + e < rows && i < i1 && h < p.G) {
+        if (lane + 32 * e < rows && i < i1 && h < p.G) {
           const long long at = static_cast<long long>(s.q0 + i) * p.Hq + kvh * p.G + h;
-          copy4_async(to + e, p.nlse + at);
-          copy4_async(to + QT + e, p.ndelta + at);
+          copy4_async(to + 32 * e, p.nlse + at);
+          copy4_async(to + QT + 32 * e, p.ndelta + at);
         } else {
-          to[e] = kNegInf;
-          to[QT + e] = 0.f;
+          to[32 * e] = kNegInf;
+          to[QT + 32 * e] = 0.f;
         }
       }
       mbar_arrive(&row_full[j % NR]);
@@ -498,10 +510,10 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
     const uint64_t dod = tc::smem_desc_sw128(smem_u32(smem + C::OFF_DO), 16, 1024);
     if (n > 0 && wwait(kv_full, 0)) {
       for (int j = 0; j < n; ++j) {
-        if (j < NDP ? !wwait(&do_full[j % ND], 0)
-                    : !wwait2(&dp_free[j % NDP], (j / NDP - 1) & 1, &do_full[j % ND], j / ND & 1)) break;
+        if (j < 1 ? !wwait(&do_full[0], 0)
+                  : !wwait2(dp_free, (j - 1) & 1, &do_full[j % ND], j / ND & 1)) break;
         tc::fence_after_sync();
-        issue_ss<D, QT>(leader, tmem + C::COL_DP + QT * (j % NDP), vd, dod + j % ND * tile16, C::KSUB, C::QSUB);
+        issue_ss<D, QT>(leader, tmem + C::COL_DP, vd, dod + j % ND * tile16, C::KSUB, C::QSUB);
         if (leader) tc::commit(&dp_full[j & 1]);
         __syncwarp();
       }
@@ -529,7 +541,7 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
     finish(&drain[2]);
   } else {
     // ---------------------------------------------------------------- P and dS
-    const int grp = (threadIdx.x - 32 * C::SOFT0) / C::GROUP;   // tiles grp, grp + 2 ...
+    const int grp = NG == 1 ? 0 : (threadIdx.x - 32 * C::SOFT0) / C::GROUP;   // tiles grp, grp + NG ...
     const int tid = threadIdx.x - 32 * C::SOFT0 - grp * C::GROUP;
     const int cols = 32 * (tid >> 7);          // first of this thread's columns
     const int quad = warp & 3;                 // TMEM lane quadrant this warp may access
@@ -542,7 +554,7 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
     if (p.window > 0) b_hi = min(b_hi, (k0 + p.window - off - i0) / QB2);
     const float2 cc = make_float2(p.scale_log2, p.scale_log2);
     bool ok = true;
-    for (int j = grp; j < n; j += 2) {
+    for (int j = grp; j < n; j += NG) {
       const int sb = j % NSB;
       const bool masked = (j >> cs) < b_lo || (j >> cs) >= b_hi;
       int lo = -128, hi = 128, nt = QB2;         // this thread's visible columns
@@ -554,10 +566,10 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
         hi = (p.window > 0 ? max(0, min(nt, k0 + key + p.window - pos0)) : nt) * GT - cols;
       }
       const uint32_t s_addr = lane_base + C::COL_S + QT * sb + cols;
-      const uint32_t dp_addr = lane_base + C::COL_DP + QT * (j % NDP) + cols;
+      const uint32_t dp_addr = lane_base + C::COL_DP + cols;
       const float4* lse4 = reinterpret_cast<const float4*>(row_s + j % NR * 2 * QT);
       const float4* del4 = lse4 + QT / 4;
-      if (!warp_wait3(&row_full[j % NR], j / NR & 1, &s_full[j % NB], j / NB & 1, &dp_full[grp], j >> 1 & 1,
+      if (!warp_wait3(&row_full[j % NR], j / NR & 1, &s_full[j % NB], j / NB & 1, &dp_full[j & 1], j >> 1 & 1,
                       abort_flag, status)) {
         ok = false;
         break;
@@ -573,7 +585,7 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
         tc::tmem_wait_ld();
         if (c == 0) {
           tc::fence_before_sync();
-          mbar_arrive(&dp_free[j % NDP]);   // a later tile's dP^T may come
+          mbar_arrive(dp_free);   // the next tile's dP^T may come
         }
 #pragma unroll
         for (int e = 0; e < 16; e += 4) {
@@ -1038,9 +1050,10 @@ int launch_prefill_back(const BackArgs& a, cudaStream_t stream) {
   p.window = a.window < std::min(a.max_kv, a.total_k) ? a.window : 0;   // (one of all keys cuts nothing)
   p.QB = 128 / p.G;
   p.nqb = (a.max_q + p.QB - 1) / p.QB;
-  p.chunks = p.G > 64 ? 2 : 1;
+  const int rows = a.d == 64 ? DkvCfg<64>::QT : DkvCfg<128>::QT;
+  p.chunks = p.G > rows ? 2 : 1;
   p.GT = (p.G + p.chunks - 1) / p.chunks;
-  p.QB2 = 64 / p.GT;
+  p.QB2 = rows / p.GT;
   p.dq = static_cast<__nv_bfloat16*>(a.dq);
   p.dk = static_cast<__nv_bfloat16*>(a.dk);
   p.dv = static_cast<__nv_bfloat16*>(a.dv);
