@@ -222,9 +222,9 @@ struct BackArgs {
   float* sink_part;                     // [back_blocks(), Hq]
 };
 // Rows of sink_part: blocks of query tokens of the pass that computes delta.
-int back_block_tokens(int32_t total_q, int32_t Hq);
+int back_block_tokens(int32_t Hq);
 inline int64_t back_blocks(int32_t total_q, int32_t Hq) {
-  const int64_t per = back_block_tokens(total_q, Hq);
+  const int64_t per = back_block_tokens(Hq);
   return (total_q + per - 1) / per;
 }
 int launch_prefill_back(const BackArgs& a, cudaStream_t stream);

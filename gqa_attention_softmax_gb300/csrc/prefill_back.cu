@@ -25,6 +25,7 @@
 // SINKATTN_TIMEOUT, drains its copies and MMAs, frees TMEM and exits.
 #include <algorithm>
 
+#include "chain.cuh"
 #include "common.cuh"
 #include "internal.h"
 #include "tc.cuh"
@@ -46,6 +47,7 @@ struct BackParams {
   float *dsinks, *nlse, *ndelta, *sink_part;   // (workspace: [total_q, Hq] -lse log2 e, -delta)
   int per;       // tokens of a block of the delta pass
   int delta_blocks, sink_blocks;
+  int dq_waits;  // there is no pass of dk and dv between the delta pass and that of dq
   int QB, nqb;   // query tokens of a tile of 128 rows, tiles of the longest sequence
   int GT, chunks, QB2;   // heads and tokens of a tile of the dk, dv pass, tiles of a token
 };
@@ -60,7 +62,7 @@ __device__ __forceinline__ float dot8(uint4 x, uint4 y, float s) {
   return s;
 }
 
-constexpr int kDeltaRows = 1024;   // rows (token, head) of a block of the delta pass at most
+constexpr int kDeltaRows = 256;    // rows (token, head) of a block of the delta pass at most
 constexpr int kDeltaHeads = 256;   // heads of a block
 
 // -delta and -lse log2 e of p.per tokens and up to kDeltaHeads heads, d / 8 threads a
@@ -70,6 +72,7 @@ __global__ void __launch_bounds__(256) back_delta_kernel(const BackParams p) {
   constexpr int C = D / 8;
   constexpr int kIlp = 4;   // rows of a thread in flight
   __shared__ float term[kDeltaRows];
+  grid_launch_dependents();
   const int h0 = blockIdx.y * kDeltaHeads;
   const int nh = min(kDeltaHeads, p.Hq - h0);
   const int t0 = blockIdx.x * p.per;
@@ -127,7 +130,7 @@ __device__ __forceinline__ void reduce_sinks(const BackParams& p, int chunk, flo
   if (h < p.Hq) {
 #pragma unroll 8
     for (int b = slice; b < p.delta_blocks; b += kSlices)
-      x += p.sink_part[static_cast<long long>(b) * p.Hq + h];
+      x += __ldcg(&p.sink_part[static_cast<long long>(b) * p.Hq + h]);
   }
   s[slice][threadIdx.x % 32] = x;
   __syncthreads();
@@ -357,12 +360,12 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
   const int kvh = static_cast<int>(blockIdx.x) % per % p.Hkv;
   const int b = static_cast<int>(blockIdx.x) % per / p.Hkv;
   const Seq s = load_seq(p, b);
-  if (!s.ok) {
-    if (threadIdx.x == 0) atomicExch(status, SINKATTN_BAD_LENGTHS);
+  if (!s.ok && threadIdx.x == 0) atomicExch(status, SINKATTN_BAD_LENGTHS);
+  const int k0 = kt * 128;
+  if (!s.ok || k0 >= s.lk) {   // uniform over the CTA, before any barrier or TMEM use
+    grid_dependency_wait();    // (the next launch takes it that the one before this is done)
     return;
   }
-  const int k0 = kt * 128;
-  if (k0 >= s.lk) return;   // uniform over the CTA, before any barrier or TMEM use
   const int nk = min(128, s.lk - k0);
   const int off = s.lk - s.lq;   // position of query 0
   // queries [i0, i1) see some key of the tile
@@ -472,18 +475,28 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
       mbar_arrive(&row_full[j % NR]);
       arrive_after_copies(&row_full[j % NR]);
     };
+    auto load_q = [&](int x) {
+      issued_q = x + 1;
+      load(&tmQ, x, smem + C::OFF_Q + x % NQ * C::Q_TILE, &q_full[x % NQ]);
+    };
+    auto load_do = [&](int y) {
+      issued_do = y + 1;
+      load(&tmDo, y, smem + C::OFF_DO + y % ND * C::Q_TILE, &do_full[y % ND]);
+    };
+    // The first tiles' copies need nothing of the launch before this one, the rows do.
+    // The next launch's blocks may take the SMs that this one leaves.
+    for (int x = 0; x < min(NQ, n); ++x) load_q(x);
+    for (int y = 0; y < min(ND, n); ++y) load_do(y);
+    grid_dependency_wait();
+    grid_launch_dependents();
     // Q of tile x, and the tiles whose dO and rows take the places of the same tile x - NQ
     for (int x = 0; x < n + NQ - NR; ++x) {
       if (x >= NQ && !wwait(&q_empty[x % NQ], (x / NQ - 1) & 1)) break;
-      if (x < n) {
-        issued_q = x + 1;
-        load(&tmQ, x, smem + C::OFF_Q + x % NQ * C::Q_TILE, &q_full[x % NQ]);
-      }
+      if (x >= NQ && x < n) load_q(x);
       const int y = x - (NQ - ND), z = x - (NQ - NR);
-      if (y >= 0 && y < n) {
-        if (y >= ND && !wwait(&do_empty[y % ND], (y / ND - 1) & 1)) break;
-        issued_do = y + 1;
-        load(&tmDo, y, smem + C::OFF_DO + y % ND * C::Q_TILE, &do_full[y % ND]);
+      if (y >= ND && y < n) {
+        if (!wwait(&do_empty[y % ND], (y / ND - 1) & 1)) break;
+        load_do(y);
       }
       if (z >= 0) load_rows(z);
     }
@@ -684,10 +697,9 @@ struct DqCfg {
 };
 
 template <int D>
-__global__ void __launch_bounds__(DqCfg<D>::THREADS, DqCfg<D>::CTAS)
-    back_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmDo,
-                   const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                   const BackParams p) {
+__device__ __forceinline__ void back_dq_block(const CUtensorMap& tmQ, const CUtensorMap& tmDo,
+                                              const CUtensorMap& tmK, const CUtensorMap& tmV,
+                                              const BackParams& p) {
   using C = DqCfg<D>;
   constexpr int NK = C::NK, NV = C::NV, NSB = C::NSB, NDP = C::NDP, NG = C::NG, NSUB = C::NSUB, KT = C::KT;
   extern __shared__ uint8_t smem_raw[];
@@ -885,8 +897,8 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, DqCfg<D>::CTAS)
     const int lo_r = p.window > 0 ? max(0, pos - p.window + 1) : 0;
     float nlse = kNegInf, ndel = 0.f;
     if (valid) {
-      nlse = p.nlse[at];
-      ndel = p.ndelta[at];
+      nlse = __ldcg(&p.nlse[at]);
+      ndel = __ldcg(&p.ndelta[at]);
     }
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const uint32_t dp_addr = lane_base + C::COL_DP + KT * grp + cols;
@@ -962,8 +974,21 @@ __global__ void __launch_bounds__(DqCfg<D>::THREADS, DqCfg<D>::CTAS)
   }
 }
 
-int launched(const char* what) {
-  const cudaError_t e = cudaGetLastError();
+// This launch needs nothing of the one before it (the pass of dk and dv, which
+// has waited for the pass before that): its blocks start where those leave
+// room. What the delta pass wrote is loaded around L1. The first block ends
+// after that launch, so that whoever waits for this one has waited for both.
+template <int D>
+__global__ void __launch_bounds__(DqCfg<D>::THREADS, DqCfg<D>::CTAS)
+    back_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmDo,
+                   const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                   const BackParams p) {
+  if (p.dq_waits) grid_dependency_wait();
+  back_dq_block<D>(tmQ, tmDo, tmK, tmV, p);
+  if (blockIdx.x == 0) grid_dependency_wait();
+}
+
+int launched(const char* what, cudaError_t e) {
   if (e == cudaSuccess) return SINKATTN_OK;
   set_error("%s launch: %s", what, cudaGetErrorString(e));
   return SINKATTN_CUDA_ERROR;
@@ -1003,6 +1028,7 @@ int launch_back(BackParams& p, cudaStream_t stream) {
       (rc = make_rows_tmap(&tmV, p.v, kv_rows, D, DQ::KT, 128)) ||
       (rc = make_rows_tmap(&tmK2, p.k, kv_rows, D, 128, 128)) ||
       (rc = make_rows_tmap(&tmV2, p.v, kv_rows, D, 128, 128)) ||
+      (rc = set_smem(set_chained_smem(back_delta_kernel<D>, 0))) ||
       (rc = set_smem(set_chained_smem(back_dkv_kernel<D>, KV::SMEM))) ||
       (rc = set_smem(set_chained_smem(back_dq_kernel<D>, DQ::SMEM))))
     return rc;
@@ -1010,27 +1036,29 @@ int launch_back(BackParams& p, cudaStream_t stream) {
     back_delta_kernel<D><<<dim3(static_cast<unsigned>(p.delta_blocks),
                                 static_cast<unsigned>((p.Hq + kDeltaHeads - 1) / kDeltaHeads)),
                            256, 0, stream>>>(p);
-    if ((rc = launched("delta"))) return rc;
+    if ((rc = launched("delta", cudaGetLastError()))) return rc;
   }
   if (dkv_items > 0) {
-    back_dkv_kernel<D><<<static_cast<unsigned>(dkv_items), KV::THREADS, KV::SMEM, stream>>>(
-        tmQ2, tmDo2, tmK2, tmV2, p);
-    if ((rc = launched("dk, dv"))) return rc;
+    const dim3 grid(static_cast<unsigned>(dkv_items));
+    cudaError_t e;
+    if (p.delta_blocks > 0) {
+      e = launch_chained(back_dkv_kernel<D>, grid, KV::THREADS, KV::SMEM, stream, tmQ2, tmDo2, tmK2, tmV2, p);
+    } else {   // the first launch of the call reads its inputs at once
+      back_dkv_kernel<D><<<grid, KV::THREADS, KV::SMEM, stream>>>(tmQ2, tmDo2, tmK2, tmV2, p);
+      e = cudaGetLastError();
+    }
+    if ((rc = launched("dk, dv", e))) return rc;
   }
-  if (dq_items > 0) {
-    back_dq_kernel<D><<<static_cast<unsigned>(dq_items), DQ::THREADS, DQ::SMEM, stream>>>(
-        tmQ, tmDo, tmK, tmV, p);
-    return launched("dq");
-  }
-  return SINKATTN_OK;
+  p.dq_waits = dkv_items == 0;
+  if (dq_items == 0) return SINKATTN_OK;
+  return launched("dq", launch_chained(back_dq_kernel<D>, dim3(static_cast<unsigned>(dq_items)), DQ::THREADS,
+                                       DQ::SMEM, stream, tmQ, tmDo, tmK, tmV, p));
 }
 
 }  // namespace
 
-// Rows of a block: 1024 where that leaves every SM several blocks, else 256.
-int back_block_tokens(int32_t total_q, int32_t Hq) {
-  const bool many = static_cast<int64_t>(total_q) * Hq >= int64_t{4 * 152} * kDeltaRows;
-  return std::max(1, (many ? kDeltaRows : kDeltaRows / 4) / std::min<int32_t>(Hq, kDeltaHeads));
+int back_block_tokens(int32_t Hq) {
+  return std::max(1, kDeltaRows / std::min<int32_t>(Hq, kDeltaHeads));
 }
 
 int launch_prefill_back(const BackArgs& a, cudaStream_t stream) {
@@ -1058,7 +1086,7 @@ int launch_prefill_back(const BackArgs& a, cudaStream_t stream) {
   p.dk = static_cast<__nv_bfloat16*>(a.dk);
   p.dv = static_cast<__nv_bfloat16*>(a.dv);
   p.dsinks = a.dsinks; p.nlse = a.nlse; p.ndelta = a.ndelta; p.sink_part = a.sink_part;
-  p.per = back_block_tokens(a.total_q, a.Hq);
+  p.per = back_block_tokens(a.Hq);
   p.delta_blocks = static_cast<int>(back_blocks(a.total_q, a.Hq));
   return a.d == 64 ? launch_back<64>(p, stream) : launch_back<128>(p, stream);
 }
