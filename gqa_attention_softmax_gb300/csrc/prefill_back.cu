@@ -76,22 +76,31 @@ __global__ void __launch_bounds__(256) back_delta_kernel(const BackParams p) {
   const int h0 = blockIdx.y * kDeltaHeads;
   const int nh = min(kDeltaHeads, p.Hq - h0);
   const int t0 = blockIdx.x * p.per;
-  const int total = min(p.total_q, p.cu_q[p.batch]);   // rows behind it are not read
-  const int nt = min(p.per, total - t0);
-  const int rows = max(nt, 0) * nh;
+  const int total = p.sinks ? p.cu_q[p.batch] : 0;   // (rows behind it have no gradient)
+  const int nt = min(p.per, p.total_q - t0);
+  const int rows = nt * nh;
   const int c = threadIdx.x % C;
+  const float per_head = 1.f / nh;   // (r + 1/2) / nh is off by less than 1 / (2 nh): rows < 2^9, nh <= 2^8
   for (int base = 0; base < rows; base += kIlp * 256 / C) {
-    float s[kIlp];
+    float s[kIlp], lse[kIlp], dlse[kIlp], sink[kIlp];
     long long at[kIlp];
+    int tok[kIlp];
     uint4 x[kIlp], y[kIlp];
 #pragma unroll
     for (int i = 0; i < kIlp; ++i) {
       const int r = base + i * (256 / C) + threadIdx.x / C;
       x[i] = y[i] = make_uint4(0, 0, 0, 0);
       if (r < rows) {
-        at[i] = static_cast<long long>(t0 + r / nh) * p.Hq + h0 + r % nh;
+        tok[i] = t0 + __float2int_rz((r + 0.5f) * per_head);
+        const int h = h0 + r - (tok[i] - t0) * nh;
+        at[i] = static_cast<long long>(tok[i]) * p.Hq + h;
         x[i] = __ldg(reinterpret_cast<const uint4*>(p.dout + at[i] * D) + c);
         y[i] = __ldcs(reinterpret_cast<const uint4*>(p.out + at[i] * D) + c);
+        if (c == 0) {
+          lse[i] = p.lse[at[i]];
+          dlse[i] = p.dlse ? p.dlse[at[i]] : 0.f;
+          sink[i] = p.sinks ? p.sinks[h] : 0.f;
+        }
       }
     }
 #pragma unroll
@@ -101,13 +110,11 @@ __global__ void __launch_bounds__(256) back_delta_kernel(const BackParams p) {
 #pragma unroll
       for (int m = 1; m < C; m <<= 1) s[i] += __shfl_xor_sync(0xffffffffu, s[i], m);
       if (r < rows && c == 0) {
-        if (p.dlse) s[i] -= p.dlse[at[i]];
-        const float lse = p.lse[at[i]];
-        p.ndelta[at[i]] = -s[i];
+        const float delta = s[i] - dlse[i];
+        p.ndelta[at[i]] = -delta;
         // a row that sees nothing (lse -inf) has P = 0, as for lse +inf
-        p.nlse[at[i]] = lse == kNegInf ? kNegInf : -lse * kLog2e;
-        // (then there is no sink)
-        if (p.sinks) term[r] = -expf(p.sinks[h0 + r % nh] - lse) * s[i];
+        p.nlse[at[i]] = lse[i] == kNegInf ? kNegInf : -lse[i] * kLog2e;
+        if (p.sinks) term[r] = tok[i] < total ? -expf(sink[i] - lse[i]) * delta : 0.f;
       }
     }
   }

@@ -47,6 +47,7 @@ struct RopeParams {
   const float *q_weight, *k_weight;         // [d] or nullptr
   float eps, factor;
   int tokens, batch, Hq, Hkv, r;
+  uint32_t inv_heads;                       // ceil(2^32 / (Hq + 2 Hkv))
   int per_block, parts;                     // tokens of a block; blocks that share its heads
   __nv_bfloat16 *q_out, *k_out, *v_out;     // pack; append: q_out
   // append
@@ -254,7 +255,7 @@ __device__ __forceinline__ void prepare_tokens(const RopeParams& p, int tok0, in
 template <int D, int LAYOUT, int KIND>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
   constexpr int C = D / 8;                 // threads of a head
-  constexpr int kIlp = 2;
+  constexpr int kIlp = 4;
   __shared__ float2 cs[kMaxTokens][D / 2];
   __shared__ Token info[kMaxTokens];
   __shared__ int pos_s[kMaxTokens];
@@ -287,7 +288,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
       tok[i] = -1;
       raw[i] = make_uint4(0, 0, 0, 0);
       if (row >= rows) continue;
-      const int t = row / heads;
+      const int t = static_cast<int>(__umulhi(row, p.inv_heads));
       const int h = row - t * heads;
       const long long g = tok0 + t;
       if (KIND == kPack && info[t].row < 0) continue;
@@ -391,7 +392,7 @@ __global__ void __launch_bounds__(kThreads) rope_backward_kernel(const RopeParam
         head[i] = 0;
         raw[i] = xr[i] = make_uint4(0, 0, 0, 0);
         if (row >= rows) continue;
-        const int t = row / heads;
+        const int t = static_cast<int>(__umulhi(row, p.inv_heads));
         const int h = row - t * heads;
         const long long g = tok0 + t;
         const Token at = info[t];
@@ -515,7 +516,7 @@ int rope_args(int32_t tokens, int32_t Hq, int32_t Hkv, int32_t d, const uint64_t
   set_error("%s", "");
   if (tokens < 0) return refuse(SINKATTN_INVALID_ARG, "tokens must be non-negative");
   if (Hq < 1 || Hkv < 1) return refuse(SINKATTN_INVALID_ARG, "head counts must be positive");
-  if (Hq > 65536 || Hkv > 65536) return refuse(SINKATTN_UNSUPPORTED, "more than 2^16 heads");
+  if (Hq > 4096 || Hkv > 4096) return refuse(SINKATTN_UNSUPPORTED, "more than 4096 heads");
   if (d != 64 && d != 128) return refuse(SINKATTN_UNSUPPORTED, "head_dim is not 64 or 128");
   if (rotary_dim < 0 || rotary_dim > d || rotary_dim % 2)
     return refuse(SINKATTN_INVALID_ARG, "rotary_dim must be even and at most head_dim");
@@ -533,6 +534,9 @@ int rope_args(int32_t tokens, int32_t Hq, int32_t Hkv, int32_t d, const uint64_t
   p->Hq = Hq;
   p->Hkv = Hkv;
   p->r = rotary_dim;
+  // row / heads is the upper half of row * inv_heads for the rows of a block: below 2^32 / heads
+  const uint32_t heads = static_cast<uint32_t>(Hq) + 2 * Hkv;
+  p->inv_heads = static_cast<uint32_t>(((uint64_t{1} << 32) + heads - 1) / heads);
   p->turns = reinterpret_cast<const unsigned long long*>(turns);
   p->factor = factor;
   p->q_weight = q_weight;
@@ -589,7 +593,7 @@ int launch_forward(RopeParams& p, int d, int kind, int interleaved, cudaStream_t
   while (p.per_block < 4 && p.tokens / (2 * p.per_block) >= 8LL * sm_count()) p.per_block *= 2;
   // few tokens: their heads go to several blocks
   p.parts = 1;
-  while (p.tokens * int64_t{p.parts} < sm_count() && units > int64_t{p.parts} * 2 * kThreads) p.parts *= 2;
+  while (p.tokens * int64_t{p.parts} < sm_count() && units > int64_t{p.parts} * kThreads) p.parts *= 2;
   const int64_t blocks = (int64_t{p.tokens} + p.per_block - 1) / p.per_block * p.parts;
   if (blocks >= (int64_t{1} << 31)) return refuse(SINKATTN_UNSUPPORTED, "too many work items");
   void (*kern)(const RopeParams) =
