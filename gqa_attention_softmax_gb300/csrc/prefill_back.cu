@@ -112,9 +112,9 @@ __global__ void __launch_bounds__(256) back_delta_kernel(const BackParams p) {
       if (r < rows && c == 0) {
         const float delta = s[i] - dlse[i];
         p.ndelta[at[i]] = -delta;
-        // a row that sees nothing (lse -inf) has P = 0, as for lse +inf
+        // a row with lse -inf has no weights (P = 0, as for lse +inf, which exponentials give)
         p.nlse[at[i]] = lse[i] == kNegInf ? kNegInf : -lse[i] * kLog2e;
-        if (p.sinks) term[r] = tok[i] < total ? -expf(sink[i] - lse[i]) * delta : 0.f;
+        if (p.sinks) term[r] = tok[i] < total && lse[i] != kNegInf ? -expf(sink[i] - lse[i]) * delta : 0.f;
       }
     }
   }

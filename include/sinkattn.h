@@ -572,7 +572,8 @@ SINKATTN_API int sinkattn_pages_lists(const int32_t* table, int32_t num_pages, i
  * written (zeros where nothing is visible); rows behind it stay as they are.
  * Sums are fp32; P and dS are rounded to bf16 for the products. Results do not
  * depend on timing. A sequence whose inputs hold NaN or infinities gets NaN; the
- * other sequences do not. Lengths that contradict the host sizes record
+ * other sequences do not. A row whose lse is -inf has no weights: it gives and gets
+ * no gradient. Each sequence needs Lq_b <= Lk_b. Lengths that contradict the host sizes record
  * SINKATTN_BAD_LENGTHS and leave that sequence's gradients undefined.
  */
 SINKATTN_API int sinkattn_prefill_backward(

@@ -115,6 +115,31 @@ def test_peaked_weights(d):
     check(call(x, h), x, h)
 
 
+@gpu
+@pytest.mark.parametrize("shape", [(8, 2, 64), (8, 2, 128)])
+def test_sinks_of_minus_infinity(shape):
+    """Heads whose sink is -inf have none: dsinks 0. A row with lse -inf has no
+    weights: no gradient of its own and none for others, as if its dout were 0."""
+    x, h = make([50, 70], [50, 90], *shape)
+    x["sinks"][::3] = -torch.inf
+    out, lse = attention(x["q"].double(), x["k"].double(), x["v"].double(), x["sinks"].double(), **h)
+    x["out"], x["lse"] = out.to(torch.bfloat16), lse.float().contiguous()
+    got = call(x, h)
+    assert (got[3][::3] == 0).all()
+    for a, b in zip(got[:3], call(dict(x, sinks=None), h)):
+        assert torch.equal(a, b)
+    check(got, x, h)
+    for token, head in ((0, 0), (49, 2), (110, 7), (110, 3)):
+        x["dout"][token, head] = 0
+    want = call(x, h)
+    assert (want[0][110, 3] == 0).all()
+    for token, head in ((0, 0), (49, 2), (110, 7), (110, 3)):
+        x["dout"][token, head] = 1
+        x["lse"][token, head] = -torch.inf
+    for a, b in zip(call(x, h), want):
+        assert torch.equal(a, b)
+
+
 def _differences(x, h, name, direction, step):
     """d/dt of sum(dout * out) at x[name] + t direction, by central differences in 64 bits."""
     vals = []
@@ -285,10 +310,11 @@ def test_lengths_that_contradict_the_sizes_are_recorded():
 @gpu
 @pytest.mark.parametrize("shape", [(8, 1, 64), (8, 1, 128)])
 @pytest.mark.parametrize("tile", [0, 3])
-def test_a_wait_that_runs_out_is_recorded(shape, tile):
+@pytest.mark.parametrize("sinks", [False, True])
+def test_a_wait_that_runs_out_is_recorded(shape, tile, sinks):
     """A test hook shortens the waits to about 10 ms and leaves one tile's copies out."""
-    x, h = make([700], [700], *shape)
-    want = [t.clone() for t in call(x, h)]
+    x, h = make([700], [700], *shape, sinks=sinks)
+    want = [t.clone() for t in call(x, h) if t is not None]
     assert sa.sinkattn_debug_status() == 0
     sa.sinkattn_debug_set_hooks(20_000_000, tile)
     try:
