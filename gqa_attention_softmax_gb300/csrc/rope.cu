@@ -16,13 +16,15 @@
 // up to 2^-24 |position| radians instead.
 //
 // A thread holds eight elements of one head, four whole pairs, so that the
-// rotation needs no exchange, and d / 8 threads hold a head. All heads of a
-// token share its cosines: a block computes them once per token into shared
-// memory. The mean squares and all arithmetic between the loads and the stores are
-// 32-bit; each output is rounded once.
+// rotation needs no exchange; d / 8 threads hold a head, a warp takes two or
+// four heads at a time and, where there are tokens enough, all heads of its token: the
+// cosines and the weights stay in registers, and no row needs more of an address than an addition.
+// A warp's rows are loaded four at a time. The mean squares and all arithmetic
+// between the loads and the stores are 32-bit; each output is rounded once.
 #include <algorithm>
 #include <cmath>
 
+#include "chain.cuh"
 #include "common.cuh"
 #include "internal.h"
 
@@ -33,7 +35,7 @@ __device__ int g_status_rope;
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTokens = 8;   // tokens of a block
+constexpr int kIlp = 4;   // rows of a thread in flight
 
 enum Layout { kHalf = 0, kInterleaved = 1, kHalfOdd = 2 };
 enum Kind { kPack = 0, kAppend = 1, kAppendFp8 = 2 };
@@ -47,8 +49,7 @@ struct RopeParams {
   const float *q_weight, *k_weight;         // [d] or nullptr
   float eps, factor;
   int tokens, batch, Hq, Hkv, r;
-  uint32_t inv_heads;                       // ceil(2^32 / (Hq + 2 Hkv))
-  int per_block, parts;                     // tokens of a block; blocks that share its heads
+  int parts;                                // warps that share the heads of a token
   __nv_bfloat16 *q_out, *k_out, *v_out;     // pack; append: q_out
   // append
   const int32_t* slots;
@@ -63,10 +64,11 @@ struct RopeParams {
   float* part;                              // [blocks][2][d]
 };
 
-// What a block knows of each of its tokens.
+// Where a token's keys and values lie.
 struct Token {
   long long row;   // pack, backward: ragged row of KV head 0 (-1: none); append: pool row of it
   int step;        // rows from one KV head's to the next's
+  int pos;
 };
 
 // Elements of thread c's four pairs: (first(e), second(e)), e = 0 .. 3; pair 4c + e.
@@ -110,34 +112,35 @@ __device__ __forceinline__ uint4 load_row(const __nv_bfloat16* row, int c, int r
 __device__ __forceinline__ float lo_f(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float hi_f(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
+// The four pairs' members, two pairs in one register pair.
 template <int LAYOUT>
-__device__ __forceinline__ void unpack(uint4 u, float (&a)[4], float (&b)[4]) {
+__device__ __forceinline__ void unpack(uint4 u, float2 (&a)[2], float2 (&b)[2]) {
   if constexpr (LAYOUT == kInterleaved) {
-    a[0] = lo_f(u.x), b[0] = hi_f(u.x), a[1] = lo_f(u.y), b[1] = hi_f(u.y);
-    a[2] = lo_f(u.z), b[2] = hi_f(u.z), a[3] = lo_f(u.w), b[3] = hi_f(u.w);
+    a[0] = make_float2(lo_f(u.x), lo_f(u.y)), b[0] = make_float2(hi_f(u.x), hi_f(u.y));
+    a[1] = make_float2(lo_f(u.z), lo_f(u.w)), b[1] = make_float2(hi_f(u.z), hi_f(u.w));
   } else {
-    a[0] = lo_f(u.x), a[1] = hi_f(u.x), a[2] = lo_f(u.y), a[3] = hi_f(u.y);
-    b[0] = lo_f(u.z), b[1] = hi_f(u.z), b[2] = lo_f(u.w), b[3] = hi_f(u.w);
+    a[0] = make_float2(lo_f(u.x), hi_f(u.x)), a[1] = make_float2(lo_f(u.y), hi_f(u.y));
+    b[0] = make_float2(lo_f(u.z), hi_f(u.z)), b[1] = make_float2(lo_f(u.w), hi_f(u.w));
   }
 }
 
 template <int LAYOUT>
-__device__ __forceinline__ void store_row(__nv_bfloat16* row, int c, int r, const float (&a)[4],
-                                          const float (&b)[4]) {
+__device__ __forceinline__ void store_row(__nv_bfloat16* row, int c, int r, const float2 (&a)[2],
+                                          const float2 (&b)[2]) {
   if constexpr (LAYOUT == kInterleaved) {
     *reinterpret_cast<uint4*>(row + 8 * c) =
-        make_uint4(pack_bf16x2(a[0], b[0]), pack_bf16x2(a[1], b[1]), pack_bf16x2(a[2], b[2]),
-                   pack_bf16x2(a[3], b[3]));
+        make_uint4(pack_bf16x2(a[0].x, b[0].x), pack_bf16x2(a[0].y, b[0].y),
+                   pack_bf16x2(a[1].x, b[1].x), pack_bf16x2(a[1].y, b[1].y));
   } else if constexpr (LAYOUT == kHalf) {
     *reinterpret_cast<uint2*>(row + first_of<LAYOUT>(c, 0, r)) =
-        make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
+        make_uint2(pack_bf16x2(a[0].x, a[0].y), pack_bf16x2(a[1].x, a[1].y));
     *reinterpret_cast<uint2*>(row + second_of<LAYOUT>(c, 0, r)) =
-        make_uint2(pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3]));
+        make_uint2(pack_bf16x2(b[0].x, b[0].y), pack_bf16x2(b[1].x, b[1].y));
   } else {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      row[first_of<LAYOUT>(c, e, r)] = __float2bfloat16_rn(a[e]);
-      row[second_of<LAYOUT>(c, e, r)] = __float2bfloat16_rn(b[e]);
+      row[first_of<LAYOUT>(c, e, r)] = __float2bfloat16_rn(e & 1 ? a[e >> 1].y : a[e >> 1].x);
+      row[second_of<LAYOUT>(c, e, r)] = __float2bfloat16_rn(e & 1 ? b[e >> 1].y : b[e >> 1].x);
     }
   }
 }
@@ -152,21 +155,21 @@ __device__ __forceinline__ uint32_t codes2(float x0, float x1, float s) {
 }
 
 template <int LAYOUT>
-__device__ __forceinline__ void store_codes(uint8_t* row, int c, int r, const float (&a)[4],
-                                            const float (&b)[4], float s) {
+__device__ __forceinline__ void store_codes(uint8_t* row, int c, int r, const float2 (&a)[2],
+                                            const float2 (&b)[2], float s) {
   if constexpr (LAYOUT == kInterleaved) {
     *reinterpret_cast<uint2*>(row + 8 * c) =
-        make_uint2(codes2(a[0], b[0], s) | codes2(a[1], b[1], s) << 16,
-                   codes2(a[2], b[2], s) | codes2(a[3], b[3], s) << 16);
+        make_uint2(codes2(a[0].x, b[0].x, s) | codes2(a[0].y, b[0].y, s) << 16,
+                   codes2(a[1].x, b[1].x, s) | codes2(a[1].y, b[1].y, s) << 16);
   } else if constexpr (LAYOUT == kHalf) {
     *reinterpret_cast<uint32_t*>(row + first_of<LAYOUT>(c, 0, r)) =
-        codes2(a[0], a[1], s) | codes2(a[2], a[3], s) << 16;
+        codes2(a[0].x, a[0].y, s) | codes2(a[1].x, a[1].y, s) << 16;
     *reinterpret_cast<uint32_t*>(row + second_of<LAYOUT>(c, 0, r)) =
-        codes2(b[0], b[1], s) | codes2(b[2], b[3], s) << 16;
+        codes2(b[0].x, b[0].y, s) | codes2(b[1].x, b[1].y, s) << 16;
   } else {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const uint32_t two = codes2(a[e], b[e], s);
+      const uint32_t two = codes2(e & 1 ? a[e >> 1].y : a[e >> 1].x, e & 1 ? b[e >> 1].y : b[e >> 1].x, s);
       row[first_of<LAYOUT>(c, e, r)] = static_cast<uint8_t>(two);
       row[second_of<LAYOUT>(c, e, r)] = static_cast<uint8_t>(two >> 8);
     }
@@ -181,12 +184,14 @@ __device__ __forceinline__ float head_sum(float x) {
   return x;
 }
 
-__device__ __forceinline__ float sum_squares(const float (&a)[4], const float (&b)[4]) {
-  float s = 0.f;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) s = fmaf(a[e], a[e], fmaf(b[e], b[e], s));
-  return s;
+__device__ __forceinline__ float dot_pairs(const float2 (&a)[2], const float2 (&b)[2], const float2 (&x)[2],
+                                           const float2 (&y)[2]) {
+  const float2 s = __ffma2_rn(a[1], x[1], __ffma2_rn(b[0], y[0], __fmul2_rn(a[0], x[0])));
+  const float2 t = __ffma2_rn(b[1], y[1], s);
+  return t.x + t.y;
 }
+
+__device__ __forceinline__ float2 neg2(float2 x) { return make_float2(-x.x, -x.y); }
 
 // The sequence of token t: the b with cu[b] <= t < cu[b + 1], or -1.
 __device__ __forceinline__ int sequence_of(const int32_t* cu, int batch, int t) {
@@ -200,271 +205,266 @@ __device__ __forceinline__ int sequence_of(const int32_t* cu, int batch, int t) 
   return lo;
 }
 
-// Cosine and sine of every pair of tokens tok0 .. tok0 + n - 1 into cs [n][d / 2]
-// (1 and 0 past the rotated pairs), and where the tokens' rows lie.
-template <int D, bool APPEND>
-__device__ __forceinline__ void prepare_tokens(const RopeParams& p, int tok0, int n,
-                                               float2 (*cs)[D / 2], Token* info, int* pos_s) {
-  if (threadIdx.x < n) {
-    const int t = tok0 + threadIdx.x;
-    Token k{-1, 0};
-    int pos = 0;
-    if constexpr (APPEND) {
-      pos = p.positions[t];
-      const int slot = p.slots[t];
-      if (slot >= 0 && slot < p.n_slots) {   // (a padding token writes no keys)
-        k.row = ((static_cast<long long>(slot >> p.shift) * p.Hkv) << p.shift) +
-                (slot & ((1 << p.shift) - 1));
-        k.step = 1 << p.shift;
-      }
-    } else {
-      const int b = sequence_of(p.cu, p.batch, t);
-      if (b >= 0) {   // (rows behind the last sequence stay as they are)
-        const int start = p.cu[b], end = p.cu[b + 1];
-        if (start < 0 || end > p.tokens || t < start || t >= end) {
-          atomicExch(&g_status_rope, SINKATTN_BAD_LENGTHS);
-        } else {
-          k.row = static_cast<long long>(p.Hkv) * start + (t - start);
-          k.step = end - start;
-          pos = p.positions ? p.positions[t] : t - start;
-        }
+template <bool APPEND>
+__device__ __forceinline__ Token token_of(const RopeParams& p, int t) {
+  Token k{-1, 0, 0};
+  if constexpr (APPEND) {
+    k.pos = p.positions[t];
+    const int slot = p.slots[t];
+    if (slot >= 0 && slot < p.n_slots) {   // (a padding token writes no keys)
+      k.row = ((static_cast<long long>(slot >> p.shift) * p.Hkv) << p.shift) + (slot & ((1 << p.shift) - 1));
+      k.step = 1 << p.shift;
+    }
+  } else {
+    const int b = sequence_of(p.cu, p.batch, t);
+    if (b >= 0) {   // (rows behind the last sequence stay as they are)
+      const int start = p.cu[b], end = p.cu[b + 1];
+      if (start < 0 || end > p.tokens || t < start || t >= end) {
+        atomicExch(&g_status_rope, SINKATTN_BAD_LENGTHS);
+      } else {
+        k.row = static_cast<long long>(p.Hkv) * start + (t - start);
+        k.step = end - start;
+        k.pos = p.positions ? p.positions[t] : t - start;
       }
     }
-    info[threadIdx.x] = k;
-    pos_s[threadIdx.x] = pos;
   }
-  __syncthreads();
-  for (int u = threadIdx.x; u < n * (D / 2); u += kThreads) {
-    const int t = u / (D / 2), i = u % (D / 2);
-    float2 v = make_float2(1.f, 0.f);
-    if (i < p.r / 2) {
-      const unsigned long long turn =
-          p.turns[i] * static_cast<unsigned long long>(static_cast<long long>(pos_s[t]));
-      // the upper 32 bits as a signed fraction: half turns in [-1, 1)
-      const float x = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f;
-      sincospif(x, &v.y, &v.x);
-      v.x *= p.factor;
-      v.y *= p.factor;
-    }
-    cs[t][i] = v;
-  }
-  __syncthreads();
+  return k;
 }
 
-// A block takes p.per_block tokens, or one of p.parts shares of their heads.
-template <int D, int LAYOUT, int KIND>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
-  constexpr int C = D / 8;                 // threads of a head
-  constexpr int kIlp = 4;
-  __shared__ float2 cs[kMaxTokens][D / 2];
-  __shared__ Token info[kMaxTokens];
-  __shared__ int pos_s[kMaxTokens];
-  const int tok0 = blockIdx.x / p.parts * p.per_block;
-  const int n = min(p.per_block, p.tokens - tok0);
-  prepare_tokens<D, KIND != kPack>(p, tok0, n, cs, info, pos_s);
-
-  const int c = threadIdx.x % C;
-  const int heads = p.Hq + 2 * p.Hkv;
-  const int rows = n * heads;
-  float wq[8], wk[8];
+// Cosine and sine of thread c's four pairs at a position (1 and 0 past the rotated ones).
+__device__ __forceinline__ void angles(const RopeParams& p, int pos, int c, float2 (&co)[2], float2 (&si)[2]) {
+  float x[4], y[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const int i = first_of<LAYOUT>(c, e, p.r), j = second_of<LAYOUT>(c, e, p.r);
-    wq[e] = p.q_weight ? p.q_weight[i] : 1.f;
-    wq[4 + e] = p.q_weight ? p.q_weight[j] : 1.f;
-    wk[e] = p.k_weight ? p.k_weight[i] : 1.f;
-    wk[4 + e] = p.k_weight ? p.k_weight[j] : 1.f;
+    const int i = 4 * c + e;
+    x[e] = 1.f;
+    y[e] = 0.f;
+    if (i < p.r / 2) {
+      const unsigned long long turn = p.turns[i] * static_cast<unsigned long long>(static_cast<long long>(pos));
+      // the upper 32 bits as a signed fraction: half turns in [-1, 1)
+      sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &y[e], &x[e]);
+      x[e] *= p.factor;
+      y[e] *= p.factor;
+    }
   }
-  const bool any_norm = p.q_weight || p.k_weight;
-  const int step = kThreads / C;
-  const int part = blockIdx.x % p.parts;
-  // (the trip count is the same for all threads: the head sums are warp-collective)
-  for (int base = part * step * kIlp; base < rows; base += p.parts * step * kIlp) {
-    uint4 raw[kIlp];
-    int tok[kIlp], head[kIlp];
+  co[0] = make_float2(x[0], x[1]), co[1] = make_float2(x[2], x[3]);
+  si[0] = make_float2(y[0], y[1]), si[1] = make_float2(y[2], y[3]);
+}
+
+// Thread c's eight weights (1 without a norm).
+template <int LAYOUT>
+__device__ __forceinline__ void load_weights(const float* w, int c, int r, float2 (&a)[2], float2 (&b)[2]) {
 #pragma unroll
-    for (int i = 0; i < kIlp; ++i) {
-      const int row = base + i * step + static_cast<int>(threadIdx.x) / C;
-      tok[i] = -1;
-      raw[i] = make_uint4(0, 0, 0, 0);
-      if (row >= rows) continue;
-      const int t = static_cast<int>(__umulhi(row, p.inv_heads));
-      const int h = row - t * heads;
-      const long long g = tok0 + t;
-      if (KIND == kPack && info[t].row < 0) continue;
-      tok[i] = t;
-      head[i] = h;
-      if (h < p.Hq) raw[i] = load_row<LAYOUT>(p.q + g * p.q_stride + h * D, c, p.r);
-      else if (info[t].row < 0) tok[i] = -1;
-      else if (h < p.Hq + p.Hkv)
-        raw[i] = load_row<LAYOUT>(p.k + g * p.k_stride + (h - p.Hq) * D, c, p.r);
-      else
-        raw[i] = load_row<kInterleaved>(p.v + g * p.v_stride + (h - p.Hq - p.Hkv) * D, c, p.r);
+  for (int e = 0; e < 2; ++e) {
+    a[e] = b[e] = make_float2(1.f, 1.f);
+    if (w == nullptr) continue;
+    a[e] = make_float2(w[first_of<LAYOUT>(c, 2 * e, r)], w[first_of<LAYOUT>(c, 2 * e + 1, r)]);
+    b[e] = make_float2(w[second_of<LAYOUT>(c, 2 * e, r)], w[second_of<LAYOUT>(c, 2 * e + 1, r)]);
+  }
+}
+
+// The passes (of 32 / C heads: first q's, then k's, then v's) of share `part` of a token.
+struct Share {
+  int q_lo, q_hi, k_lo, k_hi, v_lo, v_hi;
+};
+__device__ __forceinline__ Share share_of(int Hq, int Hkv, int per_pass, int part, int parts) {
+  const int nq = (Hq + per_pass - 1) / per_pass, nk = (Hkv + per_pass - 1) / per_pass;
+  const int all = nq + 2 * nk;
+  const int lo = all * part / parts, hi = all * (part + 1) / parts;
+  return {min(lo, nq), min(hi, nq), min(max(lo - nq, 0), nk), min(max(hi - nq, 0), nk),
+          max(lo - nq - nk, 0), max(hi - nq - nk, 0)};
+}
+
+// Norm and rotation of heads `pass * 32 / C + s` of one token, pass lo .. hi - 1.
+template <int D, int LAYOUT, typename Store>
+__device__ __forceinline__ void rotate_rows(const RopeParams& p, const __nv_bfloat16* src, int heads, int lo,
+                                            int hi, const float* w, const float2 (&co)[2],
+                                            const float2 (&si)[2], int c, int s, Store store) {
+  constexpr int R = 32 / (D / 8);
+  if (lo >= hi) return;
+  // y_a = rs (x_a (w_a cos) - x_b (w_b sin)), y_b = rs (x_b (w_b cos) + x_a (w_a sin))
+  float2 wa[2], wb[2], ca[2], sb[2], cb[2], sa[2];
+  load_weights<LAYOUT>(w, c, p.r, wa, wb);
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    ca[e] = __fmul2_rn(wa[e], co[e]);
+    sa[e] = __fmul2_rn(wa[e], si[e]);
+    cb[e] = __fmul2_rn(wb[e], co[e]);
+    sb[e] = neg2(__fmul2_rn(wb[e], si[e]));
+  }
+  for (int i = lo; i < hi; i += kIlp) {
+    uint4 raw[kIlp];
+#pragma unroll
+    for (int u = 0; u < kIlp; ++u) {
+      const int h = (i + u) * R + s;
+      raw[u] = make_uint4(0, 0, 0, 0);
+      if (i + u < hi && h < heads) raw[u] = load_row<LAYOUT>(src + h * D, c, p.r);
     }
 #pragma unroll
-    for (int i = 0; i < kIlp; ++i) {
-      float a[4], b[4];
-      unpack<LAYOUT>(raw[i], a, b);
+    for (int u = 0; u < kIlp; ++u) {
+      const int h = (i + u) * R + s;
+      float2 a[2], b[2];
+      unpack<LAYOUT>(raw[u], a, b);
       float rs = 1.f;
-      if (any_norm) rs = rsqrtf(head_sum<D>(sum_squares(a, b)) * (1.f / D) + p.eps);
-      if (tok[i] < 0) continue;
-      const int t = tok[i], h = head[i];
-      const Token at = info[t];
-      if (h >= p.Hq + p.Hkv) {
-        const long long row = at.row + static_cast<long long>(h - p.Hq - p.Hkv) * at.step;
-        if constexpr (KIND == kAppendFp8) {
-          float x[4], y[4];
-          unpack<kInterleaved>(raw[i], x, y);
-          store_codes<kInterleaved>(p.v_pages + row * D, c, p.r, x, y,
-                                    p.v_scale[h - p.Hq - p.Hkv]);
-        } else {
-          __nv_bfloat16* out = KIND == kPack ? p.v_out : reinterpret_cast<__nv_bfloat16*>(p.v_pages);
-          *reinterpret_cast<uint4*>(out + row * D + 8 * c) = raw[i];
-        }
-        continue;
-      }
-      const bool is_q = h < p.Hq;
-      if (is_q ? p.q_weight != nullptr : p.k_weight != nullptr) {
+      if (w != nullptr) rs = rsqrtf(head_sum<D>(dot_pairs(a, b, a, b)) * (1.f / D) + p.eps);
+      float2 y[2], z[2];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          a[e] *= rs * (is_q ? wq[e] : wk[e]);
-          b[e] *= rs * (is_q ? wq[4 + e] : wk[4 + e]);
+      for (int e = 0; e < 2; ++e) {
+        y[e] = __ffma2_rn(a[e], ca[e], __fmul2_rn(b[e], sb[e]));
+        z[e] = __ffma2_rn(b[e], cb[e], __fmul2_rn(a[e], sa[e]));
+        if (w != nullptr) {
+          y[e] = __fmul2_rn(y[e], make_float2(rs, rs));
+          z[e] = __fmul2_rn(z[e], make_float2(rs, rs));
         }
       }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        // kHalf past the rotated pairs: cs holds 1 and 0
-        const float2 w = cs[t][4 * c + e];
-        const float x = a[e], y = b[e];
-        a[e] = x * w.x - y * w.y;
-        b[e] = y * w.x + x * w.y;
-      }
-      if (is_q) {
-        store_row<LAYOUT>(p.q_out + (static_cast<long long>(tok0 + t) * p.Hq + h) * D, c, p.r, a, b);
-      } else {
-        const long long row = at.row + static_cast<long long>(h - p.Hq) * at.step;
-        if constexpr (KIND == kAppendFp8)
-          store_codes<LAYOUT>(p.k_pages + row * D, c, p.r, a, b, p.k_scale[h - p.Hq]);
-        else
-          store_row<LAYOUT>((KIND == kPack ? p.k_out : reinterpret_cast<__nv_bfloat16*>(p.k_pages)) +
-                                row * D, c, p.r, a, b);
-      }
+      if (i + u < hi && h < heads) store(h, y, z);
     }
   }
 }
 
-// Gradients of the projection's rows; blocks walk over the groups of
-// p.per_block tokens with the grid's stride and leave their sums of the
-// weights' gradients in p.part.
+template <int D, int LAYOUT, int KIND>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
+  constexpr int C = D / 8, R = 32 / C;   // threads of a head, heads of a pass
+  const long long unit = static_cast<long long>(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32;
+  const int t = static_cast<int>(unit / p.parts), part = static_cast<int>(unit % p.parts);
+  if (t >= p.tokens) return;             // (whole warps)
+  const Token at = token_of<KIND != kPack>(p, t);
+  if (KIND == kPack && at.row < 0) return;
+  const int lane = threadIdx.x & 31, c = lane % C, s = lane / C;
+  const Share sh = share_of(p.Hq, p.Hkv, R, part, p.parts);
+  float2 co[2], si[2];
+  angles(p, at.pos, c, co, si);
+  __nv_bfloat16* q_out = p.q_out + static_cast<long long>(t) * p.Hq * D;
+  rotate_rows<D, LAYOUT>(p, p.q + t * p.q_stride, p.Hq, sh.q_lo, sh.q_hi, p.q_weight, co, si, c, s,
+                         [&](int h, const float2 (&a)[2], const float2 (&b)[2]) {
+                           store_row<LAYOUT>(q_out + h * D, c, p.r, a, b);
+                         });
+  if (at.row < 0) return;
+  rotate_rows<D, LAYOUT>(p, p.k + t * p.k_stride, p.Hkv, sh.k_lo, sh.k_hi, p.k_weight, co, si, c, s,
+                         [&](int h, const float2 (&a)[2], const float2 (&b)[2]) {
+                           const long long row = at.row + static_cast<long long>(h) * at.step;
+                           if constexpr (KIND == kAppendFp8)
+                             store_codes<LAYOUT>(p.k_pages + row * D, c, p.r, a, b, p.k_scale[h]);
+                           else
+                             store_row<LAYOUT>((KIND == kPack ? p.k_out
+                                                              : reinterpret_cast<__nv_bfloat16*>(p.k_pages)) +
+                                                   row * D, c, p.r, a, b);
+                         });
+  for (int i = sh.v_lo; i < sh.v_hi; ++i) {
+    const int h = i * R + s;
+    if (h >= p.Hkv) continue;
+    const uint4 raw = load_row<kInterleaved>(p.v + t * p.v_stride + h * D, c, p.r);
+    const long long row = at.row + static_cast<long long>(h) * at.step;
+    if constexpr (KIND == kAppendFp8) {
+      float2 a[2], b[2];
+      unpack<kInterleaved>(raw, a, b);
+      store_codes<kInterleaved>(p.v_pages + row * D, c, p.r, a, b, p.v_scale[h]);
+    } else {
+      __nv_bfloat16* out = KIND == kPack ? p.v_out : reinterpret_cast<__nv_bfloat16*>(p.v_pages);
+      *reinterpret_cast<uint4*>(out + row * D + 8 * c) = raw;
+    }
+  }
+}
+
+// Gradients of heads `pass * 32 / C + s` of one token: grad(h) and in(h) are the
+// rows of dy and of x, `sum` takes this thread's share of the weights' gradients.
+template <int D, int LAYOUT, typename Grad, typename Store>
+__device__ __forceinline__ void rotate_rows_back(const RopeParams& p, Grad grad, const __nv_bfloat16* in,
+                                                 int heads, int lo, int hi, const float* w,
+                                                 const float2 (&co)[2], const float2 (&si)[2], int c, int s,
+                                                 float2 (&sum_a)[2], float2 (&sum_b)[2], Store store) {
+  constexpr int R = 32 / (D / 8);
+  constexpr int kBackIlp = 2;
+  if (lo >= hi) return;
+  float2 wa[2], wb[2];
+  load_weights<LAYOUT>(w, c, p.r, wa, wb);
+  const float2 ns[2] = {neg2(si[0]), neg2(si[1])};
+  for (int i = lo; i < hi; i += kBackIlp) {
+    uint4 raw[kBackIlp], xr[kBackIlp];
+#pragma unroll
+    for (int u = 0; u < kBackIlp; ++u) {
+      const int h = (i + u) * R + s;
+      raw[u] = xr[u] = make_uint4(0, 0, 0, 0);
+      if (i + u < hi && h < heads) {
+        raw[u] = load_row<LAYOUT>(grad(h), c, p.r);
+        if (w != nullptr) xr[u] = load_row<LAYOUT>(in + h * D, c, p.r);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kBackIlp; ++u) {
+      const int h = (i + u) * R + s;
+      float2 a[2], b[2], y[2], z[2];
+      unpack<LAYOUT>(raw[u], a, b);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {   // g = R^T dy
+        y[e] = __ffma2_rn(a[e], co[e], __fmul2_rn(b[e], si[e]));
+        z[e] = __ffma2_rn(b[e], co[e], __fmul2_rn(a[e], ns[e]));
+      }
+      if (w != nullptr) {
+        float2 xa[2], xb[2], ua[2], ub[2];
+        unpack<LAYOUT>(xr[u], xa, xb);
+        const float rs = rsqrtf(head_sum<D>(dot_pairs(xa, xb, xa, xb)) * (1.f / D) + p.eps);
+        const float2 rs2 = make_float2(rs, rs);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {   // (rows past the last have g = 0)
+          xa[e] = __fmul2_rn(xa[e], rs2);
+          xb[e] = __fmul2_rn(xb[e], rs2);
+          sum_a[e] = __ffma2_rn(y[e], xa[e], sum_a[e]);
+          sum_b[e] = __ffma2_rn(z[e], xb[e], sum_b[e]);
+          ua[e] = __fmul2_rn(y[e], wa[e]);
+          ub[e] = __fmul2_rn(z[e], wb[e]);
+        }
+        const float dot = head_sum<D>(dot_pairs(ua, ub, xa, xb)) * (-1.f / D);
+        const float2 dot2 = make_float2(dot, dot);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          y[e] = __fmul2_rn(rs2, __ffma2_rn(xa[e], dot2, ua[e]));
+          z[e] = __fmul2_rn(rs2, __ffma2_rn(xb[e], dot2, ub[e]));
+        }
+      }
+      if (i + u < hi && h < heads) store(h, y, z);
+    }
+  }
+}
+
+// Gradients of the projection's rows; warps walk over the tokens (and shares
+// of them) with the grid's stride and leave their block's sums of the weights'
+// gradients in p.part.
 template <int D, int LAYOUT, bool NORM>
 __global__ void __launch_bounds__(kThreads) rope_backward_kernel(const RopeParams p) {
-  constexpr int C = D / 8;
-  constexpr int kIlp = 2;
-  __shared__ float2 cs[kMaxTokens][D / 2];
-  __shared__ Token info[kMaxTokens];
-  __shared__ int pos_s[kMaxTokens];
-  __shared__ float sums[kThreads][9];
-  const int c = threadIdx.x % C;
-  const int heads = p.Hq + 2 * p.Hkv;
-  float wq[8], wk[8], sq[8], sk[8];
+  constexpr int C = D / 8, R = 32 / C;
+  __shared__ float sums[NORM ? kThreads : 1][9];
+  grid_launch_dependents();
+  const int lane = threadIdx.x & 31, c = lane % C, s = lane / C;
+  float2 qa[2], qb[2], ka[2], kb[2];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int i = e < 4 ? first_of<LAYOUT>(c, e, p.r) : second_of<LAYOUT>(c, e - 4, p.r);
-    wq[e] = NORM && p.q_weight ? p.q_weight[i] : 1.f;
-    wk[e] = NORM && p.k_weight ? p.k_weight[i] : 1.f;
-    sq[e] = sk[e] = 0.f;
-  }
-  const int step = kThreads / C;
-  const int groups = (p.tokens + p.per_block - 1) / p.per_block;
-  for (int grp = blockIdx.x; grp < groups; grp += gridDim.x) {
-    const int tok0 = grp * p.per_block;
-    const int n = min(p.per_block, p.tokens - tok0);
-    __syncthreads();   // the group before has read cs and info
-    prepare_tokens<D, false>(p, tok0, n, cs, info, pos_s);
-    const int rows = n * heads;
-    for (int base = 0; base < rows; base += step * kIlp) {
-      uint4 raw[kIlp], xr[kIlp];
-      int tok[kIlp], head[kIlp];
-#pragma unroll
-      for (int i = 0; i < kIlp; ++i) {
-        const int row = base + i * step + static_cast<int>(threadIdx.x) / C;
-        tok[i] = -1;
-        head[i] = 0;
-        raw[i] = xr[i] = make_uint4(0, 0, 0, 0);
-        if (row >= rows) continue;
-        const int t = static_cast<int>(__umulhi(row, p.inv_heads));
-        const int h = row - t * heads;
-        const long long g = tok0 + t;
-        const Token at = info[t];
-        if (at.row < 0) continue;
-        tok[i] = t;
-        head[i] = h;
-        if (h < p.Hq) {
-          raw[i] = load_row<LAYOUT>(p.dq + (g * p.Hq + h) * D, c, p.r);
-          if (NORM && p.q_weight) xr[i] = load_row<LAYOUT>(p.q + g * p.q_stride + h * D, c, p.r);
-        } else if (h < p.Hq + p.Hkv) {
-          const int kh = h - p.Hq;
-          raw[i] = load_row<LAYOUT>(p.dk + (at.row + static_cast<long long>(kh) * at.step) * D, c, p.r);
-          if (NORM && p.k_weight) xr[i] = load_row<LAYOUT>(p.k + g * p.k_stride + kh * D, c, p.r);
-        } else {
-          const int kh = h - p.Hq - p.Hkv;
-          raw[i] = load_row<kInterleaved>(
-              p.dv + (at.row + static_cast<long long>(kh) * at.step) * D, c, p.r);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kIlp; ++i) {
-        const int t = max(tok[i], 0), h = head[i];
-        const long long g = tok0 + t;
-        const bool is_q = h < p.Hq;
-        float a[4], b[4];
-        unpack<LAYOUT>(raw[i], a, b);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 w = cs[t][4 * c + e];
-          const float x = a[e], y = b[e];
-          a[e] = x * w.x + y * w.y;
-          b[e] = y * w.x - x * w.y;
-        }
-        if constexpr (NORM) {
-          float x[4], y[4];
-          unpack<LAYOUT>(xr[i], x, y);
-          const float rs = rsqrtf(head_sum<D>(sum_squares(x, y)) * (1.f / D) + p.eps);
-          float u[4], v[4], dot = 0.f;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            x[e] *= rs;
-            y[e] *= rs;
-            u[e] = a[e] * (is_q ? wq[e] : wk[e]);
-            v[e] = b[e] * (is_q ? wq[4 + e] : wk[4 + e]);
-            dot = fmaf(u[e], x[e], fmaf(v[e], y[e], dot));
-          }
-          dot = head_sum<D>(dot) * (1.f / D);
-          const bool normed = tok[i] >= 0 && h < p.Hq + p.Hkv &&
-                              (is_q ? p.q_weight != nullptr : p.k_weight != nullptr);
-          if (normed) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if (is_q) {
-                sq[e] = fmaf(a[e], x[e], sq[e]);
-                sq[4 + e] = fmaf(b[e], y[e], sq[4 + e]);
-              } else {
-                sk[e] = fmaf(a[e], x[e], sk[e]);
-                sk[4 + e] = fmaf(b[e], y[e], sk[4 + e]);
-              }
-              a[e] = rs * (u[e] - x[e] * dot);
-              b[e] = rs * (v[e] - y[e] * dot);
-            }
-          }
-        }
-        if (tok[i] < 0) continue;
-        if (is_q)
-          store_row<LAYOUT>(p.dq_in + g * p.dq_stride + h * D, c, p.r, a, b);
-        else if (h < p.Hq + p.Hkv)
-          store_row<LAYOUT>(p.dk_in + g * p.dk_stride + (h - p.Hq) * D, c, p.r, a, b);
-        else
-          *reinterpret_cast<uint4*>(p.dv_in + g * p.dv_stride + (h - p.Hq - p.Hkv) * D + 8 * c) = raw[i];
-      }
+  for (int e = 0; e < 2; ++e) qa[e] = qb[e] = ka[e] = kb[e] = make_float2(0.f, 0.f);
+  const long long units = static_cast<long long>(p.tokens) * p.parts;
+  for (long long unit = static_cast<long long>(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32; unit < units;
+       unit += static_cast<long long>(gridDim.x) * (kThreads / 32)) {
+    const int t = static_cast<int>(unit / p.parts), part = static_cast<int>(unit % p.parts);
+    const Token at = token_of<false>(p, t);
+    if (at.row < 0) continue;
+    const Share sh = share_of(p.Hq, p.Hkv, R, part, p.parts);
+    float2 co[2], si[2];
+    angles(p, at.pos, c, co, si);
+    const __nv_bfloat16* dq = p.dq + static_cast<long long>(t) * p.Hq * D;
+    rotate_rows_back<D, LAYOUT>(p, [&](int h) { return dq + h * D; }, NORM ? p.q + t * p.q_stride : nullptr,
+                                p.Hq, sh.q_lo, sh.q_hi, NORM ? p.q_weight : nullptr, co, si, c, s, qa, qb,
+                                [&](int h, const float2 (&a)[2], const float2 (&b)[2]) {
+                                  store_row<LAYOUT>(p.dq_in + t * p.dq_stride + h * D, c, p.r, a, b);
+                                });
+    rotate_rows_back<D, LAYOUT>(
+        p, [&](int h) { return p.dk + (at.row + static_cast<long long>(h) * at.step) * D; },
+        NORM ? p.k + t * p.k_stride : nullptr, p.Hkv, sh.k_lo, sh.k_hi, NORM ? p.k_weight : nullptr, co, si, c,
+        s, ka, kb, [&](int h, const float2 (&a)[2], const float2 (&b)[2]) {
+          store_row<LAYOUT>(p.dk_in + t * p.dk_stride + h * D, c, p.r, a, b);
+        });
+    for (int i = sh.v_lo; i < sh.v_hi; ++i) {
+      const int h = i * R + s;
+      if (h < p.Hkv)
+        *reinterpret_cast<uint4*>(p.dv_in + t * p.dv_stride + h * D + 8 * c) = load_row<kInterleaved>(
+            p.dv + (at.row + static_cast<long long>(h) * at.step) * D, c, p.r);
     }
   }
   if constexpr (NORM) {
@@ -473,33 +473,41 @@ __global__ void __launch_bounds__(kThreads) rope_backward_kernel(const RopeParam
     for (int which = 0; which < 2; ++which) {
       __syncthreads();
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sums[threadIdx.x][e] = which ? sk[e] : sq[e];
+      for (int e = 0; e < 2; ++e) {
+        const float2 a = which ? ka[e] : qa[e], b = which ? kb[e] : qb[e];
+        sums[threadIdx.x][2 * e] = a.x;
+        sums[threadIdx.x][2 * e + 1] = a.y;
+        sums[threadIdx.x][4 + 2 * e] = b.x;
+        sums[threadIdx.x][5 + 2 * e] = b.y;
+      }
       __syncthreads();
       if (threadIdx.x < D) {
         const int cc = threadIdx.x / 8, e = threadIdx.x % 8;
-        float s = 0.f;
-        for (int j = 0; j < kThreads / C; ++j) s += sums[j * C + cc][e];
+        float x = 0.f;
+        for (int j = 0; j < kThreads / C; ++j) x += sums[j * C + cc][e];
         const int el = e < 4 ? first_of<LAYOUT>(cc, e, p.r) : second_of<LAYOUT>(cc, e - 4, p.r);
-        p.part[(static_cast<long long>(blockIdx.x) * 2 + which) * D + el] = s;
+        p.part[(static_cast<long long>(blockIdx.x) * 2 + which) * D + el] = x;
       }
     }
   }
 }
 
 // The weights' gradients: the blocks' sums added in a fixed order, 32 columns
-// of the 2 d a block, eight threads a column.
-__global__ void __launch_bounds__(256) rope_weights_kernel(const float* part, int blocks, int d,
-                                                           float* dq_weight, float* dk_weight) {
-  __shared__ float s[8][32];
-  const int col = blockIdx.x * 32 + threadIdx.x % 32, slice = threadIdx.x / 32;
-  float x = 0.f;
-  for (int b = slice; b < blocks; b += 8) x += part[static_cast<long long>(b) * 2 * d + col];
-  s[slice][threadIdx.x % 32] = x;
+// of the 2 d a block, 32 threads a column.
+__global__ void __launch_bounds__(1024) rope_weights_kernel(const float* part, int blocks, int d,
+                                                            float* dq_weight, float* dk_weight) {
+  __shared__ float s[32][33];
+  grid_dependency_wait();
+  const int x = threadIdx.x % 32, slice = threadIdx.x / 32, col = blockIdx.x * 32 + x;
+  float sum = 0.f;
+#pragma unroll 8
+  for (int b = slice; b < blocks; b += 32) sum += part[static_cast<long long>(b) * 2 * d + col];
+  s[slice][x] = sum;
   __syncthreads();
   if (slice != 0) return;
-  for (int j = 1; j < 8; ++j) x += s[j][threadIdx.x];
+  for (int j = 1; j < 32; ++j) sum += s[j][x];
   float* out = col < d ? dq_weight : dk_weight;
-  if (out) out[col % d] = x;
+  if (out) out[col % d] = sum;
 }
 
 int refuse(int status, const char* text) {
@@ -534,9 +542,6 @@ int rope_args(int32_t tokens, int32_t Hq, int32_t Hkv, int32_t d, const uint64_t
   p->Hq = Hq;
   p->Hkv = Hkv;
   p->r = rotary_dim;
-  // row / heads is the upper half of row * inv_heads for the rows of a block: below 2^32 / heads
-  const uint32_t heads = static_cast<uint32_t>(Hq) + 2 * Hkv;
-  p->inv_heads = static_cast<uint32_t>(((uint64_t{1} << 32) + heads - 1) / heads);
   p->turns = reinterpret_cast<const unsigned long long*>(turns);
   p->factor = factor;
   p->q_weight = q_weight;
@@ -578,23 +583,24 @@ void (*pick_backward(int layout))(const RopeParams) {
                                   : rope_backward_kernel<D, kHalfOdd, NORM>;
 }
 
-int launched(const char* what) {
-  const cudaError_t e = cudaGetLastError();
+int launched(const char* what, cudaError_t e) {
   if (e == cudaSuccess) return SINKATTN_OK;
   set_error("%s launch: %s", what, cudaGetErrorString(e));
   return SINKATTN_CUDA_ERROR;
 }
 
+// Warps that share a token's heads: one, while that leaves every SM 16 warps.
+int shares(int32_t tokens, int32_t Hq, int32_t Hkv, int d) {
+  const int R = 256 / d, passes = (Hq + R - 1) / R + 2 * ((Hkv + R - 1) / R);
+  int parts = 1;
+  while (int64_t{tokens} * parts < 16LL * 152 && 2 * parts <= passes) parts *= 2;
+  return parts;
+}
+
 int launch_forward(RopeParams& p, int d, int kind, int interleaved, cudaStream_t stream) {
   const int layout = layout_of(p.r, interleaved);
-  const int64_t units = (static_cast<int64_t>(p.Hq) + 2 * p.Hkv) * (d / 8);   // threads of a token
-  // tokens of a block: four, while that leaves every SM eight blocks
-  p.per_block = 1;
-  while (p.per_block < 4 && p.tokens / (2 * p.per_block) >= 8LL * sm_count()) p.per_block *= 2;
-  // few tokens: their heads go to several blocks
-  p.parts = 1;
-  while (p.tokens * int64_t{p.parts} < sm_count() && units > int64_t{p.parts} * kThreads) p.parts *= 2;
-  const int64_t blocks = (int64_t{p.tokens} + p.per_block - 1) / p.per_block * p.parts;
+  p.parts = shares(p.tokens, p.Hq, p.Hkv, d);
+  const int64_t blocks = (int64_t{p.tokens} * p.parts + kThreads / 32 - 1) / (kThreads / 32);
   if (blocks >= (int64_t{1} << 31)) return refuse(SINKATTN_UNSUPPORTED, "too many work items");
   void (*kern)(const RopeParams) =
       d == 64 ? (kind == kPack     ? pick_layout<64, kPack>(layout)
@@ -604,12 +610,12 @@ int launch_forward(RopeParams& p, int d, int kind, int interleaved, cudaStream_t
                  : kind == kAppend ? pick_layout<128, kAppend>(layout)
                                    : pick_layout<128, kAppendFp8>(layout));
   kern<<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(p);
-  return launched("rope");
+  return launched("rope", cudaGetLastError());
 }
 
 // (a fixed bound, so that neither the workspace nor the order of the sums goes by the device)
 int backward_blocks(int32_t tokens) {
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((int64_t{tokens} + 1) / 2, 6 * 152)));
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(tokens, 4 * 152)));
 }
 
 int append(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
@@ -839,16 +845,17 @@ int sinkattn_rope_qkv_backward(const void* dq, const void* dk, const void* dv, c
   p.dv_in = static_cast<__nv_bfloat16*>(dv_in);
   p.dq_stride = dq_stride, p.dk_stride = dk_stride, p.dv_stride = dv_stride;
   p.part = static_cast<float*>(workspace);
-  p.per_block = tokens >= 8 * blocks ? 4 : 2;
+  p.parts = shares(tokens, num_qo_heads, num_kv_heads, head_dim);
   const int layout = layout_of(p.r, interleaved);
   void (*kern)(const RopeParams) =
       head_dim == 64 ? (norm ? pick_backward<64, true>(layout) : pick_backward<64, false>(layout))
                      : (norm ? pick_backward<128, true>(layout) : pick_backward<128, false>(layout));
   kern<<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(p);
-  if ((rc = launched("rope backward")) || !norm) return rc;
-  rope_weights_kernel<<<static_cast<unsigned>(2 * head_dim / 32), 256, 0, s>>>(
-      p.part, blocks, head_dim, q_weight ? dq_weight : nullptr, k_weight ? dk_weight : nullptr);
-  return launched("rope weights");
+  if ((rc = launched("rope backward", cudaGetLastError())) || !norm) return rc;
+  return launched("rope weights",
+                  launch_chained(rope_weights_kernel, dim3(static_cast<unsigned>(2 * head_dim / 32)), 1024, 0, s,
+                                 static_cast<const float*>(p.part), blocks, head_dim,
+                                 q_weight ? dq_weight : nullptr, k_weight ? dk_weight : nullptr));
 }
 
 int sinkattn_rope_append_paged(const void* q, const void* k, const void* v, int64_t q_stride,
