@@ -367,18 +367,21 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
 }
 
 // Gradients of heads `pass * 32 / C + s` of one token: grad(h) and in(h) are the
-// rows of dy and of x, `sum` takes this thread's share of the weights' gradients.
-template <int D, int LAYOUT, typename Grad, typename Store>
+// rows of dy and of x; this thread's share of the weights' gradients is added to
+// its column of `sums`.
+template <int D, int LAYOUT, bool NORM, typename Grad, typename Store>
 __device__ __forceinline__ void rotate_rows_back(const RopeParams& p, Grad grad, const __nv_bfloat16* in,
                                                  int heads, int lo, int hi, const float* w,
                                                  const float2 (&co)[2], const float2 (&si)[2], int c, int s,
-                                                 float2 (&sum_a)[2], float2 (&sum_b)[2], Store store) {
+                                                 float (*sums)[kThreads], Store store) {
   constexpr int R = 32 / (D / 8);
-  constexpr int kBackIlp = 2;
+  constexpr int kBackIlp = NORM ? 2 : 4;   // (with a norm each row brings its x along)
   if (lo >= hi) return;
   float2 wa[2], wb[2];
   load_weights<LAYOUT>(w, c, p.r, wa, wb);
   const float2 ns[2] = {neg2(si[0]), neg2(si[1])};
+  float2 sum_a[2], sum_b[2];
+  sum_a[0] = sum_a[1] = sum_b[0] = sum_b[1] = make_float2(0.f, 0.f);
   for (int i = lo; i < hi; i += kBackIlp) {
     uint4 raw[kBackIlp], xr[kBackIlp];
 #pragma unroll
@@ -425,20 +428,30 @@ __device__ __forceinline__ void rotate_rows_back(const RopeParams& p, Grad grad,
       if (i + u < hi && h < heads) store(h, y, z);
     }
   }
+  if constexpr (NORM) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      sums[2 * e][threadIdx.x] += sum_a[e].x;
+      sums[2 * e + 1][threadIdx.x] += sum_a[e].y;
+      sums[4 + 2 * e][threadIdx.x] += sum_b[e].x;
+      sums[5 + 2 * e][threadIdx.x] += sum_b[e].y;
+    }
+  }
 }
 
 // Gradients of the projection's rows; warps walk over the tokens (and shares
 // of them) with the grid's stride and leave their block's sums of the weights'
 // gradients in p.part.
 template <int D, int LAYOUT, bool NORM>
-__global__ void __launch_bounds__(kThreads) rope_backward_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kThreads, 3) rope_backward_kernel(const RopeParams p) {
   constexpr int C = D / 8, R = 32 / C;
-  __shared__ float sums[NORM ? kThreads : 1][9];
+  __shared__ float sums[NORM ? 16 : 1][kThreads];   // q's, then k's; a column is its thread's own
   grid_launch_dependents();
   const int lane = threadIdx.x & 31, c = lane % C, s = lane / C;
-  float2 qa[2], qb[2], ka[2], kb[2];
+  if constexpr (NORM) {
 #pragma unroll
-  for (int e = 0; e < 2; ++e) qa[e] = qb[e] = ka[e] = kb[e] = make_float2(0.f, 0.f);
+    for (int e = 0; e < 16; ++e) sums[e][threadIdx.x] = 0.f;
+  }
   const long long units = static_cast<long long>(p.tokens) * p.parts;
   for (long long unit = static_cast<long long>(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32; unit < units;
        unit += static_cast<long long>(gridDim.x) * (kThreads / 32)) {
@@ -449,15 +462,15 @@ __global__ void __launch_bounds__(kThreads) rope_backward_kernel(const RopeParam
     float2 co[2], si[2];
     angles(p, at.pos, c, co, si);
     const __nv_bfloat16* dq = p.dq + static_cast<long long>(t) * p.Hq * D;
-    rotate_rows_back<D, LAYOUT>(p, [&](int h) { return dq + h * D; }, NORM ? p.q + t * p.q_stride : nullptr,
-                                p.Hq, sh.q_lo, sh.q_hi, NORM ? p.q_weight : nullptr, co, si, c, s, qa, qb,
+    rotate_rows_back<D, LAYOUT, NORM>(p, [&](int h) { return dq + h * D; }, NORM ? p.q + t * p.q_stride : nullptr,
+                                p.Hq, sh.q_lo, sh.q_hi, NORM ? p.q_weight : nullptr, co, si, c, s, sums,
                                 [&](int h, const float2 (&a)[2], const float2 (&b)[2]) {
                                   store_row<LAYOUT>(p.dq_in + t * p.dq_stride + h * D, c, p.r, a, b);
                                 });
-    rotate_rows_back<D, LAYOUT>(
+    rotate_rows_back<D, LAYOUT, NORM>(
         p, [&](int h) { return p.dk + (at.row + static_cast<long long>(h) * at.step) * D; },
         NORM ? p.k + t * p.k_stride : nullptr, p.Hkv, sh.k_lo, sh.k_hi, NORM ? p.k_weight : nullptr, co, si, c,
-        s, ka, kb, [&](int h, const float2 (&a)[2], const float2 (&b)[2]) {
+        s, sums + (NORM ? 8 : 0), [&](int h, const float2 (&a)[2], const float2 (&b)[2]) {
           store_row<LAYOUT>(p.dk_in + t * p.dk_stride + h * D, c, p.r, a, b);
         });
     for (int i = sh.v_lo; i < sh.v_hi; ++i) {
@@ -469,25 +482,13 @@ __global__ void __launch_bounds__(kThreads) rope_backward_kernel(const RopeParam
   }
   if constexpr (NORM) {
     // the block's sums, over the threads that hold the same elements, in a fixed order
-#pragma unroll
-    for (int which = 0; which < 2; ++which) {
-      __syncthreads();
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float2 a = which ? ka[e] : qa[e], b = which ? kb[e] : qb[e];
-        sums[threadIdx.x][2 * e] = a.x;
-        sums[threadIdx.x][2 * e + 1] = a.y;
-        sums[threadIdx.x][4 + 2 * e] = b.x;
-        sums[threadIdx.x][5 + 2 * e] = b.y;
-      }
-      __syncthreads();
-      if (threadIdx.x < D) {
-        const int cc = threadIdx.x / 8, e = threadIdx.x % 8;
-        float x = 0.f;
-        for (int j = 0; j < kThreads / C; ++j) x += sums[j * C + cc][e];
-        const int el = e < 4 ? first_of<LAYOUT>(cc, e, p.r) : second_of<LAYOUT>(cc, e - 4, p.r);
-        p.part[(static_cast<long long>(blockIdx.x) * 2 + which) * D + el] = x;
-      }
+    __syncthreads();
+    if (threadIdx.x < 2 * D) {
+      const int which = threadIdx.x / D, cc = threadIdx.x % D / 8, e = threadIdx.x % 8;
+      float x = 0.f;
+      for (int j = 0; j < kThreads / C; ++j) x += sums[8 * which + e][j * C + cc];
+      const int el = e < 4 ? first_of<LAYOUT>(cc, e, p.r) : second_of<LAYOUT>(cc, e - 4, p.r);
+      p.part[(static_cast<long long>(blockIdx.x) * 2 + which) * D + el] = x;
     }
   }
 }
@@ -615,7 +616,7 @@ int launch_forward(RopeParams& p, int d, int kind, int interleaved, cudaStream_t
 
 // (a fixed bound, so that neither the workspace nor the order of the sums goes by the device)
 int backward_blocks(int32_t tokens) {
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(tokens, 4 * 152)));
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(tokens, 3 * 152)));
 }
 
 int append(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
@@ -824,7 +825,11 @@ int sinkattn_rope_qkv_backward(const void* dq, const void* dk, const void* dv, c
   if (!cu_seqlens || !aligned(cu_seqlens, 4) || !aligned(positions, 4))
     return refuse(SINKATTN_INVALID_ARG,
                   "cu_seqlens must be non-null, cu_seqlens and positions 4-byte aligned");
-  const int blocks = backward_blocks(tokens);
+  p.parts = shares(tokens, num_qo_heads, num_kv_heads, head_dim);
+  // without sums of weights' gradients there is no reason to hold a block longer
+  const int64_t blocks = norm ? backward_blocks(tokens) : (int64_t{tokens} * p.parts + kThreads / 32 - 1) /
+                                                              (kThreads / 32);
+  if (blocks >= (int64_t{1} << 31)) return refuse(SINKATTN_UNSUPPORTED, "too many work items");
   if (norm) {
     if (!workspace || !aligned(workspace, 256))
       return refuse(SINKATTN_INVALID_ARG, "workspace must be non-null and 256-byte aligned");
@@ -845,7 +850,6 @@ int sinkattn_rope_qkv_backward(const void* dq, const void* dk, const void* dv, c
   p.dv_in = static_cast<__nv_bfloat16*>(dv_in);
   p.dq_stride = dq_stride, p.dk_stride = dk_stride, p.dv_stride = dv_stride;
   p.part = static_cast<float*>(workspace);
-  p.parts = shares(tokens, num_qo_heads, num_kv_heads, head_dim);
   const int layout = layout_of(p.r, interleaved);
   void (*kern)(const RopeParams) =
       head_dim == 64 ? (norm ? pick_backward<64, true>(layout) : pick_backward<64, false>(layout))
@@ -854,7 +858,7 @@ int sinkattn_rope_qkv_backward(const void* dq, const void* dk, const void* dv, c
   if ((rc = launched("rope backward", cudaGetLastError())) || !norm) return rc;
   return launched("rope weights",
                   launch_chained(rope_weights_kernel, dim3(static_cast<unsigned>(2 * head_dim / 32)), 1024, 0, s,
-                                 static_cast<const float*>(p.part), blocks, head_dim,
+                                 static_cast<const float*>(p.part), static_cast<int>(blocks), head_dim,
                                  q_weight ? dq_weight : nullptr, k_weight ? dk_weight : nullptr));
 }
 
