@@ -35,7 +35,7 @@ __device__ int g_status_rope;
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kIlp = 4;   // rows of a thread in flight
+constexpr int kSlots = 4;  // of a warp's ring in shared memory: one step's rows each
 
 enum Layout { kHalf = 0, kInterleaved = 1, kHalfOdd = 2 };
 enum Kind { kPack = 0, kAppend = 1, kAppendFp8 = 2 };
@@ -92,10 +92,10 @@ __device__ __forceinline__ int second_of(int c, int e, int r) {
 template <int LAYOUT>
 __device__ __forceinline__ uint4 load_row(const __nv_bfloat16* row, int c, int r) {
   if constexpr (LAYOUT == kInterleaved) {
-    return __ldcs(reinterpret_cast<const uint4*>(row + 8 * c));
+    return *reinterpret_cast<const uint4*>(row + 8 * c);
   } else if constexpr (LAYOUT == kHalf) {
-    const uint2 a = __ldcs(reinterpret_cast<const uint2*>(row + first_of<LAYOUT>(c, 0, r)));
-    const uint2 b = __ldcs(reinterpret_cast<const uint2*>(row + second_of<LAYOUT>(c, 0, r)));
+    const uint2 a = *reinterpret_cast<const uint2*>(row + first_of<LAYOUT>(c, 0, r));
+    const uint2 b = *reinterpret_cast<const uint2*>(row + second_of<LAYOUT>(c, 0, r));
     return make_uint4(a.x, a.y, b.x, b.y);
   } else {
     const uint16_t* s = reinterpret_cast<const uint16_t*>(row);
@@ -263,179 +263,215 @@ __device__ __forceinline__ void load_weights(const float* w, int c, int r, float
   }
 }
 
-// The passes (of 32 / C heads: first q's, then k's, then v's) of share `part` of a token.
+// Share `part` of a token's work: passes of 32 / C heads, PER of them a step,
+// first q's, then k's, then v's.
 struct Share {
-  int q_lo, q_hi, k_lo, k_hi, v_lo, v_hi;
+  int lo[3], hi[3];   // passes
 };
 __device__ __forceinline__ Share share_of(int Hq, int Hkv, int per_pass, int part, int parts) {
   const int nq = (Hq + per_pass - 1) / per_pass, nk = (Hkv + per_pass - 1) / per_pass;
   const int all = nq + 2 * nk;
   const int lo = all * part / parts, hi = all * (part + 1) / parts;
-  return {min(lo, nq), min(hi, nq), min(max(lo - nq, 0), nk), min(max(hi - nq, 0), nk),
-          max(lo - nq - nk, 0), max(hi - nq - nk, 0)};
+  return {{min(lo, nq), min(max(lo - nq, 0), nk), max(lo - nq - nk, 0)},
+          {min(hi, nq), min(max(hi - nq, 0), nk), max(hi - nq - nk, 0)}};
 }
 
-// Norm and rotation of heads `pass * 32 / C + s` of one token, pass lo .. hi - 1.
-template <int D, int LAYOUT, typename Store>
-__device__ __forceinline__ void rotate_rows(const RopeParams& p, const __nv_bfloat16* src, int heads, int lo,
-                                            int hi, const float* w, const float2 (&co)[2],
-                                            const float2 (&si)[2], int c, int s, Store store) {
+// 16 bytes to shared memory; zeros, and nothing read, unless `ok`.
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                   static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+               "l"(src), "r"(ok ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Norm and rotation of a step's rows, from the ring; h0 is this thread's head in the first pass.
+template <int D, int LAYOUT, int PER, typename Store>
+__device__ __forceinline__ void rotate_step(const RopeParams& p, const __nv_bfloat16* slot, int h0, int left,
+                                            int heads, bool normed, const float2 (&ca)[2], const float2 (&sb)[2],
+                                            const float2 (&cb)[2], const float2 (&sa)[2], int c, int s,
+                                            Store store) {
   constexpr int R = 32 / (D / 8);
-  if (lo >= hi) return;
-  // y_a = rs (x_a (w_a cos) - x_b (w_b sin)), y_b = rs (x_b (w_b cos) + x_a (w_a sin))
-  float2 wa[2], wb[2], ca[2], sb[2], cb[2], sa[2];
-  load_weights<LAYOUT>(w, c, p.r, wa, wb);
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    ca[e] = __fmul2_rn(wa[e], co[e]);
-    sa[e] = __fmul2_rn(wa[e], si[e]);
-    cb[e] = __fmul2_rn(wb[e], co[e]);
-    sb[e] = neg2(__fmul2_rn(wb[e], si[e]));
-  }
-  for (int i = lo; i < hi; i += kIlp) {
-    uint4 raw[kIlp];
+  for (int u = 0; u < PER; ++u) {
+    const int h = h0 + u * R;
+    float2 a[2], b[2], y[2], z[2];
+    unpack<LAYOUT>(load_row<LAYOUT>(slot + (u * R + s) * D, c, p.r), a, b);
 #pragma unroll
-    for (int u = 0; u < kIlp; ++u) {
-      const int h = (i + u) * R + s;
-      raw[u] = make_uint4(0, 0, 0, 0);
-      if (i + u < hi && h < heads) raw[u] = load_row<LAYOUT>(src + h * D, c, p.r);
+    for (int e = 0; e < 2; ++e) {
+      y[e] = __ffma2_rn(a[e], ca[e], __fmul2_rn(b[e], sb[e]));
+      z[e] = __ffma2_rn(b[e], cb[e], __fmul2_rn(a[e], sa[e]));
     }
-#pragma unroll
-    for (int u = 0; u < kIlp; ++u) {
-      const int h = (i + u) * R + s;
-      float2 a[2], b[2];
-      unpack<LAYOUT>(raw[u], a, b);
-      float rs = 1.f;
-      if (w != nullptr) rs = rsqrtf(head_sum<D>(dot_pairs(a, b, a, b)) * (1.f / D) + p.eps);
-      float2 y[2], z[2];
+    if (normed) {
+      const float rs = rsqrtf(head_sum<D>(dot_pairs(a, b, a, b)) * (1.f / D) + p.eps);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        y[e] = __ffma2_rn(a[e], ca[e], __fmul2_rn(b[e], sb[e]));
-        z[e] = __ffma2_rn(b[e], cb[e], __fmul2_rn(a[e], sa[e]));
-        if (w != nullptr) {
-          y[e] = __fmul2_rn(y[e], make_float2(rs, rs));
-          z[e] = __fmul2_rn(z[e], make_float2(rs, rs));
-        }
+        y[e] = __fmul2_rn(y[e], make_float2(rs, rs));
+        z[e] = __fmul2_rn(z[e], make_float2(rs, rs));
       }
-      if (i + u < hi && h < heads) store(h, y, z);
     }
+    if (u < left && h < heads) store(h, y, z);
   }
 }
 
 template <int D, int LAYOUT, int KIND>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kThreads, 3) rope_kernel(const RopeParams p) {
   constexpr int C = D / 8, R = 32 / C;   // threads of a head, heads of a pass
+  constexpr int PER = 2;
+  __shared__ alignas(16) __nv_bfloat16 ring[kThreads / 32][kSlots][PER * R * D];
   const long long unit = static_cast<long long>(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32;
   const int t = static_cast<int>(unit / p.parts), part = static_cast<int>(unit % p.parts);
   if (t >= p.tokens) return;             // (whole warps)
-  const Token at = token_of<KIND != kPack>(p, t);
-  if (KIND == kPack && at.row < 0) return;
   const int lane = threadIdx.x & 31, c = lane % C, s = lane / C;
+  auto& mine = ring[threadIdx.x / 32];
   const Share sh = share_of(p.Hq, p.Hkv, R, part, p.parts);
+  const int nq = (sh.hi[0] - sh.lo[0] + PER - 1) / PER, nk = (sh.hi[1] - sh.lo[1] + PER - 1) / PER;
+  const int n = nq + nk + (sh.hi[2] - sh.lo[2] + PER - 1) / PER;   // steps
+  const auto issue = [&](int st) {
+    if (st < n) {
+      const int seg = st < nq ? 0 : st < nq + nk ? 1 : 2;
+      const int pass = (seg == 0 ? sh.lo[0] + PER * st
+                                 : seg == 1 ? sh.lo[1] + PER * (st - nq) : sh.lo[2] + PER * (st - nq - nk));
+      const int hi = seg == 0 ? sh.hi[0] : seg == 1 ? sh.hi[1] : sh.hi[2];
+      const __nv_bfloat16* row = (seg == 0 ? p.q + t * p.q_stride
+                                           : seg == 1 ? p.k + t * p.k_stride : p.v + t * p.v_stride) + 8 * c;
+#pragma unroll
+      for (int u = 0; u < PER; ++u) {
+        const int h = (pass + u) * R + s;
+        const bool ok = pass + u < hi && h < (seg == 0 ? p.Hq : p.Hkv);
+        copy16(&mine[st % kSlots][u * R * D + lane * 8], row + (ok ? h * D : 0), ok);
+      }
+    }
+    commit_copies();   // (an empty group keeps the count)
+  };
+  int st = 0;
+  // the rows of step st are there, and those of the step before have been read by all lanes
+  const auto next = [&]() {
+    wait_copies<kSlots - 2>();
+    __syncwarp();
+    issue(st + kSlots - 1);
+  };
+#pragma unroll
+  for (int i = 0; i < kSlots - 1; ++i) issue(i);
+
+  const Token at = token_of<KIND != kPack>(p, t);
+  if (KIND == kPack && at.row < 0) {
+    wait_copies<0>();
+    return;
+  }
   float2 co[2], si[2];
   angles(p, at.pos, c, co, si);
-  __nv_bfloat16* q_out = p.q_out + static_cast<long long>(t) * p.Hq * D;
-  rotate_rows<D, LAYOUT>(p, p.q + t * p.q_stride, p.Hq, sh.q_lo, sh.q_hi, p.q_weight, co, si, c, s,
-                         [&](int h, const float2 (&a)[2], const float2 (&b)[2]) {
-                           store_row<LAYOUT>(q_out + h * D, c, p.r, a, b);
-                         });
-  if (at.row < 0) return;
-  rotate_rows<D, LAYOUT>(p, p.k + t * p.k_stride, p.Hkv, sh.k_lo, sh.k_hi, p.k_weight, co, si, c, s,
-                         [&](int h, const float2 (&a)[2], const float2 (&b)[2]) {
-                           const long long row = at.row + static_cast<long long>(h) * at.step;
-                           if constexpr (KIND == kAppendFp8)
-                             store_codes<LAYOUT>(p.k_pages + row * D, c, p.r, a, b, p.k_scale[h]);
-                           else
-                             store_row<LAYOUT>((KIND == kPack ? p.k_out
-                                                              : reinterpret_cast<__nv_bfloat16*>(p.k_pages)) +
-                                                   row * D, c, p.r, a, b);
-                         });
-  for (int i = sh.v_lo; i < sh.v_hi; ++i) {
-    const int h = i * R + s;
-    if (h >= p.Hkv) continue;
-    const uint4 raw = load_row<kInterleaved>(p.v + t * p.v_stride + h * D, c, p.r);
-    const long long row = at.row + static_cast<long long>(h) * at.step;
-    if constexpr (KIND == kAppendFp8) {
-      float2 a[2], b[2];
-      unpack<kInterleaved>(raw, a, b);
-      store_codes<kInterleaved>(p.v_pages + row * D, c, p.r, a, b, p.v_scale[h]);
-    } else {
-      __nv_bfloat16* out = KIND == kPack ? p.v_out : reinterpret_cast<__nv_bfloat16*>(p.v_pages);
-      *reinterpret_cast<uint4*>(out + row * D + 8 * c) = raw;
-    }
-  }
-}
-
-// Gradients of heads `pass * 32 / C + s` of one token: grad(h) and in(h) are the
-// rows of dy and of x; this thread's share of the weights' gradients is added to
-// its column of `sums`.
-template <int D, int LAYOUT, bool NORM, typename Grad, typename Store>
-__device__ __forceinline__ void rotate_rows_back(const RopeParams& p, Grad grad, const __nv_bfloat16* in,
-                                                 int heads, int lo, int hi, const float* w,
-                                                 const float2 (&co)[2], const float2 (&si)[2], int c, int s,
-                                                 float (*sums)[kThreads], Store store) {
-  constexpr int R = 32 / (D / 8);
-  constexpr int kBackIlp = NORM ? 2 : 4;   // (with a norm each row brings its x along)
-  if (lo >= hi) return;
-  float2 wa[2], wb[2];
-  load_weights<LAYOUT>(w, c, p.r, wa, wb);
-  const float2 ns[2] = {neg2(si[0]), neg2(si[1])};
-  float2 sum_a[2], sum_b[2];
-  sum_a[0] = sum_a[1] = sum_b[0] = sum_b[1] = make_float2(0.f, 0.f);
-  for (int i = lo; i < hi; i += kBackIlp) {
-    uint4 raw[kBackIlp], xr[kBackIlp];
-#pragma unroll
-    for (int u = 0; u < kBackIlp; ++u) {
-      const int h = (i + u) * R + s;
-      raw[u] = xr[u] = make_uint4(0, 0, 0, 0);
-      if (i + u < hi && h < heads) {
-        raw[u] = load_row<LAYOUT>(grad(h), c, p.r);
-        if (w != nullptr) xr[u] = load_row<LAYOUT>(in + h * D, c, p.r);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kBackIlp; ++u) {
-      const int h = (i + u) * R + s;
-      float2 a[2], b[2], y[2], z[2];
-      unpack<LAYOUT>(raw[u], a, b);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {   // g = R^T dy
-        y[e] = __ffma2_rn(a[e], co[e], __fmul2_rn(b[e], si[e]));
-        z[e] = __ffma2_rn(b[e], co[e], __fmul2_rn(a[e], ns[e]));
-      }
-      if (w != nullptr) {
-        float2 xa[2], xb[2], ua[2], ub[2];
-        unpack<LAYOUT>(xr[u], xa, xb);
-        const float rs = rsqrtf(head_sum<D>(dot_pairs(xa, xb, xa, xb)) * (1.f / D) + p.eps);
-        const float2 rs2 = make_float2(rs, rs);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {   // (rows past the last have g = 0)
-          xa[e] = __fmul2_rn(xa[e], rs2);
-          xb[e] = __fmul2_rn(xb[e], rs2);
-          sum_a[e] = __ffma2_rn(y[e], xa[e], sum_a[e]);
-          sum_b[e] = __ffma2_rn(z[e], xb[e], sum_b[e]);
-          ua[e] = __fmul2_rn(y[e], wa[e]);
-          ub[e] = __fmul2_rn(z[e], wb[e]);
-        }
-        const float dot = head_sum<D>(dot_pairs(ua, ub, xa, xb)) * (-1.f / D);
-        const float2 dot2 = make_float2(dot, dot);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          y[e] = __fmul2_rn(rs2, __ffma2_rn(xa[e], dot2, ua[e]));
-          z[e] = __fmul2_rn(rs2, __ffma2_rn(xb[e], dot2, ub[e]));
-        }
-      }
-      if (i + u < hi && h < heads) store(h, y, z);
-    }
-  }
-  if constexpr (NORM) {
+#pragma unroll 1
+  for (int seg = 0; seg < 2; ++seg) {   // queries, keys
+    const float* w = seg ? p.k_weight : p.q_weight;
+    const int heads = seg ? p.Hkv : p.Hq, end = seg ? nq + nk : nq;
+    if (seg && at.row < 0) break;
+    if (st >= end) continue;
+    // y_a = rs (x_a (w_a cos) - x_b (w_b sin)), y_b = rs (x_b (w_b cos) + x_a (w_a sin))
+    float2 wa[2], wb[2], ca[2], sb[2], cb[2], sa[2];
+    load_weights<LAYOUT>(w, c, p.r, wa, wb);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      sums[2 * e][threadIdx.x] += sum_a[e].x;
-      sums[2 * e + 1][threadIdx.x] += sum_a[e].y;
-      sums[4 + 2 * e][threadIdx.x] += sum_b[e].x;
-      sums[5 + 2 * e][threadIdx.x] += sum_b[e].y;
+      ca[e] = __fmul2_rn(wa[e], co[e]);
+      sa[e] = __fmul2_rn(wa[e], si[e]);
+      cb[e] = __fmul2_rn(wb[e], co[e]);
+      sb[e] = neg2(__fmul2_rn(wb[e], si[e]));
     }
+    if (seg == 0) {
+      __nv_bfloat16* q_out = p.q_out + static_cast<long long>(t) * p.Hq * D;
+      for (int pass = sh.lo[0]; st < end; ++st, pass += PER) {
+        next();
+        rotate_step<D, LAYOUT, PER>(p, mine[st % kSlots], pass * R + s, sh.hi[0] - pass, heads, w != nullptr, ca,
+                                    sb, cb, sa, c, s, [&](int h, const float2 (&a)[2], const float2 (&b)[2]) {
+                                      store_row<LAYOUT>(q_out + h * D, c, p.r, a, b);
+                                    });
+      }
+    } else {
+      for (int pass = sh.lo[1]; st < end; ++st, pass += PER) {
+        next();
+        rotate_step<D, LAYOUT, PER>(
+            p, mine[st % kSlots], pass * R + s, sh.hi[1] - pass, heads, w != nullptr, ca, sb, cb, sa, c, s,
+            [&](int h, const float2 (&a)[2], const float2 (&b)[2]) {
+              const long long row = at.row + static_cast<long long>(h) * at.step;
+              if constexpr (KIND == kAppendFp8)
+                store_codes<LAYOUT>(p.k_pages + row * D, c, p.r, a, b, p.k_scale[h]);
+              else
+                store_row<LAYOUT>(
+                    (KIND == kPack ? p.k_out : reinterpret_cast<__nv_bfloat16*>(p.k_pages)) + row * D, c, p.r, a,
+                    b);
+            });
+      }
+    }
+  }
+  if (at.row >= 0) {
+    for (int pass = sh.lo[2]; st < n; ++st, pass += PER) {
+      next();
+#pragma unroll
+      for (int u = 0; u < PER; ++u) {
+        const int h = (pass + u) * R + s;
+        if (pass + u >= sh.hi[2] || h >= p.Hkv) continue;
+        const uint4 raw = load_row<kInterleaved>(mine[st % kSlots] + (u * R + s) * D, c, p.r);
+        const long long row = at.row + static_cast<long long>(h) * at.step;
+        if constexpr (KIND == kAppendFp8) {
+          float2 a[2], b[2];
+          unpack<kInterleaved>(raw, a, b);
+          store_codes<kInterleaved>(p.v_pages + row * D, c, p.r, a, b, p.v_scale[h]);
+        } else {
+          __nv_bfloat16* out = KIND == kPack ? p.v_out : reinterpret_cast<__nv_bfloat16*>(p.v_pages);
+          *reinterpret_cast<uint4*>(out + row * D + 8 * c) = raw;
+        }
+      }
+    }
+  }
+  wait_copies<0>();
+}
+
+// Gradients of a step's rows: dy in the slot's first half, x, with a norm, in
+// the second; this thread's share of the weights' gradients is added to `sum`.
+template <int D, int LAYOUT, bool NORM, int PER, typename Store>
+__device__ __forceinline__ void rotate_step_back(const RopeParams& p, const __nv_bfloat16* slot, int h0, int left,
+                                                 int heads, bool normed, const float2 (&wa)[2],
+                                                 const float2 (&wb)[2], const float2 (&co)[2],
+                                                 const float2 (&si)[2], int c, int s, float2 (&sum_a)[2],
+                                                 float2 (&sum_b)[2], Store store) {
+  constexpr int R = 32 / (D / 8);
+#pragma unroll
+  for (int u = 0; u < PER; ++u) {
+    const int h = h0 + u * R;
+    float2 a[2], b[2], y[2], z[2];
+    unpack<LAYOUT>(load_row<LAYOUT>(slot + (u * R + s) * D, c, p.r), a, b);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {   // g = R^T dy
+      y[e] = __ffma2_rn(a[e], co[e], __fmul2_rn(b[e], si[e]));
+      z[e] = __ffma2_rn(b[e], co[e], __fmul2_rn(neg2(a[e]), si[e]));
+    }
+    if (NORM && normed) {
+      float2 xa[2], xb[2], ua[2], ub[2];
+      unpack<LAYOUT>(load_row<LAYOUT>(slot + (PER * R + u * R + s) * D, c, p.r), xa, xb);
+      const float rs = rsqrtf(head_sum<D>(dot_pairs(xa, xb, xa, xb)) * (1.f / D) + p.eps);
+      const float2 rs2 = make_float2(rs, rs);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {   // (rows past the last have g = 0)
+        xa[e] = __fmul2_rn(xa[e], rs2);
+        xb[e] = __fmul2_rn(xb[e], rs2);
+        sum_a[e] = __ffma2_rn(y[e], xa[e], sum_a[e]);
+        sum_b[e] = __ffma2_rn(z[e], xb[e], sum_b[e]);
+        ua[e] = __fmul2_rn(y[e], wa[e]);
+        ub[e] = __fmul2_rn(z[e], wb[e]);
+      }
+      const float dot = head_sum<D>(dot_pairs(ua, ub, xa, xb)) * (-1.f / D);
+      const float2 dot2 = make_float2(dot, dot);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        y[e] = __fmul2_rn(rs2, __ffma2_rn(xa[e], dot2, ua[e]));
+        z[e] = __fmul2_rn(rs2, __ffma2_rn(xb[e], dot2, ub[e]));
+      }
+    }
+    if (u < left && h < heads) store(h, y, z);
   }
 }
 
@@ -445,9 +481,12 @@ __device__ __forceinline__ void rotate_rows_back(const RopeParams& p, Grad grad,
 template <int D, int LAYOUT, bool NORM>
 __global__ void __launch_bounds__(kThreads, 3) rope_backward_kernel(const RopeParams p) {
   constexpr int C = D / 8, R = 32 / C;
+  constexpr int PER = NORM ? 1 : 2;
+  __shared__ alignas(16) __nv_bfloat16 ring[kThreads / 32][kSlots][2 * R * D];
   __shared__ float sums[NORM ? 16 : 1][kThreads];   // q's, then k's; a column is its thread's own
   grid_launch_dependents();
   const int lane = threadIdx.x & 31, c = lane % C, s = lane / C;
+  auto& mine = ring[threadIdx.x / 32];
   if constexpr (NORM) {
 #pragma unroll
     for (int e = 0; e < 16; ++e) sums[e][threadIdx.x] = 0.f;
@@ -459,27 +498,80 @@ __global__ void __launch_bounds__(kThreads, 3) rope_backward_kernel(const RopePa
     const Token at = token_of<false>(p, t);
     if (at.row < 0) continue;
     const Share sh = share_of(p.Hq, p.Hkv, R, part, p.parts);
+    const int nq = (sh.hi[0] - sh.lo[0] + PER - 1) / PER, nk = (sh.hi[1] - sh.lo[1] + PER - 1) / PER;
+    const int n = nq + nk + (sh.hi[2] - sh.lo[2] + PER - 1) / PER;   // steps
+    const auto issue = [&](int st) {
+      if (st < n) {
+        const int seg = st < nq ? 0 : st < nq + nk ? 1 : 2;
+        const int pass = (seg == 0 ? sh.lo[0] + PER * st
+                                   : seg == 1 ? sh.lo[1] + PER * (st - nq) : sh.lo[2] + PER * (st - nq - nk));
+        const int hi = seg == 0 ? sh.hi[0] : seg == 1 ? sh.hi[1] : sh.hi[2];
+        const __nv_bfloat16* g = (seg == 0 ? p.dq + static_cast<long long>(t) * p.Hq * D
+                                           : (seg == 1 ? p.dk : p.dv) + at.row * D) + 8 * c;
+        const long long step = seg == 0 ? D : static_cast<long long>(at.step) * D;
+#pragma unroll
+        for (int u = 0; u < PER; ++u) {
+          const int h = (pass + u) * R + s;
+          const bool ok = pass + u < hi && h < (seg == 0 ? p.Hq : p.Hkv);
+          copy16(&mine[st % kSlots][u * R * D + lane * 8], g + (ok ? h * step : 0), ok);
+          if (NORM && (seg == 0 ? p.q_weight : seg == 1 ? p.k_weight : nullptr) != nullptr) {
+            const __nv_bfloat16* x = (seg == 0 ? p.q + t * p.q_stride : p.k + t * p.k_stride) + 8 * c;
+            copy16(&mine[st % kSlots][(PER + u) * R * D + lane * 8], x + (ok ? h * D : 0), ok);
+          }
+        }
+      }
+      commit_copies();   // (an empty group keeps the count)
+    };
+    int st = 0;
+    const auto next = [&]() {   // as in rope_kernel
+      wait_copies<kSlots - 2>();
+      __syncwarp();
+      issue(st + kSlots - 1);
+    };
+    __syncwarp();   // the unit before has been read
+#pragma unroll
+    for (int i = 0; i < kSlots - 1; ++i) issue(i);
     float2 co[2], si[2];
     angles(p, at.pos, c, co, si);
-    const __nv_bfloat16* dq = p.dq + static_cast<long long>(t) * p.Hq * D;
-    rotate_rows_back<D, LAYOUT, NORM>(p, [&](int h) { return dq + h * D; }, NORM ? p.q + t * p.q_stride : nullptr,
-                                p.Hq, sh.q_lo, sh.q_hi, NORM ? p.q_weight : nullptr, co, si, c, s, sums,
-                                [&](int h, const float2 (&a)[2], const float2 (&b)[2]) {
-                                  store_row<LAYOUT>(p.dq_in + t * p.dq_stride + h * D, c, p.r, a, b);
-                                });
-    rotate_rows_back<D, LAYOUT, NORM>(
-        p, [&](int h) { return p.dk + (at.row + static_cast<long long>(h) * at.step) * D; },
-        NORM ? p.k + t * p.k_stride : nullptr, p.Hkv, sh.k_lo, sh.k_hi, NORM ? p.k_weight : nullptr, co, si, c,
-        s, sums + (NORM ? 8 : 0), [&](int h, const float2 (&a)[2], const float2 (&b)[2]) {
-          store_row<LAYOUT>(p.dk_in + t * p.dk_stride + h * D, c, p.r, a, b);
-        });
-    for (int i = sh.v_lo; i < sh.v_hi; ++i) {
-      const int h = i * R + s;
-      if (h < p.Hkv)
-        *reinterpret_cast<uint4*>(p.dv_in + t * p.dv_stride + h * D + 8 * c) = load_row<kInterleaved>(
-            p.dv + (at.row + static_cast<long long>(h) * at.step) * D, c, p.r);
+#pragma unroll 1
+    for (int seg = 0; seg < 2; ++seg) {   // queries, keys
+      const int end = seg ? nq + nk : nq, hi = seg ? sh.hi[1] : sh.hi[0];
+      if (st >= end) continue;
+      const float* w = !NORM ? nullptr : seg ? p.k_weight : p.q_weight;
+      __nv_bfloat16* out = seg ? p.dk_in + t * p.dk_stride : p.dq_in + t * p.dq_stride;
+      float2 wa[2], wb[2], sum_a[2], sum_b[2];
+      load_weights<LAYOUT>(w, c, p.r, wa, wb);
+      sum_a[0] = sum_a[1] = sum_b[0] = sum_b[1] = make_float2(0.f, 0.f);
+      for (int pass = seg ? sh.lo[1] : sh.lo[0]; st < end; ++st, pass += PER) {
+        next();
+        rotate_step_back<D, LAYOUT, NORM, PER>(
+            p, mine[st % kSlots], pass * R + s, hi - pass, seg ? p.Hkv : p.Hq, w != nullptr, wa, wb, co, si, c, s,
+            sum_a, sum_b, [&](int h, const float2 (&a)[2], const float2 (&b)[2]) {
+              store_row<LAYOUT>(out + h * D, c, p.r, a, b);
+            });
+      }
+      if constexpr (NORM) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          sums[8 * seg + 2 * e][threadIdx.x] += sum_a[e].x;
+          sums[8 * seg + 2 * e + 1][threadIdx.x] += sum_a[e].y;
+          sums[8 * seg + 4 + 2 * e][threadIdx.x] += sum_b[e].x;
+          sums[8 * seg + 5 + 2 * e][threadIdx.x] += sum_b[e].y;
+        }
+      }
+    }
+    for (int pass = sh.lo[2]; st < n; ++st, pass += PER) {
+      next();
+#pragma unroll
+      for (int u = 0; u < PER; ++u) {
+        const int h = (pass + u) * R + s;
+        if (pass + u < sh.hi[2] && h < p.Hkv)
+          *reinterpret_cast<uint4*>(p.dv_in + t * p.dv_stride + h * D + 8 * c) =
+              load_row<kInterleaved>(mine[st % kSlots] + (u * R + s) * D, c, p.r);
+      }
     }
   }
+  wait_copies<0>();
   if constexpr (NORM) {
     // the block's sums, over the threads that hold the same elements, in a fixed order
     __syncthreads();
