@@ -478,15 +478,25 @@ __device__ __forceinline__ void rotate_step_back(const RopeParams& p, const __nv
 // Gradients of the projection's rows; warps walk over the tokens (and shares
 // of them) with the grid's stride and leave their block's sums of the weights'
 // gradients in p.part.
+template <int D, bool NORM>
+struct BackCfg {
+  static constexpr int PER = 2;
+  static constexpr int BLOCKS = NORM ? 2 : 3;               // of an SM
+  static constexpr int SLOT = (NORM ? 4 : 2) * (32 / (D / 8)) * D;   // elements
+  static constexpr int RING = kThreads / 32 * kSlots * SLOT * 2;     // bytes
+  static constexpr int SMEM = RING + (NORM ? 16 * kThreads * 4 : 0);
+};
 template <int D, int LAYOUT, bool NORM>
-__global__ void __launch_bounds__(kThreads, 3) rope_backward_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kThreads, BackCfg<D, NORM>::BLOCKS) rope_backward_kernel(const RopeParams p) {
   constexpr int C = D / 8, R = 32 / C;
-  constexpr int PER = NORM ? 1 : 2;
-  __shared__ alignas(16) __nv_bfloat16 ring[kThreads / 32][kSlots][2 * R * D];
-  __shared__ float sums[NORM ? 16 : 1][kThreads];   // q's, then k's; a column is its thread's own
+  using C_ = BackCfg<D, NORM>;
+  constexpr int PER = C_::PER;
+  extern __shared__ __align__(16) uint8_t smem[];
+  // q's, then k's; a column is its thread's own
+  float (*sums)[kThreads] = reinterpret_cast<float(*)[kThreads]>(smem + C_::RING);
   grid_launch_dependents();
   const int lane = threadIdx.x & 31, c = lane % C, s = lane / C;
-  auto& mine = ring[threadIdx.x / 32];
+  auto* mine = reinterpret_cast<__nv_bfloat16(*)[C_::SLOT]>(smem + threadIdx.x / 32 * (C_::RING / (kThreads / 32)));
   if constexpr (NORM) {
 #pragma unroll
     for (int e = 0; e < 16; ++e) sums[e][threadIdx.x] = 0.f;
@@ -495,8 +505,7 @@ __global__ void __launch_bounds__(kThreads, 3) rope_backward_kernel(const RopePa
   for (long long unit = static_cast<long long>(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32; unit < units;
        unit += static_cast<long long>(gridDim.x) * (kThreads / 32)) {
     const int t = static_cast<int>(unit / p.parts), part = static_cast<int>(unit % p.parts);
-    const Token at = token_of<false>(p, t);
-    if (at.row < 0) continue;
+    Token at{-1, 0, 0};
     const Share sh = share_of(p.Hq, p.Hkv, R, part, p.parts);
     const int nq = (sh.hi[0] - sh.lo[0] + PER - 1) / PER, nk = (sh.hi[1] - sh.lo[1] + PER - 1) / PER;
     const int n = nq + nk + (sh.hi[2] - sh.lo[2] + PER - 1) / PER;   // steps
@@ -529,8 +538,14 @@ __global__ void __launch_bounds__(kThreads, 3) rope_backward_kernel(const RopePa
       issue(st + kSlots - 1);
     };
     __syncwarp();   // the unit before has been read
-#pragma unroll
-    for (int i = 0; i < kSlots - 1; ++i) issue(i);
+    // (only the rows of k and v are where the sequence says)
+    for (int i = 0; i < min(nq, kSlots - 1); ++i) issue(i);
+    at = token_of<false>(p, t);
+    if (at.row < 0) {
+      wait_copies<0>();
+      continue;
+    }
+    for (int i = min(nq, kSlots - 1); i < kSlots - 1; ++i) issue(i);
     float2 co[2], si[2];
     angles(p, at.pos, c, co, si);
 #pragma unroll 1
@@ -708,7 +723,7 @@ int launch_forward(RopeParams& p, int d, int kind, int interleaved, cudaStream_t
 
 // (a fixed bound, so that neither the workspace nor the order of the sums goes by the device)
 int backward_blocks(int32_t tokens) {
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(tokens, 3 * 152)));
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(tokens, 2 * 152)));
 }
 
 int append(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
@@ -946,7 +961,11 @@ int sinkattn_rope_qkv_backward(const void* dq, const void* dk, const void* dv, c
   void (*kern)(const RopeParams) =
       head_dim == 64 ? (norm ? pick_backward<64, true>(layout) : pick_backward<64, false>(layout))
                      : (norm ? pick_backward<128, true>(layout) : pick_backward<128, false>(layout));
-  kern<<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(p);
+  const int smem = head_dim == 64 ? (norm ? BackCfg<64, true>::SMEM : BackCfg<64, false>::SMEM)
+                                  : (norm ? BackCfg<128, true>::SMEM : BackCfg<128, false>::SMEM);
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return refuse(SINKATTN_CUDA_ERROR, "cudaFuncSetAttribute failed");
+  kern<<<static_cast<unsigned>(blocks), kThreads, smem, s>>>(p);
   if ((rc = launched("rope backward", cudaGetLastError())) || !norm) return rc;
   return launched("rope weights",
                   launch_chained(rope_weights_kernel, dim3(static_cast<unsigned>(2 * head_dim / 32)), 1024, 0, s,
