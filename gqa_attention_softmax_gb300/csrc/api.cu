@@ -307,8 +307,9 @@ int sinkattn_prefill_backward_workspace_bytes(int32_t total_q, int32_t num_qo_he
   if (total_q < 0 || num_qo_heads <= 0) return fail(SINKATTN_INVALID_ARG, "bad sizes");
   if (static_cast<int64_t>(total_q) * num_qo_heads >= (int64_t{1} << 31))
     return fail(SINKATTN_UNSUPPORTED, "problem exceeds 2^31 rows");
-  *bytes = 2 * back_row_bytes(total_q, num_qo_heads) +
-           static_cast<size_t>(back_blocks(total_q, num_qo_heads)) * num_qo_heads * 4;
+  *bytes = total_q == 0 ? 0
+                        : 2 * back_row_bytes(total_q, num_qo_heads) + 256 +
+                              static_cast<size_t>(back_sink_blocks(total_q, num_qo_heads)) * num_qo_heads * 4;
   return SINKATTN_OK;
 }
 
@@ -379,7 +380,8 @@ int sinkattn_prefill_backward(const void* dout, const void* q, const void* k, co
   char* ws = static_cast<char*>(workspace);
   a.nlse = reinterpret_cast<float*>(ws);
   a.ndelta = reinterpret_cast<float*>(ws + back_row_bytes(total_q, num_qo_heads));
-  a.sink_part = reinterpret_cast<float*>(ws + 2 * back_row_bytes(total_q, num_qo_heads));
+  a.sink_count = reinterpret_cast<int*>(ws + 2 * back_row_bytes(total_q, num_qo_heads));
+  a.sink_part = reinterpret_cast<float*>(ws + 2 * back_row_bytes(total_q, num_qo_heads) + 256);
   return launch_prefill_back(a, s);
 }
 

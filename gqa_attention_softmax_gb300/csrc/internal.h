@@ -219,12 +219,13 @@ struct BackArgs {
   float* dsinks;                        // nullptr where sinks is
   // workspace
   float *nlse, *ndelta;                 // [total_q, Hq]
-  float* sink_part;                     // [back_blocks(), Hq]
+  float* sink_part;                     // [back_sink_blocks(), Hq]
+  int* sink_count;
 };
-// Rows of sink_part: blocks of query tokens of the pass that computes delta.
-int back_block_tokens(int32_t Hq);
-inline int64_t back_blocks(int32_t total_q, int32_t Hq) {
-  const int64_t per = back_block_tokens(Hq);
+// Query tokens of a block that sums the sinks' gradients (8192 rows, or a token), and these blocks.
+inline int back_sink_tokens(int32_t Hq) { return Hq < 8192 ? 8192 / Hq : 1; }
+inline int64_t back_sink_blocks(int32_t total_q, int32_t Hq) {
+  const int64_t per = back_sink_tokens(Hq);
   return (total_q + per - 1) / per;
 }
 int launch_prefill_back(const BackArgs& a, cudaStream_t stream);

@@ -3,10 +3,10 @@
 // the visible keys and delta = dout . out - dlse, dS = P (dout v^T - delta):
 // dq = c dS k, dk = c dS^T q, dv = P^T dout, dsink = -sum exp(s - lse) delta.
 //
-// Three passes. back_delta_kernel: delta and the sinks' gradients, one read of
-// dout and out. back_dkv_kernel: one CTA holds 128 keys of a KV head and walks
-// over the query rows that see them; back_dq_kernel: one CTA holds 128 query
-// rows (tokens x the heads of a group) and walks over the keys they see. P and
+// Two passes. back_dq_kernel: one CTA holds 128 query rows (tokens x the heads of a
+// group), computes their delta and walks over the keys they see;
+// back_dkv_kernel: one CTA holds 128 keys of a KV head and walks over the query
+// rows that see them; its last blocks sum the sinks' gradients. P and
 // dS are computed in both, seven products a tile pair instead of five: no sum
 // crosses CTAs, so there are no atomics (whose order would change the results),
 // no fp32 buffer of dq in memory, and the group's heads add up in the
@@ -45,9 +45,9 @@ struct BackParams {
   int causal, window;
   __nv_bfloat16 *dq, *dk, *dv;
   float *dsinks, *nlse, *ndelta, *sink_part;   // (workspace: [total_q, Hq] -lse log2 e, -delta)
-  int per;       // tokens of a block of the delta pass
-  int delta_blocks, sink_blocks;
-  int dq_waits;  // there is no pass of dk and dv between the delta pass and that of dq
+  int* sink_count;                   // (workspace) blocks that have left their sums
+  int sink_tokens, sink_blocks;      // tokens of a block that sums the sinks' gradients, these blocks
+  int dkv_items;
   int QB, nqb;   // query tokens of a tile of 128 rows, tiles of the longest sequence
   int GT, chunks, QB2;   // heads and tokens of a tile of the dk, dv pass, tiles of a token
 };
@@ -62,88 +62,55 @@ __device__ __forceinline__ float dot8(uint4 x, uint4 y, float s) {
   return s;
 }
 
-constexpr int kDeltaRows = 256;    // rows (token, head) of a block of the delta pass at most
-constexpr int kDeltaHeads = 256;   // heads of a block
-
-// -delta and -lse log2 e of p.per tokens and up to kDeltaHeads heads, d / 8 threads a
-// row, and those rows' sum of the sinks' gradients, in the order of the tokens.
-template <int D>
-__global__ void __launch_bounds__(256) back_delta_kernel(const BackParams p) {
-  constexpr int C = D / 8;
-  constexpr int kIlp = 4;   // rows of a thread in flight
-  __shared__ float term[kDeltaRows];
-  grid_launch_dependents();
-  const int h0 = blockIdx.y * kDeltaHeads;
-  const int nh = min(kDeltaHeads, p.Hq - h0);
-  const int t0 = blockIdx.x * p.per;
-  const int total = p.sinks ? p.cu_q[p.batch] : 0;   // (rows behind it have no gradient)
-  const int nt = min(p.per, p.total_q - t0);
-  const int rows = nt * nh;
-  const int c = threadIdx.x % C;
-  const float per_head = 1.f / nh;   // (r + 1/2) / nh is off by less than 1 / (2 nh): rows < 2^9, nh <= 2^8
-  for (int base = 0; base < rows; base += kIlp * 256 / C) {
-    float s[kIlp], lse[kIlp], dlse[kIlp], sink[kIlp];
-    long long at[kIlp];
-    int tok[kIlp];
-    uint4 x[kIlp], y[kIlp];
-#pragma unroll
-    for (int i = 0; i < kIlp; ++i) {
-      const int r = base + i * (256 / C) + threadIdx.x / C;
-      x[i] = y[i] = make_uint4(0, 0, 0, 0);
-      if (r < rows) {
-        tok[i] = t0 + __float2int_rz((r + 0.5f) * per_head);
-        const int h = h0 + r - (tok[i] - t0) * nh;
-        at[i] = static_cast<long long>(tok[i]) * p.Hq + h;
-        x[i] = __ldg(reinterpret_cast<const uint4*>(p.dout + at[i] * D) + c);
-        y[i] = __ldcs(reinterpret_cast<const uint4*>(p.out + at[i] * D) + c);
-        if (c == 0) {
-          lse[i] = p.lse[at[i]];
-          dlse[i] = p.dlse ? p.dlse[at[i]] : 0.f;
-          sink[i] = p.sinks ? p.sinks[h] : 0.f;
-        }
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kIlp; ++i) {
-      const int r = base + i * (256 / C) + threadIdx.x / C;
-      s[i] = dot8(x[i], y[i], 0.f);
-#pragma unroll
-      for (int m = 1; m < C; m <<= 1) s[i] += __shfl_xor_sync(0xffffffffu, s[i], m);
-      if (r < rows && c == 0) {
-        const float delta = s[i] - dlse[i];
-        p.ndelta[at[i]] = -delta;
-        // a row with lse -inf has no weights (P = 0, as for lse +inf, which exponentials give)
-        p.nlse[at[i]] = lse[i] == kNegInf ? kNegInf : -lse[i] * kLog2e;
-        if (p.sinks) term[r] = tok[i] < total && lse[i] != kNegInf ? -expf(sink[i] - lse[i]) * delta : 0.f;
-      }
-    }
-  }
-  if (!p.sinks) return;
-  __syncthreads();
-  if (threadIdx.x < nh) {
-    float s = 0.f;
-    for (int t = 0; t < nt; ++t) s += term[t * nh + threadIdx.x];
-    p.sink_part[static_cast<long long>(blockIdx.x) * p.Hq + h0 + threadIdx.x] = s;
-  }
-}
-
-// dsinks of 32 heads: the blocks' sums added in a fixed order, by all threads
-// of a block (s: shared memory, 32 words a warp). These are the first blocks of the pass that computes dq.
+// dsinks_h = sum over the rows of e^{s_h - lse} (-delta), of p.sink_tokens tokens a block, by all threads
+// of it (s: shared memory, 32 words a warp and one more). Each block leaves its
+// sums in p.sink_part; the one that comes last, whichever it is, adds them up in their order.
 template <int kThreads>
-__device__ __forceinline__ void reduce_sinks(const BackParams& p, int chunk, float (*s)[32]) {
+__device__ __forceinline__ void sum_sinks(const BackParams& p, int blk, float (*s)[32]) {
   constexpr int kSlices = kThreads / 32;
-  const int h = chunk * 32 + threadIdx.x % 32, slice = threadIdx.x / 32;
-  float x = 0.f;
-  if (h < p.Hq) {
-#pragma unroll 8
-    for (int b = slice; b < p.delta_blocks; b += kSlices)
-      x += __ldcg(&p.sink_part[static_cast<long long>(b) * p.Hq + h]);
+  const int lane = threadIdx.x % 32, slice = threadIdx.x / 32;
+  int* last = reinterpret_cast<int*>(s + kSlices);
+  // (rows outside the sequences have no gradient)
+  const int t0 = max(blk * p.sink_tokens, p.cu_q[0]);
+  const int end = max(0, min(p.total_q, p.cu_q[p.batch]));
+  const int t1 = min(end - blk * p.sink_tokens, p.sink_tokens) + blk * p.sink_tokens;
+  auto reduce = [&](int h, float x, float* to) {   // over the slices
+    s[slice][lane] = x;
+    __syncthreads();
+    if (slice == 0 && h < p.Hq) {
+      for (int j = 1; j < kSlices; ++j) x += s[j][lane];
+      to[h] = x;
+    }
+    __syncthreads();
+  };
+  for (int h = lane; h < p.Hq + lane; h += 32) {
+    float x = 0.f;
+    if (h < p.Hq) {
+      const float sink = p.sinks[h] * kLog2e;
+#pragma unroll 4
+      for (int t = t0 + slice; t < t1; t += kSlices) {
+        const long long at = static_cast<long long>(t) * p.Hq + h;
+        x = fmaf(exp2f(sink + __ldcg(&p.nlse[at])), __ldcg(&p.ndelta[at]), x);
+      }
+    }
+    reduce(h, x, p.sink_blocks == 1 ? p.dsinks : p.sink_part + static_cast<long long>(blk) * p.Hq);
   }
-  s[slice][threadIdx.x % 32] = x;
+  if (p.sink_blocks == 1) return;
+  __threadfence();
   __syncthreads();
-  if (slice != 0 || h >= p.Hq) return;
-  for (int j = 1; j < kSlices; ++j) x += s[j][threadIdx.x];
-  p.dsinks[h] = x;
+  if (threadIdx.x == 0) *last = atomicAdd(p.sink_count, 1) == p.sink_blocks - 1;
+  __syncthreads();
+  if (!*last) return;
+  __threadfence();
+  for (int h = lane; h < p.Hq + lane; h += 32) {
+    float x = 0.f;
+    if (h < p.Hq) {
+#pragma unroll 8
+      for (int b = slice; b < p.sink_blocks; b += kSlices)
+        x += __ldcg(&p.sink_part[static_cast<long long>(b) * p.Hq + h]);
+    }
+    reduce(h, x, p.dsinks);
+  }
 }
 
 struct Seq {
@@ -361,6 +328,11 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
+  if (static_cast<int>(blockIdx.x) >= p.dkv_items) {   // (the last blocks: they fill the SMs that the others leave)
+    grid_dependency_wait();
+    sum_sinks<C::THREADS>(p, blockIdx.x - p.dkv_items, reinterpret_cast<float(*)[32]>(smem));
+    return;
+  }
   // items: the first key tiles (which the most queries see) of all sequences and KV heads first
   const int per = p.Hkv * p.batch;
   const int kt = static_cast<int>(blockIdx.x) / per;
@@ -370,7 +342,7 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
   if (!s.ok && threadIdx.x == 0) atomicExch(status, SINKATTN_BAD_LENGTHS);
   const int k0 = kt * 128;
   if (!s.ok || k0 >= s.lk) {   // uniform over the CTA, before any barrier or TMEM use
-    grid_dependency_wait();    // (the next launch takes it that the one before this is done)
+    grid_dependency_wait();    // (this launch ends after the one before)
     return;
   }
   const int nk = min(128, s.lk - k0);
@@ -491,11 +463,9 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
       load(&tmDo, y, smem + C::OFF_DO + y % ND * C::Q_TILE, &do_full[y % ND]);
     };
     // The first tiles' copies need nothing of the launch before this one, the rows do.
-    // The next launch's blocks may take the SMs that this one leaves.
     for (int x = 0; x < min(NQ, n); ++x) load_q(x);
     for (int y = 0; y < min(ND, n); ++y) load_do(y);
     grid_dependency_wait();
-    grid_launch_dependents();
     // Q of tile x, and the tiles whose dO and rows take the places of the same tile x - NQ
     for (int x = 0; x < n + NQ - NR; ++x) {
       if (x >= NQ && !wwait(&q_empty[x % NQ], (x / NQ - 1) & 1)) break;
@@ -694,7 +664,8 @@ struct DqCfg {
   static constexpr int OFF_V = OFF_K + NK * K_TILE;
   static constexpr int OFF_BAR = OFF_V + NV * K_TILE;
   static constexpr int N_BARS = 1 + 2 * NK + 2 * NV + 3 * NSB + 2 + NDP + 1 + 3;
-  static constexpr int SMEM = 1024 + OFF_BAR + N_BARS * 8 + 16;
+  static constexpr int OFF_ROW = OFF_BAR + N_BARS * 8 + 16;   // [128] (-lse log2 e, -delta)
+  static constexpr int SMEM = 1024 + OFF_ROW + 128 * 8;
   static constexpr uint32_t COLS = 512 / CTAS;
   static constexpr uint32_t COL_S = 0;
   static constexpr uint32_t COL_DP = NSB * KT;
@@ -710,10 +681,6 @@ __device__ __forceinline__ void back_dq_block(const CUtensorMap& tmQ, const CUte
   using C = DqCfg<D>;
   constexpr int NK = C::NK, NV = C::NV, NSB = C::NSB, NDP = C::NDP, NG = C::NG, NSUB = C::NSUB, KT = C::KT;
   extern __shared__ uint8_t smem_raw[];
-  if (static_cast<int>(blockIdx.x) < p.sink_blocks) {
-    reduce_sinks<C::THREADS>(p, blockIdx.x, reinterpret_cast<float(*)[32]>(smem_raw));
-    return;
-  }
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
@@ -736,7 +703,7 @@ __device__ __forceinline__ void back_dq_block(const CUtensorMap& tmQ, const CUte
   const int lane = threadIdx.x & 31;
 
   // items: the last query blocks (which see the most keys) first
-  const int item = static_cast<int>(blockIdx.x) - p.sink_blocks;
+  const int item = static_cast<int>(blockIdx.x);
   const int per = p.Hkv * p.batch;
   const int qb = p.nqb - 1 - item / per;
   const int kvh = item % per % p.Hkv;
@@ -902,11 +869,48 @@ __device__ __forceinline__ void back_dq_block(const CUtensorMap& tmQ, const CUte
     // keys [lo_r, hi_r) are visible to the row
     const int hi_r = valid ? (p.causal ? pos + 1 : s.lk) : 0;
     const int lo_r = p.window > 0 ? max(0, pos - p.window + 1) : 0;
-    float nlse = kNegInf, ndel = 0.f;
-    if (valid) {
-      nlse = __ldcg(&p.nlse[at]);
-      ndel = __ldcg(&p.ndelta[at]);
+    // -lse log2 e and -delta of the tile's rows, D / 8 threads a row, all of a thread's
+    // loads at once, while the first tiles are on their way: for this pass and, through
+    // the workspace, for that of dk and dv.
+    float2* const rows = reinterpret_cast<float2*>(smem + C::OFF_ROW);
+    {
+      constexpr int DC = D / 8, R = 32 / DC, N = 128 / (NG * C::GROUP / 32 * R);
+      const int c = lane % DC, r0 = (warp - C::SOFT0) * N * R + lane / DC;
+      uint4 x[N], y[N];
+      float lse[N], dlse[N];
+      long long where[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int r = r0 + i * R, t = r / G;
+        x[i] = y[i] = make_uint4(0, 0, 0, 0);
+        lse[i] = dlse[i] = 0.f;
+        where[i] = -1;
+        if (t >= nt || r >= G * p.QB) continue;
+        where[i] = static_cast<long long>(s.q0 + t0 + t) * p.Hq + kvh * G + (r - t * G);
+        x[i] = __ldg(reinterpret_cast<const uint4*>(p.dout + where[i] * D) + c);
+        y[i] = __ldcs(reinterpret_cast<const uint4*>(p.out + where[i] * D) + c);
+        if (c != 0) continue;
+        lse[i] = p.lse[where[i]];
+        if (p.dlse) dlse[i] = p.dlse[where[i]];
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        float sum = dot8(x[i], y[i], 0.f);
+#pragma unroll
+        for (int m = 1; m < DC; m <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+        if (c != 0) continue;
+        // a row with lse -inf has no weights (P = 0, as for lse +inf, which exponentials give)
+        const float nl = where[i] < 0 || lse[i] == kNegInf ? kNegInf : -lse[i] * kLog2e;
+        const float nd = dlse[i] - sum;
+        rows[r0 + i * R] = make_float2(nl, nd);
+        if (where[i] >= 0) {
+          p.nlse[where[i]] = nl;
+          p.ndelta[where[i]] = nd;
+        }
+      }
+      asm volatile("bar.sync 1, %0;" ::"n"(NG * C::GROUP) : "memory");   // (all the warps of P and dS)
     }
+    const float nlse = rows[row].x, ndel = rows[row].y;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const uint32_t dp_addr = lane_base + C::COL_DP + KT * grp + cols;
     const float2 cc = make_float2(p.scale_log2, p.scale_log2);
@@ -981,18 +985,16 @@ __device__ __forceinline__ void back_dq_block(const CUtensorMap& tmQ, const CUte
   }
 }
 
-// This launch needs nothing of the one before it (the pass of dk and dv, which
-// has waited for the pass before that): its blocks start where those leave
-// room. What the delta pass wrote is loaded around L1. The first block ends
-// after that launch, so that whoever waits for this one has waited for both.
+// The first launch of a call: the blocks of dk and dv may come as these leave
+// their SMs, and wait for the rows' numbers where they need them.
 template <int D>
 __global__ void __launch_bounds__(DqCfg<D>::THREADS, DqCfg<D>::CTAS)
     back_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmDo,
                    const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                    const BackParams p) {
-  if (p.dq_waits) grid_dependency_wait();
+  grid_launch_dependents();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.sink_count = 0;
   back_dq_block<D>(tmQ, tmDo, tmK, tmV, p);
-  if (blockIdx.x == 0) grid_dependency_wait();
 }
 
 int launched(const char* what, cudaError_t e) {
@@ -1014,9 +1016,9 @@ int launch_back(BackParams& p, cudaStream_t stream) {
   // every size is checked, and every map made, before the first launch
   const int64_t per = static_cast<int64_t>(p.Hkv) * p.batch;
   const int64_t dkv_items = (static_cast<int64_t>(p.max_kv) + 127) / 128 * per;
-  p.sink_blocks = p.dsinks ? (p.Hq + 31) / 32 : 0;
-  const int64_t dq_items = p.nqb * per + p.sink_blocks;
-  if (std::max(dkv_items, dq_items) >= (int64_t{1} << 31)) {
+  const int64_t dq_items = p.total_q > 0 ? p.nqb * per : 0;
+  p.sink_blocks = p.dsinks ? (dq_items ? static_cast<int>(back_sink_blocks(p.total_q, p.Hq)) : 1) : 0;
+  if (std::max(dkv_items + p.sink_blocks, dq_items) >= (int64_t{1} << 31)) {
     set_error("too many work items");
     return SINKATTN_UNSUPPORTED;
   }
@@ -1035,38 +1037,25 @@ int launch_back(BackParams& p, cudaStream_t stream) {
       (rc = make_rows_tmap(&tmV, p.v, kv_rows, D, DQ::KT, 128)) ||
       (rc = make_rows_tmap(&tmK2, p.k, kv_rows, D, 128, 128)) ||
       (rc = make_rows_tmap(&tmV2, p.v, kv_rows, D, 128, 128)) ||
-      (rc = set_smem(set_chained_smem(back_delta_kernel<D>, 0))) ||
       (rc = set_smem(set_chained_smem(back_dkv_kernel<D>, KV::SMEM))) ||
       (rc = set_smem(set_chained_smem(back_dq_kernel<D>, DQ::SMEM))))
     return rc;
-  if (p.delta_blocks > 0) {
-    back_delta_kernel<D><<<dim3(static_cast<unsigned>(p.delta_blocks),
-                                static_cast<unsigned>((p.Hq + kDeltaHeads - 1) / kDeltaHeads)),
-                           256, 0, stream>>>(p);
-    if ((rc = launched("delta", cudaGetLastError()))) return rc;
+  if (dq_items > 0) {
+    back_dq_kernel<D><<<static_cast<unsigned>(dq_items), DQ::THREADS, DQ::SMEM, stream>>>(tmQ, tmDo, tmK, tmV, p);
+    if ((rc = launched("dq", cudaGetLastError()))) return rc;
   }
-  if (dkv_items > 0) {
-    const dim3 grid(static_cast<unsigned>(dkv_items));
-    cudaError_t e;
-    if (p.delta_blocks > 0) {
-      e = launch_chained(back_dkv_kernel<D>, grid, KV::THREADS, KV::SMEM, stream, tmQ2, tmDo2, tmK2, tmV2, p);
-    } else {   // the first launch of the call reads its inputs at once
-      back_dkv_kernel<D><<<grid, KV::THREADS, KV::SMEM, stream>>>(tmQ2, tmDo2, tmK2, tmV2, p);
-      e = cudaGetLastError();
-    }
-    if ((rc = launched("dk, dv", e))) return rc;
-  }
-  p.dq_waits = dkv_items == 0;
-  if (dq_items == 0) return SINKATTN_OK;
-  return launched("dq", launch_chained(back_dq_kernel<D>, dim3(static_cast<unsigned>(dq_items)), DQ::THREADS,
-                                       DQ::SMEM, stream, tmQ, tmDo, tmK, tmV, p));
+  p.dkv_items = static_cast<int>(dkv_items);
+  const dim3 grid(static_cast<unsigned>(dkv_items + p.sink_blocks));
+  if (grid.x == 0) return SINKATTN_OK;
+  if (dq_items > 0)
+    return launched("dk, dv", launch_chained(back_dkv_kernel<D>, grid, KV::THREADS, KV::SMEM, stream, tmQ2,
+                                             tmDo2, tmK2, tmV2, p));
+  // the first launch of the call reads its inputs at once
+  back_dkv_kernel<D><<<grid, KV::THREADS, KV::SMEM, stream>>>(tmQ2, tmDo2, tmK2, tmV2, p);
+  return launched("dk, dv", cudaGetLastError());
 }
 
 }  // namespace
-
-int back_block_tokens(int32_t Hq) {
-  return std::max(1, kDeltaRows / std::min<int32_t>(Hq, kDeltaHeads));
-}
 
 int launch_prefill_back(const BackArgs& a, cudaStream_t stream) {
   BackParams p{};
@@ -1093,8 +1082,8 @@ int launch_prefill_back(const BackArgs& a, cudaStream_t stream) {
   p.dk = static_cast<__nv_bfloat16*>(a.dk);
   p.dv = static_cast<__nv_bfloat16*>(a.dv);
   p.dsinks = a.dsinks; p.nlse = a.nlse; p.ndelta = a.ndelta; p.sink_part = a.sink_part;
-  p.per = back_block_tokens(a.Hq);
-  p.delta_blocks = static_cast<int>(back_blocks(a.total_q, a.Hq));
+  p.sink_count = a.sink_count;
+  p.sink_tokens = back_sink_tokens(a.Hq);
   return a.d == 64 ? launch_back<64>(p, stream) : launch_back<128>(p, stream);
 }
 
