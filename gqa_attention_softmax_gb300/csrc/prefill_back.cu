@@ -49,6 +49,7 @@ struct BackParams {
   int sink_tokens, sink_blocks;      // tokens of a block that sums the sinks' gradients, these blocks
   int dkv_items;
   int QB, nqb;   // query tokens of a tile of 128 rows, tiles of the longest sequence
+  int run, nrun; // tiles of a CTA of the pass of dq, CTAs of the longest sequence
   int GT, chunks, QB2;   // heads and tokens of a tile of the dk, dv pass, tiles of a token
 };
 
@@ -663,9 +664,9 @@ struct DqCfg {
   static constexpr int OFF_K = 2 * Q_TILE;
   static constexpr int OFF_V = OFF_K + NK * K_TILE;
   static constexpr int OFF_BAR = OFF_V + NV * K_TILE;
-  static constexpr int N_BARS = 1 + 2 * NK + 2 * NV + 3 * NSB + 2 + NDP + 1 + 3;
-  static constexpr int OFF_ROW = OFF_BAR + N_BARS * 8 + 16;   // [128] (-lse log2 e, -delta)
-  static constexpr int SMEM = 1024 + OFF_ROW + 128 * 8;
+  static constexpr int N_BARS = 2 + 2 * NK + 2 * NV + 3 * NSB + 2 + NDP + 2 + 2 + 3;
+  static constexpr int OFF_ROW = OFF_BAR + N_BARS * 8 + 16;   // [2][128] (-lse log2 e, -delta)
+  static constexpr int SMEM = OFF_ROW + 2 * 128 * 8;
   static constexpr uint32_t COLS = 512 / CTAS;
   static constexpr uint32_t COL_S = 0;
   static constexpr uint32_t COL_DP = NSB * KT;
@@ -680,12 +681,11 @@ __device__ __forceinline__ void back_dq_block(const CUtensorMap& tmQ, const CUte
                                               const BackParams& p) {
   using C = DqCfg<D>;
   constexpr int NK = C::NK, NV = C::NV, NSB = C::NSB, NDP = C::NDP, NG = C::NG, NSUB = C::NSUB, KT = C::KT;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];   // (swizzled tiles start on 1024 bytes)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* q_full = bars;
-  uint64_t* k_full = q_full + 1;       // [NK]
+  uint64_t* q_empty = q_full + 1;      // S and dP of the query tile done
+  uint64_t* k_full = q_empty + 1;      // [NK]
   uint64_t* k_empty = k_full + NK;     // [NK] dQ, the last that reads the stage, done
   uint64_t* v_full = k_empty + NK;     // [NV]
   uint64_t* v_empty = v_full + NV;     // [NV] dP done
@@ -694,36 +694,48 @@ __device__ __forceinline__ void back_dq_block(const CUtensorMap& tmQ, const CUte
   uint64_t* ds_full = s_free + NSB;    // [NSB] dS written (the group's arrivals)
   uint64_t* dp_full = ds_full + NSB;   // [2] of even and odd tiles: dP written
   uint64_t* dp_free = dp_full + 2;     // [NDP] dP read (the group's arrivals)
-  uint64_t* all_done = dp_free + NDP;  // dQ
-  uint64_t* drain = all_done + 1;      // [3]
+  uint64_t* dq_full = dp_free + NDP;   // a query tile's dQ done
+  uint64_t* dq_free = dq_full + 1;     // and read
+  uint64_t* row_full = dq_free + 1;    // [2] the rows' numbers there (all arrive)
+  uint64_t* drain = row_full + 2;      // [3]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 3);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
   int* status = &g_status_prefill_back;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
-  // items: the last query blocks (which see the most keys) first
-  const int item = static_cast<int>(blockIdx.x);
+  // A CTA's query tiles: m of them, the highest first, at the end of the first
+  // grid rows, where they see the most keys.
   const int per = p.Hkv * p.batch;
-  const int qb = p.nqb - 1 - item / per;
-  const int kvh = item % per % p.Hkv;
-  const int b = item % per / p.Hkv;
+  const int run = p.nrun - 1 - static_cast<int>(blockIdx.x) / per;
+  const int kvh = static_cast<int>(blockIdx.x) % per % p.Hkv;
+  const int b = static_cast<int>(blockIdx.x) % per / p.Hkv;
   const Seq s = load_seq(p, b);
   if (!s.ok) {
     if (threadIdx.x == 0) atomicExch(status, SINKATTN_BAD_LENGTHS);
     return;
   }
-  const int t0 = qb * p.QB;
-  if (t0 >= s.lq) return;   // uniform over the CTA, before any barrier or TMEM use
-  const int nt = min(p.QB, s.lq - t0);
-  const int pos0 = s.lk - s.lq + t0;
-  const int k_hi = p.causal ? pos0 + nt : s.lk;                 // keys [k_lo, k_hi) are seen by some row
-  const int k_lo = p.window > 0 ? max(0, pos0 - p.window + 1) : 0;
-  const int n = (k_hi - k_lo + KT - 1) / KT;                    // at least 1
+  const int end = min((run + 1) * p.run, (s.lq + p.QB - 1) / p.QB);
+  const int m = end - run * p.run;
+  if (m <= 0) return;   // uniform over the CTA, before any barrier or TMEM use
   const int G = p.G;
+  struct Tile {
+    int t0, nt, pos0;   // its queries, the first one's position
+    int k_lo, n;        // tiles of the keys [k_lo ...) that some row sees (at least 1)
+  };
+  auto tile = [&](int i) {
+    Tile x;
+    x.t0 = (end - 1 - i) * p.QB;
+    x.nt = min(p.QB, s.lq - x.t0);
+    x.pos0 = s.lk - s.lq + x.t0;
+    x.k_lo = p.window > 0 ? max(0, x.pos0 - p.window + 1) : 0;
+    x.n = ((p.causal ? x.pos0 + x.nt : s.lk) - x.k_lo + KT - 1) / KT;
+    return x;
+  };
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
+    mbar_init(q_empty, 2);
     for (int i = 0; i < NK; ++i) {
       mbar_init(&k_full[i], 1);
       mbar_init(&k_empty[i], 1);
@@ -739,7 +751,9 @@ __device__ __forceinline__ void back_dq_block(const CUtensorMap& tmQ, const CUte
     }
     for (int i = 0; i < 2; ++i) mbar_init(&dp_full[i], 1);
     for (int i = 0; i < NDP; ++i) mbar_init(&dp_free[i], C::GROUP);
-    mbar_init(all_done, 1);
+    mbar_init(dq_full, 1);
+    mbar_init(dq_free, NSUB * 128);
+    for (int i = 0; i < 2; ++i) mbar_init(&row_full[i], NG * C::GROUP);
     for (int i = 0; i < 3; ++i) mbar_init(&drain[i], 1);
     *abort_flag = 0;
     fence_barrier_init();
@@ -752,7 +766,7 @@ __device__ __forceinline__ void back_dq_block(const CUtensorMap& tmQ, const CUte
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  int issued_k = 0, issued_v = 0;   // tiles whose copies were issued (or left out by the test hook)
+  int issued_q = 0, issued_k = 0, issued_v = 0;   // tiles whose copies were issued (or left out by the test hook)
   auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
     return warp_wait(bar, parity, abort_flag, status);
   };
@@ -772,62 +786,79 @@ __device__ __forceinline__ void back_dq_block(const CUtensorMap& tmQ, const CUte
   if (warp == 0) {
     // ---------------------------------------------------------------- copies
     const uint64_t policy = policy_evict_last();   // K and V are re-read by every query block
-    const int slab = p.Hkv * s.k0 + kvh * s.lk + k_lo;
     const int skip_tile = hook_skip_tile();
-    auto load = [&](const CUtensorMap* map, int j, uint8_t* to, uint64_t* bar) {   // into a free stage
+    auto load = [&](const CUtensorMap* map, int j, int row, uint8_t* to, uint64_t* bar) {   // into a free stage
       if (j != skip_tile && leader) {   // test hook: the waits for this tile run out
         mbar_arrive_expect_tx(bar, C::K_TILE);
 #pragma unroll
         for (int sub = 0; sub < NSUB; ++sub)
-          tma_load_2d_hint(to + sub * C::KSUB, map, sub * 64, slab + j * KT, bar, policy);
+          tma_load_2d_hint(to + sub * C::KSUB, map, sub * 64, row, bar, policy);
       }
       __syncwarp();
     };
-    if (leader) {
-      // (rows that no copy writes are lanes whose results are not stored)
-      mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(2 * NSUB * 128 * G * p.QB));
+    bool ok = true;
+    for (int i = 0, g = 0; i < m && ok; ++i) {   // g: tiles of keys before
+      const Tile t = tile(i);
+      const int slab = p.Hkv * s.k0 + kvh * s.lk + t.k_lo;
+      if (i > 0 && !wwait(q_empty, (i - 1) & 1)) break;
+      issued_q = i + 1;
+      if (leader) {
+        // (rows that no copy writes are lanes whose results are not stored)
+        mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(2 * NSUB * 128 * G * p.QB));
 #pragma unroll
-      for (int sub = 0; sub < NSUB; ++sub) {
-        tc::tma_load_3d(smem + C::OFF_Q + sub * C::QSUB, &tmQ, sub * 64, kvh * G, s.q0 + t0, q_full);
-        tc::tma_load_3d(smem + C::OFF_DO + sub * C::QSUB, &tmDo, sub * 64, kvh * G, s.q0 + t0, q_full);
+        for (int sub = 0; sub < NSUB; ++sub) {
+          tc::tma_load_3d(smem + C::OFF_Q + sub * C::QSUB, &tmQ, sub * 64, kvh * G, s.q0 + t.t0, q_full);
+          tc::tma_load_3d(smem + C::OFF_DO + sub * C::QSUB, &tmDo, sub * 64, kvh * G, s.q0 + t.t0, q_full);
+        }
       }
-    }
-    __syncwarp();
-    for (int x = 0; x < n + NK - NV; ++x) {
-      if (x < n) {
-        if (x >= NK && !wwait(&k_empty[x % NK], (x / NK - 1) & 1)) break;
-        issued_k = x + 1;
-        load(&tmK, x, smem + C::OFF_K + x % NK * C::K_TILE, &k_full[x % NK]);
+      __syncwarp();
+      for (int x = g; x < g + t.n + NK - NV; ++x) {
+        if (x < g + t.n) {
+          if (x >= NK && !(ok = wwait(&k_empty[x % NK], (x / NK - 1) & 1))) break;
+          issued_k = x + 1;
+          load(&tmK, x, slab + (x - g) * KT, smem + C::OFF_K + x % NK * C::K_TILE, &k_full[x % NK]);
+        }
+        const int y = x - (NK - NV);   // V lags by the stages that K has more
+        if (y < g) continue;
+        if (y >= NV && !(ok = wwait(&v_empty[y % NV], (y / NV - 1) & 1))) break;
+        issued_v = y + 1;
+        load(&tmV, y, slab + (y - g) * KT, smem + C::OFF_V + y % NV * C::K_TILE, &v_full[y % NV]);
       }
-      const int y = x - (NK - NV);   // V lags by the stages that K has more
-      if (y < 0) continue;
-      if (y >= NV && !wwait(&v_empty[y % NV], (y / NV - 1) & 1)) break;
-      issued_v = y + 1;
-      load(&tmV, y, smem + C::OFF_V + y % NV * C::K_TILE, &v_full[y % NV]);
+      g += t.n;
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- S = Q K^T
     const uint64_t qd = tc::smem_desc_sw128(smem_u32(smem + C::OFF_Q), 16, 1024);
     const uint64_t kd = tc::smem_desc_sw128(smem_u32(smem + C::OFF_K), 16, 1024);
-    if (wwait(q_full, 0)) {
-      for (int j = 0; j < n; ++j) {
-        if (j < NSB ? !wwait(&k_full[j % NK], j / NK & 1)
-                    : !wwait2(&s_free[j % NSB], (j / NSB - 1) & 1, &k_full[j % NK], j / NK & 1)) break;
+    bool ok = true;
+    for (int i = 0, j = 0; i < m && ok; ++i) {
+      const int end_j = j + tile(i).n;
+      if (!wwait(q_full, i & 1)) break;
+      for (; j < end_j; ++j) {
+        ok = j < NSB ? wwait(&k_full[j % NK], j / NK & 1)
+                     : wwait2(&s_free[j % NSB], (j / NSB - 1) & 1, &k_full[j % NK], j / NK & 1);
+        if (!ok) break;
         tc::fence_after_sync();
         issue_ss<D, KT>(leader, tmem + C::COL_S + KT * (j % NSB), qd, kd + j % NK * tile16, C::QSUB, C::KSUB);
         if (leader) tc::commit(&s_full[j % NSB]);
         __syncwarp();
       }
+      if (leader) tc::commit(q_empty);
+      __syncwarp();
     }
     finish(&drain[0]);
   } else if (warp == 2) {
     // ---------------------------------------------------------------- dP = dO V^T
     const uint64_t dod = tc::smem_desc_sw128(smem_u32(smem + C::OFF_DO), 16, 1024);
     const uint64_t vd = tc::smem_desc_sw128(smem_u32(smem + C::OFF_V), 16, 1024);
-    if (wwait(q_full, 0)) {
-      for (int j = 0; j < n; ++j) {
-        if (j < NDP ? !wwait(&v_full[j % NV], 0)
-                    : !wwait2(&dp_free[j % NDP], (j / NDP - 1) & 1, &v_full[j % NV], j / NV & 1)) break;
+    bool ok = true;
+    for (int i = 0, j = 0; i < m && ok; ++i) {
+      const int end_j = j + tile(i).n;
+      if (!wwait(q_full, i & 1)) break;
+      for (; j < end_j; ++j) {
+        ok = j < NDP ? wwait(&v_full[j % NV], 0)
+                     : wwait2(&dp_free[j % NDP], (j / NDP - 1) & 1, &v_full[j % NV], j / NV & 1);
+        if (!ok) break;
         tc::fence_after_sync();
         issue_ss<D, KT>(leader, tmem + C::COL_DP + KT * (j % NDP), dod, vd + j % NV * tile16, C::QSUB, C::KSUB);
         if (leader) {
@@ -836,23 +867,31 @@ __device__ __forceinline__ void back_dq_block(const CUtensorMap& tmQ, const CUte
         }
         __syncwarp();
       }
+      if (leader) tc::commit(q_empty);
+      __syncwarp();
     }
     finish(&drain[1]);
   } else if (warp == 3) {
     // ---------------------------------------------------------------- dQ += dS K
     const uint64_t kt = tc::smem_desc_sw128(smem_u32(smem + C::OFF_K), C::KSUB, 1024);   // MN-major
-    for (int j = 0; j < n; ++j) {
-      if (!wwait(&ds_full[j % NSB], j / NSB & 1)) break;
-      tc::fence_after_sync();
-      issue_ts<D, KT / 16>(leader, tmem + C::COL_DQ, tmem + C::COL_S + KT * (j % NSB), kt + j % NK * tile16,
-                           j == 0);
-      if (leader) {
-        tc::commit(&s_free[j % NSB]);
-        tc::commit(&k_empty[j % NK]);
+    bool ok = true;
+    for (int i = 0, j = 0; i < m && ok; ++i) {
+      const int first = j, end_j = j + tile(i).n;
+      if (i > 0 && !wwait(dq_free, (i - 1) & 1)) break;
+      for (; j < end_j; ++j) {
+        if (!(ok = wwait(&ds_full[j % NSB], j / NSB & 1))) break;
+        tc::fence_after_sync();
+        issue_ts<D, KT / 16>(leader, tmem + C::COL_DQ, tmem + C::COL_S + KT * (j % NSB), kt + j % NK * tile16,
+                             j == first);
+        if (leader) {
+          tc::commit(&s_free[j % NSB]);
+          tc::commit(&k_empty[j % NK]);
+        }
+        __syncwarp();
       }
+      if (leader) tc::commit(dq_full);
       __syncwarp();
     }
-    if (leader) tc::commit(all_done);
     finish(&drain[2]);
   } else {
     // ---------------------------------------------------------------- P and dS
@@ -862,112 +901,125 @@ __device__ __forceinline__ void back_dq_block(const CUtensorMap& tmQ, const CUte
     const int quad = warp & 3;
     const int row = quad * 32 + lane;
     const int rt = row / G;
-    const bool valid = rt < nt && row < G * p.QB;
-    const int h = kvh * G + (row - rt * G);
-    const long long at = static_cast<long long>(s.q0 + t0 + rt) * p.Hq + h;
-    const int pos = pos0 + rt;
-    // keys [lo_r, hi_r) are visible to the row
-    const int hi_r = valid ? (p.causal ? pos + 1 : s.lk) : 0;
-    const int lo_r = p.window > 0 ? max(0, pos - p.window + 1) : 0;
-    // -lse log2 e and -delta of the tile's rows, D / 8 threads a row, all of a thread's
-    // loads at once, while the first tiles are on their way: for this pass and, through
-    // the workspace, for that of dk and dv.
     float2* const rows = reinterpret_cast<float2*>(smem + C::OFF_ROW);
-    {
+    // -lse log2 e and -delta of tile i's rows, D / 8 threads a row, all of a thread's
+    // loads at once: for this pass and, through the workspace, for that of dk and dv.
+    auto row_numbers = [&](int i) {
       constexpr int DC = D / 8, R = 32 / DC, N = 128 / (NG * C::GROUP / 32 * R);
       const int c = lane % DC, r0 = (warp - C::SOFT0) * N * R + lane / DC;
+      const Tile t = tile(i);
       uint4 x[N], y[N];
       float lse[N], dlse[N];
       long long where[N];
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int r = r0 + i * R, t = r / G;
-        x[i] = y[i] = make_uint4(0, 0, 0, 0);
-        lse[i] = dlse[i] = 0.f;
-        where[i] = -1;
-        if (t >= nt || r >= G * p.QB) continue;
-        where[i] = static_cast<long long>(s.q0 + t0 + t) * p.Hq + kvh * G + (r - t * G);
-        x[i] = __ldg(reinterpret_cast<const uint4*>(p.dout + where[i] * D) + c);
-        y[i] = __ldcs(reinterpret_cast<const uint4*>(p.out + where[i] * D) + c);
+      for (int e = 0; e < N; ++e) {
+        const int r = r0 + e * R, tok = r / G;
+        x[e] = y[e] = make_uint4(0, 0, 0, 0);
+        lse[e] = dlse[e] = 0.f;
+        where[e] = -1;
+        if (tok >= t.nt || r >= G * p.QB) continue;
+        where[e] = static_cast<long long>(s.q0 + t.t0 + tok) * p.Hq + kvh * G + (r - tok * G);
+        x[e] = __ldg(reinterpret_cast<const uint4*>(p.dout + where[e] * D) + c);
+        y[e] = __ldcs(reinterpret_cast<const uint4*>(p.out + where[e] * D) + c);
         if (c != 0) continue;
-        lse[i] = p.lse[where[i]];
-        if (p.dlse) dlse[i] = p.dlse[where[i]];
+        lse[e] = p.lse[where[e]];
+        if (p.dlse) dlse[e] = p.dlse[where[e]];
       }
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        float sum = dot8(x[i], y[i], 0.f);
+      for (int e = 0; e < N; ++e) {
+        float sum = dot8(x[e], y[e], 0.f);
 #pragma unroll
-        for (int m = 1; m < DC; m <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+        for (int k = 1; k < DC; k <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
         if (c != 0) continue;
         // a row with lse -inf has no weights (P = 0, as for lse +inf, which exponentials give)
-        const float nl = where[i] < 0 || lse[i] == kNegInf ? kNegInf : -lse[i] * kLog2e;
-        const float nd = dlse[i] - sum;
-        rows[r0 + i * R] = make_float2(nl, nd);
-        if (where[i] >= 0) {
-          p.nlse[where[i]] = nl;
-          p.ndelta[where[i]] = nd;
+        const float nl = where[e] < 0 || lse[e] == kNegInf ? kNegInf : -lse[e] * kLog2e;
+        const float nd = dlse[e] - sum;
+        rows[(i & 1) * 128 + r0 + e * R] = make_float2(nl, nd);
+        if (where[e] >= 0) {
+          p.nlse[where[e]] = nl;
+          p.ndelta[where[e]] = nd;
         }
       }
-      asm volatile("bar.sync 1, %0;" ::"n"(NG * C::GROUP) : "memory");   // (all the warps of P and dS)
-    }
-    const float nlse = rows[row].x, ndel = rows[row].y;
+      mbar_arrive(&row_full[i & 1]);
+    };
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const uint32_t dp_addr = lane_base + C::COL_DP + KT * grp + cols;
     const float2 cc = make_float2(p.scale_log2, p.scale_log2);
-    const float2 nl = make_float2(nlse, nlse), nd = make_float2(ndel, ndel);
-    // every row of the block sees every key of tiles [j_lo, j_hi) (rows that are not stored need no mask)
-    int j_lo = 0;
-    const int j_hi = ((p.causal ? min(s.lk, pos0 + 1) : s.lk) - k_lo) / KT;
-    if (p.window > 0) j_lo = max(0, (pos0 + nt - p.window - k_lo + KT - 1) / KT);
     bool ok = true;
-    for (int j = grp; j < n; j += NG) {
-      const bool masked = j < j_lo || j >= j_hi;
-      const int j0 = k_lo + j * KT;
-      const int lo = lo_r - j0 - cols, hi = hi_r - j0 - cols;
-      const uint32_t s_addr = lane_base + C::COL_S + KT * (j % NSB) + cols;
-      if (!wwait2(&s_full[j % NSB], j / NSB & 1, &dp_full[j & 1], j >> 1 & 1)) { ok = false; break; }
-      tc::fence_after_sync();
-      if (j0 + KT > s.lk) {
-        // The keys end inside the tile: the rows behind them are another head's or sequence's,
-        // whose NaN would pass through zero weights. (S(j), the other reader, is done.)
-        zero_rows<NSUB>(smem + C::OFF_K + j % NK * C::K_TILE, C::KSUB, s.lk - j0, KT, tid, C::GROUP);
-        tc::fence_proxy_async_smem();
-      }
-      float w[2][16];
-      tc::tmem_ld16(dp_addr, w[0]);
-      tc::tmem_ld16(dp_addr + 16, w[1]);
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float v[16];
-        tc::tmem_ld16(s_addr + 16 * c, v);
-        tc::tmem_wait_ld();
-        if (c == 0) {
+    for (int i = 0, g = 0;; ++i) {   // g: tiles of keys before
+      if (i < m && ok) row_numbers(i);
+      if (i > 0) {
+        // -------------------------------------------------------- epilogue of the tile before
+        if (ok) ok = wwait(dq_full, (i - 1) & 1);
+        tc::fence_after_sync();
+        const int blk = (warp - C::SOFT0) >> 2;   // four warps store 64 columns
+        if (blk < NSUB) {
+          const Tile t = tile(i - 1);
+          const long long at = static_cast<long long>(s.q0 + t.t0 + rt) * p.Hq + kvh * G + (row - rt * G);
+          tc::store_o_rows<64>(lane_base + C::COL_DQ + 64 * blk, !ok, p.sm_scale, p.dq + at * D + 64 * blk,
+                               rt < t.nt && row < G * p.QB, lane);
           tc::fence_before_sync();
-          mbar_arrive(&dp_free[grp]);   // a later tile's dP may come
+          mbar_arrive(dq_free);
         }
-#pragma unroll
-        for (int e = 0; e < 16; e += 2) {
-          weights2(v[e], v[e + 1], cc, nl);
-          scores2(w[c][e], w[c][e + 1], v[e], v[e + 1], nd);
-        }
-        if (masked) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (c * 16 + e < lo || c * 16 + e >= hi) w[c][e] = 0.f;
-        }
-        store_packed(s_addr + 16 * c, w[c]);
       }
-      tc::tmem_wait_st();
-      tc::fence_before_sync();
-      mbar_arrive(&ds_full[j % NSB]);
+      if (i == m || !ok) break;
+      const Tile t = tile(i);
+      const bool valid = rt < t.nt && row < G * p.QB;
+      const int pos = t.pos0 + rt;
+      // keys [lo_r, hi_r) are visible to the row
+      const int hi_r = valid ? (p.causal ? pos + 1 : s.lk) : 0;
+      const int lo_r = p.window > 0 ? max(0, pos - p.window + 1) : 0;
+      // every row of the block sees every key of tiles [j_lo, j_hi) (rows that are not stored need no mask)
+      int j_lo = g;
+      const int j_hi = g + ((p.causal ? min(s.lk, t.pos0 + 1) : s.lk) - t.k_lo) / KT;
+      if (p.window > 0) j_lo = g + max(0, (t.pos0 + t.nt - p.window - t.k_lo + KT - 1) / KT);
+      ok = wwait(&row_full[i & 1], i >> 1 & 1);
+      const float2 num = rows[(i & 1) * 128 + row];
+      const float2 nl = make_float2(num.x, num.x), nd = make_float2(num.y, num.y);
+      const int end_j = g + t.n;
+      for (int j = NG == 1 ? g : g + ((grp ^ g) & (NG - 1)); j < end_j && ok; j += NG) {
+        const bool masked = j < j_lo || j >= j_hi;
+        const int j0 = t.k_lo + (j - g) * KT;
+        const int lo = lo_r - j0 - cols, hi = hi_r - j0 - cols;
+        const uint32_t s_addr = lane_base + C::COL_S + KT * (j % NSB) + cols;
+        if (!(ok = wwait2(&s_full[j % NSB], j / NSB & 1, &dp_full[j & 1], j >> 1 & 1))) break;
+        tc::fence_after_sync();
+        if (j0 + KT > s.lk) {
+          // The keys end inside the tile: the rows behind them are another head's or sequence's,
+          // whose NaN would pass through zero weights. (S(j), the other reader, is done.)
+          zero_rows<NSUB>(smem + C::OFF_K + j % NK * C::K_TILE, C::KSUB, s.lk - j0, KT, tid, C::GROUP);
+          tc::fence_proxy_async_smem();
+        }
+        float w[2][16];
+        tc::tmem_ld16(dp_addr, w[0]);
+        tc::tmem_ld16(dp_addr + 16, w[1]);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float v[16];
+          tc::tmem_ld16(s_addr + 16 * c, v);
+          tc::tmem_wait_ld();
+          if (c == 0) {
+            tc::fence_before_sync();
+            mbar_arrive(&dp_free[grp]);   // a later tile's dP may come
+          }
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) {
+            weights2(v[e], v[e + 1], cc, nl);
+            scores2(w[c][e], w[c][e + 1], v[e], v[e + 1], nd);
+          }
+          if (masked) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (c * 16 + e < lo || c * 16 + e >= hi) w[c][e] = 0.f;
+          }
+          store_packed(s_addr + 16 * c, w[c]);
+        }
+        tc::tmem_wait_st();
+        tc::fence_before_sync();
+        mbar_arrive(&ds_full[j % NSB]);
+      }
+      g = end_j;
     }
-    // ------------------------------------------------------------ epilogue
-    if (ok) ok = wwait(all_done, 0);
-    tc::fence_after_sync();
-    const int blk = (warp - C::SOFT0) >> 2;   // four warps store 64 columns
-    if (blk < NSUB)
-      tc::store_o_rows<64>(lane_base + C::COL_DQ + 64 * blk, !ok, p.sm_scale, p.dq + at * D + 64 * blk,
-                           valid, lane);
   }
 
   tc::tmem_wait_ld();
@@ -975,7 +1027,7 @@ __device__ __forceinline__ void back_dq_block(const CUtensorMap& tmQ, const CUte
   tc::fence_before_sync();
   __syncthreads();
   if (warp == 0 && lane == 0 && *abort_flag) {
-    mbar_drain(q_full, 0);
+    mbar_drain(q_full, (issued_q - 1) & 1);
     for (int i = max(0, issued_k - NK); i < issued_k; ++i) mbar_drain(&k_full[i % NK], i / NK & 1);
     for (int i = max(0, issued_v - NV); i < issued_v; ++i) mbar_drain(&v_full[i % NV], i / NV & 1);
   }
@@ -1009,6 +1061,8 @@ int set_smem(cudaError_t e) {
   return SINKATTN_CUDA_ERROR;
 }
 
+constexpr int kRunTiles = 16;   // tiles of keys that a CTA of the pass of dq goes through, where it can choose
+
 template <int D>
 int launch_back(BackParams& p, cudaStream_t stream) {
   using KV = DkvCfg<D>;
@@ -1016,7 +1070,14 @@ int launch_back(BackParams& p, cudaStream_t stream) {
   // every size is checked, and every map made, before the first launch
   const int64_t per = static_cast<int64_t>(p.Hkv) * p.batch;
   const int64_t dkv_items = (static_cast<int64_t>(p.max_kv) + 127) / 128 * per;
-  const int64_t dq_items = p.total_q > 0 ? p.nqb * per : 0;
+  // Query tiles of a CTA: several where they see few keys, so that the next one's rows
+  // come while it ends the one before, but not so many that SMs would be left without work.
+  const int64_t seen = p.window > 0 ? int64_t{p.window} + p.QB : std::max(p.max_kv / 2, 1);
+  const int64_t tiles = (seen + DQ::KT - 1) / DQ::KT;
+  const int64_t spread = p.nqb * per / (4 * 152 * DQ::CTAS);
+  p.run = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({kRunTiles / tiles, spread, 8})));
+  p.nrun = (p.nqb + p.run - 1) / p.run;
+  const int64_t dq_items = p.total_q > 0 ? p.nrun * per : 0;
   p.sink_blocks = p.dsinks ? (dq_items ? static_cast<int>(back_sink_blocks(p.total_q, p.Hq)) : 1) : 0;
   if (std::max(dkv_items + p.sink_blocks, dq_items) >= (int64_t{1} << 31)) {
     set_error("too many work items");
