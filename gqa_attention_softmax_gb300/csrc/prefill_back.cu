@@ -1128,13 +1128,14 @@ int launch_prefill_back(const BackArgs& a, cudaStream_t stream) {
   p.lse = a.lse; p.sinks = a.sinks; p.dlse = a.dlse;
   p.cu_q = a.cu_q; p.cu_k = a.cu_k;
   p.batch = a.batch; p.total_q = a.total_q; p.total_k = a.total_k;
-  p.max_q = a.max_q; p.max_kv = a.max_kv;
+  p.max_q = std::min(a.max_q, a.total_q);   // (bounds may be far above what there is)
+  p.max_kv = std::min(a.max_kv, a.total_k);
   p.Hq = a.Hq; p.Hkv = a.Hkv; p.G = a.Hq / a.Hkv;
   p.sm_scale = a.sm_scale; p.scale_log2 = a.sm_scale * kLog2e;
   p.causal = a.causal;
-  p.window = a.window < std::min(a.max_kv, a.total_k) ? a.window : 0;   // (one of all keys cuts nothing)
+  p.window = a.window < p.max_kv ? a.window : 0;   // (one of all keys cuts nothing)
   p.QB = 128 / p.G;
-  p.nqb = (a.max_q + p.QB - 1) / p.QB;
+  p.nqb = static_cast<int>((int64_t{p.max_q} + p.QB - 1) / p.QB);
   const int rows = a.d == 64 ? DkvCfg<64>::QT : DkvCfg<128>::QT;
   p.chunks = p.G > rows ? 2 : 1;
   p.GT = (p.G + p.chunks - 1) / p.chunks;

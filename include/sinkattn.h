@@ -574,7 +574,7 @@ SINKATTN_API int sinkattn_pages_lists(const int32_t* table, int32_t num_pages, i
  * depend on timing. A sequence whose inputs hold NaN or infinities gets NaN; the
  * other sequences do not. A row whose lse is -inf has no weights: it gives and gets
  * no gradient. Each sequence needs Lq_b <= Lk_b. Lengths that contradict the host sizes record
- * SINKATTN_BAD_LENGTHS and leave that sequence's gradients undefined.
+ * SINKATTN_BAD_LENGTHS and leave that sequence's gradients and dsinks undefined.
  */
 SINKATTN_API int sinkattn_prefill_backward(
     const void* dout, const void* q, const void* k, const void* v, const void* out,
@@ -625,7 +625,7 @@ SINKATTN_API int sinkattn_rope_turns(const double* inv_freq, int32_t n, uint64_t
  *     token contiguous, token i at element i * q_stride (k_stride, v_stride):
  *     multiples of 8, so slices of one projection's output need no copy;
  *   cu_seqlens int32 [batch + 1] (device), tokens = cu_seqlens[batch] (rows
- *     behind it are neither read nor written);
+ *     behind it have no effect, and none are written);
  *   positions int32 [tokens] (device), or NULL: the index in the sequence;
  *   q_weight, k_weight fp32 [d] (device) or NULL: y = w * x * rsqrt(mean x^2 +
  *     eps) over the head's d elements before the rotation; NULL: no norm;

@@ -117,6 +117,32 @@ def test_peaked_weights(d):
 
 @gpu
 @pytest.mark.parametrize("shape", [(8, 2, 64), (8, 2, 128)])
+def test_maxima_far_above_the_lengths(shape):
+    """max_seqlen_* only bound the lengths: the largest int32 gives what the exact ones give."""
+    for window in (0, 40):
+        x, h = make([33, 200], [50, 200], *shape, window=window)
+        cu = [torch.tensor(h[n], dtype=torch.int32, device="cuda") for n in ("cu_q", "cu_k")]
+        got = sa.sinkattn_prefill_backward(
+            x["dout"], x["q"], x["k"], x["v"], x["out"], x["lse"], x["sinks"], *cu, 2 ** 31 - 1,
+            2 ** 31 - 1, h["hkv"], window=window)
+        for a, b in zip(got, call(x, h)):
+            assert torch.equal(a, b)
+
+
+@gpu
+@pytest.mark.parametrize("shape", [(16, 2, 64), (16, 2, 128)])
+@pytest.mark.parametrize("window", [1, 20, 200])
+def test_many_tokens_in_short_windows(shape, window):
+    """Several query tiles a CTA: as many tokens as give each SM a few of them, of sequences
+    of every length."""
+    gen = torch.Generator().manual_seed(5)
+    lens = torch.randint(0, 400, (64,), generator=gen).tolist() + [0, 1, 3000]
+    x, h = make(lens, lens, *shape, window=window)
+    check(call(x, h), x, h)
+
+
+@gpu
+@pytest.mark.parametrize("shape", [(8, 2, 64), (8, 2, 128)])
 def test_sinks_of_minus_infinity(shape):
     """Heads whose sink is -inf have none: dsinks 0. A row with lse -inf has no
     weights: no gradient of its own and none for others, as if its dout were 0."""
