@@ -24,6 +24,7 @@
 // unrounded. Every wait is bounded; on a timeout the CTA records
 // SINKATTN_TIMEOUT, drains its copies and MMAs, frees TMEM and exits.
 #include <algorithm>
+#include <type_traits>
 
 #include "chain.cuh"
 #include "common.cuh"
@@ -50,6 +51,7 @@ struct BackParams {
   int dkv_items;
   int QB, nqb;   // query tokens of a tile of 128 rows, tiles of the longest sequence
   int run, nrun; // tiles of a CTA of the pass of dq, CTAs of the longest sequence
+  int krun;      // tiles of a CTA of the pass of dk and dv
   int GT, chunks, QB2;   // heads and tokens of a tile of the dk, dv pass, tiles of a token
 };
 
@@ -260,6 +262,21 @@ __device__ __forceinline__ void store_packed(uint32_t addr, const float (&v)[16]
   tc::tmem_st8(addr, pk);
 }
 
+__device__ __forceinline__ void store_zeros(uint32_t addr) {   // 8 columns
+  const uint32_t zero[8] = {};
+  tc::tmem_st8(addr, zero);
+}
+
+// Of a warp's 32 x 32 square of a tile that the mask cuts, 0 of the columns before lo
+// and from hi on are visible to a lane. The diagonals cut few of a tile's squares: the
+// others take no comparisons, or no arithmetic at all.
+enum Seen { kAll, kSome, kNone };
+__device__ __forceinline__ Seen seen_by_warp(bool masked, int lo, int hi) {
+  if (!masked) return kAll;   // (uniform over the warp)
+  if (__all_sync(0xffffffffu, lo <= 0 && hi >= 32)) return kAll;
+  return __any_sync(0xffffffffu, max(lo, 0) < min(hi, 32)) ? kSome : kNone;
+}
+
 // dK, dV. S^T = K Q^T and dP^T = V dO^T (M 128 keys, N QT query rows, K d; all from
 // shared memory), dV += P^T dO and dK += dS^T Q (M 128 keys, N d, K QT; P^T and
 // dS^T from TMEM, where both replace S^T). Keys in the TMEM lanes make P^T and
@@ -289,7 +306,7 @@ struct DkvCfg {
   static constexpr int NR = 4;                      // slots of the rows' lse and delta
   static constexpr int OFF_ROW = OFF_DO + ND * Q_TILE;   // [NR][-lse log2 e, -delta][QT]
   static constexpr int OFF_BAR = OFF_ROW + NR * 2 * QT * 4;
-  static constexpr int N_BARS = 1 + 2 * NQ + 2 * ND + NB + NR + 2 * NSB + 2 + 1 + 1 + 3;
+  static constexpr int N_BARS = 2 + 2 * NQ + 2 * ND + NB + NR + 2 * NSB + 2 + 1 + 2 + 3;
   static_assert(NR % NG == 0 && NR <= ND && ND <= NQ, "order of the copies");
   static constexpr int SMEM = OFF_BAR + N_BARS * 8 + 16;
   static constexpr uint32_t COL_S = 0;
@@ -311,7 +328,8 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
   extern __shared__ __align__(1024) uint8_t smem[];   // (swizzled tiles start on 1024 bytes)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* kv_full = bars;
-  uint64_t* q_full = kv_full + 1;      // [NQ]
+  uint64_t* kv_empty = kv_full + 1;    // S^T and dP^T of the key tile done
+  uint64_t* q_full = kv_empty + 1;     // [NQ]
   uint64_t* q_empty = q_full + NQ;     // [NQ] dK, the last that reads the stage, done
   uint64_t* do_full = q_empty + NQ;    // [ND]
   uint64_t* do_empty = do_full + ND;   // [ND] dP^T and dV done
@@ -321,8 +339,9 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
   uint64_t* p_full = s_free + NSB;     // [NSB] P^T and dS^T written (the group's arrivals)
   uint64_t* dp_full = p_full + NSB;    // [2] of even and odd tiles: dP^T written
   uint64_t* dp_free = dp_full + 2;     // dP^T read (the group's arrivals)
-  uint64_t* all_done = dp_free + 1;    // dV and dK
-  uint64_t* drain = all_done + 1;      // [3]
+  uint64_t* dkv_full = dp_free + 1;    // a key tile's dV and dK done
+  uint64_t* dkv_free = dkv_full + 1;   // and read
+  uint64_t* drain = dkv_free + 1;      // [3]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 3);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
   int* status = &g_status_prefill_back;
@@ -334,28 +353,38 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
     sum_sinks<C::THREADS>(p, blockIdx.x - p.dkv_items, reinterpret_cast<float(*)[32]>(smem));
     return;
   }
-  // items: the first key tiles (which the most queries see) of all sequences and KV heads first
+  // A CTA's key tiles: m of them; the first ones (which the most queries see) of all
+  // sequences and KV heads are those of the first CTAs.
   const int per = p.Hkv * p.batch;
-  const int kt = static_cast<int>(blockIdx.x) / per;
+  const int kt = static_cast<int>(blockIdx.x) / per * p.krun;
   const int kvh = static_cast<int>(blockIdx.x) % per % p.Hkv;
   const int b = static_cast<int>(blockIdx.x) % per / p.Hkv;
   const Seq s = load_seq(p, b);
   if (!s.ok && threadIdx.x == 0) atomicExch(status, SINKATTN_BAD_LENGTHS);
-  const int k0 = kt * 128;
-  if (!s.ok || k0 >= s.lk) {   // uniform over the CTA, before any barrier or TMEM use
+  const int m = s.ok ? min(p.krun, (s.lk - 128 * kt + 127) / 128) : 0;
+  if (m <= 0) {   // uniform over the CTA, before any barrier or TMEM use
     grid_dependency_wait();    // (this launch ends after the one before)
     return;
   }
-  const int nk = min(128, s.lk - k0);
   const int off = s.lk - s.lq;   // position of query 0
-  // queries [i0, i1) see some key of the tile
-  const int i0 = p.causal ? max(0, k0 - off) : 0;
-  const int i1 = p.window > 0 ? max(0, min(s.lq, k0 + nk - 1 + p.window - off)) : s.lq;
   const int GT = p.GT, cs = p.chunks - 1, QB2 = p.QB2, rows = GT * QB2;
-  const int n = i1 > i0 ? (i1 - i0 + QB2 - 1) / QB2 << cs : 0;
+  struct Tile {
+    int k0, nk;        // its keys
+    int i0, i1, n;     // queries [i0, i1) see some of them, in n tiles (which may be 0)
+  };
+  auto tile = [&](int i) {
+    Tile t;
+    t.k0 = 128 * (kt + i);
+    t.nk = min(128, s.lk - t.k0);
+    t.i0 = p.causal ? max(0, t.k0 - off) : 0;
+    t.i1 = p.window > 0 ? max(0, min(s.lq, t.k0 + t.nk - 1 + p.window - off)) : s.lq;
+    t.n = t.i1 > t.i0 ? (t.i1 - t.i0 + QB2 - 1) / QB2 << cs : 0;
+    return t;
+  };
 
   if (threadIdx.x == 0) {
     mbar_init(kv_full, 1);
+    mbar_init(kv_empty, 2);
     for (int i = 0; i < NQ; ++i) {
       mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 1);
@@ -372,7 +401,8 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
     }
     for (int i = 0; i < 2; ++i) mbar_init(&dp_full[i], 1);
     mbar_init(dp_free, C::GROUP);
-    mbar_init(all_done, 1);
+    mbar_init(dkv_full, 1);
+    mbar_init(dkv_free, 2 * NSUB * 128);
     for (int i = 0; i < 3; ++i) mbar_init(&drain[i], 1);
     *abort_flag = 0;
     fence_barrier_init();
@@ -390,7 +420,7 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  int issued_q = 0, issued_do = 0;   // tiles whose copies were issued (or left out by the test hook)
+  int issued_kv = 0, issued_q = 0, issued_do = 0;   // tiles whose copies were issued (or left out by the test hook)
   auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
     return warp_wait(bar, parity, abort_flag, status);
   };
@@ -409,26 +439,17 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
   if (warp == 0) {
     // ---------------------------------------------------------------- copies
     const int skip_tile = hook_skip_tile();
-    auto load = [&](const CUtensorMap* map, int j, uint8_t* to, uint64_t* bar) {   // into a free stage
+    // Tile j of the CTA, tile x of its key tile t, into a free stage.
+    auto load = [&](const CUtensorMap* map, const Tile& t, int j, int x, uint8_t* to, uint64_t* bar) {
       if (j != skip_tile && leader) {   // test hook: the waits for this tile run out
         mbar_arrive_expect_tx(bar, static_cast<uint32_t>(NSUB * 128 * rows));
-        const int tok = s.q0 + i0 + (j >> cs) * QB2, head = kvh * p.G + (j & cs) * GT;
+        const int tok = s.q0 + t.i0 + (x >> cs) * QB2, head = kvh * p.G + (x & cs) * GT;
 #pragma unroll
         for (int sub = 0; sub < NSUB; ++sub)
           tc::tma_load_3d(to + sub * C::QSUB, map, sub * 64, head, tok, bar);
       }
       __syncwarp();
     };
-    if (n > 0 && leader) {
-      mbar_arrive_expect_tx(kv_full, 2 * C::K_TILE);
-      const int slab = p.Hkv * s.k0 + kvh * s.lk + k0;
-#pragma unroll
-      for (int sub = 0; sub < NSUB; ++sub) {
-        tma_load_2d(smem + C::OFF_K + sub * C::KSUB, &tmK, sub * 64, slab, kv_full);
-        tma_load_2d(smem + C::OFF_V + sub * C::KSUB, &tmV, sub * 64, slab, kv_full);
-      }
-    }
-    __syncwarp();
     // -lse log2(e) and -delta of a tile's rows, QT / 32 a lane. A row outside the tile
     // gets lse = +inf: P = 0. Both kinds of writes arrive, the copies when they have landed.
     constexpr int kRows = QT / 32;
@@ -438,12 +459,12 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
       rt[e] = (lane + 32 * e) / GT;
       rh[e] = (lane + 32 * e) % GT;
     }
-    auto load_rows = [&](int j) {
+    auto load_rows = [&](const Tile& t, int j, int x) {
       float* to = reinterpret_cast<float*>(smem + C::OFF_ROW) + j % NR * 2 * QT + lane;
 #pragma unroll
       for (int e = 0; e < kRows; ++e) {
-        const int i = i0 + (j >> cs) * QB2 + rt[e], h = (j & cs) * GT + rh[e];
-        if (lane + 32 * e < rows && i < i1 && h < p.G) {
+        const int i = t.i0 + (x >> cs) * QB2 + rt[e], h = (x & cs) * GT + rh[e];
+        if (lane + 32 * e < rows && i < t.i1 && h < p.G) {
           const long long at = static_cast<long long>(s.q0 + i) * p.Hq + kvh * p.G + h;
           copy4_async(to + 32 * e, p.nlse + at);
           copy4_async(to + QT + 32 * e, p.ndelta + at);
@@ -455,80 +476,120 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
       mbar_arrive(&row_full[j % NR]);
       arrive_after_copies(&row_full[j % NR]);
     };
-    auto load_q = [&](int x) {
-      issued_q = x + 1;
-      load(&tmQ, x, smem + C::OFF_Q + x % NQ * C::Q_TILE, &q_full[x % NQ]);
-    };
-    auto load_do = [&](int y) {
-      issued_do = y + 1;
-      load(&tmDo, y, smem + C::OFF_DO + y % ND * C::Q_TILE, &do_full[y % ND]);
-    };
-    // The first tiles' copies need nothing of the launch before this one, the rows do.
-    for (int x = 0; x < min(NQ, n); ++x) load_q(x);
-    for (int y = 0; y < min(ND, n); ++y) load_do(y);
-    grid_dependency_wait();
-    // Q of tile x, and the tiles whose dO and rows take the places of the same tile x - NQ
-    for (int x = 0; x < n + NQ - NR; ++x) {
-      if (x >= NQ && !wwait(&q_empty[x % NQ], (x / NQ - 1) & 1)) break;
-      if (x >= NQ && x < n) load_q(x);
-      const int y = x - (NQ - ND), z = x - (NQ - NR);
-      if (y >= ND && y < n) {
-        if (!wwait(&do_empty[y % ND], (y / ND - 1) & 1)) break;
-        load_do(y);
+    // Q of a key tile's tile x, and the tiles whose dO and rows take the places of
+    // the same tile x - NQ. The first tiles' copies need nothing of the launch before this one, the rows do.
+    bool ok = true;
+    for (int i = 0, g = 0; i < m && ok; ++i) {   // g: tiles before
+      const Tile t = tile(i);
+      if (t.n == 0) continue;
+      if (issued_kv > 0 && !wwait(kv_empty, (issued_kv - 1) & 1)) break;
+      ++issued_kv;
+      if (leader) {
+        mbar_arrive_expect_tx(kv_full, 2 * C::K_TILE);
+        const int slab = p.Hkv * s.k0 + kvh * s.lk + t.k0;
+#pragma unroll
+        for (int sub = 0; sub < NSUB; ++sub) {
+          tma_load_2d(smem + C::OFF_K + sub * C::KSUB, &tmK, sub * 64, slab, kv_full);
+          tma_load_2d(smem + C::OFF_V + sub * C::KSUB, &tmV, sub * 64, slab, kv_full);
+        }
       }
-      if (z >= 0) load_rows(z);
+      __syncwarp();
+      for (int x = 0; x < t.n + NQ - NR; ++x) {
+        const int j = g + x;
+        if (j >= NQ && !(ok = wwait(&q_empty[j % NQ], (j / NQ - 1) & 1))) break;
+        if (x < t.n) {
+          issued_q = j + 1;
+          load(&tmQ, t, j, x, smem + C::OFF_Q + j % NQ * C::Q_TILE, &q_full[j % NQ]);
+        }
+        const int y = x - (NQ - ND), z = x - (NQ - NR);
+        if (y >= 0 && y < t.n) {
+          const int jy = g + y;
+          if (jy >= ND && !(ok = wwait(&do_empty[jy % ND], (jy / ND - 1) & 1))) break;
+          issued_do = jy + 1;
+          load(&tmDo, t, jy, y, smem + C::OFF_DO + jy % ND * C::Q_TILE, &do_full[jy % ND]);
+        }
+        if (z >= 0) {
+          if (g + z == 0) grid_dependency_wait();
+          load_rows(t, g + z, z);
+        }
+      }
+      g += t.n;
     }
+    grid_dependency_wait();   // (without rows too: this launch ends after the one before)
     wait_copies();   // (before the CTA's shared memory goes away)
   } else if (warp == 1) {
     // ---------------------------------------------------------------- S^T = K Q^T
     const uint64_t kd = tc::smem_desc_sw128(smem_u32(smem + C::OFF_K), 16, 1024);
     const uint64_t qd = tc::smem_desc_sw128(smem_u32(smem + C::OFF_Q), 16, 1024);
-    if (n > 0 && wwait(kv_full, 0)) {
-      for (int j = 0; j < n; ++j) {
+    bool ok = true;
+    for (int i = 0, j = 0, c = 0; i < m && ok; ++i) {   // c: key tiles with work before
+      const int end_j = j + tile(i).n;
+      if (j == end_j) continue;
+      if (!wwait(kv_full, c & 1)) break;
+      for (; j < end_j; ++j) {
         const int sb = j % NSB;
-        if (j < NSB ? !wwait(&q_full[j % NQ], 0)
-                    : !wwait2(&s_free[sb], (j / NSB - 1) & 1, &q_full[j % NQ], j / NQ & 1)) break;
+        ok = j < NSB ? wwait(&q_full[j % NQ], 0)
+                     : wwait2(&s_free[sb], (j / NSB - 1) & 1, &q_full[j % NQ], j / NQ & 1);
+        if (!ok) break;
         tc::fence_after_sync();
         issue_ss<D, QT>(leader, tmem + C::COL_S + QT * sb, kd, qd + j % NQ * tile16, C::KSUB, C::QSUB);
         if (leader) tc::commit(&s_full[j % NB]);
         __syncwarp();
       }
+      if (leader) tc::commit(kv_empty);
+      __syncwarp();
+      ++c;
     }
     finish(&drain[0]);
   } else if (warp == 2) {
     // ---------------------------------------------------------------- dP^T = V dO^T
     const uint64_t vd = tc::smem_desc_sw128(smem_u32(smem + C::OFF_V), 16, 1024);
     const uint64_t dod = tc::smem_desc_sw128(smem_u32(smem + C::OFF_DO), 16, 1024);
-    if (n > 0 && wwait(kv_full, 0)) {
-      for (int j = 0; j < n; ++j) {
-        if (j < 1 ? !wwait(&do_full[0], 0)
-                  : !wwait2(dp_free, (j - 1) & 1, &do_full[j % ND], j / ND & 1)) break;
+    bool ok = true;
+    for (int i = 0, j = 0, c = 0; i < m && ok; ++i) {
+      const int end_j = j + tile(i).n;
+      if (j == end_j) continue;
+      if (!wwait(kv_full, c & 1)) break;
+      for (; j < end_j; ++j) {
+        ok = j < 1 ? wwait(&do_full[0], 0) : wwait2(dp_free, (j - 1) & 1, &do_full[j % ND], j / ND & 1);
+        if (!ok) break;
         tc::fence_after_sync();
         issue_ss<D, QT>(leader, tmem + C::COL_DP, vd, dod + j % ND * tile16, C::KSUB, C::QSUB);
         if (leader) tc::commit(&dp_full[j & 1]);
         __syncwarp();
       }
+      if (leader) tc::commit(kv_empty);
+      __syncwarp();
+      ++c;
     }
     finish(&drain[1]);
   } else if (warp == 3) {
     // ------------------------------------------ dV += P^T dO and dK += dS^T Q
     const uint64_t dot = tc::smem_desc_sw128(smem_u32(smem + C::OFF_DO), C::QSUB, 1024);   // MN-major
     const uint64_t qt = tc::smem_desc_sw128(smem_u32(smem + C::OFF_Q), C::QSUB, 1024);
-    for (int j = 0; j < n; ++j) {
-      const int sb = j % NSB;
-      const uint32_t pt = tmem + C::COL_S + QT * sb;
-      if (!wwait(&p_full[sb], j / NSB & 1)) break;
-      tc::fence_after_sync();
-      issue_ts<D, QT / 16>(leader, tmem + C::COL_DV, pt, dot + j % ND * tile16, j == 0);
-      if (leader) tc::commit(&do_empty[j % ND]);
-      issue_ts<D, QT / 16>(leader, tmem + C::COL_DK, pt + 8, qt + j % NQ * tile16, j == 0);
-      if (leader) {
-        tc::commit(&s_free[sb]);
-        tc::commit(&q_empty[j % NQ]);
+    bool ok = true;
+    for (int i = 0, j = 0, c = 0; i < m && ok; ++i) {
+      const int first = j, end_j = j + tile(i).n;
+      if (j == end_j) continue;
+      if (c > 0 && !wwait(dkv_free, (c - 1) & 1)) break;
+      for (; j < end_j; ++j) {
+        const int sb = j % NSB;
+        const uint32_t pt = tmem + C::COL_S + QT * sb;
+        if (!(ok = wwait(&p_full[sb], j / NSB & 1))) break;
+        tc::fence_after_sync();
+        issue_ts<D, QT / 16>(leader, tmem + C::COL_DV, pt, dot + j % ND * tile16, j == first);
+        if (leader) tc::commit(&do_empty[j % ND]);
+        issue_ts<D, QT / 16>(leader, tmem + C::COL_DK, pt + 8, qt + j % NQ * tile16, j == first);
+        if (leader) {
+          tc::commit(&s_free[sb]);
+          tc::commit(&q_empty[j % NQ]);
+        }
+        __syncwarp();
       }
+      if (leader) tc::commit(dkv_full);
       __syncwarp();
+      ++c;
     }
-    if (leader) tc::commit(all_done);
     finish(&drain[2]);
   } else {
     // ---------------------------------------------------------------- P and dS
@@ -539,84 +600,107 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
     const int key = quad * 32 + lane;          // key of the tile
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const float* row_s = reinterpret_cast<const float*>(smem + C::OFF_ROW) + cols;   // [NR][2][QT]
-    // every key of the tile sees every row of the token blocks [b_lo, b_hi)
-    int b_lo = 0, b_hi = (i1 - i0) / QB2;
-    if (p.causal) b_lo = max(0, (k0 + 127 - off - i0 + QB2 - 1) / QB2);
-    if (p.window > 0) b_hi = min(b_hi, (k0 + p.window - off - i0) / QB2);
     const float2 cc = make_float2(p.scale_log2, p.scale_log2);
     bool ok = true;
-    for (int j = grp; j < n; j += NG) {
-      const int sb = j % NSB;
-      const bool masked = (j >> cs) < b_lo || (j >> cs) >= b_hi;
-      int lo = -128, hi = 128, nt = QB2;         // this thread's visible columns
-      if (masked) {
-        const int t0 = i0 + (j >> cs) * QB2;     // first query of the tile
-        const int pos0 = off + t0;
-        nt = min(QB2, i1 - t0);
-        lo = (p.causal ? max(0, min(nt, k0 + key - pos0)) * GT : 0) - cols;
-        hi = (p.window > 0 ? max(0, min(nt, k0 + key + p.window - pos0)) : nt) * GT - cols;
+    for (int i = 0, g = 0, done = 0; i < m && ok; ++i) {   // tiles, key tiles with work before
+      const Tile t = tile(i);
+      // every key of the tile sees every row of tiles [j_lo, j_hi), whole blocks of tokens
+      int j_lo = g, j_hi = (t.i1 - t.i0) / QB2;
+      if (p.causal) j_lo += max(0, (t.k0 + 127 - off - t.i0 + QB2 - 1) / QB2) << cs;
+      if (p.window > 0) j_hi = min(j_hi, (t.k0 + p.window - off - t.i0) / QB2);
+      j_hi = g + (j_hi << cs);
+      const int end_j = g + t.n;
+      for (int j = NG == 1 ? g : g + ((grp ^ g) & (NG - 1)); j < end_j; j += NG) {
+        const int sb = j % NSB;
+        const bool masked = j < j_lo || j >= j_hi;
+        int lo = -128, hi = 128, nt = QB2;         // this thread's visible columns
+        if (masked) {
+          const int t0 = t.i0 + ((j - g) >> cs) * QB2;   // first query of the tile
+          const int pos0 = off + t0;
+          nt = min(QB2, t.i1 - t0);
+          lo = (p.causal ? max(0, min(nt, t.k0 + key - pos0)) * GT : 0) - cols;
+          hi = (p.window > 0 ? max(0, min(nt, t.k0 + key + p.window - pos0)) : nt) * GT - cols;
+        }
+        const Seen seen = seen_by_warp(masked, lo, hi);
+        const uint32_t s_addr = lane_base + C::COL_S + QT * sb + cols;
+        const uint32_t dp_addr = lane_base + C::COL_DP + cols;
+        const float4* lse4 = reinterpret_cast<const float4*>(row_s + j % NR * 2 * QT);
+        const float4* del4 = lse4 + QT / 4;
+        if (!warp_wait3(&row_full[j % NR], j / NR & 1, &s_full[j % NB], j / NB & 1, &dp_full[j & 1], j >> 1 & 1,
+                        abort_flag, status)) {
+          ok = false;
+          break;
+        }
+        tc::fence_after_sync();
+        auto square = [&](auto cut) {   // P and dS of the warp's square
+          float w[2][16];
+          tc::tmem_ld16(dp_addr, w[0]);
+          tc::tmem_ld16(dp_addr + 16, w[1]);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float v[16];
+            tc::tmem_ld16(s_addr + 16 * c, v);
+            tc::tmem_wait_ld();
+            if (c == 0) {
+              tc::fence_before_sync();
+              mbar_arrive(dp_free);   // the next tile's dP^T may come
+            }
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+              const float4 l = lse4[c * 4 + e / 4], d = del4[c * 4 + e / 4];
+              weights2(v[e], v[e + 1], cc, make_float2(l.x, l.y));
+              weights2(v[e + 2], v[e + 3], cc, make_float2(l.z, l.w));
+              scores2(w[c][e], w[c][e + 1], v[e], v[e + 1], make_float2(d.x, d.y));
+              scores2(w[c][e + 2], w[c][e + 3], v[e + 2], v[e + 3], make_float2(d.z, d.w));
+            }
+            if constexpr (decltype(cut)::value) {   // (0 x NaN of another row is not 0)
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                if (c * 16 + e < lo || c * 16 + e >= hi) v[e] = w[c][e] = 0.f;
+            }
+            store_packed(s_addr + 16 * c, v);
+            store_packed(s_addr + 16 * c + 8, w[c]);
+          }
+        };
+        if (seen == kAll) {
+          square(std::false_type());
+        } else if (seen == kSome) {
+          square(std::true_type());
+        } else {
+          mbar_arrive(dp_free);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) store_zeros(s_addr + 8 * c);
+        }
+        if (nt < QB2) {
+          // The visible rows end inside the tile: those behind them may be another
+          // sequence's, whose NaN would pass through zero weights. Both products
+          // that read the tile along d are done.
+          zero_rows<NSUB>(smem + C::OFF_Q + j % NQ * C::Q_TILE, C::QSUB, nt * GT, QT, tid, C::GROUP);
+          zero_rows<NSUB>(smem + C::OFF_DO + j % ND * C::Q_TILE, C::QSUB, nt * GT, QT, tid, C::GROUP);
+          tc::fence_proxy_async_smem();
+        }
+        tc::tmem_wait_st();
+        tc::fence_before_sync();
+        mbar_arrive(&p_full[sb]);
       }
-      const uint32_t s_addr = lane_base + C::COL_S + QT * sb + cols;
-      const uint32_t dp_addr = lane_base + C::COL_DP + cols;
-      const float4* lse4 = reinterpret_cast<const float4*>(row_s + j % NR * 2 * QT);
-      const float4* del4 = lse4 + QT / 4;
-      if (!warp_wait3(&row_full[j % NR], j / NR & 1, &s_full[j % NB], j / NB & 1, &dp_full[j & 1], j >> 1 & 1,
-                      abort_flag, status)) {
-        ok = false;
-        break;
-      }
+      // ------------------------------------------------------------ epilogue
+      if (ok && t.n > 0) ok = wwait(dkv_full, done & 1);
       tc::fence_after_sync();
-      float w[2][16];
-      tc::tmem_ld16(dp_addr, w[0]);
-      tc::tmem_ld16(dp_addr + 16, w[1]);
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float v[16];
-        tc::tmem_ld16(s_addr + 16 * c, v);
-        tc::tmem_wait_ld();
-        if (c == 0) {
-          tc::fence_before_sync();
-          mbar_arrive(dp_free);   // the next tile's dP^T may come
-        }
-#pragma unroll
-        for (int e = 0; e < 16; e += 4) {
-          const float4 l = lse4[c * 4 + e / 4], d = del4[c * 4 + e / 4];
-          weights2(v[e], v[e + 1], cc, make_float2(l.x, l.y));
-          weights2(v[e + 2], v[e + 3], cc, make_float2(l.z, l.w));
-          scores2(w[c][e], w[c][e + 1], v[e], v[e + 1], make_float2(d.x, d.y));
-          scores2(w[c][e + 2], w[c][e + 3], v[e + 2], v[e + 3], make_float2(d.z, d.w));
-        }
-        if (masked) {   // (0 x NaN of another row is not 0)
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (c * 16 + e < lo || c * 16 + e >= hi) v[e] = w[c][e] = 0.f;
-        }
-        store_packed(s_addr + 16 * c, v);
-        store_packed(s_addr + 16 * c + 8, w[c]);
+      const int k = 128 * (kt + i) + key;
+      const long long row = static_cast<long long>(p.Hkv) * s.k0 + static_cast<long long>(kvh) * s.lk + k;
+      // four warps store 64 columns: dV's, then dK's
+      const int blk = (warp - C::SOFT0) >> 2;
+      const bool is_dk = blk >= NSUB;
+      if (blk < 2 * NSUB) {
+        tc::store_o_rows<64>(lane_base + C::COL_DV + 64 * blk, !(ok && t.n > 0), is_dk ? p.sm_scale : 1.f,
+                             (is_dk ? p.dk : p.dv) + row * D + 64 * (is_dk ? blk - NSUB : blk), k < s.lk,
+                             lane);
+        tc::fence_before_sync();
+        if (t.n > 0) mbar_arrive(dkv_free);
       }
-      if (nt < QB2) {
-        // The visible rows end inside the tile: those behind them may be another
-        // sequence's, whose NaN would pass through zero weights. Both products
-        // that read the tile along d are done.
-        zero_rows<NSUB>(smem + C::OFF_Q + j % NQ * C::Q_TILE, C::QSUB, nt * GT, QT, tid, C::GROUP);
-        zero_rows<NSUB>(smem + C::OFF_DO + j % ND * C::Q_TILE, C::QSUB, nt * GT, QT, tid, C::GROUP);
-        tc::fence_proxy_async_smem();
-      }
-      tc::tmem_wait_st();
-      tc::fence_before_sync();
-      mbar_arrive(&p_full[sb]);
+      g = end_j;
+      done += t.n > 0;
     }
-    // ------------------------------------------------------------ epilogue
-    if (ok && n > 0) ok = wwait(all_done, 0);
-    tc::fence_after_sync();
-    const long long row = static_cast<long long>(p.Hkv) * s.k0 + static_cast<long long>(kvh) * s.lk + k0 + key;
-    // four warps store 64 columns: dV's, then dK's
-    const int blk = (warp - C::SOFT0) >> 2;
-    const bool is_dk = blk >= NSUB;
-    if (blk < 2 * NSUB)
-      tc::store_o_rows<64>(lane_base + C::COL_DV + 64 * blk, !(ok && n > 0), is_dk ? p.sm_scale : 1.f,
-                           (is_dk ? p.dk : p.dv) + row * D + 64 * (is_dk ? blk - NSUB : blk), key < nk,
-                           lane);
   }
 
   // a warp that left its loop early may still have TMEM loads or stores in flight
@@ -627,7 +711,7 @@ __global__ void __launch_bounds__(DkvCfg<D>::THREADS, 1)
   if (warp == 0 && lane == 0 && *abort_flag) {
     // a wait gave up: let every issued copy land before the CTA's shared
     // memory goes away (a left-out tile's phase never completes: bounded)
-    if (n > 0) mbar_drain(kv_full, 0);
+    if (issued_kv > 0) mbar_drain(kv_full, (issued_kv - 1) & 1);
     for (int i = max(0, issued_q - NQ); i < issued_q; ++i) mbar_drain(&q_full[i % NQ], i / NQ & 1);
     for (int i = max(0, issued_do - ND); i < issued_do; ++i) mbar_drain(&do_full[i % ND], i / ND & 1);
   }
@@ -981,6 +1065,7 @@ __device__ __forceinline__ void back_dq_block(const CUtensorMap& tmQ, const CUte
         const bool masked = j < j_lo || j >= j_hi;
         const int j0 = t.k_lo + (j - g) * KT;
         const int lo = lo_r - j0 - cols, hi = hi_r - j0 - cols;
+        const Seen seen = seen_by_warp(masked, lo, hi);
         const uint32_t s_addr = lane_base + C::COL_S + KT * (j % NSB) + cols;
         if (!(ok = wwait2(&s_full[j % NSB], j / NSB & 1, &dp_full[j & 1], j >> 1 & 1))) break;
         tc::fence_after_sync();
@@ -990,29 +1075,40 @@ __device__ __forceinline__ void back_dq_block(const CUtensorMap& tmQ, const CUte
           zero_rows<NSUB>(smem + C::OFF_K + j % NK * C::K_TILE, C::KSUB, s.lk - j0, KT, tid, C::GROUP);
           tc::fence_proxy_async_smem();
         }
-        float w[2][16];
-        tc::tmem_ld16(dp_addr, w[0]);
-        tc::tmem_ld16(dp_addr + 16, w[1]);
+        auto square = [&](auto cut) {   // dS of the warp's square
+          float w[2][16];
+          tc::tmem_ld16(dp_addr, w[0]);
+          tc::tmem_ld16(dp_addr + 16, w[1]);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float v[16];
-          tc::tmem_ld16(s_addr + 16 * c, v);
-          tc::tmem_wait_ld();
-          if (c == 0) {
-            tc::fence_before_sync();
-            mbar_arrive(&dp_free[grp]);   // a later tile's dP may come
-          }
+          for (int c = 0; c < 2; ++c) {
+            float v[16];
+            tc::tmem_ld16(s_addr + 16 * c, v);
+            tc::tmem_wait_ld();
+            if (c == 0) {
+              tc::fence_before_sync();
+              mbar_arrive(&dp_free[grp]);   // a later tile's dP may come
+            }
 #pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            weights2(v[e], v[e + 1], cc, nl);
-            scores2(w[c][e], w[c][e + 1], v[e], v[e + 1], nd);
-          }
-          if (masked) {
+            for (int e = 0; e < 16; e += 2) {
+              weights2(v[e], v[e + 1], cc, nl);
+              scores2(w[c][e], w[c][e + 1], v[e], v[e + 1], nd);
+            }
+            if constexpr (decltype(cut)::value) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              if (c * 16 + e < lo || c * 16 + e >= hi) w[c][e] = 0.f;
+              for (int e = 0; e < 16; ++e)
+                if (c * 16 + e < lo || c * 16 + e >= hi) w[c][e] = 0.f;
+            }
+            store_packed(s_addr + 16 * c, w[c]);
           }
-          store_packed(s_addr + 16 * c, w[c]);
+        };
+        if (seen == kAll) {
+          square(std::false_type());
+        } else if (seen == kSome) {
+          square(std::true_type());
+        } else {
+          mbar_arrive(&dp_free[grp]);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) store_zeros(s_addr + 16 * c);
         }
         tc::tmem_wait_st();
         tc::fence_before_sync();
@@ -1061,7 +1157,20 @@ int set_smem(cudaError_t e) {
   return SINKATTN_CUDA_ERROR;
 }
 
-constexpr int kRunTiles = 16;   // tiles of keys that a CTA of the pass of dq goes through, where it can choose
+// How many of `items` equal tiles a CTA goes through, `ctas` of them on an SM: the
+// number for which the last wave ends first, if a tile takes `steps` steps and a CTA
+// one more, to start and to end. 16,384 tokens of 64/8 heads of 64 in windows of
+// 128: dq TODO us at the TODO this gives, TODO at one; dk and dv TODO at TODO, TODO at one.
+int tiles_of_cta(int64_t items, int ctas, int64_t steps) {
+  int best = 1;
+  int64_t least = 0;
+  for (int n = 1; n <= 32; ++n) {
+    const int64_t waves = ((items + n - 1) / n + 152 * ctas - 1) / (152 * ctas);
+    const int64_t time = waves * (n * steps + 1);
+    if (n == 1 || time < least) best = n, least = time;
+  }
+  return best;
+}
 
 template <int D>
 int launch_back(BackParams& p, cudaStream_t stream) {
@@ -1069,14 +1178,15 @@ int launch_back(BackParams& p, cudaStream_t stream) {
   using DQ = DqCfg<D>;
   // every size is checked, and every map made, before the first launch
   const int64_t per = static_cast<int64_t>(p.Hkv) * p.batch;
-  const int64_t dkv_items = (static_cast<int64_t>(p.max_kv) + 127) / 128 * per;
-  // Query tiles of a CTA: several where they see few keys, so that the next one's rows
-  // come while it ends the one before, but not so many that SMs would be left without work.
-  const int64_t seen = p.window > 0 ? int64_t{p.window} + p.QB : std::max(p.max_kv / 2, 1);
-  const int64_t tiles = (seen + DQ::KT - 1) / DQ::KT;
-  const int64_t spread = p.nqb * per / (4 * 152 * DQ::CTAS);
-  p.run = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({kRunTiles / tiles, spread, 8})));
+  // Tiles of a CTA. Without a window the tiles differ in what they see, and one
+  // each, the longest first, fills the SMs best. With one they are alike and short.
+  const int64_t seqs = std::min<int64_t>(p.total_q / p.QB + p.batch, static_cast<int64_t>(p.nqb) * p.batch);
+  const int64_t kseqs = std::min<int64_t>(p.total_k / 128 + p.batch, (int64_t{p.max_kv} + 127) / 128 * p.batch);
+  const int64_t window = p.window;
+  p.run = p.window > 0 ? tiles_of_cta(seqs * p.Hkv, DQ::CTAS, (window + p.QB) / DQ::KT + 1) : 1;
+  p.krun = p.window > 0 ? tiles_of_cta(kseqs * p.Hkv, 1, ((window + 127) / p.QB2 + 1) * p.chunks) : 1;
   p.nrun = (p.nqb + p.run - 1) / p.run;
+  const int64_t dkv_items = ((static_cast<int64_t>(p.max_kv) + 127) / 128 + p.krun - 1) / p.krun * per;
   const int64_t dq_items = p.total_q > 0 ? p.nrun * per : 0;
   p.sink_blocks = p.dsinks ? (dq_items ? static_cast<int>(back_sink_blocks(p.total_q, p.Hq)) : 1) : 0;
   if (std::max(dkv_items + p.sink_blocks, dq_items) >= (int64_t{1} << 31)) {
