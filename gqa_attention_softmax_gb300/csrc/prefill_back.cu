@@ -1159,8 +1159,9 @@ int set_smem(cudaError_t e) {
 
 // How many of `items` equal tiles a CTA goes through, `ctas` of them on an SM: the
 // number for which the last wave ends first, if a tile takes `steps` steps and a CTA
-// one more, to start and to end. 16,384 tokens of 64/8 heads of 64 in windows of
-// 128: dq TODO us at the TODO this gives, TODO at one; dk and dv TODO at TODO, TODO at one.
+// one more, to start and to end. 10,168 tokens of 64/8 heads of 64 in windows of
+// 128: dq 114 us with the 17 that this gives (150 with one), dk and dv 101 with 5
+// (113 with one).
 int tiles_of_cta(int64_t items, int ctas, int64_t steps) {
   int best = 1;
   int64_t least = 0;
@@ -1178,13 +1179,22 @@ int launch_back(BackParams& p, cudaStream_t stream) {
   using DQ = DqCfg<D>;
   // every size is checked, and every map made, before the first launch
   const int64_t per = static_cast<int64_t>(p.Hkv) * p.batch;
-  // Tiles of a CTA. Without a window the tiles differ in what they see, and one
-  // each, the longest first, fills the SMs best. With one they are alike and short.
-  const int64_t seqs = std::min<int64_t>(p.total_q / p.QB + p.batch, static_cast<int64_t>(p.nqb) * p.batch);
-  const int64_t kseqs = std::min<int64_t>(p.total_k / 128 + p.batch, (int64_t{p.max_kv} + 127) / 128 * p.batch);
+  // Tiles of a CTA. In windows that are short for their sequences all tiles see about
+  // as much. Else the longest come first, and the pass of dk and dv, whose tiles are long,
+  // takes one each (2 x 6000 tokens of 64/4 heads of 128: 2.83 ms with one, 3.37 with
+  // two), that of dq up to eight while they leave every place on an SM four runs (2.68 ms,
+  // 24 x 512 tokens 456 us; with one 2.83 and 557. 3,000 tokens of 24/8 heads, which
+  // leave too few: 64 us with one, 97 with eight). With equal shares in windows of a third
+  // of the sequences the same 12,000 tokens took 1.90 ms, 1.73 with one each.
+  const bool alike = p.window > 0 && p.window <= p.max_q / 8;
   const int64_t window = p.window;
-  p.run = p.window > 0 ? tiles_of_cta(seqs * p.Hkv, DQ::CTAS, (window + p.QB) / DQ::KT + 1) : 1;
-  p.krun = p.window > 0 ? tiles_of_cta(kseqs * p.Hkv, 1, ((window + 127) / p.QB2 + 1) * p.chunks) : 1;
+  const int64_t q_tiles =
+      p.Hkv * std::min<int64_t>(p.total_q / p.QB + p.batch, static_cast<int64_t>(p.nqb) * p.batch);
+  const int64_t k_tiles =
+      p.Hkv * std::min<int64_t>(p.total_k / 128 + p.batch, (int64_t{p.max_kv} + 127) / 128 * p.batch);
+  p.run = alike ? tiles_of_cta(q_tiles, DQ::CTAS, (window + p.QB) / DQ::KT + 1)
+                : static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, q_tiles / (4 * 152 * DQ::CTAS))));
+  p.krun = alike ? tiles_of_cta(k_tiles, 1, ((window + 127) / p.QB2 + 1) * p.chunks) : 1;
   p.nrun = (p.nqb + p.run - 1) / p.run;
   const int64_t dkv_items = ((static_cast<int64_t>(p.max_kv) + 127) / 128 + p.krun - 1) / p.krun * per;
   const int64_t dq_items = p.total_q > 0 ? p.nrun * per : 0;

@@ -142,6 +142,18 @@ def test_many_tokens_in_short_windows(shape, window):
 
 
 @gpu
+@pytest.mark.parametrize("shape", [(64, 8, 64), (16, 2, 128)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_many_tokens(shape, causal):
+    """Several query tiles a CTA without a window, and keys behind sequences of fewer queries."""
+    gen = torch.Generator().manual_seed(6)
+    lens = torch.randint(0, 300, (50,), generator=gen).tolist() + [0, 1, 1000]
+    more = torch.randint(0, 100, (53,), generator=gen).tolist()
+    x, h = make(lens, [a + b for a, b in zip(lens, more)], *shape, causal=causal)
+    check(call(x, h), x, h)
+
+
+@gpu
 @pytest.mark.parametrize("shape", [(8, 2, 64), (8, 2, 128)])
 def test_sinks_of_minus_infinity(shape):
     """Heads whose sink is -inf have none: dsinks 0. A row with lse -inf has no
