@@ -17,10 +17,17 @@
 //
 // A thread holds eight elements of one head, four whole pairs, so that the
 // rotation needs no exchange; d / 8 threads hold a head, a warp takes two or
-// four heads at a time and, where there are tokens enough, all heads of its token: the
-// cosines and the weights stay in registers, and no row needs more of an address than an addition.
-// A warp's rows are loaded four at a time. The mean squares and all arithmetic
-// between the loads and the stores are 32-bit; each output is rounded once.
+// four heads at a time and, where there are tokens enough, all heads of its
+// token: cosines and weights stay in registers. Rows come through a ring in
+// shared memory, three steps ahead of the arithmetic and the first ones before the
+// token's sequence is known: in registers, four rows a thread, too little was on
+// its way (82 us where the ring takes 71). The mean squares and all arithmetic between the
+// loads and the stores are 32-bit; each output is rounded once.
+//
+// All passes are bound by HBM. Measured, reads and writes together (copy: 6.78
+// TB/s): 12,000 tokens of 64 + 2 x 4 heads of 128 with norms, forward 71 us (6.2 TB/s),
+// backward 120 us (5.4 TB/s, with the weights' sums), 21,800 of them into e4m3 pages 121 us
+// (6.4 TB/s); 10,168 tokens of 64 + 2 x 8 heads of 64, backward without norms, 30 us.
 #include <algorithm>
 #include <cmath>
 
@@ -478,6 +485,8 @@ __device__ __forceinline__ void rotate_step_back(const RopeParams& p, const __nv
 // Gradients of the projection's rows; warps walk over the tokens (and shares
 // of them) with the grid's stride and leave their block's sums of the weights'
 // gradients in p.part.
+// With norms, two rows of dy and of x a thread at once take 110 registers and 16 KB of ring a
+// slot: two blocks an SM (120 us for 12,000 tokens of 64 + 2 x 4 heads of 128; one row each, three blocks: 146).
 template <int D, bool NORM>
 struct BackCfg {
   static constexpr int PER = 2;
@@ -697,7 +706,8 @@ int launched(const char* what, cudaError_t e) {
   return SINKATTN_CUDA_ERROR;
 }
 
-// Warps that share a token's heads: one, while that leaves every SM 16 warps.
+// Warps that share a token's heads: one, while that leaves every SM 16 warps. (37 tokens of
+// 64 + 2 x 8 heads of 64: 3.2 us.)
 int shares(int32_t tokens, int32_t Hq, int32_t Hkv, int d) {
   const int R = 256 / d, passes = (Hq + R - 1) / R + 2 * ((Hkv + R - 1) / R);
   int parts = 1;
