@@ -142,6 +142,18 @@ def test_many_tokens_in_short_windows(shape, window):
 
 
 @gpu
+@pytest.mark.parametrize("shape", [(16, 2, 64), (16, 2, 128)])
+def test_many_keys_that_no_query_sees(shape):
+    """A short window at the end of long sequences: key tiles without work before, between
+    and behind those with some, several of them a CTA."""
+    gen = torch.Generator().manual_seed(7)
+    lens = torch.randint(0, 400, (64,), generator=gen).tolist() + [0, 1, 700]
+    more = torch.randint(0, 900, (67,), generator=gen).tolist()
+    x, h = make(lens, [a + b for a, b in zip(lens, more)], *shape, window=30)
+    check(call(x, h), x, h)
+
+
+@gpu
 @pytest.mark.parametrize("shape", [(64, 8, 64), (16, 2, 128)])
 @pytest.mark.parametrize("causal", [True, False])
 def test_many_tokens(shape, causal):
@@ -353,6 +365,27 @@ def test_a_wait_that_runs_out_is_recorded(shape, tile, sinks):
     """A test hook shortens the waits to about 10 ms and leaves one tile's copies out."""
     x, h = make([700], [700], *shape, sinks=sinks)
     want = [t.clone() for t in call(x, h) if t is not None]
+    assert sa.sinkattn_debug_status() == 0
+    sa.sinkattn_debug_set_hooks(20_000_000, tile)
+    try:
+        call(x, h)
+        assert sa.sinkattn_debug_status() == TIMEOUT
+    finally:
+        sa.sinkattn_debug_set_hooks(0, -1)
+    for a, b in zip(want, call(x, h)):
+        assert torch.equal(a, b)
+    assert sa.sinkattn_debug_status() == 0
+
+
+@gpu
+@pytest.mark.parametrize("shape", [(16, 2, 64), (16, 2, 128)])
+@pytest.mark.parametrize("tile", [0, 5, 12])
+def test_a_wait_that_runs_out_among_several_tiles(shape, tile):
+    """As above, in CTAs that go through several tiles: the first CTA of dq has 7 query
+    tiles of one tile of keys each at d 64 and 14 at d 128, that of dk and dv key tiles of
+    159 and 128 queries, 10 and 8 tiles at d 64, 20 and 16 at d 128."""
+    x, h = make([256] * 64, [256] * 64, *shape, window=32)
+    want = [t.clone() for t in call(x, h)]
     assert sa.sinkattn_debug_status() == 0
     sa.sinkattn_debug_set_hooks(20_000_000, tile)
     try:
