@@ -16,7 +16,7 @@
 // S, warp 2 that of dP, warp 3 those that take P and dS, and groups of eight or sixteen
 // warps compute these, one thread per TMEM lane and 32 columns. A product is
 // seen by those who wait for it about 500 cycles after the tensor core has
-// done it, and a tile goes through three of them in turn. So tiles are small (64
+// done it, and a tile goes through three of them in turn. So tiles are small (64 or 128
 // columns), and TMEM holds as many of them on their way as fit beside the
 // accumulators; each kind of product has a warp of its own, because an issuing
 // warp's waits, MMAs and commits take 100 to 250 cycles each, one after the other.
