@@ -849,6 +849,9 @@ def sinkattn_prefill_backward_workspace_bytes(total_q, num_qo_heads) -> int:
     return int(n.value)
 
 
+_back_bytes = functools.lru_cache(maxsize=256)(sinkattn_prefill_backward_workspace_bytes)
+
+
 def _given_or_new(t, what, shape, dtype, dev, stream):
     if t is None:
         return _new(shape, dtype, dev, stream)
@@ -903,7 +906,7 @@ def sinkattn_prefill_backward(dout, q, k, v, out, lse, sinks, cu_seqlens_q, cu_s
     dv = _given_or_new(dv, "dv", k.shape, bf16, dev, stream)
     if sinks is not None:
         dsinks = _given_or_new(dsinks, "dsinks", (Hq,), f32, dev, stream)
-    need = sinkattn_prefill_backward_workspace_bytes(total_q, Hq)
+    need = _back_bytes(total_q, Hq)
     workspace = _workspace(workspace, need, dev, stream)
     _launch(dev, lib().sinkattn_prefill_backward, dout.data_ptr(), q.data_ptr(), k.data_ptr(),
             v.data_ptr(), out.data_ptr(), lse.data_ptr(),
@@ -1044,6 +1047,9 @@ def sinkattn_rope_qkv_backward_workspace_bytes(tokens, head_dim) -> int:
     return int(n.value)
 
 
+_rope_back_bytes = functools.lru_cache(maxsize=256)(sinkattn_rope_qkv_backward_workspace_bytes)
+
+
 def sinkattn_rope_qkv_backward(dq, dk, dv, cu_seqlens, rope, q=None, k=None, q_weight=None,
                                k_weight=None, eps=1e-6, positions=None, dq_in=None, dk_in=None,
                                dv_in=None, dq_weight=None, dk_weight=None, workspace=None,
@@ -1075,11 +1081,11 @@ def sinkattn_rope_qkv_backward(dq, dk, dv, cu_seqlens, rope, q=None, k=None, q_w
         ins[0] = _rope_rows(q, "q", dev, Hq, d, tokens)
     if k_weight is not None:
         ins[1] = _rope_rows(k, "k", dev, Hkv, d, tokens)
-    if dq_in is None or dk_in is None or dv_in is None:
+    given = (dq_in, dk_in, dv_in)
+    if any(t is None for t in given):
         rows = _new((tokens, Hq + 2 * Hkv, d), bf16, dev, stream)
-        dq_in = rows[:, :Hq] if dq_in is None else dq_in
-        dk_in = rows[:, Hq:Hq + Hkv] if dk_in is None else dk_in
-        dv_in = rows[:, Hq + Hkv:] if dv_in is None else dv_in
+        dq_in, dk_in, dv_in = [a if t is None else t
+                               for t, a in zip(given, rows.split((Hq, Hkv, Hkv), 1))]
     outs = [_rope_rows(t, what, dev, heads, d, tokens) for t, what, heads in (
         (dq_in, "dq_in", Hq), (dk_in, "dk_in", Hkv), (dv_in, "dv_in", Hkv))]
     if q_weight is not None:
@@ -1092,7 +1098,7 @@ def sinkattn_rope_qkv_backward(dq, dk, dv, cu_seqlens, rope, q=None, k=None, q_w
         raise SinkAttnError(INVALID_ARG, "dk_weight without k_weight")
     ws_p, ws_n = None, 0
     if q_weight is not None or k_weight is not None:
-        need = sinkattn_rope_qkv_backward_workspace_bytes(tokens, d)
+        need = _rope_back_bytes(tokens, d)
         workspace = _workspace(workspace, need, dev, stream)
         ws_p, ws_n = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _launch(dev, lib().sinkattn_rope_qkv_backward, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
