@@ -449,6 +449,7 @@ __device__ __forceinline__ void rotate_step_back(const RopeParams& p, const __nv
 #pragma unroll
   for (int u = 0; u < PER; ++u) {
     const int h = h0 + u * R;
+    const bool real = u < left && h < heads;   // (rows past the last are zeros)
     float2 a[2], b[2], y[2], z[2];
     unpack<LAYOUT>(load_row<LAYOUT>(slot + (u * R + s) * D, c, p.r), a, b);
 #pragma unroll
@@ -459,10 +460,11 @@ __device__ __forceinline__ void rotate_step_back(const RopeParams& p, const __nv
     if (NORM && normed) {
       float2 xa[2], xb[2], ua[2], ub[2];
       unpack<LAYOUT>(load_row<LAYOUT>(slot + (PER * R + u * R + s) * D, c, p.r), xa, xb);
-      const float rs = rsqrtf(head_sum<D>(dot_pairs(xa, xb, xa, xb)) * (1.f / D) + p.eps);
+      const float ms = head_sum<D>(dot_pairs(xa, xb, xa, xb)) * (1.f / D) + p.eps;
+      const float rs = real ? rsqrtf(ms) : 0.f;   // (without eps that of zeros is infinite, and 0 x inf NaN)
       const float2 rs2 = make_float2(rs, rs);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {   // (rows past the last have g = 0)
+      for (int e = 0; e < 2; ++e) {
         xa[e] = __fmul2_rn(xa[e], rs2);
         xb[e] = __fmul2_rn(xb[e], rs2);
         sum_a[e] = __ffma2_rn(y[e], xa[e], sum_a[e]);
@@ -478,7 +480,7 @@ __device__ __forceinline__ void rotate_step_back(const RopeParams& p, const __nv
         z[e] = __fmul2_rn(rs2, __ffma2_rn(xb[e], dot2, ub[e]));
       }
     }
-    if (u < left && h < heads) store(h, y, z);
+    if (real) store(h, y, z);
   }
 }
 

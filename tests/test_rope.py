@@ -278,6 +278,22 @@ def test_backward_of_many_tokens(T):
 
 
 @gpu
+@pytest.mark.parametrize("shape,lens", [((24, 8, 64), [70]), ((5, 1, 64), [70]), ((20, 4, 128), [70]),
+                                        ((64, 8, 64), [17, 40]), ((64, 8, 64), [1300]),
+                                        ((1, 1, 128), [5]), ((1, 1, 64), [3000])])
+@pytest.mark.parametrize("norms", [(True, True), (True, False), (False, True)])
+def test_eps_of_zero(shape, lens, norms, monkeypatch):
+    """Rows that are not zero have gradients without eps, the weights' among them, wherever a
+    token's heads do not fill the rows that a warp takes at once."""
+    monkeypatch.setitem(globals(), "EPS", 0.0)
+    x, rot, cu, T = make(lens, *shape, 64, False, *norms)
+    assert (x["q"] != 0).any(-1).all() and (x["k"] != 0).any(-1).all()
+    check_forward(forward(x), x, rot, cu, T)
+    g = grads(x, cu)
+    check_backward(backward(x, g), g, x, rot, cu)
+
+
+@gpu
 @pytest.mark.parametrize("norms", [(True, True), (False, False)])
 def test_backward_against_differences(norms):
     """sum(g * y) along random directions of the inputs: the slack is the sum of the elements'
