@@ -212,6 +212,15 @@ __device__ __forceinline__ int sequence_of(const int32_t* cu, int batch, int t) 
   return lo;
 }
 
+// Records cu_seqlens that leave [0, tokens] or decrease, entry by entry (a bad one need
+// not be where any token looks): thread `i` of `n`.
+__device__ __forceinline__ void check_sequences(const RopeParams& p, long long i, long long n) {
+  for (; i <= p.batch; i += n) {
+    const int at = p.cu[i];
+    if (at < 0 || at > p.tokens || (i > 0 && p.cu[i - 1] > at)) atomicExch(&g_status_rope, SINKATTN_BAD_LENGTHS);
+  }
+}
+
 template <bool APPEND>
 __device__ __forceinline__ Token token_of(const RopeParams& p, int t) {
   Token k{-1, 0, 0};
@@ -366,6 +375,7 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const RopeParams p) {
   for (int i = 0; i < kSlots - 1; ++i) issue(i);
 
   const Token at = token_of<KIND != kPack>(p, t);
+  if constexpr (KIND == kPack) check_sequences(p, unit * 32 + lane, static_cast<long long>(p.tokens) * p.parts * 32);
   if (KIND == kPack && at.row < 0) {
     wait_copies<0>();
     return;
@@ -598,6 +608,8 @@ __global__ void __launch_bounds__(kThreads, BackCfg<D, NORM>::BLOCKS) rope_backw
     }
   }
   wait_copies<0>();
+  check_sequences(p, static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x,
+                  static_cast<long long>(gridDim.x) * kThreads);
   if constexpr (NORM) {
     // the block's sums, over the threads that hold the same elements, in a fixed order
     __syncthreads();

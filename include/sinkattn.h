@@ -631,7 +631,9 @@ SINKATTN_API int sinkattn_rope_turns(const double* inv_freq, int32_t n, uint64_t
  *     eps) over the head's d elements before the rotation; NULL: no norm;
  *   q_out bf16 [tokens, Hq, d]; k_out, v_out bf16 ragged HND [Hkv * tokens, d].
  * Arithmetic is fp32, each output is rounded once. cu_seqlens that leave
- * [0, tokens] record SINKATTN_BAD_LENGTHS; the tokens concerned are left out.
+ * [0, tokens] or decrease record SINKATTN_BAD_LENGTHS; tokens of sequences that
+ * leave [0, tokens] are left out, those of sequences that overlap are undefined.
+ * (A call of no tokens or no sequences reads nothing, cu_seqlens neither.)
  */
 SINKATTN_API int sinkattn_rope_qkv(const void* q, const void* k, const void* v, int64_t q_stride,
                                    int64_t k_stride, int64_t v_stride, const int32_t* cu_seqlens,
@@ -650,7 +652,7 @@ SINKATTN_API int sinkattn_rope_qkv(const void* q, const void* k, const void* v, 
  * dq_weight, dk_weight fp32 [d] those of the weights, summed in an order that
  * does not depend on timing. workspace: sinkattn_rope_qkv_backward_workspace_bytes()
  * bytes, 256-byte aligned, needed where there is a norm. With no tokens the weights'
- * gradients are zero.
+ * gradients are zero. cu_seqlens are checked as there.
  */
 SINKATTN_API int sinkattn_rope_qkv_backward(
     const void* dq, const void* dk, const void* dv, const void* q, const void* k, int64_t q_stride,

@@ -508,6 +508,31 @@ def test_lengths_beyond_the_tokens_are_recorded():
     assert torch.equal(got[1][:60], want[1][:60])
 
 
+@gpu
+@pytest.mark.parametrize("bad", [[0, 40, 90], [0, 40, 90, 40], [-5, 30, 40], [50, 60, 70], [0, 30, 10, 40],
+                                 [0, -3], [-9, -3], [0] * 3000 + [41], [-1] + [0] * 3000 + [40]])
+def test_bad_lengths_that_no_token_meets_are_recorded(bad):
+    """Entries outside [0, 40], and ones that decrease, wherever they stand."""
+    x, rot, cu, T = make([30, 10], 8, 2, 64, 64)
+    g = grads(x, cu)
+    x["cu"] = torch.tensor(bad, dtype=torch.int32, device="cuda")
+    for step in (lambda: forward(x), lambda: backward(x, g),
+                 lambda: backward(dict(x, q_weight=None, k_weight=None), g)):
+        step()
+        assert sa.sinkattn_debug_status() == BAD_LENGTHS
+        assert sa.sinkattn_debug_status() == 0
+
+
+@gpu
+@pytest.mark.parametrize("good", [[0, 40], [0, 0, 17, 17, 40, 40], [3, 20], [0, 0], [40, 40], [0] * 3000 + [40]])
+def test_lengths_in_order_are_not_recorded(good):
+    x, rot, cu, T = make([30, 10], 8, 2, 64, 64)
+    g = grads(x, cu)
+    x["cu"] = torch.tensor(good, dtype=torch.int32, device="cuda")
+    forward(x), backward(x, g), backward(dict(x, q_weight=None, k_weight=None), g)
+    assert sa.sinkattn_debug_status() == 0
+
+
 # ----------------------------------------------------------------------------
 # refusals: nothing launches
 # ----------------------------------------------------------------------------
