@@ -82,9 +82,10 @@ __device__ __forceinline__ void sum_sinks(const BackParams& p, int blk, float (*
   constexpr int kSlices = kThreads / 32;
   const int lane = threadIdx.x % 32, slice = threadIdx.x / 32;
   int* last = reinterpret_cast<int*>(s + kSlices);
-  // (rows outside the sequences have no gradient)
+  // (rows outside the sequences have no gradient; where the bound says that there are no
+  // queries, the pass of dq, which leaves their numbers, has not run)
   const int t0 = max(blk * p.sink_tokens, p.cu_q[0]);
-  const int end = max(0, min(p.total_q, p.cu_q[p.batch]));
+  const int end = p.max_q > 0 ? max(0, min(p.total_q, p.cu_q[p.batch])) : 0;
   const int t1 = min(end - blk * p.sink_tokens, p.sink_tokens) + blk * p.sink_tokens;
   auto reduce = [&](int h, float x, float* to) {   // over the slices
     s[slice][lane] = x;
@@ -1205,7 +1206,9 @@ int launch_back(BackParams& p, cudaStream_t stream) {
                 : static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, q_tiles / (4 * 152 * DQ::CTAS))));
   p.krun = alike ? tiles_of_cta(k_tiles, 1, ((window + 127) / p.QB2 + 1) * p.chunks) : 1;
   p.nrun = (p.nqb + p.run - 1) / p.run;
-  const int64_t dkv_items = ((static_cast<int64_t>(p.max_kv) + 127) / 128 + p.krun - 1) / p.krun * per;
+  // (one tile where the bound says none: its CTAs see a sequence that has keys all the same)
+  const int64_t longest = std::max<int64_t>(1, (static_cast<int64_t>(p.max_kv) + 127) / 128);
+  const int64_t dkv_items = (longest + p.krun - 1) / p.krun * per;
   const int64_t dq_items = p.total_q > 0 ? p.nrun * per : 0;
   p.sink_blocks = p.dsinks ? (dq_items ? static_cast<int>(back_sink_blocks(p.total_q, p.Hq)) : 1) : 0;
   if (std::max(dkv_items + p.sink_blocks, dq_items) >= (int64_t{1} << 31)) {
@@ -1236,7 +1239,6 @@ int launch_back(BackParams& p, cudaStream_t stream) {
   }
   p.dkv_items = static_cast<int>(dkv_items);
   const dim3 grid(static_cast<unsigned>(dkv_items + p.sink_blocks));
-  if (grid.x == 0) return SINKATTN_OK;
   if (dq_items > 0)
     return launched("dk, dv", launch_chained(back_dkv_kernel<D>, grid, KV::THREADS, KV::SMEM, stream, tmQ2,
                                              tmDo2, tmK2, tmV2, p));

@@ -575,6 +575,8 @@ SINKATTN_API int sinkattn_pages_lists(const int32_t* table, int32_t num_pages, i
  * other sequences do not. A row whose lse is -inf has no weights: it gives and gets
  * no gradient. Each sequence needs Lq_b <= Lk_b. Lengths that contradict the host sizes record
  * SINKATTN_BAD_LENGTHS and leave that sequence's gradients and dsinks undefined.
+ * (A call of no keys, total_k = 0, or of no sequences reads nothing, cu_seqlens neither;
+ * dsinks is zero.)
  */
 SINKATTN_API int sinkattn_prefill_backward(
     const void* dout, const void* q, const void* k, const void* v, const void* out,

@@ -358,6 +358,27 @@ def test_lengths_that_contradict_the_sizes_are_recorded():
 
 
 @gpu
+@pytest.mark.parametrize("shape", [(8, 2, 64), (8, 2, 128)])
+def test_maxima_of_zero(shape):
+    """Sequences that have keys, or queries, although the bound says that there are none, are
+    recorded; without queries dsinks is zero whatever the workspace holds."""
+    x, h = make([50, 60], [50, 60], *shape)
+    cu = torch.tensor(h["cu_q"], dtype=torch.int32, device="cuda")
+    none = torch.zeros_like(cu)
+    args = [x[n] for n in ("dout", "q", "k", "v", "out", "lse", "sinks")]
+    for most in ((0, 0), (0, 60)):
+        ws = torch.full((1 << 20,), 0x40, dtype=torch.uint8, device="cuda")
+        got = sa.sinkattn_prefill_backward(*args, cu, cu, *most, 2, workspace=ws)
+        assert sa.sinkattn_debug_status() == BAD_LENGTHS
+        assert (got[3] == 0).all()
+    # nothing but rows behind the last sequence
+    outs = {n: torch.full_like(x[n[1:]], 7.0) for n in ("dq", "dk", "dv")}
+    got = sa.sinkattn_prefill_backward(*args, none, none, 0, 0, 2, **outs)
+    assert sa.sinkattn_debug_status() == 0
+    assert all((t == 7.0).all() for t in got[:3]) and (got[3] == 0).all()
+
+
+@gpu
 @pytest.mark.parametrize("shape", [(8, 1, 64), (8, 1, 128)])
 @pytest.mark.parametrize("tile", [0, 3])
 @pytest.mark.parametrize("sinks", [False, True])
