@@ -357,8 +357,9 @@ int sinkattn_prefill_backward(const void* dout, const void* q, const void* k, co
   }
   if (!dk || !dv || !aligned16(dk) || !aligned16(dv))
     return fail(SINKATTN_INVALID_ARG, "dk and dv must be non-null and 16-byte aligned");
-  if (!cu_seqlens_q || !cu_seqlens_k)
-    return fail(SINKATTN_INVALID_ARG, "cu_seqlens must be non-null");
+  if (!cu_seqlens_q || !cu_seqlens_k ||
+      ((reinterpret_cast<uintptr_t>(cu_seqlens_q) | reinterpret_cast<uintptr_t>(cu_seqlens_k)) & 3u))
+    return fail(SINKATTN_INVALID_ARG, "cu_seqlens must be non-null and 4-byte aligned");
   if (!no_q && (!dout || !out || !dq || !aligned16(dout) || !aligned16(out) || !aligned16(dq)))
     return fail(SINKATTN_INVALID_ARG, "dout, out and dq must be non-null and 16-byte aligned");
   if (!no_q && !lse) return fail(SINKATTN_INVALID_ARG, "lse must be non-null");

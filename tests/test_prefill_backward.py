@@ -452,6 +452,12 @@ def test_refusals(kw, status):
     assert sa.sinkattn_last_error() != ""
 
 
+@pytest.mark.parametrize("name", ["cu_q", "cu_k"])
+def test_misaligned_lengths_are_refused(name):
+    """(A kernel would read a word across its boundary.)"""
+    assert raw(**{name: A + 2}) == INVALID_ARG and "aligned" in sa.sinkattn_last_error()
+
+
 def test_workspace_bytes():
     n = sa.sinkattn_prefill_backward_workspace_bytes(100, 64)
     assert n >= 100 * 64 * 4 and n % 4 == 0
