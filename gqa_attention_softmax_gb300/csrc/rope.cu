@@ -9,11 +9,11 @@
 // factor. Backward: g = R^T dy, u = w * g, xh = x rs with rs = rsqrt(mean x^2 +
 // eps), dx = rs (u - xh mean(u xh)), dw = sum of g xh over tokens and heads.
 //
-// Angles. The frequencies come as turns per position in units of 2^-64, so
-// position * turns modulo 2^64 is the angle's fraction of a turn with an error
-// of at most |position| 2^-65 turns, whatever the position; its upper 32 bits
-// go to sincospif. A 32-bit product of position and frequency would be off by
-// up to 2^-24 |position| radians instead.
+// Angles. The frequencies come as turns per position in units of 2^-64, rounded
+// to the nearest, so position * turns modulo 2^64 is the angle's fraction of a
+// turn with an error of at most |position| 2^-65 turns, 2^-34 at the farthest; its upper
+// 32 bits go to sincospif, which takes 24 of them (2^-26 turns). A 32-bit product
+// of position and frequency would be off by up to 2^-24 |position| radians instead.
 //
 // A thread holds eight elements of one head, four whole pairs, so that the
 // rotation needs no exchange; d / 8 threads hold a head, a warp takes two or
@@ -862,9 +862,16 @@ int sinkattn_rope_turns(const double* inv_freq, int32_t n, uint64_t* turns) {
     if (!std::isfinite(inv_freq[i]))
       return refuse(SINKATTN_INVALID_ARG, "inv_freq must be finite");
   for (int i = 0; i < n; ++i) {
-    const double t = inv_freq[i] * 0.15915494309189533577;   // 1 / (2 pi)
-    const double part = t - std::floor(t);
-    turns[i] = part < 1.0 ? static_cast<uint64_t>(std::ldexp(part, 64)) : 0;
+    // f / (2 pi) as hi + lo: 1 / (2 pi) in two doubles, and the product's rounding (hi is an
+    // fma, so that no compiler takes the product unrounded into the difference below)
+    const double f = std::fabs(inv_freq[i]), c = 0x1.45f306dc9c883p-3, c_lo = -0x1.6b01ec5417056p-57;
+    const double hi = std::fma(f, c, 0.0), lo = std::fma(f, c_lo, std::fma(f, c, -hi));
+    // whole units of hi (its fraction is exact), then what is left of it and lo, rounded
+    const double units = std::ldexp(hi - std::floor(hi), 64), whole = std::floor(units);
+    const double rest = std::nearbyint(units - whole + std::ldexp(std::fmod(lo, 1.0), 64));
+    const uint64_t far = std::fabs(rest) < 0x1p64 ? static_cast<uint64_t>(std::fabs(rest)) : 0;
+    const uint64_t word = static_cast<uint64_t>(whole) + (rest < 0.0 ? uint64_t{0} - far : far);
+    turns[i] = inv_freq[i] < 0.0 ? uint64_t{0} - word : word;
   }
   return SINKATTN_OK;
 }

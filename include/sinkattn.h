@@ -596,8 +596,9 @@ SINKATTN_API int sinkattn_prefill_backward_workspace_bytes(int32_t total_q, int3
  * turned by the angle position * f_i and scaled by attention_factor; the other
  * elements stay as they are. The frequencies are passed as
  *   turns: uint64 [rotary_dim / 2] (device), f_i / (2 pi) modulo 1 in units of 2^-64,
- * so that an angle is exact at any int32 position (sinkattn_rope_turns makes
- * them from f_i in host memory).
+ * rounded to the nearest, so that position times turns is off by at most 2^-34
+ * turns at any int32 position (sinkattn_rope_turns makes them from f_i in host
+ * memory); cosine and sine are then fp32, of an angle rounded to 2^-26 turns.
  * sinkattn_rope_frequencies (host only) gives f_i = base^(-2i / rotary_dim) and
  * the factor of cosine and sine, scaled for contexts beyond the trained ones:
  *   SINKATTN_ROPE_PLAIN: as they are, attention_factor 1;

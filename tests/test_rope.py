@@ -10,6 +10,7 @@ means: 2^-16 A. The weights' gradients sum terms that carry 2^-16 each, in
 chains of less than 2^8 additions (2^-16 of the terms): 2^-15 A.
 """
 import math
+from fractions import Fraction
 
 import numpy as np
 import pytest
@@ -65,6 +66,22 @@ def test_turns():
         got = t / 2.0 ** 64
         off = abs(got - want)
         assert min(off, 1 - off) <= 2.0 ** -50 * max(1.0, abs(f)), f
+
+
+def test_turns_are_rounded_to_the_nearest_word():
+    """Against 1 / (2 pi) to 60 digits: half a unit of 2^-64, and where the frequency has f
+    turns a position 2^-100 f of them for the two-double product (2^-30 of a unit up to 2^6)."""
+    inv_2pi = Fraction("0.159154943091895335768883763372514362034459645740456448747667")
+    freq = [1.0, 0.3, -0.01, 1e-4, 7.5, -7.5, 0.0, 1e-18, 1e-30, 2 * math.pi, 63.9, -1e-19]
+    for scaling in ("none", "linear", "ntk", "yarn"):
+        freq += sa.sinkattn_rope_frequencies(128, 150000.0, scaling, 32.0, 4096)[0]
+    for f, t in zip(freq, sa.sinkattn_rope_turns(freq)):
+        assert 0 <= t < 2 ** 64
+        off = (Fraction(f) * inv_2pi * 2 ** 64 - t) % 2 ** 64
+        assert min(off, 2 ** 64 - off) <= Fraction(1, 2) + Fraction(1, 2 ** 30), f
+    # (whole turns and more are modulo 1, without an overflow on the way)
+    for f in (1e15, -3e18, 1e300, 1.7e308):
+        assert 0 <= sa.sinkattn_rope_turns([f])[0] < 2 ** 64
 
 
 @pytest.mark.parametrize("kw", [
