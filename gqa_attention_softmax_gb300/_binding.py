@@ -926,7 +926,9 @@ ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 def sinkattn_rope_frequencies(rotary_dim, base=10000.0, scaling="none", factor=1.0,
                               original_len=0, beta_fast=32.0, beta_slow=1.0):
     """(angles per position of the rotary_dim / 2 pairs, attention factor) of
-    plain, "linear", "ntk" or "yarn" scaled rotary positions; host arithmetic only."""
+    plain, "linear", "ntk" or "yarn" scaled rotary positions; host arithmetic only.
+    ("yarn" blends linearly in the pair's index, between borders that are not
+    rounded; Rope takes the frequencies of another rule as ``inv_freq``.)"""
     if isinstance(scaling, str) and scaling not in ROPE_SCALINGS:
         raise SinkAttnError(INVALID_ARG, "scaling must be one of %s" % ", ".join(ROPE_SCALINGS))
     code = ROPE_SCALINGS[scaling] if isinstance(scaling, str) else scaling

@@ -832,8 +832,8 @@ int sinkattn_rope_frequencies(int32_t rotary_dim, double base, int32_t scaling, 
                   "YaRN needs original_len of at least 1 and 0 < beta_slow < beta_fast");
   const double r = rotary_dim;
   if (scaling == SINKATTN_ROPE_NTK && rotary_dim > 2) base *= std::pow(factor, r / (r - 2.0));
-  // YaRN: pairs below `low` keep their frequency, pairs above `high` have it
-  // divided by the factor, those between are blended
+  // YaRN: pairs below `low` keep their frequency, pairs above `high` (which may be below
+  // the first) have it divided by the factor, those between are blended, linearly in the index
   double low = 0.0, high = 0.0;
   if (scaling == SINKATTN_ROPE_YARN) {
     const double pi2 = 6.283185307179586476925;
@@ -845,7 +845,8 @@ int sinkattn_rope_frequencies(int32_t rotary_dim, double base, int32_t scaling, 
     inv_freq[i] = f;
     if (scaling == SINKATTN_ROPE_LINEAR) inv_freq[i] = f / factor;
     if (scaling == SINKATTN_ROPE_YARN) {
-      const double ramp = std::min(1.0, std::max(0.0, (i - low) / std::max(high - low, 0.001)));
+      const double ramp =
+          i > high ? 1.0 : std::min(1.0, std::max(0.0, (i - low) / std::max(high - low, 0.001)));
       inv_freq[i] = f / factor * ramp + f * (1.0 - ramp);
     }
   }

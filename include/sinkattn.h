@@ -605,11 +605,17 @@ SINKATTN_API int sinkattn_prefill_backward_workspace_bytes(int32_t total_q, int3
  *   SINKATTN_ROPE_LINEAR: f_i / factor;
  *   SINKATTN_ROPE_NTK: base times factor^(r / (r - 2)), r = rotary_dim, which divides the
  *     lowest frequency by factor;
- *   SINKATTN_ROPE_YARN ("YaRN: Efficient Context Window Extension of Large
+ *   SINKATTN_ROPE_YARN (after "YaRN: Efficient Context Window Extension of Large
  *     Language Models", Peng et al., 2023): pairs that turn more than beta_fast
  *     times within original_len positions keep f_i, those that turn less than
- *     beta_slow times get f_i / factor, with a linear ramp over i between, and
- *     attention_factor = 0.1 ln(factor) + 1.
+ *     beta_slow times get f_i / factor; between, the share of f_i / factor grows
+ *     linearly with the pair's index i, from the index at which a pair turns
+ *     beta_fast times (0 at least) to that at which it turns beta_slow times
+ *     (rotary_dim - 1 at most), neither of them rounded. attention_factor =
+ *     0.1 ln(factor) + 1. This is the ramp of common model code, gpt-oss's among
+ *     it; the paper's is linear in the number of turns instead, and other model
+ *     code rounds the two indices outwards: for a model made with another rule
+ *     compute its f_i and pass those to sinkattn_rope_turns.
  */
 #define SINKATTN_ROPE_PLAIN 0
 #define SINKATTN_ROPE_LINEAR 1

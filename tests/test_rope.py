@@ -58,6 +58,29 @@ def test_scaled_frequencies():
     assert (np.diff(ratio) <= 1e-15).all() and ((ratio > 1 / 8 + 1e-9) & (ratio < 1 - 1e-9)).any()
 
 
+def test_yarn_between_the_borders():
+    """gpt-oss's constants: the borders are the indices 8.0927791 and 17.398024, the shares
+    between them written out."""
+    plain, _ = sa.sinkattn_rope_frequencies(64, 150000.0)
+    yarn, a = sa.sinkattn_rope_frequencies(64, 150000.0, "yarn", 32.0, 4096)
+    kept = {0: 1.0, 8: 1.0, 9: 0.9055510956043724, 10: 0.80144314790322064, 11: 0.69733520020206889,
+            12: 0.59322725250091713, 13: 0.48911930479976537, 14: 0.38501135709861361,
+            15: 0.28090340939746185, 16: 0.17679546169631009, 17: 0.072687513995158332,
+            18: 0.03125, 31: 0.03125}
+    for i, share in kept.items():
+        assert math.isclose(yarn[i] / plain[i], share, rel_tol=1e-12), i
+    assert math.isclose(yarn[10], 0.019335001126540358, rel_tol=1e-12)
+    assert math.isclose(a, 1.3465735902799727, rel_tol=1e-7)
+
+
+@pytest.mark.parametrize("r", [2, 64])
+def test_yarn_of_pairs_that_all_turn_less_than_the_slow_border(r):
+    """Five positions, of which the fastest pair makes 0.8 turns: every frequency is divided."""
+    plain, _ = sa.sinkattn_rope_frequencies(r, 10000.0)
+    yarn, _ = sa.sinkattn_rope_frequencies(r, 10000.0, "yarn", 8.0, 5)
+    assert np.allclose(np.array(yarn) / np.array(plain), 1 / 8, rtol=1e-12)
+
+
 def test_turns():
     """Turns are the frequency over 2 pi modulo 1 (of doubles: 2^-52 of the quotient)."""
     freq = [1.0, 0.5, 1e-4, 2 * math.pi * 3.25, -0.25 * 2 * math.pi, 0.0]
