@@ -957,31 +957,38 @@ class Rope:
     (2i, 2i + 1)). The frequencies are those of sinkattn_rope_frequencies, or
     ``inv_freq`` (a sequence of rotary_dim / 2 angles per position) with
     ``attention_factor``, which overrides the scaling's own where given. They
-    live on ``device``, so make the object once and keep it."""
-    __slots__ = ("_turns", "rotary_dim", "interleaved", "attention_factor", "inv_freq", "device")
+    live on ``device``, so make the object once and keep it; it does not change."""
+    __slots__ = ("_turns", "_args", "_inv_freq", "_device")
 
     def __init__(self, rotary_dim, base=10000.0, interleaved=False, scaling="none", factor=1.0,
                  original_len=0, beta_fast=32.0, beta_slow=1.0, inv_freq=None,
                  attention_factor=None, device="cuda"):
-        self.rotary_dim, = _i32(rotary_dim)
+        r, = _i32(rotary_dim)
         if inv_freq is None:
-            inv_freq, own = sinkattn_rope_frequencies(rotary_dim, base, scaling, factor,
-                                                      original_len, beta_fast, beta_slow)
+            inv_freq, own = sinkattn_rope_frequencies(r, base, scaling, factor, original_len,
+                                                      beta_fast, beta_slow)
         else:
             inv_freq, own = [float(x) for x in inv_freq], 1.0
-            if self.rotary_dim < 0 or 2 * len(inv_freq) != self.rotary_dim:
+            if r < 0 or 2 * len(inv_freq) != r:
                 raise SinkAttnError(INVALID_ARG, "inv_freq must have rotary_dim / 2 entries")
-        self.attention_factor = float(own if attention_factor is None else attention_factor)
-        if not math.isfinite(self.attention_factor):
+        own = float(own if attention_factor is None else attention_factor)
+        if not math.isfinite(own):
             raise SinkAttnError(INVALID_ARG, "attention_factor must be finite")
-        self.interleaved = bool(interleaved)
-        self.inv_freq = tuple(inv_freq)
+        self._inv_freq = tuple(inv_freq)
         # (int64 holds the unsigned words)
         words = [t - 2 ** 64 if t >= 2 ** 63 else t for t in sinkattn_rope_turns(inv_freq)]
         self._turns = torch.tensor(words or [0], dtype=torch.int64).to(device)
-        self.device = _need_cuda(self._turns, "device")
+        self._device = _need_cuda(self._turns, "device")
+        # what every entry point takes beside the words, whose number goes by the first (their
+        # address is asked for at each call: a copy of the object has words of its own)
+        self._args = (r, 1 if interleaved else 0, own)
 
     turns = property(lambda self: self._turns)
+    rotary_dim = property(lambda self: self._args[0])
+    interleaved = property(lambda self: bool(self._args[1]))
+    attention_factor = property(lambda self: self._args[2])
+    inv_freq = property(lambda self: self._inv_freq)
+    device = property(lambda self: self._device)
 
 
 def _rope_rows(t, what, dev, heads, d, tokens):
@@ -1010,13 +1017,12 @@ def _rope_common(q, k, v, rope, q_weight, k_weight, positions):
 
 
 def _rope_args(rope, q_weight, k_weight, positions, dev, d, tokens):
-    if not isinstance(rope, Rope) or rope.device != dev:
+    if not isinstance(rope, Rope) or rope._device != dev:
         raise SinkAttnError(INVALID_ARG, "rope must be a Rope on %s" % dev)
     qw, kw = [None if t is None else _need(t, what, torch.float32, dev, (d,))
               for t, what in ((q_weight, "q_weight"), (k_weight, "k_weight"))]
     pos = None if positions is None else _need(positions, "positions", torch.int32, dev, (tokens,))
-    return pos, (rope._turns.data_ptr(), rope.rotary_dim, 1 if rope.interleaved else 0,
-                 rope.attention_factor, qw, kw)
+    return pos, (rope._turns.data_ptr(), *rope._args, qw, kw)
 
 
 def sinkattn_rope_qkv(q, k, v, cu_seqlens, rope, q_weight=None, k_weight=None, eps=1e-6,

@@ -9,6 +9,7 @@ and products add a few 2^-24: 2^-17 A in all. Backward there are two such
 means: 2^-16 A. The weights' gradients sum terms that carry 2^-16 each, in
 chains of less than 2^8 additions (2^-16 of the terms): 2^-15 A.
 """
+import copy
 import math
 from fractions import Fraction
 
@@ -122,6 +123,33 @@ def test_turns_refusals():
     for bad in (float("nan"), float("inf")):
         with pytest.raises(sa.SinkAttnError):
             sa.sinkattn_rope_turns([1.0, bad])
+
+
+@pytest.mark.parametrize("name", ["rotary_dim", "interleaved", "attention_factor", "inv_freq", "turns",
+                                  "device"])
+def test_a_rope_does_not_change(name):
+    """(A rotary_dim that grew would send the kernels past the end of the words.)"""
+    rope = sa.Rope.__new__(sa.Rope)   # (a whole one needs a device)
+    with pytest.raises(AttributeError):
+        setattr(rope, name, 128)
+
+
+@gpu
+def test_rope_attributes():
+    rope = sa.Rope(64, base=150000.0, interleaved=True, scaling="yarn", factor=32.0, original_len=4096)
+    inv, a = sa.sinkattn_rope_frequencies(64, 150000.0, "yarn", 32.0, 4096)
+    assert rope.rotary_dim == 64 and rope.interleaved is True and rope.attention_factor == a
+    assert rope.inv_freq == tuple(inv) and rope.device == torch.device("cuda", torch.cuda.current_device())
+    assert [t % 2 ** 64 for t in rope.turns.tolist()] == sa.sinkattn_rope_turns(inv)
+    # a copy, as of a model that holds one, has words of its own
+    x, rot, cu, T = make([20], 8, 2, 64, 64)
+    want = forward(x)
+    twin = copy.deepcopy(x["rope"])
+    assert twin.turns.data_ptr() != x["rope"].turns.data_ptr()
+    x["rope"].turns.zero_()
+    x["rope"] = twin
+    for a, b in zip(want, forward(x)):
+        assert torch.equal(a, b)
 
 
 # ----------------------------------------------------------------------------
