@@ -338,6 +338,64 @@ def test_streams_and_graphs():
 
 
 @gpu
+@pytest.mark.parametrize("shape", [(64, 8, 64), (3, 1, 128), (24, 8, 64)])
+@pytest.mark.parametrize("tokens", [[1], [127], [128], [130, 3], [700, 1, 333]])
+def test_needs_no_more_workspace_than_it_says(tokens, shape):
+    """The queried bytes, between bytes of a pattern that stay as they are (blocks of
+    128, 2730 and 341 tokens sum the sinks' gradients)."""
+    x, h = make(tokens, tokens, *shape)
+    need = sa.sinkattn_prefill_backward_workspace_bytes(sum(tokens), shape[0])
+    whole = torch.full((need + 8192,), 0x5a, dtype=torch.uint8, device="cuda")
+    at = 4096 - whole.data_ptr() % 256
+    mine = whole[at:at + need]
+    assert mine.data_ptr() % 256 == 0
+    got = call(x, h, workspace=mine)
+    assert (whole[:at] == 0x5a).all() and (whole[at + need:] == 0x5a).all()
+    check(got, x, h)
+    for a, b in zip(got, call(x, h)):
+        assert torch.equal(a, b)
+    with pytest.raises(sa.SinkAttnError) as e:
+        call(x, h, workspace=mine[:-1])
+    assert e.value.status == INVALID_ARG and "needs %d" % need in str(e.value)
+
+
+@gpu
+@pytest.mark.parametrize("shape", [(34, 34, 64), (64, 2, 128)])
+def test_rows_past_32_bit_offsets(shape):
+    """Sequences of 64 tokens, the last ones' rows past 2^31 elements of q, dout, out and dq, and of
+    k, v, dk and dv too in the first shape (35 GB), against the 64-bit formula."""
+    hq, hkv, d = shape
+    n = 2 ** 31 // (64 * hq * d) + 12
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    r = lambda *s: torch.empty(s, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)   # noqa: E731
+    T = 64 * n
+    x = dict(q=r(T, hq, d), k=r(hkv * T, d), v=r(hkv * T, d), dout=r(T, hq, d),
+             sinks=torch.rand(hq, generator=gen, device="cuda") * 4 - 2)
+    h = dict(cu_q=list(range(0, T + 1, 64)), hkv=hkv, scale=d ** -0.5, causal=True, window=0)
+    h["cu_k"] = h["cu_q"]
+    assert x["q"].numel() > 2 ** 31 + 8 * 64 * hq * d
+    cu = torch.tensor(h["cu_q"], dtype=torch.int32, device="cuda")
+    x["out"], x["lse"] = sa.sinkattn_prefill(x["q"], x["k"], x["v"], x["sinks"], cu, cu, 64, 64, hkv)
+    got = call(x, h)
+    for a, b in ((0, 64), (T - 192, T)):
+        part = {m: x[m][a:b] for m in ("q", "dout", "out", "lse")}
+        part.update({m: x[m][hkv * a:hkv * b] for m in ("k", "v")}, sinks=None)
+        cut = list(range(0, b - a + 1, 64))
+        check((got[0][a:b], got[1][hkv * a:hkv * b], got[2][hkv * a:hkv * b], None), part,
+              dict(h, cu_q=cut, cu_k=cut))
+    weight = torch.exp(x["sinks"].double() - x["lse"].double())
+    want = torch.zeros(hq, dtype=torch.float64, device="cuda")
+    size = torch.zeros_like(want)
+    for a in range(0, T, 1 << 16):
+        terms = x["dout"][a:a + (1 << 16)].double() * x["out"][a:a + (1 << 16)].double()
+        want -= (weight[a:a + (1 << 16)] * terms.sum(-1)).sum(0)
+        size += (weight[a:a + (1 << 16)] * terms.abs().sum(-1)).sum(0)
+    # terms as in tests/_gradient_model.py; up to 240 rows a block and 4,116 blocks, each in 20
+    # slices: chains of at most 12 + 20 + 206 + 20 additions, 2^-15 of the terms
+    assert ((got[3].double() - want).abs() <= (2.0 ** -12 + 2.0 ** -15) * size).all()
+
+
+@gpu
 def test_lengths_that_contradict_the_sizes_are_recorded():
     x, h = make([50, 60], [50, 60], 8, 2, 64)
     cu = torch.tensor(h["cu_q"], dtype=torch.int32, device="cuda")

@@ -576,6 +576,100 @@ def test_lengths_beyond_the_tokens_are_recorded():
     assert torch.equal(got[1][:60], want[1][:60])
 
 
+def in_a_field(n):
+    """n bytes, 256-byte aligned, between bytes of a pattern, and a check that these are as they were."""
+    whole = torch.full((n + 8192,), 0x5a, dtype=torch.uint8, device="cuda")
+    at = 4096 - whole.data_ptr() % 256
+    mine = whole[at:at + n]
+    assert mine.data_ptr() % 256 == 0
+
+    def untouched():
+        return bool((whole[:at] == 0x5a).all() and (whole[at + n:] == 0x5a).all())
+    return mine, untouched
+
+
+@gpu
+@pytest.mark.parametrize("T", [1, 5, 303, 304, 305, 5000])
+@pytest.mark.parametrize("shape", [(64, 8, 64), (20, 4, 128)])
+def test_backward_needs_no_more_workspace_than_it_says(T, shape):
+    x, rot, cu, _ = make([T], *shape, 64)
+    g = grads(x, cu)
+    need = sa.sinkattn_rope_qkv_backward_workspace_bytes(T, shape[2])
+    mine, untouched = in_a_field(need)
+    got = backward(x, g, workspace=mine)
+    assert untouched()
+    check_backward(got, g, x, rot, cu)
+    for a, b in zip(got, backward(x, g)):
+        assert torch.equal(a, b)
+    with pytest.raises(sa.SinkAttnError) as e:
+        backward(x, g, workspace=mine[:-1])
+    assert e.value.status == INVALID_ARG and "too small" in str(e.value)
+
+
+@gpu
+@pytest.mark.parametrize("norms", [(True, True), (False, False)])
+def test_rows_past_32_bit_offsets(norms):
+    """Every array of the packed form and of its backward pass has more than 2^31 elements
+    (540,000 tokens of 3 x 32 heads of 128: 40 GB)."""
+    T, hq, d = 540000, 32, 128
+    assert T * hq * d > 2 ** 31
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    rows = torch.empty((T, 3 * hq, d), dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+    w = [1 + 0.3 * torch.randn(d, generator=gen, device="cuda") if n else None for n in norms]
+    rope = sa.Rope(d, base=150000.0)
+    cu = [0, T - 130, T - 3, T]
+    x = dict(q=rows[:, :hq], k=rows[:, hq:2 * hq], v=rows[:, 2 * hq:], q_weight=w[0], k_weight=w[1],
+             rope=rope, cu=torch.tensor(cu, dtype=torch.int32, device="cuda"), positions=None)
+    at = torch.cat([torch.arange(20), torch.arange(T - 150, T)]).cuda()
+    pos = torch.cat([torch.arange(20), torch.arange(T - 150, T - 130), torch.arange(127),
+                     torch.arange(3)]).cuda()
+    rot = Rotation(rope.inv_freq, 1.0, False, pos)
+    # ragged HND rows of those tokens' heads
+    start = torch.tensor(cu, device="cuda")
+    b = torch.searchsorted(start, at, right=True) - 1
+    hnd = (hq * start[b] + at - start[b])[:, None] + torch.arange(hq, device="cuda")[None, :] * (
+        start[b + 1] - start[b])[:, None]
+    assert hnd.max() * d > 2 ** 31
+    q, k, v = forward(x)
+    close(q[at], *rotated(x["q"][at], w[0], EPS, rot), "q")
+    close(k[hnd], *rotated(x["k"][at], w[1], EPS, rot), "k")
+    assert torch.equal(v[hnd], x["v"][at])
+    got = backward(x, (q, k, v))
+    for name, dx, dy in (("q", got[0], q[at]), ("k", got[1], k[hnd])):
+        val, size, _, _ = rotated_gradients(dy, x[name][at], x[name + "_weight"], EPS, rot)
+        close(dx[at], val, size, "d" + name, of=2.0 ** -16)
+    assert torch.equal(got[2][at], x["v"][at])
+
+
+@gpu
+@pytest.mark.parametrize("fp8", [False, True])
+def test_pools_past_32_bit_offsets(fp8):
+    """The last pages of pools of more than 2^31 elements (bf16: 2 x 4.4 GB)."""
+    hq, hkv, d, page, T = 8, 4, 128, 64, 70
+    pages = 2 ** 31 // (hkv * page * d) + 70
+    x, rot, _, _ = make([T], hq, hkv, d, 128, positions=list(range(T)))
+    slots = (torch.arange(T) * page + torch.arange(T) % page + (pages - T) * page).int().cuda()
+    pools = [torch.zeros((pages, hkv, page, d), dtype=torch.uint8 if fp8 else torch.bfloat16,
+                         device="cuda") for _ in range(2)]
+    args = (x["q"], x["k"], x["v"], x["positions"], slots, x["rope"])
+    if fp8:
+        scales = [torch.full((hkv,), 5 / 448, device="cuda") for _ in range(2)]
+        sa.sinkattn_rope_append_paged_fp8(*args, *scales, *pools, x["q_weight"], x["k_weight"], EPS)
+    else:
+        sa.sinkattn_rope_append_paged(*args, *pools, x["q_weight"], x["k_weight"], EPS)
+    # as into a small pool
+    small = [torch.zeros((T, hkv, page, d), dtype=p.dtype, device="cuda") for p in pools]
+    low = slots - (pages - T) * page
+    args = (*args[:4], low, x["rope"])
+    if fp8:
+        sa.sinkattn_rope_append_paged_fp8(*args, *scales, *small, x["q_weight"], x["k_weight"], EPS)
+    else:
+        sa.sinkattn_rope_append_paged(*args, *small, x["q_weight"], x["k_weight"], EPS)
+    for p, want in zip(pools, small):
+        assert want.any() and torch.equal(p[-T:], want)
+        assert not p[:-T].any()
+
+
 @gpu
 @pytest.mark.parametrize("bad", [[0, 40, 90], [0, 40, 90, 40], [-5, 30, 40], [50, 60, 70], [0, 30, 10, 40],
                                  [0, -3], [-9, -3], [0] * 3000 + [41], [-1] + [0] * 3000 + [40]])
