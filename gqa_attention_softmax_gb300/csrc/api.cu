@@ -365,7 +365,8 @@ int sinkattn_prefill_backward(const void* dout, const void* q, const void* k, co
   if (!no_q && !lse) return fail(SINKATTN_INVALID_ARG, "lse must be non-null");
   size_t need = 0;
   if ((rc = sinkattn_prefill_backward_workspace_bytes(total_q, num_qo_heads, &need))) return rc;
-  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+  // (without queries it takes no bytes, and none are looked at)
+  if (need > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)))
     return fail(SINKATTN_INVALID_ARG, "workspace must be non-null and 256-byte aligned");
   if (workspace_bytes < need)
     return fail(SINKATTN_INVALID_ARG, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
@@ -378,11 +379,13 @@ int sinkattn_prefill_backward(const void* dout, const void* q, const void* k, co
   a.Hq = num_qo_heads; a.Hkv = num_kv_heads; a.d = head_dim;
   a.sm_scale = sm_scale; a.causal = causal; a.window = window;
   a.dq = dq; a.dk = dk; a.dv = dv; a.dsinks = dsinks;
-  char* ws = static_cast<char*>(workspace);
-  a.nlse = reinterpret_cast<float*>(ws);
-  a.ndelta = reinterpret_cast<float*>(ws + back_row_bytes(total_q, num_qo_heads));
-  a.sink_count = reinterpret_cast<int*>(ws + 2 * back_row_bytes(total_q, num_qo_heads));
-  a.sink_part = reinterpret_cast<float*>(ws + 2 * back_row_bytes(total_q, num_qo_heads) + 256);
+  if (need > 0) {
+    char* ws = static_cast<char*>(workspace);
+    a.nlse = reinterpret_cast<float*>(ws);
+    a.ndelta = reinterpret_cast<float*>(ws + back_row_bytes(total_q, num_qo_heads));
+    a.sink_count = reinterpret_cast<int*>(ws + 2 * back_row_bytes(total_q, num_qo_heads));
+    a.sink_part = reinterpret_cast<float*>(ws + 2 * back_row_bytes(total_q, num_qo_heads) + 256);
+  }
   return launch_prefill_back(a, s);
 }
 

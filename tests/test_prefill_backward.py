@@ -360,6 +360,17 @@ def test_needs_no_more_workspace_than_it_says(tokens, shape):
 
 
 @gpu
+@pytest.mark.parametrize("shape", [(8, 2, 64), (8, 2, 128)])
+def test_no_queries_need_no_workspace(shape):
+    """(The query says 0 bytes, for which a caller may have no address.)"""
+    x, h = make([0, 0], [33, 200], *shape)
+    assert sa.sinkattn_prefill_backward_workspace_bytes(0, shape[0]) == 0
+    outs = {n: torch.full_like(x[n[1:]], 7.0) for n in ("dk", "dv")}
+    got = call(x, h, workspace=torch.empty(0, dtype=torch.uint8, device="cuda"), **outs)
+    assert all((t == 0).all() for t in got[1:])
+
+
+@gpu
 @pytest.mark.parametrize("shape", [(34, 34, 64), (64, 2, 128)])
 def test_rows_past_32_bit_offsets(shape):
     """Sequences of 64 tokens, the last ones' rows past 2^31 elements of q, dout, out and dq, and of
@@ -514,6 +525,12 @@ def test_refusals(kw, status):
 def test_misaligned_lengths_are_refused(name):
     """(A kernel would read a word across its boundary.)"""
     assert raw(**{name: A + 2}) == INVALID_ARG and "aligned" in sa.sinkattn_last_error()
+
+
+def test_no_queries_need_no_workspace_address():
+    """The call gets past it, as far as the work items, of which these sizes have too many."""
+    assert raw(total_q=0, max_q=0, ws=None, n=0, batch=65535, hkv=4, hq=4, total_k=1 << 24,
+               max_k=1 << 24) == UNSUPPORTED
 
 
 def test_workspace_bytes():
