@@ -158,12 +158,18 @@ __device__ __forceinline__ bool try_wait_for(uint64_t* bar, uint32_t parity, uin
 
 // Between two tries of a wait that began at `since` (0: now): -1 where it is to be
 // given up, because another warp has, or because its time is over, else when it
-// began. (Out of line: the loops of the issuing warps are short, and what they
-// fetch of their instructions is what they cost.)
+// began. The time is for a part that has failed, so it does not begin while the
+// launch before still runs: what dk and dv wait for in the end may be that. (Here it
+// costs nothing when the first try succeeds; before the waits, in every warp, the
+// smallest call took 11.3 us instead of 10.7.) Out of line: the loops of the issuing
+// warps are short, and what they fetch of their instructions is what they cost.
 __device__ __noinline__ long long give_up(long long since, volatile int* abort_flag, int* status) {
   if (*abort_flag) return -1;
+  if (since == 0) {
+    grid_dependency_wait();
+    return clock64();
+  }
   const long long now = clock64();
-  if (since == 0) return now;
   if (now - since <= g_wait_limit_cycles) return since;
   *abort_flag = 1;
   atomicExch(status, SINKATTN_TIMEOUT);

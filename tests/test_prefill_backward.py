@@ -488,6 +488,31 @@ def test_a_wait_that_runs_out_among_several_tiles(shape, tile):
     assert sa.sinkattn_debug_status() == 0
 
 
+@gpu
+@pytest.mark.parametrize("d,limit", [(64, 100_000), (128, 160_000)])
+def test_no_wait_runs_out_while_the_first_pass_runs(d, limit):
+    """150 query tiles, one an SM: as the short ones end, CTAs of dk and dv come and have to
+    wait for the longest, 300 tiles of keys (100 us and more). The limit, half of that, is
+    that of a wait within a pass, whose tiles take about 1 us each."""
+    T = 19200
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    r = lambda *s: torch.randn(s, generator=gen, device="cuda").to(torch.bfloat16)   # noqa: E731
+    x = dict(q=r(T, 1, d), k=r(T, d), v=r(T, d), dout=r(T, 1, d), sinks=torch.zeros(1, device="cuda"))
+    cu = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    x["out"], x["lse"] = sa.sinkattn_prefill(x["q"], x["k"], x["v"], x["sinks"], cu, cu, T, T, 1)
+    h = dict(cu_q=[0, T], cu_k=[0, T], hkv=1, scale=d ** -0.5, causal=True, window=0)
+    want = call(x, h)
+    assert sa.sinkattn_debug_status() == 0
+    sa.sinkattn_debug_set_hooks(limit, -1)
+    try:
+        got = call(x, h)
+        assert sa.sinkattn_debug_status() == 0
+    finally:
+        sa.sinkattn_debug_set_hooks(0, -1)
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+
+
 # ----------------------------------------------------------------------------
 # refusals: nothing launches
 # ----------------------------------------------------------------------------
