@@ -874,7 +874,9 @@ def sinkattn_prefill_backward(dout, q, k, v, out, lse, sinks, cu_seqlens_q, cu_s
     """Gradients of sinkattn_prefill: dout bf16 [total_q, Hq, d] is that of
     out, dlse fp32 [total_q, Hq] (or None) that of lse; out and lse are what
     the forward call returned for the same q, k, v, sinks. Returns (dq, dk, dv,
-    dsinks), bf16 in the inputs' layouts and fp32 [Hq] (None without sinks)."""
+    dsinks), bf16 in the inputs' layouts and fp32 [Hq] (None without sinks). Rows
+    behind the last sequence are not written: give zeroed tensors where a padded
+    batch's gradients go on."""
     dev = _need_cuda(q, "q")
     bf16, f32, i32 = torch.bfloat16, torch.float32, torch.int32
     _need(q, "q", bf16, dev, 3)
@@ -1032,7 +1034,8 @@ def sinkattn_rope_qkv(q, k, v, cu_seqlens, rope, q_weight=None, k_weight=None, e
     token stride that is a multiple of 8) are normed per head (q_weight,
     k_weight fp32 [d]; None: not), q and k rotated by ``rope`` at ``positions``
     (int32 [tokens]; None: the index in the sequence). Returns (q [tokens, Hq,
-    d], k, v ragged HND [Hkv * tokens, d])."""
+    d], k, v ragged HND [Hkv * tokens, d]); rows behind the last sequence are not
+    written."""
     dev, tokens, Hq, Hkv, d, rows, pos, args = _rope_common(q, k, v, rope, q_weight, k_weight,
                                                             positions)
     cu = _need(cu_seqlens, "cu_seqlens", torch.int32, dev, 1)
@@ -1066,7 +1069,8 @@ def sinkattn_rope_qkv_backward(dq, dk, dv, cu_seqlens, rope, q=None, k=None, q_w
     [tokens, Hq, d], dk and dv ragged HND. q and k, its inputs, are read where
     they are normed. Returns (dq_in, dk_in, dv_in, dq_weight, dk_weight); by default the
     first three are slices of one [tokens, (Hq + 2 Hkv) * d] gradient of the
-    projection's output."""
+    projection's output. Rows behind the last sequence are not written: give zeroed
+    tensors where a padded batch's gradients go on."""
     dev = _need_cuda(dq, "dq")
     bf16, f32 = torch.bfloat16, torch.float32
     _need(dq, "dq", bf16, dev, 3)
@@ -1153,7 +1157,8 @@ def sinkattn_rope_append_paged_fp8(q, k, v, positions, slots, rope, k_scale, v_s
                                    v_pages, q_weight=None, k_weight=None, eps=1e-6, q_out=None,
                                    stream=None):
     """sinkattn_rope_append_paged into pools of e4m3 codes (uint8): the code
-    nearest to the rotated key / scale[head] (ties to even, saturating at 448)."""
+    nearest to the fp32 quotient of the rotated key and scale[head] (ties to even,
+    saturating at 448)."""
     return _rope_append(lib().sinkattn_rope_append_paged_fp8, torch.uint8, (k_scale, v_scale), q, k,
                         v, positions, slots, rope, k_pages, v_pages, q_weight, k_weight, eps,
                         q_out, stream)

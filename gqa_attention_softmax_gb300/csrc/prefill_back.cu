@@ -24,10 +24,11 @@
 // unrounded. Every wait is bounded; on a timeout the CTA records
 // SINKATTN_TIMEOUT, drains its copies and MMAs, frees TMEM and exits.
 //
-// Measured (full causal): 10,168 tokens of 64/8 heads of 64 in four sequences, dq
-// 345 us and dk, dv 398 (71 and 64 % of the tensor core's time; 812 TFLOP/s of the
-// formulas' five products for the call); 2 x 6000 tokens of 64/4 heads of 128, 1133 and 1525 us
-// (89 and 95 %, 1.0 PFLOP/s). What bounds them: at d 128 the tensor core, where
+// Measured (full causal): 10,168 tokens of 64/8 heads of 64 in four sequences 759 us (837
+// TFLOP/s of the formulas' five products); 2 x 6000 tokens of 64/4 heads of 128 2.73 to 2.89 ms
+// (1.02 to 1.08 PFLOP/s), as the power limit allows: calls in a graph, one behind the other.
+// Each pass alone, under the profiler: dq 346 us and dk, dv 400 (71 and 64 % of the tensor core's
+// time); 1133 and 1525 us (89 and 95 %). What bounds them: at d 128 the tensor core, where
 // an MMA of 64 columns takes as long as one of 128 (a tile of 128 columns has no
 // room for a second buffer); at d 64 the chain of a tile's products and of P and dS.
 // dq in tiles of 128 keys, one CTA an SM, took 450 us at d 64 and 1240 at d 128
@@ -1201,7 +1202,10 @@ int launch_back(BackParams& p, cudaStream_t stream) {
   // two), that of dq up to eight while they leave every place on an SM four runs (2.68 ms,
   // 24 x 512 tokens 456 us; with one 2.83 and 557. 3,000 tokens of 24/8 heads, which
   // leave too few: 64 us with one, 97 with eight). With equal shares in windows of a third
-  // of the sequences the same 12,000 tokens took 1.90 ms, 1.73 with one each.
+  // of the sequences the same 12,000 tokens took 1.90 ms, 1.73 with one each. (All of these in
+  // short bursts, before the power limit.) At the border between the two rules, 10,168 tokens
+  // of 64/8 heads of 64 in sequences of up to 4096: windows of 512 take 368 us with equal
+  // shares, of 513 347 without; of 128, 212 and of 256, 264.
   const bool alike = p.window > 0 && p.window <= p.max_q / 8;
   const int64_t window = p.window;
   const int64_t q_tiles =
@@ -1265,7 +1269,7 @@ int launch_prefill_back(const BackArgs& a, cudaStream_t stream) {
   p.lse = a.lse; p.sinks = a.sinks; p.dlse = a.dlse;
   p.cu_q = a.cu_q; p.cu_k = a.cu_k;
   p.batch = a.batch; p.total_q = a.total_q; p.total_k = a.total_k;
-  p.max_q = std::min(a.max_q, a.total_q);   // (bounds may be far above what there is)
+  p.max_q = std::min(a.max_q, a.total_q);   // (a bound may be above what there is)
   p.max_kv = std::min(a.max_kv, a.total_k);
   p.Hq = a.Hq; p.Hkv = a.Hkv; p.G = a.Hq / a.Hkv;
   p.sm_scale = a.sm_scale; p.scale_log2 = a.sm_scale * kLog2e;

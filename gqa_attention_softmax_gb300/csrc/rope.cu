@@ -22,12 +22,19 @@
 // shared memory, three steps ahead of the arithmetic and the first ones before the
 // token's sequence is known: in registers, four rows a thread, too little was on
 // its way (82 us where the ring takes 71). The mean squares and all arithmetic between the
-// loads and the stores are 32-bit; each output is rounded once.
+// loads and the stores are 32-bit; each output is rounded once. The weight is multiplied into
+// cosine and sine once for all heads, and the inverse root comes last: a multiplication
+// an element fewer, in another order than the formula's, which bf16 outputs do not show and which
+// moves an e4m3 code now and then where the quotient lies next to the middle of two.
 //
-// All passes are bound by HBM. Measured, reads and writes together (copy: 6.78
-// TB/s): 12,000 tokens of 64 + 2 x 4 heads of 128 with norms, forward 71 us (6.2 TB/s),
-// backward 120 us (5.4 TB/s, with the weights' sums), 21,800 of them into e4m3 pages 121 us
-// (6.4 TB/s); 10,168 tokens of 64 + 2 x 8 heads of 64, backward without norms, 30 us.
+// All passes are bound by HBM. Measured, several calls in a graph, reads and writes together
+// (copy: 6.78 TB/s): 12,000 tokens of 64 + 2 x 4 heads of 128 with norms, forward 71 to 77 us
+// (by where the buffers lie; 6.2 to 5.8 TB/s), backward 120.6 us (5.4 TB/s, with the weights' sums),
+// 21,800 of them into e4m3 pages 121 us (6.4 TB/s); 10,168 tokens of 64 + 2 x 8 heads of 64,
+// backward without norms, 33.7 us (6.2 TB/s). Interleaved pairs and a rotation of half a head take
+// the same. The half layout with a rotary_dim that is no multiple of 8 does not: no thread's four
+// pairs lie in whole words, so elements come from the ring and go to memory one by one. With 100
+// of the 128 rotated: forward 139 us, backward 171, e4m3 pages 268; with 38 of 64, backward 75.
 #include <algorithm>
 #include <cmath>
 
