@@ -32,8 +32,8 @@
 // (by where the buffers lie; 6.2 to 5.8 TB/s), backward 120.6 us (5.4 TB/s, with the weights' sums),
 // 21,800 of them into e4m3 pages 121 us (6.4 TB/s); 10,168 tokens of 64 + 2 x 8 heads of 64,
 // backward without norms, 33.7 us (6.2 TB/s). Interleaved pairs and a rotation of half a head take
-// the same. The half layout with a rotary_dim that is no multiple of 8 does not: no thread's four
-// pairs lie in whole words, so elements come from the ring and go to memory one by one. With 100
+// the same. The half layout with a rotary_dim that is no multiple of 8 does not: a thread's four
+// pairs then straddle words, so elements come from the ring and go to memory one by one. With 100
 // of the 128 rotated: forward 139 us, backward 171, e4m3 pages 268; with 38 of 64, backward 75.
 #include <algorithm>
 #include <cmath>
