@@ -34,9 +34,10 @@
 // backward without norms, 33.7 us (6.2 TB/s). Interleaved pairs and a rotation of half a head take
 // the same. The half layout with a rotary_dim that is no multiple of 8 does not: a thread's four
 // pairs then straddle words, so elements come from the ring and go to memory one by one. With 100
-// of the 128 rotated: forward 139 us, backward 171, e4m3 pages 268; with 38 of 64, backward 75.
+// of the 128 rotated: forward 138 us, backward 171, e4m3 pages 264; with 38 of 64, backward 71.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "chain.cuh"
 #include "common.cuh"
@@ -274,6 +275,17 @@ __device__ __forceinline__ void angles(const RopeParams& p, int pos, int c, floa
   si[0] = make_float2(y[0], y[1]), si[1] = make_float2(y[2], y[3]);
 }
 
+// Thread c's pairs past the rotated ones as they were: by 1 and 0 an infinity would make its
+// partner NaN. (Not under a norm, which lets no element stay as it is.)
+__device__ __forceinline__ void keep_rest(int c, int r, const float2 (&a)[2], const float2 (&b)[2],
+                                          float2 (&y)[2], float2 (&z)[2]) {
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    if (4 * c + 2 * e >= r / 2) y[e].x = a[e].x, z[e].x = b[e].x;
+    if (4 * c + 2 * e + 1 >= r / 2) y[e].y = a[e].y, z[e].y = b[e].y;
+  }
+}
+
 // Thread c's eight weights (1 without a norm).
 template <int LAYOUT>
 __device__ __forceinline__ void load_weights(const float* w, int c, int r, float2 (&a)[2], float2 (&b)[2]) {
@@ -313,7 +325,9 @@ __device__ __forceinline__ void wait_copies() {
 }
 
 // Norm and rotation of a step's rows, from the ring; h0 is this thread's head in the first pass.
-template <int D, int LAYOUT, int PER, typename Store>
+// REST: rows without a norm of which a part is not rotated. (Kernels of their own: the choice among
+// the elements took 3 % of every other pass, and as a path of the same kernel up to 2 %.)
+template <int D, int LAYOUT, int PER, bool REST, typename Store>
 __device__ __forceinline__ void rotate_step(const RopeParams& p, const __nv_bfloat16* slot, int h0, int left,
                                             int heads, bool normed, const float2 (&ca)[2], const float2 (&sb)[2],
                                             const float2 (&cb)[2], const float2 (&sa)[2], int c, int s,
@@ -329,7 +343,8 @@ __device__ __forceinline__ void rotate_step(const RopeParams& p, const __nv_bflo
       y[e] = __ffma2_rn(a[e], ca[e], __fmul2_rn(b[e], sb[e]));
       z[e] = __ffma2_rn(b[e], cb[e], __fmul2_rn(a[e], sa[e]));
     }
-    if (normed) {
+    if constexpr (REST) keep_rest(c, p.r, a, b, y, z);
+    if (!REST && normed) {
       const float rs = rsqrtf(head_sum<D>(dot_pairs(a, b, a, b)) * (1.f / D) + p.eps);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
@@ -341,7 +356,7 @@ __device__ __forceinline__ void rotate_step(const RopeParams& p, const __nv_bflo
   }
 }
 
-template <int D, int LAYOUT, int KIND>
+template <int D, int LAYOUT, int KIND, bool REST>
 __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const RopeParams p) {
   constexpr int C = D / 8, R = 32 / C;   // threads of a head, heads of a pass
   constexpr int PER = 2;
@@ -405,31 +420,37 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const RopeParams p) {
       cb[e] = __fmul2_rn(wb[e], co[e]);
       sb[e] = neg2(__fmul2_rn(wb[e], si[e]));
     }
-    if (seg == 0) {
-      __nv_bfloat16* q_out = p.q_out + static_cast<long long>(t) * p.Hq * D;
-      for (int pass = sh.lo[0]; st < end; ++st, pass += PER) {
-        next();
-        rotate_step<D, LAYOUT, PER>(p, mine[st % kSlots], pass * R + s, sh.hi[0] - pass, heads, w != nullptr, ca,
-                                    sb, cb, sa, c, s, [&](int h, const float2 (&a)[2], const float2 (&b)[2]) {
-                                      store_row<LAYOUT>(q_out + h * D, c, p.r, a, b);
-                                    });
+    const auto rows = [&](auto rest) {
+      constexpr bool kRest = decltype(rest)::value;
+      if (seg == 0) {
+        __nv_bfloat16* q_out = p.q_out + static_cast<long long>(t) * p.Hq * D;
+        for (int pass = sh.lo[0]; st < end; ++st, pass += PER) {
+          next();
+          rotate_step<D, LAYOUT, PER, kRest>(
+              p, mine[st % kSlots], pass * R + s, sh.hi[0] - pass, heads, w != nullptr, ca, sb, cb, sa, c, s,
+              [&](int h, const float2 (&a)[2], const float2 (&b)[2]) {
+                store_row<LAYOUT>(q_out + h * D, c, p.r, a, b);
+              });
+        }
+      } else {
+        for (int pass = sh.lo[1]; st < end; ++st, pass += PER) {
+          next();
+          rotate_step<D, LAYOUT, PER, kRest>(
+              p, mine[st % kSlots], pass * R + s, sh.hi[1] - pass, heads, w != nullptr, ca, sb, cb, sa, c, s,
+              [&](int h, const float2 (&a)[2], const float2 (&b)[2]) {
+                const long long row = at.row + static_cast<long long>(h) * at.step;
+                if constexpr (KIND == kAppendFp8)
+                  store_codes<LAYOUT>(p.k_pages + row * D, c, p.r, a, b, p.k_scale[h]);
+                else
+                  store_row<LAYOUT>(
+                      (KIND == kPack ? p.k_out : reinterpret_cast<__nv_bfloat16*>(p.k_pages)) + row * D, c, p.r,
+                      a, b);
+              });
+        }
       }
-    } else {
-      for (int pass = sh.lo[1]; st < end; ++st, pass += PER) {
-        next();
-        rotate_step<D, LAYOUT, PER>(
-            p, mine[st % kSlots], pass * R + s, sh.hi[1] - pass, heads, w != nullptr, ca, sb, cb, sa, c, s,
-            [&](int h, const float2 (&a)[2], const float2 (&b)[2]) {
-              const long long row = at.row + static_cast<long long>(h) * at.step;
-              if constexpr (KIND == kAppendFp8)
-                store_codes<LAYOUT>(p.k_pages + row * D, c, p.r, a, b, p.k_scale[h]);
-              else
-                store_row<LAYOUT>(
-                    (KIND == kPack ? p.k_out : reinterpret_cast<__nv_bfloat16*>(p.k_pages)) + row * D, c, p.r, a,
-                    b);
-            });
-      }
-    }
+    };
+    if (REST && w == nullptr) rows(std::bool_constant<REST>());
+    else rows(std::false_type());
   }
   if (at.row >= 0) {
     for (int pass = sh.lo[2]; st < n; ++st, pass += PER) {
@@ -456,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(const RopeParams p) {
 
 // Gradients of a step's rows: dy in the slot's first half, x, with a norm, in
 // the second; this thread's share of the weights' gradients is added to `sum`.
-template <int D, int LAYOUT, bool NORM, int PER, typename Store>
+template <int D, int LAYOUT, bool NORM, int PER, bool REST, typename Store>
 __device__ __forceinline__ void rotate_step_back(const RopeParams& p, const __nv_bfloat16* slot, int h0, int left,
                                                  int heads, bool normed, const float2 (&wa)[2],
                                                  const float2 (&wb)[2], const float2 (&co)[2],
@@ -474,7 +495,8 @@ __device__ __forceinline__ void rotate_step_back(const RopeParams& p, const __nv
       y[e] = __ffma2_rn(a[e], co[e], __fmul2_rn(b[e], si[e]));
       z[e] = __ffma2_rn(b[e], co[e], __fmul2_rn(neg2(a[e]), si[e]));
     }
-    if (NORM && normed) {
+    if constexpr (REST) keep_rest(c, p.r, a, b, y, z);
+    if (NORM && !REST && normed) {
       float2 xa[2], xb[2], ua[2], ub[2];
       unpack<LAYOUT>(load_row<LAYOUT>(slot + (PER * R + u * R + s) * D, c, p.r), xa, xb);
       const float ms = head_sum<D>(dot_pairs(xa, xb, xa, xb)) * (1.f / D) + p.eps;
@@ -514,7 +536,7 @@ struct BackCfg {
   static constexpr int RING = kThreads / 32 * kSlots * SLOT * 2;     // bytes
   static constexpr int SMEM = RING + (NORM ? 16 * kThreads * 4 : 0);
 };
-template <int D, int LAYOUT, bool NORM>
+template <int D, int LAYOUT, bool NORM, bool REST>
 __global__ void __launch_bounds__(kThreads, BackCfg<D, NORM>::BLOCKS) rope_backward_kernel(const RopeParams p) {
   constexpr int C = D / 8, R = 32 / C;
   using C_ = BackCfg<D, NORM>;
@@ -585,14 +607,18 @@ __global__ void __launch_bounds__(kThreads, BackCfg<D, NORM>::BLOCKS) rope_backw
       float2 wa[2], wb[2], sum_a[2], sum_b[2];
       load_weights<LAYOUT>(w, c, p.r, wa, wb);
       sum_a[0] = sum_a[1] = sum_b[0] = sum_b[1] = make_float2(0.f, 0.f);
-      for (int pass = seg ? sh.lo[1] : sh.lo[0]; st < end; ++st, pass += PER) {
-        next();
-        rotate_step_back<D, LAYOUT, NORM, PER>(
-            p, mine[st % kSlots], pass * R + s, hi - pass, seg ? p.Hkv : p.Hq, w != nullptr, wa, wb, co, si, c, s,
-            sum_a, sum_b, [&](int h, const float2 (&a)[2], const float2 (&b)[2]) {
-              store_row<LAYOUT>(out + h * D, c, p.r, a, b);
-            });
-      }
+      const auto rows = [&](auto rest) {
+        for (int pass = seg ? sh.lo[1] : sh.lo[0]; st < end; ++st, pass += PER) {
+          next();
+          rotate_step_back<D, LAYOUT, NORM, PER, decltype(rest)::value>(
+              p, mine[st % kSlots], pass * R + s, hi - pass, seg ? p.Hkv : p.Hq, w != nullptr, wa, wb, co, si, c,
+              s, sum_a, sum_b, [&](int h, const float2 (&a)[2], const float2 (&b)[2]) {
+                store_row<LAYOUT>(out + h * D, c, p.r, a, b);
+              });
+        }
+      };
+      if (REST && w == nullptr) rows(std::bool_constant<REST>());   // (as in rope_kernel)
+      else rows(std::false_type());
       if constexpr (NORM) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -707,18 +733,29 @@ int layout_of(int32_t rotary_dim, int32_t interleaved) {
   return interleaved ? kInterleaved : rotary_dim % 8 == 0 ? kHalf : kHalfOdd;
 }
 
-template <int D, int KIND>
+// Whether some rows are neither normed nor rotated as a whole.
+bool has_rest(const RopeParams& p, int d) { return p.r < d && !(p.q_weight && p.k_weight); }
+
+template <int D, int KIND, bool REST>
 void (*pick_layout(int layout))(const RopeParams) {
-  return layout == kHalf          ? rope_kernel<D, kHalf, KIND>
-         : layout == kInterleaved ? rope_kernel<D, kInterleaved, KIND>
-                                  : rope_kernel<D, kHalfOdd, KIND>;
+  return layout == kHalf          ? rope_kernel<D, kHalf, KIND, REST>
+         : layout == kInterleaved ? rope_kernel<D, kInterleaved, KIND, REST>
+                                  : rope_kernel<D, kHalfOdd, KIND, REST>;
+}
+template <int D, int KIND>
+void (*pick_forward(const RopeParams& p, int layout))(const RopeParams) {
+  return has_rest(p, D) ? pick_layout<D, KIND, true>(layout) : pick_layout<D, KIND, false>(layout);
 }
 
+template <int D, bool NORM, bool REST>
+void (*pick_back_layout(int layout))(const RopeParams) {
+  return layout == kHalf          ? rope_backward_kernel<D, kHalf, NORM, REST>
+         : layout == kInterleaved ? rope_backward_kernel<D, kInterleaved, NORM, REST>
+                                  : rope_backward_kernel<D, kHalfOdd, NORM, REST>;
+}
 template <int D, bool NORM>
-void (*pick_backward(int layout))(const RopeParams) {
-  return layout == kHalf          ? rope_backward_kernel<D, kHalf, NORM>
-         : layout == kInterleaved ? rope_backward_kernel<D, kInterleaved, NORM>
-                                  : rope_backward_kernel<D, kHalfOdd, NORM>;
+void (*pick_backward(const RopeParams& p, int layout))(const RopeParams) {
+  return has_rest(p, D) ? pick_back_layout<D, NORM, true>(layout) : pick_back_layout<D, NORM, false>(layout);
 }
 
 int launched(const char* what, cudaError_t e) {
@@ -742,12 +779,12 @@ int launch_forward(RopeParams& p, int d, int kind, int interleaved, cudaStream_t
   const int64_t blocks = (int64_t{p.tokens} * p.parts + kThreads / 32 - 1) / (kThreads / 32);
   if (blocks >= (int64_t{1} << 31)) return refuse(SINKATTN_UNSUPPORTED, "too many work items");
   void (*kern)(const RopeParams) =
-      d == 64 ? (kind == kPack     ? pick_layout<64, kPack>(layout)
-                 : kind == kAppend ? pick_layout<64, kAppend>(layout)
-                                   : pick_layout<64, kAppendFp8>(layout))
-              : (kind == kPack     ? pick_layout<128, kPack>(layout)
-                 : kind == kAppend ? pick_layout<128, kAppend>(layout)
-                                   : pick_layout<128, kAppendFp8>(layout));
+      d == 64 ? (kind == kPack     ? pick_forward<64, kPack>(p, layout)
+                 : kind == kAppend ? pick_forward<64, kAppend>(p, layout)
+                                   : pick_forward<64, kAppendFp8>(p, layout))
+              : (kind == kPack     ? pick_forward<128, kPack>(p, layout)
+                 : kind == kAppend ? pick_forward<128, kAppend>(p, layout)
+                                   : pick_forward<128, kAppendFp8>(p, layout));
   kern<<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(p);
   return launched("rope", cudaGetLastError());
 }
@@ -998,8 +1035,8 @@ int sinkattn_rope_qkv_backward(const void* dq, const void* dk, const void* dv, c
   p.part = static_cast<float*>(workspace);
   const int layout = layout_of(p.r, interleaved);
   void (*kern)(const RopeParams) =
-      head_dim == 64 ? (norm ? pick_backward<64, true>(layout) : pick_backward<64, false>(layout))
-                     : (norm ? pick_backward<128, true>(layout) : pick_backward<128, false>(layout));
+      head_dim == 64 ? (norm ? pick_backward<64, true>(p, layout) : pick_backward<64, false>(p, layout))
+                     : (norm ? pick_backward<128, true>(p, layout) : pick_backward<128, false>(p, layout));
   const int smem = head_dim == 64 ? (norm ? BackCfg<64, true>::SMEM : BackCfg<64, false>::SMEM)
                                   : (norm ? BackCfg<128, true>::SMEM : BackCfg<128, false>::SMEM);
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)

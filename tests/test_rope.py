@@ -284,6 +284,41 @@ def test_zero_rows():
     check_backward(backward(x, g), g, x, rot, cu)
 
 
+@gpu
+@pytest.mark.parametrize("d,r,inter", [(64, 32, False), (64, 38, False), (64, 0, False), (64, 6, True),
+                                       (128, 64, False), (128, 100, True), (128, 126, False)])
+@pytest.mark.parametrize("q_norm", [False, True])
+def test_elements_that_are_not_rotated_stay_as_they_are(d, r, inter, q_norm):
+    """Bit for bit without a norm, whatever stands beside them: infinities, NaN, both zeros.
+    (q with a norm, k without: the second path of the same launches.)"""
+    x, rot, cu, T = make([40, 23], 8, 3, d, r, inter, q_norm, False)
+    gen = torch.Generator().manual_seed(6)
+    odd = torch.tensor([math.inf, -math.inf, math.nan, -0.0, 0.0, 1.0, -2.0], dtype=torch.bfloat16)
+    mix = lambda *s: odd[torch.randint(0, 7, s, generator=gen)].cuda()   # noqa: E731
+
+    def same(a, b):
+        return bool(((a.view(torch.int16) == b.view(torch.int16)) | (a.isnan() & b.isnan())).all())
+
+    x["k"][..., r:] = mix(T, 3, d - r)
+    if not q_norm:
+        x["q"][..., r:] = mix(T, 8, d - r)
+    rows = hnd_rows(cu, 3, "cuda")
+    q, k, v = forward(x)
+    assert same(k[rows][..., r:], x["k"][..., r:])
+    assert torch.isfinite(k[rows][..., :r]).all() and torch.isfinite(q[..., :r]).all()
+    if not q_norm:
+        assert same(q[..., r:], x["q"][..., r:])
+    pools = [torch.zeros((4, 3, 16, d), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    slots = torch.arange(T, dtype=torch.int32, device="cuda")
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    sa.sinkattn_rope_append_paged(x["q"], x["k"], x["v"], pos, slots, x["rope"], *pools, x["q_weight"], None, EPS)
+    assert same(pools[0].transpose(1, 2).reshape(-1, 3, d)[:T, :, r:].contiguous(), x["k"][..., r:].contiguous())
+    g = [t.clone() for t in grads(x, cu)]
+    g[1][..., r:] = mix(3 * T, d - r)
+    got = backward(x, g)
+    assert same(got[1][..., r:], g[1][rows][..., r:]) and torch.isfinite(got[1][..., :r]).all()
+
+
 # ----------------------------------------------------------------------------
 # backward
 # ----------------------------------------------------------------------------
