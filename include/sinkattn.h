@@ -599,7 +599,8 @@ SINKATTN_API int sinkattn_prefill_backward_workspace_bytes(int32_t total_q, int3
  * Rotary positions. A head's first rotary_dim elements are cut into pairs, in
  * the interleaved layout (2i, 2i + 1), else (i, i + rotary_dim / 2); pair i is
  * turned by the angle position * f_i and scaled by attention_factor; the other
- * elements stay as they are (without a norm bit for bit, infinities and zeros' signs too). The frequencies are passed as
+ * elements stay as they are (without a norm bit for bit, infinities and zeros'
+ * signs too). The frequencies are passed as
  *   turns: uint64 [rotary_dim / 2] (device), f_i / (2 pi) modulo 1 in units of 2^-64,
  * rounded to the nearest, so that position times turns is off by at most 2^-34
  * turns at any int32 position (sinkattn_rope_turns makes them from f_i in host
