@@ -574,7 +574,7 @@ SINKATTN_API int sinkattn_pages_lists(const int32_t* table, int32_t num_pages, i
  *     may overlap need two workspaces.
  * Every element of dq, dk, dv and dsinks up to the last sequence's end is
  * written (zeros where nothing is visible); rows behind it stay as they are.
- * Outputs overlap neither the inputs, which the second pass reads again, nor one another.
+ * Outputs must not overlap the inputs, which the second pass reads again, or one another.
  * Sums are fp32; P and dS are rounded to bf16 for the products. Results do not
  * depend on timing. A sequence whose inputs hold NaN or infinities gets NaN; the
  * other sequences do not. A row whose lse is -inf has no weights: it gives and gets
@@ -646,10 +646,10 @@ SINKATTN_API int sinkattn_rope_turns(const double* inv_freq, int32_t n, uint64_t
  *     eps) over the head's d elements before the rotation; NULL: no norm;
  *   q_out bf16 [tokens, Hq, d]; k_out, v_out bf16 ragged HND [Hkv * tokens, d].
  * Arithmetic is fp32, each output is rounded once; the weight multiplies cosine
- * and sine first, the inverse root comes last. (A row whose mean square plus eps is
- * 0 or leaves fp32's range, as one of zeros without eps, has no norm: its outputs
- * are NaN or infinite.) Outputs overlap neither the inputs nor one another.
- * cu_seqlens that leave [0, tokens] or decrease record SINKATTN_BAD_LENGTHS; tokens of sequences that
+ * and sine first, the inverse root comes last. (Outputs of a row whose mean square
+ * plus eps is 0, as one of zeros without eps, or leaves fp32's range are undefined.)
+ * Outputs must not overlap the inputs or one another. cu_seqlens that leave
+ * [0, tokens] or decrease record SINKATTN_BAD_LENGTHS; tokens of sequences that
  * leave [0, tokens] are left out, those of sequences that overlap are undefined.
  * (A call of no tokens or no sequences reads nothing, cu_seqlens neither.)
  */
